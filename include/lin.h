@@ -323,6 +323,88 @@ lin_status lin_gate_up_w16(const float *X, const uint16_t *WG16, const uint16_t 
                            lin_stream_t stream);
 
 /*
+ * Attention
+ * ---------
+ * The attention between the QKV and the output projection of a training
+ * step, and its gradient, on 16-bit queries, keys and values. The pages name
+ * it (10_backward_attention) without a description; these are the standard
+ * definitions. Per sequence and query head h (key head h / (heads_q /
+ * heads_kv)):
+ *   S = scale Q K^T, masked;  P = softmax(S) over the keys;  O = P V
+ *   LSE_i = log sum_j exp(S_ij)                (natural logarithm)
+ * and, with delta_i = sum_d dO_id O_id and dP = dO V^T,
+ *   dS = P (dP - delta);  dQ = scale dS K;  dK = scale dS^T Q;  dV = P^T dO,
+ * dK and dV summed over the query heads that share a key head. The mask
+ * leaves the sequence's own keys and, with `causal`, those with
+ * j <= i + (keys - queries): the last query sees every key. A row that the
+ * mask leaves nothing has O = 0, LSE = -inf and gives and gets no gradient.
+ *
+ * Tensors     lin_heads: [tokens, heads, dim], the dim entries of a head
+ *             contiguous, strides in entries (multiples of 8, base 16-byte
+ *             aligned); so q, k and v can be views of one packed buffer, and
+ *             tokens-first or heads-first. Strides of an extent of one are
+ *             not looked at. Q, O, DO, DQ: tokens_q x heads_q; K, V, DK, DV:
+ *             tokens_k x heads_kv. All binary16 or all bfloat16 (dtype).
+ *             LSE: f32 [heads_q][tokens_q].
+ * Sequences   packed one after another: sequence b's rows are cu_q[b] ..
+ *             cu_q[b+1] - 1 of Q and cu_k[b] .. cu_k[b+1] - 1 of K (int32,
+ *             device memory, sequences + 1 offsets that do not decrease;
+ *             lengths of 0 are fine); max_q and max_k are at least the longest
+ *             lengths (rows past them are not computed). cu_q NULL: one
+ *             sequence of all tokens_q rows; likewise cu_k. Rows outside
+ *             every sequence are neither read nor written, whatever they
+ *             hold. Offsets outside the tensor are held to it.
+ * Arithmetic  Products on the tensor cores from the 16-bit operands with
+ *             float32 accumulation; softmax statistics, delta and every sum
+ *             in float32. P and dS are rounded to the tensors' 16-bit type
+ *             for the product that follows them (dS scaled by a power of two
+ *             so that binary16 holds it whatever the size of dO, while the
+ *             rows of V have norms up to 1024); O, dQ, dK and dV are rounded
+ *             once. Sums have a fixed order: the same call gives the same
+ *             bits.
+ * Shapes      dim a multiple of 8 up to 128; heads_q a multiple of heads_kv;
+ *             sequences up to 65535; max_q and max_k up to 65535 * 128;
+ *             scale > 0. Else LIN_ERROR_UNSUPPORTED_SHAPE (scale:
+ *             LIN_ERROR_INVALID_VALUE).
+ * Workspace   backward: (tokens_q + sequences * ceil(max_q / 128)) * heads_q
+ *             floats from the library's pool, in stream order (a graph
+ *             memory node under capture).
+ * Errors      as for the linear layers; LIN_ERROR_MISALIGNED also for strides
+ *             that are no multiple of 8, LIN_ERROR_INVALID_VALUE for strides
+ *             under which two entries of a tensor would share a place;
+ *             LIN_ERROR_ALIASING if an output shares an entry with another
+ *             tensor of the call (interleaved views of one buffer do not).
+ */
+typedef enum lin_dtype { LIN_BINARY16 = 0, LIN_BFLOAT16 = 1 } lin_dtype;
+
+typedef struct lin_heads {
+  void *data;
+  int64_t token_stride;
+  int64_t head_stride;
+} lin_heads;
+
+typedef struct lin_attention_shape {
+  int32_t dtype;    /* lin_dtype */
+  int32_t causal;   /* 0 or 1 */
+  int64_t tokens_q, tokens_k;
+  int64_t heads_q, heads_kv, dim;
+  int64_t sequences;
+  int64_t max_q, max_k;
+  const int32_t *cu_q, *cu_k;
+  float scale;
+} lin_attention_shape;
+
+/* O and LSE from Q, K, V. One kernel. */
+lin_status lin_attention(const lin_attention_shape *shape, const lin_heads *Q, const lin_heads *K,
+                         const lin_heads *V, const lin_heads *O, float *LSE, lin_stream_t stream);
+
+/* DQ, DK, DV from DO and the forward call's inputs and results. Two kernels. */
+lin_status lin_attention_backward(const lin_attention_shape *shape, const lin_heads *Q,
+                                  const lin_heads *K, const lin_heads *V, const lin_heads *O,
+                                  const float *LSE, const lin_heads *DO, const lin_heads *DQ,
+                                  const lin_heads *DK, const lin_heads *DV, lin_stream_t stream);
+
+/*
  * Host-operand forms
  * ------------------
  * lin_<form>_host: the six forward forms above with every operand (X or GATE

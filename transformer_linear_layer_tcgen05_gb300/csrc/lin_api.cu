@@ -201,6 +201,39 @@ bool encode_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_
                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool encode_heads(CUtensorMap* m, const void* base, uint64_t dim, uint64_t heads, uint64_t tokens,
+                  uint64_t head_bytes, uint64_t token_bytes) {
+  const cuuint64_t dims[3] = {dim, heads, tokens};
+  const cuuint64_t strides[2] = {head_bytes, token_bytes};
+  const cuuint32_t box[3] = {64, 1, 128};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return driver().encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims,
+                         strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+void* take_stream_workspace(int dev, size_t bytes, cudaStream_t stream) {
+  void* ws = nullptr;
+  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
+  cudaError_t e = cudaStreamIsCapturing(stream, &cs);
+  if (e == cudaSuccess && cs == cudaStreamCaptureStatusActive) {
+    e = cudaMallocAsync(&ws, bytes, stream);
+  } else if (e == cudaSuccess && cs == cudaStreamCaptureStatusNone) {
+    cudaMemPool_t pool = workspace_pool(dev);
+    e = pool ? cudaMallocFromPoolAsync(&ws, bytes, pool, stream) : cudaErrorMemoryAllocation;
+  } else if (e == cudaSuccess) {
+    e = cudaErrorStreamCaptureInvalidated;
+  }
+  if (e != cudaSuccess) {
+    cuda_fail(e);   // (recorded for lin_last_cuda_error)
+    return nullptr;
+  }
+  return ws;
+}
+
+uint64_t wait_limit_ns() { return kDefaultTimeoutNs; }
+
 // Cluster size of the binary16 kernels: enough CTAs along N to share the
 // transformed A operand, within what N can use. LIN_F16_KERNEL overrides it
 // for measurements: "tile" selects the per-tile kernel, "1", "2" or "4" a

@@ -1,0 +1,130 @@
+// lin_attn.cuh -- what the attention kernels share: tile geometry, the
+// sequences' extents, operand descriptors and the 16-bit conversions.
+//
+// The kernels work in tiles of 128 queries x 128 keys. An operand tile is 128
+// tokens of one head, [128 rows][64 entries] of 16 bits with the 128-byte
+// swizzle, one such sub-tile for heads of up to 64 entries and two for up to
+// 128 (entries past the head's size are zero-filled by the copy). The same
+// tile serves as a K-major operand (the contraction runs over the entries: S
+// = Q K^T, dP = dO V^T) and as an MN-major one (it runs over the tokens: P V,
+// P^T dO, dS^T Q, dS K).
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "lin_attn.h"
+#include "lin_common.cuh"
+
+namespace lin {
+
+constexpr float kLog2E = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+constexpr int kAttnThreads = 320;   // 8 element-wise warps, 1 copying, 1 issuing products
+constexpr int kAttnCopyWarp = 8;
+constexpr int kAttnMmaWarp = 9;
+
+// Sequence b's first row and length in a packed tensor of `tokens` rows; the
+// offsets come from device memory, so they are held inside the tensor and
+// the length at `most` (the grid's extent).
+struct SeqRange {
+  int start, len;
+};
+__device__ __forceinline__ SeqRange seq_range(const int32_t* cu, int b, int tokens, int most) {
+  if (!cu) return SeqRange{0, min(tokens, most)};
+  const int s = min(max(cu[b], 0), tokens);
+  const int e = min(max(cu[b + 1], s), tokens);
+  return SeqRange{s, min(e - s, most)};
+}
+
+// Sub-tiles, bytes and descriptors of a [128 tokens][DP entries] operand tile.
+template <int DP>
+struct AttnTile {
+  static constexpr int SUB = DP / 64;
+  static constexpr uint32_t SUB_BYTES = 128 * 128;
+  static constexpr uint32_t BYTES = SUB * SUB_BYTES;
+  // K-major, step kk of 16 entries
+  static __device__ __forceinline__ uint64_t k_major(uint32_t tile, int kk) {
+    return umma_desc_sw128(tile + (kk >> 2) * SUB_BYTES + (kk & 3) * 32, 16, 1024);
+  }
+  // MN-major, step kk of 16 tokens
+  static __device__ __forceinline__ uint64_t mn_major(uint32_t tile, int kk) {
+    return umma_desc_sw128(tile + kk * 2048, SUB_BYTES, 1024);
+  }
+};
+
+template <bool BF16, bool B_MN, int N>
+__host__ __device__ constexpr uint32_t attn_idesc() {
+  return umma_idesc(BF16 ? 1u : 0u, false, B_MN, 128, N);
+}
+
+// Two values rounded to nearest even in the tensors' 16-bit type, the first
+// in the low half.
+template <bool BF16>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi) {
+  if constexpr (BF16) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    return pack_half2(lo, hi);
+  }
+}
+
+template <bool BF16>
+__device__ __forceinline__ float2 unpack16(uint32_t v) {
+  if constexpr (BF16) {
+    return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+  } else {
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+  }
+}
+
+// D[128 x 128] = A B^T over the DP entries of two operand tiles.
+template <int DP, bool BF16>
+__device__ __forceinline__ void umma_entries(uint32_t d, uint32_t a, uint32_t b) {
+  constexpr uint32_t idesc = attn_idesc<BF16, false, 128>();
+#pragma unroll
+  for (int kk = 0; kk < DP / 16; ++kk)
+    umma_f16(d, AttnTile<DP>::k_major(a, kk), AttnTile<DP>::k_major(b, kk), idesc, kk > 0);
+}
+
+// D[128 x DP] (+)= A B over 128 tokens: A in tensor memory, its first 64
+// tokens in the 32 columns at `a`, the others in those at `a_hi`; B an
+// operand tile.
+template <int DP, bool BF16>
+__device__ __forceinline__ void umma_tokens(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b,
+                                            bool accumulate) {
+  constexpr uint32_t idesc = attn_idesc<BF16, true, DP>();
+#pragma unroll
+  for (int kk = 0; kk < 8; ++kk)
+    umma_f16_tmem_a(d, (kk < 4 ? a : a_hi) + (kk & 3) * 8, AttnTile<DP>::mn_major(b, kk), idesc,
+                    accumulate || kk > 0);
+}
+
+// Zeroes rows [first, 128) of an operand tile: a contraction over tokens must
+// not meet what lies behind a sequence's end (another sequence's rows, or
+// padding that may hold infinities or NaN, which a zero weight would not
+// remove). One warp, after the copy has landed; the fence orders the stores
+// before the tensor core's reads.
+template <int DP>
+__device__ __forceinline__ void zero_rows(uint32_t tile, int first, int lane) {
+  for (int s = 0; s < AttnTile<DP>::SUB; ++s)
+    for (int i = first * 8 + lane; i < 128 * 8; i += 32)
+      st_shared_v4(tile + s * AttnTile<DP>::SUB_BYTES + i * 16, 0u, 0u, 0u, 0u);
+}
+
+// One operand tile (tokens z .. z + 127 of head h) into shared memory.
+template <int DP>
+__device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int h, int z,
+                                          uint32_t bar) {
+#pragma unroll
+  for (int s = 0; s < AttnTile<DP>::SUB; ++s)
+    tma_load_3d(dst + s * AttnTile<DP>::SUB_BYTES, map, s * 64, h, z, bar);
+}
+
+// Eight 16-bit entries of a row to global memory.
+__device__ __forceinline__ void store16(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(a, b, c, d);
+}
+
+}  // namespace lin

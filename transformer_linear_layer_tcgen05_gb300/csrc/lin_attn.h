@@ -1,0 +1,55 @@
+// lin_attn.h -- launch interface of the attention kernels (host and device).
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+namespace lin {
+
+// One [tokens][heads][dim] tensor of 16-bit entries, strides in entries.
+struct HeadsPtr {
+  uint16_t* p;
+  int64_t token_stride, head_stride;
+};
+
+struct AttnArgs {
+  const int32_t* cu_q;   // [sequences + 1] row offsets (null: one sequence)
+  const int32_t* cu_k;
+  int32_t tokens_q, tokens_k, max_q, max_k;
+  int32_t heads_q, group, dim;   // group: query heads per key head
+  int32_t causal;
+  float scale;
+  uint64_t timeout_ns;
+  int* status;
+};
+
+struct AttnFwdArgs {
+  AttnArgs s;
+  HeadsPtr o;
+  float* lse;   // [heads_q][tokens_q]
+};
+
+struct AttnBwdArgs {
+  AttnArgs s;
+  HeadsPtr o, dout;       // read row by row for delta
+  const float* lse;       // [heads_q][tokens_q]
+  float* delta;           // [heads_q][tokens_q]: sum of dO * O of each row
+  float* norm;            // [sequences][heads_q][q tiles]: largest row norm of dO
+  HeadsPtr dq, dk, dv;
+};
+
+struct AttnFwdMaps {
+  CUtensorMap q, k, v;
+};
+struct AttnBwdMaps {
+  CUtensorMap q, k, v, dout;
+};
+
+cudaError_t launch_attn_fwd(bool bf16, const AttnFwdMaps& maps, const AttnFwdArgs& args,
+                            int heads_kv, int sequences, cudaStream_t stream);
+// The dQ kernel (which also leaves delta and norm), then the dK, dV kernel.
+cudaError_t launch_attn_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArgs& args,
+                            int heads_kv, int sequences, cudaStream_t stream);
+
+}  // namespace lin

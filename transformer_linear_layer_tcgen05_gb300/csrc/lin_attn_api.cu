@@ -1,0 +1,241 @@
+// lin_attn_api.cu -- the attention entry points of include/lin.h: checks of
+// the arguments, tensor maps, workspace and launch.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "lin.h"
+#include "lin_attn.h"
+#include "lin_internal.h"
+
+namespace lin_detail {
+
+namespace {
+
+constexpr int64_t kMaxExtent = 0x7fffffffLL;
+
+// One [tokens][heads][dim] tensor of a call.
+struct View {
+  const lin_heads* t;
+  int64_t tokens, heads;
+  bool out;
+  // strides with those of an extent of one (which are never used) set to
+  // something valid
+  int64_t ts, hs;
+  uint64_t extent;   // bytes from the first to behind the last entry
+};
+
+lin_status check_view(View& v, int64_t dim) {
+  if (v.tokens == 0) {
+    v.ts = v.hs = dim;
+    v.extent = 0;
+    return LIN_SUCCESS;
+  }
+  if (!v.t->data) return LIN_ERROR_INVALID_VALUE;
+  v.hs = v.heads > 1 ? v.t->head_stride : dim;
+  v.ts = v.tokens > 1 ? v.t->token_stride : std::max(dim, v.hs * v.heads);
+  // no entry may be at two places of the tensor: the larger stride steps
+  // over the smaller one's whole extent
+  const bool head_inner = v.heads == 1 || (v.tokens > 1 && v.hs <= v.ts) || v.tokens == 1;
+  const int64_t small = head_inner ? v.hs : v.ts, large = head_inner ? v.ts : v.hs;
+  const int64_t inner = head_inner ? v.heads : v.tokens;
+  if (small < dim || large < dim) return LIN_ERROR_INVALID_VALUE;
+  if (v.hs % 8 != 0 || v.ts % 8 != 0) return LIN_ERROR_MISALIGNED;
+  // (the tensor maps hold byte strides below 2^40)
+  if (v.hs >= (1LL << 39) || v.ts >= (1LL << 39)) return LIN_ERROR_UNSUPPORTED_SHAPE;
+  if (large < (inner - 1) * small + dim) return LIN_ERROR_INVALID_VALUE;
+  if ((reinterpret_cast<uintptr_t>(v.t->data) & 15u) != 0) return LIN_ERROR_MISALIGNED;
+  const unsigned __int128 ext =
+      (unsigned __int128)(v.tokens - 1) * v.ts + (unsigned __int128)(v.heads - 1) * v.hs + dim;
+  if (ext >> 61) return LIN_ERROR_UNSUPPORTED_SHAPE;
+  v.extent = (uint64_t)ext * 2;
+  return LIN_SUCCESS;
+}
+
+// Whether two views share an entry. Views whose ranges of memory meet may
+// still be disjoint: the q, k and v heads of one buffer of tokens.
+bool views_overlap(const View& a, const View& b, int64_t dim) {
+  if (!overlaps(a.t->data, a.extent, b.t->data, b.extent)) return false;
+  const int64_t ra = (a.heads - 1) * a.hs + dim, rb = (b.heads - 1) * b.hs + dim;
+  if (a.tokens > 1 && b.tokens > 1 && a.ts == b.ts && ra <= a.ts && rb <= b.ts) {
+    const int64_t d = (static_cast<const char*>(b.t->data) - static_cast<const char*>(a.t->data)) / 2;
+    const int64_t r = ((d % a.ts) + a.ts) % a.ts;   // b's row starts r entries into one of a's
+    return !(r >= ra && a.ts - r >= rb);
+  }
+  return true;
+}
+
+struct Checked {
+  int dev;
+  int* word;
+  int64_t max_q, max_k;
+  bool nothing;   // nothing to compute
+};
+
+// The checks that both directions share. `views`: every tensor of the call;
+// `lse` is read (backward) or written (forward).
+lin_status check_attention(const lin_attention_shape* s, View* views, int nviews, const float* lse,
+                           bool lse_out, Checked* got) {
+  got->nothing = false;
+  if (!s) return LIN_ERROR_INVALID_VALUE;
+  for (int i = 0; i < nviews; ++i)
+    if (!views[i].t) return LIN_ERROR_INVALID_VALUE;
+  if (s->dtype != LIN_BINARY16 && s->dtype != LIN_BFLOAT16) return LIN_ERROR_INVALID_VALUE;
+  if (s->tokens_q < 0 || s->tokens_k < 0 || s->sequences < 0 || s->max_q < 0 || s->max_k < 0 ||
+      s->heads_q < 1 || s->heads_kv < 1 || s->dim < 1)
+    return LIN_ERROR_INVALID_VALUE;
+  if (!(s->scale > 0.0f) || std::isinf(s->scale)) return LIN_ERROR_INVALID_VALUE;
+  if ((!s->cu_q || !s->cu_k) && s->sequences != 1) return LIN_ERROR_INVALID_VALUE;
+  if (s->tokens_q > kMaxExtent || s->tokens_k > kMaxExtent || s->sequences > 65535 ||
+      s->heads_q > kMaxExtent / 65536 || s->heads_kv > s->heads_q ||
+      s->heads_q % s->heads_kv != 0 || s->dim % 8 != 0 || s->dim > 128)
+    return LIN_ERROR_UNSUPPORTED_SHAPE;
+  got->max_q = s->cu_q ? std::min(s->max_q, s->tokens_q) : s->tokens_q;
+  got->max_k = s->cu_k ? std::min(s->max_k, s->tokens_k) : s->tokens_k;
+  if (got->max_q > 65535LL * 128 || got->max_k > 65535LL * 128) return LIN_ERROR_UNSUPPORTED_SHAPE;
+  for (int i = 0; i < nviews; ++i) {
+    views[i].tokens = views[i].tokens < 0 ? s->tokens_k : s->tokens_q;   // (-1: of the keys)
+    const lin_status st = check_view(views[i], s->dim);
+    if (st != LIN_SUCCESS) return st;
+  }
+  const uint64_t lse_bytes = (uint64_t)s->heads_q * (uint64_t)s->tokens_q * 4;
+  if (lse_bytes && !lse) return LIN_ERROR_INVALID_VALUE;
+  auto misaligned4 = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 3u) != 0; };
+  if (misaligned4(lse) || misaligned4(s->cu_q) || misaligned4(s->cu_k)) return LIN_ERROR_MISALIGNED;
+  const uint64_t cu_bytes = ((uint64_t)s->sequences + 1) * 4;
+  for (int i = 0; i < nviews; ++i) {
+    const View& v = views[i];
+    if (overlaps(lse, lse_bytes, v.t->data, v.extent) && (v.out || lse_out)) return LIN_ERROR_ALIASING;
+    if (!v.out) continue;
+    if ((s->cu_q && overlaps(s->cu_q, cu_bytes, v.t->data, v.extent)) ||
+        (s->cu_k && overlaps(s->cu_k, cu_bytes, v.t->data, v.extent)))
+      return LIN_ERROR_ALIASING;
+    for (int k = 0; k < nviews; ++k)
+      if (k != i && views_overlap(v, views[k], s->dim)) return LIN_ERROR_ALIASING;
+  }
+  if (lse_out && ((s->cu_q && overlaps(lse, lse_bytes, s->cu_q, cu_bytes)) ||
+                  (s->cu_k && overlaps(lse, lse_bytes, s->cu_k, cu_bytes))))
+    return LIN_ERROR_ALIASING;
+  lin_status st = current_device(&got->dev, &got->word);
+  if (st != LIN_SUCCESS) return st;
+  for (int i = 0; i < nviews; ++i)
+    if (views[i].extent &&
+        (st = check_buffer(views[i].t->data, views[i].extent, got->dev)) != LIN_SUCCESS)
+      return st;
+  if (lse_bytes && (st = check_buffer(lse, lse_bytes, got->dev)) != LIN_SUCCESS) return st;
+  if (s->cu_q && (st = check_buffer(s->cu_q, cu_bytes, got->dev)) != LIN_SUCCESS) return st;
+  if (s->cu_k && (st = check_buffer(s->cu_k, cu_bytes, got->dev)) != LIN_SUCCESS) return st;
+  got->nothing = s->sequences == 0;
+  return LIN_SUCCESS;
+}
+
+bool encode_view(CUtensorMap* m, const View& v, int64_t dim) {
+  return encode_heads(m, v.t->data, (uint64_t)dim, (uint64_t)v.heads, (uint64_t)v.tokens,
+                      (uint64_t)v.hs * 2, (uint64_t)v.ts * 2);
+}
+
+lin::HeadsPtr heads_ptr(const View& v) {
+  return lin::HeadsPtr{static_cast<uint16_t*>(v.t->data), v.ts, v.hs};
+}
+
+lin::AttnArgs attn_args(const lin_attention_shape* s, const Checked& c) {
+  lin::AttnArgs a{};
+  a.cu_q = s->cu_q;
+  a.cu_k = s->cu_k;
+  a.tokens_q = (int32_t)s->tokens_q;
+  a.tokens_k = (int32_t)s->tokens_k;
+  a.max_q = (int32_t)c.max_q;
+  a.max_k = (int32_t)c.max_k;
+  a.heads_q = (int32_t)s->heads_q;
+  a.group = (int32_t)(s->heads_q / s->heads_kv);
+  a.dim = (int32_t)s->dim;
+  a.causal = s->causal != 0;
+  a.scale = s->scale;
+  a.timeout_ns = wait_limit_ns();
+  a.status = c.word;
+  return a;
+}
+
+lin_status attention(const lin_attention_shape* s, const lin_heads* Q, const lin_heads* K,
+                     const lin_heads* V, const lin_heads* O, float* LSE, cudaStream_t stream) {
+  set_last_launch_info(0, 0);
+  const int64_t hq = s ? s->heads_q : 0, hk = s ? s->heads_kv : 0;
+  View v[] = {{Q, 0, hq, false}, {K, -1, hk, false}, {V, -1, hk, false}, {O, 0, hq, true}};
+  Checked c;
+  const lin_status st = check_attention(s, v, 4, LSE, true, &c);
+  if (st != LIN_SUCCESS) return st;
+  if (c.nothing || c.max_q == 0) return LIN_SUCCESS;
+  lin::AttnFwdMaps maps;
+  bool ok = encode_view(&maps.q, v[0], s->dim);
+  // without keys the K and V maps are never used
+  ok &= encode_view(&maps.k, v[1].extent ? v[1] : v[0], s->dim);
+  ok &= encode_view(&maps.v, v[2].extent ? v[2] : v[0], s->dim);
+  if (!ok) return cuda_fail(cudaErrorInvalidValue);
+  lin::AttnFwdArgs a{attn_args(s, c), heads_ptr(v[3]), LSE};
+  const cudaError_t e = lin::launch_attn_fwd(s->dtype == LIN_BFLOAT16, maps, a, (int)s->heads_kv,
+                                             (int)s->sequences, stream);
+  if (e != cudaSuccess) return cuda_fail(e);
+  set_last_launch_info(1, 0);
+  return LIN_SUCCESS;
+}
+
+lin_status attention_backward(const lin_attention_shape* s, const lin_heads* Q, const lin_heads* K,
+                              const lin_heads* V, const lin_heads* O, const float* LSE,
+                              const lin_heads* DO, const lin_heads* DQ, const lin_heads* DK,
+                              const lin_heads* DV, cudaStream_t stream) {
+  set_last_launch_info(0, 0);
+  const int64_t hq = s ? s->heads_q : 0, hk = s ? s->heads_kv : 0;
+  View v[] = {{Q, 0, hq, false},  {K, -1, hk, false}, {V, -1, hk, false}, {O, 0, hq, false},
+              {DO, 0, hq, false}, {DQ, 0, hq, true},  {DK, -1, hk, true}, {DV, -1, hk, true}};
+  Checked c;
+  const lin_status st = check_attention(s, v, 8, LSE, false, &c);
+  if (st != LIN_SUCCESS) return st;
+  if (c.nothing || (c.max_q == 0 && c.max_k == 0)) return LIN_SUCCESS;
+  lin::AttnBwdMaps maps;
+  const View& q = v[0].extent ? v[0] : v[1];   // (an empty side's maps are never used)
+  const View& k = v[1].extent ? v[1] : v[0];
+  bool ok = encode_view(&maps.q, q, s->dim) && encode_view(&maps.k, k, s->dim);
+  ok = ok && encode_view(&maps.v, v[2].extent ? v[2] : q, s->dim);
+  ok = ok && encode_view(&maps.dout, v[4].extent ? v[4] : k, s->dim);
+  if (!ok) return cuda_fail(cudaErrorInvalidValue);
+  // workspace: delta [heads][tokens], then the largest dO norms of the query tiles
+  const uint64_t delta = (uint64_t)s->heads_q * (uint64_t)s->tokens_q;
+  const uint64_t norms =
+      (uint64_t)s->sequences * (uint64_t)s->heads_q * (uint64_t)((c.max_q + 127) / 128);
+  const size_t bytes = (size_t)std::max<uint64_t>(16, (delta + norms) * 4);
+  float* ws = static_cast<float*>(take_stream_workspace(c.dev, bytes, stream));
+  if (!ws) return LIN_ERROR_CUDA;
+  lin::AttnBwdArgs a{attn_args(s, c), heads_ptr(v[3]), heads_ptr(v[4]), LSE, ws, ws + delta,
+                     heads_ptr(v[5]), heads_ptr(v[6]), heads_ptr(v[7])};
+  cudaError_t e = lin::launch_attn_bwd(s->dtype == LIN_BFLOAT16, maps, a, (int)s->heads_kv,
+                                       (int)s->sequences, stream);
+  const cudaError_t ef = cudaFreeAsync(ws, stream);
+  if (e == cudaSuccess) e = ef;
+  if (e != cudaSuccess) return cuda_fail(e);
+  set_last_launch_info((c.max_q > 0) + (c.max_k > 0), bytes);
+  return LIN_SUCCESS;
+}
+
+}  // namespace
+}  // namespace lin_detail
+
+extern "C" {
+
+lin_status lin_attention(const lin_attention_shape* shape, const lin_heads* Q, const lin_heads* K,
+                         const lin_heads* V, const lin_heads* O, float* LSE,
+                         lin_stream_t stream) {
+  return lin_detail::attention(shape, Q, K, V, O, LSE, reinterpret_cast<cudaStream_t>(stream));
+}
+
+lin_status lin_attention_backward(const lin_attention_shape* shape, const lin_heads* Q,
+                                  const lin_heads* K, const lin_heads* V, const lin_heads* O,
+                                  const float* LSE, const lin_heads* DO, const lin_heads* DQ,
+                                  const lin_heads* DK, const lin_heads* DV, lin_stream_t stream) {
+  return lin_detail::attention_backward(shape, Q, K, V, O, LSE, DO, DQ, DK, DV,
+                                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"

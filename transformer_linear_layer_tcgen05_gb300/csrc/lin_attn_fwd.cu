@@ -1,0 +1,332 @@
+// lin_attn_fwd.cu -- attention forward: O = softmax(scale Q K^T) V and each
+// row's log-sum-exp.
+//
+// One pass over the keys with the running maximum m and sum l of the softmax:
+// for each tile of 128 keys S = Q K^T goes to tensor memory, the row's thread
+// takes p = 2^(c s - c m) (c = scale log2 e), writes it back as 16-bit P over
+// S, and O += P V accumulates in tensor memory. When a row's maximum grows by
+// more than 8 in base-2 units the row's l and O are scaled down to the new
+// one; below that the old maximum stays in place (p then reaches 2^8, well
+// inside both 16-bit types' range) and O is left alone: the quotient O / l
+// does not depend on it.
+//
+// A CTA runs two tiles of 128 queries of one head against the same keys: 128
+// threads per tile (one per row) take turns on the exponentials while the
+// tensor cores work for the other tile, and each K, V tile is read once for
+// 256 queries. The products of one thread execute in issue order, so S of
+// the next tile is issued right behind the P V that reads P out of the same
+// columns. Heads vary fastest over the grid and the causal mask's longest
+// query tiles come first.
+#include "lin_attn.cuh"
+
+namespace lin {
+
+namespace {
+
+template <int DP>
+struct FwdCfg {
+  static constexpr int NKV = DP == 64 ? 3 : 2;   // stages of the K and of the V ring
+  static constexpr uint32_t TILE = AttnTile<DP>::BYTES;
+  // barrier slots
+  static constexpr int Q_FULL = 0;               // 2
+  static constexpr int K_FULL = 2;
+  static constexpr int K_EMPTY = K_FULL + NKV;
+  static constexpr int V_FULL = K_EMPTY + NKV;
+  static constexpr int V_EMPTY = V_FULL + NKV;
+  static constexpr int S_FULL = V_EMPTY + NKV;   // 2
+  static constexpr int P_READY = S_FULL + 2;     // 2
+  static constexpr int O_FULL = P_READY + 2;     // 2
+  static constexpr int DRAIN = O_FULL + 2;       // every product of the CTA is done
+  static constexpr int BARS = DRAIN + 1;
+  static constexpr uint32_t OFF_TMEM = BARS * 8, OFF_ABORT = OFF_TMEM + 4;
+  static_assert(OFF_ABORT + 4 <= 1024, "barrier region");
+  static constexpr uint32_t OFF_Q = 1024;
+  static constexpr uint32_t OFF_K = OFF_Q + 2 * TILE;
+  static constexpr uint32_t OFF_V = OFF_K + NKV * TILE;
+  static constexpr uint32_t SMEM = OFF_V + NKV * TILE + 1024;   // + alignment of the base
+  static_assert(SMEM <= 232448, "shared memory");
+  // tensor memory columns: S (and P over it) of the two tiles, then O
+  static constexpr uint32_t S_COL = 0, O_COL = 256;
+};
+
+// Key tiles that the queries [i0, i0 + 128) of a sequence need.
+__device__ __forceinline__ int fwd_key_tiles(int i0, int lq, int lk, int causal) {
+  if (i0 >= lq) return 0;
+  const int last = min(i0 + 127, lq - 1);
+  const int hi = causal ? min(lk, last + lk - lq + 1) : lk;
+  return hi > 0 ? (hi + 127) / 128 : 0;
+}
+
+}  // namespace
+
+template <int DP, bool BF16>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    lin_attn_fwd_kernel(const __grid_constant__ AttnFwdMaps maps,
+                        const __grid_constant__ AttnFwdArgs args) {
+  using C = FwdCfg<DP>;
+  extern __shared__ uint8_t smem_raw[];
+  const AttnArgs& a = args.s;
+  const int h = blockIdx.x, b = blockIdx.z;
+  const int i0 = (gridDim.y - 1 - blockIdx.y) * 256;   // longest rows of a causal mask first
+  const SeqRange sq = seq_range(a.cu_q, b, a.tokens_q, a.max_q);
+  if (i0 >= sq.len) return;   // (the whole CTA)
+  const SeqRange sk = seq_range(a.cu_k, b, a.tokens_k, a.max_k);
+  const int n0 = fwd_key_tiles(i0, sq.len, sk.len, a.causal);
+  const int n1 = fwd_key_tiles(i0 + 128, sq.len, sk.len, a.causal);
+  const int n = max(n0, n1);
+  const int hk = h / a.group;
+
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* const gen = smem_raw + (base - smem_u32(smem_raw));
+  auto bar = [&](int slot) { return base + (uint32_t)slot * 8u; };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  volatile int* abort = reinterpret_cast<volatile int*>(gen + C::OFF_ABORT);
+  const WaitCtl ctl{a.timeout_ns, abort, a.status};
+
+  if (warp == kAttnMmaWarp) {
+    tmem_alloc(base + C::OFF_TMEM, 512);
+    tmem_relinquish_alloc_permit();
+  }
+  if (tid == 0) {
+    *abort = 0;
+    for (int i = 0; i < C::BARS; ++i)
+      mbar_init(bar(i), i >= C::P_READY && i < C::P_READY + 2 ? 128 : 1);
+    fence_barrier_init();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gen + C::OFF_TMEM);
+
+  if (warp == kAttnCopyWarp) {
+    if (lane == 0 && n > 0) {
+      const int z = sq.start + i0;
+      int k_issued = 0, v_issued = 0;
+      bool second = false;
+      if (n0 > 0) {   // (the first rows of a causal mask may see no key at all)
+        mbar_arrive_expect_tx(bar(C::Q_FULL), C::TILE);
+        load_tile<DP>(base + C::OFF_Q, &maps.q, h, z, bar(C::Q_FULL));
+      }
+      for (int j = 0; j < n; ++j) {
+        const int s = j % C::NKV, round = j / C::NKV;
+        if (round > 0 && !wait_phase(bar(C::K_EMPTY + s), (round - 1) & 1, ctl)) break;
+        mbar_arrive_expect_tx(bar(C::K_FULL + s), C::TILE);
+        load_tile<DP>(base + C::OFF_K + s * C::TILE, &maps.k, hk, sk.start + j * 128,
+                      bar(C::K_FULL + s));
+        ++k_issued;
+        if (j == 0 && n1 > 0) {
+          mbar_arrive_expect_tx(bar(C::Q_FULL + 1), C::TILE);
+          load_tile<DP>(base + C::OFF_Q + C::TILE, &maps.q, h, z + 128, bar(C::Q_FULL + 1));
+          second = true;
+        }
+        if (round > 0 && !wait_phase(bar(C::V_EMPTY + s), (round - 1) & 1, ctl)) break;
+        mbar_arrive_expect_tx(bar(C::V_FULL + s), C::TILE);
+        load_tile<DP>(base + C::OFF_V + s * C::TILE, &maps.v, hk, sk.start + j * 128,
+                      bar(C::V_FULL + s));
+        ++v_issued;
+      }
+      // no copy may still be in flight when the CTA ends (after a wait that
+      // ran out; otherwise all of these have completed)
+      if (*abort) {
+        if (n0 > 0) wait_phase(bar(C::Q_FULL), 0, ctl, false);
+        if (second) wait_phase(bar(C::Q_FULL + 1), 0, ctl, false);
+        for (int j = max(0, k_issued - C::NKV); j < k_issued; ++j)
+          wait_phase(bar(C::K_FULL + j % C::NKV), (j / C::NKV) & 1, ctl, false);
+        for (int j = max(0, v_issued - C::NKV); j < v_issued; ++j)
+          wait_phase(bar(C::V_FULL + j % C::NKV), (j / C::NKV) & 1, ctl, false);
+      }
+    }
+  } else if (warp == kAttnMmaWarp) {
+    if (n > 0) {
+      const int nt[2] = {n0, n1};
+      auto scores = [&](int t, int j) {   // S_t = Q_t K_j^T
+        if (lane == 0) {
+          umma_entries<DP, BF16>(tmem + C::S_COL + t * 128, base + C::OFF_Q + t * C::TILE,
+                                 base + C::OFF_K + (j % C::NKV) * C::TILE);
+          umma_commit(bar(C::S_FULL + t));
+        }
+        __syncwarp();
+      };
+      bool ok = warp_wait_phase(bar(C::K_FULL), 0, ctl);
+      for (int t = 0; t < 2 && ok; ++t) {
+        if (nt[t] == 0) continue;
+        ok = warp_wait_phase(bar(C::Q_FULL + t), 0, ctl);
+        tc_fence_after_sync();
+        if (ok) scores(t, 0);
+      }
+      if (ok && lane == 0) umma_commit(bar(C::K_EMPTY));
+      for (int j = 0; j < n && ok; ++j) {
+        const int s = j % C::NKV, s1 = (j + 1) % C::NKV;
+        if (j + 1 < n) ok = warp_wait_phase(bar(C::K_FULL + s1), ((j + 1) / C::NKV) & 1, ctl);
+        ok = ok && warp_wait_phase(bar(C::V_FULL + s), (j / C::NKV) & 1, ctl);
+        if (!ok) break;
+        if (sk.len - j * 128 < 128) {
+          zero_rows<DP>(base + C::OFF_V + s * C::TILE, sk.len - j * 128, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (j >= nt[t]) continue;
+          ok = warp_wait_phase(bar(C::P_READY + t), j & 1, ctl);
+          if (!ok) break;
+          tc_fence_after_sync();
+          if (lane == 0) {
+            const uint32_t p = tmem + C::S_COL + t * 128;
+            umma_tokens<DP, BF16>(tmem + C::O_COL + t * DP, p, p + 32,
+                                  base + C::OFF_V + s * C::TILE, j > 0);
+            if (j + 1 >= nt[t]) umma_commit(bar(C::O_FULL + t));
+          }
+          __syncwarp();
+          if (j + 1 < nt[t]) scores(t, j + 1);
+        }
+        if (ok && lane == 0) {
+          umma_commit(bar(C::V_EMPTY + s));
+          if (j + 1 < n) umma_commit(bar(C::K_EMPTY + s1));
+        }
+      }
+      // tensor memory stays allocated until every issued product has finished
+      if (lane == 0) {
+        umma_commit(bar(C::DRAIN));
+        wait_phase(bar(C::DRAIN), 0, ctl, false);
+      }
+      __syncwarp();
+    }
+  } else {
+    const int t = warp >> 2, row = tid & 127;
+    const int nk = t ? n1 : n0;
+    const int i = i0 + t * 128 + row;   // query of the sequence
+    const bool live = i < sq.len;
+    const float c = a.scale * kLog2E;
+    // the last key that this row may see
+    const int lim = live ? (a.causal ? min(sk.len - 1, i + sk.len - sq.len) : sk.len - 1) : -1;
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // 32 lanes per warp, lane field at bit 16
+    const uint32_t s_col = tmem + lanes + C::S_COL + t * 128;
+    const uint32_t o_col = tmem + lanes + C::O_COL + t * DP;
+    float m = -INFINITY, l = 0.0f;
+    bool ok = true;
+    for (int j = 0; j < nk; ++j) {
+      ok = warp_wait_phase(bar(C::S_FULL + t), j & 1, ctl);
+      if (!ok) break;
+      tc_fence_after_sync();
+      uint32_t s[4][32];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(s_col + q * 32, s[q]);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) tmem_wait_ld_x32(s[q]);
+      const int lim_j = lim - j * 128;
+      if (__any_sync(0xffffffffu, lim_j < 127)) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (q * 32 + e > lim_j) s[q][e] = 0xff800000u;   // -inf
+      }
+      float mx[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        mx[q] = __uint_as_float(s[q][0]);
+#pragma unroll
+        for (int e = 1; e < 32; ++e) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][e]));
+      }
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      // (a row without a key so far has m = -inf: the difference is inf)
+      const bool grow = top > m && !((top - m) * c <= 8.0f);
+      if (__any_sync(0xffffffffu, grow)) {
+        const float to = fmaxf(m, top);
+        const float alpha = to > m ? ex2_approx((m - to) * c) : 1.0f;
+        m = to;
+        if (j > 0) {   // P V of the tiles so far is complete: S of this one came behind it
+          l *= alpha;
+#pragma unroll
+          for (int q = 0; q < DP / 32; ++q) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(o_col + q * 32, o);
+            tmem_wait_ld_x32(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st_32x32b_x32(o_col + q * 32, o);
+          }
+        }
+      }
+      const float shift = m == -INFINITY ? 0.0f : -m * c;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        uint32_t p[32];
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const int k = q * 64 + 2 * e;
+          const float x = ex2_approx(fmaf(__uint_as_float(s[k >> 5][k & 31]), c, shift));
+          const float y = ex2_approx(fmaf(__uint_as_float(s[k >> 5][(k & 31) + 1]), c, shift));
+          sum[(e & 1) * 2] += x;
+          sum[(e & 1) * 2 + 1] += y;
+          p[e] = pack16<BF16>(x, y);
+        }
+        tmem_st_32x32b_x32(s_col + q * 32, p);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tmem_wait_st();
+      tc_fence_before_sync();
+      mbar_arrive(bar(C::P_READY + t));
+    }
+    if (ok && nk > 0) {
+      ok = warp_wait_phase(bar(C::O_FULL + t), 0, ctl);
+      tc_fence_after_sync();
+    }
+    if (ok) {
+      // a row without a key: O = 0 and a log-sum-exp of -inf
+      const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // (NaN stays NaN)
+      const int64_t token = sq.start + i;
+      uint16_t* out = args.o.p + token * args.o.token_stride + (int64_t)h * args.o.head_stride;
+#pragma unroll
+      for (int q = 0; q < DP / 32; ++q) {
+        uint32_t o[32];
+        if (nk > 0) {   // (uniform over the warp)
+          tmem_ld_32x32b_x32(o_col + q * 32, o);
+          tmem_wait_ld_x32(o);
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int col = q * 32 + g * 8;
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = __uint_as_float(o[g * 8 + 2 * e]), y = __uint_as_float(o[g * 8 + 2 * e + 1]);
+            w[e] = nk > 0 ? pack16<BF16>(l == 0.0f ? 0.0f : x * inv, l == 0.0f ? 0.0f : y * inv) : 0u;
+          }
+          if (live && col < a.dim) store16(out + col, w[0], w[1], w[2], w[3]);
+        }
+      }
+      if (live)
+        args.lse[(int64_t)h * a.tokens_q + token] =
+            l == 0.0f ? -INFINITY : m * a.scale + logf(l);
+    }
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  __syncthreads();
+  if (warp == kAttnMmaWarp) {
+    tc_fence_after_sync();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+cudaError_t launch_attn_fwd(bool bf16, const AttnFwdMaps& maps, const AttnFwdArgs& args,
+                            int heads_kv, int sequences, cudaStream_t stream) {
+  const dim3 grid((unsigned)(heads_kv * args.s.group), (unsigned)((args.s.max_q + 255) / 256),
+                  (unsigned)sequences);
+  auto go = [&](auto kernel, uint32_t smem) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, kAttnThreads, smem, stream>>>(maps, args);
+    return cudaGetLastError();
+  };
+  if (args.s.dim <= 64)
+    return bf16 ? go(lin_attn_fwd_kernel<64, true>, FwdCfg<64>::SMEM)
+                : go(lin_attn_fwd_kernel<64, false>, FwdCfg<64>::SMEM);
+  return bf16 ? go(lin_attn_fwd_kernel<128, true>, FwdCfg<128>::SMEM)
+              : go(lin_attn_fwd_kernel<128, false>, FwdCfg<128>::SMEM);
+}
+
+}  // namespace lin

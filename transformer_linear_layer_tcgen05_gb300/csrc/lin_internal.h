@@ -246,6 +246,24 @@ lin_status checked_device(int* dev);
 cudaMemPool_t device_pool(int dev);
 // What lin_last_launch_info() reports for the calling thread.
 void set_last_launch_info(int kernels, uint64_t workspace_bytes);
+// The pieces of lin_api.cu that the entry points of other files share: the
+// current device after the library's checks and its status record, a
+// buffer's checks, the error record, and the SM count.
+lin_status current_device(int* dev_out, int** status_word);
+lin_status check_buffer(const void* p, uint64_t bytes, int dev);
+bool overlaps(const void* a, uint64_t abytes, const void* b, uint64_t bbytes);
+lin_status cuda_fail(cudaError_t e);
+int sm_count(int dev);
+// Tensor map of a [tokens][heads][dim] tensor of 16-bit entries (strides in
+// bytes) in boxes of 128 tokens x 1 head x 64 entries, 128-byte swizzle.
+bool encode_heads(CUtensorMap* m, const void* base, uint64_t dim, uint64_t heads, uint64_t tokens,
+                  uint64_t head_bytes, uint64_t token_bytes);
+// Workspace in stream order from the library's pool (a graph memory node on
+// a stream under capture); null if there is none to be had. Given back by
+// cudaFreeAsync on the same stream.
+void* take_stream_workspace(int dev, size_t bytes, cudaStream_t stream);
+// Limit of one wait inside a kernel.
+uint64_t wait_limit_ns();
 // A forward form (0 matmul, 1 residual, 2 SwiGLU) on buffers that are pieces
 // of the library's own device allocations (no allocation-range checks).
 lin_status run_forward_staged(int form, bool w16, const float* X, const float* G, const float* U,

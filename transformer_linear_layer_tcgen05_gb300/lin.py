@@ -84,7 +84,26 @@ SIGNATURES = {
     "lin_matmul_residual_w16_host": [_P, _P, _P, _P, _I, _I, _I, _S],
     "lin_matmul_residual_swiglu_a_w16_host": [_P, _P, _P, _P, _P, _I, _I, _I, _S],
     "lin_set_host_block_bytes": [ctypes.c_uint64],
+    "lin_attention": [_P, _P, _P, _P, _P, _P, _S],
+    "lin_attention_backward": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S],
 }
+
+
+class Heads(ctypes.Structure):
+    """lin_heads: a [tokens, heads, dim] tensor, strides in entries."""
+    _fields_ = [("data", _P), ("token_stride", _I), ("head_stride", _I)]
+
+
+class AttentionShape(ctypes.Structure):
+    """lin_attention_shape."""
+    _fields_ = [("dtype", ctypes.c_int32), ("causal", ctypes.c_int32),
+                ("tokens_q", _I), ("tokens_k", _I), ("heads_q", _I), ("heads_kv", _I),
+                ("dim", _I), ("sequences", _I), ("max_q", _I), ("max_k", _I),
+                ("cu_q", _P), ("cu_k", _P), ("scale", _F)]
+
+
+LIN_BINARY16 = 0
+LIN_BFLOAT16 = 1
 
 _lib = None
 
@@ -389,6 +408,103 @@ def lin_gate_up_w16(X, WG16, WU16, GATE, UP, stream=None):
     return GATE, UP
 
 
+# ------------------------------------------------------------ 16-bit head tensors
+
+def _dtype16(t):
+    import torch
+    if t.dtype == torch.float16:
+        return LIN_BINARY16
+    if t.dtype == torch.bfloat16:
+        return LIN_BFLOAT16
+    raise TypeError("16-bit tensors are float16 or bfloat16")
+
+
+def _heads(t, name, like=None):
+    """The lin_heads of a [tokens, heads, dim] CUDA tensor of 16-bit entries
+    (its last dimension contiguous; views of a packed buffer are fine)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
+        raise TypeError(f"{name} must be a CUDA tensor [tokens, heads, dim]")
+    if _dtype16(t) != _dtype16(like if like is not None else t):
+        raise TypeError(f"{name} must have the type of the other tensors")
+    if t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the entries of a head must be contiguous")
+    return Heads(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _offsets(t, name, count=None):
+    import torch
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or \
+            t.dim() != 1 or not t.is_contiguous() or t.numel() < 1:
+        raise TypeError(f"{name} must be a contiguous int32 CUDA tensor of offsets")
+    if count is not None and t.numel() != count:
+        raise ValueError(f"{name} must have {count} entries")
+    return t.data_ptr()
+
+
+def _f32_flat(t, name, shape):
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda or \
+            tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous float32 CUDA tensor {list(shape)}")
+    return t.data_ptr()
+
+
+def _attention_shape(Q, K, V, cu_q, cu_k, max_q, max_k, causal, scale):
+    tq, hq, d = Q.shape
+    tk, hk, dk = K.shape
+    if dk != d or tuple(V.shape) != (tk, hk, d):
+        raise ValueError(f"shape mismatch: Q{tuple(Q.shape)} K{tuple(K.shape)} V{tuple(V.shape)}")
+    if (cu_q is None) != (cu_k is None):
+        raise ValueError("cu_q and cu_k go together")
+    if cu_q is not None and (max_q is None or max_k is None):
+        raise ValueError("packed sequences need max_q and max_k")
+    n = 1 if cu_q is None else cu_q.numel() - 1
+    return AttentionShape(_dtype16(Q), 1 if causal else 0, tq, tk, hq, hk, d, n,
+                          tq if cu_q is None else int(max_q), tk if cu_q is None else int(max_k),
+                          _offsets(cu_q, "cu_q"), _offsets(cu_k, "cu_k", n + 1),
+                          d ** -0.5 if scale is None else float(scale))
+
+
+def lin_attention(Q, K, V, O, LSE, cu_q=None, cu_k=None, max_q=None, max_k=None, causal=True,
+                  scale=None, stream=None):
+    """O = softmax(scale Q K^T) V and LSE, the rows' log-sum-exp.
+
+    Q, O [tokens, heads, dim], K, V [key tokens, key heads, dim]: float16 or
+    bfloat16, dim a multiple of 8 up to 128, views of a packed buffer
+    allowed; LSE [heads, tokens] float32. ``cu_q`` and ``cu_k``: int32
+    offsets of packed sequences (with their longest lengths max_q, max_k),
+    else one sequence. ``scale`` defaults to dim ** -0.5; ``causal`` counts
+    from the end (the last query sees every key)."""
+    q, k, v, o = (_heads(t, n, Q) for t, n in ((Q, "Q"), (K, "K"), (V, "V"), (O, "O")))
+    shape = _attention_shape(Q, K, V, cu_q, cu_k, max_q, max_k, causal, scale)
+    if tuple(O.shape) != tuple(Q.shape):
+        raise ValueError("O must have Q's shape")
+    lse = _f32_flat(LSE, "LSE", (Q.shape[1], Q.shape[0]))
+    r = ctypes.byref
+    _call("lin_attention", r(shape), r(q), r(k), r(v), r(o), lse, _stream_handle(stream))
+    return O, LSE
+
+
+def lin_attention_backward(Q, K, V, O, LSE, DO, DQ, DK, DV, cu_q=None, cu_k=None, max_q=None,
+                           max_k=None, causal=True, scale=None, stream=None):
+    """dQ, dK, dV of lin_attention from dO and that call's inputs and results
+    (dK and dV summed over the query heads that share a key head)."""
+    ts = [_heads(t, n, Q) for t, n in ((Q, "Q"), (K, "K"), (V, "V"), (O, "O"), (DO, "dO"),
+                                       (DQ, "dQ"), (DK, "dK"), (DV, "dV"))]
+    shape = _attention_shape(Q, K, V, cu_q, cu_k, max_q, max_k, causal, scale)
+    for t, n, like in ((O, "O", Q), (DO, "dO", Q), (DQ, "dQ", Q), (DK, "dK", K), (DV, "dV", V)):
+        if tuple(t.shape) != tuple(like.shape):
+            raise ValueError(f"{n} must be {list(like.shape)}")
+    lse = _f32_flat(LSE, "LSE", (Q.shape[1], Q.shape[0]))
+    r = ctypes.byref
+    _call("lin_attention_backward", r(shape), r(ts[0]), r(ts[1]), r(ts[2]), r(ts[3]), lse,
+          r(ts[4]), r(ts[5]), r(ts[6]), r(ts[7]), _stream_handle(stream))
+    return DQ, DK, DV
+
+
 def lin_last_launch_info() -> tuple:
     """(kernels launched, workspace bytes taken) by the last compute call made
     on this thread."""
@@ -523,6 +639,8 @@ FORM_FUNCS = {
 OTHER_FUNCS = {
     "lm_head_cross_entropy_w16": lin_lm_head_cross_entropy_w16,
     "gate_up_w16": lin_gate_up_w16,
+    "attention": lin_attention,
+    "attention_backward": lin_attention_backward,
 }
 
 
