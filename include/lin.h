@@ -405,6 +405,66 @@ lin_status lin_attention_backward(const lin_attention_shape *shape, const lin_he
                                   const lin_heads *DK, const lin_heads *DV, lin_stream_t stream);
 
 /*
+ * Norms and rotation of the query and key heads
+ * ---------------------------------------------
+ * What stands between the QKV projection and attention (the pages name
+ * 04_rope without a description), in one pass: X [tokens, (heads_q + 2
+ * heads_kv) * dim] f32, the projection's rows of query, key and value heads.
+ * Per token and head, with x its dim entries and w = WQ or WK [dim]:
+ *   q, k = turn(w * x / sqrt(mean(x^2) + eps)),   v = x
+ * rounded to the 16-bit type of Q, K and V. turn() takes the pairs (i, i +
+ * rot/2), or (2i, 2i + 1) if interleaved, i < rot/2, of the first rot entries
+ * by the angles of the token's table row: (a cos - b sin, a sin + b cos). COS
+ * and SIN: [table_rows, rot/2] f32; positions: int32 [tokens] (NULL: 0, 1,
+ * ...), held to the table. The backward form is its adjoint: DX (as X) and
+ * DWQ, DWK [dim] from DQ, DK, DV, with x's norm computed again.
+ * dim: a multiple of 8 up to 256; rot: a multiple of 8 up to dim (0: no
+ * rotation, no tables); fewer than 2^40 entries. Q, K, V: lin_heads as for
+ * attention. Outputs overlap nothing (interleaved views of one buffer do
+ * not). All arithmetic in float32; the weights' gradients are summed in a
+ * fixed order. Workspace (backward): 2 * dim floats for each of at most four
+ * CTAs per SM.
+ */
+typedef struct lin_qk_norm_rope_shape {
+  int32_t dtype;         /* lin_dtype of Q, K, V */
+  int32_t interleaved;   /* 0: pairs (i, i + rot/2); 1: pairs (2i, 2i + 1) */
+  int64_t tokens, heads_q, heads_kv, dim, rot, table_rows;
+  float eps;
+} lin_qk_norm_rope_shape;
+
+lin_status lin_qk_norm_rope(const lin_qk_norm_rope_shape *shape, const float *X, const float *WQ,
+                            const float *WK, const float *COS, const float *SIN,
+                            const int32_t *positions, const lin_heads *Q, const lin_heads *K,
+                            const lin_heads *V, lin_stream_t stream);
+lin_status lin_qk_norm_rope_backward(const lin_qk_norm_rope_shape *shape, const float *X,
+                                     const float *WQ, const float *WK, const float *COS,
+                                     const float *SIN, const int32_t *positions,
+                                     const lin_heads *DQ, const lin_heads *DK,
+                                     const lin_heads *DV, float *DX, float *DWQ, float *DWK,
+                                     lin_stream_t stream);
+
+/* Distillation from a teacher's top logits: per row, with z = LOGITS (M rows
+ * of V, ld entries apart; what lm_head writes) and the row's K listed
+ * entries (ids, teacher: [M, K], int32 and f32),
+ *   q = softmax(z / temperature) over all V,
+ *   p = softmax(teacher / temperature) over the listed entries,
+ *   losses[s] = temperature^2 sum_k p_k (log p_k - log q[ids_k]),
+ *   DLOGITS[s, v] = temperature (q_v - p_v) inv_norm   (p_v = 0 if not listed)
+ * and *loss_sum = the sum of the losses (a fixed order). An id outside [0, V)
+ * is an empty place, and so is a teacher logit of -inf; a row of empty places
+ * (padding) has loss 0 and a zero gradient row. An entry listed twice counts
+ * with both probabilities. DLOGITS (rows ldd apart) may be LOGITS itself
+ * (with ldd == ld) or NULL (the losses alone); otherwise outputs overlap
+ * nothing. Only the V entries of a row are read or written. V < 2^31 - 65536,
+ * M < 2^28, K up to 1024; temperature > 0. Rows of any stride; those of
+ * 16-byte units (ld and ldd multiples of 4, 16-byte aligned bases) are read
+ * faster. Arithmetic in float32. */
+lin_status lin_distill_topk(const float *LOGITS, int64_t ld, const int32_t *ids,
+                            const float *teacher, float *DLOGITS, int64_t ldd, float *losses,
+                            float *loss_sum, int64_t M, int64_t V, int64_t K, float temperature,
+                            float inv_norm, lin_stream_t stream);
+
+/*
  * Host-operand forms
  * ------------------
  * lin_<form>_host: the six forward forms above with every operand (X or GATE

@@ -31,7 +31,7 @@ SOURCES = ["lin_api.cu", "lin_kernels_tf32.cu", "lin_kernels_f16.cu",
            "lin_kernels_cluster_swiglu.cu", "lin_kernels_cluster_cvt.cu",
            "lin_kernels_cluster_bt.cu", "lin_kernels_cluster_dual.cu", "lin_loss.cu",
            "lin_noalloc.cu", "lin_host.cu", "lin_attn_fwd.cu", "lin_attn_bwd.cu",
-           "lin_attn_api.cu"]
+           "lin_attn_api.cu", "lin_rope.cu", "lin_distill.cu", "lin_step_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
           "--expt-relaxed-constexpr", "-I", INCLUDE, "-I", CSRC]

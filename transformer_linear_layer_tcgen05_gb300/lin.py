@@ -86,6 +86,9 @@ SIGNATURES = {
     "lin_set_host_block_bytes": [ctypes.c_uint64],
     "lin_attention": [_P, _P, _P, _P, _P, _P, _S],
     "lin_attention_backward": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S],
+    "lin_qk_norm_rope": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S],
+    "lin_qk_norm_rope_backward": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S],
+    "lin_distill_topk": [_P, _I, _P, _P, _P, _I, _P, _P, _I, _I, _I, _F, _F, _S],
 }
 
 
@@ -100,6 +103,13 @@ class AttentionShape(ctypes.Structure):
                 ("tokens_q", _I), ("tokens_k", _I), ("heads_q", _I), ("heads_kv", _I),
                 ("dim", _I), ("sequences", _I), ("max_q", _I), ("max_k", _I),
                 ("cu_q", _P), ("cu_k", _P), ("scale", _F)]
+
+
+class QkNormRopeShape(ctypes.Structure):
+    """lin_qk_norm_rope_shape."""
+    _fields_ = [("dtype", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("tokens", _I),
+                ("heads_q", _I), ("heads_kv", _I), ("dim", _I), ("rot", _I), ("table_rows", _I),
+                ("eps", _F)]
 
 
 LIN_BINARY16 = 0
@@ -505,6 +515,100 @@ def lin_attention_backward(Q, K, V, O, LSE, DO, DQ, DK, DV, cu_q=None, cu_k=None
     return DQ, DK, DV
 
 
+def _qk_norm_rope_args(X, wq, wk, COS, SIN, positions, Q, K, V, eps, interleaved, names):
+    import torch
+    hs = [_heads(t, n, Q) for t, n in zip((Q, K, V), names)]
+    t, hq, d = Q.shape
+    hk = K.shape[1]
+    if tuple(K.shape) != (t, hk, d) or tuple(V.shape) != (t, hk, d) or \
+            tuple(_f32(X, "X").shape) != (t, (hq + 2 * hk) * d):
+        raise ValueError(f"shape mismatch: X{tuple(X.shape)} " + " ".join(
+            f"{n}{tuple(x.shape)}" for n, x in zip(names, (Q, K, V))))
+    w = [_f32_flat(wq, "wq", (d,)), _f32_flat(wk, "wk", (d,))]
+    rot = rows = 0
+    tables = [None, None]
+    if COS is not None or SIN is not None:
+        rows, half = _f32(COS, "COS").shape
+        tables = [COS.data_ptr(), _f32_flat(SIN, "SIN", (rows, half))]
+        rot = 2 * half
+    pos = None
+    if positions is not None:
+        if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32 or \
+                not positions.is_cuda or not positions.is_contiguous() or \
+                tuple(positions.shape) != (t,):
+            raise TypeError("positions must be a contiguous int32 CUDA tensor, one per token")
+        pos = positions.data_ptr()
+    shape = QkNormRopeShape(_dtype16(Q), 1 if interleaved else 0, t, hq, hk, d, rot, rows,
+                            float(eps))
+    r = ctypes.byref
+    return [r(shape), X.data_ptr(), *w, *tables, pos, r(hs[0]), r(hs[1]), r(hs[2])]
+
+
+def lin_qk_norm_rope(X, wq, wk, COS, SIN, positions, Q, K, V, eps=1e-6, interleaved=False,
+                     stream=None):
+    """The heads that attention reads from the QKV projection's rows: per-head
+    RMS norm (weights wq, wk [dim]) and rotation of the query and key heads,
+    the value heads as they are, rounded to 16 bits.
+
+    X [tokens, (heads + 2 key heads) * dim] float32; Q [tokens, heads, dim],
+    K, V [tokens, key heads, dim] float16 or bfloat16, views of a packed
+    buffer allowed; COS, SIN [rows, rot / 2] float32 (None: no rotation);
+    positions int32 [tokens], rows of the tables (None: 0, 1, ...)."""
+    _call("lin_qk_norm_rope",
+          *_qk_norm_rope_args(X, wq, wk, COS, SIN, positions, Q, K, V, eps, interleaved, "QKV"),
+          _stream_handle(stream))
+    return Q, K, V
+
+
+def lin_qk_norm_rope_backward(X, wq, wk, COS, SIN, positions, DQ, DK, DV, DX, dwq, dwk, eps=1e-6,
+                              interleaved=False, stream=None):
+    """dX, dwq, dwk of lin_qk_norm_rope from dQ, dK, dV."""
+    args = _qk_norm_rope_args(X, wq, wk, COS, SIN, positions, DQ, DK, DV, eps, interleaved,
+                              ("dQ", "dK", "dV"))
+    d = DQ.shape[2]
+    _call("lin_qk_norm_rope_backward", *args, _f32_flat(DX, "dX", X.shape),
+          _f32_flat(dwq, "dwq", (d,)), _f32_flat(dwk, "dwk", (d,)), _stream_handle(stream))
+    return DX, dwq, dwk
+
+
+def _f32_rows(t, name, shape=None):
+    """A float32 CUDA matrix with contiguous rows, any row stride."""
+    import torch
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda or t.dim() != 2:
+        raise TypeError(f"{name} must be a float32 CUDA matrix")
+    if (t.shape[1] > 1 and t.stride(1) != 1) or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must have contiguous rows" +
+                         (f" and the shape {tuple(shape)}" if shape is not None else ""))
+    return t
+
+
+def lin_distill_topk(LOGITS, ids, teacher, DLOGITS, losses, loss_sum, temperature=1.0,
+                     inv_norm=1.0, stream=None):
+    """Distillation from a teacher's top logits: per row temperature^2 times
+    the divergence KL(p || q) of q = softmax(LOGITS / temperature) from p =
+    softmax(teacher / temperature) over the row's listed entries, and its
+    gradient (times inv_norm).
+
+    LOGITS [M, V] float32 (any row stride); ids, teacher [M, K] int32 and
+    float32 (an id outside [0, V): an empty place); DLOGITS like LOGITS,
+    LOGITS itself, or None (the losses alone); losses [M], loss_sum [1]."""
+    import torch
+    M, V = _f32_rows(LOGITS, "logits").shape
+    if not isinstance(ids, torch.Tensor) or ids.dtype != torch.int32 or not ids.is_cuda or \
+            ids.dim() != 2 or ids.shape[0] != M or not ids.is_contiguous():
+        raise TypeError("ids must be a contiguous int32 CUDA matrix with a row per row of logits")
+    K = ids.shape[1]
+    t = _f32_flat(teacher, "teacher", (M, K))
+    d, ldd = None, 0
+    if DLOGITS is not None:
+        d = _f32_rows(DLOGITS, "dlogits", LOGITS.shape).data_ptr()
+        ldd = DLOGITS.stride(0)
+    _call("lin_distill_topk", LOGITS.data_ptr(), LOGITS.stride(0), ids.data_ptr(), t, d, ldd,
+          _f32_flat(losses, "losses", (M,)), _f32_flat(loss_sum, "loss_sum", (1,)), M, V, K,
+          float(temperature), float(inv_norm), _stream_handle(stream))
+    return DLOGITS, losses, loss_sum
+
+
 def lin_last_launch_info() -> tuple:
     """(kernels launched, workspace bytes taken) by the last compute call made
     on this thread."""
@@ -641,6 +745,9 @@ OTHER_FUNCS = {
     "gate_up_w16": lin_gate_up_w16,
     "attention": lin_attention,
     "attention_backward": lin_attention_backward,
+    "qk_norm_rope": lin_qk_norm_rope,
+    "qk_norm_rope_backward": lin_qk_norm_rope_backward,
+    "distill_topk": lin_distill_topk,
 }
 
 
