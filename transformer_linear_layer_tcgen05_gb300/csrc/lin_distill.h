@@ -15,9 +15,14 @@ struct DistillArgs {
   int64_t M, V, ld, ldd;
   int32_t K;
   float tau, inv_norm;
-  int32_t cluster, tile;  // CTAs of a row and the logits of each (set at launch)
+  uint64_t timeout_ns;
+  int* status;
+  // set at launch: CTAs of a row, parts of a row to each of them, 16-byte
+  // units of a part, parts that shared memory holds
+  int32_t cluster, segs, tile, slots;
 };
 
-cudaError_t launch_distill(const DistillArgs& a, cudaStream_t stream);
+// The rows' losses and gradients, then the sum of the losses.
+cudaError_t launch_distill(const DistillArgs& a, float* loss_sum, int sms, cudaStream_t stream);
 
 }  // namespace lin

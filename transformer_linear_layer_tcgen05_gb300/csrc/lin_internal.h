@@ -212,9 +212,6 @@ cudaError_t launch_cross_entropy(float* logits, const float4* row_stats, int sta
                                  const int32_t* targets, float* losses, float* loss_sum, int M,
                                  int V, float alpha, float beta, float inv_norm, unsigned* done,
                                  int* status, cudaStream_t stream);
-// *loss_sum = the sum of the M losses, in a fixed order (one CTA, a
-// programmatic dependent of the kernel that writes them).
-cudaError_t launch_sum_losses(const float* losses, int M, float* loss_sum, cudaStream_t stream);
 // Y (+ R) from the partial tiles of a split: tiles tile0 .. tile0 +
 // split_rem - 1 of width `bn` (cluster tiles of `cn` CTAs along N, `num_ng`
 // of them per row block; or, `pair`, tiles of 256 rows whose two CTAs hold

@@ -176,19 +176,6 @@ __global__ void __launch_bounds__(kLossThreads)
   if (threadIdx.x == 0) *out = v;
 }
 
-cudaError_t launch_sum_losses(const float* losses, int M, float* loss_sum, cudaStream_t stream) {
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(1, 1, 1);
-  cfg.blockDim = dim3(kLossThreads, 1, 1);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, lin_sum_losses_kernel, losses, M, loss_sum);
-}
-
 cudaError_t launch_cross_entropy(float* logits, const float4* row_stats, int stats_cols,
                                  const int32_t* targets, float* losses, float* loss_sum, int M,
                                  int V, float alpha, float beta, float inv_norm, unsigned* done,
@@ -207,7 +194,9 @@ cudaError_t launch_cross_entropy(float* logits, const float4* row_stats, int sta
                                      stats_cols, targets, losses, V, alpha, beta, inv_norm, done,
                                      loss_sum, status);
   if (e != cudaSuccess || done) return e;
-  return launch_sum_losses(losses, M, loss_sum, stream);
+  cfg.gridDim = dim3(1, 1, 1);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, lin_sum_losses_kernel, (const float*)losses, M, loss_sum);
 }
 
 }  // namespace lin

@@ -182,9 +182,8 @@ lin_status distill_topk(const float* LOGITS, int64_t ld, const int32_t* ids, con
     return e == cudaSuccess ? LIN_SUCCESS : cuda_fail(e);
   }
   lin::DistillArgs a{LOGITS, ids, teacher, DLOGITS, losses, M, V, ld, ldd, (int32_t)K, tau,
-                     inv_norm, 1, 0};
-  cudaError_t e = lin::launch_distill(a, stream);
-  if (e == cudaSuccess) e = lin::launch_sum_losses(losses, (int)M, loss_sum, stream);
+                     inv_norm, wait_limit_ns(), word, 1, 1, 0, 1};
+  const cudaError_t e = lin::launch_distill(a, loss_sum, sm_count(dev), stream);
   if (e != cudaSuccess) return cuda_fail(e);
   set_last_launch_info(2, 0);
   return LIN_SUCCESS;
