@@ -4,16 +4,16 @@
 //   dz = tau (q - p) inv_norm.
 //
 // Bound by memory: 4 bytes read and, with the gradient, 4 written per logit.
-// Persistent CTAs (clusters of up to eight along a long row) walk over the
-// rows. A bulk copy brings a CTA's part of a row into shared memory, from
-// where it is read twice: for the maximum and the sum of exponentials, the
-// CTA's and the cluster's (through distributed shared memory), and for the
-// gradient, written straight out; the next row's copy follows at once.
-// Several CTAs share an SM, so that one's copy and waits are filled by the
-// others' arithmetic and stores. A warp of its own prepares the teacher's
-// entries one row ahead, since their two dependent loads (id, then its logit)
-// would otherwise stand in every row's way; their places in dz are written
-// again, behind the row, with p taken off.
+// Persistent CTAs (clusters of up to 16 along a long row) walk over the rows.
+// Bulk copies bring a CTA's part of the coming rows into a ring of slots in
+// shared memory, from where a row is read twice: for the maximum and the sum
+// of exponentials, the CTA's and the cluster's (through distributed shared
+// memory), and for the gradient, written straight out. The gradient comes one
+// row later than the sums, so that the exchange between the CTAs, whose
+// latency is near the time of a whole row, stands in nobody's way. Warps of
+// their own prepare the teacher's entries ahead, since their two dependent
+// loads (id, then its logit) would do the same; their places in dz are
+// written again, behind the row, with p taken off.
 //
 // A row is handled in the 16-byte units of memory that it touches, so rows
 // may start anywhere: only the first and the last unit can be partial, and
@@ -28,36 +28,36 @@ namespace lin {
 namespace {
 
 constexpr int kSlots = 3;                // parts of a row in shared memory, at most
+constexpr int kMaxCluster = 16;          // CTAs along a row
+constexpr int kExch = 4;                 // rows whose exchange may be under way (a peer is at
+                                         // most three ahead)
+constexpr int kEnt = 3;                  // rows whose entries are held
 constexpr int kChunk = 4;                // 16-byte units of a thread in registers at once
+constexpr float kDLog2E = 1.4426950408889634f;
+constexpr float kDLn2 = 0.6931471805599453f;
+constexpr float kLowest = -3.402823466e+38f;
 
-// CTAs that an SM's registers are to hold, and the 16-byte units of a slot.
+// CTAs that an SM's registers are to hold, the 16-byte units of a slot, and a
+// CTA's threads (the last warp has the teacher's entries).
 __host__ __device__ constexpr int distill_ctas(int warps) {
   return warps == 8 ? 4 : warps == 4 ? 7 : 16;
 }
 __host__ __device__ constexpr int distill_units(int warps) {
   return warps == 8 ? 4096 : warps * 256;
 }
-constexpr float kDLog2E = 1.4426950408889634f;
-constexpr float kDLn2 = 0.6931471805599453f;
+__host__ __device__ constexpr int distill_threads(int warps) { return (warps + 1) * 32; }
 
-// (m, s): maximum and sum of 2^(x - m), joined; -inf maxima (nothing) are no-ops.
-__device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
-  const float mx = fmaxf(m, m2);
-  if (mx == -INFINITY) {
-    s += s2;   // (both 0, or NaN)
-    return;
-  }
-  s = (m == -INFINITY ? 0.0f : s * ex2_approx(m - mx)) +
-      (m2 == -INFINITY ? 0.0f : s2 * ex2_approx(m2 - mx));
-  m = mx;
-}
-
-__device__ __forceinline__ void warp_join(float& m, float& s) {
+// (m, s): maximum of x and sum of 2^((x - m) c), joined over the warp's lanes.
+// m starts at the type's lowest value, not at -inf, so that a difference of
+// maxima is always a number.
+__device__ __forceinline__ void warp_join(float& m, float& s, float c) {
+  float mx = m;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const float m2 = __shfl_xor_sync(0xffffffffu, m, o), s2 = __shfl_xor_sync(0xffffffffu, s, o);
-    join(m, s, m2, s2);
-  }
+  for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+  s *= ex2_approx((m - mx) * c);
+  m = mx;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
 }
 
 // A row as units of 16 bytes: its first logit is entry `phase` of unit 0.
@@ -78,38 +78,38 @@ __device__ __forceinline__ Row row_units(const float* p, int V) {
 
 }  // namespace
 
-// WARPS warps (and the teacher's) per CTA; a slot of shared memory holds a
+// WARPS warps (and kEnt for the teacher's entries) per CTA; a slot of shared memory holds a
 // CTA's part of a row of up to distill_units() units. A row of more parts
 // than there are slots is streamed twice, for its sum and for its gradient.
 template <int WARPS>
-__global__ void __launch_bounds__(WARPS * 32 + 32, distill_ctas(WARPS))
+__global__ void __launch_bounds__(distill_threads(WARPS), distill_ctas(WARPS))
     lin_distill_kernel(const __grid_constant__ DistillArgs a) {
   constexpr int MAIN = WARPS * 32;
-  __shared__ __align__(8) uint64_t bars[kSlots + 6];
+  __shared__ __align__(8) uint64_t bars[kSlots + kExch + 2 * kEnt];
   __shared__ float2 red[2][WARPS];
-  __shared__ float2 stats[2][8];         // (m, s) of each CTA of the cluster, by the row's parity
-  __shared__ float2 teacher[2];          // sum p (log2 p - z c); whether the row has an entry
+  __shared__ float2 stats[kExch][kMaxCluster];   // (m, s) of each CTA of the cluster
+  __shared__ float4 teacher[kEnt];       // sum p log2 p, sum p z, whether the row has an entry
   __shared__ volatile int abort;
-  extern __shared__ float4 ring[];       // slots x tile units, then 2 x (ids, p, z)[KP]
+  extern __shared__ float4 ring[];       // slots x tile units, then kEnt x (ids, p, z)[KP]
   const int KP = (a.K + 3) & ~3;         // (whole groups of four, the last one padded with -1)
   int* const ids = reinterpret_cast<int*>(ring + a.slots * a.tile);
-  float* const ps = reinterpret_cast<float*>(ids + 2 * KP);
-  float* const zs = ps + 2 * KP;
+  float* const ps = reinterpret_cast<float*>(ids + kEnt * KP);
+  float* const zs = ps + kEnt * KP;
   const int C = a.cluster, rank = C > 1 ? (int)cluster_ctarank() : 0;
   const int V = (int)a.V;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int64_t row0 = blockIdx.x / C, row_step = gridDim.x / C;
   const float c = kDLog2E / a.tau;       // base-2 exponent of a logit
   const uint32_t full = smem_u32(bars);                    // [kSlots] the copies
-  const uint32_t stat_full = full + 8 * kSlots;           // [2] the cluster's (m, s)
-  const uint32_t ent_full = stat_full + 16;                // [2] the teacher's entries
-  const uint32_t ent_empty = ent_full + 16;                // [2]
+  const uint32_t stat_full = full + 8 * kSlots;            // [kExch] the cluster's (m, s)
+  const uint32_t ent_full = stat_full + 8 * kExch;         // [kEnt] the teacher's entries
+  const uint32_t ent_empty = ent_full + 8 * kEnt;          // [kEnt]
   const WaitCtl ctl{a.timeout_ns, &abort, a.status};
   if (tid == 0) {
     abort = 0;
     for (int i = 0; i < kSlots; ++i) mbar_init(full + 8 * i, 1);
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(stat_full + 8 * i, (uint32_t)C);
+    for (int i = 0; i < kExch; ++i) mbar_init(stat_full + 8 * i, (uint32_t)C);
+    for (int i = 0; i < kEnt; ++i) {
       mbar_init(ent_full + 8 * i, 1);
       mbar_init(ent_empty + 8 * i, WARPS);
     }
@@ -117,25 +117,52 @@ __global__ void __launch_bounds__(WARPS * 32 + 32, distill_ctas(WARPS))
   }
   __syncthreads();
   if (C > 1) cluster_sync_all();   // the peers' barriers are ready
+  pdl_launch_dependents();         // (the sum of the losses waits for this grid's end)
 
-  if (warp == WARPS) {   // the teacher's entries of each row, one row ahead
+  if (warp == WARPS) {   // the teacher's entries of each row
+    // (the first 32 are loaded a row ahead of their use)
+    int id_next = -1;
+    float t_next = 0.0f;
+    auto prefetch = [&](int64_t i) {
+      if (i < a.M && lane < a.K) {
+        id_next = a.ids[i * a.K + lane];
+        t_next = a.teacher[i * a.K + lane];
+      }
+    };
+    prefetch(row0);
     int it = 0;
     for (int64_t i = row0; i < a.M; i += row_step, ++it) {
-      const int b = it & 1;
-      if (it >= 2 && !warp_wait_phase(ent_empty + 8 * b, ((it >> 1) - 1) & 1, ctl)) return;
+      const int b = it % kEnt;
+      const int id_first = id_next;
+      const float t_first = t_next;
+      prefetch(i + row_step);
+      if (it >= kEnt) {
+        // (this warp is rows ahead: it leaves the issue slots to the others
+        // while it waits, for about a limit's time at most)
+        int64_t naps = (int64_t)(a.timeout_ns / 200);
+        while (!mbar_try_wait(ent_empty + 8 * b, (it / kEnt - 1) & 1)) {
+          if (abort || --naps < 0) return;
+          __nanosleep(200);
+        }
+        __syncwarp();
+      }
       int* id_b = ids + b * KP;
       float *p_b = ps + b * KP, *z_b = zs + b * KP;
       const float* row = a.logits + i * a.ld;
+      const int phase = row_units(row, V).phase;
       float m = -INFINITY;
       if (lane < KP - a.K) id_b[a.K + lane] = -1;
 #pragma unroll 4
       for (int k = lane; k < a.K; k += 32) {
-        const int id = a.ids[i * a.K + k];
+        const int id = k < 32 ? id_first : a.ids[i * a.K + k];
         const bool ok = id >= 0 && id < V;
-        const float t = ok ? a.teacher[i * a.K + k] * c : -INFINITY;
-        id_b[k] = ok ? id : -1;
+        const float t = ok ? (k < 32 ? t_first : a.teacher[i * a.K + k]) * c : -INFINITY;
         p_b[k] = t;
-        z_b[k] = ok ? row[id] : 0.0f;
+        // (the loss, by rank 0, needs every entry's logit; the gradient those
+        // of the CTA's own part)
+        const bool mine = ok && (C == 1 || ((id + phase) / 4 / a.tile) % C == rank);
+        id_b[k] = mine ? id : -1;
+        z_b[k] = mine || (ok && rank == 0) ? row[id] : 0.0f;
         m = fmaxf(m, t);
       }
 #pragma unroll
@@ -146,36 +173,40 @@ __global__ void __launch_bounds__(WARPS * 32 + 32, distill_ctas(WARPS))
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       const float ls = log2f(s);
-      float kl = 0.0f;
+      float plp = 0.0f, pz = 0.0f;
       for (int k = lane; k < a.K; k += 32) {
         const float lp = p_b[k] - m - ls;
         const float p = any ? ex2_approx(lp) : 0.0f;
         p_b[k] = p;
-        if (p > 0.0f) kl += p * (lp - z_b[k] * c);   // (0 log 0 = 0)
+        if (p > 0.0f) {   // (0 log 0 = 0)
+          plp = fmaf(p, lp, plp);
+          pz = fmaf(p, z_b[k], pz);
+        }
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) kl += __shfl_xor_sync(0xffffffffu, kl, o);
+      for (int o = 16; o > 0; o >>= 1) {
+        plp += __shfl_xor_sync(0xffffffffu, plp, o);
+        pz += __shfl_xor_sync(0xffffffffu, pz, o);
+      }
       __syncwarp();
       // An entry listed twice: its first place takes all of its probability,
-      // the others are marked (-2 - id, so that they are still told apart).
-      auto entry = [](int id) { return id < -1 ? -2 - id : id; };
-      bool twins = false;
+      // the others are marked (-2 - id).
+      uint32_t twin_at = 0;   // the lane's places k0 + lane that have an equal before them
       for (int k0 = 0; k0 < a.K; k0 += 32) {
-        const int k = k0 + lane;
-        const int id = k < a.K ? id_b[k] : -1;
-        bool twin = false;
-        for (int q = 0; q <= k0 + 28 && q < KP; q += 4) {
+        const int id = k0 + lane < a.K ? id_b[k0 + lane] : -1;
+        bool twin = (__match_any_sync(0xffffffffu, id) & ((1u << lane) - 1u)) != 0;
+#pragma unroll 4
+        for (int q = 0; q < k0; q += 4) {
           const int4 o = *reinterpret_cast<const int4*>(id_b + q);
-          twin = twin || (q < k && entry(o.x) == id) || (q + 1 < k && entry(o.y) == id) ||
-                 (q + 2 < k && entry(o.z) == id) || (q + 3 < k && entry(o.w) == id);
+          twin = twin || o.x == id || o.y == id || o.z == id || o.w == id;
         }
-        __syncwarp();
-        if (twin && id >= 0) {
-          id_b[k] = -2 - id;
-          twins = true;
-        }
-        __syncwarp();
+        if (twin && id >= 0) twin_at |= 1u << (k0 >> 5);
       }
+      __syncwarp();
+      const bool twins = twin_at != 0;
+      for (int k = lane; twin_at != 0; k += 32, twin_at >>= 1)
+        if (twin_at & 1u) id_b[k] = -2 - id_b[k];
+      __syncwarp();
       if (__any_sync(0xffffffffu, twins)) {
         for (int k = lane; k < a.K; k += 32) {
           const int id = id_b[k];
@@ -186,7 +217,7 @@ __global__ void __launch_bounds__(WARPS * 32 + 32, distill_ctas(WARPS))
           p_b[k] = p;   // (the marked places' own stay as they were)
         }
       }
-      if (lane == 0) teacher[b] = make_float2(kl, any ? 1.0f : 0.0f);
+      if (lane == 0) teacher[b] = make_float4(plp, pz, any ? 1.0f : 0.0f, 0.0f);
       __syncwarp();
       if (lane == 0) mbar_arrive(ent_full + 8 * b);
     }
@@ -222,141 +253,182 @@ __global__ void __launch_bounds__(WARPS * 32 + 32, distill_ctas(WARPS))
   if (tid == 0)
     for (int i = 0; i < a.slots; ++i) issue();
 
-  // Unit u of row r: entry u - u0 of a slot, or one by one if it is partial;
-  // -inf outside the row.
-  auto unit = [&](const Row& r, const float4* slot, int u, int u0, int u1) -> float4 {
-    if (u >= u1) return make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-    if (u >= r.full0 && u < r.full1) return slot[u - u0];
-    float e[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int v = 4 * u + j - r.phase;
-      e[j] = v >= 0 && v < V ? r.unit0[4 * (int64_t)u + j] : -INFINITY;
+  // The row's entries outside its whole units (at most three before, three
+  // behind) that are in units u0 .. u1 - 1: lanes 0 .. 3 and 4 .. 7 of warp 0
+  // have one each; -1: none.
+  auto edge_entry = [&](const Row& r, int u0, int u1) -> int {
+    if (warp != 0 || lane >= 8) return -1;
+    int v;
+    if (lane < 4) {   // in unit 0
+      if (r.phase == 0 || u0 > 0 || u1 < 1) return -1;
+      v = lane - r.phase;
+    } else {          // in the last unit
+      if (r.full1 < r.full0 || r.full1 >= r.units || r.full1 < u0 || r.full1 >= u1) return -1;
+      v = 4 * r.full1 + (lane - 4) - r.phase;
     }
-    return make_float4(e[0], e[1], e[2], e[3]);
+    return v >= 0 && v < V ? v : -1;
   };
-  int slot_i = 0, slot_round = 0;   // slot and round of the next copy to use
-  auto next_slot = [&]() {
-    if (++slot_i == a.slots) {
-      slot_i = 0;
-      slot_round ^= 1;
+  // The slot of the next copy to use, for the sums and for the gradients (one
+  // after the other from the same one where a row is streamed twice).
+  struct Cursor {
+    int slot, parity;
+  };
+  Cursor at_sums{0, 0}, at_grad{0, 0};
+  auto wait_copy = [&](const Cursor& q) {
+    return warp_wait_phase(full + 8 * q.slot, (uint32_t)q.parity, ctl);
+  };
+  auto advance = [&](Cursor& q) {
+    if (++q.slot == a.slots) {
+      q.slot = 0;
+      q.parity ^= 1;
     }
   };
 
-  int it = 0;   // rows done
-  bool ok = true;
-  for (int64_t i = row0; i < a.M && ok; i += row_step, ++it) {
-    const int b = it & 1;
-    const Row r = row_units(a.logits + i * a.ld, V);
-    float m = -INFINITY, s = 0.0f;
-    const int slot_first = slot_i, round_first = slot_round;
+  // Row `it` of the CTA: maximum and sum of its part, sent to the cluster.
+  auto sums = [&](int it, int64_t i) -> bool {
+    const float* row = a.logits + i * a.ld;
+    const Row r = row_units(row, V);
+    float m = kLowest, s = 0.0f;
     for (int seg = 0; seg < S; ++seg) {
-      ok = warp_wait_phase(full + 8 * slot_i, slot_round, ctl);
-      if (!ok) break;
+      if (!wait_copy(at_sums)) return false;
       const int u0 = unit_begin(seg), u1 = min(u0 + a.tile, r.units);
-      const float4* slot = ring + slot_i * a.tile;
-#pragma unroll 1
-      for (int k = u0 + tid; k < u1; k += kChunk * MAIN) {
-        float4 x[kChunk];
-        float mx = -INFINITY;
+      const int lo = max(u0, r.full0), hi = min(u1, r.full1);
+      const float4* slot = ring + at_sums.slot * a.tile - u0;
+      auto add = [&](const float4* x, int count) {   // (count: a constant)
+        float mx = m;
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) {
-          x[j] = unit(r, slot, k + j * MAIN, u0, u1);
+        for (int j = 0; j < count; ++j)
           mx = fmaxf(mx, fmaxf(fmaxf(x[j].x, x[j].y), fmaxf(x[j].z, x[j].w)));
-        }
-        mx *= c;
-        const float shift = mx == -INFINITY ? 0.0f : -mx;
-        float t0 = 0.0f, t1 = 0.0f;
+        const float2 low = make_float2(-mx, -mx), cc = make_float2(c, c);
+        float2 t0 = make_float2(s * ex2_approx((m - mx) * c), 0.0f), t1 = make_float2(0.0f, 0.0f);
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) {
-          t0 += ex2_approx(fmaf(x[j].x, c, shift)) + ex2_approx(fmaf(x[j].y, c, shift));
-          t1 += ex2_approx(fmaf(x[j].z, c, shift)) + ex2_approx(fmaf(x[j].w, c, shift));
+        for (int j = 0; j < count; ++j) {
+          const float2 u = mul2(add2(make_float2(x[j].x, x[j].y), low), cc);
+          const float2 v = mul2(add2(make_float2(x[j].z, x[j].w), low), cc);
+          t0 = add2(t0, make_float2(ex2_approx(u.x), ex2_approx(u.y)));
+          t1 = add2(t1, make_float2(ex2_approx(v.x), ex2_approx(v.y)));
         }
-        join(m, s, mx, t0 + t1);
+        t0 = add2(t0, t1);
+        m = mx;
+        s = t0.x + t0.y;
+      };
+      int k = lo + tid;
+      for (; k + (kChunk - 1) * MAIN < hi; k += kChunk * MAIN) {
+        float4 x[kChunk];
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) x[j] = slot[k + j * MAIN];
+        add(x, kChunk);
       }
-      next_slot();
+      for (; k < hi; k += MAIN) {
+        const float4 x = slot[k];
+        add(&x, 1);
+      }
+      const int v = edge_entry(r, u0, u1);
+      if (v >= 0) {
+        const float x = row[v], mx = fmaxf(m, x);
+        s = s * ex2_approx((m - mx) * c) + ex2_approx((x - mx) * c);
+        m = mx;
+      }
+      advance(at_sums);
       if (twice) {   // the slot is free again
         named_bar_sync(1, MAIN);
         if (tid == 0) issue();
       }
     }
-    if (!ok) break;
-    warp_join(m, s);
-    if (lane == 0) red[b][warp] = make_float2(m, s);
+    warp_join(m, s, c);
+    if (lane == 0) red[it & 1][warp] = make_float2(m, s);
     named_bar_sync(1, MAIN);
     if (!a.dlogits && !twice && tid == 0)   // (the losses alone: the row is done with)
       for (int seg = 0; seg < S; ++seg) issue();
-    // every warp joins the warps' values by itself, in the same order
-    m = lane < WARPS ? red[b][lane].x : -INFINITY;
-    s = lane < WARPS ? red[b][lane].y : 0.0f;
-    warp_join(m, s);
-    // (before the exchange: a peer may overwrite the row behind it, and the
-    // teacher's warp has read its logits by now)
-    ok = warp_wait_phase(ent_full + 8 * b, (it >> 1) & 1, ctl);
-    if (!ok) break;
-    if (C > 1) {
-      if (warp == 0 && lane < C) {
-        const uint32_t to = mapa_shared(smem_u32(&stats[b][rank]), (uint32_t)lane);
+    if (C > 1 && warp == 0) {
+      // (before the exchange: a peer may overwrite the row behind it, and
+      // this CTA's teacher warp has to have read its logits by then)
+      if (!warp_wait_phase(ent_full + 8 * (it % kEnt), (it / kEnt) & 1, ctl)) return false;
+      m = lane < WARPS ? red[it & 1][lane].x : kLowest;
+      s = lane < WARPS ? red[it & 1][lane].y : 0.0f;
+      warp_join(m, s, c);
+      if (lane < C) {
+        const int e = it % kExch;
+        const uint32_t to = mapa_shared(smem_u32(&stats[e][rank]), (uint32_t)lane);
         asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(m), "f"(s) : "memory");
-        mbar_arrive_remote(mapa_shared(stat_full + 8 * b, (uint32_t)lane));
+        mbar_arrive_remote(mapa_shared(stat_full + 8 * e, (uint32_t)lane));
       }
-      ok = warp_wait_phase_cluster(stat_full + 8 * b, (it >> 1) & 1, ctl);
-      if (!ok) break;
-      m = stats[b][0].x;
-      s = stats[b][0].y;
-      for (int q = 1; q < C; ++q) join(m, s, stats[b][q].x, stats[b][q].y);
     }
-    const float lse = m + log2f(s);   // base 2
-    const bool any = teacher[b].y != 0.0f;
+    return true;
+  };
+
+  // Row `it`: its loss and gradient.
+  auto finish = [&](int it, int64_t i) -> bool {
+    const int b = it % kEnt;
+    if (!warp_wait_phase(ent_full + 8 * b, (it / kEnt) & 1, ctl)) return false;
+    float m, s;
+    if (C > 1) {
+      const int e = it % kExch;
+      if (!warp_wait_phase_cluster(stat_full + 8 * e, (it / kExch) & 1, ctl)) return false;
+      m = lane < C ? stats[e][lane].x : kLowest;
+      s = lane < C ? stats[e][lane].y : 0.0f;
+    } else {
+      m = lane < WARPS ? red[it & 1][lane].x : kLowest;
+      s = lane < WARPS ? red[it & 1][lane].y : 0.0f;
+    }
+    warp_join(m, s, c);   // (each warp by itself, in the same order)
+    const float ls = log2f(s);   // the row's log-sum-exp less its maximum, base 2
+    const float4 tp = teacher[b];
+    const bool any = tp.z != 0.0f;
     if (rank == 0 && tid == 0)
-      a.losses[i] = any ? a.tau * a.tau * kDLn2 * (teacher[b].x + lse) : 0.0f;
+      a.losses[i] = any ? a.tau * a.tau * kDLn2 * (tp.x - (tp.y - m) * c + ls) : 0.0f;
     if (a.dlogits) {
+      const float* row = a.logits + i * a.ld;
+      const Row r = row_units(row, V);
       float* out = a.dlogits + i * a.ldd;
       const float f = any ? a.tau * a.inv_norm : 0.0f;
       // 16-byte stores where the gradient's units lie as the logits' do
       const bool vec = (((reinterpret_cast<uintptr_t>(out) >> 2) - r.phase) & 3u) == 0;
       float* out0 = out - r.phase;
-      if (!twice) {   // the same slots once more
-        slot_i = slot_first;
-        slot_round = round_first;
-      }
       for (int seg = 0; seg < S; ++seg) {
-        if (twice) {
-          ok = warp_wait_phase(full + 8 * slot_i, slot_round, ctl);
-          if (!ok) break;
-        }
+        Cursor& at = twice ? at_sums : at_grad;
+        if (twice && !wait_copy(at)) return false;
         const int u0 = unit_begin(seg), u1 = min(u0 + a.tile, r.units);
-        const float4* slot = ring + slot_i * a.tile;
-#pragma unroll 1
-        for (int k = u0 + tid; k < u1; k += kChunk * MAIN) {
+        const int lo = max(u0, r.full0), hi = min(u1, r.full1);
+        const float4* slot = ring + at.slot * a.tile - u0;
+        const int ve = edge_entry(r, u0, u1);
+        const float edge = ve >= 0 ? row[ve] : 0.0f;   // (before it may be overwritten)
+        auto grad = [&](float x) { return f * ex2_approx(fmaf(x - m, c, -ls)); };
+        const float2 low = make_float2(-m, -m), cc = make_float2(c, c), ll = make_float2(-ls, -ls),
+                     ff = make_float2(f, f);
+        auto put = [&](int u, const float4& x) {
+          const float2 p = fma2(add2(make_float2(x.x, x.y), low), cc, ll);
+          const float2 q = fma2(add2(make_float2(x.z, x.w), low), cc, ll);
+          const float2 g = mul2(make_float2(ex2_approx(p.x), ex2_approx(p.y)), ff);
+          const float2 h = mul2(make_float2(ex2_approx(q.x), ex2_approx(q.y)), ff);
+          float4 y = make_float4(g.x, g.y, h.x, h.y);
+          if (!any) y = make_float4(0.f, 0.f, 0.f, 0.f);   // (whatever the logits hold)
+          float* o = out0 + 4 * (int64_t)u;
+          if (vec) {
+            __stcs(reinterpret_cast<float4*>(o), y);
+          } else {
+            o[0] = y.x;
+            o[1] = y.y;
+            o[2] = y.z;
+            o[3] = y.w;
+          }
+        };
+        int k = lo + tid;
+        for (; k + (kChunk - 1) * MAIN < hi; k += kChunk * MAIN) {
           float4 x[kChunk];
 #pragma unroll
-          for (int j = 0; j < kChunk; ++j) x[j] = unit(r, slot, k + j * MAIN, u0, u1);
+          for (int j = 0; j < kChunk; ++j) x[j] = slot[k + j * MAIN];
 #pragma unroll
-          for (int j = 0; j < kChunk; ++j) {
-            const int u = k + j * MAIN;
-            if (u >= u1) continue;
-            float e[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-#pragma unroll
-            for (int q = 0; q < 4; ++q) e[q] = any ? f * ex2_approx(fmaf(e[q], c, -lse)) : 0.0f;
-            if (vec && u >= r.full0 && u < r.full1) {
-              *reinterpret_cast<float4*>(out0 + 4 * (int64_t)u) = make_float4(e[0], e[1], e[2], e[3]);
-            } else {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int v = 4 * u + q - r.phase;
-                if (v >= 0 && v < V) out[v] = e[q];
-              }
-            }
-          }
+          for (int j = 0; j < kChunk; ++j) put(k + j * MAIN, x[j]);
         }
-        next_slot();
+        for (; k < hi; k += MAIN) put(k, slot[k]);
+        if (ve >= 0) out[ve] = any ? grad(edge) : 0.0f;
+        advance(at);
         if (twice) {
           named_bar_sync(1, MAIN);
           if (tid == 0) issue();
         }
       }
-      if (!ok) break;
       named_bar_sync(1, MAIN);   // the slots are read; the row's stores come before the entries'
       if (!twice && tid == 0)
         for (int seg = 0; seg < S; ++seg) issue();
@@ -365,12 +437,21 @@ __global__ void __launch_bounds__(WARPS * 32 + 32, distill_ctas(WARPS))
       if (any)
         for (int k = tid; k < a.K; k += MAIN) {
           const int id = id_b[k];
-          if (id >= 0 && ((id + r.phase) / 4 / a.tile) % C == rank)
-            out[id] = f * (ex2_approx(fmaf(z_b[k], c, -lse)) - p_b[k]);
+          if (id >= 0) out[id] = f * (ex2_approx(fmaf(z_b[k] - m, c, -ls)) - p_b[k]);
         }
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(ent_empty + 8 * b);
+    return true;
+  };
+
+  // The gradient one row behind the sums where the slots hold two rows' parts
+  // (the losses alone: always), else right behind them.
+  const int delay = a.dlogits && a.slots < 2 * S ? 0 : 1;
+  const int rows = row0 < a.M ? (int)((a.M - row0 + row_step - 1) / row_step) : 0;
+  for (int it = 0; it < rows + delay; ++it) {
+    if (it < rows && !sums(it, row0 + it * row_step)) break;
+    if (it >= delay && !finish(it - delay, row0 + (it - delay) * row_step)) break;
   }
   // no copy may still be in flight when the CTA ends (only after a wait that
   // ran out: every copy is otherwise used)
@@ -402,20 +483,18 @@ __global__ void __launch_bounds__(1024)
 namespace {
 
 template <int WARPS>
-cudaError_t launch_rows(DistillArgs a, int sms, cudaStream_t stream) {
+cudaError_t launch_rows(DistillArgs a, int64_t units, int sms, cudaStream_t stream) {
   constexpr int kMax = distill_units(WARPS);
-  // (a row of V logits touches at most (V + 6) / 4 units)
-  const int64_t units = (a.V + 6) / 4;
   a.cluster = 1;
-  while (a.cluster < 8 && (int64_t)a.cluster * kMax < units) a.cluster *= 2;
+  while (a.cluster < kMaxCluster && (int64_t)a.cluster * kMax < units) a.cluster *= 2;
   const int64_t part = (units + a.cluster - 1) / a.cluster;
   a.segs = (int32_t)((part + kMax - 1) / kMax);
   a.tile = (int32_t)((part + a.segs - 1) / a.segs);
   // slots: what a row needs, and up to two more for the next rows' copies
   // where they cost no CTA of the SM
-  const size_t entries = (size_t)((a.K + 3) & ~3) * 24, slot = (size_t)a.tile * 16;
+  const size_t entries = (size_t)((a.K + 3) & ~3) * 12 * kEnt, slot = (size_t)a.tile * 16;
   auto resident_ctas = [&](int slots) {
-    return std::min<int64_t>(distill_ctas(WARPS), 225 * 1024 / (slots * slot + entries + 1536));
+    return std::min<int64_t>(distill_ctas(WARPS), 225 * 1024 / (slots * slot + entries + 2048));
   };
   a.slots = std::min(a.segs, kSlots);
   while (a.slots < kSlots && resident_ctas(a.slots + 1) == resident_ctas(a.segs)) ++a.slots;
@@ -423,6 +502,8 @@ cudaError_t launch_rows(DistillArgs a, int sms, cudaStream_t stream) {
   auto kernel = lin_distill_kernel<WARPS>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
+  if (e == cudaSuccess && a.cluster > 8)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -430,7 +511,7 @@ cudaError_t launch_rows(DistillArgs a, int sms, cudaStream_t stream) {
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.blockDim = dim3(WARPS * 32 + 32, 1, 1);
+  cfg.blockDim = dim3(distill_threads(WARPS), 1, 1);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = attr;
@@ -448,7 +529,7 @@ cudaError_t launch_rows(DistillArgs a, int sms, cudaStream_t stream) {
     cfg.gridDim = dim3((unsigned)a.cluster, 1, 1);
     e = a.cluster > 1
             ? cudaOccupancyMaxActiveClusters(&n, kernel, &cfg)
-            : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, WARPS * 32 + 32, smem);
+            : cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, distill_threads(WARPS), smem);
     if (e != cudaSuccess) return e;
     if (n < 1) return cudaErrorInvalidConfiguration;
     last = Resident{sms, a.cluster, smem, a.cluster > 1 ? n : (int64_t)n * sms};
@@ -461,12 +542,14 @@ cudaError_t launch_rows(DistillArgs a, int sms, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_distill(const DistillArgs& a, float* loss_sum, int sms, cudaStream_t stream) {
+  // 16-byte units that a row touches: V / 4 where every row starts on one
+  const bool whole = a.ld % 4 == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0;
+  const int64_t units = whole ? (a.V + 3) / 4 : (a.V + 6) / 4;
   // Rows share an SM as far as they fit, so that the waits of one row are
   // filled by others: as few warps to a row as hold it.
-  const int64_t units = (a.V + 6) / 4;
-  cudaError_t e = units <= distill_units(1)   ? launch_rows<1>(a, sms, stream)
-                  : units <= distill_units(4) ? launch_rows<4>(a, sms, stream)
-                                              : launch_rows<8>(a, sms, stream);
+  cudaError_t e = units <= distill_units(1)   ? launch_rows<1>(a, units, sms, stream)
+                  : units <= distill_units(4) ? launch_rows<4>(a, units, sms, stream)
+                                              : launch_rows<8>(a, units, sms, stream);
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

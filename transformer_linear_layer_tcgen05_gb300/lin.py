@@ -21,6 +21,8 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
+from array import array
 
 # LIN_CHECKED=1 loads the checked build (liblin_checked.so: the kernels check
 # their indices and report LIN_ERROR_DEVICE_CHECK; see include/lin.h).
@@ -92,25 +94,9 @@ SIGNATURES = {
 }
 
 
-class Heads(ctypes.Structure):
-    """lin_heads: a [tokens, heads, dim] tensor, strides in entries."""
-    _fields_ = [("data", _P), ("token_stride", _I), ("head_stride", _I)]
-
-
-class AttentionShape(ctypes.Structure):
-    """lin_attention_shape."""
-    _fields_ = [("dtype", ctypes.c_int32), ("causal", ctypes.c_int32),
-                ("tokens_q", _I), ("tokens_k", _I), ("heads_q", _I), ("heads_kv", _I),
-                ("dim", _I), ("sequences", _I), ("max_q", _I), ("max_k", _I),
-                ("cu_q", _P), ("cu_k", _P), ("scale", _F)]
-
-
-class QkNormRopeShape(ctypes.Structure):
-    """lin_qk_norm_rope_shape."""
-    _fields_ = [("dtype", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("tokens", _I),
-                ("heads_q", _I), ("heads_kv", _I), ("dim", _I), ("rot", _I), ("table_rows", _I),
-                ("eps", _F)]
-
+# lin_attention_shape and lin_qk_norm_rope_shape, field by field
+_ATTENTION_SHAPE = struct.Struct("@ii qq qqq q qq PP f4x".replace(" ", ""))
+_QK_NORM_ROPE_SHAPE = struct.Struct("@iiqqqqqqf4x")
 
 LIN_BINARY16 = 0
 LIN_BFLOAT16 = 1
@@ -171,9 +157,11 @@ def check(fn: str, status: int) -> None:
 # ----------------------------------------------------------------- tensor layer
 
 def _stream_handle(stream):
-    import torch
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # (current_stream() builds an object around this handle: 3 us of a
+        # call; the short calls below would feel it)
+        torch = _t()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -419,63 +407,91 @@ def lin_gate_up_w16(X, WG16, WU16, GATE, UP, stream=None):
 
 
 # ------------------------------------------------------------ 16-bit head tensors
+#
+# These calls are short, so their marshalling is too: one array of int64 for
+# all of a call's lin_heads (three fields of eight bytes each), packed bytes
+# for its shape, and torch looked up once.
 
-def _dtype16(t):
-    import torch
-    if t.dtype == torch.float16:
-        return LIN_BINARY16
-    if t.dtype == torch.bfloat16:
-        return LIN_BFLOAT16
-    raise TypeError("16-bit tensors are float16 or bfloat16")
-
-
-def _heads(t, name, like=None):
-    """The lin_heads of a [tokens, heads, dim] CUDA tensor of 16-bit entries
-    (its last dimension contiguous; views of a packed buffer are fine)."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dim() != 3:
-        raise TypeError(f"{name} must be a CUDA tensor [tokens, heads, dim]")
-    if _dtype16(t) != _dtype16(like if like is not None else t):
-        raise TypeError(f"{name} must have the type of the other tensors")
-    if t.shape[2] > 1 and t.stride(2) != 1:
-        raise ValueError(f"{name}: the entries of a head must be contiguous")
-    return Heads(t.data_ptr(), t.stride(0), t.stride(1))
+_torch = None
+_DTYPE16 = {}
 
 
-def _offsets(t, name, count=None):
-    import torch
-    if t is None:
-        return None
+def _t():
+    """torch, imported on first use (importing this module loads nothing)."""
+    global _torch
+    if _torch is None:
+        import torch
+        _DTYPE16.update({torch.float16: LIN_BINARY16, torch.bfloat16: LIN_BFLOAT16})
+        _torch = torch
+    return _torch
+
+
+def _heads(tensors, names):
+    """(dtype, addresses, keep): the lin_heads of [tokens, heads, dim] CUDA
+    tensors of one 16-bit type (the last dimension contiguous; views of a
+    packed buffer are fine); `keep` holds the memory of the addresses."""
+    torch_tensor = _t().Tensor
+    first, fields = None, []
+    for t, name in zip(tensors, names):
+        if not isinstance(t, torch_tensor) or not t.is_cuda or t.dim() != 3:
+            raise TypeError(f"{name} must be a CUDA tensor [tokens, heads, dim]")
+        if first is None:
+            first = t.dtype
+        if t.dtype is not first or first not in _DTYPE16:
+            raise TypeError(f"{name} must be float16 or bfloat16, all of one type")
+        token, head, entry = t.stride()
+        if entry != 1 and t.shape[2] > 1:
+            raise ValueError(f"{name}: the entries of a head must be contiguous")
+        fields += (t.data_ptr(), token, head)
+    keep = array("q", fields)
+    base = keep.buffer_info()[0]
+    return _DTYPE16[first], range(base, base + 8 * len(fields), 24), keep
+
+
+def _int32(t, name, shape):
+    """Address of a contiguous int32 CUDA tensor (None: of any one dimension)."""
+    torch = _t()
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or \
-            t.dim() != 1 or not t.is_contiguous() or t.numel() < 1:
-        raise TypeError(f"{name} must be a contiguous int32 CUDA tensor of offsets")
-    if count is not None and t.numel() != count:
-        raise ValueError(f"{name} must have {count} entries")
+            not t.is_contiguous() or (t.shape != shape if shape is not None else
+                                      t.dim() != 1 or t.numel() < 1):
+        raise TypeError(f"{name} must be a contiguous int32 CUDA tensor" +
+                        (f" {list(shape)}" if shape is not None else ""))
     return t.data_ptr()
 
 
 def _f32_flat(t, name, shape):
-    import torch
+    """Address of a contiguous float32 CUDA tensor of the given shape."""
+    torch = _t()
     if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda or \
-            tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+            t.shape != shape or not t.is_contiguous():
         raise TypeError(f"{name} must be a contiguous float32 CUDA tensor {list(shape)}")
     return t.data_ptr()
 
 
-def _attention_shape(Q, K, V, cu_q, cu_k, max_q, max_k, causal, scale):
+def _attention_shape(dtype, Q, K, V, cu_q, cu_k, max_q, max_k, causal, scale):
     tq, hq, d = Q.shape
     tk, hk, dk = K.shape
-    if dk != d or tuple(V.shape) != (tk, hk, d):
+    if dk != d or V.shape != K.shape:
         raise ValueError(f"shape mismatch: Q{tuple(Q.shape)} K{tuple(K.shape)} V{tuple(V.shape)}")
-    if (cu_q is None) != (cu_k is None):
-        raise ValueError("cu_q and cu_k go together")
-    if cu_q is not None and (max_q is None or max_k is None):
-        raise ValueError("packed sequences need max_q and max_k")
-    n = 1 if cu_q is None else cu_q.numel() - 1
-    return AttentionShape(_dtype16(Q), 1 if causal else 0, tq, tk, hq, hk, d, n,
-                          tq if cu_q is None else int(max_q), tk if cu_q is None else int(max_k),
-                          _offsets(cu_q, "cu_q"), _offsets(cu_k, "cu_k", n + 1),
-                          d ** -0.5 if scale is None else float(scale))
+    n = 1
+    if cu_q is None and cu_k is None:
+        max_q, max_k, cu_q, cu_k = tq, tk, 0, 0
+    else:
+        if cu_q is None or cu_k is None:
+            raise ValueError("cu_q and cu_k go together")
+        if max_q is None or max_k is None:
+            raise ValueError("packed sequences need max_q and max_k")
+        n = cu_k.numel() - 1
+        if cu_q.numel() != n + 1:
+            raise ValueError("cu_q and cu_k must have the same number of entries")
+        cu_q, cu_k = _int32(cu_q, "cu_q", None), _int32(cu_k, "cu_k", None)
+    return _ATTENTION_SHAPE.pack(dtype, 1 if causal else 0, tq, tk, hq, hk, d, n, max_q, max_k,
+                                 cu_q, cu_k, d ** -0.5 if scale is None else scale)
+
+
+def _same_shape(t, name, like):
+    if t.shape != like.shape:
+        raise ValueError(f"{name} must be {list(like.shape)}")
 
 
 def lin_attention(Q, K, V, O, LSE, cu_q=None, cu_k=None, max_q=None, max_k=None, causal=True,
@@ -488,60 +504,50 @@ def lin_attention(Q, K, V, O, LSE, cu_q=None, cu_k=None, max_q=None, max_k=None,
     offsets of packed sequences (with their longest lengths max_q, max_k),
     else one sequence. ``scale`` defaults to dim ** -0.5; ``causal`` counts
     from the end (the last query sees every key)."""
-    q, k, v, o = (_heads(t, n, Q) for t, n in ((Q, "Q"), (K, "K"), (V, "V"), (O, "O")))
-    shape = _attention_shape(Q, K, V, cu_q, cu_k, max_q, max_k, causal, scale)
-    if tuple(O.shape) != tuple(Q.shape):
-        raise ValueError("O must have Q's shape")
-    lse = _f32_flat(LSE, "LSE", (Q.shape[1], Q.shape[0]))
-    r = ctypes.byref
-    _call("lin_attention", r(shape), r(q), r(k), r(v), r(o), lse, _stream_handle(stream))
+    dtype, h, keep = _heads((Q, K, V, O), "QKVO")
+    shape = _attention_shape(dtype, Q, K, V, cu_q, cu_k, max_q, max_k, causal, scale)
+    _same_shape(O, "O", Q)
+    _call("lin_attention", shape, *h,
+          _f32_flat(LSE, "LSE", (Q.shape[1], Q.shape[0])), _stream_handle(stream))
     return O, LSE
+
+
+_BACKWARD_NAMES = ("Q", "K", "V", "O", "dO", "dQ", "dK", "dV")
 
 
 def lin_attention_backward(Q, K, V, O, LSE, DO, DQ, DK, DV, cu_q=None, cu_k=None, max_q=None,
                            max_k=None, causal=True, scale=None, stream=None):
     """dQ, dK, dV of lin_attention from dO and that call's inputs and results
     (dK and dV summed over the query heads that share a key head)."""
-    ts = [_heads(t, n, Q) for t, n in ((Q, "Q"), (K, "K"), (V, "V"), (O, "O"), (DO, "dO"),
-                                       (DQ, "dQ"), (DK, "dK"), (DV, "dV"))]
-    shape = _attention_shape(Q, K, V, cu_q, cu_k, max_q, max_k, causal, scale)
-    for t, n, like in ((O, "O", Q), (DO, "dO", Q), (DQ, "dQ", Q), (DK, "dK", K), (DV, "dV", V)):
-        if tuple(t.shape) != tuple(like.shape):
-            raise ValueError(f"{n} must be {list(like.shape)}")
-    lse = _f32_flat(LSE, "LSE", (Q.shape[1], Q.shape[0]))
-    r = ctypes.byref
-    _call("lin_attention_backward", r(shape), r(ts[0]), r(ts[1]), r(ts[2]), r(ts[3]), lse,
-          r(ts[4]), r(ts[5]), r(ts[6]), r(ts[7]), _stream_handle(stream))
+    dtype, h, keep = _heads((Q, K, V, O, DO, DQ, DK, DV), _BACKWARD_NAMES)
+    shape = _attention_shape(dtype, Q, K, V, cu_q, cu_k, max_q, max_k, causal, scale)
+    for t, name in ((O, "O"), (DO, "dO"), (DQ, "dQ")):
+        _same_shape(t, name, Q)
+    for t, name in ((DK, "dK"), (DV, "dV")):
+        _same_shape(t, name, K)
+    _call("lin_attention_backward", shape, *h[:4],
+          _f32_flat(LSE, "LSE", (Q.shape[1], Q.shape[0])), *h[4:], _stream_handle(stream))
     return DQ, DK, DV
 
 
 def _qk_norm_rope_args(X, wq, wk, COS, SIN, positions, Q, K, V, eps, interleaved, names):
-    import torch
-    hs = [_heads(t, n, Q) for t, n in zip((Q, K, V), names)]
+    dtype, h, keep = _heads((Q, K, V), names)
     t, hq, d = Q.shape
     hk = K.shape[1]
-    if tuple(K.shape) != (t, hk, d) or tuple(V.shape) != (t, hk, d) or \
-            tuple(_f32(X, "X").shape) != (t, (hq + 2 * hk) * d):
+    if K.shape != (t, hk, d) or V.shape != K.shape or \
+            _f32(X, "X").shape != (t, (hq + 2 * hk) * d):
         raise ValueError(f"shape mismatch: X{tuple(X.shape)} " + " ".join(
             f"{n}{tuple(x.shape)}" for n, x in zip(names, (Q, K, V))))
-    w = [_f32_flat(wq, "wq", (d,)), _f32_flat(wk, "wk", (d,))]
     rot = rows = 0
-    tables = [None, None]
+    cos = sin = None
     if COS is not None or SIN is not None:
         rows, half = _f32(COS, "COS").shape
-        tables = [COS.data_ptr(), _f32_flat(SIN, "SIN", (rows, half))]
+        cos, sin = COS.data_ptr(), _f32_flat(SIN, "SIN", (rows, half))
         rot = 2 * half
-    pos = None
-    if positions is not None:
-        if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32 or \
-                not positions.is_cuda or not positions.is_contiguous() or \
-                tuple(positions.shape) != (t,):
-            raise TypeError("positions must be a contiguous int32 CUDA tensor, one per token")
-        pos = positions.data_ptr()
-    shape = QkNormRopeShape(_dtype16(Q), 1 if interleaved else 0, t, hq, hk, d, rot, rows,
-                            float(eps))
-    r = ctypes.byref
-    return [r(shape), X.data_ptr(), *w, *tables, pos, r(hs[0]), r(hs[1]), r(hs[2])]
+    pos = None if positions is None else _int32(positions, "positions", (t,))
+    shape = _QK_NORM_ROPE_SHAPE.pack(dtype, 1 if interleaved else 0, t, hq, hk, d, rot, rows, eps)
+    return keep, (shape, X.data_ptr(), _f32_flat(wq, "wq", (d,)),
+                  _f32_flat(wk, "wk", (d,)), cos, sin, pos, *h)
 
 
 def lin_qk_norm_rope(X, wq, wk, COS, SIN, positions, Q, K, V, eps=1e-6, interleaved=False,
@@ -554,17 +560,17 @@ def lin_qk_norm_rope(X, wq, wk, COS, SIN, positions, Q, K, V, eps=1e-6, interlea
     K, V [tokens, key heads, dim] float16 or bfloat16, views of a packed
     buffer allowed; COS, SIN [rows, rot / 2] float32 (None: no rotation);
     positions int32 [tokens], rows of the tables (None: 0, 1, ...)."""
-    _call("lin_qk_norm_rope",
-          *_qk_norm_rope_args(X, wq, wk, COS, SIN, positions, Q, K, V, eps, interleaved, "QKV"),
-          _stream_handle(stream))
+    keep, args = _qk_norm_rope_args(X, wq, wk, COS, SIN, positions, Q, K, V, eps, interleaved,
+                                    "QKV")
+    _call("lin_qk_norm_rope", *args, _stream_handle(stream))
     return Q, K, V
 
 
 def lin_qk_norm_rope_backward(X, wq, wk, COS, SIN, positions, DQ, DK, DV, DX, dwq, dwk, eps=1e-6,
                               interleaved=False, stream=None):
     """dX, dwq, dwk of lin_qk_norm_rope from dQ, dK, dV."""
-    args = _qk_norm_rope_args(X, wq, wk, COS, SIN, positions, DQ, DK, DV, eps, interleaved,
-                              ("dQ", "dK", "dV"))
+    keep, args = _qk_norm_rope_args(X, wq, wk, COS, SIN, positions, DQ, DK, DV, eps, interleaved,
+                                    ("dQ", "dK", "dV"))
     d = DQ.shape[2]
     _call("lin_qk_norm_rope_backward", *args, _f32_flat(DX, "dX", X.shape),
           _f32_flat(dwq, "dwq", (d,)), _f32_flat(dwk, "dwk", (d,)), _stream_handle(stream))
@@ -573,7 +579,7 @@ def lin_qk_norm_rope_backward(X, wq, wk, COS, SIN, positions, DQ, DK, DV, DX, dw
 
 def _f32_rows(t, name, shape=None):
     """A float32 CUDA matrix with contiguous rows, any row stride."""
-    import torch
+    torch = _t()
     if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda or t.dim() != 2:
         raise TypeError(f"{name} must be a float32 CUDA matrix")
     if (t.shape[1] > 1 and t.stride(1) != 1) or (shape is not None and t.shape != shape):
@@ -592,20 +598,17 @@ def lin_distill_topk(LOGITS, ids, teacher, DLOGITS, losses, loss_sum, temperatur
     LOGITS [M, V] float32 (any row stride); ids, teacher [M, K] int32 and
     float32 (an id outside [0, V): an empty place); DLOGITS like LOGITS,
     LOGITS itself, or None (the losses alone); losses [M], loss_sum [1]."""
-    import torch
     M, V = _f32_rows(LOGITS, "logits").shape
-    if not isinstance(ids, torch.Tensor) or ids.dtype != torch.int32 or not ids.is_cuda or \
-            ids.dim() != 2 or ids.shape[0] != M or not ids.is_contiguous():
-        raise TypeError("ids must be a contiguous int32 CUDA matrix with a row per row of logits")
-    K = ids.shape[1]
-    t = _f32_flat(teacher, "teacher", (M, K))
+    K = ids.shape[-1] if isinstance(ids, _t().Tensor) and ids.dim() == 2 else 0
+    i = _int32(ids, "ids", (M, K))
     d, ldd = None, 0
     if DLOGITS is not None:
         d = _f32_rows(DLOGITS, "dlogits", LOGITS.shape).data_ptr()
         ldd = DLOGITS.stride(0)
-    _call("lin_distill_topk", LOGITS.data_ptr(), LOGITS.stride(0), ids.data_ptr(), t, d, ldd,
-          _f32_flat(losses, "losses", (M,)), _f32_flat(loss_sum, "loss_sum", (1,)), M, V, K,
-          float(temperature), float(inv_norm), _stream_handle(stream))
+    _call("lin_distill_topk", LOGITS.data_ptr(), LOGITS.stride(0), i,
+          _f32_flat(teacher, "teacher", (M, K)), d, ldd, _f32_flat(losses, "losses", (M,)),
+          _f32_flat(loss_sum, "loss_sum", (1,)), M, V, K, temperature, inv_norm,
+          _stream_handle(stream))
     return DLOGITS, losses, loss_sum
 
 
