@@ -17,6 +17,7 @@
 #include "lin_common.cuh"
 #include "lin_rope.h"
 
+#include <algorithm>
 #include <cuda_bf16.h>
 
 namespace lin {
@@ -25,7 +26,7 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kFwdHeads = 4;   // heads of a group's turn
-constexpr int kBwdHeads = 2;   // (the gradient holds x and dy)
+constexpr int kBwdHeads = 4;
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -116,11 +117,10 @@ __global__ void __launch_bounds__(kRopeThreads)
     lin_qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int GROUPS = kRopeThreads / G;
   const int heads = a.hq + 2 * a.hk;
-  const int chunks = (heads + kFwdHeads - 1) / kFwdHeads;
-  const int64_t item = (int64_t)blockIdx.x * GROUPS + threadIdx.x / G;
-  const bool real = item < a.tokens * chunks;   // (a warp's shuffles need all of its lanes)
-  const int64_t t = real ? item / chunks : 0;
-  const int h0 = real ? (int)(item % chunks) * kFwdHeads : heads;
+  const unsigned chunks = (unsigned)((heads + kFwdHeads - 1) / kFwdHeads);
+  const int64_t t = (int64_t)(blockIdx.x / chunks) * GROUPS + threadIdx.x / G;
+  // (a warp's shuffles need all of its lanes: groups behind the last token stay)
+  const int h0 = t < a.tokens ? (int)(blockIdx.x % chunks) * kFwdHeads : heads;
   const Place at = place<INTER>(threadIdx.x % G, a.dim, a.rot);
   Eight x[kFwdHeads];
 #pragma unroll
@@ -157,37 +157,46 @@ __global__ void __launch_bounds__(kRopeThreads)
   }
 }
 
-// The gradient: each group walks over (token, heads) items with a fixed
-// stride and keeps its lanes' share of dwq and dwk; the CTA's groups are
-// added in a fixed order and leave one partial row each, which a second
-// kernel adds.
+// The gradient. The CTAs below a.q_ctas take the query heads, the others the
+// key and the value heads, so that a lane keeps one weight's gradient. Each
+// group walks over (token, heads) items with a fixed stride; the CTA's groups
+// are added in a fixed order and leave one partial row, and a second kernel
+// adds those.
 template <int G, bool INTER, bool BF16>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, 2)
     lin_qk_norm_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int GROUPS = kRopeThreads / G;
   __shared__ float part[GROUPS][G * 8 + 4];
   const int heads = a.hq + 2 * a.hk;
-  const int chunks = (heads + kBwdHeads - 1) / kBwdHeads;
-  const int64_t items = a.tokens * chunks;
+  const bool isq = (int)blockIdx.x < a.q_ctas;
+  const int h_lo = isq ? 0 : a.hq, h_hi = isq ? a.hq : heads;
+  const int cta = isq ? (int)blockIdx.x : (int)blockIdx.x - a.q_ctas;
+  const int ctas = isq ? a.q_ctas : (int)gridDim.x - a.q_ctas;
+  const int chunks = (h_hi - h_lo + kBwdHeads - 1) / kBwdHeads;
   const int group = threadIdx.x / G;
   const Place at = place<INTER>(threadIdx.x % G, a.dim, a.rot);
-  const Eight wq = at.on ? load8f(a.wq, at) : Eight{}, wk = at.on ? load8f(a.wk, at) : Eight{};
-  Eight dwq{}, dwk{};
-  for (int64_t base = (int64_t)blockIdx.x * GROUPS; base < items;
-       base += (int64_t)gridDim.x * GROUPS) {
-    const int64_t item = base + group;
-    const bool real = item < items;
-    const int64_t t = real ? item / chunks : 0;
-    const int h0 = real ? (int)(item % chunks) * kBwdHeads : heads;
+  const Eight w = at.on ? load8f(isq ? a.wq : a.wk, at) : Eight{};
+  const float inv_dim = 1.0f / (float)a.dim;
+  Eight dw{};
+  // items token * chunks + chunk, from cta * GROUPS + group in steps of ctas * GROUPS
+  const int step = ctas * GROUPS, step_t = step / chunks, step_c = step % chunks;
+  int64_t t = (cta * GROUPS + group) / chunks;
+  int chunk = (cta * GROUPS + group) % chunks;
+  // (all groups of a warp go round together: the shuffles need its lanes)
+  for (; __any_sync(0xffffffffu, t < a.tokens); t += step_t) {
+    const int h0 = t < a.tokens ? h_lo + chunk * kBwdHeads : h_hi;
     Eight x[kBwdHeads], g[kBwdHeads];
+    const float* xt = a.x + (t * heads + h0) * a.dim;
 #pragma unroll
     for (int i = 0; i < kBwdHeads; ++i) {
       const int h = h0 + i;
-      x[i] = Eight{};
+      x[i] = at.on && h < h_hi && h < a.hq + a.hk ? load8f(xt + i * a.dim, at) : Eight{};
+    }
+#pragma unroll
+    for (int i = 0; i < kBwdHeads; ++i) {
       g[i] = Eight{};
-      if (!at.on || h >= heads) continue;
-      if (h < a.hq + a.hk) x[i] = load8f(a.x + (t * heads + h) * a.dim, at);
-      const uint16_t* y = head16(a, t, h);
+      if (!at.on || h0 + i >= h_hi) continue;
+      const uint16_t* y = head16(a, t, h0 + i);
       const uint2 u0 = *reinterpret_cast<const uint2*>(y + at.o0);
       const uint2 u1 = *reinterpret_cast<const uint2*>(y + at.o1);
       const uint32_t us[4] = {u0.x, u0.y, u1.x, u1.y};
@@ -199,86 +208,80 @@ __global__ void __launch_bounds__(kRopeThreads)
       }
     }
     float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (at.on && at.turned && h0 < heads) {
+    if (at.on && at.turned && h0 < h_hi) {
       const int64_t row = table_row(a, t) * (a.rot / 2) + at.pair;
       c = *reinterpret_cast<const float4*>(a.cos + row);
       s = *reinterpret_cast<const float4*>(a.sin + row);
     }
+    float* out = a.dx + (t * heads + h0) * a.dim;
 #pragma unroll
     for (int i = 0; i < kBwdHeads; ++i) {
-      const int h = h0 + i;
-      const bool normed = h < a.hq + a.hk;
+      const bool normed = h0 + i < a.hq + a.hk;
       if (normed && at.turned) turn<INTER, true>(g[i], c, s);   // dn
-      const bool isq = h < a.hq;
       float ss = 0.0f, sg = 0.0f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         ss = fmaf(x[i].v[e], x[i].v[e], ss);
-        sg = fmaf(g[i].v[e] * (isq ? wq.v[e] : wk.v[e]), x[i].v[e], sg);
+        sg = fmaf(g[i].v[e] * w.v[e], x[i].v[e], sg);
       }
       ss = group_sum<G>(ss);
       sg = group_sum<G>(sg);
-      const float r = rsqrtf(ss / (float)a.dim + a.eps);
-      const float k = sg * r * r / (float)a.dim;   // mean(g n) / sqrt(...)
-      if (!at.on || h >= heads) continue;
-      Eight d;
+      const float r = rsqrtf(fmaf(ss, inv_dim, a.eps));
+      const float k = sg * r * r * inv_dim;   // mean(g n) / sqrt(...)
+      if (!at.on || h0 + i >= h_hi) continue;
+      if (normed) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        if (!normed) {
-          d.v[e] = g[i].v[e];
-          continue;
+        for (int e = 0; e < 8; ++e) {
+          dw.v[e] = fmaf(g[i].v[e], x[i].v[e] * r, dw.v[e]);
+          g[i].v[e] = r * (g[i].v[e] * w.v[e] - x[i].v[e] * k);
         }
-        const float dn = g[i].v[e] * x[i].v[e] * r;
-        if (isq)
-          dwq.v[e] += dn;
-        else
-          dwk.v[e] += dn;
-        d.v[e] = r * (g[i].v[e] * (isq ? wq.v[e] : wk.v[e]) - x[i].v[e] * k);
       }
-      float* out = a.dx + (t * heads + h) * a.dim;
-      *reinterpret_cast<float4*>(out + at.o0) = make_float4(d.v[0], d.v[1], d.v[2], d.v[3]);
-      *reinterpret_cast<float4*>(out + at.o1) = make_float4(d.v[4], d.v[5], d.v[6], d.v[7]);
+      const float* d = g[i].v;
+      *reinterpret_cast<float4*>(out + i * a.dim + at.o0) = make_float4(d[0], d[1], d[2], d[3]);
+      *reinterpret_cast<float4*>(out + i * a.dim + at.o1) = make_float4(d[4], d[5], d[6], d[7]);
+    }
+    chunk += step_c;
+    if (chunk >= chunks) {
+      chunk -= chunks;
+      ++t;
     }
   }
+  if (at.on) {
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    const Eight& d = which ? dwk : dwq;
-    __syncthreads();
-    if (at.on) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        part[group][at.o0 + e] = d.v[e];
-        part[group][at.o1 + e] = d.v[4 + e];
-      }
+    for (int e = 0; e < 4; ++e) {
+      part[group][at.o0 + e] = dw.v[e];
+      part[group][at.o1 + e] = dw.v[4 + e];
     }
-    __syncthreads();
-    for (int col = threadIdx.x; col < a.dim; col += kRopeThreads) {
-      float sum = 0.0f;
+  }
+  __syncthreads();
+  for (int col = threadIdx.x; col < a.dim; col += kRopeThreads) {
+    float sum = 0.0f;
 #pragma unroll 8
-      for (int q = 0; q < GROUPS; ++q) sum += part[q][col];
-      a.partial[((int64_t)which * gridDim.x + blockIdx.x) * a.dim + col] = sum;
-    }
+    for (int q = 0; q < GROUPS; ++q) sum += part[q][col];
+    a.partial[(int64_t)blockIdx.x * a.dim + col] = sum;
   }
 }
 
-// dwq and dwk from the CTAs' partial rows [2][rows][dim]: a CTA per 32
-// columns of one of them, its 32 warps each a share of the rows, then a
-// fixed-order sum over the warps.
+// dwq (y 0) from the first q_rows of the CTAs' partial rows, dwk (y 1) from
+// the others: a CTA per 32 columns, its 32 warps each a share of the rows,
+// then a fixed-order sum over the warps.
 __global__ void __launch_bounds__(1024)
-    lin_sum_partial_rows_kernel(const float* __restrict__ partial, int rows, int dim,
+    lin_sum_partial_rows_kernel(const float* __restrict__ partial, int q_rows, int all_rows, int dim,
                                 float* __restrict__ dwq, float* __restrict__ dwk) {
   __shared__ float part[32][33];
   pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int col = blockIdx.x * 32 + lane;
-  const float* p = partial + (int64_t)blockIdx.y * rows * dim;
+  const int lo = blockIdx.y ? q_rows : 0, hi = blockIdx.y ? all_rows : q_rows;
   float sum = 0.0f;
   if (col < dim)
-    for (int r = warp; r < rows; r += 32) sum += p[(int64_t)r * dim + col];
+#pragma unroll 8
+    for (int r = lo + warp; r < hi; r += 32) sum += partial[(int64_t)r * dim + col];
   part[warp][lane] = sum;
   __syncthreads();
   if (warp == 0 && col < dim) {
     sum = 0.0f;
+#pragma unroll
     for (int w = 0; w < 32; ++w) sum += part[w][lane];
     (blockIdx.y ? dwk : dwq)[col] = sum;
   }
@@ -307,19 +310,24 @@ cudaError_t launch_qk_norm_rope(const RopeArgs& a, bool inter, bool bf16, cudaSt
   return with_shape(a.dim, inter, bf16, [&](auto g, auto i, auto b) {
     constexpr int G = decltype(g)::value;
     constexpr int GROUPS = kRopeThreads / G;
-    const int64_t items = a.tokens * ((a.hq + 2 * a.hk + kFwdHeads - 1) / kFwdHeads);
-    const int64_t grid = (items + GROUPS - 1) / GROUPS;
+    const int64_t grid = (a.tokens + GROUPS - 1) / GROUPS *
+                         ((a.hq + 2 * a.hk + kFwdHeads - 1) / kFwdHeads);
     lin_qk_norm_rope_kernel<G, decltype(i)::value, decltype(b)::value>
         <<<(unsigned)grid, kRopeThreads, 0, stream>>>(a);
     return cudaGetLastError();
   });
 }
 
-int qk_norm_rope_bwd_ctas(const RopeArgs& a, int sms) {
+int qk_norm_rope_bwd_ctas(RopeArgs& a, int sms) {
   const int groups = kRopeThreads / (a.dim <= 32 ? 4 : a.dim <= 64 ? 8 : a.dim <= 128 ? 16 : 32);
-  const int64_t items = a.tokens * ((a.hq + 2 * a.hk + kBwdHeads - 1) / kBwdHeads);
-  const int64_t need = (items + groups - 1) / groups;
-  return (int)(need < (int64_t)sms * 4 ? need : (int64_t)sms * 4);
+  auto need = [&](int heads) {
+    return (a.tokens * ((heads + kBwdHeads - 1) / kBwdHeads) + groups - 1) / groups;
+  };
+  // two CTAs an SM (as many as its registers hold), shared out by the heads
+  const int64_t q = need(a.hq), kv = need(2 * a.hk);
+  const int64_t all = std::min<int64_t>(q + kv, 2 * (int64_t)sms);
+  a.q_ctas = (int32_t)std::min(std::max<int64_t>(all * q / (q + kv), 1), std::max<int64_t>(all - 1, 1));
+  return (int)std::max<int64_t>(all, 2);
 }
 
 cudaError_t launch_qk_norm_rope_bwd(const RopeArgs& a, bool inter, bool bf16, int ctas,
@@ -339,8 +347,8 @@ cudaError_t launch_qk_norm_rope_bwd(const RopeArgs& a, bool inter, bool bf16, in
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, lin_sum_partial_rows_kernel, (const float*)a.partial, ctas, a.dim,
-                            a.dwq, a.dwk);
+  return cudaLaunchKernelEx(&cfg, lin_sum_partial_rows_kernel, (const float*)a.partial, a.q_ctas,
+                            ctas, a.dim, a.dwq, a.dwk);
 }
 
 }  // namespace lin

@@ -20,12 +20,13 @@ struct RopeArgs {
   HeadsPtr q, k, v;       // written (forward) or read (gradient)
   float* dx;              // gradient: as x
   float *dwq, *dwk;       // gradient: [dim]
-  float* partial;         // gradient: [2][CTAs][dim]
+  float* partial;         // gradient: [CTAs][dim]
+  int32_t q_ctas;         // gradient: CTAs that take the query heads (set with their number)
 };
 
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, bool inter, bool bf16, cudaStream_t stream);
-// CTAs of the gradient's kernel (rows of its partial sums).
-int qk_norm_rope_bwd_ctas(const RopeArgs& a, int sms);
+// CTAs of the gradient's kernel (rows of its partial sums); sets a.q_ctas.
+int qk_norm_rope_bwd_ctas(RopeArgs& a, int sms);
 cudaError_t launch_qk_norm_rope_bwd(const RopeArgs& a, bool inter, bool bf16, int ctas,
                                     cudaStream_t stream);
 

@@ -132,7 +132,7 @@ lin_status qk_norm_rope(const lin_qk_norm_rope_shape* s, const float* X, const f
   a.dwq = DWQ;
   a.dwk = DWK;
   const int ctas = lin::qk_norm_rope_bwd_ctas(a, sm_count(dev));
-  const size_t bytes = (size_t)ctas * 2 * (size_t)s->dim * 4;
+  const size_t bytes = (size_t)ctas * (size_t)s->dim * 4;
   a.partial = static_cast<float*>(take_stream_workspace(dev, bytes, stream));
   if (!a.partial) return LIN_ERROR_CUDA;
   cudaError_t e = lin::launch_qk_norm_rope_bwd(a, inter, bf16, ctas, stream);
