@@ -422,7 +422,7 @@ lin_status lin_attention_backward(const lin_attention_shape *shape, const lin_he
  * rotation, no tables); fewer than 2^40 entries. Q, K, V: lin_heads as for
  * attention. Outputs overlap nothing (interleaved views of one buffer do
  * not). All arithmetic in float32; the weights' gradients are summed in a
- * fixed order. Workspace (backward): dim floats for each of at most two CTAs
+ * fixed order. Workspace (backward): dim floats for each of at most four CTAs
  * per SM.
  */
 typedef struct lin_qk_norm_rope_shape {

@@ -25,8 +25,14 @@ namespace lin {
 namespace {
 
 constexpr int kRopeThreads = 256;
-constexpr int kFwdHeads = 4;   // heads of a group's turn
-constexpr int kBwdHeads = 4;
+// Heads of a group's turn and CTAs whose registers an SM holds: the bytes in
+// flight grow with either, and the registers allow one or the other. Two
+// heads in 48 warps an SM (forward) and 32 (gradient) measured best; 16384
+// tokens of 32 + 2 x 8 heads of 128, forward and gradient, us: two heads x 6
+// and 4 CTAs 103 and 170 (5.9 and 6.0 TB/s), four heads x 3 and 2 CTAs 132
+// and 208, one head x 8 and 8 CTAs 120 and 261.
+constexpr int kFwdHeads = 2, kFwdCtas = 6;
+constexpr int kBwdHeads = 2, kBwdCtas = 4;
 
 template <bool BF16>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
@@ -113,7 +119,7 @@ __device__ __forceinline__ uint16_t* head16(const RopeArgs& a, int64_t t, int he
 }  // namespace
 
 template <int G, bool INTER, bool BF16>
-__global__ void __launch_bounds__(kRopeThreads)
+__global__ void __launch_bounds__(kRopeThreads, kFwdCtas)
     lin_qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int GROUPS = kRopeThreads / G;
   const int heads = a.hq + 2 * a.hk;
@@ -163,7 +169,7 @@ __global__ void __launch_bounds__(kRopeThreads)
 // are added in a fixed order and leave one partial row, and a second kernel
 // adds those.
 template <int G, bool INTER, bool BF16>
-__global__ void __launch_bounds__(kRopeThreads, 2)
+__global__ void __launch_bounds__(kRopeThreads, kBwdCtas)
     lin_qk_norm_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int GROUPS = kRopeThreads / G;
   __shared__ float part[GROUPS][G * 8 + 4];
@@ -323,9 +329,9 @@ int qk_norm_rope_bwd_ctas(RopeArgs& a, int sms) {
   auto need = [&](int heads) {
     return (a.tokens * ((heads + kBwdHeads - 1) / kBwdHeads) + groups - 1) / groups;
   };
-  // two CTAs an SM (as many as its registers hold), shared out by the heads
+  // the CTAs that run at once, shared out by the heads
   const int64_t q = need(a.hq), kv = need(2 * a.hk);
-  const int64_t all = std::min<int64_t>(q + kv, 2 * (int64_t)sms);
+  const int64_t all = std::min<int64_t>(q + kv, kBwdCtas * (int64_t)sms);
   a.q_ctas = (int32_t)std::min(std::max<int64_t>(all * q / (q + kv), 1), std::max<int64_t>(all - 1, 1));
   return (int)std::max<int64_t>(all, 2);
 }
