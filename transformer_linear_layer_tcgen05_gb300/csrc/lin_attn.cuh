@@ -38,19 +38,25 @@ __device__ __forceinline__ SeqRange seq_range(const int32_t* cu, int b, int toke
 }
 
 // Sub-tiles, bytes and descriptors of a [128 tokens][DP entries] operand tile.
+// A descriptor's address field counts 16-byte units from bit 0, so the steps
+// of a product add constants to the tile's descriptor.
 template <int DP>
 struct AttnTile {
   static constexpr int SUB = DP / 64;
   static constexpr uint32_t SUB_BYTES = 128 * 128;
   static constexpr uint32_t BYTES = SUB * SUB_BYTES;
-  // K-major, step kk of 16 entries
-  static __device__ __forceinline__ uint64_t k_major(uint32_t tile, int kk) {
-    return umma_desc_sw128(tile + (kk >> 2) * SUB_BYTES + (kk & 3) * 32, 16, 1024);
+  static constexpr uint64_t UNITS = BYTES / 16;
+  // K-major (steps of 16 entries), MN-major (steps of 16 tokens)
+  static __device__ __forceinline__ uint64_t k_major(uint32_t tile) {
+    return umma_desc_sw128(tile, 16, 1024);
   }
-  // MN-major, step kk of 16 tokens
-  static __device__ __forceinline__ uint64_t mn_major(uint32_t tile, int kk) {
-    return umma_desc_sw128(tile + kk * 2048, SUB_BYTES, 1024);
+  static __device__ __forceinline__ uint64_t mn_major(uint32_t tile) {
+    return umma_desc_sw128(tile, SUB_BYTES, 1024);
   }
+  static constexpr uint64_t entry_step(int kk) {
+    return (uint64_t)((kk >> 2) * SUB_BYTES + (kk & 3) * 32) / 16;
+  }
+  static constexpr uint64_t token_step(int kk) { return (uint64_t)kk * 2048 / 16; }
 };
 
 template <bool BF16, bool B_MN, int N>
@@ -79,33 +85,33 @@ __device__ __forceinline__ float2 unpack16(uint32_t v) {
   }
 }
 
-// D[128 x 128] = A B^T over the DP entries of two operand tiles.
+// D[128 x 128] = A B^T over the DP entries of two operand tiles (K-major
+// descriptors).
 template <int DP, bool BF16>
-__device__ __forceinline__ void umma_entries(uint32_t d, uint32_t a, uint32_t b) {
+__device__ __forceinline__ void umma_entries(uint32_t d, uint64_t a, uint64_t b) {
   constexpr uint32_t idesc = attn_idesc<BF16, false, 128>();
 #pragma unroll
   for (int kk = 0; kk < DP / 16; ++kk)
-    umma_f16(d, AttnTile<DP>::k_major(a, kk), AttnTile<DP>::k_major(b, kk), idesc, kk > 0);
+    umma_f16(d, a + AttnTile<DP>::entry_step(kk), b + AttnTile<DP>::entry_step(kk), idesc, kk > 0);
 }
 
-// D[128 x DP] (+)= A B over 128 tokens: A in tensor memory, its first 64
-// tokens in the 32 columns at `a`, the others in those at `a_hi`; B an
-// operand tile.
+// D[128 x DP] (+)= A B over tokens 64 half .. 64 half + 63: A in tensor
+// memory, these tokens in the 32 columns at `a`; B an operand tile (MN-major
+// descriptor). `first`: the accumulator starts here.
 template <int DP, bool BF16>
-__device__ __forceinline__ void umma_tokens(uint32_t d, uint32_t a, uint32_t a_hi, uint32_t b,
-                                            bool accumulate) {
+__device__ __forceinline__ void umma_tokens(uint32_t d, uint32_t a, uint64_t b, int half, bool first) {
   constexpr uint32_t idesc = attn_idesc<BF16, true, DP>();
 #pragma unroll
-  for (int kk = 0; kk < 8; ++kk)
-    umma_f16_tmem_a(d, (kk < 4 ? a : a_hi) + (kk & 3) * 8, AttnTile<DP>::mn_major(b, kk), idesc,
-                    accumulate || kk > 0);
+  for (int kk = 0; kk < 4; ++kk)
+    umma_f16_tmem_a(d, a + kk * 8, b + AttnTile<DP>::token_step(half * 4 + kk), idesc,
+                    kk > 0 || !first);
 }
 
 // Zeroes rows [first, 128) of an operand tile: a contraction over tokens must
 // not meet what lies behind a sequence's end (another sequence's rows, or
 // padding that may hold infinities or NaN, which a zero weight would not
-// remove). One warp, after the copy has landed; the fence orders the stores
-// before the tensor core's reads.
+// remove). One warp, after the copy has landed; a fence then orders the
+// stores before the tensor core's reads.
 template <int DP>
 __device__ __forceinline__ void zero_rows(uint32_t tile, int first, int lane) {
   for (int s = 0; s < AttnTile<DP>::SUB; ++s)

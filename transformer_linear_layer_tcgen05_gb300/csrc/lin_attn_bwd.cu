@@ -32,6 +32,8 @@ namespace {
 
 constexpr float kPShift = 8.0f;     // P^T is scaled by 2^8
 constexpr int kNormExp = 4;         // dO rows count as having a norm near 2^4
+constexpr int kDkvThreads = kAttnThreads + 32;
+constexpr int kTailWarp = 10;       // of the dK, dV kernel: cuts tiles at the sequence's end
 
 template <int DP>
 struct BwdCfg {
@@ -42,10 +44,12 @@ struct BwdCfg {
   static constexpr int EMPTY = FULL + NS;
   static constexpr int S_FULL = EMPTY + NS;      // S complete
   static constexpr int DP_FULL = S_FULL + 1;     // dP complete
-  static constexpr int S_DONE = DP_FULL + 1;     // S read (dQ) / P^T written (dK, dV): 256 threads
-  static constexpr int DS_READY = S_DONE + 1;    // dS written: 256 threads
-  static constexpr int OUT_FULL = DS_READY + 1;  // the sums complete (every product is)
+  static constexpr int S_DONE = DP_FULL + 1;     // 2 halves: S read (dQ) / P^T written (dK, dV)
+  static constexpr int DS_READY = S_DONE + 2;    // 2 halves: dS written
+  static constexpr int TAIL = DS_READY + 2;      // NS: the stage, cut at the sequence's end
+  static constexpr int OUT_FULL = TAIL + NS;     // the sums complete (every product is)
   static constexpr int BARS = OUT_FULL + 1;
+  static constexpr bool by_half(int i) { return i >= S_DONE && i < TAIL; }
   static constexpr uint32_t OFF_TMEM = BARS * 8, OFF_ABORT = OFF_TMEM + 4;
   static_assert(OFF_ABORT + 4 <= 512, "barrier region");
   static constexpr uint32_t OFF_RED = 512;       // 128 floats
@@ -113,14 +117,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (tid == 0) {
     *abort = 0;
     for (int i = 0; i < C::BARS; ++i)
-      mbar_init(bar(i), i == C::S_DONE || i == C::DS_READY ? 256 : 1);
+      mbar_init(bar(i), C::by_half(i) ? 128 : 1);
     fence_barrier_init();
   }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gen + C::OFF_TMEM);
+  // (an allocation of all 512 columns begins at column 0)
+  constexpr uint32_t tmem = 0;
 
+  const int k_left = sk.len - (n - 1) * 128;   // keys of the last tile (128 or more: all)
   if (warp == kAttnCopyWarp) {
     if (lane == 0 && n > 0) {
       mbar_arrive_expect_tx(bar(C::OWN_FULL), 2 * C::TILE);
@@ -140,61 +146,71 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           wait_phase(bar(C::FULL + j % C::NS), (j / C::NS) & 1, ctl, false);
       }
     }
+    __syncwarp();
+    if (n > 0 && k_left < 128) {   // cut the last K tile at the sequence's end (dS K runs over it)
+      const int s = (n - 1) % C::NS;
+      if (warp_wait_phase(bar(C::FULL + s), ((n - 1) / C::NS) & 1, ctl)) {
+        zero_rows<DP>(k_tile(s), k_left, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::TAIL));
+      }
+    }
   } else if (warp == kAttnMmaWarp) {
-    if (n > 0) {
-      auto scores = [&](int j) {   // S = Q K_j^T
-        if (lane == 0) {
-          umma_entries<DP, BF16>(tmem + C::S_COL, q_tile, k_tile(j % C::NS));
-          umma_commit(bar(C::S_FULL));
-        }
-        __syncwarp();
+    if (n > 0 && elect_one()) {   // one thread issues every product
+      const uint64_t q_desc = AttnTile<DP>::k_major(q_tile), do_desc = AttnTile<DP>::k_major(do_tile);
+      const uint64_t k_desc = AttnTile<DP>::k_major(k_tile(0)), v_desc = AttnTile<DP>::k_major(v_tile(0));
+      const uint64_t kt_desc = AttnTile<DP>::mn_major(k_tile(0));
+      constexpr uint64_t STAGE = 2 * AttnTile<DP>::UNITS;
+      auto scores = [&](int s) {   // S = Q K^T, K in stage s
+        umma_entries<DP, BF16>(C::S_COL, q_desc, k_desc + s * STAGE);
+        umma_commit(bar(C::S_FULL));
       };
-      auto dprobs = [&](int j) {   // dP = dO V_j^T
-        if (lane == 0) {
-          umma_entries<DP, BF16>(tmem + C::DP_COL, do_tile, v_tile(j % C::NS));
-          umma_commit(bar(C::DP_FULL));
-        }
-        __syncwarp();
+      auto dprobs = [&](int s) {   // dP = dO V^T
+        umma_entries<DP, BF16>(C::DP_COL, do_desc, v_desc + s * STAGE);
+        umma_commit(bar(C::DP_FULL));
       };
-      auto arrived = [&](int j) {   // K_j and V_j are in shared memory, cut at the sequence's end
-        if (!warp_wait_phase(bar(C::FULL + j % C::NS), (j / C::NS) & 1, ctl)) return false;
-        if (sk.len - j * 128 < 128) {
-          zero_rows<DP>(k_tile(j % C::NS), sk.len - j * 128, lane);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        return true;
+      auto arrived = [&](int j, int s, uint32_t round) {   // K_j, V_j in shared memory
+        return wait_phase(bar(C::FULL + s), round & 1, ctl) &&
+               (j + 1 < n || k_left >= 128 || wait_phase(bar(C::TAIL), 0, ctl));
       };
-      bool ok = warp_wait_phase(bar(C::OWN_FULL), 0, ctl) && arrived(0);
-      tc_fence_after_sync();
+      int s = 0, s1 = 1 % C::NS;
+      uint32_t round1 = C::NS == 1;
+      bool ok = wait_phase(bar(C::OWN_FULL), 0, ctl) && arrived(0, 0, 0);
       if (ok) {
         scores(0);
         dprobs(0);
       }
       for (int j = 0; j < n && ok; ++j) {
         if (j + 1 < n) {
-          ok = arrived(j + 1) && warp_wait_phase(bar(C::S_DONE), j & 1, ctl);
+          ok = arrived(j + 1, s1, round1) && wait_phase(bar(C::S_DONE), j & 1, ctl) &&
+               wait_phase(bar(C::S_DONE + 1), j & 1, ctl);
           if (!ok) break;
           tc_fence_after_sync();
-          scores(j + 1);
+          scores(s1);
         }
-        ok = warp_wait_phase(bar(C::DS_READY), j & 1, ctl);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          ok = ok && wait_phase(bar(C::DS_READY + half), j & 1, ctl);
+          if (!ok) break;
+          tc_fence_after_sync();
+          umma_tokens<DP, BF16>(C::OUT_COL, C::DP_COL + half * 64, kt_desc + s * STAGE, half,
+                                j == 0 && half == 0);
+        }
         if (!ok) break;
-        tc_fence_after_sync();
-        if (lane == 0) {
-          umma_tokens<DP, BF16>(tmem + C::OUT_COL, tmem + C::DP_COL, tmem + C::DP_COL + 64,
-                                k_tile(j % C::NS), j > 0);
-          umma_commit(bar(C::EMPTY + j % C::NS));
+        umma_commit(bar(C::EMPTY + s));
+        if (j + 1 < n) dprobs(s1);
+        s = s1;
+        if (++s1 == C::NS) {
+          s1 = 0;
+          ++round1;
         }
-        __syncwarp();
-        if (j + 1 < n) dprobs(j + 1);
       }
-      if (lane == 0) {   // (also on the way out: tensor memory must be idle at the end)
-        umma_commit(bar(C::OUT_FULL));
-        wait_phase(bar(C::OUT_FULL), 0, ctl, false);
-      }
-      __syncwarp();
+      // (also on the way out: tensor memory must be idle at the end)
+      umma_commit(bar(C::OUT_FULL));
+      wait_phase(bar(C::OUT_FULL), 0, ctl, false);
     }
+    __syncwarp();
   } else {
     const int half = warp >> 2, row = tid & 127;
     const int i = i0 + row;
@@ -263,12 +279,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       tmem_wait_ld_x32(p[0]);
       tmem_wait_ld_x32(p[1]);
       tc_fence_before_sync();
-      mbar_arrive(bar(C::S_DONE));
+      mbar_arrive(bar(C::S_DONE + half));
+      const float2 cc = make_float2(c, c), ll = make_float2(nl, nl);
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          p[q][e] = __float_as_uint(ex2_approx(fmaf(__uint_as_float(p[q][e]), c, nl)));
+        for (int e = 0; e < 32; e += 2) {
+          const float2 x = fma2(make_float2(__uint_as_float(p[q][e]), __uint_as_float(p[q][e + 1])), cc, ll);
+          p[q][e] = __float_as_uint(ex2_approx(x.x));
+          p[q][e + 1] = __float_as_uint(ex2_approx(x.y));
+        }
       ok = warp_wait_phase(bar(C::DP_FULL), j & 1, ctl);
       if (!ok) break;
       tc_fence_after_sync();
@@ -299,12 +319,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         nd = -delta * amp;
         if (half == 0 && live) args.delta[(int64_t)h * a.tokens_q + token] = delta;
       }
+      const float2 aa = make_float2(amp, amp), dd = make_float2(nd, nd);
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          d[q][e] = __float_as_uint(__uint_as_float(p[q][e]) *
-                                    fmaf(__uint_as_float(d[q][e]), amp, nd));
+        for (int e = 0; e < 32; e += 2) {
+          const float2 x = fma2(make_float2(__uint_as_float(d[q][e]), __uint_as_float(d[q][e + 1])), aa, dd);
+          const float2 y = mul2(make_float2(__uint_as_float(p[q][e]), __uint_as_float(p[q][e + 1])), x);
+          d[q][e] = __float_as_uint(y.x);
+          d[q][e + 1] = __float_as_uint(y.y);
+        }
       const int lim_j = lim - j * 128 - half * 64;
       if (__any_sync(0xffffffffu, lim_j < 63)) {   // masked keys, whatever their dP holds
 #pragma unroll
@@ -321,7 +345,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       tmem_st_32x32b_x32(dp_col, w);
       tmem_wait_st();
       tc_fence_before_sync();
-      mbar_arrive(bar(C::DS_READY));
+      mbar_arrive(bar(C::DS_READY + half));
     }
     if (ok && n > 0) {
       ok = warp_wait_phase(bar(C::OUT_FULL), 0, ctl);
@@ -364,7 +388,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 // ---------------------------------------------------------------- dK, dV
 
 template <int DP, bool BF16>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+__global__ void __launch_bounds__(kDkvThreads, 1)
     lin_attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps,
                         const __grid_constant__ AttnBwdArgs args) {
   using C = BwdCfg<DP>;
@@ -381,6 +405,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const int t0 = a.causal ? min(max(k0 - off, 0) / 128, t1) : 0;
   const int per = t1 - t0;
   const int n = per * a.group;
+  const int q_left = sq.len - (t1 - 1) * 128;   // queries of the last tile
   const int h0 = hk * a.group;
 
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -401,7 +426,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (tid == 0) {
     *abort = 0;
     for (int i = 0; i < C::BARS; ++i)
-      mbar_init(bar(i), i == C::S_DONE || i == C::DS_READY ? 256 : 1);
+      mbar_init(bar(i), C::by_half(i) ? 128 : 1);
     fence_barrier_init();
   }
   // the largest row norm of dO that this tile meets (every tile of the
@@ -411,7 +436,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int tiles = (a.max_q + 127) / 128;
     const float* nm = args.norm + ((int64_t)b * a.heads_q + h0) * tiles;
     float big = 0.0f;
-    for (int i = tid; i < tiles * a.group; i += kAttnThreads) big = fmaxf(big, nm[i]);
+    for (int i = tid; i < tiles * a.group; i += kDkvThreads) big = fmaxf(big, nm[i]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
     if (lane == 0) red[warp] = big;
@@ -419,10 +444,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gen + C::OFF_TMEM);
+  // (an allocation of all 512 columns begins at column 0)
+  constexpr uint32_t tmem = 0;
   float big = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kAttnThreads / 32; ++w) big = fmaxf(big, red[w]);
+  for (int w = 0; w < kDkvThreads / 32; ++w) big = fmaxf(big, red[w]);
   const int ne = norm_exponent(big);
   // scale of dP and delta: dS then carries 2^ne, P's 2^8 taken back
   const float damp = pow2i(ne) * pow2i(-(int)kPShift);
@@ -470,71 +496,89 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           wait_phase(bar(C::FULL + it % C::NS), (it / C::NS) & 1, ctl, false);
       }
     }
-  } else if (warp == kAttnMmaWarp) {
-    if (n > 0) {
-      auto scores = [&](int it) {   // S^T = K Q^T
-        if (lane == 0) {
-          umma_entries<DP, BF16>(tmem + C::S_COL, k_tile, q_tile(it % C::NS));
-          umma_commit(bar(C::S_FULL));
-        }
-        __syncwarp();
-      };
-      auto dprobs = [&](int it) {   // dP^T = V dO^T
-        if (lane == 0) {
-          umma_entries<DP, BF16>(tmem + C::DP_COL, v_tile, do_tile(it % C::NS));
-          umma_commit(bar(C::DP_FULL));
-        }
-        __syncwarp();
-      };
-      auto arrived = [&](int it) {   // Q and dO are in shared memory, cut at the sequence's end
+  } else if (warp == kTailWarp) {
+    // Where the last query tile of a head is cut by the sequence's end, this
+    // warp hands every stage on to the products (a phase that nobody waited
+    // for would not be told from the one before it), that tile with the rows
+    // behind the end zeroed: they enter the products that run over the queries.
+    if (n > 0 && q_left < 128) {
+      int tile = 0;
+      for (int it = 0; it < n; ++it) {
         const int s = it % C::NS;
-        if (!warp_wait_phase(bar(C::FULL + s), (it / C::NS) & 1, ctl)) return false;
-        const int left = sq.len - (t0 + it % per) * 128;
-        if (left < 128) {
-          zero_rows<DP>(q_tile(s), left, lane);
-          zero_rows<DP>(do_tile(s), left, lane);
+        if (!warp_wait_phase(bar(C::FULL + s), (it / C::NS) & 1, ctl)) break;
+        if (++tile == per) {
+          tile = 0;
+          zero_rows<DP>(q_tile(s), q_left, lane);
+          zero_rows<DP>(do_tile(s), q_left, lane);
           fence_proxy_async_smem();
-          __syncwarp();
         }
-        return true;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::TAIL + s));
+      }
+    }
+  } else if (warp == kAttnMmaWarp) {
+    if (n > 0 && elect_one()) {   // one thread issues every product
+      const uint64_t k_desc = AttnTile<DP>::k_major(k_tile), v_desc = AttnTile<DP>::k_major(v_tile);
+      const uint64_t q_desc = AttnTile<DP>::k_major(q_tile(0)), do_desc = AttnTile<DP>::k_major(do_tile(0));
+      const uint64_t qt_desc = AttnTile<DP>::mn_major(q_tile(0));
+      const uint64_t dot_desc = AttnTile<DP>::mn_major(do_tile(0));
+      constexpr uint64_t STAGE = 2 * AttnTile<DP>::UNITS;
+      auto scores = [&](int s) {   // S^T = K Q^T, Q in stage s
+        umma_entries<DP, BF16>(C::S_COL, k_desc, q_desc + s * STAGE);
+        umma_commit(bar(C::S_FULL));
       };
-      bool ok = warp_wait_phase(bar(C::OWN_FULL), 0, ctl) && arrived(0);
-      tc_fence_after_sync();
+      auto dprobs = [&](int s) {   // dP^T = V dO^T
+        umma_entries<DP, BF16>(C::DP_COL, v_desc, do_desc + s * STAGE);
+        umma_commit(bar(C::DP_FULL));
+      };
+      const int ready = q_left < 128 ? C::TAIL : C::FULL;
+      auto arrived = [&](int s, uint32_t round) {   // Q and dO are in shared memory
+        return wait_phase(bar(ready + s), round & 1, ctl);
+      };
+      int s = 0, s1 = 1 % C::NS;
+      uint32_t round1 = C::NS == 1;
+      bool ok = wait_phase(bar(C::OWN_FULL), 0, ctl) && arrived(0, 0);
       if (ok) {
         scores(0);
         dprobs(0);
       }
       for (int it = 0; it < n && ok; ++it) {
-        const int s = it % C::NS;
-        ok = warp_wait_phase(bar(C::S_DONE), it & 1, ctl);
-        if (!ok) break;
-        tc_fence_after_sync();
-        if (lane == 0)   // dV += P^T dO
-          umma_tokens<DP, BF16>(tmem + C::OUT_COL, tmem + C::S_COL, tmem + C::S_COL + 64,
-                                do_tile(s), it > 0);
-        __syncwarp();
-        if (it + 1 < n) {
-          ok = arrived(it + 1);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {   // dV += P^T dO
+          ok = ok && wait_phase(bar(C::S_DONE + half), it & 1, ctl);
           if (!ok) break;
-          scores(it + 1);
+          tc_fence_after_sync();
+          umma_tokens<DP, BF16>(C::OUT_COL, C::S_COL + half * 64, dot_desc + s * STAGE, half,
+                                it == 0 && half == 0);
         }
-        ok = warp_wait_phase(bar(C::DS_READY), it & 1, ctl);
         if (!ok) break;
-        tc_fence_after_sync();
-        if (lane == 0) {   // dK += dS^T Q
-          umma_tokens<DP, BF16>(tmem + C::OUT_COL + DP, tmem + C::DP_COL, tmem + C::DP_COL + 64,
-                                q_tile(s), it > 0);
-          umma_commit(bar(C::EMPTY + s));
+        if (it + 1 < n) {
+          ok = arrived(s1, round1);
+          if (!ok) break;
+          scores(s1);
         }
-        __syncwarp();
-        if (it + 1 < n) dprobs(it + 1);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {   // dK += dS^T Q
+          ok = ok && wait_phase(bar(C::DS_READY + half), it & 1, ctl);
+          if (!ok) break;
+          tc_fence_after_sync();
+          umma_tokens<DP, BF16>(C::OUT_COL + DP, C::DP_COL + half * 64, qt_desc + s * STAGE, half,
+                                it == 0 && half == 0);
+        }
+        if (!ok) break;
+        umma_commit(bar(C::EMPTY + s));
+        if (it + 1 < n) dprobs(s1);
+        s = s1;
+        if (++s1 == C::NS) {
+          s1 = 0;
+          ++round1;
+        }
       }
-      if (lane == 0) {   // (also on the way out: tensor memory must be idle at the end)
-        umma_commit(bar(C::OUT_FULL));
-        wait_phase(bar(C::OUT_FULL), 0, ctl, false);
-      }
-      __syncwarp();
+      // (also on the way out: tensor memory must be idle at the end)
+      umma_commit(bar(C::OUT_FULL));
+      wait_phase(bar(C::OUT_FULL), 0, ctl, false);
     }
+    __syncwarp();
   } else {
     const int half = warp >> 2, row = tid & 127;
     const int key = k0 + row;
@@ -560,16 +604,21 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       tmem_ld_32x32b_x32(s_col + 32, p[1]);
       tmem_wait_ld_x32(p[0]);
       tmem_wait_ld_x32(p[1]);
+      const float2 cc = make_float2(c, c), pp = make_float2(damp, damp);
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float4 r = nl[q * 8 + e];
-          const float rs[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            p[q][e * 4 + k] = __float_as_uint(
-                ex2_approx(fmaf(__uint_as_float(p[q][e * 4 + k]), c, rs[k])));
+          uint32_t* x = &p[q][e * 4];
+          const float2 u = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), cc,
+                                make_float2(r.x, r.y));
+          const float2 v = fma2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), cc,
+                                make_float2(r.z, r.w));
+          x[0] = __float_as_uint(ex2_approx(u.x));
+          x[1] = __float_as_uint(ex2_approx(u.y));
+          x[2] = __float_as_uint(ex2_approx(v.x));
+          x[3] = __float_as_uint(ex2_approx(v.y));
         }
       // causal: the key meets the queries from key - off on
       const int from = key - off - i0 - half * 64;
@@ -588,7 +637,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       tmem_st_32x32b_x32(s_col, w);
       tmem_wait_st();
       tc_fence_before_sync();
-      mbar_arrive(bar(C::S_DONE));
+      mbar_arrive(bar(C::S_DONE + half));
       ok = warp_wait_phase(bar(C::DP_FULL), it & 1, ctl);
       if (!ok) break;
       tc_fence_after_sync();
@@ -601,12 +650,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           const float4 r = nd[q * 8 + e];
-          const float rs[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float x = fmaf(__uint_as_float(d[q][e * 4 + k]), damp, rs[k]);
-            d[q][e * 4 + k] = __float_as_uint(__uint_as_float(p[q][e * 4 + k]) * x);
-          }
+          uint32_t* x = &d[q][e * 4];
+          const uint32_t* y = &p[q][e * 4];
+          const float2 u = mul2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])),
+                                fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), pp,
+                                     make_float2(r.x, r.y)));
+          const float2 v = mul2(make_float2(__uint_as_float(y[2]), __uint_as_float(y[3])),
+                                fma2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), pp,
+                                     make_float2(r.z, r.w)));
+          x[0] = __float_as_uint(u.x);
+          x[1] = __float_as_uint(u.y);
+          x[2] = __float_as_uint(v.x);
+          x[3] = __float_as_uint(v.y);
         }
       if (cut) {
 #pragma unroll
@@ -622,7 +677,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       tmem_st_32x32b_x32(dp_col, w);
       tmem_wait_st();
       tc_fence_before_sync();
-      mbar_arrive(bar(C::DS_READY));
+      mbar_arrive(bar(C::DS_READY + half));
     }
     if (ok && n > 0) {
       ok = warp_wait_phase(bar(C::OUT_FULL), 0, ctl);
@@ -667,19 +722,20 @@ cudaError_t launch_attn_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArg
                             int heads_kv, int sequences, cudaStream_t stream) {
   const unsigned tq = (unsigned)((args.s.max_q + 127) / 128);
   const unsigned tk = (unsigned)((args.s.max_k + 127) / 128);
-  auto go = [&](auto kernel, uint32_t smem, dim3 grid) {
+  auto go = [&](auto kernel, uint32_t smem, dim3 grid, int threads) {
     if (grid.x == 0 || grid.y == 0 || grid.z == 0) return cudaSuccess;
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kAttnThreads, smem, stream>>>(maps, args);
+    kernel<<<grid, threads, smem, stream>>>(maps, args);
     return cudaGetLastError();
   };
   auto both = [&](auto dq, auto dkv, uint32_t smem) {
     const cudaError_t e =
-        go(dq, smem, dim3((unsigned)(heads_kv * args.s.group), tq, (unsigned)sequences));
+        go(dq, smem, dim3((unsigned)(heads_kv * args.s.group), tq, (unsigned)sequences),
+           kAttnThreads);
     if (e != cudaSuccess) return e;
-    return go(dkv, smem, dim3((unsigned)heads_kv, tk, (unsigned)sequences));
+    return go(dkv, smem, dim3((unsigned)heads_kv, tk, (unsigned)sequences), kDkvThreads);
   };
   if (args.s.dim <= 64)
     return bf16 ? both(lin_attn_dq_kernel<64, true>, lin_attn_dkv_kernel<64, true>, BwdCfg<64>::SMEM)

@@ -34,9 +34,10 @@ struct FwdCfg {
   static constexpr int V_FULL = K_EMPTY + NKV;
   static constexpr int V_EMPTY = V_FULL + NKV;
   static constexpr int S_FULL = V_EMPTY + NKV;   // 2
-  static constexpr int P_READY = S_FULL + 2;     // 2
-  static constexpr int O_FULL = P_READY + 2;     // 2
-  static constexpr int DRAIN = O_FULL + 2;       // every product of the CTA is done
+  static constexpr int P_READY = S_FULL + 2;     // 2 x 2: first and second half of the keys
+  static constexpr int O_FULL = P_READY + 4;     // 2
+  static constexpr int TAIL = O_FULL + 2;        // the last V tile is cut at the sequence's end
+  static constexpr int DRAIN = TAIL + 1;         // every product of the CTA is done
   static constexpr int BARS = DRAIN + 1;
   static constexpr uint32_t OFF_TMEM = BARS * 8, OFF_ABORT = OFF_TMEM + 4;
   static_assert(OFF_ABORT + 4 <= 1024, "barrier region");
@@ -90,14 +91,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   if (tid == 0) {
     *abort = 0;
     for (int i = 0; i < C::BARS; ++i)
-      mbar_init(bar(i), i >= C::P_READY && i < C::P_READY + 2 ? 128 : 1);
+      mbar_init(bar(i), i >= C::P_READY && i < C::P_READY + 4 ? 128 : 1);
     fence_barrier_init();
   }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(gen + C::OFF_TMEM);
+  // (an allocation of all 512 columns begins at column 0)
+  constexpr uint32_t tmem = 0;
 
+  const int v_left = sk.len - (n - 1) * 128;   // keys of the last tile (128 or more: all)
   if (warp == kAttnCopyWarp) {
     if (lane == 0 && n > 0) {
       const int z = sq.start + i0;
@@ -136,61 +139,72 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           wait_phase(bar(C::V_FULL + j % C::NKV), (j / C::NKV) & 1, ctl, false);
       }
     }
-  } else if (warp == kAttnMmaWarp) {
-    if (n > 0) {
-      const int nt[2] = {n0, n1};
-      auto scores = [&](int t, int j) {   // S_t = Q_t K_j^T
-        if (lane == 0) {
-          umma_entries<DP, BF16>(tmem + C::S_COL + t * 128, base + C::OFF_Q + t * C::TILE,
-                                 base + C::OFF_K + (j % C::NKV) * C::TILE);
-          umma_commit(bar(C::S_FULL + t));
-        }
+    __syncwarp();
+    if (n > 0 && v_left < 128) {   // cut the last V tile at the sequence's end
+      const int s = (n - 1) % C::NKV;
+      if (warp_wait_phase(bar(C::V_FULL + s), ((n - 1) / C::NKV) & 1, ctl)) {
+        zero_rows<DP>(base + C::OFF_V + s * C::TILE, v_left, lane);
+        fence_proxy_async_smem();
         __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::TAIL));
+      }
+    }
+  } else if (warp == kAttnMmaWarp) {
+    if (n > 0 && elect_one()) {   // one thread issues every product
+      const uint64_t q_desc = AttnTile<DP>::k_major(base + C::OFF_Q);
+      const uint64_t k_desc = AttnTile<DP>::k_major(base + C::OFF_K);
+      const uint64_t v_desc = AttnTile<DP>::mn_major(base + C::OFF_V);
+      auto scores = [&](int t, int s) {   // S_t = Q_t K^T, K in stage s
+        umma_entries<DP, BF16>(C::S_COL + t * 128, q_desc + t * AttnTile<DP>::UNITS,
+                               k_desc + s * AttnTile<DP>::UNITS);
+        umma_commit(bar(C::S_FULL + t));
       };
-      bool ok = warp_wait_phase(bar(C::K_FULL), 0, ctl);
+      bool ok = wait_phase(bar(C::K_FULL), 0, ctl);
       for (int t = 0; t < 2 && ok; ++t) {
-        if (nt[t] == 0) continue;
-        ok = warp_wait_phase(bar(C::Q_FULL + t), 0, ctl);
-        tc_fence_after_sync();
+        if ((t ? n1 : n0) == 0) continue;
+        ok = wait_phase(bar(C::Q_FULL + t), 0, ctl);
         if (ok) scores(t, 0);
       }
-      if (ok && lane == 0) umma_commit(bar(C::K_EMPTY));
+      if (ok) umma_commit(bar(C::K_EMPTY));
+      int s = 0, s1 = 1 % C::NKV;           // stages of tiles j and j + 1
+      uint32_t round = 0, round1 = C::NKV == 1;
       for (int j = 0; j < n && ok; ++j) {
-        const int s = j % C::NKV, s1 = (j + 1) % C::NKV;
-        if (j + 1 < n) ok = warp_wait_phase(bar(C::K_FULL + s1), ((j + 1) / C::NKV) & 1, ctl);
-        ok = ok && warp_wait_phase(bar(C::V_FULL + s), (j / C::NKV) & 1, ctl);
-        if (!ok) break;
-        if (sk.len - j * 128 < 128) {
-          zero_rows<DP>(base + C::OFF_V + s * C::TILE, sk.len - j * 128, lane);
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
-        for (int t = 0; t < 2 && ok; ++t) {
-          if (j >= nt[t]) continue;
-          ok = warp_wait_phase(bar(C::P_READY + t), j & 1, ctl);
-          if (!ok) break;
-          tc_fence_after_sync();
-          if (lane == 0) {
-            const uint32_t p = tmem + C::S_COL + t * 128;
-            umma_tokens<DP, BF16>(tmem + C::O_COL + t * DP, p, p + 32,
-                                  base + C::OFF_V + s * C::TILE, j > 0);
-            if (j + 1 >= nt[t]) umma_commit(bar(C::O_FULL + t));
+        if (j + 1 < n) ok = wait_phase(bar(C::K_FULL + s1), round1 & 1, ctl);
+        ok = ok && wait_phase(bar(C::V_FULL + s), round & 1, ctl);
+        if (ok && j + 1 == n && v_left < 128) ok = wait_phase(bar(C::TAIL), 0, ctl);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int nt = t ? n1 : n0;
+          if (j >= nt || !ok) continue;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            ok = ok && wait_phase(bar(C::P_READY + 2 * t + half), j & 1, ctl);
+            if (!ok) break;
+            tc_fence_after_sync();
+            umma_tokens<DP, BF16>(C::O_COL + t * DP, C::S_COL + t * 128 + half * 32,
+                                  v_desc + s * AttnTile<DP>::UNITS, half, j == 0 && half == 0);
           }
-          __syncwarp();
-          if (j + 1 < nt[t]) scores(t, j + 1);
+          if (!ok) break;
+          if (j + 1 < nt)
+            scores(t, s1);
+          else
+            umma_commit(bar(C::O_FULL + t));
         }
-        if (ok && lane == 0) {
-          umma_commit(bar(C::V_EMPTY + s));
-          if (j + 1 < n) umma_commit(bar(C::K_EMPTY + s1));
+        if (!ok) break;
+        umma_commit(bar(C::V_EMPTY + s));
+        if (j + 1 < n) umma_commit(bar(C::K_EMPTY + s1));
+        s = s1;
+        round = round1;
+        if (++s1 == C::NKV) {
+          s1 = 0;
+          ++round1;
         }
       }
       // tensor memory stays allocated until every issued product has finished
-      if (lane == 0) {
-        umma_commit(bar(C::DRAIN));
-        wait_phase(bar(C::DRAIN), 0, ctl, false);
-      }
-      __syncwarp();
+      umma_commit(bar(C::DRAIN));
+      wait_phase(bar(C::DRAIN), 0, ctl, false);
     }
+    __syncwarp();
   } else {
     const int t = warp >> 2, row = tid & 127;
     const int nk = t ? n1 : n0;
@@ -226,9 +240,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       for (int q = 0; q < 4; ++q) {
         mx[q] = __uint_as_float(s[q][0]);
 #pragma unroll
-        for (int e = 1; e < 32; ++e) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][e]));
+        for (int e = 1; e < 31; e += 2)
+          mx[q] = max3(mx[q], __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
+        mx[q] = fmaxf(mx[q], __uint_as_float(s[q][31]));
       }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
       // (a row without a key so far has m = -inf: the difference is inf)
       const bool grow = top > m && !((top - m) * c <= 8.0f);
       if (__any_sync(0xffffffffu, grow)) {
@@ -249,25 +265,28 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
       }
       const float shift = m == -INFINITY ? 0.0f : -m * c;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+      const float2 cc = make_float2(c, c), sh = make_float2(shift, shift);
+      float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < 2; ++q) {   // the product may start on the first half
         uint32_t p[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
           const int k = q * 64 + 2 * e;
-          const float x = ex2_approx(fmaf(__uint_as_float(s[k >> 5][k & 31]), c, shift));
-          const float y = ex2_approx(fmaf(__uint_as_float(s[k >> 5][(k & 31) + 1]), c, shift));
-          sum[(e & 1) * 2] += x;
-          sum[(e & 1) * 2 + 1] += y;
-          p[e] = pack16<BF16>(x, y);
+          float2 x = make_float2(__uint_as_float(s[k >> 5][k & 31]),
+                                 __uint_as_float(s[k >> 5][(k & 31) + 1]));
+          x = fma2(x, cc, sh);
+          x = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+          sum[e & 1] = add2(sum[e & 1], x);
+          p[e] = pack16<BF16>(x.x, x.y);
         }
         tmem_st_32x32b_x32(s_col + q * 32, p);
+        tmem_wait_st();
+        tc_fence_before_sync();
+        mbar_arrive(bar(C::P_READY + 2 * t + q));
       }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      tmem_wait_st();
-      tc_fence_before_sync();
-      mbar_arrive(bar(C::P_READY + t));
+      sum[0] = add2(sum[0], sum[1]);
+      l += sum[0].x + sum[0].y;
     }
     if (ok && nk > 0) {
       ok = warp_wait_phase(bar(C::O_FULL + t), 0, ctl);
