@@ -23,6 +23,15 @@ namespace lin {
 
 namespace {
 
+// Three warpgroups: the two tiles' rows, and the copying and issuing warps
+// (two of the third's stay idle: registers are handed over by whole
+// warpgroups). A thread that holds a row of S wants more than the 168
+// registers of an even share; without the hand-over the loop spilled and the
+// 8192-token case took 578 us instead of 348.
+constexpr int kFwdThreads = 384;
+constexpr int kFwdRegsRow = 208, kFwdRegsIssue = 88;
+static_assert(2 * kFwdRegsRow + kFwdRegsIssue <= 3 * 168, "registers of the launch");
+
 template <int DP>
 struct FwdCfg {
   static constexpr int NKV = DP == 64 ? 3 : 2;   // stages of the K and of the V ring
@@ -61,7 +70,7 @@ __device__ __forceinline__ int fwd_key_tiles(int i0, int lq, int lk, int causal)
 }  // namespace
 
 template <int DP, bool BF16>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+__global__ void __launch_bounds__(kFwdThreads, 1)
     lin_attn_fwd_kernel(const __grid_constant__ AttnFwdMaps maps,
                         const __grid_constant__ AttnFwdArgs args) {
   using C = FwdCfg<DP>;
@@ -101,111 +110,115 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   constexpr uint32_t tmem = 0;
 
   const int v_left = sk.len - (n - 1) * 128;   // keys of the last tile (128 or more: all)
-  if (warp == kAttnCopyWarp) {
-    if (lane == 0 && n > 0) {
-      const int z = sq.start + i0;
-      int k_issued = 0, v_issued = 0;
-      bool second = false;
-      if (n0 > 0) {   // (the first rows of a causal mask may see no key at all)
-        mbar_arrive_expect_tx(bar(C::Q_FULL), C::TILE);
-        load_tile<DP>(base + C::OFF_Q, &maps.q, h, z, bar(C::Q_FULL));
-      }
-      for (int j = 0; j < n; ++j) {
-        const int s = j % C::NKV, round = j / C::NKV;
-        if (round > 0 && !wait_phase(bar(C::K_EMPTY + s), (round - 1) & 1, ctl)) break;
-        mbar_arrive_expect_tx(bar(C::K_FULL + s), C::TILE);
-        load_tile<DP>(base + C::OFF_K + s * C::TILE, &maps.k, hk, sk.start + j * 128,
-                      bar(C::K_FULL + s));
-        ++k_issued;
-        if (j == 0 && n1 > 0) {
-          mbar_arrive_expect_tx(bar(C::Q_FULL + 1), C::TILE);
-          load_tile<DP>(base + C::OFF_Q + C::TILE, &maps.q, h, z + 128, bar(C::Q_FULL + 1));
-          second = true;
+  if (warp >= 8) {
+    setmaxnreg_dec<kFwdRegsIssue>();
+    if (warp == kAttnCopyWarp) {
+      if (lane == 0 && n > 0) {
+        const int z = sq.start + i0;
+        int k_issued = 0, v_issued = 0;
+        bool second = false;
+        if (n0 > 0) {   // (the first rows of a causal mask may see no key at all)
+          mbar_arrive_expect_tx(bar(C::Q_FULL), C::TILE);
+          load_tile<DP>(base + C::OFF_Q, &maps.q, h, z, bar(C::Q_FULL));
         }
-        if (round > 0 && !wait_phase(bar(C::V_EMPTY + s), (round - 1) & 1, ctl)) break;
-        mbar_arrive_expect_tx(bar(C::V_FULL + s), C::TILE);
-        load_tile<DP>(base + C::OFF_V + s * C::TILE, &maps.v, hk, sk.start + j * 128,
-                      bar(C::V_FULL + s));
-        ++v_issued;
+        for (int j = 0; j < n; ++j) {
+          const int s = j % C::NKV, round = j / C::NKV;
+          if (round > 0 && !wait_phase(bar(C::K_EMPTY + s), (round - 1) & 1, ctl)) break;
+          mbar_arrive_expect_tx(bar(C::K_FULL + s), C::TILE);
+          load_tile<DP>(base + C::OFF_K + s * C::TILE, &maps.k, hk, sk.start + j * 128,
+                        bar(C::K_FULL + s));
+          ++k_issued;
+          if (j == 0 && n1 > 0) {
+            mbar_arrive_expect_tx(bar(C::Q_FULL + 1), C::TILE);
+            load_tile<DP>(base + C::OFF_Q + C::TILE, &maps.q, h, z + 128, bar(C::Q_FULL + 1));
+            second = true;
+          }
+          if (round > 0 && !wait_phase(bar(C::V_EMPTY + s), (round - 1) & 1, ctl)) break;
+          mbar_arrive_expect_tx(bar(C::V_FULL + s), C::TILE);
+          load_tile<DP>(base + C::OFF_V + s * C::TILE, &maps.v, hk, sk.start + j * 128,
+                        bar(C::V_FULL + s));
+          ++v_issued;
+        }
+        // no copy may still be in flight when the CTA ends (after a wait that
+        // ran out; otherwise all of these have completed)
+        if (*abort) {
+          if (n0 > 0) wait_phase(bar(C::Q_FULL), 0, ctl, false);
+          if (second) wait_phase(bar(C::Q_FULL + 1), 0, ctl, false);
+          for (int j = max(0, k_issued - C::NKV); j < k_issued; ++j)
+            wait_phase(bar(C::K_FULL + j % C::NKV), (j / C::NKV) & 1, ctl, false);
+          for (int j = max(0, v_issued - C::NKV); j < v_issued; ++j)
+            wait_phase(bar(C::V_FULL + j % C::NKV), (j / C::NKV) & 1, ctl, false);
+        }
       }
-      // no copy may still be in flight when the CTA ends (after a wait that
-      // ran out; otherwise all of these have completed)
-      if (*abort) {
-        if (n0 > 0) wait_phase(bar(C::Q_FULL), 0, ctl, false);
-        if (second) wait_phase(bar(C::Q_FULL + 1), 0, ctl, false);
-        for (int j = max(0, k_issued - C::NKV); j < k_issued; ++j)
-          wait_phase(bar(C::K_FULL + j % C::NKV), (j / C::NKV) & 1, ctl, false);
-        for (int j = max(0, v_issued - C::NKV); j < v_issued; ++j)
-          wait_phase(bar(C::V_FULL + j % C::NKV), (j / C::NKV) & 1, ctl, false);
+      __syncwarp();
+      if (n > 0 && v_left < 128) {   // cut the last V tile at the sequence's end
+        const int s = (n - 1) % C::NKV;
+        if (warp_wait_phase(bar(C::V_FULL + s), ((n - 1) / C::NKV) & 1, ctl)) {
+          zero_rows<DP>(base + C::OFF_V + s * C::TILE, v_left, lane);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(C::TAIL));
+        }
       }
-    }
-    __syncwarp();
-    if (n > 0 && v_left < 128) {   // cut the last V tile at the sequence's end
-      const int s = (n - 1) % C::NKV;
-      if (warp_wait_phase(bar(C::V_FULL + s), ((n - 1) / C::NKV) & 1, ctl)) {
-        zero_rows<DP>(base + C::OFF_V + s * C::TILE, v_left, lane);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::TAIL));
-      }
-    }
-  } else if (warp == kAttnMmaWarp) {
-    if (n > 0 && elect_one()) {   // one thread issues every product
-      const uint64_t q_desc = AttnTile<DP>::k_major(base + C::OFF_Q);
-      const uint64_t k_desc = AttnTile<DP>::k_major(base + C::OFF_K);
-      const uint64_t v_desc = AttnTile<DP>::mn_major(base + C::OFF_V);
-      auto scores = [&](int t, int s) {   // S_t = Q_t K^T, K in stage s
-        umma_entries<DP, BF16>(C::S_COL + t * 128, q_desc + t * AttnTile<DP>::UNITS,
-                               k_desc + s * AttnTile<DP>::UNITS);
-        umma_commit(bar(C::S_FULL + t));
-      };
-      bool ok = wait_phase(bar(C::K_FULL), 0, ctl);
-      for (int t = 0; t < 2 && ok; ++t) {
-        if ((t ? n1 : n0) == 0) continue;
-        ok = wait_phase(bar(C::Q_FULL + t), 0, ctl);
-        if (ok) scores(t, 0);
-      }
-      if (ok) umma_commit(bar(C::K_EMPTY));
-      int s = 0, s1 = 1 % C::NKV;           // stages of tiles j and j + 1
-      uint32_t round = 0, round1 = C::NKV == 1;
-      for (int j = 0; j < n && ok; ++j) {
-        if (j + 1 < n) ok = wait_phase(bar(C::K_FULL + s1), round1 & 1, ctl);
-        ok = ok && wait_phase(bar(C::V_FULL + s), round & 1, ctl);
-        if (ok && j + 1 == n && v_left < 128) ok = wait_phase(bar(C::TAIL), 0, ctl);
+    } else if (warp == kAttnMmaWarp) {
+      if (n > 0 && elect_one()) {   // one thread issues every product
+        const uint64_t q_desc = AttnTile<DP>::k_major(base + C::OFF_Q);
+        const uint64_t k_desc = AttnTile<DP>::k_major(base + C::OFF_K);
+        const uint64_t v_desc = AttnTile<DP>::mn_major(base + C::OFF_V);
+        auto scores = [&](int t, int s) {   // S_t = Q_t K^T, K in stage s
+          umma_entries<DP, BF16>(C::S_COL + t * 128, q_desc + t * AttnTile<DP>::UNITS,
+                                 k_desc + s * AttnTile<DP>::UNITS);
+          umma_commit(bar(C::S_FULL + t));
+        };
+        bool ok = wait_phase(bar(C::K_FULL), 0, ctl);
+        for (int t = 0; t < 2 && ok; ++t) {
+          if ((t ? n1 : n0) == 0) continue;
+          ok = wait_phase(bar(C::Q_FULL + t), 0, ctl);
+          if (ok) scores(t, 0);
+        }
+        if (ok) umma_commit(bar(C::K_EMPTY));
+        int s = 0, s1 = 1 % C::NKV;           // stages of tiles j and j + 1
+        uint32_t round = 0, round1 = C::NKV == 1;
+        for (int j = 0; j < n && ok; ++j) {
+          if (j + 1 < n) ok = wait_phase(bar(C::K_FULL + s1), round1 & 1, ctl);
+          ok = ok && wait_phase(bar(C::V_FULL + s), round & 1, ctl);
+          if (ok && j + 1 == n && v_left < 128) ok = wait_phase(bar(C::TAIL), 0, ctl);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int nt = t ? n1 : n0;
-          if (j >= nt || !ok) continue;
+          for (int t = 0; t < 2; ++t) {
+            const int nt = t ? n1 : n0;
+            if (j >= nt || !ok) continue;
 #pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            ok = ok && wait_phase(bar(C::P_READY + 2 * t + half), j & 1, ctl);
+            for (int half = 0; half < 2; ++half) {
+              ok = ok && wait_phase(bar(C::P_READY + 2 * t + half), j & 1, ctl);
+              if (!ok) break;
+              tc_fence_after_sync();
+              umma_tokens<DP, BF16>(C::O_COL + t * DP, C::S_COL + t * 128 + half * 32,
+                                    v_desc + s * AttnTile<DP>::UNITS, half, j == 0 && half == 0);
+            }
             if (!ok) break;
-            tc_fence_after_sync();
-            umma_tokens<DP, BF16>(C::O_COL + t * DP, C::S_COL + t * 128 + half * 32,
-                                  v_desc + s * AttnTile<DP>::UNITS, half, j == 0 && half == 0);
+            if (j + 1 < nt)
+              scores(t, s1);
+            else
+              umma_commit(bar(C::O_FULL + t));
           }
           if (!ok) break;
-          if (j + 1 < nt)
-            scores(t, s1);
-          else
-            umma_commit(bar(C::O_FULL + t));
+          umma_commit(bar(C::V_EMPTY + s));
+          if (j + 1 < n) umma_commit(bar(C::K_EMPTY + s1));
+          s = s1;
+          round = round1;
+          if (++s1 == C::NKV) {
+            s1 = 0;
+            ++round1;
+          }
         }
-        if (!ok) break;
-        umma_commit(bar(C::V_EMPTY + s));
-        if (j + 1 < n) umma_commit(bar(C::K_EMPTY + s1));
-        s = s1;
-        round = round1;
-        if (++s1 == C::NKV) {
-          s1 = 0;
-          ++round1;
-        }
+        // tensor memory stays allocated until every issued product has finished
+        umma_commit(bar(C::DRAIN));
+        wait_phase(bar(C::DRAIN), 0, ctl, false);
       }
-      // tensor memory stays allocated until every issued product has finished
-      umma_commit(bar(C::DRAIN));
-      wait_phase(bar(C::DRAIN), 0, ctl, false);
+      __syncwarp();
     }
-    __syncwarp();
   } else {
+    setmaxnreg_inc<kFwdRegsRow>();
     const int t = warp >> 2, row = tid & 127;
     const int nk = t ? n1 : n0;
     const int i = i0 + t * 128 + row;   // query of the sequence
@@ -338,7 +351,7 @@ cudaError_t launch_attn_fwd(bool bf16, const AttnFwdMaps& maps, const AttnFwdArg
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, kAttnThreads, smem, stream>>>(maps, args);
+    kernel<<<grid, kFwdThreads, smem, stream>>>(maps, args);
     return cudaGetLastError();
   };
   if (args.s.dim <= 64)
