@@ -24,6 +24,19 @@ constexpr int kAttnThreads = 320;   // 8 element-wise warps, 1 copying, 1 issuin
 constexpr int kAttnCopyWarp = 8;
 constexpr int kAttnMmaWarp = 9;
 
+// A place in a ring of N stages and the parity of its round.
+template <int N>
+struct RingAt {
+  int s = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == N) {
+      s = 0;
+      parity ^= 1;
+    }
+  }
+};
+
 // Sequence b's first row and length in a packed tensor of `tokens` rows; the
 // offsets come from device memory, so they are held inside the tensor and
 // the length at `most` (the grid's extent).

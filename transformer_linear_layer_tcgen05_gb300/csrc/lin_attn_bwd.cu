@@ -35,32 +35,49 @@ constexpr int kNormExp = 4;         // dO rows count as having a norm near 2^4
 constexpr int kDkvThreads = kAttnThreads + 32;
 constexpr int kTailWarp = 10;       // of the dK, dV kernel: cuts tiles at the sequence's end
 
+// The streamed operands are two rings: A (K in the dQ kernel, Q in the other),
+// whose tile enters the first and the last product of its turn, and B (V, dO).
+// A's next tile is wanted early in a turn and its last one is still in use
+// then, so with heads of 128, where shared memory holds five tiles beside the
+// CTA's own two, A has three of them.
 template <int DP>
 struct BwdCfg {
-  static constexpr int NS = DP == 64 ? 4 : 2;    // stages of the streamed pair of tiles
+  static constexpr int NA = DP == 64 ? 4 : 3, NB = DP == 64 ? 4 : 2;
   static constexpr uint32_t TILE = AttnTile<DP>::BYTES;
   static constexpr int OWN_FULL = 0;             // the CTA's own two tiles
-  static constexpr int FULL = 1;                 // the streamed pair
-  static constexpr int EMPTY = FULL + NS;
-  static constexpr int S_FULL = EMPTY + NS;      // S complete
+  static constexpr int A_FULL = 1, A_EMPTY = A_FULL + NA;
+  static constexpr int B_FULL = A_EMPTY + NA, B_EMPTY = B_FULL + NB;
+  static constexpr int S_FULL = B_EMPTY + NB;    // S complete
   static constexpr int DP_FULL = S_FULL + 1;     // dP complete
   static constexpr int S_DONE = DP_FULL + 1;     // 2 halves: S read (dQ) / P^T written (dK, dV)
   static constexpr int DS_READY = S_DONE + 2;    // 2 halves: dS written
-  static constexpr int TAIL = DS_READY + 2;      // NS: the stage, cut at the sequence's end
-  static constexpr int OUT_FULL = TAIL + NS;     // the sums complete (every product is)
+  static constexpr int A_TAIL = DS_READY + 2;    // the stage, cut at the sequence's end
+  static constexpr int B_TAIL = A_TAIL + NA;
+  static constexpr int OUT_FULL = B_TAIL + NB;   // the sums complete (every product is)
   static constexpr int BARS = OUT_FULL + 1;
-  static constexpr bool by_half(int i) { return i >= S_DONE && i < TAIL; }
+  static constexpr bool by_half(int i) { return i >= S_DONE && i < A_TAIL; }
   static constexpr uint32_t OFF_TMEM = BARS * 8, OFF_ABORT = OFF_TMEM + 4;
-  static_assert(OFF_ABORT + 4 <= 512, "barrier region");
-  static constexpr uint32_t OFF_RED = 512;       // 128 floats
-  static constexpr uint32_t OFF_ROWS = 1024;     // [NS][2][128] floats: -L log2 e (+ 8), -a delta
-  static constexpr uint32_t OFF_OWN = OFF_ROWS + 4096;
-  static_assert(NS * 1024 <= 4096, "row statistics");
-  static constexpr uint32_t OFF_RING = OFF_OWN + 2 * TILE;
-  static constexpr uint32_t SMEM = OFF_RING + NS * 2 * TILE + 1024;
+  static constexpr uint32_t OFF_RED = 448;       // 16 floats
+  static_assert(OFF_ABORT + 4 <= OFF_RED, "barrier region");
+  static constexpr uint32_t OFF_OWN = 0;         // (tiles first: they want 1024-byte bases)
+  static constexpr uint32_t OFF_A = 2 * TILE, OFF_B = OFF_A + NA * TILE;
+  // [NA][128] floats: -L log2 e + 8; then [NB][128]: -a delta
+  static constexpr uint32_t OFF_ROWS = OFF_B + NB * TILE;
+  static constexpr uint32_t OFF_CTL = OFF_ROWS + (NA + NB) * 512;
+  static constexpr uint32_t SMEM = OFF_CTL + 512;
+  static_assert((NA + NB) * 512 >= 2048, "the dQ kernel's row sums");
   static_assert(SMEM <= 232448, "shared memory");
   static constexpr uint32_t S_COL = 0, DP_COL = 128, OUT_COL = 256;   // sums: DP columns each
 };
+
+// The CTA's shared memory, which the tiles' swizzle wants at a multiple of
+// 1024 bytes (it begins there: the kernels have no other shared memory). At
+// any other place the kernel would compute nonsense: reported, never run.
+__device__ __forceinline__ bool smem_aligned(const void* p, int* status) {
+  if ((smem_u32(p) & 1023u) == 0) return true;
+  if (threadIdx.x == 0) report_check(status, CHK_BUFFER, smem_u32(p));
+  return false;
+}
 
 // 2^e as a float, e held to where 2^e and 2^-e are normal.
 __device__ __forceinline__ float pow2i(int e) {
@@ -100,18 +117,19 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const int n = hi > 0 ? (hi + 127) / 128 : 0;
   const int hk = h / a.group;
 
-  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  uint8_t* const gen = smem_raw + (base - smem_u32(smem_raw));
-  auto bar = [&](int slot) { return base + (uint32_t)slot * 8u; };
+  if (!smem_aligned(smem_raw, a.status)) return;
+  const uint32_t base = smem_u32(smem_raw);
+  uint8_t* const ctl_gen = smem_raw + C::OFF_CTL;
+  auto bar = [&](int slot) { return base + C::OFF_CTL + (uint32_t)slot * 8u; };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  volatile int* abort = reinterpret_cast<volatile int*>(gen + C::OFF_ABORT);
+  volatile int* abort = reinterpret_cast<volatile int*>(ctl_gen + C::OFF_ABORT);
   const WaitCtl ctl{a.timeout_ns, abort, a.status};
   const uint32_t q_tile = base + C::OFF_OWN, do_tile = q_tile + C::TILE;
-  auto k_tile = [&](int s) { return base + C::OFF_RING + (uint32_t)s * 2u * C::TILE; };
-  auto v_tile = [&](int s) { return k_tile(s) + C::TILE; };
+  auto k_tile = [&](int s) { return base + C::OFF_A + (uint32_t)s * C::TILE; };
+  auto v_tile = [&](int s) { return base + C::OFF_B + (uint32_t)s * C::TILE; };
 
   if (warp == kAttnMmaWarp) {
-    tmem_alloc(base + C::OFF_TMEM, 512);
+    tmem_alloc(base + C::OFF_CTL + C::OFF_TMEM, 512);
     tmem_relinquish_alloc_permit();
   }
   if (tid == 0) {
@@ -132,28 +150,34 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       mbar_arrive_expect_tx(bar(C::OWN_FULL), 2 * C::TILE);
       load_tile<DP>(q_tile, &maps.q, h, sq.start + i0, bar(C::OWN_FULL));
       load_tile<DP>(do_tile, &maps.dout, h, sq.start + i0, bar(C::OWN_FULL));
-      int issued = 0;
-      for (int j = 0; j < n; ++j, ++issued) {
-        const int s = j % C::NS, round = j / C::NS;
-        if (round > 0 && !wait_phase(bar(C::EMPTY + s), (round - 1) & 1, ctl)) break;
-        mbar_arrive_expect_tx(bar(C::FULL + s), 2 * C::TILE);
-        load_tile<DP>(k_tile(s), &maps.k, hk, sk.start + j * 128, bar(C::FULL + s));
-        load_tile<DP>(v_tile(s), &maps.v, hk, sk.start + j * 128, bar(C::FULL + s));
+      int a_issued = 0, b_issued = 0;
+      for (int j = 0; j < n; ++j) {
+        const int sa = j % C::NA, ra = j / C::NA, sb = j % C::NB, rb = j / C::NB;
+        if (ra > 0 && !wait_phase(bar(C::A_EMPTY + sa), (ra - 1) & 1, ctl)) break;
+        mbar_arrive_expect_tx(bar(C::A_FULL + sa), C::TILE);
+        load_tile<DP>(k_tile(sa), &maps.k, hk, sk.start + j * 128, bar(C::A_FULL + sa));
+        ++a_issued;
+        if (rb > 0 && !wait_phase(bar(C::B_EMPTY + sb), (rb - 1) & 1, ctl)) break;
+        mbar_arrive_expect_tx(bar(C::B_FULL + sb), C::TILE);
+        load_tile<DP>(v_tile(sb), &maps.v, hk, sk.start + j * 128, bar(C::B_FULL + sb));
+        ++b_issued;
       }
       if (*abort) {   // no copy may still be in flight when the CTA ends
         wait_phase(bar(C::OWN_FULL), 0, ctl, false);
-        for (int j = max(0, issued - C::NS); j < issued; ++j)
-          wait_phase(bar(C::FULL + j % C::NS), (j / C::NS) & 1, ctl, false);
+        for (int j = max(0, a_issued - C::NA); j < a_issued; ++j)
+          wait_phase(bar(C::A_FULL + j % C::NA), (j / C::NA) & 1, ctl, false);
+        for (int j = max(0, b_issued - C::NB); j < b_issued; ++j)
+          wait_phase(bar(C::B_FULL + j % C::NB), (j / C::NB) & 1, ctl, false);
       }
     }
     __syncwarp();
     if (n > 0 && k_left < 128) {   // cut the last K tile at the sequence's end (dS K runs over it)
-      const int s = (n - 1) % C::NS;
-      if (warp_wait_phase(bar(C::FULL + s), ((n - 1) / C::NS) & 1, ctl)) {
+      const int s = (n - 1) % C::NA;
+      if (warp_wait_phase(bar(C::A_FULL + s), ((n - 1) / C::NA) & 1, ctl)) {
         zero_rows<DP>(k_tile(s), k_left, lane);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::TAIL));
+        if (lane == 0) mbar_arrive(bar(C::A_TAIL));
       }
     }
   } else if (warp == kAttnMmaWarp) {
@@ -161,50 +185,46 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const uint64_t q_desc = AttnTile<DP>::k_major(q_tile), do_desc = AttnTile<DP>::k_major(do_tile);
       const uint64_t k_desc = AttnTile<DP>::k_major(k_tile(0)), v_desc = AttnTile<DP>::k_major(v_tile(0));
       const uint64_t kt_desc = AttnTile<DP>::mn_major(k_tile(0));
-      constexpr uint64_t STAGE = 2 * AttnTile<DP>::UNITS;
-      auto scores = [&](int s) {   // S = Q K^T, K in stage s
-        umma_entries<DP, BF16>(C::S_COL, q_desc, k_desc + s * STAGE);
+      constexpr uint64_t STAGE = AttnTile<DP>::UNITS;
+      RingAt<C::NA> ka, kn;   // K of tile j, and of the next S
+      RingAt<C::NB> vn;       // V of the next dP
+      int kj = 0;             // tile of kn
+      auto scores = [&]() -> bool {   // S = Q K^T of the next tile
+        if (!wait_phase(bar(C::A_FULL + kn.s), kn.parity, ctl) ||
+            (++kj == n && k_left < 128 && !wait_phase(bar(C::A_TAIL), 0, ctl)))
+          return false;
+        umma_entries<DP, BF16>(C::S_COL, q_desc, k_desc + kn.s * STAGE);
         umma_commit(bar(C::S_FULL));
+        kn.next();
+        return true;
       };
-      auto dprobs = [&](int s) {   // dP = dO V^T
-        umma_entries<DP, BF16>(C::DP_COL, do_desc, v_desc + s * STAGE);
+      auto dprobs = [&]() -> bool {   // dP = dO V^T of the next tile
+        if (!wait_phase(bar(C::B_FULL + vn.s), vn.parity, ctl)) return false;
+        umma_entries<DP, BF16>(C::DP_COL, do_desc, v_desc + vn.s * STAGE);
         umma_commit(bar(C::DP_FULL));
+        umma_commit(bar(C::B_EMPTY + vn.s));
+        vn.next();
+        return true;
       };
-      auto arrived = [&](int j, int s, uint32_t round) {   // K_j, V_j in shared memory
-        return wait_phase(bar(C::FULL + s), round & 1, ctl) &&
-               (j + 1 < n || k_left >= 128 || wait_phase(bar(C::TAIL), 0, ctl));
-      };
-      int s = 0, s1 = 1 % C::NS;
-      uint32_t round1 = C::NS == 1;
-      bool ok = wait_phase(bar(C::OWN_FULL), 0, ctl) && arrived(0, 0, 0);
-      if (ok) {
-        scores(0);
-        dprobs(0);
-      }
+      bool ok = wait_phase(bar(C::OWN_FULL), 0, ctl) && scores() && dprobs();
       for (int j = 0; j < n && ok; ++j) {
         if (j + 1 < n) {
-          ok = arrived(j + 1, s1, round1) && wait_phase(bar(C::S_DONE), j & 1, ctl) &&
-               wait_phase(bar(C::S_DONE + 1), j & 1, ctl);
-          if (!ok) break;
+          ok = wait_phase(bar(C::S_DONE), j & 1, ctl) && wait_phase(bar(C::S_DONE + 1), j & 1, ctl);
           tc_fence_after_sync();
-          scores(s1);
+          ok = ok && scores();
         }
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           ok = ok && wait_phase(bar(C::DS_READY + half), j & 1, ctl);
           if (!ok) break;
           tc_fence_after_sync();
-          umma_tokens<DP, BF16>(C::OUT_COL, C::DP_COL + half * 64, kt_desc + s * STAGE, half,
+          umma_tokens<DP, BF16>(C::OUT_COL, C::DP_COL + half * 64, kt_desc + ka.s * STAGE, half,
                                 j == 0 && half == 0);
         }
         if (!ok) break;
-        umma_commit(bar(C::EMPTY + s));
-        if (j + 1 < n) dprobs(s1);
-        s = s1;
-        if (++s1 == C::NS) {
-          s1 = 0;
-          ++round1;
-        }
+        umma_commit(bar(C::A_EMPTY + ka.s));
+        ka.next();
+        if (j + 1 < n) ok = dprobs();
       }
       // (also on the way out: tensor memory must be idle at the end)
       umma_commit(bar(C::OUT_FULL));
@@ -240,13 +260,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         }
       }
     }
-    float* red = reinterpret_cast<float*>(gen + C::OFF_ROWS);   // 4 x 128 floats
+    float* red = reinterpret_cast<float*>(smem_raw + C::OFF_ROWS);   // 4 x 128 floats
     red[half * 128 + row] = dsum;
     red[256 + half * 128 + row] = nsum;
     named_bar_sync(1, 256);
     float delta = red[row] + red[128 + row];
     const float norm = sqrtf(red[256 + row] + red[384 + row]);
-    float* red2 = reinterpret_cast<float*>(gen + C::OFF_RED);
+    float* red2 = reinterpret_cast<float*>(ctl_gen + C::OFF_RED);
     if (half == 0) {
       if (live && n != 1) args.delta[(int64_t)h * a.tokens_q + token] = delta;
       float big = norm;   // (NaN rows do not count)
@@ -408,19 +428,21 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   const int q_left = sq.len - (t1 - 1) * 128;   // queries of the last tile
   const int h0 = hk * a.group;
 
-  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-  uint8_t* const gen = smem_raw + (base - smem_u32(smem_raw));
-  auto bar = [&](int slot) { return base + (uint32_t)slot * 8u; };
+  if (!smem_aligned(smem_raw, a.status)) return;
+  const uint32_t base = smem_u32(smem_raw);
+  uint8_t* const ctl_gen = smem_raw + C::OFF_CTL;
+  auto bar = [&](int slot) { return base + C::OFF_CTL + (uint32_t)slot * 8u; };
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  volatile int* abort = reinterpret_cast<volatile int*>(gen + C::OFF_ABORT);
+  volatile int* abort = reinterpret_cast<volatile int*>(ctl_gen + C::OFF_ABORT);
   const WaitCtl ctl{a.timeout_ns, abort, a.status};
   const uint32_t k_tile = base + C::OFF_OWN, v_tile = k_tile + C::TILE;
-  auto q_tile = [&](int s) { return base + C::OFF_RING + (uint32_t)s * 2u * C::TILE; };
-  auto do_tile = [&](int s) { return q_tile(s) + C::TILE; };
-  auto rows = [&](int s) { return reinterpret_cast<float*>(gen + C::OFF_ROWS) + s * 256; };
+  auto q_tile = [&](int s) { return base + C::OFF_A + (uint32_t)s * C::TILE; };
+  auto do_tile = [&](int s) { return base + C::OFF_B + (uint32_t)s * C::TILE; };
+  auto lse_rows = [&](int s) { return reinterpret_cast<float*>(smem_raw + C::OFF_ROWS) + s * 128; };
+  auto delta_rows = [&](int s) { return lse_rows(C::NA + s); };
 
   if (warp == kAttnMmaWarp) {
-    tmem_alloc(base + C::OFF_TMEM, 512);
+    tmem_alloc(base + C::OFF_CTL + C::OFF_TMEM, 512);
     tmem_relinquish_alloc_permit();
   }
   if (tid == 0) {
@@ -431,7 +453,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   }
   // the largest row norm of dO that this tile meets (every tile of the
   // heads: the masked ones do no harm)
-  float* red = reinterpret_cast<float*>(gen + C::OFF_RED);
+  float* red = reinterpret_cast<float*>(ctl_gen + C::OFF_RED);
   {
     const int tiles = (a.max_q + 127) / 128;
     const float* nm = args.norm + ((int64_t)b * a.heads_q + h0) * tiles;
@@ -460,9 +482,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         load_tile<DP>(k_tile, &maps.k, hk, sk.start + k0, bar(C::OWN_FULL));
         load_tile<DP>(v_tile, &maps.v, hk, sk.start + k0, bar(C::OWN_FULL));
       }
-      int issued = 0;
-      for (int it = 0; it < n; ++it, ++issued) {
-        const int s = it % C::NS, round = it / C::NS;
+      int a_issued = 0, b_issued = 0;
+      for (int it = 0; it < n; ++it) {
+        const int sa = it % C::NA, ra = it / C::NA, sb = it % C::NB, rb = it / C::NB;
         const int h = h0 + it / per, i0 = (t0 + it % per) * 128;
         // the rows' statistics, in the form that the element-wise warps add:
         // rows behind the sequence's end and rows without a key have P = 0
@@ -475,25 +497,33 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
           nl[e] = lse == -INFINITY ? -INFINITY : fmaf(-lse, kLog2E, kPShift);
           nd[e] = i < sq.len ? args.delta[at] * -damp : 0.0f;
         }
-        if (round > 0 && !lane0_wait_phase(bar(C::EMPTY + s), (round - 1) & 1, ctl, lane)) break;
+        if (ra > 0 && !lane0_wait_phase(bar(C::A_EMPTY + sa), (ra - 1) & 1, ctl, lane)) break;
         __syncwarp();   // (the stage's last readers are done for every lane)
-        float* r = rows(s);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          r[e * 32 + lane] = nl[e];
-          r[128 + e * 32 + lane] = nd[e];
-        }
+        for (int e = 0; e < 4; ++e) lse_rows(sa)[e * 32 + lane] = nl[e];
         __syncwarp();
         if (lane == 0) {
-          mbar_arrive_expect_tx(bar(C::FULL + s), 2 * C::TILE);
-          load_tile<DP>(q_tile(s), &maps.q, h, sq.start + i0, bar(C::FULL + s));
-          load_tile<DP>(do_tile(s), &maps.dout, h, sq.start + i0, bar(C::FULL + s));
+          mbar_arrive_expect_tx(bar(C::A_FULL + sa), C::TILE);
+          load_tile<DP>(q_tile(sa), &maps.q, h, sq.start + i0, bar(C::A_FULL + sa));
         }
+        ++a_issued;
+        if (rb > 0 && !lane0_wait_phase(bar(C::B_EMPTY + sb), (rb - 1) & 1, ctl, lane)) break;
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) delta_rows(sb)[e * 32 + lane] = nd[e];
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(C::B_FULL + sb), C::TILE);
+          load_tile<DP>(do_tile(sb), &maps.dout, h, sq.start + i0, bar(C::B_FULL + sb));
+        }
+        ++b_issued;
       }
       if (lane == 0 && *abort) {   // no copy may still be in flight when the CTA ends
         wait_phase(bar(C::OWN_FULL), 0, ctl, false);
-        for (int it = max(0, issued - C::NS); it < issued; ++it)
-          wait_phase(bar(C::FULL + it % C::NS), (it / C::NS) & 1, ctl, false);
+        for (int it = max(0, a_issued - C::NA); it < a_issued; ++it)
+          wait_phase(bar(C::A_FULL + it % C::NA), (it / C::NA) & 1, ctl, false);
+        for (int it = max(0, b_issued - C::NB); it < b_issued; ++it)
+          wait_phase(bar(C::B_FULL + it % C::NB), (it / C::NB) & 1, ctl, false);
       }
     }
   } else if (warp == kTailWarp) {
@@ -503,17 +533,27 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     // behind the end zeroed: they enter the products that run over the queries.
     if (n > 0 && q_left < 128) {
       int tile = 0;
+      RingAt<C::NA> qa;
+      RingAt<C::NB> da;
       for (int it = 0; it < n; ++it) {
-        const int s = it % C::NS;
-        if (!warp_wait_phase(bar(C::FULL + s), (it / C::NS) & 1, ctl)) break;
-        if (++tile == per) {
-          tile = 0;
-          zero_rows<DP>(q_tile(s), q_left, lane);
-          zero_rows<DP>(do_tile(s), q_left, lane);
+        const bool cut = ++tile == per;
+        if (cut) tile = 0;
+        if (!warp_wait_phase(bar(C::A_FULL + qa.s), qa.parity, ctl)) break;
+        if (cut) {
+          zero_rows<DP>(q_tile(qa.s), q_left, lane);
           fence_proxy_async_smem();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::TAIL + s));
+        if (lane == 0) mbar_arrive(bar(C::A_TAIL + qa.s));
+        if (!warp_wait_phase(bar(C::B_FULL + da.s), da.parity, ctl)) break;
+        if (cut) {
+          zero_rows<DP>(do_tile(da.s), q_left, lane);
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::B_TAIL + da.s));
+        qa.next();
+        da.next();
       }
     }
   } else if (warp == kAttnMmaWarp) {
@@ -522,57 +562,51 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       const uint64_t q_desc = AttnTile<DP>::k_major(q_tile(0)), do_desc = AttnTile<DP>::k_major(do_tile(0));
       const uint64_t qt_desc = AttnTile<DP>::mn_major(q_tile(0));
       const uint64_t dot_desc = AttnTile<DP>::mn_major(do_tile(0));
-      constexpr uint64_t STAGE = 2 * AttnTile<DP>::UNITS;
-      auto scores = [&](int s) {   // S^T = K Q^T, Q in stage s
-        umma_entries<DP, BF16>(C::S_COL, k_desc, q_desc + s * STAGE);
+      constexpr uint64_t STAGE = AttnTile<DP>::UNITS;
+      const int a_ready = q_left < 128 ? C::A_TAIL : C::A_FULL;
+      const int b_ready = q_left < 128 ? C::B_TAIL : C::B_FULL;
+      RingAt<C::NA> qa, qn;   // Q of tile it, and of the next S^T
+      RingAt<C::NB> da, dn;   // dO of tile it, and of the next dP^T
+      auto scores = [&]() -> bool {   // S^T = K Q^T of the next tile
+        if (!wait_phase(bar(a_ready + qn.s), qn.parity, ctl)) return false;
+        umma_entries<DP, BF16>(C::S_COL, k_desc, q_desc + qn.s * STAGE);
         umma_commit(bar(C::S_FULL));
+        qn.next();
+        return true;
       };
-      auto dprobs = [&](int s) {   // dP^T = V dO^T
-        umma_entries<DP, BF16>(C::DP_COL, v_desc, do_desc + s * STAGE);
+      auto dprobs = [&]() -> bool {   // dP^T = V dO^T of the next tile
+        if (!wait_phase(bar(b_ready + dn.s), dn.parity, ctl)) return false;
+        umma_entries<DP, BF16>(C::DP_COL, v_desc, do_desc + dn.s * STAGE);
         umma_commit(bar(C::DP_FULL));
+        dn.next();
+        return true;
       };
-      const int ready = q_left < 128 ? C::TAIL : C::FULL;
-      auto arrived = [&](int s, uint32_t round) {   // Q and dO are in shared memory
-        return wait_phase(bar(ready + s), round & 1, ctl);
-      };
-      int s = 0, s1 = 1 % C::NS;
-      uint32_t round1 = C::NS == 1;
-      bool ok = wait_phase(bar(C::OWN_FULL), 0, ctl) && arrived(0, 0);
-      if (ok) {
-        scores(0);
-        dprobs(0);
-      }
+      bool ok = wait_phase(bar(C::OWN_FULL), 0, ctl) && scores() && dprobs();
       for (int it = 0; it < n && ok; ++it) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {   // dV += P^T dO
           ok = ok && wait_phase(bar(C::S_DONE + half), it & 1, ctl);
           if (!ok) break;
           tc_fence_after_sync();
-          umma_tokens<DP, BF16>(C::OUT_COL, C::S_COL + half * 64, dot_desc + s * STAGE, half,
+          umma_tokens<DP, BF16>(C::OUT_COL, C::S_COL + half * 64, dot_desc + da.s * STAGE, half,
                                 it == 0 && half == 0);
         }
-        if (!ok) break;
-        if (it + 1 < n) {
-          ok = arrived(s1, round1);
-          if (!ok) break;
-          scores(s1);
-        }
+        if (ok && it + 1 < n) ok = scores();
 #pragma unroll
         for (int half = 0; half < 2; ++half) {   // dK += dS^T Q
           ok = ok && wait_phase(bar(C::DS_READY + half), it & 1, ctl);
           if (!ok) break;
           tc_fence_after_sync();
-          umma_tokens<DP, BF16>(C::OUT_COL + DP, C::DP_COL + half * 64, qt_desc + s * STAGE, half,
+          umma_tokens<DP, BF16>(C::OUT_COL + DP, C::DP_COL + half * 64, qt_desc + qa.s * STAGE, half,
                                 it == 0 && half == 0);
         }
         if (!ok) break;
-        umma_commit(bar(C::EMPTY + s));
-        if (it + 1 < n) dprobs(s1);
-        s = s1;
-        if (++s1 == C::NS) {
-          s1 = 0;
-          ++round1;
-        }
+        // (dO's stage too: its rows' delta was read for dS)
+        umma_commit(bar(C::A_EMPTY + qa.s));
+        umma_commit(bar(C::B_EMPTY + da.s));
+        qa.next();
+        da.next();
+        if (it + 1 < n) ok = dprobs();
       }
       // (also on the way out: tensor memory must be idle at the end)
       umma_commit(bar(C::OUT_FULL));
@@ -588,16 +622,20 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     const uint32_t s_col = tmem + lanes + C::S_COL + half * 64;
     const uint32_t dp_col = tmem + lanes + C::DP_COL + half * 64;
     bool ok = true;
+    int tile = 0;   // of its head
+    RingAt<C::NA> qa;
+    RingAt<C::NB> da;
     for (int it = 0; it < n; ++it) {
-      const int s = it % C::NS;
-      const int i0 = (t0 + it % per) * 128;
-      const float4* nl = reinterpret_cast<const float4*>(rows(s) + half * 64);
-      const float4* nd = reinterpret_cast<const float4*>(rows(s) + 128 + half * 64);
+      const int i0 = (t0 + tile) * 128;
+      if (++tile == per) tile = 0;
+      const float4* nl = reinterpret_cast<const float4*>(lse_rows(qa.s) + half * 64);
+      const float4* nd = reinterpret_cast<const float4*>(delta_rows(da.s) + half * 64);
       ok = warp_wait_phase(bar(C::S_FULL), it & 1, ctl);
       if (!ok) break;
-      // (the rows' statistics came before the copies that S waited for)
-      ok = warp_wait_phase(bar(C::FULL + s), (it / C::NS) & 1, ctl);
+      // (the rows' statistics came before the copies that the products waited for)
+      ok = warp_wait_phase(bar(C::A_FULL + qa.s), qa.parity, ctl);
       if (!ok) break;
+      qa.next();
       tc_fence_after_sync();
       uint32_t p[2][32], d[2][32], w[32];
       tmem_ld_32x32b_x32(s_col, p[0]);
@@ -638,8 +676,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       tmem_wait_st();
       tc_fence_before_sync();
       mbar_arrive(bar(C::S_DONE + half));
-      ok = warp_wait_phase(bar(C::DP_FULL), it & 1, ctl);
+      ok = warp_wait_phase(bar(C::DP_FULL), it & 1, ctl) &&
+           warp_wait_phase(bar(C::B_FULL + da.s), da.parity, ctl);
       if (!ok) break;
+      da.next();
       tc_fence_after_sync();
       tmem_ld_32x32b_x32(dp_col, d[0]);
       tmem_ld_32x32b_x32(dp_col + 32, d[1]);
