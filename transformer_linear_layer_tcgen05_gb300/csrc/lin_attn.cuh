@@ -50,13 +50,13 @@ __device__ __forceinline__ SeqRange seq_range(const int32_t* cu, int b, int toke
   return SeqRange{s, min(e - s, most)};
 }
 
-// Sub-tiles, bytes and descriptors of a [128 tokens][DP entries] operand tile.
-// A descriptor's address field counts 16-byte units from bit 0, so the steps
-// of a product add constants to the tile's descriptor.
-template <int DP>
+// Sub-tiles, bytes and descriptors of a [ROWS tokens][DP entries] operand
+// tile. A descriptor's address field counts 16-byte units from bit 0, so the
+// steps of a product add constants to the tile's descriptor.
+template <int DP, int ROWS = 128>
 struct AttnTile {
   static constexpr int SUB = DP / 64;
-  static constexpr uint32_t SUB_BYTES = 128 * 128;
+  static constexpr uint32_t SUB_BYTES = ROWS * 128;
   static constexpr uint32_t BYTES = SUB * SUB_BYTES;
   static constexpr uint64_t UNITS = BYTES / 16;
   // K-major (steps of 16 entries), MN-major (steps of 16 tokens)
@@ -108,37 +108,63 @@ __device__ __forceinline__ void umma_entries(uint32_t d, uint64_t a, uint64_t b)
     umma_f16(d, a + AttnTile<DP>::entry_step(kk), b + AttnTile<DP>::entry_step(kk), idesc, kk > 0);
 }
 
-// D[128 x DP] (+)= A B over tokens 64 half .. 64 half + 63: A in tensor
-// memory, these tokens in the 32 columns at `a`; B an operand tile (MN-major
-// descriptor). `first`: the accumulator starts here.
-template <int DP, bool BF16>
-__device__ __forceinline__ void umma_tokens(uint32_t d, uint32_t a, uint64_t b, int half, bool first) {
-  constexpr uint32_t idesc = attn_idesc<BF16, true, DP>();
+// The same with A's 128 rows in tensor memory (entries 2c, 2c + 1 in column c).
+template <int DP, int ROWS, bool BF16>
+__device__ __forceinline__ void umma_entries_tmem(uint32_t d, uint32_t a, uint64_t b) {
+  constexpr uint32_t idesc = attn_idesc<BF16, false, ROWS>();
 #pragma unroll
-  for (int kk = 0; kk < 4; ++kk)
-    umma_f16_tmem_a(d, a + kk * 8, b + AttnTile<DP>::token_step(half * 4 + kk), idesc,
-                    kk > 0 || !first);
+  for (int kk = 0; kk < DP / 16; ++kk)
+    umma_f16_tmem_a(d, a + kk * 8, b + AttnTile<DP, ROWS>::entry_step(kk), idesc, kk > 0);
 }
 
-// Zeroes rows [first, 128) of an operand tile: a contraction over tokens must
+// D[128 x DP] (+)= A B over 16 STEPS tokens from token 16 `from` of an operand
+// tile B (MN-major descriptor); A in tensor memory, these tokens in the 8
+// STEPS columns at `a`. `first`: the accumulator starts here.
+template <int DP, bool BF16, int STEPS>
+__device__ __forceinline__ void umma_tokens(uint32_t d, uint32_t a, uint64_t b, int from, bool first) {
+  constexpr uint32_t idesc = attn_idesc<BF16, true, DP>();
+#pragma unroll
+  for (int kk = 0; kk < STEPS; ++kk)
+    umma_f16_tmem_a(d, a + kk * 8, b + AttnTile<DP>::token_step(from + kk), idesc, kk > 0 || !first);
+}
+
+// Zeroes rows [first, ROWS) of an operand tile: a contraction over tokens must
 // not meet what lies behind a sequence's end (another sequence's rows, or
 // padding that may hold infinities or NaN, which a zero weight would not
 // remove). One warp, after the copy has landed; a fence then orders the
 // stores before the tensor core's reads.
-template <int DP>
+template <int DP, int ROWS>
 __device__ __forceinline__ void zero_rows(uint32_t tile, int first, int lane) {
-  for (int s = 0; s < AttnTile<DP>::SUB; ++s)
-    for (int i = first * 8 + lane; i < 128 * 8; i += 32)
-      st_shared_v4(tile + s * AttnTile<DP>::SUB_BYTES + i * 16, 0u, 0u, 0u, 0u);
+  for (int s = 0; s < AttnTile<DP, ROWS>::SUB; ++s)
+    for (int i = first * 8 + lane; i < ROWS * 8; i += 32)
+      st_shared_v4(tile + s * AttnTile<DP, ROWS>::SUB_BYTES + i * 16, 0u, 0u, 0u, 0u);
 }
 
-// One operand tile (tokens z .. z + 127 of head h) into shared memory.
-template <int DP>
+// One operand tile (tokens z .. z + ROWS - 1 of head h; the map's box has as
+// many) into shared memory.
+template <int DP, int ROWS>
 __device__ __forceinline__ void load_tile(uint32_t dst, const CUtensorMap* map, int h, int z,
                                           uint32_t bar) {
 #pragma unroll
-  for (int s = 0; s < AttnTile<DP>::SUB; ++s)
-    tma_load_3d(dst + s * AttnTile<DP>::SUB_BYTES, map, s * 64, h, z, bar);
+  for (int s = 0; s < AttnTile<DP, ROWS>::SUB; ++s)
+    tma_load_3d(dst + s * AttnTile<DP, ROWS>::SUB_BYTES, map, s * 64, h, z, bar);
+}
+
+// Part `part` of PARTS of a head's row (null: zeros) in registers, two entries
+// to each: zero behind the head's size.
+template <int DP, int PARTS>
+__device__ __forceinline__ void load_row_part(uint32_t (&r)[DP / PARTS / 2], const uint16_t* row,
+                                              int part, int dim) {
+#pragma unroll
+  for (int e = 0; e < DP / PARTS / 8; ++e) {
+    const int col = part * (DP / PARTS) + e * 8;
+    const uint4 x = row && col < dim ? __ldg(reinterpret_cast<const uint4*>(row + col))
+                                     : make_uint4(0u, 0u, 0u, 0u);
+    r[e * 4] = x.x;
+    r[e * 4 + 1] = x.y;
+    r[e * 4 + 2] = x.z;
+    r[e * 4 + 3] = x.w;
+  }
 }
 
 // Eight 16-bit entries of a row to global memory.

@@ -32,11 +32,16 @@ struct AttnFwdArgs {
 
 struct AttnBwdArgs {
   AttnArgs s;
-  HeadsPtr o, dout;       // read row by row for delta
+  HeadsPtr q, k, v;       // the CTAs' own rows (the streamed ones come by the maps)
+  HeadsPtr o, dout;
   const float* lse;       // [heads_q][tokens_q]
   float* delta;           // [heads_q][tokens_q]: sum of dO * O of each row
   float* norm;            // [sequences][heads_q][q tiles]: largest row norm of dO
   HeadsPtr dq, dk, dv;
+  // parts of the keys for dQ and of the queries for dK, dV, and, where there
+  // are several, their f32 sums [part][token][head][dim]
+  int32_t q_parts, k_parts;
+  float *dq_part, *dk_part, *dv_part;
 };
 
 struct AttnFwdMaps {
@@ -48,8 +53,13 @@ struct AttnBwdMaps {
 
 cudaError_t launch_attn_fwd(bool bf16, const AttnFwdMaps& maps, const AttnFwdArgs& args,
                             int heads_kv, int sequences, cudaStream_t stream);
-// The dQ kernel (which also leaves delta and norm), then the dK, dV kernel.
+// Parts that the backward kernels' other side is cut into (see there).
+int attn_parts(int64_t ctas, int64_t rows, int sms);
+// Tokens of a box of the backward kernels' maps.
+constexpr int kAttnBwdBox = 128;
+// The dQ kernel (which also leaves delta and norm), the dK, dV kernel, and the
+// sums of their parts; *kernels: how many that were.
 cudaError_t launch_attn_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArgs& args,
-                            int heads_kv, int sequences, cudaStream_t stream);
+                            int heads_kv, int sequences, int* kernels, cudaStream_t stream);
 
 }  // namespace lin

@@ -80,9 +80,9 @@ lin_status check_attention(const lin_attention_shape* s, View* views, int nviews
   return LIN_SUCCESS;
 }
 
-bool encode_view(CUtensorMap* m, const View& v, int64_t dim) {
+bool encode_view(CUtensorMap* m, const View& v, int64_t dim, int box_tokens) {
   return encode_heads(m, v.t->data, (uint64_t)dim, (uint64_t)v.heads, (uint64_t)v.tokens,
-                      (uint64_t)v.hs * 2, (uint64_t)v.ts * 2);
+                      (uint64_t)v.hs * 2, (uint64_t)v.ts * 2, (uint32_t)box_tokens);
 }
 
 lin::AttnArgs attn_args(const lin_attention_shape* s, const Checked& c) {
@@ -113,10 +113,10 @@ lin_status attention(const lin_attention_shape* s, const lin_heads* Q, const lin
   if (st != LIN_SUCCESS) return st;
   if (c.nothing || c.max_q == 0) return LIN_SUCCESS;
   lin::AttnFwdMaps maps;
-  bool ok = encode_view(&maps.q, v[0], s->dim);
+  bool ok = encode_view(&maps.q, v[0], s->dim, 128);
   // without keys the K and V maps are never used
-  ok &= encode_view(&maps.k, v[1].extent ? v[1] : v[0], s->dim);
-  ok &= encode_view(&maps.v, v[2].extent ? v[2] : v[0], s->dim);
+  ok &= encode_view(&maps.k, v[1].extent ? v[1] : v[0], s->dim, 128);
+  ok &= encode_view(&maps.v, v[2].extent ? v[2] : v[0], s->dim, 128);
   if (!ok) return cuda_fail(cudaErrorInvalidValue);
   lin::AttnFwdArgs a{attn_args(s, c), heads_ptr(v[3]), LSE};
   const cudaError_t e = lin::launch_attn_fwd(s->dtype == LIN_BFLOAT16, maps, a, (int)s->heads_kv,
@@ -141,25 +141,47 @@ lin_status attention_backward(const lin_attention_shape* s, const lin_heads* Q, 
   lin::AttnBwdMaps maps;
   const View& q = v[0].extent ? v[0] : v[1];   // (an empty side's maps are never used)
   const View& k = v[1].extent ? v[1] : v[0];
-  bool ok = encode_view(&maps.q, q, s->dim) && encode_view(&maps.k, k, s->dim);
-  ok = ok && encode_view(&maps.v, v[2].extent ? v[2] : q, s->dim);
-  ok = ok && encode_view(&maps.dout, v[4].extent ? v[4] : k, s->dim);
+  const int box = lin::kAttnBwdBox;
+  const bool ok = encode_view(&maps.q, q, s->dim, box) && encode_view(&maps.k, k, s->dim, box) &&
+                  encode_view(&maps.v, v[2].extent ? v[2] : q, s->dim, box) &&
+                  encode_view(&maps.dout, v[4].extent ? v[4] : k, s->dim, box);
   if (!ok) return cuda_fail(cudaErrorInvalidValue);
-  // workspace: delta [heads][tokens], then the largest dO norms of the query tiles
+  lin::AttnBwdArgs a{};
+  a.s = attn_args(s, c);
+  a.q = heads_ptr(v[0]);
+  a.k = heads_ptr(v[1]);
+  a.v = heads_ptr(v[2]);
+  a.o = heads_ptr(v[3]);
+  a.dout = heads_ptr(v[4]);
+  a.lse = LSE;
+  a.dq = heads_ptr(v[5]);
+  a.dk = heads_ptr(v[6]);
+  a.dv = heads_ptr(v[7]);
+  const int64_t tq = (c.max_q + 127) / 128, tk = (c.max_k + 127) / 128;
+  const int sms = sm_count(c.dev);
+  a.q_parts = lin::attn_parts(tq * s->heads_q * s->sequences, c.max_k, sms);
+  a.k_parts = lin::attn_parts(tk * s->heads_kv * s->sequences, c.max_q * (int64_t)a.s.group, sms);
+  // workspace: the parts' sums, delta [heads][tokens], then the largest dO
+  // norms of the query tiles
+  const uint64_t dq = a.q_parts > 1 ? (uint64_t)a.q_parts * s->tokens_q * s->heads_q * s->dim : 0;
+  const uint64_t dk = a.k_parts > 1 ? (uint64_t)a.k_parts * s->tokens_k * s->heads_kv * s->dim : 0;
   const uint64_t delta = (uint64_t)s->heads_q * (uint64_t)s->tokens_q;
-  const uint64_t norms =
-      (uint64_t)s->sequences * (uint64_t)s->heads_q * (uint64_t)((c.max_q + 127) / 128);
-  const size_t bytes = (size_t)std::max<uint64_t>(16, (delta + norms) * 4);
+  const uint64_t norms = (uint64_t)s->sequences * (uint64_t)s->heads_q * (uint64_t)tq;
+  const size_t bytes = (size_t)std::max<uint64_t>(16, (dq + 2 * dk + delta + norms) * 4);
   float* ws = static_cast<float*>(take_stream_workspace(c.dev, bytes, stream));
   if (!ws) return LIN_ERROR_CUDA;
-  lin::AttnBwdArgs a{attn_args(s, c), heads_ptr(v[3]), heads_ptr(v[4]), LSE, ws, ws + delta,
-                     heads_ptr(v[5]), heads_ptr(v[6]), heads_ptr(v[7])};
+  a.dq_part = ws;
+  a.dk_part = ws + dq;
+  a.dv_part = a.dk_part + dk;
+  a.delta = a.dv_part + dk;
+  a.norm = a.delta + delta;
+  int kernels = 0;
   cudaError_t e = lin::launch_attn_bwd(s->dtype == LIN_BFLOAT16, maps, a, (int)s->heads_kv,
-                                       (int)s->sequences, stream);
+                                       (int)s->sequences, &kernels, stream);
   const cudaError_t ef = cudaFreeAsync(ws, stream);
   if (e == cudaSuccess) e = ef;
   if (e != cudaSuccess) return cuda_fail(e);
-  set_last_launch_info((c.max_q > 0) + (c.max_k > 0), bytes);
+  set_last_launch_info(kernels, bytes);
   return LIN_SUCCESS;
 }
 

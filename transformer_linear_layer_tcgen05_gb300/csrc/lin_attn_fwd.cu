@@ -119,23 +119,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         bool second = false;
         if (n0 > 0) {   // (the first rows of a causal mask may see no key at all)
           mbar_arrive_expect_tx(bar(C::Q_FULL), C::TILE);
-          load_tile<DP>(base + C::OFF_Q, &maps.q, h, z, bar(C::Q_FULL));
+          load_tile<DP, 128>(base + C::OFF_Q, &maps.q, h, z, bar(C::Q_FULL));
         }
         for (int j = 0; j < n; ++j) {
           const int s = j % C::NKV, round = j / C::NKV;
           if (round > 0 && !wait_phase(bar(C::K_EMPTY + s), (round - 1) & 1, ctl)) break;
           mbar_arrive_expect_tx(bar(C::K_FULL + s), C::TILE);
-          load_tile<DP>(base + C::OFF_K + s * C::TILE, &maps.k, hk, sk.start + j * 128,
+          load_tile<DP, 128>(base + C::OFF_K + s * C::TILE, &maps.k, hk, sk.start + j * 128,
                         bar(C::K_FULL + s));
           ++k_issued;
           if (j == 0 && n1 > 0) {
             mbar_arrive_expect_tx(bar(C::Q_FULL + 1), C::TILE);
-            load_tile<DP>(base + C::OFF_Q + C::TILE, &maps.q, h, z + 128, bar(C::Q_FULL + 1));
+            load_tile<DP, 128>(base + C::OFF_Q + C::TILE, &maps.q, h, z + 128, bar(C::Q_FULL + 1));
             second = true;
           }
           if (round > 0 && !wait_phase(bar(C::V_EMPTY + s), (round - 1) & 1, ctl)) break;
           mbar_arrive_expect_tx(bar(C::V_FULL + s), C::TILE);
-          load_tile<DP>(base + C::OFF_V + s * C::TILE, &maps.v, hk, sk.start + j * 128,
+          load_tile<DP, 128>(base + C::OFF_V + s * C::TILE, &maps.v, hk, sk.start + j * 128,
                         bar(C::V_FULL + s));
           ++v_issued;
         }
@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (n > 0 && v_left < 128) {   // cut the last V tile at the sequence's end
         const int s = (n - 1) % C::NKV;
         if (warp_wait_phase(bar(C::V_FULL + s), ((n - 1) / C::NKV) & 1, ctl)) {
-          zero_rows<DP>(base + C::OFF_V + s * C::TILE, v_left, lane);
+          zero_rows<DP, 128>(base + C::OFF_V + s * C::TILE, v_left, lane);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::TAIL));
@@ -192,8 +192,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
               ok = ok && wait_phase(bar(C::P_READY + 2 * t + half), j & 1, ctl);
               if (!ok) break;
               tc_fence_after_sync();
-              umma_tokens<DP, BF16>(C::O_COL + t * DP, C::S_COL + t * 128 + half * 32,
-                                    v_desc + s * AttnTile<DP>::UNITS, half, j == 0 && half == 0);
+              umma_tokens<DP, BF16, 4>(C::O_COL + t * DP, C::S_COL + t * 128 + half * 32,
+                                       v_desc + s * AttnTile<DP>::UNITS, half * 4,
+                                       j == 0 && half == 0);
             }
             if (!ok) break;
             if (j + 1 < nt)
