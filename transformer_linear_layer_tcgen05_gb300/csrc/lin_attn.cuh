@@ -98,14 +98,15 @@ __device__ __forceinline__ float2 unpack16(uint32_t v) {
   }
 }
 
-// D[128 x 128] = A B^T over the DP entries of two operand tiles (K-major
-// descriptors).
-template <int DP, bool BF16>
+// D[128 x ROWS] = A B^T over the DP entries of two operand tiles, A of 128
+// tokens, B of ROWS (K-major descriptors).
+template <int DP, bool BF16, int ROWS = 128>
 __device__ __forceinline__ void umma_entries(uint32_t d, uint64_t a, uint64_t b) {
-  constexpr uint32_t idesc = attn_idesc<BF16, false, 128>();
+  constexpr uint32_t idesc = attn_idesc<BF16, false, ROWS>();
 #pragma unroll
   for (int kk = 0; kk < DP / 16; ++kk)
-    umma_f16(d, a + AttnTile<DP>::entry_step(kk), b + AttnTile<DP>::entry_step(kk), idesc, kk > 0);
+    umma_f16(d, a + AttnTile<DP>::entry_step(kk), b + AttnTile<DP, ROWS>::entry_step(kk), idesc,
+             kk > 0);
 }
 
 // The same with A's 128 rows in tensor memory (entries 2c, 2c + 1 in column c).

@@ -56,7 +56,7 @@ cudaError_t launch_attn_fwd(bool bf16, const AttnFwdMaps& maps, const AttnFwdArg
 // Parts that the backward kernels' other side is cut into (see there).
 int attn_parts(int64_t ctas, int64_t rows, int sms);
 // Tokens of a box of the backward kernels' maps.
-constexpr int kAttnBwdBox = 128;
+constexpr int kAttnBwdBox = 64;
 // The dQ kernel (which also leaves delta and norm), the dK, dV kernel, and the
 // sums of their parts; *kernels: how many that were.
 cudaError_t launch_attn_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArgs& args,

@@ -19,20 +19,19 @@
 // for dQ, where a row of dS meets only its own row of dQ; by the largest row
 // norm that a key tile meets for dK).
 //
-// Sixteen warps do the element-wise part, four threads to a row, each a
-// quarter of the tile's columns: it is a chain of short steps (wait, read,
-// exponentials, write back), and with half as many warps its latency, not its
-// instructions, set the pace. The products are issued so that the tensor
-// cores have one while each element-wise phase runs: S of the next tile
-// behind the use of this tile's P (or its reading, in the dQ kernel), dP of
-// the next behind the use of this tile's dS.
-//
-// A product of two 128-row operands in shared memory takes the whole of its
-// 128 bytes a clock, and the copies want their part. So the CTA's own
-// operands (Q and dO, or K and V) are in tensor memory beside the
-// accumulators; dK and dV of 128 entries leave no room for that. (Products of
-// 64 columns, which would, take as long as those of 128: tiles of 64 queries,
-// in turn or in two streams, took 950 us instead of 757 at 8192 tokens.)
+// The streamed side comes in tiles of 64 rows, which take turns between two
+// streams: each has its own S and dP in tensor memory and a warpgroup of its
+// own, a thread to a row, so that one stream's element-wise work and the
+// latencies between the roles pass while the tensor cores work for the other.
+// S of a stream's next tile is issued behind the product that reads this
+// tile's P (or behind its reading, in the dQ kernel), dP of the next behind
+// the use of dS. One thread issues all of them, and its own steps count: a
+// wait takes it some 100 cycles even for a barrier that is long complete, so
+// a turn has as few as it can (one barrier for the pair of streamed tiles
+// instead of one each: 703 -> 651 us at 8192 tokens; two issuing threads: no
+// further gain). The CTA's own operands (Q and dO, or K and V) are in tensor
+// memory beside the accumulators, which spares shared memory the reading of
+// them; dK and dV of 128 entries leave no room for that.
 //
 // Where there are fewer tiles than SMs the other side is cut into parts, a
 // CTA each, whose f32 sums a third kernel adds in order.
@@ -47,67 +46,57 @@ namespace {
 
 constexpr float kPShift = 8.0f;     // P^T is scaled by 2^8
 constexpr int kNormExp = 4;         // dO rows count as having a norm near 2^4
+constexpr int kRowWarps = 8;        // the two streams' warpgroups
+constexpr int kDkvThreads = 384;
+constexpr int kTailWarp = 10;       // of the dK, dV kernel: cuts tiles at the sequence's end
+constexpr int kStatsWarp = 11;      // of the dK, dV kernel: rows' statistics
+constexpr int kTurn = 64;           // rows of a streamed tile
 
-// Five warpgroups: four for the rows, and one for the issuing roles.
-constexpr int kBwdThreads = 640;
-constexpr int kRowThreads = 512;
-constexpr int kBwdCopyWarp = 16, kBwdMmaWarp = 17;
-constexpr int kStatsWarp = 19;      // of the dK, dV kernel: rows' statistics
-constexpr int kTailWarp = 18;       // of the dK, dV kernel: cuts tiles at the sequence's end
-constexpr int kBwdRegsRow = 104, kBwdRegsIssue = 64;
-static_assert(4 * kBwdRegsRow + kBwdRegsIssue <= 5 * 96, "registers of the launch");
-
-// Shared memory and barriers of both kernels. The streamed operands are two
-// rings of tiles of 128 tokens: A (K in the dQ kernel, Q in the other), whose
-// tile enters the first and the last product of its turn, and B (V, dO). A's
-// next tile is wanted early in a turn, while its last one is still in use.
-// OWN: the CTA's own operands are two tiles in shared memory too.
-template <int DP, int NA_, int NB_, int SUMS, bool OWN, int ROW_FLOATS>
+// Shared memory and barriers of both kernels. A stage of the ring holds the
+// streamed pair of tiles: A (K in the dQ kernel, Q in the other) and B (V, dO).
+// OWN: the CTA's own operands are two tiles of 128 rows in shared memory.
+template <int DP, int N_, int SUMS, bool OWN, int ROW_FLOATS>
 struct BwdCfg {
-  static constexpr int NA = NA_, NB = NB_;
-  using Tile = AttnTile<DP>;
+  static constexpr int N = N_;                   // stages
+  static constexpr bool kOwnSmem = OWN;
+  using Tile = AttnTile<DP, kTurn>;
   static constexpr uint32_t TILE = Tile::BYTES;
   static constexpr int OWN_READY = 0;            // the CTA's own operands
-  static constexpr int A_FULL = 1, A_EMPTY = A_FULL + NA;
-  static constexpr int B_FULL = A_EMPTY + NA, B_EMPTY = B_FULL + NB;
-  static constexpr int S_FULL = B_EMPTY + NB;    // S complete
-  static constexpr int DP_FULL = S_FULL + 1;     // dP complete
-  // 4 quarters each: S read (dQ) / P^T written (dK, dV); dS written
-  static constexpr int S_DONE = DP_FULL + 1, DS_READY = S_DONE + 4;
-  static constexpr int A_TAIL = DS_READY + 4;    // the stage, cut at the sequence's end
-  static constexpr int B_TAIL = A_TAIL + NA;
-  static constexpr int SUM_READY = B_TAIL + NB;  // (dQ) the quarters' sums of P dP
+  static constexpr int FULL = 1, EMPTY = FULL + N;
+  static constexpr int TAIL = EMPTY + N;         // the stage, cut at the sequence's end
+  // of each stream: S complete, dP complete, S read (dQ) or P^T written (dK,
+  // dV), dS written
+  static constexpr int S_FULL = TAIL + N, DP_FULL = S_FULL + 2;
+  static constexpr int S_DONE = DP_FULL + 2, DS_READY = S_DONE + 2;
+  static constexpr int SUM_READY = DS_READY + 2; // (dQ) the streams' sums of P dP
   static constexpr int OUT_FULL = SUM_READY + 1; // the sums complete (every product is)
   static constexpr int BARS = OUT_FULL + 1;
   static __device__ __forceinline__ uint32_t arrivals(int i) {
-    return i == SUM_READY || (i == OWN_READY && !OWN) ? kRowThreads
-           : i >= S_DONE && i < A_TAIL                ? 128
-                                                      : 1;
+    return i == SUM_READY || (i == OWN_READY && !OWN) ? 256 : i >= S_DONE && i < SUM_READY ? 128 : 1;
   }
-  static __device__ __forceinline__ bool streamed_full(int i) {
-    return (i >= A_FULL && i < A_EMPTY) || (i >= B_FULL && i < B_EMPTY);
-  }
+  static __device__ __forceinline__ bool streamed_full(int i) { return i >= FULL && i < EMPTY; }
   static constexpr uint32_t OFF_TMEM = BARS * 8, OFF_ABORT = OFF_TMEM + 4;
-  static constexpr uint32_t OFF_RED = 416;       // 20 floats
+  static constexpr uint32_t OFF_RED = 448;       // 16 floats
   static_assert(OFF_ABORT + 4 <= OFF_RED, "barrier region");
-  static constexpr uint32_t OFF_A = OWN ? 2 * TILE : 0;   // (tiles first: 1024-byte bases)
-  static constexpr uint32_t OFF_B = OFF_A + NA * TILE;
-  // dK, dV: [NA][128] floats -L log2 e + 8, then [NB][128] -a delta; dQ: the
-  // rows' sums of dO O and dO^2, by quarters
-  static constexpr uint32_t OFF_ROWS = OFF_B + NB * TILE;
+  static constexpr uint32_t OFF_OWN = 0;         // (tiles first: they want 1024-byte bases)
+  static constexpr uint32_t OFF_A = OWN ? 2 * AttnTile<DP>::BYTES : 0;
+  static constexpr uint32_t OFF_B = OFF_A + N * TILE;
+  // dK, dV: [N][kTurn] floats -L log2 e + 8, then [N][kTurn] -a delta; dQ:
+  // the rows' sums of dO O and dO^2, by halves
+  static constexpr uint32_t OFF_ROWS = OFF_B + N * TILE;
   static constexpr uint32_t OFF_CTL = OFF_ROWS + ROW_FLOATS * 4;
   static constexpr uint32_t SMEM = OFF_CTL + 512;
   static_assert(SMEM <= 232448, "shared memory");
-  // tensor memory: S and dP (P^T and dS over them), the sums (DP columns
-  // each), the CTA's own two operands
-  static constexpr uint32_t S_COL = 0, DP_COL = 128, OUT_COL = 256;
+  // tensor memory: S of the two streams, dP of them (P^T and dS over them),
+  // the sums (DP columns each), the CTA's own two operands
+  static constexpr uint32_t S_COL = 0, DP_COL = 2 * kTurn, OUT_COL = 4 * kTurn;
   static constexpr uint32_t OWN_COL = OUT_COL + SUMS * DP;
   static_assert(OWN_COL + (OWN ? 0 : DP) <= 512, "tensor memory");
 };
 template <int DP>
-using DqCfg = BwdCfg<DP, 4, DP == 64 ? 4 : 2, 1, false, 8 * 128>;
+using DqCfg = BwdCfg<DP, 6, 1, false, 4 * 128>;
 template <int DP>
-using DkvCfg = BwdCfg<DP, DP == 64 ? 4 : 3, DP == 64 ? 4 : 2, 2, DP == 128, (DP == 64 ? 8 : 5) * 128>;
+using DkvCfg = BwdCfg<DP, DP == 64 ? 6 : 5, 2, DP == 128, 2 * (DP == 64 ? 6 : 5) * kTurn>;
 
 // The CTA's shared memory, which the tiles' swizzle wants at a multiple of
 // 1024 bytes (it begins there: the kernels have no other shared memory). At
@@ -118,27 +107,14 @@ __device__ __forceinline__ bool smem_aligned(const void* p, int* status) {
   return false;
 }
 
-// f32 columns from tensor memory, complete on return.
-template <int N>
-__device__ __forceinline__ void tmem_get(uint32_t col, uint32_t (&r)[N]) {
-  static_assert(N == 16 || N == 32, "columns");
-  if constexpr (N == 32) {
-    tmem_ld_32x32b_x32(col, r);
-    tmem_wait_ld_x32(r);
-  } else {
-    tmem_ld_32x32b_x16(col, r);
-    tmem_wait_ld_x16(r);
-  }
-}
-
-// Packed operands into tensor memory.
+// Columns of packed results and operands into tensor memory.
 template <int N>
 __device__ __forceinline__ void tmem_put(uint32_t col, const uint32_t (&r)[N]) {
-  static_assert(N == 8 || N == 16, "columns");
-  if constexpr (N == 16)
-    tmem_st_32x32b_x16(col, r);
+  static_assert(N == 16 || N == 32, "columns");
+  if constexpr (N == 32)
+    tmem_st_32x32b_x32(col, r);
   else
-    tmem_st_32x32b_x8(col, r);
+    tmem_st_32x32b_x16(col, r);
 }
 
 // 2^e as a float, e held to where 2^e and 2^-e are normal.
@@ -162,13 +138,13 @@ struct HeadGrad {
                                       int64_t tokens, int heads, int dim, int64_t token, int h)
       : row(t.p + token * t.token_stride + (int64_t)h * t.head_stride),
         part_row(parts > 1 ? parts_base + ((part * tokens + token) * heads + h) * dim : nullptr) {}
-  // N columns from c0 on, times `back` (zeros if there is nothing), those
+  // 32 columns from c0 on, times `back` (zeros if there is nothing), those
   // below dim.
-  template <bool BF16, int N>
-  __device__ __forceinline__ void put(const uint32_t (&o)[N], bool any, float back, int c0,
+  template <bool BF16>
+  __device__ __forceinline__ void put(const uint32_t (&o)[32], bool any, float back, int c0,
                                       int dim) const {
 #pragma unroll
-    for (int g = 0; g < N / 8; ++g) {
+    for (int g = 0; g < 4; ++g) {
       const int col = c0 + g * 8;
       float v[8];
 #pragma unroll
@@ -190,7 +166,7 @@ struct HeadGrad {
 // ---------------------------------------------------------------- dQ
 
 template <int DP, bool BF16>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(kAttnThreads, 1)
     lin_attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps,
                        const __grid_constant__ AttnBwdArgs args) {
   using C = DqCfg<DP>;
@@ -208,10 +184,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const SeqRange sk = seq_range(a.cu_k, b, a.tokens_k, a.max_k);
   const int last = min(i0 + 127, sq.len - 1);
   const int hi = a.causal ? min(sk.len, last + sk.len - sq.len + 1) : sk.len;
-  const int tiles = hi > 0 ? (hi + 127) / 128 : 0;
-  // this part's key tiles: j0 .. j0 + n - 1
-  const int j0 = (int)((int64_t)tiles * part / args.q_parts);
-  const int n = (int)((int64_t)tiles * (part + 1) / args.q_parts) - j0;
+  const int tiles = hi > 0 ? (hi + kTurn - 1) / kTurn : 0;
+  // this part's key tiles: j0 .. j0 + n - 1 (one or two stay together: see delta)
+  const bool few = tiles <= 2;
+  const int j0 = few ? 0 : (int)((int64_t)tiles * part / args.q_parts);
+  const int n = few ? (part == 0 ? tiles : 0)
+                    : (int)((int64_t)tiles * (part + 1) / args.q_parts) - j0;
   const int hk = h / a.group;
 
   if (!smem_aligned(smem_raw, a.status)) return;
@@ -224,7 +202,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   auto k_tile = [&](int s) { return base + C::OFF_A + (uint32_t)s * C::TILE; };
   auto v_tile = [&](int s) { return base + C::OFF_B + (uint32_t)s * C::TILE; };
 
-  if (warp == kBwdMmaWarp) {
+  if (warp == kAttnMmaWarp) {
     tmem_alloc(base + C::OFF_CTL + C::OFF_TMEM, 512);
     tmem_relinquish_alloc_permit();
   }
@@ -237,146 +215,132 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
+  pdl_launch_dependents();   // (the dK, dV kernel waits for this grid's end before it reads)
   // (an allocation of all 512 columns begins at column 0)
   constexpr uint32_t tmem = 0;
   constexpr uint32_t kQ = C::OWN_COL, kDo = kQ + DP / 2;   // Q and dO
 
-  const int k_left = sk.len - (j0 + n - 1) * 128;   // keys of the last tile (128 or more: all)
-  if (warp >= kBwdCopyWarp) {
-    setmaxnreg_dec<kBwdRegsIssue>();
-    if (warp == kBwdCopyWarp) {
-      if (lane == 0 && n > 0) {
-        int a_issued = 0, b_issued = 0;
-        for (int j = 0; j < n; ++j) {
-          const int sa = j % C::NA, ra = j / C::NA, sb = j % C::NB, rb = j / C::NB;
-          if (ra > 0 && !wait_phase(bar(C::A_EMPTY + sa), (ra - 1) & 1, ctl)) break;
-          mbar_arrive_expect_tx(bar(C::A_FULL + sa), C::TILE);
-          load_tile<DP, 128>(k_tile(sa), &maps.k, hk, sk.start + (j0 + j) * 128, bar(C::A_FULL + sa));
-          ++a_issued;
-          if (rb > 0 && !wait_phase(bar(C::B_EMPTY + sb), (rb - 1) & 1, ctl)) break;
-          mbar_arrive_expect_tx(bar(C::B_FULL + sb), C::TILE);
-          load_tile<DP, 128>(v_tile(sb), &maps.v, hk, sk.start + (j0 + j) * 128, bar(C::B_FULL + sb));
-          ++b_issued;
-        }
-        if (*abort) {   // no copy may still be in flight when the CTA ends
-          for (int j = max(0, a_issued - C::NA); j < a_issued; ++j)
-            wait_phase(bar(C::A_FULL + j % C::NA), (j / C::NA) & 1, ctl, false);
-          for (int j = max(0, b_issued - C::NB); j < b_issued; ++j)
-            wait_phase(bar(C::B_FULL + j % C::NB), (j / C::NB) & 1, ctl, false);
-        }
+  const int k_left = sk.len - (j0 + n - 1) * kTurn;   // keys of the last tile (kTurn or more: all)
+  if (warp == kAttnCopyWarp) {
+    if (lane == 0 && n > 0) {
+      int issued = 0;
+      RingAt<C::N> r;
+      for (int j = 0; j < n; ++j, ++issued) {
+        if (j >= C::N && !wait_phase(bar(C::EMPTY + r.s), r.parity ^ 1, ctl)) break;
+        mbar_arrive_expect_tx(bar(C::FULL + r.s), 2 * C::TILE);
+        load_tile<DP, kTurn>(k_tile(r.s), &maps.k, hk, sk.start + (j0 + j) * kTurn,
+                             bar(C::FULL + r.s));
+        load_tile<DP, kTurn>(v_tile(r.s), &maps.v, hk, sk.start + (j0 + j) * kTurn,
+                             bar(C::FULL + r.s));
+        r.next();
       }
-      __syncwarp();
-      if (n > 0 && k_left < 128) {   // cut the last K tile at the sequence's end (dS K runs over it)
-        const int s = (n - 1) % C::NA;
-        if (warp_wait_phase(bar(C::A_FULL + s), ((n - 1) / C::NA) & 1, ctl)) {
-          zero_rows<DP, 128>(k_tile(s), k_left, lane);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(C::A_TAIL));
-        }
+      if (*abort) {   // no copy may still be in flight when the CTA ends
+        for (int j = max(0, issued - C::N); j < issued; ++j)
+          wait_phase(bar(C::FULL + j % C::N), (j / C::N) & 1, ctl, false);
       }
-    } else if (warp == kBwdMmaWarp) {
-      if (n > 0 && elect_one()) {   // one thread issues every product
-        const uint64_t k_desc = AttnTile<DP>::k_major(k_tile(0)), v_desc = AttnTile<DP>::k_major(v_tile(0));
-        const uint64_t kt_desc = AttnTile<DP>::mn_major(k_tile(0));
-        constexpr uint64_t STAGE = AttnTile<DP>::UNITS;
-        RingAt<C::NA> ka, kn;   // K of tile j, and of the next S
-        RingAt<C::NB> vn;       // V of the next dP
-        int kj = 0;             // tile of kn
-        auto scores = [&]() -> bool {   // S = Q K^T of the next tile
-          if (!wait_phase(bar(C::A_FULL + kn.s), kn.parity, ctl) ||
-              (++kj == n && k_left < 128 && !wait_phase(bar(C::A_TAIL), 0, ctl)))
-            return false;
-          umma_entries_tmem<DP, 128, BF16>(C::S_COL, kQ, k_desc + kn.s * STAGE);
-          umma_commit(bar(C::S_FULL));
-          kn.next();
-          return true;
-        };
-        auto dprobs = [&]() -> bool {   // dP = dO V^T of the next tile
-          if (!wait_phase(bar(C::B_FULL + vn.s), vn.parity, ctl)) return false;
-          umma_entries_tmem<DP, 128, BF16>(C::DP_COL, kDo, v_desc + vn.s * STAGE);
-          umma_commit(bar(C::DP_FULL));
-          umma_commit(bar(C::B_EMPTY + vn.s));
-          vn.next();
-          return true;
-        };
-        bool ok = wait_phase(bar(C::OWN_READY), 0, ctl);
-        tc_fence_after_sync();
-        ok = ok && scores() && dprobs();
-        for (int j = 0; j < n && ok; ++j) {
-          if (j + 1 < n) {
-#pragma unroll
-            for (int q = 0; q < 4; ++q) ok = ok && wait_phase(bar(C::S_DONE + q), j & 1, ctl);
-            tc_fence_after_sync();
-            ok = ok && scores();
-          }
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            ok = ok && wait_phase(bar(C::DS_READY + q), j & 1, ctl);
-            if (!ok) break;
-            tc_fence_after_sync();
-            umma_tokens<DP, BF16, 2>(C::OUT_COL, C::DP_COL + q * 32, kt_desc + ka.s * STAGE, q * 2,
-                                     j == 0 && q == 0);
-          }
-          if (!ok) break;
-          umma_commit(bar(C::A_EMPTY + ka.s));
-          ka.next();
-          if (j + 1 < n) ok = dprobs();
-        }
-        // (also on the way out: tensor memory must be idle at the end)
-        umma_commit(bar(C::OUT_FULL));
-        wait_phase(bar(C::OUT_FULL), 0, ctl, false);
-      }
-      __syncwarp();
     }
-  } else {
-    setmaxnreg_inc<kBwdRegsRow>();
-    const int quarter = warp >> 2, row = tid & 127;
+    __syncwarp();
+    if (n > 0 && k_left < kTurn) {   // cut the last K tile at the sequence's end (dS K runs over it)
+      const int s = (n - 1) % C::N;
+      if (warp_wait_phase(bar(C::FULL + s), ((n - 1) / C::N) & 1, ctl)) {
+        zero_rows<DP, kTurn>(k_tile(s), k_left, lane);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::TAIL));
+      }
+    }
+  } else if (warp == kAttnMmaWarp) {
+    if (n > 0 && elect_one()) {   // one thread issues every product
+      const uint64_t k_desc = C::Tile::k_major(k_tile(0)), v_desc = C::Tile::k_major(v_tile(0));
+      const uint64_t kt_desc = C::Tile::mn_major(k_tile(0));
+      constexpr uint64_t STAGE = C::Tile::UNITS;
+      RingAt<C::N> r, next;   // stages of tile j, and of the next S and dP
+      int nj = 0;             // tile of `next`
+      auto scores = [&](int t) -> bool {   // S = Q K^T of the next tile
+        if (!wait_phase(bar(C::FULL + next.s), next.parity, ctl) ||
+            (++nj == n && k_left < kTurn && !wait_phase(bar(C::TAIL), 0, ctl)))
+          return false;
+        umma_entries_tmem<DP, kTurn, BF16>(C::S_COL + t * kTurn, kQ, k_desc + next.s * STAGE);
+        umma_commit(bar(C::S_FULL + t));
+        return true;
+      };
+      auto dprobs = [&](int t) {   // dP = dO V^T of that tile
+        umma_entries_tmem<DP, kTurn, BF16>(C::DP_COL + t * kTurn, kDo, v_desc + next.s * STAGE);
+        umma_commit(bar(C::DP_FULL + t));
+        next.next();
+      };
+      bool ok = wait_phase(bar(C::OWN_READY), 0, ctl);
+      tc_fence_after_sync();
+      for (int t = 0; t < 2 && t < n && ok; ++t) {
+        ok = scores(t);
+        if (ok) dprobs(t);
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        const int t = j & 1, u = (j >> 1) & 1;
+        if (j + 2 < n) {
+          ok = wait_phase(bar(C::S_DONE + t), u, ctl);
+          tc_fence_after_sync();
+          ok = ok && scores(t);
+        }
+        ok = ok && wait_phase(bar(C::DS_READY + t), u, ctl);
+        if (!ok) break;
+        tc_fence_after_sync();
+        umma_tokens<DP, BF16, kTurn / 16>(C::OUT_COL, C::DP_COL + t * kTurn, kt_desc + r.s * STAGE,
+                                          0, j == 0);
+        umma_commit(bar(C::EMPTY + r.s));
+        r.next();
+        if (j + 2 < n) dprobs(t);
+      }
+      // (also on the way out: tensor memory must be idle at the end)
+      umma_commit(bar(C::OUT_FULL));
+      wait_phase(bar(C::OUT_FULL), 0, ctl, false);
+    }
+    __syncwarp();
+  } else if (warp < kRowWarps) {
+    const int half = warp >> 2, row = tid & 127;
     const int i = i0 + row;
     const bool live = i < sq.len;
     const int64_t token = sq.start + (live ? i : 0);
     const float c = a.scale * kLog2E;
     // The row's Q and dO into tensor memory; delta and the norm of dO on the
-    // way: each of the row's four threads has a quarter of the entries.
+    // way: each of the row's two threads has half of the entries.
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     float dsum = 0.0f, nsum = 0.0f;
     {
       auto row_of = [&](const HeadsPtr& t) {
         return live ? t.p + token * t.token_stride + (int64_t)h * t.head_stride : nullptr;
       };
-      constexpr int N = DP / 8;   // columns of a quarter
-      uint32_t x[N], y[N];
-      load_row_part<DP, 4>(x, row_of(args.q), quarter, a.dim);
-      load_row_part<DP, 4>(y, row_of(args.dout), quarter, a.dim);
-      tmem_put<N>(tmem + lanes + kQ + quarter * N, x);
-      tmem_put<N>(tmem + lanes + kDo + quarter * N, y);
-      load_row_part<DP, 4>(x, row_of(args.o), quarter, a.dim);
+      uint32_t x[DP / 4], y[DP / 4];
+      load_row_part<DP, 2>(x, row_of(args.q), half, a.dim);
+      load_row_part<DP, 2>(y, row_of(args.dout), half, a.dim);
+      tmem_put<DP / 4>(tmem + lanes + kQ + half * (DP / 4), x);
+      tmem_put<DP / 4>(tmem + lanes + kDo + half * (DP / 4), y);
+      load_row_part<DP, 2>(x, row_of(args.o), half, a.dim);
       tmem_wait_st();
       tc_fence_before_sync();
       mbar_arrive(bar(C::OWN_READY));
 #pragma unroll
-      for (int e = 0; e < N; ++e) {
+      for (int e = 0; e < DP / 4; ++e) {
         const float2 u = unpack16<BF16>(x[e]), v = unpack16<BF16>(y[e]);
         dsum = fmaf(u.x, v.x, fmaf(u.y, v.y, dsum));
         nsum = fmaf(v.x, v.x, fmaf(v.y, v.y, nsum));
       }
     }
-    float* red = reinterpret_cast<float*>(smem_raw + C::OFF_ROWS);   // 2 x [4][128] floats
-    auto four = [&](const float* r) { return (r[row] + r[128 + row]) + (r[256 + row] + r[384 + row]); };
-    red[quarter * 128 + row] = dsum;
-    red[512 + quarter * 128 + row] = nsum;
-    named_bar_sync(1, kRowThreads);
-    float delta = four(red);
-    const float norm = sqrtf(four(red + 512));
+    float* red = reinterpret_cast<float*>(smem_raw + C::OFF_ROWS);   // 4 x 128 floats
+    red[half * 128 + row] = dsum;
+    red[256 + half * 128 + row] = nsum;
+    named_bar_sync(1, 256);
+    float delta = red[row] + red[128 + row];
+    const float norm = sqrtf(red[256 + row] + red[384 + row]);
     float* red2 = reinterpret_cast<float*>(ctl_gen + C::OFF_RED);
-    if (quarter == 0) {
-      if (live && tiles != 1 && part == 0) args.delta[(int64_t)h * a.tokens_q + token] = delta;
+    if (half == 0) {
+      if (live && (tiles == 0 || !few) && part == 0) args.delta[(int64_t)h * a.tokens_q + token] = delta;
       float big = norm;   // (NaN rows do not count)
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
       if (lane == 0) red2[warp] = big;
     }
-    named_bar_sync(1, kRowThreads);
+    named_bar_sync(1, 256);
     if (tid == 0 && part == 0)
       args.norm[norm_at] = fmaxf(fmaxf(red2[0], red2[1]), fmaxf(red2[2], red2[3]));
     const int ne = norm_exponent(norm);
@@ -387,74 +351,94 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const float nl = lse == -INFINITY ? -INFINITY : -lse * kLog2E;
     // the last key that this row sees
     const int lim = live ? (a.causal ? min(sk.len - 1, i + sk.len - sq.len) : sk.len - 1) : -1;
-    const uint32_t s_col = tmem + lanes + C::S_COL + quarter * 32;
-    const uint32_t dp_col = tmem + lanes + C::DP_COL + quarter * 32;
-    const float2 cc = make_float2(c, c), ll = make_float2(nl, nl), aa = make_float2(amp, amp);
+    const uint32_t s_col = tmem + lanes + C::S_COL + half * kTurn;
+    const uint32_t dp_col = tmem + lanes + C::DP_COL + half * kTurn;
+    if (few && n == 1 && half == 1) {   // (no tile: nothing to the row's sums below)
+      red[128 + row] = 0.0f;
+      red[384 + row] = 0.0f;
+      mbar_arrive(bar(C::SUM_READY));
+    }
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      ok = warp_wait_phase(bar(C::S_FULL), j & 1, ctl);
+    for (int j = half; j < n; j += 2) {   // the warpgroup's stream
+      const int u = (j >> 1) & 1;
+      ok = warp_wait_phase(bar(C::S_FULL + half), u, ctl);
       if (!ok) break;
       tc_fence_after_sync();
-      uint32_t p[32], d[32], w[16];
-      tmem_ld_32x32b_x32(s_col, p);
-      tmem_wait_ld_x32(p);
+      uint32_t p[2][32], d[2][32];
+      tmem_ld_32x32b_x32(s_col, p[0]);
+      tmem_ld_32x32b_x32(s_col + 32, p[1]);
+      tmem_wait_ld_x32(p[0]);
+      tmem_wait_ld_x32(p[1]);
       tc_fence_before_sync();
-      mbar_arrive(bar(C::S_DONE + quarter));
+      mbar_arrive(bar(C::S_DONE + half));
+      const float2 cc = make_float2(c, c), ll = make_float2(nl, nl);
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        const float2 x = fma2(make_float2(__uint_as_float(p[e]), __uint_as_float(p[e + 1])), cc, ll);
-        p[e] = __float_as_uint(ex2_approx(x.x));
-        p[e + 1] = __float_as_uint(ex2_approx(x.y));
-      }
-      ok = warp_wait_phase(bar(C::DP_FULL), j & 1, ctl);
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float2 x = fma2(make_float2(__uint_as_float(p[q][e]), __uint_as_float(p[q][e + 1])), cc, ll);
+          p[q][e] = __float_as_uint(ex2_approx(x.x));
+          p[q][e + 1] = __float_as_uint(ex2_approx(x.y));
+        }
+      ok = warp_wait_phase(bar(C::DP_FULL + half), u, ctl);
       if (!ok) break;
       tc_fence_after_sync();
-      tmem_ld_32x32b_x32(dp_col, d);
-      tmem_wait_ld_x32(d);
-      if (tiles == 1) {
-        // All of the row's keys are in this tile, so delta is at hand as the
-        // sum of P dP itself. It replaces the sum of dO O, whose O has been
+      tmem_ld_32x32b_x32(dp_col, d[0]);
+      tmem_ld_32x32b_x32(dp_col + 32, d[1]);
+      tmem_wait_ld_x32(d[0]);
+      tmem_wait_ld_x32(d[1]);
+      if (few) {
+        // All of the row's keys are in the streams' first tiles, so delta is
+        // at hand as the sum of P dP itself. It replaces the sum of dO O, whose O has been
         // rounded to 16 bits: with few keys that rounding is no longer small
         // against dP - delta (at one key the difference is zero).
         float sd = 0.0f, sp = 0.0f;
-        const int lim_q = lim - quarter * 32;
+        const int lim_h = lim - half * kTurn;
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (e <= lim_q) {
-            sd = fmaf(__uint_as_float(p[e]), __uint_as_float(d[e]), sd);
-            sp += __uint_as_float(p[e]);
-          }
-        red[quarter * 128 + row] = sd;
-        red[512 + quarter * 128 + row] = sp;
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (q * 32 + e <= lim_h) {
+              sd = fmaf(__uint_as_float(p[q][e]), __uint_as_float(d[q][e]), sd);
+              sp += __uint_as_float(p[q][e]);
+            }
+        red[half * 128 + row] = sd;
+        red[256 + half * 128 + row] = sp;
         mbar_arrive(bar(C::SUM_READY));
         ok = warp_wait_phase(bar(C::SUM_READY), 0, ctl);
         if (!ok) break;
-        sp = four(red + 512);
-        delta = sp > 0.0f ? four(red) / sp : 0.0f;
+        sp = red[256 + row] + red[384 + row];
+        delta = sp > 0.0f ? (red[row] + red[128 + row]) / sp : 0.0f;
         nd = -delta * amp;
-        if (quarter == 0 && live) args.delta[(int64_t)h * a.tokens_q + token] = delta;
+        if (half == 0 && live) args.delta[(int64_t)h * a.tokens_q + token] = delta;
       }
-      const float2 dd = make_float2(nd, nd);
+      const float2 aa = make_float2(amp, amp), dd = make_float2(nd, nd);
 #pragma unroll
-      for (int e = 0; e < 32; e += 2) {
-        const float2 x = fma2(make_float2(__uint_as_float(d[e]), __uint_as_float(d[e + 1])), aa, dd);
-        const float2 y = mul2(make_float2(__uint_as_float(p[e]), __uint_as_float(p[e + 1])), x);
-        d[e] = __float_as_uint(y.x);
-        d[e + 1] = __float_as_uint(y.y);
+      for (int q = 0; q < 2; ++q)
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float2 x = fma2(make_float2(__uint_as_float(d[q][e]), __uint_as_float(d[q][e + 1])), aa, dd);
+          const float2 y = mul2(make_float2(__uint_as_float(p[q][e]), __uint_as_float(p[q][e + 1])), x);
+          d[q][e] = __float_as_uint(y.x);
+          d[q][e + 1] = __float_as_uint(y.y);
+        }
+      const int lim_j = lim - (j0 + j) * kTurn;
+      if (__any_sync(0xffffffffu, lim_j < kTurn - 1)) {   // masked keys, whatever their dP holds
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (q * 32 + e > lim_j) d[q][e] = 0u;
       }
-      const int lim_j = lim - (j0 + j) * 128 - quarter * 32;
-      if (__any_sync(0xffffffffu, lim_j < 31)) {   // masked keys, whatever their dP holds
+      uint32_t w[32];
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (e > lim_j) d[e] = 0u;
-      }
-#pragma unroll
-      for (int e = 0; e < 16; ++e)
-        w[e] = pack16<BF16>(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]));
-      tmem_put<16>(dp_col, w);
+      for (int e = 0; e < 32; ++e)
+        w[e] = pack16<BF16>(__uint_as_float(d[e >> 4][(2 * e) & 31]),
+                            __uint_as_float(d[e >> 4][(2 * e + 1) & 31]));
+      tmem_st_32x32b_x32(dp_col, w);
       tmem_wait_st();
       tc_fence_before_sync();
-      mbar_arrive(bar(C::DS_READY + quarter));
+      mbar_arrive(bar(C::DS_READY + half));
     }
     if (ok && n > 0) {
       ok = warp_wait_phase(bar(C::OUT_FULL), 0, ctl);
@@ -464,16 +448,22 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const float back = a.scale * pow2i(-ne);
       const HeadGrad out(args.dq, args.dq_part, args.q_parts, part, a.tokens_q, a.heads_q, a.dim,
                          token, h);
-      constexpr int N = DP / 4;
-      uint32_t o[N];
-      if (n > 0) tmem_get<N>(tmem + lanes + C::OUT_COL + quarter * N, o);
-      out.put<BF16, N>(o, n > 0, back, quarter * N, live ? a.dim : 0);
+#pragma unroll
+      for (int q = 0; q < DP / 64; ++q) {
+        const int c0 = half * (DP / 2) + q * 32;
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld_32x32b_x32(tmem + lanes + C::OUT_COL + c0, o);
+          tmem_wait_ld_x32(o);
+        }
+        out.put<BF16>(o, n > 0, back, c0, live ? a.dim : 0);
+      }
     }
   }
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == kBwdMmaWarp) {
+  if (warp == kAttnMmaWarp) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }
@@ -482,7 +472,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 // ---------------------------------------------------------------- dK, dV
 
 template <int DP, bool BF16>
-__global__ void __launch_bounds__(kBwdThreads, 1)
+__global__ void __launch_bounds__(kDkvThreads, 1)
     lin_attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps,
                         const __grid_constant__ AttnBwdArgs args) {
   using C = DkvCfg<DP>;
@@ -495,14 +485,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const SeqRange sq = seq_range(a.cu_q, b, a.tokens_q, a.max_q);
   // query tiles t0 .. t1 - 1 of each head of the group
   const int off = sk.len - sq.len;   // causal: query i sees the keys up to i + off
-  const int t1 = (sq.len + 128 - 1) / 128;
-  const int t0 = a.causal ? min(max(k0 - off, 0) / 128, t1) : 0;
+  const int t1 = (sq.len + kTurn - 1) / kTurn;
+  const int t0 = a.causal ? min(max(k0 - off, 0) / kTurn, t1) : 0;
   const int per = t1 - t0;
   // this part's turns (of all heads' tiles): from .. from + n - 1
   const int from = (int)((int64_t)per * a.group * part / args.k_parts);
   const int n = (int)((int64_t)per * a.group * (part + 1) / args.k_parts) - from;
   const int tile0 = per > 0 ? from % per : 0;         // the first turn's tile of its head
-  const int q_left = sq.len - (t1 - 1) * 128;          // queries of the last tile
+  const int q_left = sq.len - (t1 - 1) * kTurn;          // queries of the last tile
   const int h0 = hk * a.group;
 
   if (!smem_aligned(smem_raw, a.status)) return;
@@ -514,10 +504,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const WaitCtl ctl{a.timeout_ns, abort, a.status};
   auto q_tile = [&](int s) { return base + C::OFF_A + (uint32_t)s * C::TILE; };
   auto do_tile = [&](int s) { return base + C::OFF_B + (uint32_t)s * C::TILE; };
-  auto lse_rows = [&](int s) { return reinterpret_cast<float*>(smem_raw + C::OFF_ROWS) + s * 128; };
-  auto delta_rows = [&](int s) { return lse_rows(C::NA + s); };
+  auto lse_rows = [&](int s) { return reinterpret_cast<float*>(smem_raw + C::OFF_ROWS) + s * kTurn; };
+  auto delta_rows = [&](int s) { return lse_rows(C::N + s); };
 
-  if (warp == kBwdMmaWarp) {
+  if (warp == kAttnMmaWarp) {
     tmem_alloc(base + C::OFF_CTL + C::OFF_TMEM, 512);
     tmem_relinquish_alloc_permit();
   }
@@ -527,6 +517,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       mbar_init(bar(i), C::streamed_full(i) ? 2 : C::arrivals(i));   // (copy and statistics)
     fence_barrier_init();
   }
+  pdl_wait();   // delta and norm come from the dQ kernel
   // the largest row norm of dO that this tile meets (every tile of the
   // heads: the masked ones do no harm)
   float* red = reinterpret_cast<float*>(ctl_gen + C::OFF_RED);
@@ -534,7 +525,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const int tiles = (a.max_q + 127) / 128;
     const float* nm = args.norm + ((int64_t)b * a.heads_q + h0) * tiles;
     float big = 0.0f;
-    for (int i = tid; i < tiles * a.group; i += kBwdThreads) big = fmaxf(big, nm[i]);
+    for (int i = tid; i < tiles * a.group; i += kDkvThreads) big = fmaxf(big, nm[i]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
     if (lane == 0) red[warp] = big;
@@ -544,324 +535,313 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   tc_fence_after_sync();
   // (an allocation of all 512 columns begins at column 0)
   constexpr uint32_t tmem = 0;
-  constexpr uint32_t kK = C::OWN_COL, kV = kK + DP / 2;   // K and V: heads of up to 64
-  const uint32_t k_own = base, v_own = base + C::TILE;      // of 128
+  constexpr uint32_t kK = C::OWN_COL, kV = kK + DP / 2;   // K and V (heads of up to 64)
+  const uint32_t k_own = base + C::OFF_OWN, v_own = k_own + AttnTile<DP>::BYTES;   // (of 128)
   float big = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kBwdThreads / 32; ++w) big = fmaxf(big, red[w]);
+  for (int w = 0; w < kDkvThreads / 32; ++w) big = fmaxf(big, red[w]);
   const int ne = norm_exponent(big);
   // scale of dP and delta: dS then carries 2^ne, P's 2^8 taken back
   const float damp = pow2i(ne) * pow2i(-(int)kPShift);
 
-  if (warp >= kBwdCopyWarp) {
-    setmaxnreg_dec<kBwdRegsIssue>();
-    if (warp == kBwdCopyWarp) {
-      if (n > 0) {
-        if (DP == 128 && lane == 0) {
-          mbar_arrive_expect_tx(bar(C::OWN_READY), 2 * C::TILE);
-          load_tile<DP, 128>(k_own, &maps.k, hk, sk.start + k0, bar(C::OWN_READY));
-          load_tile<DP, 128>(v_own, &maps.v, hk, sk.start + k0, bar(C::OWN_READY));
+  if (warp == kAttnCopyWarp) {
+    if (n > 0) {
+      if (C::kOwnSmem && lane == 0) {
+        mbar_arrive_expect_tx(bar(C::OWN_READY), 2 * AttnTile<DP>::BYTES);
+#pragma unroll
+        for (int r = 0; r < 128; r += kTurn)
+#pragma unroll
+          for (int s = 0; s < AttnTile<DP>::SUB; ++s) {
+            const uint32_t at = s * AttnTile<DP>::SUB_BYTES + r * 128;
+            tma_load_3d(k_own + at, &maps.k, s * 64, hk, sk.start + k0 + r, bar(C::OWN_READY));
+            tma_load_3d(v_own + at, &maps.v, s * 64, hk, sk.start + k0 + r, bar(C::OWN_READY));
+          }
+      }
+      if (lane == 0) {
+        int issued = 0;
+        RingAt<C::N> r;
+        int h = h0 + from / per, tile = tile0;   // of this turn (n > 0: per > 0)
+        for (int it = 0; it < n; ++it, ++issued) {
+          const int z = sq.start + (t0 + tile) * kTurn;
+          if (it >= C::N && !wait_phase(bar(C::EMPTY + r.s), r.parity ^ 1, ctl)) break;
+          mbar_arrive_expect_tx(bar(C::FULL + r.s), 2 * C::TILE);
+          load_tile<DP, kTurn>(q_tile(r.s), &maps.q, h, z, bar(C::FULL + r.s));
+          load_tile<DP, kTurn>(do_tile(r.s), &maps.dout, h, z, bar(C::FULL + r.s));
+          r.next();
+          if (++tile == per) {
+            tile = 0;
+            ++h;
+          }
         }
-        int a_issued = 0, b_issued = 0;
-        if (lane == 0) {
-          RingAt<C::NA> qa;
-          RingAt<C::NB> da;
-          int h = h0 + from / per, tile = tile0;   // of this turn (n > 0: per > 0)
-          for (int it = 0; it < n; ++it) {
-            const int z = sq.start + (t0 + tile) * 128;
-            if (it >= C::NA && !wait_phase(bar(C::A_EMPTY + qa.s), qa.parity ^ 1, ctl)) break;
-            mbar_arrive_expect_tx(bar(C::A_FULL + qa.s), C::TILE);
-            load_tile<DP, 128>(q_tile(qa.s), &maps.q, h, z, bar(C::A_FULL + qa.s));
-            ++a_issued;
-            if (it >= C::NB && !wait_phase(bar(C::B_EMPTY + da.s), da.parity ^ 1, ctl)) break;
-            mbar_arrive_expect_tx(bar(C::B_FULL + da.s), C::TILE);
-            load_tile<DP, 128>(do_tile(da.s), &maps.dout, h, z, bar(C::B_FULL + da.s));
-            ++b_issued;
-            qa.next();
-            da.next();
-            if (++tile == per) {
-              tile = 0;
-              ++h;
-            }
-          }
-          if (*abort) {   // no copy may still be in flight when the CTA ends
-            if (DP == 128) wait_phase(bar(C::OWN_READY), 0, ctl, false);
-            for (int it = max(0, a_issued - C::NA); it < a_issued; ++it)
-              wait_phase(bar(C::A_FULL + it % C::NA), (it / C::NA) & 1, ctl, false);
-            for (int it = max(0, b_issued - C::NB); it < b_issued; ++it)
-              wait_phase(bar(C::B_FULL + it % C::NB), (it / C::NB) & 1, ctl, false);
-          }
+        if (*abort) {   // no copy may still be in flight when the CTA ends
+          if (C::kOwnSmem) wait_phase(bar(C::OWN_READY), 0, ctl, false);
+          for (int it = max(0, issued - C::N); it < issued; ++it)
+            wait_phase(bar(C::FULL + it % C::N), (it / C::N) & 1, ctl, false);
         }
       }
-    } else if (warp == kStatsWarp) {
-      // The rows' statistics of each turn, in the form that the element-wise
-      // warps add: rows behind the sequence's end and rows without a key have
-      // P = 0. A warp of its own, which has the next turn's on their way while it
-      // waits for a stage: with these loads between its copies the copying warp
-      // took longer for a turn than the products (3000 cycles; 757 us at 8192
-      // tokens).
-      constexpr int N = 128 / 32;
-      RingAt<C::NA> qa;
-      RingAt<C::NB> da;
-      int h = n > 0 ? h0 + from / per : 0, tile = tile0;
-      float lse[N], delta[N];
-      auto load = [&]() {
+    }
+  } else if (warp == kStatsWarp) {
+    // The rows' statistics of each turn, in the form that the element-wise
+    // warps add: rows behind the sequence's end and rows without a key have
+    // P = 0. A warp of its own, which has the next turn's on their way while it
+    // waits for a stage: with these loads between its copies the copying warp
+    // took longer for a turn than the products (3000 cycles; 757 us at 8192
+    // tokens).
+    constexpr int N = kTurn / 32;
+    RingAt<C::N> r;
+    int h = n > 0 ? h0 + from / per : 0, tile = tile0;
+    float lse[N], delta[N];
+    auto load = [&]() {
 #pragma unroll
-        for (int e = 0; e < N; ++e) {
-          const int i = (t0 + tile) * 128 + e * 32 + lane;
-          const int64_t at = (int64_t)h * a.tokens_q + sq.start + i;
-          lse[e] = i < sq.len ? args.lse[at] : -INFINITY;
-          delta[e] = i < sq.len ? args.delta[at] : 0.0f;
-        }
-        if (++tile == per) {
-          tile = 0;
-          ++h;
-        }
-      };
-      if (n > 0) load();
-      for (int it = 0; it < n; ++it) {
-        float nl[N], nd[N];
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          nl[e] = lse[e] == -INFINITY ? -INFINITY : fmaf(-lse[e], kLog2E, kPShift);
-          nd[e] = delta[e] * -damp;
-        }
-        if (it + 1 < n) load();
-        if (it >= C::NA && !warp_wait_phase(bar(C::A_EMPTY + qa.s), qa.parity ^ 1, ctl)) break;
-#pragma unroll
-        for (int e = 0; e < N; ++e) lse_rows(qa.s)[e * 32 + lane] = nl[e];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::A_FULL + qa.s));
-        if (it >= C::NB && !warp_wait_phase(bar(C::B_EMPTY + da.s), da.parity ^ 1, ctl)) break;
-#pragma unroll
-        for (int e = 0; e < N; ++e) delta_rows(da.s)[e * 32 + lane] = nd[e];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::B_FULL + da.s));
-        qa.next();
-        da.next();
+      for (int e = 0; e < N; ++e) {
+        const int i = (t0 + tile) * kTurn + e * 32 + lane;
+        const int64_t at = (int64_t)h * a.tokens_q + sq.start + i;
+        lse[e] = i < sq.len ? args.lse[at] : -INFINITY;
+        delta[e] = i < sq.len ? args.delta[at] : 0.0f;
       }
-    } else if (warp == kTailWarp) {
-      // Where the last query tile of a head is cut by the sequence's end, this
-      // warp hands every stage on to the products (a phase that nobody waited
-      // for would not be told from the one before it), that tile with the rows
-      // behind the end zeroed: they enter the products that run over the queries.
-      if (n > 0 && q_left < 128) {
-        int tile = tile0;
-        RingAt<C::NA> qa;
-        RingAt<C::NB> da;
-        for (int it = 0; it < n; ++it) {
-          const bool cut = ++tile == per;
-          if (cut) tile = 0;
-          if (!warp_wait_phase(bar(C::A_FULL + qa.s), qa.parity, ctl)) break;
-          if (cut) {
-            zero_rows<DP, 128>(q_tile(qa.s), q_left, lane);
-            fence_proxy_async_smem();
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(C::A_TAIL + qa.s));
-          if (!warp_wait_phase(bar(C::B_FULL + da.s), da.parity, ctl)) break;
-          if (cut) {
-            zero_rows<DP, 128>(do_tile(da.s), q_left, lane);
-            fence_proxy_async_smem();
-          }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar(C::B_TAIL + da.s));
-          qa.next();
-          da.next();
-        }
+      if (++tile == per) {
+        tile = 0;
+        ++h;
       }
-    } else if (warp == kBwdMmaWarp) {
-      if (n > 0 && elect_one()) {   // one thread issues every product
-        const uint64_t q_desc = C::Tile::k_major(q_tile(0)), do_desc = C::Tile::k_major(do_tile(0));
-        const uint64_t qt_desc = C::Tile::mn_major(q_tile(0));
-        const uint64_t dot_desc = C::Tile::mn_major(do_tile(0));
-        constexpr uint64_t STAGE = C::Tile::UNITS;
-        const int a_ready = q_left < 128 ? C::A_TAIL : C::A_FULL;
-        const int b_ready = q_left < 128 ? C::B_TAIL : C::B_FULL;
-        RingAt<C::NA> qa, qn;   // Q of tile it, and of the next S^T
-        RingAt<C::NB> da, dn;   // dO of tile it, and of the next dP^T
-        auto own = [&](uint32_t d, uint32_t col, uint32_t tile, uint64_t other) {
-          if constexpr (DP == 128)
-            umma_entries<DP, BF16>(d, C::Tile::k_major(tile), other);
-          else
-            umma_entries_tmem<DP, 128, BF16>(d, col, other);
-        };
-        auto scores = [&]() -> bool {   // S^T = K Q^T of the next tile
-          if (!wait_phase(bar(a_ready + qn.s), qn.parity, ctl)) return false;
-          own(C::S_COL, kK, k_own, q_desc + qn.s * STAGE);
-          umma_commit(bar(C::S_FULL));
-          qn.next();
-          return true;
-        };
-        auto dprobs = [&]() -> bool {   // dP^T = V dO^T of the next tile
-          if (!wait_phase(bar(b_ready + dn.s), dn.parity, ctl)) return false;
-          own(C::DP_COL, kV, v_own, do_desc + dn.s * STAGE);
-          umma_commit(bar(C::DP_FULL));
-          dn.next();
-          return true;
-        };
-        bool ok = wait_phase(bar(C::OWN_READY), 0, ctl);
-        tc_fence_after_sync();
-        ok = ok && scores() && dprobs();
-        for (int it = 0; it < n && ok; ++it) {
+    };
+    if (n > 0) load();
+    for (int it = 0; it < n; ++it) {
+      float nl[N], nd[N];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {   // dV += P^T dO
-            ok = ok && wait_phase(bar(C::S_DONE + q), it & 1, ctl);
-            if (!ok) break;
-            tc_fence_after_sync();
-            umma_tokens<DP, BF16, 2>(C::OUT_COL, C::S_COL + q * 32, dot_desc + da.s * STAGE, q * 2,
-                                     it == 0 && q == 0);
-          }
-          if (ok && it + 1 < n) ok = scores();
+      for (int e = 0; e < N; ++e) {
+        nl[e] = lse[e] == -INFINITY ? -INFINITY : fmaf(-lse[e], kLog2E, kPShift);
+        nd[e] = delta[e] * -damp;
+      }
+      if (it + 1 < n) load();
+      if (it >= C::N && !warp_wait_phase(bar(C::EMPTY + r.s), r.parity ^ 1, ctl)) break;
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {   // dK += dS^T Q
-            ok = ok && wait_phase(bar(C::DS_READY + q), it & 1, ctl);
-            if (!ok) break;
-            tc_fence_after_sync();
-            umma_tokens<DP, BF16, 2>(C::OUT_COL + DP, C::DP_COL + q * 32, qt_desc + qa.s * STAGE, q * 2,
-                                     it == 0 && q == 0);
-          }
-          if (!ok) break;
-          // (dO's stage too: its rows' delta was read for dS)
-          umma_commit(bar(C::A_EMPTY + qa.s));
-          umma_commit(bar(C::B_EMPTY + da.s));
-          qa.next();
-          da.next();
-          if (it + 1 < n) ok = dprobs();
-        }
-        // (also on the way out: tensor memory must be idle at the end)
-        umma_commit(bar(C::OUT_FULL));
-        wait_phase(bar(C::OUT_FULL), 0, ctl, false);
+      for (int e = 0; e < N; ++e) {
+        lse_rows(r.s)[e * 32 + lane] = nl[e];
+        delta_rows(r.s)[e * 32 + lane] = nd[e];
       }
       __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::FULL + r.s));
+      r.next();
     }
-  } else {
-    setmaxnreg_inc<kBwdRegsRow>();
-    const int quarter = warp >> 2, row = tid & 127;
+  } else if (warp == kTailWarp) {
+    // Where the last query tile of a head is cut by the sequence's end, this
+    // warp hands every stage on to the products (a phase that nobody waited
+    // for would not be told from the one before it), that tile with the rows
+    // behind the end zeroed: they enter the products that run over the queries.
+    if (n > 0 && q_left < kTurn) {
+      int tile = tile0;
+      RingAt<C::N> r;
+      for (int it = 0; it < n; ++it) {
+        if (!warp_wait_phase(bar(C::FULL + r.s), r.parity, ctl)) break;
+        if (++tile == per) {
+          tile = 0;
+          zero_rows<DP, kTurn>(q_tile(r.s), q_left, lane);
+          zero_rows<DP, kTurn>(do_tile(r.s), q_left, lane);
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::TAIL + r.s));
+        r.next();
+      }
+    }
+  } else if (warp == kAttnMmaWarp) {
+    if (n > 0 && elect_one()) {   // one thread issues every product
+      const uint64_t q_desc = C::Tile::k_major(q_tile(0)), do_desc = C::Tile::k_major(do_tile(0));
+      const uint64_t qt_desc = C::Tile::mn_major(q_tile(0));
+      const uint64_t dot_desc = C::Tile::mn_major(do_tile(0));
+      constexpr uint64_t STAGE = C::Tile::UNITS;
+      const int ready = q_left < kTurn ? C::TAIL : C::FULL;
+      RingAt<C::N> r, next;   // stages of turn it, and of the next S^T and dP^T
+      auto own = [&](uint32_t d, uint32_t col, uint32_t tile, uint64_t other) {
+        if constexpr (C::kOwnSmem)
+          umma_entries<DP, BF16, kTurn>(d, AttnTile<DP>::k_major(tile), other);
+        else
+          umma_entries_tmem<DP, kTurn, BF16>(d, col, other);
+      };
+      auto scores = [&](int t) -> bool {   // S^T = K Q^T of the next turn
+        if (!wait_phase(bar(ready + next.s), next.parity, ctl)) return false;
+        own(C::S_COL + t * kTurn, kK, k_own, q_desc + next.s * STAGE);
+        umma_commit(bar(C::S_FULL + t));
+        return true;
+      };
+      auto dprobs = [&](int t) {   // dP^T = V dO^T of that turn
+        own(C::DP_COL + t * kTurn, kV, v_own, do_desc + next.s * STAGE);
+        umma_commit(bar(C::DP_FULL + t));
+        next.next();
+      };
+      bool ok = wait_phase(bar(C::OWN_READY), 0, ctl);
+      tc_fence_after_sync();
+      for (int t = 0; t < 2 && t < n && ok; ++t) {
+        ok = scores(t);
+        if (ok) dprobs(t);
+      }
+      for (int it = 0; it < n && ok; ++it) {
+        const int t = it & 1, u = (it >> 1) & 1;
+        ok = wait_phase(bar(C::S_DONE + t), u, ctl);
+        if (!ok) break;
+        tc_fence_after_sync();
+        umma_tokens<DP, BF16, kTurn / 16>(C::OUT_COL, C::S_COL + t * kTurn, dot_desc + r.s * STAGE,
+                                          0, it == 0);   // dV += P^T dO
+        if (it + 2 < n) ok = scores(t);
+        ok = ok && wait_phase(bar(C::DS_READY + t), u, ctl);
+        if (!ok) break;
+        tc_fence_after_sync();
+        umma_tokens<DP, BF16, kTurn / 16>(C::OUT_COL + DP, C::DP_COL + t * kTurn,
+                                          qt_desc + r.s * STAGE, 0, it == 0);   // dK += dS^T Q
+        umma_commit(bar(C::EMPTY + r.s));
+        r.next();
+        if (it + 2 < n) dprobs(t);
+      }
+      // (also on the way out: tensor memory must be idle at the end)
+      umma_commit(bar(C::OUT_FULL));
+      wait_phase(bar(C::OUT_FULL), 0, ctl, false);
+    }
+    __syncwarp();
+  } else if (warp < kRowWarps) {
+    const int half = warp >> 2, row = tid & 127;
     const int key = k0 + row;
     const bool live = key < sk.len;
     const float c = a.scale * kLog2E;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
-    const uint32_t s_col = tmem + lanes + C::S_COL + quarter * 32;
-    const uint32_t dp_col = tmem + lanes + C::DP_COL + quarter * 32;
-    if constexpr (DP == 64) {   // the row's K and V into tensor memory, a quarter by each thread
+    const uint32_t s_col = tmem + lanes + C::S_COL + half * kTurn;
+    const uint32_t dp_col = tmem + lanes + C::DP_COL + half * kTurn;
+    if constexpr (!C::kOwnSmem) {   // the row's K and V into tensor memory, half by each thread
       auto row_of = [&](const HeadsPtr& t) {
         return live ? t.p + (int64_t)(sk.start + key) * t.token_stride + (int64_t)hk * t.head_stride
                     : nullptr;
       };
-      constexpr int N = DP / 8;
-      uint32_t x[N], y[N];
-      load_row_part<DP, 4>(x, row_of(args.k), quarter, a.dim);
-      load_row_part<DP, 4>(y, row_of(args.v), quarter, a.dim);
-      tmem_put<N>(tmem + lanes + kK + quarter * N, x);
-      tmem_put<N>(tmem + lanes + kV + quarter * N, y);
+      uint32_t x[DP / 4], y[DP / 4];
+      load_row_part<DP, 2>(x, row_of(args.k), half, a.dim);
+      load_row_part<DP, 2>(y, row_of(args.v), half, a.dim);
+      tmem_put<DP / 4>(tmem + lanes + kK + half * (DP / 4), x);
+      tmem_put<DP / 4>(tmem + lanes + kV + half * (DP / 4), y);
       tmem_wait_st();
       tc_fence_before_sync();
       mbar_arrive(bar(C::OWN_READY));
     }
-    const float2 cc = make_float2(c, c), pp = make_float2(damp, damp);
+    constexpr int NQ = kTurn / 32;   // groups of 32 columns of a thread
     bool ok = true;
-    int tile = tile0;   // of its head
-    RingAt<C::NA> qa;
-    RingAt<C::NB> da;
-    for (int it = 0; it < n; ++it) {
-      const int i0 = (t0 + tile) * 128;
-      if (++tile == per) tile = 0;
-      const float4* nl = reinterpret_cast<const float4*>(lse_rows(qa.s) + quarter * 32);
-      const float4* nd = reinterpret_cast<const float4*>(delta_rows(da.s) + quarter * 32);
-      // (the rows' statistics came before the copies that the products waited for)
-      ok = warp_wait_phase(bar(C::S_FULL), it & 1, ctl) &&
-           warp_wait_phase(bar(C::A_FULL + qa.s), qa.parity, ctl);
+    int tile = per > 0 ? (tile0 + half) % per : 0;   // of its head
+    RingAt<C::N> r;
+    if (half) r.next();
+    for (int it = half; it < n; it += 2) {   // the warpgroup's stream
+      const int u = (it >> 1) & 1;
+      const int i0 = (t0 + tile) * kTurn;
+      for (tile += 2; tile >= per;) tile -= per;
+      const float4* nl = reinterpret_cast<const float4*>(lse_rows(r.s));
+      const float4* nd = reinterpret_cast<const float4*>(delta_rows(r.s));
+      ok = warp_wait_phase(bar(C::S_FULL + half), u, ctl);
       if (!ok) break;
-      qa.next();
+      // (the stage was full before S was formed)
+      ok = warp_wait_phase(bar(C::FULL + r.s), r.parity, ctl);
+      if (!ok) break;
+      r.next();
+      r.next();
       tc_fence_after_sync();
-      uint32_t p[32], d[32], w[16];
-      tmem_ld_32x32b_x32(s_col, p);
-      tmem_wait_ld_x32(p);
+      uint32_t p[NQ][32], d[NQ][32], w[NQ * 16];
 #pragma unroll
-      for (int e = 0; e < 32; e += 4) {
-        const float4 r = nl[e / 4];
-        const float2 u = fma2(make_float2(__uint_as_float(p[e]), __uint_as_float(p[e + 1])), cc,
-                              make_float2(r.x, r.y));
-        const float2 v = fma2(make_float2(__uint_as_float(p[e + 2]), __uint_as_float(p[e + 3])), cc,
-                              make_float2(r.z, r.w));
-        p[e] = __float_as_uint(ex2_approx(u.x));
-        p[e + 1] = __float_as_uint(ex2_approx(u.y));
-        p[e + 2] = __float_as_uint(ex2_approx(v.x));
-        p[e + 3] = __float_as_uint(ex2_approx(v.y));
-      }
+      for (int q = 0; q < NQ; ++q) tmem_ld_32x32b_x32(s_col + q * 32, p[q]);
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) tmem_wait_ld_x32(p[q]);
+      const float2 cc = make_float2(c, c), pp = make_float2(damp, damp);
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float4 r = nl[q * 8 + e];
+          uint32_t* x = &p[q][e * 4];
+          const float2 u = fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), cc,
+                                make_float2(r.x, r.y));
+          const float2 v = fma2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), cc,
+                                make_float2(r.z, r.w));
+          x[0] = __float_as_uint(ex2_approx(u.x));
+          x[1] = __float_as_uint(ex2_approx(u.y));
+          x[2] = __float_as_uint(ex2_approx(v.x));
+          x[3] = __float_as_uint(ex2_approx(v.y));
+        }
       // causal: the key meets the queries from key - off on
-      const int first = key - off - i0 - quarter * 32;
+      const int first = key - off - i0;
       const bool cut = a.causal && __any_sync(0xffffffffu, first > 0);
       if (cut) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (e < first) p[e] = 0u;
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (q * 32 + e < first) p[q][e] = 0u;
       }
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        w[e] = pack16<BF16>(__uint_as_float(p[2 * e]), __uint_as_float(p[2 * e + 1]));
-      tmem_put<16>(s_col, w);
+      for (int e = 0; e < NQ * 16; ++e)
+        w[e] = pack16<BF16>(__uint_as_float(p[e >> 4][(2 * e) & 31]),
+                            __uint_as_float(p[e >> 4][(2 * e + 1) & 31]));
+      tmem_put<NQ * 16>(s_col, w);
       tmem_wait_st();
       tc_fence_before_sync();
-      mbar_arrive(bar(C::S_DONE + quarter));
-      ok = warp_wait_phase(bar(C::DP_FULL), it & 1, ctl) &&
-           warp_wait_phase(bar(C::B_FULL + da.s), da.parity, ctl);
+      mbar_arrive(bar(C::S_DONE + half));
+      ok = warp_wait_phase(bar(C::DP_FULL + half), u, ctl);
       if (!ok) break;
-      da.next();
       tc_fence_after_sync();
-      tmem_ld_32x32b_x32(dp_col, d);
-      tmem_wait_ld_x32(d);
 #pragma unroll
-      for (int e = 0; e < 32; e += 4) {
-        const float4 r = nd[e / 4];
-        const float2 u = mul2(make_float2(__uint_as_float(p[e]), __uint_as_float(p[e + 1])),
-                              fma2(make_float2(__uint_as_float(d[e]), __uint_as_float(d[e + 1])), pp,
-                                   make_float2(r.x, r.y)));
-        const float2 v = mul2(make_float2(__uint_as_float(p[e + 2]), __uint_as_float(p[e + 3])),
-                              fma2(make_float2(__uint_as_float(d[e + 2]), __uint_as_float(d[e + 3])),
-                                   pp, make_float2(r.z, r.w)));
-        d[e] = __float_as_uint(u.x);
-        d[e + 1] = __float_as_uint(u.y);
-        d[e + 2] = __float_as_uint(v.x);
-        d[e + 3] = __float_as_uint(v.y);
-      }
+      for (int q = 0; q < NQ; ++q) tmem_ld_32x32b_x32(dp_col + q * 32, d[q]);
+#pragma unroll
+      for (int q = 0; q < NQ; ++q) tmem_wait_ld_x32(d[q]);
+#pragma unroll
+      for (int q = 0; q < NQ; ++q)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float4 r = nd[q * 8 + e];
+          uint32_t* x = &d[q][e * 4];
+          const uint32_t* y = &p[q][e * 4];
+          const float2 u = mul2(make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])),
+                                fma2(make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])), pp,
+                                     make_float2(r.x, r.y)));
+          const float2 v = mul2(make_float2(__uint_as_float(y[2]), __uint_as_float(y[3])),
+                                fma2(make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])), pp,
+                                     make_float2(r.z, r.w)));
+          x[0] = __float_as_uint(u.x);
+          x[1] = __float_as_uint(u.y);
+          x[2] = __float_as_uint(v.x);
+          x[3] = __float_as_uint(v.y);
+        }
       if (cut) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
-          if (e < first) d[e] = 0u;
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (q * 32 + e < first) d[q][e] = 0u;
       }
 #pragma unroll
-      for (int e = 0; e < 16; ++e)
-        w[e] = pack16<BF16>(__uint_as_float(d[2 * e]), __uint_as_float(d[2 * e + 1]));
-      tmem_put<16>(dp_col, w);
+      for (int e = 0; e < NQ * 16; ++e)
+        w[e] = pack16<BF16>(__uint_as_float(d[e >> 4][(2 * e) & 31]),
+                            __uint_as_float(d[e >> 4][(2 * e + 1) & 31]));
+      tmem_put<NQ * 16>(dp_col, w);
       tmem_wait_st();
       tc_fence_before_sync();
-      mbar_arrive(bar(C::DS_READY + quarter));
+      mbar_arrive(bar(C::DS_READY + half));
     }
     if (ok && n > 0) {
       ok = warp_wait_phase(bar(C::OUT_FULL), 0, ctl);
       tc_fence_after_sync();
     }
-    if (ok) {   // two quarters' threads write dV, the others dK: half of the entries each
-      const bool dv = quarter < 2;
-      const float back = dv ? pow2i(-(int)kPShift) : a.scale * pow2i(-ne);
-      const HeadGrad out(dv ? args.dv : args.dk, dv ? args.dv_part : args.dk_part, args.k_parts, part,
-                         a.tokens_k, a.heads_q / a.group, a.dim,
+    if (ok) {   // the first half's threads write dV, the others dK
+      const float back = half == 0 ? pow2i(-(int)kPShift) : a.scale * pow2i(-ne);
+      const HeadGrad out(half == 0 ? args.dv : args.dk, half == 0 ? args.dv_part : args.dk_part,
+                         args.k_parts, part, a.tokens_k, a.heads_q / a.group, a.dim,
                          (int64_t)sk.start + (live ? key : 0), hk);
 #pragma unroll
-      for (int q = 0; q < DP / 64; ++q) {
-        const int c0 = (quarter & 1) * (DP / 2) + q * 32;
+      for (int q = 0; q < DP / 32; ++q) {
         uint32_t o[32];
-        if (n > 0) tmem_get<32>(tmem + lanes + C::OUT_COL + (dv ? 0 : DP) + c0, o);
-        out.put<BF16, 32>(o, n > 0, back, c0, live ? a.dim : 0);
+        if (n > 0) {
+          tmem_ld_32x32b_x32(tmem + lanes + C::OUT_COL + half * DP + q * 32, o);
+          tmem_wait_ld_x32(o);
+        }
+        out.put<BF16>(o, n > 0, back, q * 32, live ? a.dim : 0);
       }
     }
   }
   __syncwarp();
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == kBwdMmaWarp) {
+  if (warp == kAttnMmaWarp) {
     tc_fence_after_sync();
     tmem_dealloc(tmem, 512);
   }
@@ -874,7 +854,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 template <bool BF16>
 __global__ void __launch_bounds__(256)
     lin_attn_sum_parts_kernel(const int32_t* cu, int tokens, int most, int dim, int parts,
-                              const float* __restrict__ part, const __grid_constant__ HeadsPtr out) {
+                              const float* __restrict__ part, const HeadsPtr out) {
   const int h = blockIdx.x, heads = gridDim.x;
   const SeqRange r = seq_range(cu, blockIdx.z, tokens, most);
   const int groups = dim / 8;
@@ -900,11 +880,11 @@ __global__ void __launch_bounds__(256)
 }
 
 // Parts of a launch of `ctas` CTAs whose longest runs over `rows` rows: as
-// many as give every SM a CTA, while each keeps at least four tiles (below
+// many as give every SM a CTA, while each keeps at least eight tiles (below
 // that the third kernel costs more than the shorter loop saves).
 int attn_parts(int64_t ctas, int64_t rows, int sms) {
   const int64_t parts = ctas > 0 ? (int64_t)sms / ctas : 1;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(parts, rows / (4 * 128)));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(parts, rows / (8 * kTurn)));
 }
 
 cudaError_t launch_attn_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArgs& args,
@@ -914,19 +894,28 @@ cudaError_t launch_attn_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArg
   const unsigned hq = (unsigned)(heads_kv * args.s.group), hk = (unsigned)heads_kv;
   const unsigned seqs = (unsigned)sequences;
   *kernels = 0;
-  auto go = [&](auto kernel, uint32_t smem, dim3 grid, int threads) {
+  auto go = [&](auto kernel, uint32_t smem, dim3 grid, int threads, bool dependent) {
     if (grid.x == 0 || grid.y == 0 || grid.z == 0) return cudaSuccess;
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
-    kernel<<<grid, threads, smem, stream>>>(maps, args);
     ++*kernels;
-    return cudaGetLastError();
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = dependent ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, maps, args);
   };
   auto both = [&](auto dq, uint32_t dq_smem, auto dkv, uint32_t dkv_smem) {
-    const cudaError_t e = go(dq, dq_smem, dim3(hq, tq, seqs * args.q_parts), kBwdThreads);
+    const cudaError_t e = go(dq, dq_smem, dim3(hq, tq, seqs * args.q_parts), kAttnThreads, false);
     if (e != cudaSuccess) return e;
-    return go(dkv, dkv_smem, dim3(hk, tk, seqs * args.k_parts), kBwdThreads);
+    return go(dkv, dkv_smem, dim3(hk, tk, seqs * args.k_parts), kDkvThreads, tq > 0);
   };
   auto sum = [&](const int32_t* cu, int tokens, int most, int parts, const float* part,
                  const HeadsPtr& out, unsigned heads) {
