@@ -67,7 +67,6 @@ def _run(t, lens, causal, scale=None, packed=True):
         how.update(cu_q=_cu([a for a, _ in lens]), cu_k=_cu([b for _, b in lens]),
                    max_q=max(a for a, _ in lens), max_k=max(b for _, b in lens))
     lin.lin_attention(t["q"], t["k"], t["v"], t["o"], t["lse"], **how)
-    assert lin.lin_last_launch_info() == (1, 0)
     lin.lin_attention_backward(t["q"], t["k"], t["v"], t["o"], t["lse"], t["do"], t["dq"],
                                t["dk"], t["dv"], **how)
     torch.cuda.synchronize()
@@ -339,3 +338,50 @@ def test_refusals():
     assert e.value.status == lin.LIN_ERROR_ALIASING
     torch.cuda.synchronize()
     assert torch.equal(t["o"].isnan(), before.isnan())
+
+
+# (lengths, query heads, key heads, dim): few CTAs and a long other side, so
+# that it is cut into parts (keys for O and dQ, queries for dK and dV), with
+# sequences of other lengths beside the long one, shared heads (whose queries
+# count as one long side), and rows that a causal mask leaves to the first
+# part alone, or nothing
+PARTS = [([(70, 2000)], 1, 1, 64), ([(1700, 90)], 2, 1, 128), ([(1600, 1600), (3, 1), (40, 200)], 1, 1, 64),
+         ([(600, 600)], 4, 1, 40), ([(1900, 1550)], 1, 1, 96)]
+
+
+@pytest.mark.parametrize("shape", PARTS, ids=lambda s: f"{s[0]}x{s[1]}h{s[2]}d{s[3]}")
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_long_and_few(shape, causal, dtype):
+    lens, hq, hk, d = shape
+    t = _setup(dtype, lens, hq, hk, d, seed=21)
+    _run(t, lens, causal)
+    kernels, workspace = lin.lin_last_launch_info()
+    assert kernels >= 2 and workspace > 0
+    _check(t, lens, causal, d ** -0.5, UNIT[dtype])
+    first = {n: t[n].clone() for n in ("o", "lse", "dq", "dk", "dv")}
+    _run(t, lens, causal)   # the parts are added in order: the same bits
+    import torch
+    for n, x in first.items():
+        assert torch.equal(t[n].nan_to_num(7.0), x.nan_to_num(7.0)), n
+
+
+def test_one_launch_each_where_there_is_no_need_for_parts():
+    import torch
+    t = _setup("float16", [(300, 300)], 2, 2, 64, seed=22)
+    lin.lin_attention(t["q"], t["k"], t["v"], t["o"], t["lse"])
+    assert lin.lin_last_launch_info() == (1, 0)
+    lin.lin_attention_backward(t["q"], t["k"], t["v"], t["o"], t["lse"], t["do"], t["dq"], t["dk"],
+                               t["dv"])
+    kernels, workspace = lin.lin_last_launch_info()
+    # delta of each row and head, and the norm of each query tile
+    assert kernels == 2 and workspace == (300 * 2 + 3 * 2) * 4
+    torch.cuda.synchronize()
+
+
+def test_many_heads_and_sequences():
+    # more CTAs than the SMs hold at once, most of them of short sequences
+    lens = [(1 + 7 * i % 150, 1 + 11 * i % 130) for i in range(60)]
+    t = _setup("bfloat16", lens, 6, 3, 64, seed=23)
+    _run(t, lens, True)
+    _check(t, lens, True, 0.125, UNIT["bfloat16"])

@@ -50,6 +50,21 @@ __device__ __forceinline__ SeqRange seq_range(const int32_t* cu, int b, int toke
   return SeqRange{s, min(e - s, most)};
 }
 
+// The sequence and the part of a CTA whose grid has `parts` of them to each
+// sequence, and the part's share of n turns.
+struct PartOf {
+  int b, part, parts;
+  __device__ __forceinline__ int begin(int n) const {
+    return parts == 1 ? 0 : (int)((int64_t)n * part / parts);
+  }
+  __device__ __forceinline__ int end(int n) const {
+    return parts == 1 ? n : (int)((int64_t)n * (part + 1) / parts);
+  }
+};
+__device__ __forceinline__ PartOf part_of(int z, int parts) {
+  return parts == 1 ? PartOf{z, 0, 1} : PartOf{z / parts, z % parts, parts};
+}
+
 // Sub-tiles, bytes and descriptors of a [ROWS tokens][DP entries] operand
 // tile. A descriptor's address field counts 16-byte units from bit 0, so the
 // steps of a product add constants to the tile's descriptor.

@@ -28,6 +28,10 @@ struct AttnFwdArgs {
   AttnArgs s;
   HeadsPtr o;
   float* lse;   // [heads_q][tokens_q]
+  // parts of the keys, and, where there are several, their results in f32:
+  // [part][token][head][dim], [part][head][token]
+  int32_t parts;
+  float *o_part, *lse_part;
 };
 
 struct AttnBwdArgs {
@@ -51,10 +55,12 @@ struct AttnBwdMaps {
   CUtensorMap q, k, v, dout;
 };
 
+// Parts that the other side of a launch of `ctas` CTAs is cut into (`rows`: of
+// the other side that the longest runs over).
+int attn_parts(int64_t ctas, int64_t rows, int sms);
+// One kernel; with several parts another one that joins them.
 cudaError_t launch_attn_fwd(bool bf16, const AttnFwdMaps& maps, const AttnFwdArgs& args,
                             int heads_kv, int sequences, cudaStream_t stream);
-// Parts that the backward kernels' other side is cut into (see there).
-int attn_parts(int64_t ctas, int64_t rows, int sms);
 // Tokens of a box of the backward kernels' maps.
 constexpr int kAttnBwdBox = 64;
 // The dQ kernel (which also leaves delta and norm), the dK, dV kernel, and the

@@ -118,11 +118,24 @@ lin_status attention(const lin_attention_shape* s, const lin_heads* Q, const lin
   ok &= encode_view(&maps.k, v[1].extent ? v[1] : v[0], s->dim, 128);
   ok &= encode_view(&maps.v, v[2].extent ? v[2] : v[0], s->dim, 128);
   if (!ok) return cuda_fail(cudaErrorInvalidValue);
-  lin::AttnFwdArgs a{attn_args(s, c), heads_ptr(v[3]), LSE};
-  const cudaError_t e = lin::launch_attn_fwd(s->dtype == LIN_BFLOAT16, maps, a, (int)s->heads_kv,
-                                             (int)s->sequences, stream);
+  lin::AttnFwdArgs a{attn_args(s, c), heads_ptr(v[3]), LSE, 1, nullptr, nullptr};
+  a.parts = lin::attn_parts((c.max_q + 255) / 256 * s->heads_q * s->sequences, c.max_k,
+                            sm_count(c.dev));
+  const uint64_t rows = (uint64_t)a.parts * (uint64_t)s->tokens_q * (uint64_t)s->heads_q;
+  const size_t bytes = a.parts > 1 ? (size_t)(rows * (uint64_t)(s->dim + 1) * 4) : 0;
+  if (bytes) {
+    a.o_part = static_cast<float*>(take_stream_workspace(c.dev, bytes, stream));
+    if (!a.o_part) return LIN_ERROR_CUDA;
+    a.lse_part = a.o_part + rows * (uint64_t)s->dim;
+  }
+  cudaError_t e = lin::launch_attn_fwd(s->dtype == LIN_BFLOAT16, maps, a, (int)s->heads_kv,
+                                       (int)s->sequences, stream);
+  if (bytes) {
+    const cudaError_t ef = cudaFreeAsync(a.o_part, stream);
+    if (e == cudaSuccess) e = ef;
+  }
   if (e != cudaSuccess) return cuda_fail(e);
-  set_last_launch_info(1, 0);
+  set_last_launch_info(a.parts > 1 ? 2 : 1, bytes);
   return LIN_SUCCESS;
 }
 

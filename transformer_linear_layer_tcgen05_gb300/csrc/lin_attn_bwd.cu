@@ -172,7 +172,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   using C = DqCfg<DP>;
   extern __shared__ uint8_t smem_raw[];
   const AttnArgs& a = args.s;
-  const int h = blockIdx.x, b = blockIdx.z / args.q_parts, part = blockIdx.z % args.q_parts;
+  const int h = blockIdx.x;
+  const PartOf at = part_of(blockIdx.z, args.q_parts);
+  const int b = at.b, part = at.part;
   const int qt = gridDim.y - 1 - blockIdx.y;   // longest rows of a causal mask first
   const int i0 = qt * 128;
   const SeqRange sq = seq_range(a.cu_q, b, a.tokens_q, a.max_q);
@@ -187,9 +189,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const int tiles = hi > 0 ? (hi + kTurn - 1) / kTurn : 0;
   // this part's key tiles: j0 .. j0 + n - 1 (one or two stay together: see delta)
   const bool few = tiles <= 2;
-  const int j0 = few ? 0 : (int)((int64_t)tiles * part / args.q_parts);
-  const int n = few ? (part == 0 ? tiles : 0)
-                    : (int)((int64_t)tiles * (part + 1) / args.q_parts) - j0;
+  const int j0 = few ? 0 : at.begin(tiles);
+  const int n = few ? (part == 0 ? tiles : 0) : at.end(tiles) - j0;
   const int hk = h / a.group;
 
   if (!smem_aligned(smem_raw, a.status)) return;
@@ -206,10 +207,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     tmem_alloc(base + C::OFF_CTL + C::OFF_TMEM, 512);
     tmem_relinquish_alloc_permit();
   }
-  if (tid == 0) {
-    *abort = 0;
-    for (int i = 0; i < C::BARS; ++i)
-      mbar_init(bar(i), C::arrivals(i));
+  if (tid == 0) *abort = 0;
+  if (tid < C::BARS) {
+    mbar_init(bar(tid), C::arrivals(tid));
     fence_barrier_init();
   }
   tc_fence_before_sync();
@@ -306,22 +306,23 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     // way: each of the row's two threads has half of the entries.
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     float dsum = 0.0f, nsum = 0.0f;
+    const float lse = live ? args.lse[(int64_t)h * a.tokens_q + token] : -INFINITY;
     {
       auto row_of = [&](const HeadsPtr& t) {
         return live ? t.p + token * t.token_stride + (int64_t)h * t.head_stride : nullptr;
       };
-      uint32_t x[DP / 4], y[DP / 4];
+      uint32_t x[DP / 4], y[DP / 4], z[DP / 4];
       load_row_part<DP, 2>(x, row_of(args.q), half, a.dim);
       load_row_part<DP, 2>(y, row_of(args.dout), half, a.dim);
+      load_row_part<DP, 2>(z, row_of(args.o), half, a.dim);
       tmem_put<DP / 4>(tmem + lanes + kQ + half * (DP / 4), x);
       tmem_put<DP / 4>(tmem + lanes + kDo + half * (DP / 4), y);
-      load_row_part<DP, 2>(x, row_of(args.o), half, a.dim);
       tmem_wait_st();
       tc_fence_before_sync();
       mbar_arrive(bar(C::OWN_READY));
 #pragma unroll
       for (int e = 0; e < DP / 4; ++e) {
-        const float2 u = unpack16<BF16>(x[e]), v = unpack16<BF16>(y[e]);
+        const float2 u = unpack16<BF16>(z[e]), v = unpack16<BF16>(y[e]);
         dsum = fmaf(u.x, v.x, fmaf(u.y, v.y, dsum));
         nsum = fmaf(v.x, v.x, fmaf(v.y, v.y, nsum));
       }
@@ -346,7 +347,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int ne = norm_exponent(norm);
     const float amp = pow2i(ne);
     float nd = -delta * amp;
-    const float lse = live ? args.lse[(int64_t)h * a.tokens_q + token] : -INFINITY;
     // a row without a key (L = -inf) has no probabilities
     const float nl = lse == -INFINITY ? -INFINITY : -lse * kLog2E;
     // the last key that this row sees
@@ -478,7 +478,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   using C = DkvCfg<DP>;
   extern __shared__ uint8_t smem_raw[];
   const AttnArgs& a = args.s;
-  const int hk = blockIdx.x, b = blockIdx.z / args.k_parts, part = blockIdx.z % args.k_parts;
+  const int hk = blockIdx.x;
+  const PartOf at = part_of(blockIdx.z, args.k_parts);
+  const int b = at.b, part = at.part;
   const int k0 = blockIdx.y * 128;   // a causal mask's first keys meet the most queries
   const SeqRange sk = seq_range(a.cu_k, b, a.tokens_k, a.max_k);
   if (k0 >= sk.len) return;   // (the whole CTA)
@@ -489,9 +491,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   const int t0 = a.causal ? min(max(k0 - off, 0) / kTurn, t1) : 0;
   const int per = t1 - t0;
   // this part's turns (of all heads' tiles): from .. from + n - 1
-  const int from = (int)((int64_t)per * a.group * part / args.k_parts);
-  const int n = (int)((int64_t)per * a.group * (part + 1) / args.k_parts) - from;
-  const int tile0 = per > 0 ? from % per : 0;         // the first turn's tile of its head
+  const int from = at.begin(per * a.group), n = at.end(per * a.group) - from;
+  const int tile0 = from > 0 ? from % per : 0;        // the first turn's tile of its head
   const int q_left = sq.len - (t1 - 1) * kTurn;          // queries of the last tile
   const int h0 = hk * a.group;
 
@@ -511,24 +512,11 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     tmem_alloc(base + C::OFF_CTL + C::OFF_TMEM, 512);
     tmem_relinquish_alloc_permit();
   }
-  if (tid == 0) {
-    *abort = 0;
-    for (int i = 0; i < C::BARS; ++i)
-      mbar_init(bar(i), C::streamed_full(i) ? 2 : C::arrivals(i));   // (copy and statistics)
+  if (tid == 0) *abort = 0;
+  if (tid < C::BARS) {
+    // (a stage has the copy's arrival and the statistics')
+    mbar_init(bar(tid), C::streamed_full(tid) ? 2 : C::arrivals(tid));
     fence_barrier_init();
-  }
-  pdl_wait();   // delta and norm come from the dQ kernel
-  // the largest row norm of dO that this tile meets (every tile of the
-  // heads: the masked ones do no harm)
-  float* red = reinterpret_cast<float*>(ctl_gen + C::OFF_RED);
-  {
-    const int tiles = (a.max_q + 127) / 128;
-    const float* nm = args.norm + ((int64_t)b * a.heads_q + h0) * tiles;
-    float big = 0.0f;
-    for (int i = tid; i < tiles * a.group; i += kDkvThreads) big = fmaxf(big, nm[i]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
-    if (lane == 0) red[warp] = big;
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -537,12 +525,22 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   constexpr uint32_t tmem = 0;
   constexpr uint32_t kK = C::OWN_COL, kV = kK + DP / 2;   // K and V (heads of up to 64)
   const uint32_t k_own = base + C::OFF_OWN, v_own = k_own + AttnTile<DP>::BYTES;   // (of 128)
-  float big = 0.0f;
+  // The exponent of dS's scale, from the largest row norm of dO that this tile
+  // meets (every tile of the heads: the masked ones do no harm). By each warp
+  // that wants it, once the dQ kernel, which leaves the norms and delta, is
+  // done; the copies and the first products do not wait for that.
+  auto scale_exponent = [&]() -> int {
+    pdl_wait();
+    const int tiles = (a.max_q + 127) / 128;
+    const float* nm = args.norm + ((int64_t)b * a.heads_q + h0) * tiles;
+    float big = 0.0f;
+    for (int i = lane; i < tiles * a.group; i += 32) big = fmaxf(big, nm[i]);
 #pragma unroll
-  for (int w = 0; w < kDkvThreads / 32; ++w) big = fmaxf(big, red[w]);
-  const int ne = norm_exponent(big);
+    for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
+    return norm_exponent(big);
+  };
   // scale of dP and delta: dS then carries 2^ne, P's 2^8 taken back
-  const float damp = pow2i(ne) * pow2i(-(int)kPShift);
+  auto ds_scale = [&](int ne) { return pow2i(ne) * pow2i(-(int)kPShift); };
 
   if (warp == kAttnCopyWarp) {
     if (n > 0) {
@@ -588,6 +586,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     // took longer for a turn than the products (3000 cycles; 757 us at 8192
     // tokens).
     constexpr int N = kTurn / 32;
+    const float damp = ds_scale(scale_exponent());
     RingAt<C::N> r;
     int h = n > 0 ? h0 + from / per : 0, tile = tile0;
     float lse[N], delta[N];
@@ -719,6 +718,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       tc_fence_before_sync();
       mbar_arrive(bar(C::OWN_READY));
     }
+    const int ne = scale_exponent();
+    const float damp = ds_scale(ne);
     constexpr int NQ = kTurn / 32;   // groups of 32 columns of a thread
     bool ok = true;
     int tile = per > 0 ? (tile0 + half) % per : 0;   // of its head
@@ -849,27 +850,35 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
 
 // ---------------------------------------------------------------- parts
 
-// A gradient from its parts' f32 sums [part][token][head][dim], added in
-// order: a CTA per 32 rows of a sequence and head, eight entries to a thread.
+// Gradients from their parts' f32 sums [part][token][head][dim], added in
+// order: one, or (dK and dV) two of the same shape in one launch. A CTA per 32
+// rows of a sequence and head, eight entries to a thread.
+struct SumParts {
+  const int32_t* cu;
+  int32_t tokens, most, dim, parts, sequences;
+  const float* part[2];
+  HeadsPtr out[2];
+};
 template <bool BF16>
 __global__ void __launch_bounds__(256)
-    lin_attn_sum_parts_kernel(const int32_t* cu, int tokens, int most, int dim, int parts,
-                              const float* __restrict__ part, const HeadsPtr out) {
+    lin_attn_sum_parts_kernel(const __grid_constant__ SumParts a) {
   const int h = blockIdx.x, heads = gridDim.x;
-  const SeqRange r = seq_range(cu, blockIdx.z, tokens, most);
-  const int groups = dim / 8;
+  const int which = blockIdx.z >= a.sequences;
+  const SeqRange r = seq_range(a.cu, blockIdx.z - which * a.sequences, a.tokens, a.most);
+  const HeadsPtr& out = a.out[which];
+  const int groups = a.dim / 8;
   pdl_wait();
   for (int k = threadIdx.x; k < 32 * groups; k += 256) {
     const int i = blockIdx.y * 32 + k / groups, col = k % groups * 8;
     if (i >= r.len) continue;
     const int64_t token = (int64_t)r.start + i;
-    const float* p = part + (token * heads + h) * dim + col;
+    const float* p = a.part[which] + (token * heads + h) * a.dim + col;
+    const int64_t step = (int64_t)a.tokens * heads * a.dim;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
 #pragma unroll 4
-    for (int q = 0; q < parts; ++q) {
+    for (int q = 0; q < a.parts; ++q, p += step) {
       const float4 u = __ldcs(reinterpret_cast<const float4*>(p));
-      const float4 v = __ldcs(reinterpret_cast<const float4*>(p + 4));
-      p += (int64_t)tokens * heads * dim;
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(p) + 1);
       x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
       y = make_float4(y.x + v.x, y.y + v.y, y.z + v.z, y.w + v.w);
     }
@@ -880,11 +889,13 @@ __global__ void __launch_bounds__(256)
 }
 
 // Parts of a launch of `ctas` CTAs whose longest runs over `rows` rows: as
-// many as give every SM a CTA, while each keeps at least eight tiles (below
-// that the third kernel costs more than the shorter loop saves).
+// many as give every SM a CTA, while each keeps at least 512 rows, and none
+// below 1536 rows, where the kernel that joins them costs more than the
+// shorter loop saves (forward, one head, us: 1024 keys 16.8 whole, 18.7 in two
+// parts; 2000 keys 28.5 and 20.3).
 int attn_parts(int64_t ctas, int64_t rows, int sms) {
-  const int64_t parts = ctas > 0 ? (int64_t)sms / ctas : 1;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(parts, rows / (8 * kTurn)));
+  if (rows < 1536 || ctas < 1) return 1;
+  return (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)sms / ctas, rows / 512));
 }
 
 cudaError_t launch_attn_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArgs& args,
@@ -917,9 +928,8 @@ cudaError_t launch_attn_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArg
     if (e != cudaSuccess) return e;
     return go(dkv, dkv_smem, dim3(hk, tk, seqs * args.k_parts), kDkvThreads, tq > 0);
   };
-  auto sum = [&](const int32_t* cu, int tokens, int most, int parts, const float* part,
-                 const HeadsPtr& out, unsigned heads) {
-    const dim3 grid(heads, (unsigned)((most + 31) / 32), seqs);
+  auto sum = [&](const SumParts& p, unsigned heads, unsigned count) {
+    const dim3 grid(heads, (unsigned)((p.most + 31) / 32), seqs * count);
     if (grid.y == 0) return cudaSuccess;
     ++*kernels;
     cudaLaunchAttribute attr[1];
@@ -931,10 +941,8 @@ cudaError_t launch_attn_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArg
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return bf16 ? cudaLaunchKernelEx(&cfg, lin_attn_sum_parts_kernel<true>, cu, tokens, most,
-                                     (int)args.s.dim, parts, part, out)
-                : cudaLaunchKernelEx(&cfg, lin_attn_sum_parts_kernel<false>, cu, tokens, most,
-                                     (int)args.s.dim, parts, part, out);
+    return bf16 ? cudaLaunchKernelEx(&cfg, lin_attn_sum_parts_kernel<true>, p)
+                : cudaLaunchKernelEx(&cfg, lin_attn_sum_parts_kernel<false>, p);
   };
   auto dims = [&](auto type) {
     constexpr bool B = decltype(type)::value;
@@ -946,11 +954,13 @@ cudaError_t launch_attn_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArg
   };
   cudaError_t e = bf16 ? dims(std::true_type{}) : dims(std::false_type{});
   if (e == cudaSuccess && args.q_parts > 1)
-    e = sum(args.s.cu_q, args.s.tokens_q, args.s.max_q, args.q_parts, args.dq_part, args.dq, hq);
+    e = sum(SumParts{args.s.cu_q, args.s.tokens_q, args.s.max_q, args.s.dim, args.q_parts, sequences,
+                     {args.dq_part, nullptr}, {args.dq, args.dq}},
+            hq, 1);
   if (e == cudaSuccess && args.k_parts > 1)
-    e = sum(args.s.cu_k, args.s.tokens_k, args.s.max_k, args.k_parts, args.dk_part, args.dk, hk);
-  if (e == cudaSuccess && args.k_parts > 1)
-    e = sum(args.s.cu_k, args.s.tokens_k, args.s.max_k, args.k_parts, args.dv_part, args.dv, hk);
+    e = sum(SumParts{args.s.cu_k, args.s.tokens_k, args.s.max_k, args.s.dim, args.k_parts, sequences,
+                     {args.dk_part, args.dv_part}, {args.dk, args.dv}},
+            hk, 2);
   return e;
 }
 

@@ -16,7 +16,9 @@
 // 256 queries. The products of one thread execute in issue order, so S of
 // the next tile is issued right behind the P V that reads P out of the same
 // columns. Heads vary fastest over the grid and the causal mask's longest
-// query tiles come first.
+// query tiles come first. Where there are fewer CTAs than SMs the keys are cut
+// into parts, a CTA each, whose results a second kernel joins by their
+// log-sum-exps.
 #include "lin_attn.cuh"
 
 namespace lin {
@@ -76,13 +78,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   using C = FwdCfg<DP>;
   extern __shared__ uint8_t smem_raw[];
   const AttnArgs& a = args.s;
-  const int h = blockIdx.x, b = blockIdx.z;
+  const int h = blockIdx.x;
+  const PartOf at = part_of(blockIdx.z, args.parts);
+  const int b = at.b;
   const int i0 = (gridDim.y - 1 - blockIdx.y) * 256;   // longest rows of a causal mask first
   const SeqRange sq = seq_range(a.cu_q, b, a.tokens_q, a.max_q);
   if (i0 >= sq.len) return;   // (the whole CTA)
   const SeqRange sk = seq_range(a.cu_k, b, a.tokens_k, a.max_k);
-  const int n0 = fwd_key_tiles(i0, sq.len, sk.len, a.causal);
-  const int n1 = fwd_key_tiles(i0 + 128, sq.len, sk.len, a.causal);
+  // key tiles of the two query tiles, and of them those of this part, from j0 on
+  const int all0 = fwd_key_tiles(i0, sq.len, sk.len, a.causal);
+  const int all1 = fwd_key_tiles(i0 + 128, sq.len, sk.len, a.causal);
+  const int all = max(all0, all1);
+  const int j0 = at.begin(all), j1 = at.end(all);
+  const int n0 = max(min(all0, j1) - j0, 0), n1 = max(min(all1, j1) - j0, 0);
   const int n = max(n0, n1);
   const int hk = h / a.group;
 
@@ -97,10 +105,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     tmem_alloc(base + C::OFF_TMEM, 512);
     tmem_relinquish_alloc_permit();
   }
-  if (tid == 0) {
-    *abort = 0;
-    for (int i = 0; i < C::BARS; ++i)
-      mbar_init(bar(i), i >= C::P_READY && i < C::P_READY + 4 ? 128 : 1);
+  if (tid == 0) *abort = 0;
+  if (tid < C::BARS) {
+    mbar_init(bar(tid), tid >= C::P_READY && tid < C::P_READY + 4 ? 128 : 1);
     fence_barrier_init();
   }
   tc_fence_before_sync();
@@ -109,7 +116,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   // (an allocation of all 512 columns begins at column 0)
   constexpr uint32_t tmem = 0;
 
-  const int v_left = sk.len - (n - 1) * 128;   // keys of the last tile (128 or more: all)
+  const int v_left = sk.len - (j0 + n - 1) * 128;   // keys of the last tile (128 or more: all)
   if (warp >= 8) {
     setmaxnreg_dec<kFwdRegsIssue>();
     if (warp == kAttnCopyWarp) {
@@ -125,7 +132,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           const int s = j % C::NKV, round = j / C::NKV;
           if (round > 0 && !wait_phase(bar(C::K_EMPTY + s), (round - 1) & 1, ctl)) break;
           mbar_arrive_expect_tx(bar(C::K_FULL + s), C::TILE);
-          load_tile<DP, 128>(base + C::OFF_K + s * C::TILE, &maps.k, hk, sk.start + j * 128,
+          load_tile<DP, 128>(base + C::OFF_K + s * C::TILE, &maps.k, hk, sk.start + (j0 + j) * 128,
                         bar(C::K_FULL + s));
           ++k_issued;
           if (j == 0 && n1 > 0) {
@@ -135,7 +142,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           }
           if (round > 0 && !wait_phase(bar(C::V_EMPTY + s), (round - 1) & 1, ctl)) break;
           mbar_arrive_expect_tx(bar(C::V_FULL + s), C::TILE);
-          load_tile<DP, 128>(base + C::OFF_V + s * C::TILE, &maps.v, hk, sk.start + j * 128,
+          load_tile<DP, 128>(base + C::OFF_V + s * C::TILE, &maps.v, hk, sk.start + (j0 + j) * 128,
                         bar(C::V_FULL + s));
           ++v_issued;
         }
@@ -241,7 +248,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(s_col + q * 32, s[q]);
 #pragma unroll
       for (int q = 0; q < 4; ++q) tmem_wait_ld_x32(s[q]);
-      const int lim_j = lim - j * 128;
+      const int lim_j = lim - (j0 + j) * 128;
       if (__any_sync(0xffffffffu, lim_j < 127)) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -311,6 +318,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // (NaN stays NaN)
       const int64_t token = sq.start + i;
       uint16_t* out = args.o.p + token * args.o.token_stride + (int64_t)h * args.o.head_stride;
+      // [part][token][head][dim] and [part][head][token]
+      float* part_row = args.o_part + (((int64_t)at.part * a.tokens_q + token) * a.heads_q + h) * a.dim;
+      float* lse = args.parts > 1 ? args.lse_part + (int64_t)at.part * a.heads_q * a.tokens_q : args.lse;
 #pragma unroll
       for (int q = 0; q < DP / 32; ++q) {
         uint32_t o[32];
@@ -327,11 +337,26 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const float x = __uint_as_float(o[g * 8 + 2 * e]), y = __uint_as_float(o[g * 8 + 2 * e + 1]);
             w[e] = nk > 0 ? pack16<BF16>(l == 0.0f ? 0.0f : x * inv, l == 0.0f ? 0.0f : y * inv) : 0u;
           }
-          if (live && col < a.dim) store16(out + col, w[0], w[1], w[2], w[3]);
+          if (!live || col >= a.dim) continue;
+          if (args.parts > 1) {   // in f32
+            const float z = nk > 0 ? inv : 0.0f;
+            float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+            if (l != 0.0f && nk > 0) {
+              u = make_float4(__uint_as_float(o[g * 8]) * z, __uint_as_float(o[g * 8 + 1]) * z,
+                              __uint_as_float(o[g * 8 + 2]) * z, __uint_as_float(o[g * 8 + 3]) * z);
+              v = make_float4(__uint_as_float(o[g * 8 + 4]) * z, __uint_as_float(o[g * 8 + 5]) * z,
+                              __uint_as_float(o[g * 8 + 6]) * z, __uint_as_float(o[g * 8 + 7]) * z);
+            }
+            float4* to = reinterpret_cast<float4*>(part_row + col);
+            to[0] = u;
+            to[1] = v;
+          } else {
+            store16(out + col, w[0], w[1], w[2], w[3]);
+          }
         }
       }
       if (live)
-        args.lse[(int64_t)h * a.tokens_q + token] =
+        lse[(int64_t)h * a.tokens_q + token] =
             l == 0.0f ? -INFINITY : m * a.scale + logf(l);
     }
   }
@@ -344,10 +369,51 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
 }
 
+// O and the log-sum-exps from the parts': weights 2^(L_p - L) of their rows,
+// added in order. A CTA per 32 rows of a sequence and head, eight entries to
+// a thread.
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+    lin_attn_join_parts_kernel(const __grid_constant__ AttnFwdArgs args) {
+  const AttnArgs& a = args.s;
+  const int h = blockIdx.x;
+  const SeqRange r = seq_range(a.cu_q, blockIdx.z, a.tokens_q, a.max_q);
+  const int groups = a.dim / 8;
+  pdl_wait();
+  for (int k = threadIdx.x; k < 32 * groups; k += 256) {
+    const int i = blockIdx.y * 32 + k / groups, col = k % groups * 8;
+    if (i >= r.len) continue;
+    const int64_t token = (int64_t)r.start + i;
+    const float* ls = args.lse_part + (int64_t)h * a.tokens_q + token;
+    const int64_t ls_step = (int64_t)a.heads_q * a.tokens_q;
+    float top = -INFINITY;
+    for (int q = 0; q < args.parts; ++q) top = fmaxf(top, ls[q * ls_step]);
+    const float shift = top == -INFINITY ? 0.0f : top;   // (a row without a key)
+    const float* p = args.o_part + (token * a.heads_q + h) * a.dim + col;
+    const int64_t step = (int64_t)a.tokens_q * a.heads_q * a.dim;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
+    float total = 0.0f;
+    for (int q = 0; q < args.parts; ++q) {
+      const float w = ex2_approx((ls[q * ls_step] - shift) * kLog2E);
+      const float4 u = __ldcs(reinterpret_cast<const float4*>(p + q * step));
+      const float4 v = __ldcs(reinterpret_cast<const float4*>(p + q * step) + 1);
+      total += w;
+      x = make_float4(fmaf(w, u.x, x.x), fmaf(w, u.y, x.y), fmaf(w, u.z, x.z), fmaf(w, u.w, x.w));
+      y = make_float4(fmaf(w, v.x, y.x), fmaf(w, v.y, y.y), fmaf(w, v.z, y.z), fmaf(w, v.w, y.w));
+    }
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    store16(args.o.p + token * args.o.token_stride + (int64_t)h * args.o.head_stride + col,
+            pack16<BF16>(x.x * inv, x.y * inv), pack16<BF16>(x.z * inv, x.w * inv),
+            pack16<BF16>(y.x * inv, y.y * inv), pack16<BF16>(y.z * inv, y.w * inv));
+    if (col == 0) args.lse[(int64_t)h * a.tokens_q + token] = top + logf(total);
+  }
+}
+
 cudaError_t launch_attn_fwd(bool bf16, const AttnFwdMaps& maps, const AttnFwdArgs& args,
                             int heads_kv, int sequences, cudaStream_t stream) {
-  const dim3 grid((unsigned)(heads_kv * args.s.group), (unsigned)((args.s.max_q + 255) / 256),
-                  (unsigned)sequences);
+  const unsigned heads = (unsigned)(heads_kv * args.s.group);
+  const dim3 grid(heads, (unsigned)((args.s.max_q + 255) / 256),
+                  (unsigned)sequences * (unsigned)args.parts);
   auto go = [&](auto kernel, uint32_t smem) {
     const cudaError_t e =
         cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
@@ -355,11 +421,25 @@ cudaError_t launch_attn_fwd(bool bf16, const AttnFwdMaps& maps, const AttnFwdArg
     kernel<<<grid, kFwdThreads, smem, stream>>>(maps, args);
     return cudaGetLastError();
   };
+  cudaError_t e;
   if (args.s.dim <= 64)
-    return bf16 ? go(lin_attn_fwd_kernel<64, true>, FwdCfg<64>::SMEM)
-                : go(lin_attn_fwd_kernel<64, false>, FwdCfg<64>::SMEM);
-  return bf16 ? go(lin_attn_fwd_kernel<128, true>, FwdCfg<128>::SMEM)
-              : go(lin_attn_fwd_kernel<128, false>, FwdCfg<128>::SMEM);
+    e = bf16 ? go(lin_attn_fwd_kernel<64, true>, FwdCfg<64>::SMEM)
+             : go(lin_attn_fwd_kernel<64, false>, FwdCfg<64>::SMEM);
+  else
+    e = bf16 ? go(lin_attn_fwd_kernel<128, true>, FwdCfg<128>::SMEM)
+             : go(lin_attn_fwd_kernel<128, false>, FwdCfg<128>::SMEM);
+  if (e != cudaSuccess || args.parts == 1) return e;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(heads, (unsigned)((args.s.max_q + 31) / 32), (unsigned)sequences);
+  cfg.blockDim = dim3(256, 1, 1);
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return bf16 ? cudaLaunchKernelEx(&cfg, lin_attn_join_parts_kernel<true>, args)
+              : cudaLaunchKernelEx(&cfg, lin_attn_join_parts_kernel<false>, args);
 }
 
 }  // namespace lin
