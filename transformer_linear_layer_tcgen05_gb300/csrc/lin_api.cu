@@ -161,8 +161,12 @@ lin_status current_device(int* dev_out, int** status_word) {
 }
 
 // The buffer [p, p + bytes) must be device (or managed) memory of `dev`
-// lying inside one allocation.
-lin_status check_buffer(const void* p, uint64_t bytes, int dev) {
+// lying inside one allocation (whose range `seen` then holds: the tensors of
+// a call are often views of few allocations, and the two queries take longer
+// than all other checks).
+lin_status check_buffer(const void* p, uint64_t bytes, int dev, SeenRange* seen) {
+  const uint64_t at = static_cast<uint64_t>(reinterpret_cast<uintptr_t>(p));
+  if (seen && at >= seen->begin && at < seen->end && bytes <= seen->end - at) return LIN_SUCCESS;
   cudaPointerAttributes a;
   cudaError_t e = cudaPointerGetAttributes(&a, p);
   if (e != cudaSuccess) {
@@ -175,8 +179,9 @@ lin_status check_buffer(const void* p, uint64_t bytes, int dev) {
   size_t size = 0;
   if (driver().range(&base, &size, reinterpret_cast<CUdeviceptr>(p)) != CUDA_SUCCESS)
     return LIN_ERROR_INVALID_VALUE;
-  const uint64_t off = static_cast<uint64_t>(reinterpret_cast<uintptr_t>(p)) - base;
+  const uint64_t off = at - base;
   if (off > size || bytes > size - off) return LIN_ERROR_INVALID_VALUE;
+  if (seen) *seen = SeenRange{(uint64_t)base, (uint64_t)base + size};
   return LIN_SUCCESS;
 }
 

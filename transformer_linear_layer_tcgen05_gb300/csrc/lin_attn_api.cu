@@ -69,13 +69,14 @@ lin_status check_attention(const lin_attention_shape* s, View* views, int nviews
     return LIN_ERROR_ALIASING;
   lin_status st = current_device(&got->dev, &got->word);
   if (st != LIN_SUCCESS) return st;
+  SeenRange seen;
   for (int i = 0; i < nviews; ++i)
     if (views[i].extent &&
-        (st = check_buffer(views[i].t->data, views[i].extent, got->dev)) != LIN_SUCCESS)
+        (st = check_buffer(views[i].t->data, views[i].extent, got->dev, &seen)) != LIN_SUCCESS)
       return st;
-  if (lse_bytes && (st = check_buffer(lse, lse_bytes, got->dev)) != LIN_SUCCESS) return st;
-  if (s->cu_q && (st = check_buffer(s->cu_q, cu_bytes, got->dev)) != LIN_SUCCESS) return st;
-  if (s->cu_k && (st = check_buffer(s->cu_k, cu_bytes, got->dev)) != LIN_SUCCESS) return st;
+  if (lse_bytes && (st = check_buffer(lse, lse_bytes, got->dev, &seen)) != LIN_SUCCESS) return st;
+  if (s->cu_q && (st = check_buffer(s->cu_q, cu_bytes, got->dev, &seen)) != LIN_SUCCESS) return st;
+  if (s->cu_k && (st = check_buffer(s->cu_k, cu_bytes, got->dev, &seen)) != LIN_SUCCESS) return st;
   got->nothing = s->sequences == 0;
   return LIN_SUCCESS;
 }

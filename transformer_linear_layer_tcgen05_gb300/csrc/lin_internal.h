@@ -250,7 +250,10 @@ void set_last_launch_info(int kernels, uint64_t workspace_bytes);
 // current device after the library's checks and its status record, a
 // buffer's checks, the error record, and the SM count.
 lin_status current_device(int* dev_out, int** status_word);
-lin_status check_buffer(const void* p, uint64_t bytes, int dev);
+struct SeenRange {   // an allocation of the device that one call has looked up
+  uint64_t begin = 0, end = 0;
+};
+lin_status check_buffer(const void* p, uint64_t bytes, int dev, SeenRange* seen = nullptr);
 bool overlaps(const void* a, uint64_t abytes, const void* b, uint64_t bbytes);
 lin_status cuda_fail(cudaError_t e);
 int sm_count(int dev);

@@ -38,10 +38,10 @@ lin_status check_buffers(const Buffer* b, int n) {
   return LIN_SUCCESS;
 }
 
-lin_status check_on_device(const Buffer* b, int n, int dev) {
+lin_status check_on_device(const Buffer* b, int n, int dev, SeenRange* seen) {
   for (int i = 0; i < n; ++i)
     if (b[i].bytes) {
-      const lin_status st = check_buffer(b[i].p, b[i].bytes, dev);
+      const lin_status st = check_buffer(b[i].p, b[i].bytes, dev, seen);
       if (st != LIN_SUCCESS) return st;
     }
   return LIN_SUCCESS;
@@ -95,9 +95,10 @@ lin_status qk_norm_rope(const lin_qk_norm_rope_shape* s, const float* X, const f
   int dev = 0;
   int* word = nullptr;
   if ((st = current_device(&dev, &word)) != LIN_SUCCESS) return st;
-  if ((st = check_on_device(b, nb, dev)) != LIN_SUCCESS) return st;
+  SeenRange seen;
+  if ((st = check_on_device(b, nb, dev, &seen)) != LIN_SUCCESS) return st;
   for (const View& w : v)
-    if (w.extent && (st = check_buffer(w.t->data, w.extent, dev)) != LIN_SUCCESS) return st;
+    if (w.extent && (st = check_buffer(w.t->data, w.extent, dev, &seen)) != LIN_SUCCESS) return st;
   if (s->tokens == 0) {   // no rows: the weights' gradients are sums of nothing
     cudaError_t e = cudaSuccess;
     if (backward) e = cudaMemsetAsync(DWQ, 0, wb, stream);
@@ -175,7 +176,8 @@ lin_status distill_topk(const float* LOGITS, int64_t ld, const int32_t* ids, con
   int dev = 0;
   int* word = nullptr;
   if ((st = current_device(&dev, &word)) != LIN_SUCCESS) return st;
-  if ((st = check_on_device(b, nb, dev)) != LIN_SUCCESS) return st;
+  SeenRange seen;
+  if ((st = check_on_device(b, nb, dev, &seen)) != LIN_SUCCESS) return st;
   if (M == 0 || V == 0) {   // no rows, or no entry that a row could list
     cudaError_t e = cudaMemsetAsync(loss_sum, 0, 4, stream);
     if (e == cudaSuccess && M > 0) e = cudaMemsetAsync(losses, 0, rows * 4, stream);

@@ -448,24 +448,23 @@ def _heads(tensors, names):
     return _DTYPE16[first], range(base, base + 8 * len(fields), 24), keep
 
 
-def _int32(t, name, shape):
-    """Address of a contiguous int32 CUDA tensor (None: of any one dimension)."""
-    torch = _t()
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or not t.is_cuda or \
+def _flat(t, name, shape, dtype):
+    """Address of a contiguous CUDA tensor of the given type and shape (None:
+    of any one dimension)."""
+    if not isinstance(t, _torch.Tensor) or t.dtype is not dtype or not t.is_cuda or \
             not t.is_contiguous() or (t.shape != shape if shape is not None else
                                       t.dim() != 1 or t.numel() < 1):
-        raise TypeError(f"{name} must be a contiguous int32 CUDA tensor" +
+        raise TypeError(f"{name} must be a contiguous {dtype} CUDA tensor" +
                         (f" {list(shape)}" if shape is not None else ""))
     return t.data_ptr()
 
 
+def _int32(t, name, shape):
+    return _flat(t, name, shape, _torch.int32)
+
+
 def _f32_flat(t, name, shape):
-    """Address of a contiguous float32 CUDA tensor of the given shape."""
-    torch = _t()
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda or \
-            t.shape != shape or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous float32 CUDA tensor {list(shape)}")
-    return t.data_ptr()
+    return _flat(t, name, shape, _torch.float32)
 
 
 def _attention_shape(dtype, Q, K, V, cu_q, cu_k, max_q, max_k, causal, scale):
@@ -599,7 +598,7 @@ def lin_distill_topk(LOGITS, ids, teacher, DLOGITS, losses, loss_sum, temperatur
     float32 (an id outside [0, V): an empty place); DLOGITS like LOGITS,
     LOGITS itself, or None (the losses alone); losses [M], loss_sum [1]."""
     M, V = _f32_rows(LOGITS, "logits").shape
-    K = ids.shape[-1] if isinstance(ids, _t().Tensor) and ids.dim() == 2 else 0
+    K = ids.shape[-1] if isinstance(ids, _torch.Tensor) and ids.dim() == 2 else 0
     i = _int32(ids, "ids", (M, K))
     d, ldd = None, 0
     if DLOGITS is not None:
