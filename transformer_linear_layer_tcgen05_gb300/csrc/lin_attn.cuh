@@ -70,7 +70,7 @@ __device__ __forceinline__ PartOf part_of(int z, int parts) {
 // steps of a product add constants to the tile's descriptor.
 template <int DP, int ROWS = 128>
 struct AttnTile {
-  static constexpr int SUB = DP / 64;
+  static constexpr int SUB = (DP + 63) / 64;
   static constexpr uint32_t SUB_BYTES = ROWS * 128;
   static constexpr uint32_t BYTES = SUB * SUB_BYTES;
   static constexpr uint64_t UNITS = BYTES / 16;

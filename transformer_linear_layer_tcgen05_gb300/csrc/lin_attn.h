@@ -32,6 +32,7 @@ struct AttnFwdArgs {
   // [part][token][head][dim], [part][head][token]
   int32_t parts;
   float *o_part, *lse_part;
+  int32_t rows;   // queries of a CTA: 128 or 256
 };
 
 struct AttnBwdArgs {

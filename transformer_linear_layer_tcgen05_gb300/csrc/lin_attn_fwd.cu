@@ -10,8 +10,9 @@
 // inside both 16-bit types' range) and O is left alone: the quotient O / l
 // does not depend on it.
 //
-// A CTA runs two tiles of 128 queries of one head against the same keys: 128
-// threads per tile (one per row) take turns on the exponentials while the
+// A CTA runs two tiles of 128 queries of one head (one, where even so every
+// CTA has an SM to itself) against the same keys: 128 threads per tile (one
+// per row) take turns on the exponentials while the
 // tensor cores work for the other tile, and each K, V tile is read once for
 // 256 queries. The products of one thread execute in issue order, so S of
 // the next tile is issued right behind the P V that reads P out of the same
@@ -20,6 +21,8 @@
 // into parts, a CTA each, whose results a second kernel joins by their
 // log-sum-exps.
 #include "lin_attn.cuh"
+
+#include <type_traits>
 
 namespace lin {
 
@@ -36,7 +39,7 @@ static_assert(2 * kFwdRegsRow + kFwdRegsIssue <= 3 * 168, "registers of the laun
 
 template <int DP>
 struct FwdCfg {
-  static constexpr int NKV = DP == 64 ? 3 : 2;   // stages of the K and of the V ring
+  static constexpr int NKV = DP <= 64 ? 3 : 2;   // stages of the K and of the V ring
   static constexpr uint32_t TILE = AttnTile<DP>::BYTES;
   // barrier slots
   static constexpr int Q_FULL = 0;               // 2
@@ -71,7 +74,9 @@ __device__ __forceinline__ int fwd_key_tiles(int i0, int lq, int lk, int causal)
 
 }  // namespace
 
-template <int DP, bool BF16>
+// (the queries of a CTA are a parameter of the compiler's: read from the
+// arguments they cost the longest rows 2 %, 347 -> 353 us)
+template <int DP, bool BF16, int ROWS>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     lin_attn_fwd_kernel(const __grid_constant__ AttnFwdMaps maps,
                         const __grid_constant__ AttnFwdArgs args) {
@@ -81,13 +86,14 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const int h = blockIdx.x;
   const PartOf at = part_of(blockIdx.z, args.parts);
   const int b = at.b;
-  const int i0 = (gridDim.y - 1 - blockIdx.y) * 256;   // longest rows of a causal mask first
+  // longest rows of a causal mask first
+  const int i0 = (int)(gridDim.y - 1 - blockIdx.y) * ROWS;
   const SeqRange sq = seq_range(a.cu_q, b, a.tokens_q, a.max_q);
   if (i0 >= sq.len) return;   // (the whole CTA)
   const SeqRange sk = seq_range(a.cu_k, b, a.tokens_k, a.max_k);
   // key tiles of the two query tiles, and of them those of this part, from j0 on
   const int all0 = fwd_key_tiles(i0, sq.len, sk.len, a.causal);
-  const int all1 = fwd_key_tiles(i0 + 128, sq.len, sk.len, a.causal);
+  const int all1 = ROWS > 128 ? fwd_key_tiles(i0 + 128, sq.len, sk.len, a.causal) : 0;
   const int all = max(all0, all1);
   const int j0 = at.begin(all), j1 = at.end(all);
   const int n0 = max(min(all0, j1) - j0, 0), n1 = max(min(all1, j1) - j0, 0);
@@ -230,7 +236,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int t = warp >> 2, row = tid & 127;
     const int nk = t ? n1 : n0;
     const int i = i0 + t * 128 + row;   // query of the sequence
-    const bool live = i < sq.len;
+    const bool live = i < sq.len && (ROWS > 128 || t == 0);
     const float c = a.scale * kLog2E;
     // the last key that this row may see
     const int lim = live ? (a.causal ? min(sk.len - 1, i + sk.len - sq.len) : sk.len - 1) : -1;
@@ -412,7 +418,7 @@ __global__ void __launch_bounds__(256)
 cudaError_t launch_attn_fwd(bool bf16, const AttnFwdMaps& maps, const AttnFwdArgs& args,
                             int heads_kv, int sequences, cudaStream_t stream) {
   const unsigned heads = (unsigned)(heads_kv * args.s.group);
-  const dim3 grid(heads, (unsigned)((args.s.max_q + 255) / 256),
+  const dim3 grid(heads, (unsigned)((args.s.max_q + args.rows - 1) / args.rows),
                   (unsigned)sequences * (unsigned)args.parts);
   auto go = [&](auto kernel, uint32_t smem) {
     const cudaError_t e =
@@ -421,13 +427,20 @@ cudaError_t launch_attn_fwd(bool bf16, const AttnFwdMaps& maps, const AttnFwdArg
     kernel<<<grid, kFwdThreads, smem, stream>>>(maps, args);
     return cudaGetLastError();
   };
-  cudaError_t e;
-  if (args.s.dim <= 64)
-    e = bf16 ? go(lin_attn_fwd_kernel<64, true>, FwdCfg<64>::SMEM)
-             : go(lin_attn_fwd_kernel<64, false>, FwdCfg<64>::SMEM);
-  else
-    e = bf16 ? go(lin_attn_fwd_kernel<128, true>, FwdCfg<128>::SMEM)
-             : go(lin_attn_fwd_kernel<128, false>, FwdCfg<128>::SMEM);
+  auto types = [&](auto size) {
+    constexpr int DP = decltype(size)::value;
+    constexpr uint32_t smem = FwdCfg<DP>::SMEM;
+    if (args.rows == 128)
+      return bf16 ? go(lin_attn_fwd_kernel<DP, true, 128>, smem)
+                  : go(lin_attn_fwd_kernel<DP, false, 128>, smem);
+    return bf16 ? go(lin_attn_fwd_kernel<DP, true, 256>, smem)
+                : go(lin_attn_fwd_kernel<DP, false, 256>, smem);
+  };
+  // (heads of 65 to 96 entries: a quarter less of both products than 128; 4096
+  // causal tokens, 16 heads of 96: 52.2 -> 49.1 us)
+  const cudaError_t e = args.s.dim <= 64   ? types(std::integral_constant<int, 64>{})
+                        : args.s.dim <= 96 ? types(std::integral_constant<int, 96>{})
+                                           : types(std::integral_constant<int, 128>{});
   if (e != cudaSuccess || args.parts == 1) return e;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
