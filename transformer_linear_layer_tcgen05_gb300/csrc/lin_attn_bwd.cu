@@ -72,7 +72,8 @@ struct BwdCfg {
   static constexpr int OUT_FULL = SUM_READY + 1; // the sums complete (every product is)
   static constexpr int BARS = OUT_FULL + 1;
   static __device__ __forceinline__ uint32_t arrivals(int i) {
-    return i == SUM_READY || (i == OWN_READY && !OWN) ? 256 : i >= S_DONE && i < SUM_READY ? 128 : 1;
+    // (a lane of each warp of rows: 8 warps, 4 of a stream)
+    return i == SUM_READY || (i == OWN_READY && !OWN) ? 8 : i >= S_DONE && i < SUM_READY ? 4 : 1;
   }
   static __device__ __forceinline__ bool streamed_full(int i) { return i >= FULL && i < EMPTY; }
   static constexpr uint32_t OFF_TMEM = BARS * 8, OFF_ABORT = OFF_TMEM + 4;
@@ -96,7 +97,7 @@ struct BwdCfg {
 template <int DP>
 using DqCfg = BwdCfg<DP, 6, 1, false, 4 * 128>;
 template <int DP>
-using DkvCfg = BwdCfg<DP, DP == 64 ? 6 : 5, 2, DP == 128, 2 * (DP == 64 ? 6 : 5) * kTurn>;
+using DkvCfg = BwdCfg<DP, DP == 64 ? 6 : 5, 2, (DP > 64), 2 * (DP == 64 ? 6 : 5) * kTurn>;
 
 // The CTA's shared memory, which the tiles' swizzle wants at a multiple of
 // 1024 bytes (it begins there: the kernels have no other shared memory). At
@@ -110,11 +111,14 @@ __device__ __forceinline__ bool smem_aligned(const void* p, int* status) {
 // Columns of packed results and operands into tensor memory.
 template <int N>
 __device__ __forceinline__ void tmem_put(uint32_t col, const uint32_t (&r)[N]) {
-  static_assert(N == 16 || N == 32, "columns");
-  if constexpr (N == 32)
+  static_assert(N == 16 || N == 24 || N == 32, "columns");
+  if constexpr (N == 32) {
     tmem_st_32x32b_x32(col, r);
-  else
-    tmem_st_32x32b_x16(col, r);
+  } else {
+    tmem_st_32x32b_x16(col, reinterpret_cast<const uint32_t(&)[16]>(r));
+    if constexpr (N == 24)
+      tmem_st_32x32b_x8(col + 16, reinterpret_cast<const uint32_t(&)[8]>(r[16]));
+  }
 }
 
 // 2^e as a float, e held to where 2^e and 2^-e are normal.
@@ -138,13 +142,13 @@ struct HeadGrad {
                                       int64_t tokens, int heads, int dim, int64_t token, int h)
       : row(t.p + token * t.token_stride + (int64_t)h * t.head_stride),
         part_row(parts > 1 ? parts_base + ((part * tokens + token) * heads + h) * dim : nullptr) {}
-  // 32 columns from c0 on, times `back` (zeros if there is nothing), those
+  // N columns from c0 on, times `back` (zeros if there is nothing), those
   // below dim.
-  template <bool BF16>
-  __device__ __forceinline__ void put(const uint32_t (&o)[32], bool any, float back, int c0,
+  template <bool BF16, int N>
+  __device__ __forceinline__ void put(const uint32_t (&o)[N], bool any, float back, int c0,
                                       int dim) const {
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
+    for (int g = 0; g < N / 8; ++g) {
       const int col = c0 + g * 8;
       float v[8];
 #pragma unroll
@@ -226,7 +230,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       int issued = 0;
       RingAt<C::N> r;
       for (int j = 0; j < n; ++j, ++issued) {
-        if (j >= C::N && !wait_phase(bar(C::EMPTY + r.s), r.parity ^ 1, ctl)) break;
+        if (j >= C::N && !attn_wait(bar(C::EMPTY + r.s), r.parity ^ 1, ctl)) break;
         mbar_arrive_expect_tx(bar(C::FULL + r.s), 2 * C::TILE);
         load_tile<DP, kTurn>(k_tile(r.s), &maps.k, hk, sk.start + (j0 + j) * kTurn,
                              bar(C::FULL + r.s));
@@ -236,13 +240,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       if (*abort) {   // no copy may still be in flight when the CTA ends
         for (int j = max(0, issued - C::N); j < issued; ++j)
-          wait_phase(bar(C::FULL + j % C::N), (j / C::N) & 1, ctl, false);
+          attn_wait(bar(C::FULL + j % C::N), (j / C::N) & 1, ctl, false);
       }
     }
     __syncwarp();
     if (n > 0 && k_left < kTurn) {   // cut the last K tile at the sequence's end (dS K runs over it)
       const int s = (n - 1) % C::N;
-      if (warp_wait_phase(bar(C::FULL + s), ((n - 1) / C::N) & 1, ctl)) {
+      if (warp_attn_wait(bar(C::FULL + s), ((n - 1) / C::N) & 1, ctl)) {
         zero_rows<DP, kTurn>(k_tile(s), k_left, lane);
         fence_proxy_async_smem();
         __syncwarp();
@@ -257,8 +261,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       RingAt<C::N> r, next;   // stages of tile j, and of the next S and dP
       int nj = 0;             // tile of `next`
       auto scores = [&](int t) -> bool {   // S = Q K^T of the next tile
-        if (!wait_phase(bar(C::FULL + next.s), next.parity, ctl) ||
-            (++nj == n && k_left < kTurn && !wait_phase(bar(C::TAIL), 0, ctl)))
+        if (!attn_wait(bar(C::FULL + next.s), next.parity, ctl) ||
+            (++nj == n && k_left < kTurn && !attn_wait(bar(C::TAIL), 0, ctl)))
           return false;
         umma_entries_tmem<DP, kTurn, BF16>(C::S_COL + t * kTurn, kQ, k_desc + next.s * STAGE);
         umma_commit(bar(C::S_FULL + t));
@@ -269,7 +273,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         umma_commit(bar(C::DP_FULL + t));
         next.next();
       };
-      bool ok = wait_phase(bar(C::OWN_READY), 0, ctl);
+      bool ok = attn_wait(bar(C::OWN_READY), 0, ctl);
       tc_fence_after_sync();
       for (int t = 0; t < 2 && t < n && ok; ++t) {
         ok = scores(t);
@@ -278,11 +282,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       for (int j = 0; j < n && ok; ++j) {
         const int t = j & 1, u = (j >> 1) & 1;
         if (j + 2 < n) {
-          ok = wait_phase(bar(C::S_DONE + t), u, ctl);
+          ok = attn_wait(bar(C::S_DONE + t), u, ctl);
           tc_fence_after_sync();
           ok = ok && scores(t);
         }
-        ok = ok && wait_phase(bar(C::DS_READY + t), u, ctl);
+        ok = ok && attn_wait(bar(C::DS_READY + t), u, ctl);
         if (!ok) break;
         tc_fence_after_sync();
         umma_tokens<DP, BF16, kTurn / 16>(C::OUT_COL, C::DP_COL + t * kTurn, kt_desc + r.s * STAGE,
@@ -293,7 +297,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       }
       // (also on the way out: tensor memory must be idle at the end)
       umma_commit(bar(C::OUT_FULL));
-      wait_phase(bar(C::OUT_FULL), 0, ctl, false);
+      attn_wait(bar(C::OUT_FULL), 0, ctl, false);
     }
     __syncwarp();
   } else if (warp < kRowWarps) {
@@ -319,7 +323,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       tmem_put<DP / 4>(tmem + lanes + kDo + half * (DP / 4), y);
       tmem_wait_st();
       tc_fence_before_sync();
-      mbar_arrive(bar(C::OWN_READY));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::OWN_READY));
 #pragma unroll
       for (int e = 0; e < DP / 4; ++e) {
         const float2 u = unpack16<BF16>(z[e]), v = unpack16<BF16>(y[e]);
@@ -356,12 +361,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (few && n == 1 && half == 1) {   // (no tile: nothing to the row's sums below)
       red[128 + row] = 0.0f;
       red[384 + row] = 0.0f;
-      mbar_arrive(bar(C::SUM_READY));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::SUM_READY));
     }
     bool ok = true;
     for (int j = half; j < n; j += 2) {   // the warpgroup's stream
       const int u = (j >> 1) & 1;
-      ok = warp_wait_phase(bar(C::S_FULL + half), u, ctl);
+      ok = warp_attn_wait(bar(C::S_FULL + half), u, ctl);
       if (!ok) break;
       tc_fence_after_sync();
       uint32_t p[2][32], d[2][32];
@@ -370,7 +376,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       tmem_wait_ld_x32(p[0]);
       tmem_wait_ld_x32(p[1]);
       tc_fence_before_sync();
-      mbar_arrive(bar(C::S_DONE + half));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::S_DONE + half));
       const float2 cc = make_float2(c, c), ll = make_float2(nl, nl);
 #pragma unroll
       for (int q = 0; q < 2; ++q)
@@ -380,7 +387,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           p[q][e] = __float_as_uint(ex2_approx(x.x));
           p[q][e + 1] = __float_as_uint(ex2_approx(x.y));
         }
-      ok = warp_wait_phase(bar(C::DP_FULL + half), u, ctl);
+      ok = warp_attn_wait(bar(C::DP_FULL + half), u, ctl);
       if (!ok) break;
       tc_fence_after_sync();
       tmem_ld_32x32b_x32(dp_col, d[0]);
@@ -404,8 +411,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
         red[half * 128 + row] = sd;
         red[256 + half * 128 + row] = sp;
-        mbar_arrive(bar(C::SUM_READY));
-        ok = warp_wait_phase(bar(C::SUM_READY), 0, ctl);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::SUM_READY));
+        ok = warp_attn_wait(bar(C::SUM_READY), 0, ctl);
         if (!ok) break;
         sp = red[256 + row] + red[384 + row];
         delta = sp > 0.0f ? (red[row] + red[128 + row]) / sp : 0.0f;
@@ -438,10 +446,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       tmem_st_32x32b_x32(dp_col, w);
       tmem_wait_st();
       tc_fence_before_sync();
-      mbar_arrive(bar(C::DS_READY + half));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::DS_READY + half));
     }
     if (ok && n > 0) {
-      ok = warp_wait_phase(bar(C::OUT_FULL), 0, ctl);
+      ok = warp_attn_wait(bar(C::OUT_FULL), 0, ctl);
       tc_fence_after_sync();
     }
     if (ok) {
@@ -449,12 +458,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       const HeadGrad out(args.dq, args.dq_part, args.q_parts, part, a.tokens_q, a.heads_q, a.dim,
                          token, h);
 #pragma unroll
-      for (int q = 0; q < DP / 64; ++q) {
-        const int c0 = half * (DP / 2) + q * 32;
-        uint32_t o[32];
+      for (int q = 0; q < DP / 32; ++q) {
+        const int c0 = half * (DP / 2) + q * 16;
+        uint32_t o[16];
         if (n > 0) {
-          tmem_ld_32x32b_x32(tmem + lanes + C::OUT_COL + c0, o);
-          tmem_wait_ld_x32(o);
+          tmem_ld_32x32b_x16(tmem + lanes + C::OUT_COL + c0, o);
+          tmem_wait_ld_x16(o);
         }
         out.put<BF16>(o, n > 0, back, c0, live ? a.dim : 0);
       }
@@ -561,7 +570,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         int h = h0 + from / per, tile = tile0;   // of this turn (n > 0: per > 0)
         for (int it = 0; it < n; ++it, ++issued) {
           const int z = sq.start + (t0 + tile) * kTurn;
-          if (it >= C::N && !wait_phase(bar(C::EMPTY + r.s), r.parity ^ 1, ctl)) break;
+          if (it >= C::N && !attn_wait(bar(C::EMPTY + r.s), r.parity ^ 1, ctl)) break;
           mbar_arrive_expect_tx(bar(C::FULL + r.s), 2 * C::TILE);
           load_tile<DP, kTurn>(q_tile(r.s), &maps.q, h, z, bar(C::FULL + r.s));
           load_tile<DP, kTurn>(do_tile(r.s), &maps.dout, h, z, bar(C::FULL + r.s));
@@ -572,9 +581,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
           }
         }
         if (*abort) {   // no copy may still be in flight when the CTA ends
-          if (C::kOwnSmem) wait_phase(bar(C::OWN_READY), 0, ctl, false);
+          if (C::kOwnSmem) attn_wait(bar(C::OWN_READY), 0, ctl, false);
           for (int it = max(0, issued - C::N); it < issued; ++it)
-            wait_phase(bar(C::FULL + it % C::N), (it / C::N) & 1, ctl, false);
+            attn_wait(bar(C::FULL + it % C::N), (it / C::N) & 1, ctl, false);
         }
       }
     }
@@ -612,7 +621,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         nd[e] = delta[e] * -damp;
       }
       if (it + 1 < n) load();
-      if (it >= C::N && !warp_wait_phase(bar(C::EMPTY + r.s), r.parity ^ 1, ctl)) break;
+      if (it >= C::N && !warp_attn_wait(bar(C::EMPTY + r.s), r.parity ^ 1, ctl)) break;
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         lse_rows(r.s)[e * 32 + lane] = nl[e];
@@ -631,7 +640,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       int tile = tile0;
       RingAt<C::N> r;
       for (int it = 0; it < n; ++it) {
-        if (!warp_wait_phase(bar(C::FULL + r.s), r.parity, ctl)) break;
+        if (!warp_attn_wait(bar(C::FULL + r.s), r.parity, ctl)) break;
         if (++tile == per) {
           tile = 0;
           zero_rows<DP, kTurn>(q_tile(r.s), q_left, lane);
@@ -658,7 +667,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
           umma_entries_tmem<DP, kTurn, BF16>(d, col, other);
       };
       auto scores = [&](int t) -> bool {   // S^T = K Q^T of the next turn
-        if (!wait_phase(bar(ready + next.s), next.parity, ctl)) return false;
+        if (!attn_wait(bar(ready + next.s), next.parity, ctl)) return false;
         own(C::S_COL + t * kTurn, kK, k_own, q_desc + next.s * STAGE);
         umma_commit(bar(C::S_FULL + t));
         return true;
@@ -668,7 +677,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         umma_commit(bar(C::DP_FULL + t));
         next.next();
       };
-      bool ok = wait_phase(bar(C::OWN_READY), 0, ctl);
+      bool ok = attn_wait(bar(C::OWN_READY), 0, ctl);
       tc_fence_after_sync();
       for (int t = 0; t < 2 && t < n && ok; ++t) {
         ok = scores(t);
@@ -676,13 +685,13 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       }
       for (int it = 0; it < n && ok; ++it) {
         const int t = it & 1, u = (it >> 1) & 1;
-        ok = wait_phase(bar(C::S_DONE + t), u, ctl);
+        ok = attn_wait(bar(C::S_DONE + t), u, ctl);
         if (!ok) break;
         tc_fence_after_sync();
         umma_tokens<DP, BF16, kTurn / 16>(C::OUT_COL, C::S_COL + t * kTurn, dot_desc + r.s * STAGE,
                                           0, it == 0);   // dV += P^T dO
         if (it + 2 < n) ok = scores(t);
-        ok = ok && wait_phase(bar(C::DS_READY + t), u, ctl);
+        ok = ok && attn_wait(bar(C::DS_READY + t), u, ctl);
         if (!ok) break;
         tc_fence_after_sync();
         umma_tokens<DP, BF16, kTurn / 16>(C::OUT_COL + DP, C::DP_COL + t * kTurn,
@@ -693,7 +702,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       }
       // (also on the way out: tensor memory must be idle at the end)
       umma_commit(bar(C::OUT_FULL));
-      wait_phase(bar(C::OUT_FULL), 0, ctl, false);
+      attn_wait(bar(C::OUT_FULL), 0, ctl, false);
     }
     __syncwarp();
   } else if (warp < kRowWarps) {
@@ -716,7 +725,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       tmem_put<DP / 4>(tmem + lanes + kV + half * (DP / 4), y);
       tmem_wait_st();
       tc_fence_before_sync();
-      mbar_arrive(bar(C::OWN_READY));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::OWN_READY));
     }
     const int ne = scale_exponent();
     const float damp = ds_scale(ne);
@@ -731,10 +741,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       for (tile += 2; tile >= per;) tile -= per;
       const float4* nl = reinterpret_cast<const float4*>(lse_rows(r.s));
       const float4* nd = reinterpret_cast<const float4*>(delta_rows(r.s));
-      ok = warp_wait_phase(bar(C::S_FULL + half), u, ctl);
+      ok = warp_attn_wait(bar(C::S_FULL + half), u, ctl);
       if (!ok) break;
       // (the stage was full before S was formed)
-      ok = warp_wait_phase(bar(C::FULL + r.s), r.parity, ctl);
+      ok = warp_attn_wait(bar(C::FULL + r.s), r.parity, ctl);
       if (!ok) break;
       r.next();
       r.next();
@@ -777,8 +787,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       tmem_put<NQ * 16>(s_col, w);
       tmem_wait_st();
       tc_fence_before_sync();
-      mbar_arrive(bar(C::S_DONE + half));
-      ok = warp_wait_phase(bar(C::DP_FULL + half), u, ctl);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::S_DONE + half));
+      ok = warp_attn_wait(bar(C::DP_FULL + half), u, ctl);
       if (!ok) break;
       tc_fence_after_sync();
 #pragma unroll
@@ -817,10 +828,11 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       tmem_put<NQ * 16>(dp_col, w);
       tmem_wait_st();
       tc_fence_before_sync();
-      mbar_arrive(bar(C::DS_READY + half));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::DS_READY + half));
     }
     if (ok && n > 0) {
-      ok = warp_wait_phase(bar(C::OUT_FULL), 0, ctl);
+      ok = warp_attn_wait(bar(C::OUT_FULL), 0, ctl);
       tc_fence_after_sync();
     }
     if (ok) {   // the first half's threads write dV, the others dK
@@ -946,11 +958,14 @@ cudaError_t launch_attn_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArg
   };
   auto dims = [&](auto type) {
     constexpr bool B = decltype(type)::value;
-    return args.s.dim <= 64
-               ? both(lin_attn_dq_kernel<64, B>, DqCfg<64>::SMEM, lin_attn_dkv_kernel<64, B>,
-                      DkvCfg<64>::SMEM)
-               : both(lin_attn_dq_kernel<128, B>, DqCfg<128>::SMEM, lin_attn_dkv_kernel<128, B>,
-                      DkvCfg<128>::SMEM);
+    auto size = [&](auto entries) {
+      constexpr int DP = decltype(entries)::value;
+      return both(lin_attn_dq_kernel<DP, B>, DqCfg<DP>::SMEM, lin_attn_dkv_kernel<DP, B>,
+                  DkvCfg<DP>::SMEM);
+    };
+    return args.s.dim <= 64   ? size(std::integral_constant<int, 64>{})
+           : args.s.dim <= 96 ? size(std::integral_constant<int, 96>{})
+                              : size(std::integral_constant<int, 128>{});
   };
   cudaError_t e = bf16 ? dims(std::true_type{}) : dims(std::false_type{});
   if (e == cudaSuccess && args.q_parts > 1)

@@ -36,7 +36,6 @@ namespace {
 constexpr int kFwdThreads = 384;
 constexpr int kFwdRegsRow = 208, kFwdRegsIssue = 88;
 static_assert(2 * kFwdRegsRow + kFwdRegsIssue <= 3 * 168, "registers of the launch");
-
 template <int DP>
 struct FwdCfg {
   static constexpr int NKV = DP <= 64 ? 3 : 2;   // stages of the K and of the V ring
@@ -49,7 +48,8 @@ struct FwdCfg {
   static constexpr int V_EMPTY = V_FULL + NKV;
   static constexpr int S_FULL = V_EMPTY + NKV;   // 2
   static constexpr int P_READY = S_FULL + 2;     // 2 x 2: first and second half of the keys
-  static constexpr int O_FULL = P_READY + 4;     // 2
+  static constexpr int S_TAKEN = P_READY + 4;    // 2
+  static constexpr int O_FULL = S_TAKEN + 2;     // 2
   static constexpr int TAIL = O_FULL + 2;        // the last V tile is cut at the sequence's end
   static constexpr int DRAIN = TAIL + 1;         // every product of the CTA is done
   static constexpr int BARS = DRAIN + 1;
@@ -60,8 +60,12 @@ struct FwdCfg {
   static constexpr uint32_t OFF_V = OFF_K + NKV * TILE;
   static constexpr uint32_t SMEM = OFF_V + NKV * TILE + 1024;   // + alignment of the base
   static_assert(SMEM <= 232448, "shared memory");
-  // tensor memory columns: S (and P over it) of the two tiles, then O
+  // P has columns of its own where the 512 hold them, and S of the next tile
+  // is then computed while the rows work on this one's
+  static constexpr bool AHEAD = DP == 64;
+  // tensor memory columns: S (and P over it) of the two tiles, O, P
   static constexpr uint32_t S_COL = 0, O_COL = 256;
+  static constexpr uint32_t p_col(int t) { return AHEAD ? 384 + t * 64 : S_COL + t * 128; }
 };
 
 // Key tiles that the queries [i0, i0 + 128) of a sequence need.
@@ -113,7 +117,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
   if (tid == 0) *abort = 0;
   if (tid < C::BARS) {
-    mbar_init(bar(tid), tid >= C::P_READY && tid < C::P_READY + 4 ? 128 : 1);
+    mbar_init(bar(tid), tid >= C::P_READY && tid < C::O_FULL ? 4 : 1);
     fence_barrier_init();
   }
   tc_fence_before_sync();
@@ -136,7 +140,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         for (int j = 0; j < n; ++j) {
           const int s = j % C::NKV, round = j / C::NKV;
-          if (round > 0 && !wait_phase(bar(C::K_EMPTY + s), (round - 1) & 1, ctl)) break;
+          if (round > 0 && !attn_wait(bar(C::K_EMPTY + s), (round - 1) & 1, ctl)) break;
           mbar_arrive_expect_tx(bar(C::K_FULL + s), C::TILE);
           load_tile<DP, 128>(base + C::OFF_K + s * C::TILE, &maps.k, hk, sk.start + (j0 + j) * 128,
                         bar(C::K_FULL + s));
@@ -146,7 +150,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             load_tile<DP, 128>(base + C::OFF_Q + C::TILE, &maps.q, h, z + 128, bar(C::Q_FULL + 1));
             second = true;
           }
-          if (round > 0 && !wait_phase(bar(C::V_EMPTY + s), (round - 1) & 1, ctl)) break;
+          if (round > 0 && !attn_wait(bar(C::V_EMPTY + s), (round - 1) & 1, ctl)) break;
           mbar_arrive_expect_tx(bar(C::V_FULL + s), C::TILE);
           load_tile<DP, 128>(base + C::OFF_V + s * C::TILE, &maps.v, hk, sk.start + (j0 + j) * 128,
                         bar(C::V_FULL + s));
@@ -155,18 +159,18 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         // no copy may still be in flight when the CTA ends (after a wait that
         // ran out; otherwise all of these have completed)
         if (*abort) {
-          if (n0 > 0) wait_phase(bar(C::Q_FULL), 0, ctl, false);
-          if (second) wait_phase(bar(C::Q_FULL + 1), 0, ctl, false);
+          if (n0 > 0) attn_wait(bar(C::Q_FULL), 0, ctl, false);
+          if (second) attn_wait(bar(C::Q_FULL + 1), 0, ctl, false);
           for (int j = max(0, k_issued - C::NKV); j < k_issued; ++j)
-            wait_phase(bar(C::K_FULL + j % C::NKV), (j / C::NKV) & 1, ctl, false);
+            attn_wait(bar(C::K_FULL + j % C::NKV), (j / C::NKV) & 1, ctl, false);
           for (int j = max(0, v_issued - C::NKV); j < v_issued; ++j)
-            wait_phase(bar(C::V_FULL + j % C::NKV), (j / C::NKV) & 1, ctl, false);
+            attn_wait(bar(C::V_FULL + j % C::NKV), (j / C::NKV) & 1, ctl, false);
         }
       }
       __syncwarp();
       if (n > 0 && v_left < 128) {   // cut the last V tile at the sequence's end
         const int s = (n - 1) % C::NKV;
-        if (warp_wait_phase(bar(C::V_FULL + s), ((n - 1) / C::NKV) & 1, ctl)) {
+        if (warp_wait_phase<kAttnNapNs>(bar(C::V_FULL + s), ((n - 1) / C::NKV) & 1, ctl)) {
           zero_rows<DP, 128>(base + C::OFF_V + s * C::TILE, v_left, lane);
           fence_proxy_async_smem();
           __syncwarp();
@@ -183,36 +187,47 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                                  k_desc + s * AttnTile<DP>::UNITS);
           umma_commit(bar(C::S_FULL + t));
         };
-        bool ok = wait_phase(bar(C::K_FULL), 0, ctl);
+        bool ok = attn_wait(bar(C::K_FULL), 0, ctl);
         for (int t = 0; t < 2 && ok; ++t) {
           if ((t ? n1 : n0) == 0) continue;
-          ok = wait_phase(bar(C::Q_FULL + t), 0, ctl);
+          ok = attn_wait(bar(C::Q_FULL + t), 0, ctl);
           if (ok) scores(t, 0);
         }
         if (ok) umma_commit(bar(C::K_EMPTY));
         int s = 0, s1 = 1 % C::NKV;           // stages of tiles j and j + 1
         uint32_t round = 0, round1 = C::NKV == 1;
         for (int j = 0; j < n && ok; ++j) {
-          if (j + 1 < n) ok = wait_phase(bar(C::K_FULL + s1), round1 & 1, ctl);
-          ok = ok && wait_phase(bar(C::V_FULL + s), round & 1, ctl);
-          if (ok && j + 1 == n && v_left < 128) ok = wait_phase(bar(C::TAIL), 0, ctl);
-#pragma unroll
+          if (j + 1 < n) ok = attn_wait(bar(C::K_FULL + s1), round1 & 1, ctl);
+          if (C::AHEAD && ok && j + 1 < n0) {
+            ok = attn_wait(bar(C::S_TAKEN), j & 1, ctl);
+            tc_fence_after_sync();
+            if (ok) scores(0, s1);
+          }
+          ok = ok && attn_wait(bar(C::V_FULL + s), round & 1, ctl);
+          if (ok && j + 1 == n && v_left < 128) ok = attn_wait(bar(C::TAIL), 0, ctl);
+#pragma unroll 1
           for (int t = 0; t < 2; ++t) {
             const int nt = t ? n1 : n0;
             if (j >= nt || !ok) continue;
-#pragma unroll
+            if (C::AHEAD && t == 1 && j + 1 < nt) {
+              ok = attn_wait(bar(C::S_TAKEN + 1), j & 1, ctl);
+              tc_fence_after_sync();
+              if (!ok) break;
+              scores(1, s1);
+            }
+#pragma unroll 1
             for (int half = 0; half < 2; ++half) {
-              ok = ok && wait_phase(bar(C::P_READY + 2 * t + half), j & 1, ctl);
+              ok = ok && attn_wait(bar(C::P_READY + 2 * t + half), j & 1, ctl);
               if (!ok) break;
               tc_fence_after_sync();
-              umma_tokens<DP, BF16, 4>(C::O_COL + t * DP, C::S_COL + t * 128 + half * 32,
+              umma_tokens<DP, BF16, 4>(C::O_COL + t * DP, C::p_col(t) + half * 32,
                                        v_desc + s * AttnTile<DP>::UNITS, half * 4,
                                        j == 0 && half == 0);
             }
             if (!ok) break;
-            if (j + 1 < nt)
+            if (!C::AHEAD && j + 1 < nt)
               scores(t, s1);
-            else
+            else   // (ahead: for every tile)
               umma_commit(bar(C::O_FULL + t));
           }
           if (!ok) break;
@@ -227,7 +242,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
         // tensor memory stays allocated until every issued product has finished
         umma_commit(bar(C::DRAIN));
-        wait_phase(bar(C::DRAIN), 0, ctl, false);
+        attn_wait(bar(C::DRAIN), 0, ctl, false);
       }
       __syncwarp();
     }
@@ -242,11 +257,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int lim = live ? (a.causal ? min(sk.len - 1, i + sk.len - sq.len) : sk.len - 1) : -1;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // 32 lanes per warp, lane field at bit 16
     const uint32_t s_col = tmem + lanes + C::S_COL + t * 128;
+    const uint32_t p_col = tmem + lanes + C::p_col(t);
     const uint32_t o_col = tmem + lanes + C::O_COL + t * DP;
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
     for (int j = 0; j < nk; ++j) {
-      ok = warp_wait_phase(bar(C::S_FULL + t), j & 1, ctl);
+      ok = warp_wait_phase<kAttnNapNs>(bar(C::S_FULL + t), j & 1, ctl);
       if (!ok) break;
       tc_fence_after_sync();
       uint32_t s[4][32];
@@ -254,6 +270,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(s_col + q * 32, s[q]);
 #pragma unroll
       for (int q = 0; q < 4; ++q) tmem_wait_ld_x32(s[q]);
+      if constexpr (C::AHEAD) {
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::S_TAKEN + t));
+      }
       const int lim_j = lim - (j0 + j) * 128;
       if (__any_sync(0xffffffffu, lim_j < 127)) {
 #pragma unroll
@@ -274,11 +295,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
       // (a row without a key so far has m = -inf: the difference is inf)
       const bool grow = top > m && !((top - m) * c <= 8.0f);
+      if (C::AHEAD && j > 0) {   // P V of the tiles so far: O may change, and P
+        ok = warp_wait_phase<kAttnNapNs>(bar(C::O_FULL + t), (j - 1) & 1, ctl);
+        if (!ok) break;
+        tc_fence_after_sync();
+      }
       if (__any_sync(0xffffffffu, grow)) {
         const float to = fmaxf(m, top);
         const float alpha = to > m ? ex2_approx((m - to) * c) : 1.0f;
         m = to;
-        if (j > 0) {   // P V of the tiles so far is complete: S of this one came behind it
+        if (j > 0) {   // P V of the tiles so far is complete (not ahead: S came behind it)
           l *= alpha;
 #pragma unroll
           for (int q = 0; q < DP / 32; ++q) {
@@ -307,16 +333,17 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           sum[e & 1] = add2(sum[e & 1], x);
           p[e] = pack16<BF16>(x.x, x.y);
         }
-        tmem_st_32x32b_x32(s_col + q * 32, p);
+        tmem_st_32x32b_x32(p_col + q * 32, p);
         tmem_wait_st();
         tc_fence_before_sync();
-        mbar_arrive(bar(C::P_READY + 2 * t + q));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::P_READY + 2 * t + q));
       }
       sum[0] = add2(sum[0], sum[1]);
       l += sum[0].x + sum[0].y;
     }
     if (ok && nk > 0) {
-      ok = warp_wait_phase(bar(C::O_FULL + t), 0, ctl);
+      ok = warp_wait_phase<kAttnNapNs>(bar(C::O_FULL + t), C::AHEAD ? (nk - 1) & 1 : 0, ctl);
       tc_fence_after_sync();
     }
     if (ok) {

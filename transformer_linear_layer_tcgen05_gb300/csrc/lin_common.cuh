@@ -51,16 +51,18 @@ struct WaitCtl {
 
 // Wait for completion of the barrier phase with parity `parity`. Returns
 // false if the wait ran out (and records the timeout) or, when
-// `honor_abort`, if another role already gave up.
+// `honor_abort`, if another role already gave up. NAP_NS: how long a failed
+// look may suspend the thread (0: the default of the hardware).
+template <uint32_t NAP_NS = 0>
 __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, const WaitCtl& c,
                                            bool honor_abort = true) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_try_wait<NAP_NS>(bar, parity)) return true;
   const uint64_t t0 = global_timer_ns();
 #pragma unroll 1
   for (;;) {
 #pragma unroll 1
     for (int i = 0; i < 16; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
+      if (mbar_try_wait<NAP_NS>(bar, parity)) return true;
     if (honor_abort && *c.abort) return false;
     if (global_timer_ns() - t0 > c.timeout_ns) {
       *c.abort = 1;
@@ -92,8 +94,9 @@ __device__ __forceinline__ bool wait_phase_cluster(uint32_t bar, uint32_t parity
 
 // Warp-uniform wait: every lane waits (each needs the acquire), and the warp
 // proceeds only if all lanes succeeded.
+template <uint32_t NAP_NS = 0>
 __device__ __forceinline__ bool warp_wait_phase(uint32_t bar, uint32_t parity, const WaitCtl& c) {
-  const bool ok = wait_phase(bar, parity, c);
+  const bool ok = wait_phase<NAP_NS>(bar, parity, c);
   return __all_sync(0xffffffffu, ok);
 }
 
