@@ -108,7 +108,8 @@
  * kernels, every shared-memory stage and buffer index, TMEM column range,
  * TMA coordinate alignment, cluster peer rank, and every global index that
  * is not a TMA access (partial tiles, row partials, transform and loss
- * loads) against its buffer. A failed check skips the access and records
+ * loads, the rows and entries that attention and distillation write) against
+ * its buffer. A failed check skips the access and records
  * LIN_ERROR_DEVICE_CHECK with the site and the offending value (a skipped
  * load then makes a bounded wait run out: the kernel still exits cleanly);
  * lin_get_device_status() reports it and lin_last_device_check() tells
@@ -366,9 +367,13 @@ lin_status lin_gate_up_w16(const float *X, const uint16_t *WG16, const uint16_t 
  *             sequences up to 65535; max_q and max_k up to 65535 * 128;
  *             scale > 0. Else LIN_ERROR_UNSUPPORTED_SHAPE (scale:
  *             LIN_ERROR_INVALID_VALUE).
- * Workspace   backward: (tokens_q + sequences * ceil(max_q / 128)) * heads_q
- *             floats from the library's pool, in stream order (a graph
- *             memory node under capture).
+ * Workspace   from the library's pool, in stream order (a graph memory node
+ *             under capture). Backward: (tokens_q + sequences * ceil(max_q /
+ *             128)) * heads_q floats. Where a call has fewer tiles of 128
+ *             rows than the device has SMs, and the other side is long, the
+ *             other side is cut into parts whose results are joined in order:
+ *             then, for each part, also the float32 results themselves
+ *             (forward: O and LSE; backward: DQ, or DK and DV).
  * Errors      as for the linear layers; LIN_ERROR_MISALIGNED also for strides
  *             that are no multiple of 8, LIN_ERROR_INVALID_VALUE for strides
  *             under which two entries of a tensor would share a place;
@@ -394,11 +399,12 @@ typedef struct lin_attention_shape {
   float scale;
 } lin_attention_shape;
 
-/* O and LSE from Q, K, V. One kernel. */
+/* O and LSE from Q, K, V. One kernel; a second one joins parts of the keys. */
 lin_status lin_attention(const lin_attention_shape *shape, const lin_heads *Q, const lin_heads *K,
                          const lin_heads *V, const lin_heads *O, float *LSE, lin_stream_t stream);
 
-/* DQ, DK, DV from DO and the forward call's inputs and results. Two kernels. */
+/* DQ, DK, DV from DO and the forward call's inputs and results. Two kernels;
+ * one more for parts of the keys (DQ), one for parts of the queries (DK, DV). */
 lin_status lin_attention_backward(const lin_attention_shape *shape, const lin_heads *Q,
                                   const lin_heads *K, const lin_heads *V, const lin_heads *O,
                                   const float *LSE, const lin_heads *DO, const lin_heads *DQ,
@@ -530,8 +536,9 @@ int lin_last_cuda_error(void);
 
 /* What the last compute call made on the calling thread enqueued: the number
  * of kernels it launched (the GEMM, plus the binary16 pre-pass of X and the
- * split-tail sum where those run, plus the loss kernels of the lm_head form;
- * all blocks' kernels for a host-operand form; 0 if it enqueued none or
+ * split-tail sum where those run, plus the loss kernels of the lm_head form,
+ * or the kernels of attention, norms and rotation, and distillation; all
+ * blocks' kernels for a host-operand form; 0 if it enqueued none or
  * failed) and the workspace bytes it took from the library's pool. Either
  * pointer may be NULL. */
 void lin_last_launch_info(int* kernels, uint64_t* workspace_bytes);

@@ -207,10 +207,11 @@ bool encode_2d(CUtensorMap* m, CUtensorMapDataType dt, const void* base, uint64_
 }
 
 bool encode_heads(CUtensorMap* m, const void* base, uint64_t dim, uint64_t heads, uint64_t tokens,
-                  uint64_t head_bytes, uint64_t token_bytes, uint32_t box_tokens) {
+                  uint64_t head_bytes, uint64_t token_bytes, uint32_t box_tokens,
+                  uint32_t box_heads) {
   const cuuint64_t dims[3] = {dim, heads, tokens};
   const cuuint64_t strides[2] = {head_bytes, token_bytes};
-  const cuuint32_t box[3] = {64, 1, box_tokens};
+  const cuuint32_t box[3] = {64, box_heads, box_tokens};
   const cuuint32_t estr[3] = {1, 1, 1};
   return driver().encode(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, const_cast<void*>(base), dims,
                          strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -4,7 +4,8 @@
 // The kernels work in tiles of 128 queries x 128 keys. An operand tile is 128
 // tokens of one head, [128 rows][64 entries] of 16 bits with the 128-byte
 // swizzle, one such sub-tile for heads of up to 64 entries and two for up to
-// 128 (entries past the head's size are zero-filled by the copy). The same
+// 128 (entries past the head's size are zero-filled by the copy). Products
+// run over 64, 96 or 128 entries: DP, the least that holds the head. The same
 // tile serves as a K-major operand (the contraction runs over the entries: S
 // = Q K^T, dP = dO V^T) and as an MN-major one (it runs over the tokens: P V,
 // P^T dO, dS^T Q, dS K).
@@ -18,7 +19,6 @@
 namespace lin {
 
 constexpr float kLog2E = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 constexpr int kAttnThreads = 320;   // 8 element-wise warps, 1 copying, 1 issuing products
 constexpr int kAttnCopyWarp = 8;

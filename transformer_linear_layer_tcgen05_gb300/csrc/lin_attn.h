@@ -32,7 +32,9 @@ struct AttnFwdArgs {
   // [part][token][head][dim], [part][head][token]
   int32_t parts;
   float *o_part, *lse_part;
-  int32_t rows;   // queries of a CTA: 128 or 256
+  // tiles of a CTA (1 or 2), query heads of a tile (1, or all that share a key
+  // head), and its queries: 128 / pack
+  int32_t tiles, pack, tile_q;
 };
 
 struct AttnBwdArgs {

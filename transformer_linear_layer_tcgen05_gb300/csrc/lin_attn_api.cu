@@ -81,9 +81,10 @@ lin_status check_attention(const lin_attention_shape* s, View* views, int nviews
   return LIN_SUCCESS;
 }
 
-bool encode_view(CUtensorMap* m, const View& v, int64_t dim, int box_tokens) {
+bool encode_view(CUtensorMap* m, const View& v, int64_t dim, int box_tokens, int box_heads = 1) {
   return encode_heads(m, v.t->data, (uint64_t)dim, (uint64_t)v.heads, (uint64_t)v.tokens,
-                      (uint64_t)v.hs * 2, (uint64_t)v.ts * 2, (uint32_t)box_tokens);
+                      (uint64_t)v.hs * 2, (uint64_t)v.ts * 2, (uint32_t)box_tokens,
+                      (uint32_t)box_heads);
 }
 
 lin::AttnArgs attn_args(const lin_attention_shape* s, const Checked& c) {
@@ -113,26 +114,40 @@ lin_status attention(const lin_attention_shape* s, const lin_heads* Q, const lin
   const lin_status st = check_attention(s, v, 4, LSE, true, &c);
   if (st != LIN_SUCCESS) return st;
   if (c.nothing || c.max_q == 0) return LIN_SUCCESS;
+  lin::AttnFwdArgs a{attn_args(s, c), heads_ptr(v[3]), LSE, 1, nullptr, nullptr, 2, 1, 128};
+  const int sms = sm_count(c.dev);
+  auto tiles = [&] {
+    return (c.max_q + a.tile_q - 1) / a.tile_q * (s->heads_q / a.pack) * s->sequences;
+  };
+  // Short queries: the query heads that share a key head in one tile, where
+  // that makes fewer tiles (32 heads over 8 of 128, us: one query on 8192 keys
+  // 33 -> 17, 16 sequences of one on 2048 114 -> 31; where it makes no fewer,
+  // the tiles are as many and each reads one head's rows).
+  if (a.s.group <= 128) {
+    const int64_t apart = tiles();
+    a.pack = a.s.group;
+    a.tile_q = 128 / a.pack;
+    if (tiles() >= apart) a.pack = 1, a.tile_q = 128;
+  }
+  // One tile to a CTA while every CTA then has an SM to itself (512 tokens, 12
+  // heads: 10.3 -> 8.9 us); beyond that the second tile's exponentials hide
+  // the products' latency and K, V are read half as often.
+  if (tiles() <= sms) a.tiles = 1;
+  const int64_t rows = (int64_t)a.tiles * a.tile_q;
+  a.parts = lin::attn_parts((c.max_q + rows - 1) / rows * (s->heads_q / a.pack) * s->sequences,
+                            c.max_k, sms);
   lin::AttnFwdMaps maps;
-  bool ok = encode_view(&maps.q, v[0], s->dim, 128);
+  bool ok = encode_view(&maps.q, v[0], s->dim, a.tile_q, a.pack);
   // without keys the K and V maps are never used
   ok &= encode_view(&maps.k, v[1].extent ? v[1] : v[0], s->dim, 128);
   ok &= encode_view(&maps.v, v[2].extent ? v[2] : v[0], s->dim, 128);
   if (!ok) return cuda_fail(cudaErrorInvalidValue);
-  lin::AttnFwdArgs a{attn_args(s, c), heads_ptr(v[3]), LSE, 1, nullptr, nullptr, 256};
-  const int sms = sm_count(c.dev);
-  const int64_t tiles = (c.max_q + 127) / 128 * s->heads_q * s->sequences;
-  // One tile to a CTA while every CTA then has an SM to itself (512 tokens, 12
-  // heads: 10.3 -> 8.9 us); beyond that the second tile's exponentials hide
-  // the products' latency and K, V are read half as often.
-  if (tiles <= sms) a.rows = 128;
-  a.parts = lin::attn_parts((c.max_q + a.rows - 1) / a.rows * s->heads_q * s->sequences, c.max_k, sms);
-  const uint64_t rows = (uint64_t)a.parts * (uint64_t)s->tokens_q * (uint64_t)s->heads_q;
-  const size_t bytes = a.parts > 1 ? (size_t)(rows * (uint64_t)(s->dim + 1) * 4) : 0;
+  const uint64_t part_rows = (uint64_t)a.parts * (uint64_t)s->tokens_q * (uint64_t)s->heads_q;
+  const size_t bytes = a.parts > 1 ? (size_t)(part_rows * (uint64_t)(s->dim + 1) * 4) : 0;
   if (bytes) {
     a.o_part = static_cast<float*>(take_stream_workspace(c.dev, bytes, stream));
     if (!a.o_part) return LIN_ERROR_CUDA;
-    a.lse_part = a.o_part + rows * (uint64_t)s->dim;
+    a.lse_part = a.o_part + part_rows * (uint64_t)s->dim;
   }
   cudaError_t e = lin::launch_attn_fwd(s->dtype == LIN_BFLOAT16, maps, a, (int)s->heads_kv,
                                        (int)s->sequences, stream);

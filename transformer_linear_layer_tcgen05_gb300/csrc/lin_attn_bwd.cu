@@ -28,10 +28,20 @@
 // the use of dS. One thread issues all of them, and its own steps count: a
 // wait takes it some 100 cycles even for a barrier that is long complete, so
 // a turn has as few as it can (one barrier for the pair of streamed tiles
-// instead of one each: 703 -> 651 us at 8192 tokens; two issuing threads: no
-// further gain). The CTA's own operands (Q and dO, or K and V) are in tensor
-// memory beside the accumulators, which spares shared memory the reading of
-// them; dK and dV of 128 entries leave no room for that.
+// instead of one each: 703 -> 651 us at 8192 tokens; two issuing threads: 641
+// for heads of 128, but 472 -> 509 for heads of 64). The CTA's own operands
+// (Q and dO, or K and V) are in tensor memory beside the accumulators, which
+// spares shared memory the reading of them; dK and dV of more than 64 entries
+// leave no room for that.
+//
+// What bounds it. 8192 causal tokens, 16 heads of 128: 633-638 us, 1080 TF/s
+// of the five products that the gradient needs and 1510 of the seven that the
+// two kernels execute, 0.78 of the cuBLAS burst rate under the same power
+// limit as the forward kernel. Adding dQ up over the key tiles in one kernel
+// of five products would want atomics, whose order changes the sums. Heads of
+// 64, same lengths: 467 us, 0.53 of that rate: the element-wise work of a
+// turn and the latencies between the roles. Short calls: 512 tokens, 12 heads
+// 19 us, two kernels of four to eight turns each behind one another.
 //
 // Where there are fewer tiles than SMs the other side is cut into parts, a
 // CTA each, whose f32 sums a third kernel adds in order.
@@ -58,7 +68,7 @@ constexpr int kTurn = 64;           // rows of a streamed tile
 template <int DP, int N_, int SUMS, bool OWN, int ROW_FLOATS>
 struct BwdCfg {
   static constexpr int N = N_;                   // stages
-  static constexpr bool kOwnSmem = OWN;
+  [[maybe_unused]] static constexpr bool kOwnSmem = OWN;
   using Tile = AttnTile<DP, kTurn>;
   static constexpr uint32_t TILE = Tile::BYTES;
   static constexpr int OWN_READY = 0;            // the CTA's own operands
@@ -79,7 +89,7 @@ struct BwdCfg {
   static constexpr uint32_t OFF_TMEM = BARS * 8, OFF_ABORT = OFF_TMEM + 4;
   static constexpr uint32_t OFF_RED = 448;       // 16 floats
   static_assert(OFF_ABORT + 4 <= OFF_RED, "barrier region");
-  static constexpr uint32_t OFF_OWN = 0;         // (tiles first: they want 1024-byte bases)
+  [[maybe_unused]] static constexpr uint32_t OFF_OWN = 0;         // (tiles first: they want 1024-byte bases)
   static constexpr uint32_t OFF_A = OWN ? 2 * AttnTile<DP>::BYTES : 0;
   static constexpr uint32_t OFF_B = OFF_A + N * TILE;
   // dK, dV: [N][kTurn] floats -L log2 e + 8, then [N][kTurn] -a delta; dQ:
@@ -465,7 +475,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           tmem_ld_32x32b_x16(tmem + lanes + C::OUT_COL + c0, o);
           tmem_wait_ld_x16(o);
         }
-        out.put<BF16>(o, n > 0, back, c0, live ? a.dim : 0);
+        const bool put = live && dcheck(token < a.tokens_q, a.status, CHK_GLOBAL, token);
+        out.put<BF16>(o, n > 0, back, c0, put ? a.dim : 0);
       }
     }
   }
@@ -847,7 +858,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
           tmem_ld_32x32b_x32(tmem + lanes + C::OUT_COL + half * DP + q * 32, o);
           tmem_wait_ld_x32(o);
         }
-        out.put<BF16>(o, n > 0, back, q * 32, live ? a.dim : 0);
+        const bool put = live && dcheck(sk.start + key < a.tokens_k, a.status, CHK_GLOBAL, sk.start + key);
+        out.put<BF16>(o, n > 0, back, q * 32, put ? a.dim : 0);
       }
     }
   }
@@ -901,13 +913,16 @@ __global__ void __launch_bounds__(256)
 }
 
 // Parts of a launch of `ctas` CTAs whose longest runs over `rows` rows: as
-// many as give every SM a CTA, while each keeps at least 512 rows, and none
-// below 1536 rows, where the kernel that joins them costs more than the
-// shorter loop saves (forward, one head, us: 1024 keys 16.8 whole, 18.7 in two
-// parts; 2000 keys 28.5 and 20.3).
+// many as give every SM a CTA, while each keeps at least 256 rows, but not
+// below 1024 rows, where the kernel that joins them costs what the shorter
+// loops save, and not above 16, where its reading does (forward and backward,
+// one head, us: 512 rows 8.1 and 18.8 whole, 9.8 and 18.9 in parts; 768: 9.7
+// and 21.7, 10.3 and 19.7; 1024: 15.5 and 33.7, 13.4 and 28.6; 2000: 28.6 and
+// 55, 17.3 and 33.3; 64 queries over 8000 keys, four heads, in 15 parts 15.5
+// and 19.8, in 31 17.3 and 21.1).
 int attn_parts(int64_t ctas, int64_t rows, int sms) {
-  if (rows < 1536 || ctas < 1) return 1;
-  return (int)std::max<int64_t>(1, std::min<int64_t>((int64_t)sms / ctas, rows / 512));
+  if (rows < 1024 || ctas < 1) return 1;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({sms / ctas, rows / 256, 16}));
 }
 
 cudaError_t launch_attn_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArgs& args,

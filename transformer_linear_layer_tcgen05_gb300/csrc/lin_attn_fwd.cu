@@ -12,14 +12,27 @@
 //
 // A CTA runs two tiles of 128 queries of one head (one, where even so every
 // CTA has an SM to itself) against the same keys: 128 threads per tile (one
-// per row) take turns on the exponentials while the
-// tensor cores work for the other tile, and each K, V tile is read once for
-// 256 queries. The products of one thread execute in issue order, so S of
-// the next tile is issued right behind the P V that reads P out of the same
-// columns. Heads vary fastest over the grid and the causal mask's longest
-// query tiles come first. Where there are fewer CTAs than SMs the keys are cut
-// into parts, a CTA each, whose results a second kernel joins by their
-// log-sum-exps.
+// per row) take turns on the exponentials while the tensor cores work for the
+// other tile, and each K, V tile is read once for 256 queries. The products
+// of one thread execute in issue order, so S of the next tile is issued right
+// behind the P V that reads P out of the same columns; heads of up to 64
+// leave columns for P of its own, and S of the next tile then comes ahead of
+// it (8192 tokens, 16 heads: 148 -> 139 us). Heads vary fastest over the grid
+// and the causal mask's longest query tiles come first. Where there are fewer
+// CTAs than SMs the keys are cut into parts, a CTA each, whose results a
+// second kernel joins by their log-sum-exps.
+//
+// What bounds it. 8192 causal tokens, 32 heads of 128: 333-339 us, 1620-1650
+// TF/s, 0.84-0.85 of the cuBLAS burst rate, with the clock pulled down to
+// 1.75-1.87 GHz by the power limit: instructions cost time there even where
+// no unit is full. 2^x by a polynomial in place of every eighth to second one
+// of the special-function unit's: 360-406 us; two threads a row: 388; a
+// thread of its own for each tile's products: 377 (the two tiles' products
+// then alternate, and each waits for both). Heads of 64, 8192 tokens: 139 us,
+// 0.51 of that rate: the rows' own work (about 1100 cycles a tile of each
+// warp, half of it the 128 exponentials) comes to twice the products'. Short
+// calls are latency: 512 tokens, 12 heads 8.3 us of which four tiles' turns
+// are some 5.
 #include "lin_attn.cuh"
 
 #include <type_traits>
@@ -68,41 +81,44 @@ struct FwdCfg {
   static constexpr uint32_t p_col(int t) { return AHEAD ? 384 + t * 64 : S_COL + t * 128; }
 };
 
-// Key tiles that the queries [i0, i0 + 128) of a sequence need.
-__device__ __forceinline__ int fwd_key_tiles(int i0, int lq, int lk, int causal) {
+// Key tiles that the queries [i0, i0 + n) of a sequence need.
+__device__ __forceinline__ int fwd_key_tiles(int i0, int n, int lq, int lk, int causal) {
   if (i0 >= lq) return 0;
-  const int last = min(i0 + 127, lq - 1);
+  const int last = min(i0 + n, lq) - 1;
   const int hi = causal ? min(lk, last + lk - lq + 1) : lk;
   return hi > 0 ? (hi + 127) / 128 : 0;
 }
 
 }  // namespace
 
-// (the queries of a CTA are a parameter of the compiler's: read from the
-// arguments they cost the longest rows 2 %, 347 -> 353 us)
-template <int DP, bool BF16, int ROWS>
+// TILES of 128 rows to a CTA. PACKED: a row is query i of one of the `pack`
+// query heads that share a key head, tile_q queries of them all to a tile.
+// (These are the compiler's parameters: read from the arguments, the rows of
+// a CTA cost the longest problems 2 %, 347 -> 353 us.)
+template <int DP, bool BF16, int TILES, bool PACKED>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     lin_attn_fwd_kernel(const __grid_constant__ AttnFwdMaps maps,
                         const __grid_constant__ AttnFwdArgs args) {
   using C = FwdCfg<DP>;
   extern __shared__ uint8_t smem_raw[];
   const AttnArgs& a = args.s;
-  const int h = blockIdx.x;
+  const int pack = PACKED ? args.pack : 1, tile_q = PACKED ? args.tile_q : 128;
+  const int h0 = (int)blockIdx.x * pack;   // the first head of the CTA
   const PartOf at = part_of(blockIdx.z, args.parts);
   const int b = at.b;
   // longest rows of a causal mask first
-  const int i0 = (int)(gridDim.y - 1 - blockIdx.y) * ROWS;
+  const int i0 = (int)(gridDim.y - 1 - blockIdx.y) * (TILES * tile_q);
   const SeqRange sq = seq_range(a.cu_q, b, a.tokens_q, a.max_q);
   if (i0 >= sq.len) return;   // (the whole CTA)
   const SeqRange sk = seq_range(a.cu_k, b, a.tokens_k, a.max_k);
   // key tiles of the two query tiles, and of them those of this part, from j0 on
-  const int all0 = fwd_key_tiles(i0, sq.len, sk.len, a.causal);
-  const int all1 = ROWS > 128 ? fwd_key_tiles(i0 + 128, sq.len, sk.len, a.causal) : 0;
+  const int all0 = fwd_key_tiles(i0, tile_q, sq.len, sk.len, a.causal);
+  const int all1 = TILES > 1 ? fwd_key_tiles(i0 + tile_q, tile_q, sq.len, sk.len, a.causal) : 0;
   const int all = max(all0, all1);
   const int j0 = at.begin(all), j1 = at.end(all);
   const int n0 = max(min(all0, j1) - j0, 0), n1 = max(min(all1, j1) - j0, 0);
   const int n = max(n0, n1);
-  const int hk = h / a.group;
+  const int hk = h0 / a.group;
 
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const gen = smem_raw + (base - smem_u32(smem_raw));
@@ -132,11 +148,12 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     if (warp == kAttnCopyWarp) {
       if (lane == 0 && n > 0) {
         const int z = sq.start + i0;
+        const uint32_t q_bytes = PACKED ? AttnTile<DP>::SUB * (uint32_t)(pack * tile_q) * 128u : C::TILE;
         int k_issued = 0, v_issued = 0;
         bool second = false;
         if (n0 > 0) {   // (the first rows of a causal mask may see no key at all)
-          mbar_arrive_expect_tx(bar(C::Q_FULL), C::TILE);
-          load_tile<DP, 128>(base + C::OFF_Q, &maps.q, h, z, bar(C::Q_FULL));
+          mbar_arrive_expect_tx(bar(C::Q_FULL), q_bytes);
+          load_tile<DP, 128>(base + C::OFF_Q, &maps.q, h0, z, bar(C::Q_FULL));
         }
         for (int j = 0; j < n; ++j) {
           const int s = j % C::NKV, round = j / C::NKV;
@@ -146,8 +163,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                         bar(C::K_FULL + s));
           ++k_issued;
           if (j == 0 && n1 > 0) {
-            mbar_arrive_expect_tx(bar(C::Q_FULL + 1), C::TILE);
-            load_tile<DP, 128>(base + C::OFF_Q + C::TILE, &maps.q, h, z + 128, bar(C::Q_FULL + 1));
+            mbar_arrive_expect_tx(bar(C::Q_FULL + 1), q_bytes);
+            load_tile<DP, 128>(base + C::OFF_Q + C::TILE, &maps.q, h0, z + tile_q, bar(C::Q_FULL + 1));
             second = true;
           }
           if (round > 0 && !attn_wait(bar(C::V_EMPTY + s), (round - 1) & 1, ctl)) break;
@@ -250,8 +267,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     setmaxnreg_inc<kFwdRegsRow>();
     const int t = warp >> 2, row = tid & 127;
     const int nk = t ? n1 : n0;
-    const int i = i0 + t * 128 + row;   // query of the sequence
-    const bool live = i < sq.len && (ROWS > 128 || t == 0);
+    const int turn = PACKED ? row / pack : row;
+    const int h = PACKED ? h0 + row - turn * pack : h0;
+    const int i = i0 + t * tile_q + turn;   // query of the sequence
+    // (packed: the last rows of a tile may be nobody's)
+    const bool live = i < sq.len && t < TILES && (!PACKED || turn < tile_q);
     const float c = a.scale * kLog2E;
     // the last key that this row may see
     const int lim = live ? (a.causal ? min(sk.len - 1, i + sk.len - sq.len) : sk.len - 1) : -1;
@@ -370,7 +390,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const float x = __uint_as_float(o[g * 8 + 2 * e]), y = __uint_as_float(o[g * 8 + 2 * e + 1]);
             w[e] = nk > 0 ? pack16<BF16>(l == 0.0f ? 0.0f : x * inv, l == 0.0f ? 0.0f : y * inv) : 0u;
           }
-          if (!live || col >= a.dim) continue;
+          if (!live || col >= a.dim || !dcheck(token < a.tokens_q, a.status, CHK_GLOBAL, token)) continue;
           if (args.parts > 1) {   // in f32
             const float z = nk > 0 ? inv : 0.0f;
             float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
@@ -445,7 +465,8 @@ __global__ void __launch_bounds__(256)
 cudaError_t launch_attn_fwd(bool bf16, const AttnFwdMaps& maps, const AttnFwdArgs& args,
                             int heads_kv, int sequences, cudaStream_t stream) {
   const unsigned heads = (unsigned)(heads_kv * args.s.group);
-  const dim3 grid(heads, (unsigned)((args.s.max_q + args.rows - 1) / args.rows),
+  const int rows = args.tiles * args.tile_q;
+  const dim3 grid(heads / (unsigned)args.pack, (unsigned)((args.s.max_q + rows - 1) / rows),
                   (unsigned)sequences * (unsigned)args.parts);
   auto go = [&](auto kernel, uint32_t smem) {
     const cudaError_t e =
@@ -457,11 +478,14 @@ cudaError_t launch_attn_fwd(bool bf16, const AttnFwdMaps& maps, const AttnFwdArg
   auto types = [&](auto size) {
     constexpr int DP = decltype(size)::value;
     constexpr uint32_t smem = FwdCfg<DP>::SMEM;
-    if (args.rows == 128)
-      return bf16 ? go(lin_attn_fwd_kernel<DP, true, 128>, smem)
-                  : go(lin_attn_fwd_kernel<DP, false, 128>, smem);
-    return bf16 ? go(lin_attn_fwd_kernel<DP, true, 256>, smem)
-                : go(lin_attn_fwd_kernel<DP, false, 256>, smem);
+    if (args.tiles == 1)
+      return bf16 ? go(lin_attn_fwd_kernel<DP, true, 1, true>, smem)
+                  : go(lin_attn_fwd_kernel<DP, false, 1, true>, smem);
+    if (args.pack > 1)
+      return bf16 ? go(lin_attn_fwd_kernel<DP, true, 2, true>, smem)
+                  : go(lin_attn_fwd_kernel<DP, false, 2, true>, smem);
+    return bf16 ? go(lin_attn_fwd_kernel<DP, true, 2, false>, smem)
+                : go(lin_attn_fwd_kernel<DP, false, 2, false>, smem);
   };
   // (heads of 65 to 96 entries: a quarter less of both products than 128; 4096
   // causal tokens, 16 heads of 96: 52.2 -> 49.1 us)

@@ -258,9 +258,10 @@ bool overlaps(const void* a, uint64_t abytes, const void* b, uint64_t bbytes);
 lin_status cuda_fail(cudaError_t e);
 int sm_count(int dev);
 // Tensor map of a [tokens][heads][dim] tensor of 16-bit entries (strides in
-// bytes) in boxes of box_tokens x 1 head x 64 entries, 128-byte swizzle.
+// bytes) in boxes of box_tokens x box_heads x 64 entries, 128-byte swizzle.
 bool encode_heads(CUtensorMap* m, const void* base, uint64_t dim, uint64_t heads, uint64_t tokens,
-                  uint64_t head_bytes, uint64_t token_bytes, uint32_t box_tokens);
+                  uint64_t head_bytes, uint64_t token_bytes, uint32_t box_tokens,
+                  uint32_t box_heads);
 // Workspace in stream order from the library's pool (a graph memory node on
 // a stream under capture); null if there is none to be had. Given back by
 // cudaFreeAsync on the same stream.
