@@ -43,11 +43,14 @@ struct AttnBwdArgs {
   HeadsPtr o, dout;
   const float* lse;       // [heads_q][tokens_q]
   float* delta;           // [heads_q][tokens_q]: sum of dO * O of each row
-  float* norm;            // [sequences][heads_q][q tiles]: largest row norm of dO
+  float* norm;            // [sequences][heads_q >> shift][row tiles]: largest row norm of dO
   HeadsPtr dq, dk, dv;
   // parts of the keys for dQ and of the queries for dK, dV, and, where there
   // are several, their f32 sums [part][token][head][dim]
   int32_t q_parts, k_parts;
+  // log2 of the query heads that are rows of one tile: 1, or all that share a
+  // key head
+  int32_t shift;
   float *dq_part, *dk_part, *dv_part;
 };
 

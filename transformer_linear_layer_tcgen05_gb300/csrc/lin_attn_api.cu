@@ -119,15 +119,16 @@ lin_status attention(const lin_attention_shape* s, const lin_heads* Q, const lin
   auto tiles = [&] {
     return (c.max_q + a.tile_q - 1) / a.tile_q * (s->heads_q / a.pack) * s->sequences;
   };
-  // Short queries: the query heads that share a key head in one tile, where
-  // that makes fewer tiles (32 heads over 8 of 128, us: one query on 8192 keys
-  // 33 -> 17, 16 sequences of one on 2048 114 -> 31; where it makes no fewer,
-  // the tiles are as many and each reads one head's rows).
+  // The query heads that share a key head as rows of one tile, unless that
+  // makes more tiles (a number of heads that does not divide 128 leaves rows
+  // unused). 32 heads over 8 of 128, us: one query on 8192 keys 33 -> 17, 16
+  // sequences of one on 2048 114 -> 31, 8192 tokens 337 -> 335; nine sequences
+  // of 600, 12 heads over 6, 23.6 -> 20.2.
   if (a.s.group <= 128) {
     const int64_t apart = tiles();
     a.pack = a.s.group;
     a.tile_q = 128 / a.pack;
-    if (tiles() >= apart) a.pack = 1, a.tile_q = 128;
+    if (tiles() > apart) a.pack = 1, a.tile_q = 128;
   }
   // One tile to a CTA while every CTA then has an SM to itself (512 tokens, 12
   // heads: 10.3 -> 8.9 us); beyond that the second tile's exponentials hide
@@ -172,14 +173,6 @@ lin_status attention_backward(const lin_attention_shape* s, const lin_heads* Q, 
   const lin_status st = check_attention(s, v, 8, LSE, false, &c);
   if (st != LIN_SUCCESS) return st;
   if (c.nothing || (c.max_q == 0 && c.max_k == 0)) return LIN_SUCCESS;
-  lin::AttnBwdMaps maps;
-  const View& q = v[0].extent ? v[0] : v[1];   // (an empty side's maps are never used)
-  const View& k = v[1].extent ? v[1] : v[0];
-  const int box = lin::kAttnBwdBox;
-  const bool ok = encode_view(&maps.q, q, s->dim, box) && encode_view(&maps.k, k, s->dim, box) &&
-                  encode_view(&maps.v, v[2].extent ? v[2] : q, s->dim, box) &&
-                  encode_view(&maps.dout, v[4].extent ? v[4] : k, s->dim, box);
-  if (!ok) return cuda_fail(cudaErrorInvalidValue);
   lin::AttnBwdArgs a{};
   a.s = attn_args(s, c);
   a.q = heads_ptr(v[0]);
@@ -191,16 +184,36 @@ lin_status attention_backward(const lin_attention_shape* s, const lin_heads* Q, 
   a.dq = heads_ptr(v[5]);
   a.dk = heads_ptr(v[6]);
   a.dv = heads_ptr(v[7]);
-  const int64_t tq = (c.max_q + 127) / 128, tk = (c.max_k + 127) / 128;
+  // The query heads that share a key head as rows of one tile, where their
+  // number divides it: never more tiles, fewer where sequences end inside one,
+  // and fewer tokens of a tile behind a causal mask (us: nine sequences of up
+  // to 997, 12 heads over 6, 64.4 -> 59.9; 8192 tokens, 16 over 4, 632 -> 627;
+  // 16 sequences of one query on 2048 keys, 32 over 8, 252 -> 149).
+  const int group = a.s.group, turn = lin::kAttnBwdBox;
+  if (group <= turn && (group & (group - 1)) == 0 && c.max_q * group <= 65535LL * 128) {
+    while ((1 << a.shift) < group) ++a.shift;
+  }
+  const int64_t tq = ((c.max_q << a.shift) + 127) / 128, tk = (c.max_k + 127) / 128;
+  const int64_t hq_tiles = s->heads_q >> a.shift;
+  lin::AttnBwdMaps maps;
+  const View& q = v[0].extent ? v[0] : v[1];   // (an empty side's maps are never used)
+  const View& k = v[1].extent ? v[1] : v[0];
+  const View& dout = v[4].extent ? v[4] : k;
+  const int heads = 1 << a.shift;
+  const bool ok = encode_view(&maps.q, q, s->dim, turn / heads, heads) &&
+                  encode_view(&maps.k, k, s->dim, turn) &&
+                  encode_view(&maps.v, v[2].extent ? v[2] : q, s->dim, turn) &&
+                  encode_view(&maps.dout, dout, s->dim, turn / heads, heads);
+  if (!ok) return cuda_fail(cudaErrorInvalidValue);
   const int sms = sm_count(c.dev);
-  a.q_parts = lin::attn_parts(tq * s->heads_q * s->sequences, c.max_k, sms);
+  a.q_parts = lin::attn_parts(tq * hq_tiles * s->sequences, c.max_k, sms);
   a.k_parts = lin::attn_parts(tk * s->heads_kv * s->sequences, c.max_q * (int64_t)a.s.group, sms);
   // workspace: the parts' sums, delta [heads][tokens], then the largest dO
   // norms of the query tiles
   const uint64_t dq = a.q_parts > 1 ? (uint64_t)a.q_parts * s->tokens_q * s->heads_q * s->dim : 0;
   const uint64_t dk = a.k_parts > 1 ? (uint64_t)a.k_parts * s->tokens_k * s->heads_kv * s->dim : 0;
   const uint64_t delta = (uint64_t)s->heads_q * (uint64_t)s->tokens_q;
-  const uint64_t norms = (uint64_t)s->sequences * (uint64_t)s->heads_q * (uint64_t)tq;
+  const uint64_t norms = (uint64_t)s->sequences * (uint64_t)hq_tiles * (uint64_t)tq;
   const size_t bytes = (size_t)std::max<uint64_t>(16, (dq + 2 * dk + delta + norms) * 4);
   float* ws = static_cast<float*>(take_stream_workspace(c.dev, bytes, stream));
   if (!ws) return LIN_ERROR_CUDA;

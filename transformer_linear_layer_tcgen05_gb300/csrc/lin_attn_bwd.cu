@@ -68,7 +68,7 @@ constexpr int kTurn = 64;           // rows of a streamed tile
 template <int DP, int N_, int SUMS, bool OWN, int ROW_FLOATS>
 struct BwdCfg {
   static constexpr int N = N_;                   // stages
-  [[maybe_unused]] static constexpr bool kOwnSmem = OWN;
+  static constexpr bool kOwnSmem = OWN;
   using Tile = AttnTile<DP, kTurn>;
   static constexpr uint32_t TILE = Tile::BYTES;
   static constexpr int OWN_READY = 0;            // the CTA's own operands
@@ -89,7 +89,7 @@ struct BwdCfg {
   static constexpr uint32_t OFF_TMEM = BARS * 8, OFF_ABORT = OFF_TMEM + 4;
   static constexpr uint32_t OFF_RED = 448;       // 16 floats
   static_assert(OFF_ABORT + 4 <= OFF_RED, "barrier region");
-  [[maybe_unused]] static constexpr uint32_t OFF_OWN = 0;         // (tiles first: they want 1024-byte bases)
+  static constexpr uint32_t OFF_OWN = 0;         // (tiles first: they want 1024-byte bases)
   static constexpr uint32_t OFF_A = OWN ? 2 * AttnTile<DP>::BYTES : 0;
   static constexpr uint32_t OFF_B = OFF_A + N * TILE;
   // dK, dV: [N][kTurn] floats -L log2 e + 8, then [N][kTurn] -a delta; dQ:
@@ -184,28 +184,31 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     lin_attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps,
                        const __grid_constant__ AttnBwdArgs args) {
   using C = DqCfg<DP>;
+  static_assert(!C::kOwnSmem && C::OFF_OWN == 0, "own operands in tensor memory");
   extern __shared__ uint8_t smem_raw[];
   const AttnArgs& a = args.s;
-  const int h = blockIdx.x;
+  // rows i << shift | head of the CTA
+  const int shift = args.shift, h0 = (int)blockIdx.x << shift;
   const PartOf at = part_of(blockIdx.z, args.q_parts);
   const int b = at.b, part = at.part;
   const int qt = gridDim.y - 1 - blockIdx.y;   // longest rows of a causal mask first
-  const int i0 = qt * 128;
+  const int r0 = qt * 128;
   const SeqRange sq = seq_range(a.cu_q, b, a.tokens_q, a.max_q);
-  const int64_t norm_at = ((int64_t)b * a.heads_q + h) * gridDim.y + qt;
-  if (i0 >= sq.len) {   // (the whole CTA)
+  const int rows = sq.len << shift;
+  const int64_t norm_at = ((int64_t)b * gridDim.x + blockIdx.x) * gridDim.y + qt;
+  if (r0 >= rows) {   // (the whole CTA)
     if (threadIdx.x == 0 && part == 0) args.norm[norm_at] = 0.0f;
     return;
   }
   const SeqRange sk = seq_range(a.cu_k, b, a.tokens_k, a.max_k);
-  const int last = min(i0 + 127, sq.len - 1);
+  const int last = min(r0 + 127, rows - 1) >> shift;
   const int hi = a.causal ? min(sk.len, last + sk.len - sq.len + 1) : sk.len;
   const int tiles = hi > 0 ? (hi + kTurn - 1) / kTurn : 0;
   // this part's key tiles: j0 .. j0 + n - 1 (one or two stay together: see delta)
   const bool few = tiles <= 2;
   const int j0 = few ? 0 : at.begin(tiles);
   const int n = few ? (part == 0 ? tiles : 0) : at.end(tiles) - j0;
-  const int hk = h / a.group;
+  const int hk = h0 / a.group;
 
   if (!smem_aligned(smem_raw, a.status)) return;
   const uint32_t base = smem_u32(smem_raw);
@@ -312,7 +315,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     __syncwarp();
   } else if (warp < kRowWarps) {
     const int half = warp >> 2, row = tid & 127;
-    const int i = i0 + row;
+    const int i = (r0 + row) >> shift, h = h0 + (row & ((1 << shift) - 1));
     const bool live = i < sq.len;
     const int64_t token = sq.start + (live ? i : 0);
     const float c = a.scale * kLog2E;
@@ -505,15 +508,19 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   const SeqRange sk = seq_range(a.cu_k, b, a.tokens_k, a.max_k);
   if (k0 >= sk.len) return;   // (the whole CTA)
   const SeqRange sq = seq_range(a.cu_q, b, a.tokens_q, a.max_q);
-  // query tiles t0 .. t1 - 1 of each head of the group
+  // Rows i << shift | head of the group (shift 0: the heads one after another),
+  // in tiles t0 .. t1 - 1 of each pass over them.
+  const int shift = args.shift;
   const int off = sk.len - sq.len;   // causal: query i sees the keys up to i + off
-  const int t1 = (sq.len + kTurn - 1) / kTurn;
-  const int t0 = a.causal ? min(max(k0 - off, 0) / kTurn, t1) : 0;
+  const int rows = sq.len << shift;
+  const int t1 = (rows + kTurn - 1) / kTurn;
+  const int t0 = a.causal ? min((max(k0 - off, 0) << shift) / kTurn, t1) : 0;
   const int per = t1 - t0;
-  // this part's turns (of all heads' tiles): from .. from + n - 1
-  const int from = at.begin(per * a.group), n = at.end(per * a.group) - from;
-  const int tile0 = from > 0 ? from % per : 0;        // the first turn's tile of its head
-  const int q_left = sq.len - (t1 - 1) * kTurn;          // queries of the last tile
+  // this part's turns (of all passes' tiles): from .. from + n - 1
+  const int passes = a.group >> shift;
+  const int from = at.begin(per * passes), n = at.end(per * passes) - from;
+  const int tile0 = from > 0 ? from % per : 0;           // the first turn's tile of its pass
+  const int q_left = rows - (t1 - 1) * kTurn;            // rows of the last tile
   const int h0 = hk * a.group;
 
   if (!smem_aligned(smem_raw, a.status)) return;
@@ -551,10 +558,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   // done; the copies and the first products do not wait for that.
   auto scale_exponent = [&]() -> int {
     pdl_wait();
-    const int tiles = (a.max_q + 127) / 128;
-    const float* nm = args.norm + ((int64_t)b * a.heads_q + h0) * tiles;
+    const int norms = ((a.max_q << args.shift) + 127) / 128 * (a.group >> args.shift);
+    const float* nm = args.norm + ((int64_t)b * gridDim.x + hk) * norms;
     float big = 0.0f;
-    for (int i = lane; i < tiles * a.group; i += 32) big = fmaxf(big, nm[i]);
+    for (int i = lane; i < norms; i += 32) big = fmaxf(big, nm[i]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
     return norm_exponent(big);
@@ -580,7 +587,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         RingAt<C::N> r;
         int h = h0 + from / per, tile = tile0;   // of this turn (n > 0: per > 0)
         for (int it = 0; it < n; ++it, ++issued) {
-          const int z = sq.start + (t0 + tile) * kTurn;
+          const int z = sq.start + ((t0 + tile) * kTurn >> shift);
           if (it >= C::N && !attn_wait(bar(C::EMPTY + r.s), r.parity ^ 1, ctl)) break;
           mbar_arrive_expect_tx(bar(C::FULL + r.s), 2 * C::TILE);
           load_tile<DP, kTurn>(q_tile(r.s), &maps.q, h, z, bar(C::FULL + r.s));
@@ -613,8 +620,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     auto load = [&]() {
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        const int i = (t0 + tile) * kTurn + e * 32 + lane;
-        const int64_t at = (int64_t)h * a.tokens_q + sq.start + i;
+        const int r = (t0 + tile) * kTurn + e * 32 + lane, i = r >> shift;
+        const int64_t at =
+            (int64_t)(h + (r & ((1 << shift) - 1))) * a.tokens_q + sq.start + i;
         lse[e] = i < sq.len ? args.lse[at] : -INFINITY;
         delta[e] = i < sq.len ? args.delta[at] : 0.0f;
       }
@@ -743,7 +751,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     const float damp = ds_scale(ne);
     constexpr int NQ = kTurn / 32;   // groups of 32 columns of a thread
     bool ok = true;
-    int tile = per > 0 ? (tile0 + half) % per : 0;   // of its head
+    int tile = per > 0 ? (tile0 + half) % per : 0;   // of its pass
+    const int from_row = max(key - off, 0) << shift;
     RingAt<C::N> r;
     if (half) r.next();
     for (int it = half; it < n; it += 2) {   // the warpgroup's stream
@@ -781,8 +790,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
           x[2] = __float_as_uint(ex2_approx(v.x));
           x[3] = __float_as_uint(ex2_approx(v.y));
         }
-      // causal: the key meets the queries from key - off on
-      const int first = key - off - i0;
+      // causal: the key meets the queries from key - off on, the rows from_row on
+      const int first = from_row - i0;
       const bool cut = a.causal && __any_sync(0xffffffffu, first > 0);
       if (cut) {
 #pragma unroll
@@ -927,7 +936,7 @@ int attn_parts(int64_t ctas, int64_t rows, int sms) {
 
 cudaError_t launch_attn_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArgs& args,
                             int heads_kv, int sequences, int* kernels, cudaStream_t stream) {
-  const unsigned tq = (unsigned)((args.s.max_q + 127) / 128);
+  const unsigned tq = (unsigned)(((args.s.max_q << args.shift) + 127) / 128);
   const unsigned tk = (unsigned)((args.s.max_k + 127) / 128);
   const unsigned hq = (unsigned)(heads_kv * args.s.group), hk = (unsigned)heads_kv;
   const unsigned seqs = (unsigned)sequences;
@@ -951,7 +960,8 @@ cudaError_t launch_attn_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArg
     return cudaLaunchKernelEx(&cfg, kernel, maps, args);
   };
   auto both = [&](auto dq, uint32_t dq_smem, auto dkv, uint32_t dkv_smem) {
-    const cudaError_t e = go(dq, dq_smem, dim3(hq, tq, seqs * args.q_parts), kAttnThreads, false);
+    const cudaError_t e = go(dq, dq_smem, dim3(hq >> args.shift, tq, seqs * args.q_parts),
+                             kAttnThreads, false);
     if (e != cudaSuccess) return e;
     return go(dkv, dkv_smem, dim3(hk, tk, seqs * args.k_parts), kDkvThreads, tq > 0);
   };
