@@ -6,6 +6,9 @@ shared library next to this file. Object files go to ``_build/`` at the
 repository root. A rebuild happens only when a source or header is newer than
 the library.
 
+The same call builds ``_lin_calls.so``, the Python extension module of the
+short calls' marshalling (csrc/lin_calls.cpp), with the host compiler.
+
 ``build_library(checked=True)`` builds the same sources with
 ``-DLIN_DEVICE_CHECKS=1`` into ``liblin_checked.so`` (objects in
 ``_build/checked/``): the checked build, whose kernels check their shared
@@ -26,6 +29,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "liblin.so")
 CHECKED_LIB_PATH = os.path.join(PKG_DIR, "liblin_checked.so")
+CALLS_PATH = os.path.join(PKG_DIR, "_lin_calls.so")
 
 SOURCES = ["lin_api.cu", "lin_kernels_tf32.cu", "lin_kernels_f16.cu",
            "lin_kernels_cluster_swiglu.cu", "lin_kernels_cluster_cvt.cu",
@@ -46,18 +50,35 @@ def _nvcc() -> str:
 
 def _inputs() -> list[str]:
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)
-             if f.endswith((".cu", ".cuh", ".h"))]
+             if f.endswith((".cu", ".cuh", ".h", ".cpp"))]
     files.append(os.path.join(INCLUDE, "lin.h"))
     files.append(os.path.abspath(__file__))
     return files
 
 
 def up_to_date(checked: bool = False) -> bool:
-    lib = CHECKED_LIB_PATH if checked else LIB_PATH
-    if not os.path.exists(lib):
+    libs = [CHECKED_LIB_PATH] if checked else [LIB_PATH, CALLS_PATH]
+    if not all(os.path.exists(lib) for lib in libs):
         return False
-    t = os.path.getmtime(lib)
+    t = min(os.path.getmtime(lib) for lib in libs)
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def _calls_command(out: str, nvcc: str) -> list[str]:
+    """The host compiler's command for the extension module."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    inc = os.path.join(root, "include")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    return [os.environ.get("CXX", "g++"), "-O2", "-std=c++20", "-fPIC", "-shared", "-Wall",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", inc,
+            "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(cuda, "include"), os.path.join(CSRC, "lin_calls.cpp"),
+            "-o", out, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda"]
 
 
 def build_library(force: bool = False, verbose: bool = False, extra_flags=(),
@@ -83,6 +104,10 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags=(),
             print(" ".join(cmd), file=sys.stderr)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                             stderr=subprocess.STDOUT, text=True)))
+    if not checked:
+        procs.append(("lin_calls.cpp", subprocess.Popen(
+            _calls_command(CALLS_PATH + ".tmp", nvcc), stdout=subprocess.PIPE,
+            stderr=subprocess.STDOUT, text=True)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -91,7 +116,7 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags=(),
         if p.returncode != 0:
             failed.append(f"{src}:\n{out}")
     if failed:
-        raise RuntimeError("nvcc failed:\n" + "\n".join(failed))
+        raise RuntimeError("compilation failed:\n" + "\n".join(failed))
     tmp = lib_path + ".tmp"
     link = [nvcc, *ARCH, "-shared", "-o", tmp, *objs]
     if verbose:
@@ -100,6 +125,8 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags=(),
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout)
     os.replace(tmp, lib_path)
+    if not checked:
+        os.replace(CALLS_PATH + ".tmp", CALLS_PATH)
     return lib_path
 
 

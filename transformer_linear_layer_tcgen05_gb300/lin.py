@@ -14,15 +14,15 @@ Two layers:
   (M, N, K) from their shapes, call the C function on the current torch
   stream (or ``stream=``) and raise ``LinError`` on a non-zero status.
   Binary16 weights may be given as ``torch.float16``, ``torch.int16`` or
-  ``torch.uint16`` tensors (only the bit patterns are read).
+  ``torch.uint16`` tensors (only the bit patterns are read). The short calls
+  (attention, norms and rotation, distillation) marshal their tensors in the
+  extension module ``_lin_calls``.
 """
 
 from __future__ import annotations
 
 import ctypes
 import os
-import struct
-from array import array
 
 # LIN_CHECKED=1 loads the checked build (liblin_checked.so: the kernels check
 # their indices and report LIN_ERROR_DEVICE_CHECK; see include/lin.h).
@@ -94,10 +94,6 @@ SIGNATURES = {
 }
 
 
-# lin_attention_shape and lin_qk_norm_rope_shape, field by field
-_ATTENTION_SHAPE = struct.Struct("@ii qq qqq q qq PP f4x".replace(" ", ""))
-_QK_NORM_ROPE_SHAPE = struct.Struct("@iiqqqqqqf4x")
-
 LIN_BINARY16 = 0
 LIN_BFLOAT16 = 1
 
@@ -157,11 +153,9 @@ def check(fn: str, status: int) -> None:
 # ----------------------------------------------------------------- tensor layer
 
 def _stream_handle(stream):
+    import torch
     if stream is None:
-        # (current_stream() builds an object around this handle: 3 us of a
-        # call; the short calls below would feel it)
-        torch = _t()
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -406,91 +400,38 @@ def lin_gate_up_w16(X, WG16, WU16, GATE, UP, stream=None):
     return GATE, UP
 
 
-# ------------------------------------------------------------ 16-bit head tensors
+# ------------------------------------------------------------ short calls
 #
-# These calls are short, so their marshalling is too: one array of int64 for
-# all of a call's lin_heads (three fields of eight bytes each), packed bytes
-# for its shape, and torch looked up once.
+# Attention, norms and rotation, and distillation are short calls of many
+# tensors: their checks and marshalling are the extension module _lin_calls
+# (csrc/lin_calls.cpp, built beside the library), bound once to the library's
+# functions.
 
-_torch = None
-_DTYPE16 = {}
-
-
-def _t():
-    """torch, imported on first use (importing this module loads nothing)."""
-    global _torch
-    if _torch is None:
-        import torch
-        _DTYPE16.update({torch.float16: LIN_BINARY16, torch.bfloat16: LIN_BFLOAT16})
-        _torch = torch
-    return _torch
+_calls = None
 
 
-def _heads(tensors, names):
-    """(dtype, addresses, keep): the lin_heads of [tokens, heads, dim] CUDA
-    tensors of one 16-bit type (the last dimension contiguous; views of a
-    packed buffer are fine); `keep` holds the memory of the addresses."""
-    torch_tensor = _t().Tensor
-    first, fields = None, []
-    for t, name in zip(tensors, names):
-        if not isinstance(t, torch_tensor) or not t.is_cuda or t.dim() != 3:
-            raise TypeError(f"{name} must be a CUDA tensor [tokens, heads, dim]")
-        if first is None:
-            first = t.dtype
-        if t.dtype is not first or first not in _DTYPE16:
-            raise TypeError(f"{name} must be float16 or bfloat16, all of one type")
-        token, head, entry = t.stride()
-        if entry != 1 and t.shape[2] > 1:
-            raise ValueError(f"{name}: the entries of a head must be contiguous")
-        fields += (t.data_ptr(), token, head)
-    keep = array("q", fields)
-    base = keep.buffer_info()[0]
-    return _DTYPE16[first], range(base, base + 8 * len(fields), 24), keep
+def _short_calls():
+    global _calls
+    if _calls is None:
+        import torch  # noqa: F401  (loads what the module links to)
+        try:
+            from . import _lin_calls
+        except ImportError as e:
+            raise RuntimeError(
+                "_lin_calls.so is not built for this interpreter; build it with "
+                "transformer_linear_layer_tcgen05_gb300.build.build_library()") from e
+        L = lib()
+        _lin_calls.bind({name: ctypes.cast(getattr(L, name), _P).value for name in (
+            "lin_attention", "lin_attention_backward", "lin_qk_norm_rope",
+            "lin_qk_norm_rope_backward", "lin_distill_topk")})
+        _calls = _lin_calls
+    return _calls
 
 
-def _flat(t, name, shape, dtype):
-    """Address of a contiguous CUDA tensor of the given type and shape (None:
-    of any one dimension)."""
-    if not isinstance(t, _torch.Tensor) or t.dtype is not dtype or not t.is_cuda or \
-            not t.is_contiguous() or (t.shape != shape if shape is not None else
-                                      t.dim() != 1 or t.numel() < 1):
-        raise TypeError(f"{name} must be a contiguous {dtype} CUDA tensor" +
-                        (f" {list(shape)}" if shape is not None else ""))
-    return t.data_ptr()
-
-
-def _int32(t, name, shape):
-    return _flat(t, name, shape, _torch.int32)
-
-
-def _f32_flat(t, name, shape):
-    return _flat(t, name, shape, _torch.float32)
-
-
-def _attention_shape(dtype, Q, K, V, cu_q, cu_k, max_q, max_k, causal, scale):
-    tq, hq, d = Q.shape
-    tk, hk, dk = K.shape
-    if dk != d or V.shape != K.shape:
-        raise ValueError(f"shape mismatch: Q{tuple(Q.shape)} K{tuple(K.shape)} V{tuple(V.shape)}")
-    n = 1
-    if cu_q is None and cu_k is None:
-        max_q, max_k, cu_q, cu_k = tq, tk, 0, 0
-    else:
-        if cu_q is None or cu_k is None:
-            raise ValueError("cu_q and cu_k go together")
-        if max_q is None or max_k is None:
-            raise ValueError("packed sequences need max_q and max_k")
-        n = cu_k.numel() - 1
-        if cu_q.numel() != n + 1:
-            raise ValueError("cu_q and cu_k must have the same number of entries")
-        cu_q, cu_k = _int32(cu_q, "cu_q", None), _int32(cu_k, "cu_k", None)
-    return _ATTENTION_SHAPE.pack(dtype, 1 if causal else 0, tq, tk, hq, hk, d, n, max_q, max_k,
-                                 cu_q, cu_k, d ** -0.5 if scale is None else scale)
-
-
-def _same_shape(t, name, like):
-    if t.shape != like.shape:
-        raise ValueError(f"{name} must be {list(like.shape)}")
+def _handle(stream):
+    """A stream's handle; None (torch's current stream) is looked up by the
+    module itself."""
+    return stream if stream is None or isinstance(stream, int) else stream.cuda_stream
 
 
 def lin_attention(Q, K, V, O, LSE, cu_q=None, cu_k=None, max_q=None, max_k=None, causal=True,
@@ -503,50 +444,19 @@ def lin_attention(Q, K, V, O, LSE, cu_q=None, cu_k=None, max_q=None, max_k=None,
     offsets of packed sequences (with their longest lengths max_q, max_k),
     else one sequence. ``scale`` defaults to dim ** -0.5; ``causal`` counts
     from the end (the last query sees every key)."""
-    dtype, h, keep = _heads((Q, K, V, O), "QKVO")
-    shape = _attention_shape(dtype, Q, K, V, cu_q, cu_k, max_q, max_k, causal, scale)
-    _same_shape(O, "O", Q)
-    _call("lin_attention", shape, *h,
-          _f32_flat(LSE, "LSE", (Q.shape[1], Q.shape[0])), _stream_handle(stream))
+    check("lin_attention", (_calls or _short_calls()).attention(
+        Q, K, V, O, LSE, cu_q, cu_k, max_q, max_k, causal, scale, _handle(stream)))
     return O, LSE
-
-
-_BACKWARD_NAMES = ("Q", "K", "V", "O", "dO", "dQ", "dK", "dV")
 
 
 def lin_attention_backward(Q, K, V, O, LSE, DO, DQ, DK, DV, cu_q=None, cu_k=None, max_q=None,
                            max_k=None, causal=True, scale=None, stream=None):
     """dQ, dK, dV of lin_attention from dO and that call's inputs and results
     (dK and dV summed over the query heads that share a key head)."""
-    dtype, h, keep = _heads((Q, K, V, O, DO, DQ, DK, DV), _BACKWARD_NAMES)
-    shape = _attention_shape(dtype, Q, K, V, cu_q, cu_k, max_q, max_k, causal, scale)
-    for t, name in ((O, "O"), (DO, "dO"), (DQ, "dQ")):
-        _same_shape(t, name, Q)
-    for t, name in ((DK, "dK"), (DV, "dV")):
-        _same_shape(t, name, K)
-    _call("lin_attention_backward", shape, *h[:4],
-          _f32_flat(LSE, "LSE", (Q.shape[1], Q.shape[0])), *h[4:], _stream_handle(stream))
+    check("lin_attention_backward", (_calls or _short_calls()).attention_backward(
+        Q, K, V, O, LSE, DO, DQ, DK, DV, cu_q, cu_k, max_q, max_k, causal, scale,
+        _handle(stream)))
     return DQ, DK, DV
-
-
-def _qk_norm_rope_args(X, wq, wk, COS, SIN, positions, Q, K, V, eps, interleaved, names):
-    dtype, h, keep = _heads((Q, K, V), names)
-    t, hq, d = Q.shape
-    hk = K.shape[1]
-    if K.shape != (t, hk, d) or V.shape != K.shape or \
-            _f32(X, "X").shape != (t, (hq + 2 * hk) * d):
-        raise ValueError(f"shape mismatch: X{tuple(X.shape)} " + " ".join(
-            f"{n}{tuple(x.shape)}" for n, x in zip(names, (Q, K, V))))
-    rot = rows = 0
-    cos = sin = None
-    if COS is not None or SIN is not None:
-        rows, half = _f32(COS, "COS").shape
-        cos, sin = COS.data_ptr(), _f32_flat(SIN, "SIN", (rows, half))
-        rot = 2 * half
-    pos = None if positions is None else _int32(positions, "positions", (t,))
-    shape = _QK_NORM_ROPE_SHAPE.pack(dtype, 1 if interleaved else 0, t, hq, hk, d, rot, rows, eps)
-    return keep, (shape, X.data_ptr(), _f32_flat(wq, "wq", (d,)),
-                  _f32_flat(wk, "wk", (d,)), cos, sin, pos, *h)
 
 
 def lin_qk_norm_rope(X, wq, wk, COS, SIN, positions, Q, K, V, eps=1e-6, interleaved=False,
@@ -559,32 +469,18 @@ def lin_qk_norm_rope(X, wq, wk, COS, SIN, positions, Q, K, V, eps=1e-6, interlea
     K, V [tokens, key heads, dim] float16 or bfloat16, views of a packed
     buffer allowed; COS, SIN [rows, rot / 2] float32 (None: no rotation);
     positions int32 [tokens], rows of the tables (None: 0, 1, ...)."""
-    keep, args = _qk_norm_rope_args(X, wq, wk, COS, SIN, positions, Q, K, V, eps, interleaved,
-                                    "QKV")
-    _call("lin_qk_norm_rope", *args, _stream_handle(stream))
+    check("lin_qk_norm_rope", (_calls or _short_calls()).qk_norm_rope(
+        X, wq, wk, COS, SIN, positions, Q, K, V, eps, interleaved, _handle(stream)))
     return Q, K, V
 
 
 def lin_qk_norm_rope_backward(X, wq, wk, COS, SIN, positions, DQ, DK, DV, DX, dwq, dwk, eps=1e-6,
                               interleaved=False, stream=None):
     """dX, dwq, dwk of lin_qk_norm_rope from dQ, dK, dV."""
-    keep, args = _qk_norm_rope_args(X, wq, wk, COS, SIN, positions, DQ, DK, DV, eps, interleaved,
-                                    ("dQ", "dK", "dV"))
-    d = DQ.shape[2]
-    _call("lin_qk_norm_rope_backward", *args, _f32_flat(DX, "dX", X.shape),
-          _f32_flat(dwq, "dwq", (d,)), _f32_flat(dwk, "dwk", (d,)), _stream_handle(stream))
+    check("lin_qk_norm_rope_backward", (_calls or _short_calls()).qk_norm_rope_backward(
+        X, wq, wk, COS, SIN, positions, DQ, DK, DV, eps, interleaved, DX, dwq, dwk,
+        _handle(stream)))
     return DX, dwq, dwk
-
-
-def _f32_rows(t, name, shape=None):
-    """A float32 CUDA matrix with contiguous rows, any row stride."""
-    torch = _t()
-    if not isinstance(t, torch.Tensor) or t.dtype != torch.float32 or not t.is_cuda or t.dim() != 2:
-        raise TypeError(f"{name} must be a float32 CUDA matrix")
-    if (t.shape[1] > 1 and t.stride(1) != 1) or (shape is not None and t.shape != shape):
-        raise ValueError(f"{name} must have contiguous rows" +
-                         (f" and the shape {tuple(shape)}" if shape is not None else ""))
-    return t
 
 
 def lin_distill_topk(LOGITS, ids, teacher, DLOGITS, losses, loss_sum, temperature=1.0,
@@ -597,17 +493,9 @@ def lin_distill_topk(LOGITS, ids, teacher, DLOGITS, losses, loss_sum, temperatur
     LOGITS [M, V] float32 (any row stride); ids, teacher [M, K] int32 and
     float32 (an id outside [0, V): an empty place); DLOGITS like LOGITS,
     LOGITS itself, or None (the losses alone); losses [M], loss_sum [1]."""
-    M, V = _f32_rows(LOGITS, "logits").shape
-    K = ids.shape[-1] if isinstance(ids, _torch.Tensor) and ids.dim() == 2 else 0
-    i = _int32(ids, "ids", (M, K))
-    d, ldd = None, 0
-    if DLOGITS is not None:
-        d = _f32_rows(DLOGITS, "dlogits", LOGITS.shape).data_ptr()
-        ldd = DLOGITS.stride(0)
-    _call("lin_distill_topk", LOGITS.data_ptr(), LOGITS.stride(0), i,
-          _f32_flat(teacher, "teacher", (M, K)), d, ldd, _f32_flat(losses, "losses", (M,)),
-          _f32_flat(loss_sum, "loss_sum", (1,)), M, V, K, temperature, inv_norm,
-          _stream_handle(stream))
+    check("lin_distill_topk", (_calls or _short_calls()).distill_topk(
+        LOGITS, ids, teacher, DLOGITS, losses, loss_sum, temperature, inv_norm,
+        _handle(stream)))
     return DLOGITS, losses, loss_sum
 
 
