@@ -385,3 +385,37 @@ def test_many_heads_and_sequences():
     t = _setup("bfloat16", lens, 6, 3, 64, seed=23)
     _run(t, lens, True)
     _check(t, lens, True, 0.125, UNIT["bfloat16"])
+
+
+# (lengths, query heads, key heads, dim): the query heads of a key head as rows
+# of one tile. Numbers of heads that divide a tile and that do not (3, 5, 48:
+# rows of a tile that are nobody's, and the heads apart in the gradient), all
+# rows of one token (128), more heads than rows (130: apart), one query on many
+# keys, sequences that end inside a tile of the packed rows, and enough of them
+# for two tiles to a CTA
+SHARED = [([(1, 700)], 32, 8, 128), ([(5, 40), (1, 1), (43, 129), (0, 7), (86, 300)], 9, 3, 64),
+          ([(31, 31), (33, 200), (2, 0)], 10, 2, 96), ([(3, 260), (1, 9)], 48, 1, 64),
+          ([(2, 150)], 128, 1, 40), ([(2, 90)], 130, 1, 64), ([(70, 70), (9, 130)], 64, 1, 80),
+          ([(17 + 3 * i, 60 + 5 * i) for i in range(24)], 16, 4, 64),
+          ([(1, 2100), (3, 40)], 12, 3, 128)]
+
+
+@pytest.mark.parametrize("shape", SHARED, ids=lambda s: f"{len(s[0])}h{s[1]}x{s[2]}d{s[3]}")
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("layout", ["packed", "heads"])
+def test_shared_heads_of_short_queries(shape, causal, layout):
+    lens, hq, hk, d = shape
+    dtype = "bfloat16" if layout == "heads" else "float16"
+    t = _setup(dtype, lens, hq, hk, d, seed=hq + d, layout=layout)
+    _run(t, lens, causal)
+    _check(t, lens, causal, d ** -0.5, UNIT[dtype])
+
+
+@pytest.mark.parametrize("dim", [72, 96, 104])
+def test_head_sizes_between_the_products(dim):
+    # a long one of each width that the products run over, with parts and
+    # without, beside one that ends inside a turn of 64 rows
+    lens = [(1100, 1100), (65, 190)]
+    t = _setup("bfloat16", lens, 2, 1, dim, seed=dim)
+    _run(t, lens, True)
+    _check(t, lens, True, dim ** -0.5, UNIT["bfloat16"])

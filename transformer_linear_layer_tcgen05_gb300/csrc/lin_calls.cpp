@@ -171,8 +171,8 @@ lin_attention_shape attention_shape(const Heads& h, const at::Tensor& q, const a
   return s;
 }
 
-// Runs `call` (the library, without the interpreter's lock) behind the checks
-// of `prepare`, and gives its status.
+// The status that `body` (a call's checks and the call) gives, as a Python
+// number; its errors as Python exceptions.
 template <typename Body>
 PyObject* guarded(Py_ssize_t n, Py_ssize_t want, Body&& body) {
   if (n != want) {
@@ -188,6 +188,7 @@ PyObject* guarded(Py_ssize_t n, Py_ssize_t want, Body&& body) {
     return nullptr;
   }
 }
+// The library's function without the interpreter's lock.
 template <typename F, typename... A>
 lin_status unlocked(F* f, A... a) {
   lin_status st;
@@ -326,18 +327,20 @@ PyObject* distill_topk(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// {name: address} of the library's functions
+// {name: address} of the library's functions: all of them, or none is taken.
 PyObject* bind(PyObject*, PyObject* addresses) {
+  void* got[5];
   for (int i = 0; i < 5; ++i) {
     PyObject* v = PyMapping_GetItemString(addresses, kNames[i]);
     if (!v) return nullptr;
-    g_address[i] = PyLong_AsVoidPtr(v);
+    got[i] = PyLong_AsVoidPtr(v);
     Py_DECREF(v);
-    if (!g_address[i]) {
+    if (!got[i]) {
       if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, kNames[i]);
       return nullptr;
     }
   }
+  for (int i = 0; i < 5; ++i) g_address[i] = got[i];
   Py_RETURN_NONE;
 }
 
