@@ -192,3 +192,21 @@ def test_refusals():
         lin.lin_distill_topk(zd, idd, td[:, :4], None, losses, total)
     with pytest.raises(ValueError):
         lin.lin_distill_topk(zd, idd, td, torch.empty(64, 4, device="cuda").t(), losses, total)
+
+
+# rows of one, two and four warps at the edges between them, and so many rows
+# that a CTA walks over several
+@pytest.mark.parametrize("m,v,k", [(40, 1020, 9), (40, 1024, 9), (40, 1027, 9), (7000, 1999, 3),
+                                   (40, 2044, 40), (40, 2048, 40), (40, 2051, 40), (5000, 1030, 5),
+                                   (40, 4100, 3), (2500, 4090, 5)])
+def test_widths_of_a_row(m, v, k):
+    import torch
+    z, ids, t = _inputs(m, v, k, seed=m + v)
+    zd, idd, td = _device(z, ids, t, v)
+    out = torch.full((m, v), 7.0, device="cuda")
+    losses, total = torch.full((m,), float("nan"), device="cuda"), torch.ones(1, device="cuda")
+    lin.lin_distill_topk(zd, idd, td, out, losses, total, 1.5, 0.5)
+    torch.cuda.synchronize()
+    assert lin.lin_get_device_status() == lin.LIN_SUCCESS
+    _check(z, ids, t, 1.5, 0.5, out.double().cpu().numpy(), losses.double().cpu().numpy(),
+           total.item())

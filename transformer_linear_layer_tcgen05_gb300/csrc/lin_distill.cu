@@ -47,7 +47,7 @@ constexpr float kLowest = -3.402823466e+38f;
 // CTAs that an SM's registers are to hold, the 16-byte units of a slot, and a
 // CTA's threads (the last warp has the teacher's entries).
 __host__ __device__ constexpr int distill_ctas(int warps) {
-  return warps == 8 ? 4 : warps == 4 ? 7 : 16;
+  return warps == 8 ? 4 : warps == 4 ? 7 : warps == 2 ? 12 : 16;
 }
 __host__ __device__ constexpr int distill_units(int warps) {
   return warps == 8 ? 4096 : warps * 256;
@@ -559,8 +559,12 @@ cudaError_t launch_distill(const DistillArgs& a, float* loss_sum, int sms, cudaS
   const bool whole = a.ld % 4 == 0 && (reinterpret_cast<uintptr_t>(a.logits) & 15u) == 0;
   const int64_t units = whole ? (a.V + 3) / 4 : (a.V + 6) / 4;
   // Rows share an SM as far as they fit, so that the waits of one row are
-  // filled by others: as few warps to a row as hold it.
+  // filled by others: as few warps to a row as hold it (16384 rows of 2048 by
+  // two warps 56 us, by four 72; of 8000 by eight 174, by four in clusters of
+  // two 221; more CTAs of one or two warps to an SM would spill: 16384 rows of
+  // 1000 45 us in 16 CTAs, 50 in 20).
   cudaError_t e = units <= distill_units(1)   ? launch_rows<1>(a, units, sms, stream)
+                  : units <= distill_units(2) ? launch_rows<2>(a, units, sms, stream)
                   : units <= distill_units(4) ? launch_rows<4>(a, units, sms, stream)
                                               : launch_rows<8>(a, units, sms, stream);
   if (e != cudaSuccess) return e;
