@@ -419,3 +419,33 @@ def test_head_sizes_between_the_products(dim):
     t = _setup("bfloat16", lens, 2, 1, dim, seed=dim)
     _run(t, lens, True)
     _check(t, lens, True, dim ** -0.5, UNIT["bfloat16"])
+
+
+@pytest.mark.parametrize("hq", [64, 128])
+def test_more_queries_than_a_grid_has_packed_tiles(hq):
+    # tiles of one or two queries would be more than the 65535 of a grid
+    import torch
+    g = torch.Generator(device="cuda")
+    g.manual_seed(31)
+    n, d, tk = 132_000, 8, 5
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").half()  # noqa: E731
+    q, k, v, do = rnd(n, hq, d), rnd(tk, 1, d), rnd(tk, 1, d), rnd(n, hq, d)
+    o, dq = torch.empty_like(q), torch.empty_like(q)
+    dk, dv = torch.empty_like(k), torch.empty_like(v)
+    lse = torch.empty(hq, n, device="cuda")
+    lin.lin_attention(q, k, v, o, lse, causal=False)
+    lin.lin_attention_backward(q, k, v, o, lse, do, dq, dk, dv, causal=False)
+    torch.cuda.synchronize()
+    assert lin.lin_get_device_status() == lin.LIN_SUCCESS
+    u, e = UNIT["float16"], 2.0 ** -14
+    k64, v64 = k[:, 0].double(), v[:, 0].double()
+    for at in (slice(0, 300), slice(65_400, 65_700), slice(n - 300, n)):
+        p = torch.softmax(q[at].double() @ k64.T * d ** -0.5, -1)
+        want = p @ v64
+        assert torch.all((o[at] - want).abs() <= u * want.abs() + (u + e) * (p @ v64.abs()) + 1e-6)
+        dp = do[at].double() @ v64.T
+        ds = p * (dp - (p * dp).sum(-1, keepdim=True))
+        want = ds @ k64 * d ** -0.5
+        size = (p * (dp.abs() + (do[at].double() * o[at].double()).abs().sum(-1, keepdim=True))) \
+            @ k64.abs() * d ** -0.5
+        assert torch.all((dq[at] - want).abs() <= u * want.abs() + (u + e) * size + 1e-6)

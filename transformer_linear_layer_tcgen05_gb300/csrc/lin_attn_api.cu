@@ -128,7 +128,8 @@ lin_status attention(const lin_attention_shape* s, const lin_heads* Q, const lin
     const int64_t apart = tiles();
     a.pack = a.s.group;
     a.tile_q = 128 / a.pack;
-    if (tiles() > apart) a.pack = 1, a.tile_q = 128;
+    // (a grid has 65535 tiles of queries at most)
+    if (tiles() > apart || c.max_q > 65535LL * a.tile_q) a.pack = 1, a.tile_q = 128;
   }
   // One tile to a CTA while every CTA then has an SM to itself (512 tokens, 12
   // heads: 10.3 -> 8.9 us); beyond that the second tile's exponentials hide
