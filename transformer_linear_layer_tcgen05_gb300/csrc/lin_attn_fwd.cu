@@ -17,7 +17,8 @@
 // of one thread execute in issue order, so S of the next tile is issued right
 // behind the P V that reads P out of the same columns; heads of up to 64
 // leave columns for P of its own, and S of the next tile then comes ahead of
-// it (8192 tokens, 16 heads: 148 -> 139 us). Heads vary fastest over the grid
+// it (8192 tokens, 16 heads: 148 -> 139 us; both tiles' S ahead of either P V
+// brings their exponentials into step: 146). Heads vary fastest over the grid
 // and the causal mask's longest query tiles come first. Where there are fewer
 // CTAs than SMs the keys are cut into parts, a CTA each, whose results a
 // second kernel joins by their log-sum-exps.
