@@ -1184,6 +1184,7 @@ lin_status lin_selftest_wait_timeout(int64_t timeout_us, lin_stream_t stream) {
   return read_and_clear_status(s);
 }
 
-int lin_version(void) { return 200; }   // 0.2.0: backward, loss, gate/up and host-operand entry points
+// 0.3.0: attention, norms and rotation of the heads, distillation
+int lin_version(void) { return 300; }
 
 }  // extern "C"
