@@ -1,0 +1,47 @@
+"""lin_distill_topk over many rows: rows that a CTA takes one after another.
+Bounds as in test_distill_gpu.py.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import step_oracle as so
+from tests.gpu_util import require_gpu
+from tests.test_distill_gpu import E, _device, _inputs
+from transformer_linear_layer_tcgen05_gb300 import lin
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    require_gpu()
+
+
+def _results(m, v, ld):
+    import torch
+    return (torch.full((m, ld), 7.0, device="cuda")[:, :v],
+            torch.full((m,), float("nan"), device="cuda"), torch.ones(1, device="cuda"))
+
+
+# Rows that one CTA takes one after another, of one, two, four and eight warps:
+# the losses alone have no barrier of the gradient's between them.
+@pytest.mark.parametrize("m,v,k", [(9000, 1000, 4), (9000, 1030, 4), (6000, 2051, 4), (3000, 4100, 9),
+                                   (3000, 8000, 9), (1500, 16384, 33), (1500, 16001, 3)])
+def test_the_losses_alone_of_many_rows(m, v, k):
+    import torch
+    z, ids, t = _inputs(m, v, k, seed=m + v)
+    zd, idd, td = _device(z, ids, t, v)
+    dz, losses, total = _results(m, v, v)
+    lin.lin_distill_topk(zd, idd, td, dz, losses, total, 1.5, 0.5)
+    torch.cuda.synchronize()
+    some = np.linspace(0, m - 1, 40).astype(int)
+    want, _ = so.distill_topk(z[some], ids[some], t[some], 1.5, 0.5)
+    got = losses.double().cpu().numpy()
+    # (z and p: tens at most, terms of 2^-17 of them)
+    assert np.all(np.abs(got[some] - want) <= E * 1.5 ** 2 * 120)
+    for _ in range(10):
+        _, l2, s2 = _results(m, v, v)
+        lin.lin_distill_topk(zd, idd, td, None, l2, s2, 1.5, 0.5)
+        assert torch.equal(l2, losses) and torch.equal(s2, total)
+    assert lin.lin_get_device_status() == lin.LIN_SUCCESS

@@ -39,6 +39,9 @@ constexpr int kMaxCluster = 16;          // CTAs along a row
 constexpr int kExch = 4;                 // rows whose exchange may be under way (a peer is at
                                          // most three ahead)
 constexpr int kEnt = 3;                  // rows whose entries are held
+constexpr int kRed = 3;                  // rows whose warps' (m, s) are held: a warp may write the
+                                         // next row's while another reads the one before last, and
+                                         // only the barrier between two rows' writes parts them
 constexpr int kChunk = 4;                // 16-byte units of a thread in registers at once
 constexpr float kDLog2E = 1.4426950408889634f;
 constexpr float kDLn2 = 0.6931471805599453f;
@@ -93,7 +96,7 @@ __global__ void __launch_bounds__(distill_threads(WARPS), distill_ctas(WARPS))
     lin_distill_kernel(const __grid_constant__ DistillArgs a) {
   constexpr int MAIN = WARPS * 32;
   __shared__ __align__(8) uint64_t bars[kSlots + kExch + 2 * kEnt];
-  __shared__ float2 red[2][WARPS];
+  __shared__ float2 red[kRed][WARPS];   // (m, s) of each warp
   __shared__ float2 stats[kExch][kMaxCluster];   // (m, s) of each CTA of the cluster
   __shared__ float4 teacher[kEnt];       // sum p log2 p, sum p z, whether the row has an entry
   __shared__ volatile int abort;
@@ -348,7 +351,7 @@ __global__ void __launch_bounds__(distill_threads(WARPS), distill_ctas(WARPS))
       }
     }
     warp_join(m, s, c);
-    if (lane == 0) red[it & 1][warp] = make_float2(m, s);
+    if (lane == 0) red[it % kRed][warp] = make_float2(m, s);
     named_bar_sync(1, MAIN);
     if (!a.dlogits && !twice && tid == 0 && ok)   // (the losses alone: the row is done with)
       for (int seg = 0; seg < S; ++seg) issue();
@@ -356,8 +359,8 @@ __global__ void __launch_bounds__(distill_threads(WARPS), distill_ctas(WARPS))
       // (before the exchange: a peer may overwrite the row behind it, and
       // this CTA's teacher warp has to have read its logits by then)
       ok = ok && warp_wait_phase(ent_full + 8 * (it % kEnt), (it / kEnt) & 1, ctl);
-      m = lane < WARPS ? red[it & 1][lane].x : kLowest;
-      s = lane < WARPS ? red[it & 1][lane].y : 0.0f;
+      m = lane < WARPS ? red[it % kRed][lane].x : kLowest;
+      s = lane < WARPS ? red[it % kRed][lane].y : 0.0f;
       warp_join(m, s, c);
       if (lane < C && ok) {
         const int e = it % kExch;
@@ -379,8 +382,8 @@ __global__ void __launch_bounds__(distill_threads(WARPS), distill_ctas(WARPS))
       m = lane < C ? stats[e][lane].x : kLowest;
       s = lane < C ? stats[e][lane].y : 0.0f;
     } else {
-      m = lane < WARPS ? red[it & 1][lane].x : kLowest;
-      s = lane < WARPS ? red[it & 1][lane].y : 0.0f;
+      m = lane < WARPS ? red[it % kRed][lane].x : kLowest;
+      s = lane < WARPS ? red[it % kRed][lane].y : 0.0f;
     }
     warp_join(m, s, c);   // (each warp by itself, in the same order)
     const float ls = log2f(s);   // the row's log-sum-exp less its maximum, base 2
