@@ -506,7 +506,12 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   const int b = at.b, part = at.part;
   const int k0 = blockIdx.y * 128;   // a causal mask's first keys meet the most queries
   const SeqRange sk = seq_range(a.cu_k, b, a.tokens_k, a.max_k);
-  if (k0 >= sk.len) return;   // (the whole CTA)
+  if (k0 >= sk.len) {   // (the whole CTA)
+    // The grid's end has to stand for the dQ kernel's too, for whatever waits
+    // for it next, even where no CTA of it has a key.
+    pdl_wait();
+    return;
+  }
   const SeqRange sq = seq_range(a.cu_q, b, a.tokens_q, a.max_q);
   // Rows i << shift | head of the group (shift 0: the heads one after another),
   // in tiles t0 .. t1 - 1 of each pass over them.
