@@ -1,5 +1,5 @@
-"""lin_distill_topk over many rows: rows that a CTA takes one after another.
-Bounds as in test_distill_gpu.py.
+"""lin_distill_topk over many rows, which a CTA takes one after another, and over
+long rows beside many entries. Bounds as in test_distill_gpu.py.
 """
 
 import numpy as np
@@ -7,7 +7,7 @@ import pytest
 
 from oracle import step_oracle as so
 from tests.gpu_util import require_gpu
-from tests.test_distill_gpu import E, _device, _inputs
+from tests.test_distill_gpu import E, _check, _device, _inputs
 from transformer_linear_layer_tcgen05_gb300 import lin
 
 pytestmark = pytest.mark.gpu
@@ -44,4 +44,26 @@ def test_the_losses_alone_of_many_rows(m, v, k):
         _, l2, s2 = _results(m, v, v)
         lin.lin_distill_topk(zd, idd, td, None, l2, s2, 1.5, 0.5)
         assert torch.equal(l2, losses) and torch.equal(s2, total)
+    assert lin.lin_get_device_status() == lin.LIN_SUCCESS
+
+
+# Rows of three parts and more (up to 48 CTA's parts of 4096 units, streamed
+# twice beyond that), beside few entries and beside as many as there may be.
+@pytest.mark.parametrize("m,v,k", [(2, 786432, 1024), (2, 786430, 970), (3, 1048576, 1024),
+                                   (2, 1048573, 5), (2, 800001, 64), (2, 600000, 1024)])
+def test_long_rows_and_many_entries(m, v, k):
+    import torch
+    z, ids, t = _inputs(m, v, k, seed=v + k)
+    zd, idd, td = _device(z, ids, t, v)
+    dz, losses, total = _results(m, v, v)
+    lin.lin_distill_topk(zd, idd, td, dz, losses, total, 2.0, 0.5)
+    torch.cuda.synchronize()
+    assert lin.lin_get_device_status() == lin.LIN_SUCCESS
+    _check(z, ids, t, 2.0, 0.5, dz.double().cpu().numpy(), losses.double().cpu().numpy(),
+           total.item())
+    _, l2, s2 = _results(m, v, v)
+    lin.lin_distill_topk(zd, idd, td, None, l2, s2, 2.0, 0.5)
+    assert torch.equal(l2, losses) and torch.equal(s2, total)
+    lin.lin_distill_topk(zd, idd, td, zd, l2, s2, 2.0, 0.5)
+    assert torch.equal(zd, dz) and torch.equal(l2, losses)
     assert lin.lin_get_device_status() == lin.LIN_SUCCESS

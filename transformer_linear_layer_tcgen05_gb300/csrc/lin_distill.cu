@@ -34,11 +34,8 @@ namespace lin {
 
 namespace {
 
-constexpr int kSlots = 3;                // parts of a row in shared memory, at most
-constexpr int kMaxCluster = 16;          // CTAs along a row
 constexpr int kExch = 4;                 // rows whose exchange may be under way (a peer is at
                                          // most three ahead)
-constexpr int kEnt = 3;                  // rows whose entries are held
 constexpr int kRed = 3;                  // rows whose warps' (m, s) are held: a warp may write the
                                          // next row's while another reads the one before last, and
                                          // only the barrier between two rows' writes parts them
@@ -46,16 +43,6 @@ constexpr int kChunk = 4;                // 16-byte units of a thread in registe
 constexpr float kDLog2E = 1.4426950408889634f;
 constexpr float kDLn2 = 0.6931471805599453f;
 constexpr float kLowest = -3.402823466e+38f;
-
-// CTAs that an SM's registers are to hold, the 16-byte units of a slot, and a
-// CTA's threads (the last warp has the teacher's entries).
-__host__ __device__ constexpr int distill_ctas(int warps) {
-  return warps == 8 ? 4 : warps == 4 ? 7 : warps == 2 ? 12 : 16;
-}
-__host__ __device__ constexpr int distill_units(int warps) {
-  return warps == 8 ? 4096 : warps * 256;
-}
-__host__ __device__ constexpr int distill_threads(int warps) { return (warps + 1) * 32; }
 
 // (m, s): maximum of x and sum of 2^((x - m) c), joined over the warp's lanes.
 // m starts at the type's lowest value, not at -inf, so that a difference of
@@ -95,7 +82,10 @@ template <int WARPS>
 __global__ void __launch_bounds__(distill_threads(WARPS), distill_ctas(WARPS))
     lin_distill_kernel(const __grid_constant__ DistillArgs a) {
   constexpr int MAIN = WARPS * 32;
-  __shared__ __align__(8) uint64_t bars[kSlots + kExch + 2 * kEnt];
+  constexpr int BARS = kSlots + kExch + 2 * kEnt;
+  static_assert(BARS * 8 + kRed * WARPS * 8 + kExch * kMaxCluster * 8 + kEnt * 16 + 16 <=
+                    (int)kDistillStatic, "shared memory beside the slots");
+  __shared__ __align__(8) uint64_t bars[BARS];
   __shared__ float2 red[kRed][WARPS];   // (m, s) of each warp
   __shared__ float2 stats[kExch][kMaxCluster];   // (m, s) of each CTA of the cluster
   __shared__ float4 teacher[kEnt];       // sum p log2 p, sum p z, whether the row has an entry
@@ -500,21 +490,12 @@ namespace {
 
 template <int WARPS>
 cudaError_t launch_rows(DistillArgs a, int64_t units, int sms, cudaStream_t stream) {
-  constexpr int kMax = distill_units(WARPS);
-  a.cluster = 1;
-  while (a.cluster < kMaxCluster && (int64_t)a.cluster * kMax < units) a.cluster *= 2;
-  const int64_t part = (units + a.cluster - 1) / a.cluster;
-  a.segs = (int32_t)((part + kMax - 1) / kMax);
-  a.tile = (int32_t)((part + a.segs - 1) / a.segs);
-  // slots: what a row needs, and up to two more for the next rows' copies
-  // where they cost no CTA of the SM
-  const size_t entries = (size_t)((a.K + 3) & ~3) * 12 * kEnt, slot = (size_t)a.tile * 16;
-  auto resident_ctas = [&](int slots) {
-    return std::min<int64_t>(distill_ctas(WARPS), 225 * 1024 / (slots * slot + entries + 2048));
-  };
-  a.slots = std::min(a.segs, kSlots);
-  while (a.slots < kSlots && resident_ctas(a.slots + 1) == resident_ctas(a.segs)) ++a.slots;
-  const size_t smem = a.slots * slot + entries;
+  const DistillLayout d = distill_layout(WARPS, units, a.K);
+  a.cluster = d.cluster;
+  a.segs = d.segs;
+  a.tile = d.tile;
+  a.slots = d.slots;
+  const size_t smem = d.smem;
   auto kernel = lin_distill_kernel<WARPS>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)smem);
