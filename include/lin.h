@@ -358,10 +358,11 @@ lin_status lin_gate_up_w16(const float *X, const uint16_t *WG16, const uint16_t 
  * Arithmetic  Products on the tensor cores from the 16-bit operands with
  *             float32 accumulation; softmax statistics, delta and every sum
  *             in float32. P and dS are rounded to the tensors' 16-bit type
- *             for the product that follows them (dS scaled by a power of two
- *             so that binary16 holds it whatever the size of dO, while the
- *             rows of V have norms up to 1024); O, dQ, dK and dV are rounded
- *             once. Sums have a fixed order: the same call gives the same
+ *             for the product that follows them (dS scaled by powers of two,
+ *             from each row of dO for dQ and from the largest that a tile of
+ *             128 keys meets for dK, so that binary16 holds it whatever the
+ *             size of dO, while the rows of V have norms up to 1024); O, dQ,
+ *             dK and dV are rounded once. Sums have a fixed order: the same call gives the same
  *             bits.
  * Shapes      dim a multiple of 8 up to 128; heads_q a multiple of heads_kv;
  *             sequences up to 65535; max_q and max_k up to 65535 * 128;

@@ -2,10 +2,12 @@
 as in test_attention_gpu.py unless a test says otherwise.
 """
 
+import numpy as np
 import pytest
 
+from oracle import step_oracle as so
 from tests.gpu_util import require_gpu
-from tests.test_attention_gpu import _cu, _setup
+from tests.test_attention_gpu import UNIT, _cu, _host, _run, _setup
 from transformer_linear_layer_tcgen05_gb300 import lin
 
 pytestmark = pytest.mark.gpu
@@ -35,3 +37,57 @@ def test_gradient_without_keys_where_parts_are_asked_for():
         assert torch.all(t["dq"] == 0)
     assert t["dk"].isnan().all() and t["dv"].isnan().all()   # (rows of no sequence)
     assert lin.lin_get_device_status() == lin.LIN_SUCCESS
+
+
+def _uneven(lens, hq, hk, d, dtype, k, seed):
+    """Inputs whose dO falls by 2^k from a sequence's first row to its last."""
+    import torch
+    t = _setup(dtype, lens, hq, hk, d, seed=seed)
+    t["v"].mul_(0.25)
+    at = 0
+    for n, _ in lens:
+        fall = 2.0 ** torch.round(12 - k * torch.arange(n, device="cuda") / max(n - 1, 1))
+        t["do"][at:at + n] *= fall.to(t["do"].dtype)[:, None, None]
+        at += n
+    return t
+
+
+# One sequence, several with more and with fewer keys than queries, one long
+# enough for parts of the queries, and heads that share a tile.
+UNEVEN = [([(512, 512)], 2, 2, 64), ([(300, 500), (450, 400)], 4, 2, 128),
+          ([(1100, 1100)], 1, 1, 64), ([(640, 640)], 3, 1, 96)]
+
+
+@pytest.mark.parametrize("shape", UNEVEN, ids=lambda s: f"{s[0]}h{s[1]}x{s[2]}d{s[3]}")
+@pytest.mark.parametrize("k", [14, 18])
+def test_key_gradients_where_early_rows_are_large(shape, k):
+    # A late key of a causal mask meets late rows only, so the scale of its dS
+    # in binary16 must come from those. dS carries a scale that brings the
+    # largest norm of dO among them to 2^4 or more: an entry's subnormal
+    # spacing is then at most 2^-24 2^-4 of that norm, half of it an entry's
+    # error; an entry of dK sums them times |q|. (The rows count in tiles of
+    # 128, hence the first row of the sum.)
+    lens, hq, hk, d = shape
+    t = _uneven(lens, hq, hk, d, "float16", k, seed=40 + k)
+    _run(t, lens, True)
+    q, kk, v, do = (_host(t[n]) for n in ("q", "k", "v", "do"))
+    cu_q = np.concatenate([[0], np.cumsum([a for a, _ in lens])])
+    cu_k = np.concatenate([[0], np.cumsum([b for _, b in lens])])
+    scale, u = d ** -0.5, UNIT["float16"]
+    grads, sizes = so.attention_backward(q, kk, v, do, True, scale, cu_q, cu_k)
+    spacing = np.zeros_like(kk)
+    norms = np.sqrt((do ** 2).sum(-1))
+    for b, (lq, lk) in enumerate(lens):
+        for j in range(lk):
+            first = max(j // 128 * 128 - (lk - lq) - 128, 0)
+            rows = slice(cu_q[b] + first, cu_q[b] + lq)
+            top = norms[rows].reshape(-1, hk, hq // hk).max(axis=(0, 2))
+            mag = np.abs(q[rows]).reshape(-1, hk, hq // hk, d).sum(axis=(0, 2))
+            spacing[cu_k[b] + j] = scale * 2.0 ** -29 * top[:, None] * mag
+    err = np.abs(_host(t["dk"]) - grads[1])
+    assert np.all(err <= u * np.abs(grads[1]) + (u + 2.0 ** -14) * sizes[1] + 2.0 ** -25 + spacing)
+    for at, name in ((0, "dq"), (2, "dv")):
+        err = np.abs(_host(t[name]) - grads[at])
+        # (P carries 2^8 in binary16: an error of 2^-33 of dO's sum)
+        far = 2.0 ** -33 * np.abs(do).sum() if name == "dv" else 0.0
+        assert np.all(err <= u * np.abs(grads[at]) + (u + 2.0 ** -14) * sizes[at] + 2.0 ** -25 + far)

@@ -558,15 +558,18 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   constexpr uint32_t kK = C::OWN_COL, kV = kK + DP / 2;   // K and V (heads of up to 64)
   const uint32_t k_own = base + C::OFF_OWN, v_own = k_own + AttnTile<DP>::BYTES;   // (of 128)
   // The exponent of dS's scale, from the largest row norm of dO that this tile
-  // meets (every tile of the heads: the masked ones do no harm). By each warp
-  // that wants it, once the dQ kernel, which leaves the norms and delta, is
-  // done; the copies and the first products do not wait for that.
+  // of keys meets, in tiles of 128 rows: behind a causal mask from the one of
+  // its first turn on (the rows before it may be larger by more than binary16
+  // spans). By each warp that wants it, once the dQ kernel, which leaves the
+  // norms and delta, is done; the copies and the first products do not wait for
+  // that.
   auto scale_exponent = [&]() -> int {
     pdl_wait();
-    const int norms = ((a.max_q << args.shift) + 127) / 128 * (a.group >> args.shift);
-    const float* nm = args.norm + ((int64_t)b * gridDim.x + hk) * norms;
+    const int tiles = ((a.max_q << shift) + 127) / 128;
+    const float* nm = args.norm + ((int64_t)b * gridDim.x + hk) * tiles * passes;
     float big = 0.0f;
-    for (int i = lane; i < norms; i += 32) big = fmaxf(big, nm[i]);
+    for (int p = 0; p < passes; ++p, nm += tiles)
+      for (int i = t0 * kTurn / 128 + lane; i < tiles; i += 32) big = fmaxf(big, nm[i]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
     return norm_exponent(big);
