@@ -459,7 +459,8 @@ lin_status lin_qk_norm_rope_backward(const lin_qk_norm_rope_shape *shape, const 
  *   DLOGITS[s, v] = temperature (q_v - p_v) inv_norm   (p_v = 0 if not listed)
  * and *loss_sum = the sum of the losses (a fixed order). An id outside [0, V)
  * is an empty place, and so is a teacher logit of -inf; a row of empty places
- * (padding) has loss 0 and a zero gradient row. An entry listed twice counts
+ * (padding) has loss 0 and a zero gradient row. A teacher logit of NaN or +inf
+ * makes its row's loss, and the gradients of its entries, NaN. An entry listed twice counts
  * with both probabilities. DLOGITS (rows ldd apart) may be LOGITS itself
  * (with ldd == ld) or NULL (the losses alone); otherwise outputs overlap
  * nothing. Only the V entries of a row are read or written. V < 2^31 - 65536,

@@ -1,5 +1,5 @@
 """lin_distill_topk over many rows, which a CTA takes one after another, and over
-long rows beside many entries. Bounds as in test_distill_gpu.py.
+long rows beside many entries, and odd values. Bounds as in test_distill_gpu.py.
 """
 
 import numpy as np
@@ -67,3 +67,44 @@ def test_long_rows_and_many_entries(m, v, k):
     lin.lin_distill_topk(zd, idd, td, zd, l2, s2, 2.0, 0.5)
     assert torch.equal(zd, dz) and torch.equal(l2, losses)
     assert lin.lin_get_device_status() == lin.LIN_SUCCESS
+
+
+@pytest.mark.parametrize("v", [900, 5000, 40000])
+def test_teacher_logits_that_are_no_numbers(v):
+    # the softmax over a row's entries is NaN where one of its logits is NaN
+    # or infinite: so is the loss, and so are the gradients of its entries;
+    # the other rows, and a row's other logits, are not touched by it
+    import torch
+    z, ids, t = _inputs(6, v, 40, seed=9)
+    ids[:] = np.arange(100, 140)
+    odd = t.copy()
+    odd[0, 3] = np.nan
+    odd[1, :] = np.nan
+    odd[2, 35] = np.inf
+    odd[4, :] = np.nan
+    odd[4, 7] = -np.inf          # an empty place in a row of NaN
+    odd[5, 1] = np.nan
+    ids[5] = -1                  # a padding row, whatever its places hold
+    zd, idd, td = _device(z, ids, odd, v)
+    dz, losses, total = _results(6, v, v)
+    lin.lin_distill_topk(zd, idd, td, dz, losses, total, 1.5)
+    torch.cuda.synchronize()
+    got = losses.cpu().numpy()
+    assert np.isnan(got[[0, 1, 2, 4]]).all() and np.isnan(total.item())
+    assert got[5] == 0 and torch.all(dz[5] == 0)
+    want_l, want_d = so.distill_topk(z, ids, t, 1.5, 1.0)
+    size = 1.5 ** 2 * (np.abs(z).max() + 40)
+    assert abs(got[3] - want_l[3]) <= E * size
+    g = dz.double().cpu().numpy()
+    for row in (0, 1, 2, 4):
+        listed = np.zeros(v, dtype=bool)
+        listed[100:140] = True
+        if row == 4:
+            listed[107] = False
+        assert np.isnan(g[row, listed]).all()
+        # (an entry without probability has tau q)
+        q = so.distill_topk(z[row:row + 1], np.array([[v - 1]]), np.zeros((1, 1)), 1.5, 1.0)[1][0]
+        others = ~listed
+        others[v - 1] = False
+        assert np.all(np.abs(g[row] - q)[others] <= E * q[others] + 1e-37)
+    assert np.isfinite(g[3]).all()

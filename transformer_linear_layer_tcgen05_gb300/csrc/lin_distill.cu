@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(distill_threads(WARPS), distill_ctas(WARPS))
       const float* row = a.logits + i * a.ld;
       const int phase = row_units(row, V).phase;
       float m = -INFINITY;
+      bool has = false;   // an entry: not -inf (a NaN is one, which the maximum passes over)
       if (lane < KP - a.K) id_b[a.K + lane] = -1;
 #pragma unroll 4
       for (int k = lane; k < a.K; k += 32) {
@@ -163,11 +164,12 @@ __global__ void __launch_bounds__(distill_threads(WARPS), distill_ctas(WARPS))
         const bool mine = ok && (C == 1 || ((id + phase) / 4 / a.tile) % C == rank);
         id_b[k] = mine ? id : -1;
         z_b[k] = mine || (ok && rank == 0) ? row[id] : 0.0f;
+        has = has || !(t == -INFINITY);
         m = fmaxf(m, t);
       }
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const bool any = m != -INFINITY;
+      const bool any = __any_sync(0xffffffffu, has);
       float s = 0.0f;
       for (int k = lane; k < a.K; k += 32) s += any ? ex2_approx(p_b[k] - m) : 0.0f;
 #pragma unroll
@@ -176,9 +178,9 @@ __global__ void __launch_bounds__(distill_threads(WARPS), distill_ctas(WARPS))
       float plp = 0.0f, pz = 0.0f;
       for (int k = lane; k < a.K; k += 32) {
         const float lp = p_b[k] - m - ls;
-        const float p = any ? ex2_approx(lp) : 0.0f;
+        const float p = p_b[k] == -INFINITY ? 0.0f : ex2_approx(lp);
         p_b[k] = p;
-        if (p > 0.0f) {   // (0 log 0 = 0)
+        if (!(p == 0.0f)) {   // (0 log 0 = 0; a NaN counts)
           plp = fmaf(p, lp, plp);
           pz = fmaf(p, z_b[k], pz);
         }
