@@ -108,3 +108,20 @@ def test_teacher_logits_that_are_no_numbers(v):
         others[v - 1] = False
         assert np.all(np.abs(g[row] - q)[others] <= E * q[others] + 1e-37)
     assert np.isfinite(g[3]).all()
+
+
+@pytest.mark.parametrize("v", [700, 3001, 33000])
+@pytest.mark.parametrize("tau", [1.0, 2.5])
+def test_logits_far_from_zero(v, tau):
+    # a softmax does not depend on what its logits have in common: with 2^16
+    # added to both sides' (on a grid of 2^-7, so that every sum is exact) the
+    # results are those of the logits without it, within the bounds of these
+    import torch
+    z, ids, t = _inputs(5, v, 12, seed=10)
+    z, t = (np.round(x * 128) / 128 for x in (z, t))
+    zd, idd, td = _device(z + np.float32(65536), ids, t + np.float32(65536), v)
+    dz, losses, total = _results(5, v, v)
+    lin.lin_distill_topk(zd, idd, td, dz, losses, total, tau, 0.5)
+    torch.cuda.synchronize()
+    _check(z, ids, t, tau, 0.5, dz.double().cpu().numpy(), losses.double().cpu().numpy(),
+           total.item())

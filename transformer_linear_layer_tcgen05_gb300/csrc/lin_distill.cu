@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(distill_threads(WARPS), distill_ctas(WARPS))
   __shared__ __align__(8) uint64_t bars[BARS];
   __shared__ float2 red[kRed][WARPS];   // (m, s) of each warp
   __shared__ float2 stats[kExch][kMaxCluster];   // (m, s) of each CTA of the cluster
-  __shared__ float4 teacher[kEnt];       // sum p log2 p, sum p z, whether the row has an entry
+  __shared__ float4 teacher[kEnt];       // sum p log2 p, sum p (z - w), whether the row has an entry, w
   __shared__ volatile int abort;
   extern __shared__ float4 ring[];       // slots x tile units, then kEnt x (ids, p, z)[KP]
   const int KP = (a.K + 3) & ~3;         // (whole groups of four, the last one padded with -1)
@@ -150,39 +150,48 @@ __global__ void __launch_bounds__(distill_threads(WARPS), distill_ctas(WARPS))
       float *p_b = ps + b * KP, *z_b = zs + b * KP;
       const float* row = a.logits + i * a.ld;
       const int phase = row_units(row, V).phase;
-      float m = -INFINITY;
+      float m = -INFINITY, ref = -INFINITY;
       bool has = false;   // an entry: not -inf (a NaN is one, which the maximum passes over)
       if (lane < KP - a.K) id_b[a.K + lane] = -1;
 #pragma unroll 4
       for (int k = lane; k < a.K; k += 32) {
         const int id = k < 32 ? id_first : a.ids[i * a.K + k];
         const bool ok = id >= 0 && id < V;
-        const float t = ok ? (k < 32 ? t_first : a.teacher[i * a.K + k]) * c : -INFINITY;
+        const float t = ok ? (k < 32 ? t_first : a.teacher[i * a.K + k]) : -INFINITY;
         p_b[k] = t;
         // (the loss, by rank 0, needs every entry's logit; the gradient those
         // of the CTA's own part)
         const bool mine = ok && (C == 1 || ((id + phase) / 4 / a.tile) % C == rank);
         id_b[k] = mine ? id : -1;
-        z_b[k] = mine || (ok && rank == 0) ? row[id] : 0.0f;
+        const float z = mine || (ok && rank == 0) ? row[id] : -INFINITY;
+        z_b[k] = z;
+        ref = fmaxf(ref, z);
         has = has || !(t == -INFINITY);
         m = fmaxf(m, t);
       }
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      for (int o = 16; o > 0; o >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        ref = fmaxf(ref, __shfl_xor_sync(0xffffffffu, ref, o));
+      }
+      // Both sides' logits enter as differences (from the largest of the
+      // teacher's, and of the row's listed ones), before anything is rounded:
+      // what they have in common costs no accuracy.
+      if (!(fabsf(ref) < INFINITY)) ref = 0.0f;
       const bool any = __any_sync(0xffffffffu, has);
       float s = 0.0f;
-      for (int k = lane; k < a.K; k += 32) s += any ? ex2_approx(p_b[k] - m) : 0.0f;
+      for (int k = lane; k < a.K; k += 32) s += any ? ex2_approx((p_b[k] - m) * c) : 0.0f;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       const float ls = log2f(s);
       float plp = 0.0f, pz = 0.0f;
       for (int k = lane; k < a.K; k += 32) {
-        const float lp = p_b[k] - m - ls;
+        const float lp = fmaf(p_b[k] - m, c, -ls);
         const float p = p_b[k] == -INFINITY ? 0.0f : ex2_approx(lp);
         p_b[k] = p;
         if (!(p == 0.0f)) {   // (0 log 0 = 0; a NaN counts)
           plp = fmaf(p, lp, plp);
-          pz = fmaf(p, z_b[k], pz);
+          pz = fmaf(p, z_b[k] - ref, pz);
         }
       }
 #pragma unroll
@@ -219,7 +228,7 @@ __global__ void __launch_bounds__(distill_threads(WARPS), distill_ctas(WARPS))
           p_b[k] = p;   // (the marked places' own stay as they were)
         }
       }
-      if (lane == 0) teacher[b] = make_float4(plp, pz, any ? 1.0f : 0.0f, 0.0f);
+      if (lane == 0) teacher[b] = make_float4(plp, pz, any ? 1.0f : 0.0f, ref);
       __syncwarp();
       if (lane == 0) mbar_arrive(ent_full + 8 * b);
     }
@@ -382,7 +391,7 @@ __global__ void __launch_bounds__(distill_threads(WARPS), distill_ctas(WARPS))
     const float4 tp = teacher[b];
     const bool any = tp.z != 0.0f;
     if (rank == 0 && tid == 0 && ok)
-      a.losses[i] = any ? a.tau * a.tau * kDLn2 * (tp.x - (tp.y - m) * c + ls) : 0.0f;
+      a.losses[i] = any ? a.tau * a.tau * kDLn2 * (tp.x - (tp.y + (tp.w - m)) * c + ls) : 0.0f;
     if (a.dlogits) {
       const float* row = a.logits + i * a.ld;
       const Row r = row_units(row, V);
