@@ -379,7 +379,10 @@ lin_status lin_gate_up_w16(const float *X, const uint16_t *WG16, const uint16_t 
  *             that are no multiple of 8, LIN_ERROR_INVALID_VALUE for strides
  *             under which two entries of a tensor would share a place;
  *             LIN_ERROR_ALIASING if an output shares an entry with another
- *             tensor of the call (interleaved views of one buffer do not).
+ *             tensor of the call. Interleaved views of one buffer of the same
+ *             strides do not, nor do those of the same token stride whose
+ *             heads of a token lie within it; others whose ranges meet count
+ *             as sharing one.
  */
 typedef enum lin_dtype { LIN_BINARY16 = 0, LIN_BFLOAT16 = 1 } lin_dtype;
 

@@ -7,7 +7,7 @@ import pytest
 
 from oracle import step_oracle as so
 from tests.gpu_util import require_gpu
-from tests.test_attention_gpu import UNIT, _cu, _host, _run, _setup
+from tests.test_attention_gpu import UNIT, _check, _cu, _host, _run, _setup
 from transformer_linear_layer_tcgen05_gb300 import lin
 
 pytestmark = pytest.mark.gpu
@@ -91,3 +91,20 @@ def test_key_gradients_where_early_rows_are_large(shape, k):
         # (P carries 2^8 in binary16: an error of 2^-33 of dO's sum)
         far = 2.0 ** -33 * np.abs(do).sum() if name == "dv" else 0.0
         assert np.all(err <= u * np.abs(grads[at]) + (u + 2.0 ** -14) * sizes[at] + 2.0 ** -25 + far)
+
+
+def test_views_of_heads_outside_tokens_interleaved():
+    # q, k and v side by side for each head and token, both orders
+    import torch
+    lens, h, d = [(90, 90)], 3, 64
+    for outer in ("heads", "tokens"):
+        t = _setup("float16", lens, h, h, d, seed=70)
+        for names in (("q", "k", "v"), ("dq", "dk", "dv")):
+            shape = (h, 90, 3, d) if outer == "heads" else (90, h, 3, d)
+            buf = torch.full(shape, float("nan"), device="cuda", dtype=torch.float16)
+            for i, n in enumerate(names):
+                view = buf[:, :, i].transpose(0, 1) if outer == "heads" else buf[:, :, i]
+                view.copy_(t[n])
+                t[n] = view
+        _run(t, lens, True, packed=False)
+        _check(t, lens, True, d ** -0.5, UNIT["float16"])

@@ -52,16 +52,34 @@ inline lin_status check_view(View& v, int64_t dim) {
 }
 
 // Whether two views share an entry. Views whose ranges of memory meet may
-// still be disjoint: the q, k and v heads of one buffer of tokens.
+// still be disjoint: the q, k and v heads of one buffer, whichever way its
+// tokens and heads lie. Exact for equal strides (those of an extent of one
+// count as any); views of other strides share an entry unless each token's
+// heads of either lie within a row of the other's.
 inline bool views_overlap(const View& a, const View& b, int64_t dim) {
   if (!overlaps(a.t->data, a.extent, b.t->data, b.extent)) return false;
   const int64_t ra = (a.heads - 1) * a.hs + dim, rb = (b.heads - 1) * b.hs + dim;
-  if (a.tokens > 1 && b.tokens > 1 && a.ts == b.ts && ra <= a.ts && rb <= b.ts) {
-    const int64_t d = (static_cast<const char*>(b.t->data) - static_cast<const char*>(a.t->data)) / 2;
+  // b's first entry from a's, in entries
+  const int64_t d = (static_cast<const char*>(b.t->data) - static_cast<const char*>(a.t->data)) / 2;
+  if (a.tokens > 1 && b.tokens > 1 && a.ts == b.ts && ra <= a.ts && rb <= a.ts) {
     const int64_t r = ((d % a.ts) + a.ts) % a.ts;   // b's row starts r entries into one of a's
-    return !(r >= ra && a.ts - r >= rb);
+    if (r >= ra && a.ts - r >= rb) return false;
   }
-  return true;
+  if ((a.tokens > 1 && b.tokens > 1 && a.ts != b.ts) || (a.heads > 1 && b.heads > 1 && a.hs != b.hs))
+    return true;
+  // A head of b lies d + i ts + j hs from one of a, for the differences i of
+  // their tokens and j of their heads: fewer than dim entries away, they meet.
+  const int64_t ts = a.tokens > 1 ? a.ts : b.ts, hs = a.heads > 1 ? a.hs : b.hs;
+  const int64_t i_lo = 1 - a.tokens, i_hi = b.tokens - 1;
+  for (int64_t j = 1 - a.heads; j < b.heads; ++j) {
+    const int64_t r = d + j * hs;
+    const int64_t near = -r / ts;   // (toward zero: one of the two nearest is it or beside it)
+    for (int64_t i = near - 1; i <= near + 1; ++i) {
+      const int64_t at = r + std::min(std::max(i, i_lo), i_hi) * ts;
+      if (at > -dim && at < dim) return true;
+    }
+  }
+  return false;
 }
 
 inline lin::HeadsPtr heads_ptr(const View& v) {
