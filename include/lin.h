@@ -338,7 +338,10 @@ lin_status lin_gate_up_w16(const float *X, const uint16_t *WG16, const uint16_t 
  * dK and dV summed over the query heads that share a key head. The mask
  * leaves the sequence's own keys and, with `causal`, those with
  * j <= i + (keys - queries): the last query sees every key. A row that the
- * mask leaves nothing has O = 0, LSE = -inf and gives and gets no gradient.
+ * mask leaves nothing has O = 0, LSE = -inf and gives and gets no gradient,
+ * whatever its Q and DO hold. (A NaN or an infinity in a row that takes part
+ * may show in the other rows of its sequence, those that the mask parts from
+ * it among them: it enters their products with a weight of zero.)
  *
  * Tensors     lin_heads: [tokens, heads, dim], the dim entries of a head
  *             contiguous, strides in entries (multiples of 8, base 16-byte

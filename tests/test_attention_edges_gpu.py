@@ -108,3 +108,47 @@ def test_views_of_heads_outside_tokens_interleaved():
                 t[n] = view
         _run(t, lens, True, packed=False)
         _check(t, lens, True, d ** -0.5, UNIT["float16"])
+
+
+# (lengths, query heads, key heads, dim): more queries than keys, so that a
+# causal mask leaves the first rows nothing; as many as a turn of 64 rows has,
+# fewer and more, heads that share a tile, parts of the queries, and a sequence
+# with every row seen beside one without
+HIDDEN = [([(200, 90)], 2, 2, 64), ([(130, 70)], 4, 2, 128), ([(192, 128)], 1, 1, 96),
+          ([(70, 3), (40, 40), (300, 299)], 6, 2, 64), ([(1700, 90)], 2, 1, 64), ([(90, 25)], 3, 1, 72)]
+
+
+@pytest.mark.parametrize("shape", HIDDEN, ids=lambda s: f"{s[0]}h{s[1]}x{s[2]}d{s[3]}")
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_rows_without_a_key_give_no_gradient(shape, dtype):
+    # Rows that the mask leaves nothing hold NaN and infinities (in Q and dO):
+    # they reach nothing, and do not set the scale of the other rows' dS
+    # (binary16 alone would lose a dO of 2^-14).
+    import torch
+    lens, hq, hk, d = shape
+    t = _setup(dtype, lens, hq, hk, d, seed=50)
+    t["do"].mul_(2.0 ** -14)
+    clean = {n: t[n].clone() for n in ("q", "do")}
+    at, nothing = 0, []
+    for lq, lk in lens:
+        hidden = slice(at, at + max(lq - lk, 0))
+        nothing.append(hidden)
+        for n, odd in (("q", float("inf")), ("do", float("-inf"))):
+            t[n][hidden] = float("nan")
+            t[n][hidden][::3] = odd
+            clean[n][hidden] = 0
+        at += lq
+    _run(t, lens, True)
+    for rows in nothing:
+        assert torch.all(t["o"][rows] == 0) and torch.all(t["dq"][rows] == 0)
+        assert torch.all(t["lse"][:, rows] == -float("inf"))
+    q, do = (_host(clean[n]) for n in ("q", "do"))
+    k, v = _host(t["k"]), _host(t["v"])
+    cu_q = np.concatenate([[0], np.cumsum([a for a, _ in lens])])
+    cu_k = np.concatenate([[0], np.cumsum([b for _, b in lens])])
+    u = UNIT[dtype]
+    grads, sizes = so.attention_backward(q, k, v, do, True, d ** -0.5, cu_q, cu_k)
+    for name, g, size in zip(("dq", "dk", "dv"), grads, sizes):
+        err = np.abs(_host(t[name]) - g)
+        # (the result itself may be subnormal: half its spacing of 2^-24)
+        assert np.all(err <= u * np.abs(g) + (u + 2.0 ** -14) * size + 2.0 ** -25), name

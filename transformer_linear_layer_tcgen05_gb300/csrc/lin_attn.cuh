@@ -166,15 +166,15 @@ __device__ __forceinline__ void umma_tokens(uint32_t d, uint32_t a, uint64_t b, 
     umma_f16_tmem_a(d, a + kk * 8, b + AttnTile<DP>::token_step(from + kk), idesc, kk > 0 || !first);
 }
 
-// Zeroes rows [first, ROWS) of an operand tile: a contraction over tokens must
+// Zeroes rows [first, last) of an operand tile: a contraction over tokens must
 // not meet what lies behind a sequence's end (another sequence's rows, or
-// padding that may hold infinities or NaN, which a zero weight would not
-// remove). One warp, after the copy has landed; a fence then orders the
-// stores before the tensor core's reads.
+// padding), nor rows that a causal mask leaves no key: they may hold infinities
+// or NaN, which a zero weight would not remove. One warp, after the copy has
+// landed; a fence then orders the stores before the tensor core's reads.
 template <int DP, int ROWS>
-__device__ __forceinline__ void zero_rows(uint32_t tile, int first, int lane) {
+__device__ __forceinline__ void zero_rows(uint32_t tile, int first, int last, int lane) {
   for (int s = 0; s < AttnTile<DP, ROWS>::SUB; ++s)
-    for (int i = first * 8 + lane; i < ROWS * 8; i += 32)
+    for (int i = first * 8 + lane; i < last * 8; i += 32)
       st_shared_v4(tile + s * AttnTile<DP, ROWS>::SUB_BYTES + i * 16, 0u, 0u, 0u, 0u);
 }
 

@@ -58,7 +58,7 @@ constexpr float kPShift = 8.0f;     // P^T is scaled by 2^8
 constexpr int kNormExp = 4;         // dO rows count as having a norm near 2^4
 constexpr int kRowWarps = 8;        // the two streams' warpgroups
 constexpr int kDkvThreads = 384;
-constexpr int kTailWarp = 10;       // of the dK, dV kernel: cuts tiles at the sequence's end
+constexpr int kTailWarp = 10;       // of the dK, dV kernel: zeroes rows that take no part
 constexpr int kStatsWarp = 11;      // of the dK, dV kernel: rows' statistics
 constexpr int kTurn = 64;           // rows of a streamed tile
 
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (n > 0 && k_left < kTurn) {   // cut the last K tile at the sequence's end (dS K runs over it)
       const int s = (n - 1) % C::N;
       if (warp_attn_wait(bar(C::FULL + s), ((n - 1) / C::N) & 1, ctl)) {
-        zero_rows<DP, kTurn>(k_tile(s), k_left, lane);
+        zero_rows<DP, kTurn>(k_tile(s), k_left, kTurn, lane);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::TAIL));
@@ -354,7 +354,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     float* red2 = reinterpret_cast<float*>(ctl_gen + C::OFF_RED);
     if (half == 0) {
       if (live && (tiles == 0 || !few) && part == 0) args.delta[(int64_t)h * a.tokens_q + token] = delta;
-      float big = norm;   // (NaN rows do not count)
+      // (rows without a key, L = -inf, do not count, whatever their dO holds;
+      // nor do NaN)
+      float big = lse == -INFINITY ? 0.0f : norm;
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
       if (lane == 0) red2[warp] = big;
@@ -526,6 +528,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   const int from = at.begin(per * passes), n = at.end(per * passes) - from;
   const int tile0 = from > 0 ? from % per : 0;           // the first turn's tile of its pass
   const int q_left = rows - (t1 - 1) * kTurn;            // rows of the last tile
+  // rows of the first tile that see no key at all (more queries than keys)
+  const int q_none = a.causal ? (max(-off, 0) << shift) - t0 * kTurn : 0;
+  const bool cut_rows = q_left < kTurn || q_none > 0;
   const int h0 = hk * a.group;
 
   if (!smem_aligned(smem_raw, a.status)) return;
@@ -659,20 +664,28 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       r.next();
     }
   } else if (warp == kTailWarp) {
-    // Where the last query tile of a head is cut by the sequence's end, this
-    // warp hands every stage on to the products (a phase that nobody waited
-    // for would not be told from the one before it), that tile with the rows
-    // behind the end zeroed: they enter the products that run over the queries.
-    if (n > 0 && q_left < kTurn) {
+    // Where the last query tile of a head is cut by the sequence's end, or its
+    // first one begins with rows without a key, this warp hands every stage on
+    // to the products (a phase that nobody waited for would not be told from
+    // the one before it), those tiles with such rows zeroed: they enter the
+    // products that run over the queries.
+    if (n > 0 && cut_rows) {
       int tile = tile0;
       RingAt<C::N> r;
       for (int it = 0; it < n; ++it) {
         if (!warp_attn_wait(bar(C::FULL + r.s), r.parity, ctl)) break;
+        if (tile == 0 && q_none > 0) {
+          zero_rows<DP, kTurn>(q_tile(r.s), 0, q_none, lane);
+          zero_rows<DP, kTurn>(do_tile(r.s), 0, q_none, lane);
+          fence_proxy_async_smem();
+        }
         if (++tile == per) {
           tile = 0;
-          zero_rows<DP, kTurn>(q_tile(r.s), q_left, lane);
-          zero_rows<DP, kTurn>(do_tile(r.s), q_left, lane);
-          fence_proxy_async_smem();
+          if (q_left < kTurn) {
+            zero_rows<DP, kTurn>(q_tile(r.s), q_left, kTurn, lane);
+            zero_rows<DP, kTurn>(do_tile(r.s), q_left, kTurn, lane);
+            fence_proxy_async_smem();
+          }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::TAIL + r.s));
@@ -685,7 +698,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       const uint64_t qt_desc = C::Tile::mn_major(q_tile(0));
       const uint64_t dot_desc = C::Tile::mn_major(do_tile(0));
       constexpr uint64_t STAGE = C::Tile::UNITS;
-      const int ready = q_left < kTurn ? C::TAIL : C::FULL;
+      const int ready = cut_rows ? C::TAIL : C::FULL;
       RingAt<C::N> r, next;   // stages of turn it, and of the next S^T and dP^T
       auto own = [&](uint32_t d, uint32_t col, uint32_t tile, uint64_t other) {
         if constexpr (C::kOwnSmem)

@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (n > 0 && v_left < 128) {   // cut the last V tile at the sequence's end
         const int s = (n - 1) % C::NKV;
         if (warp_wait_phase<kAttnNapNs>(bar(C::V_FULL + s), ((n - 1) / C::NKV) & 1, ctl)) {
-          zero_rows<DP, 128>(base + C::OFF_V + s * C::TILE, v_left, lane);
+          zero_rows<DP, 128>(base + C::OFF_V + s * C::TILE, v_left, 128, lane);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::TAIL));
