@@ -376,8 +376,9 @@ lin_status lin_gate_up_w16(const float *X, const uint16_t *WG16, const uint16_t 
  *             128)) * heads_q floats. Where a call has fewer tiles of 128
  *             rows than the device has SMs, and the other side is long, the
  *             other side is cut into parts whose results are joined in order:
- *             then, for each part, also the float32 results themselves
- *             (forward: O and LSE; backward: DQ, or DK and DV).
+ *             then, for each part (at most 16), also the float32 results of
+ *             sequences * max_q (DK, DV: max_k) rows themselves (forward: O
+ *             and LSE; backward: DQ, or DK and DV).
  * Errors      as for the linear layers; LIN_ERROR_MISALIGNED also for strides
  *             that are no multiple of 8, LIN_ERROR_INVALID_VALUE for strides
  *             under which two entries of a tensor would share a place;

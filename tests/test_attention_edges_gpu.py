@@ -152,3 +152,43 @@ def test_rows_without_a_key_give_no_gradient(shape, dtype):
         err = np.abs(_host(t[name]) - g)
         # (the result itself may be subnormal: half its spacing of 2^-24)
         assert np.all(err <= u * np.abs(g) + (u + 2.0 ** -14) * size + 2.0 ** -25), name
+
+
+def test_parts_are_held_for_the_sequences_rows_only():
+    # one short sequence in tensors of many rows: the parts' float32 results
+    # are those of the sequence's rows, whatever else the tensors hold
+    import torch
+    n, lq, lk, h, d = 100_000, 70, 2000, 2, 64
+    g = torch.Generator(device="cuda")
+    g.manual_seed(60)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").half()  # noqa: E731
+    big = lambda: torch.full((n, h, d), float("nan"), device="cuda", dtype=torch.float16)  # noqa: E731
+    q0, k0 = 31_000, 90_001
+    for lq, lk in ((70, 2000), (2000, 70)):
+        t = dict(q=big(), k=big(), v=big(), do=big(), o=big(), dq=big(), dk=big(), dv=big(),
+                 lse=torch.full((h, n), float("nan"), device="cuda"))
+        for name, at, m in (("q", q0, lq), ("do", q0, lq), ("k", k0, lk), ("v", k0, lk)):
+            t[name][at:at + m] = rnd(m, h, d)
+        how = dict(cu_q=torch.tensor([q0, q0 + lq], dtype=torch.int32, device="cuda"),
+                   cu_k=torch.tensor([k0, k0 + lk], dtype=torch.int32, device="cuda"), max_q=lq,
+                   max_k=lk, causal=False)
+        lin.lin_attention(t["q"], t["k"], t["v"], t["o"], t["lse"], **how)
+        kernels, workspace = lin.lin_last_launch_info()
+        if lk == 2000:
+            assert kernels == 2   # (at most 16 parts)
+            assert 0 < workspace <= 16 * lq * h * (d + 1) * 4
+        lin.lin_attention_backward(t["q"], t["k"], t["v"], t["o"], t["lse"], t["do"], t["dq"],
+                                   t["dk"], t["dv"], **how)
+        kernels, workspace = lin.lin_last_launch_info()
+        assert kernels == 3
+        assert 0 < workspace <= (n * h + 16 * h + 16 * 2 * 70 * h * d) * 4   # (delta: as LSE)
+        torch.cuda.synchronize()
+        assert lin.lin_get_device_status() == lin.LIN_SUCCESS
+        inner = {x: (y[:, q0:q0 + lq] if x == "lse" else
+                     y[k0:k0 + lk] if x in ("k", "v", "dk", "dv") else y[q0:q0 + lq])
+                 for x, y in t.items()}
+        _check(inner, [(lq, lk)], False, d ** -0.5, UNIT["float16"])
+        for x in ("o", "dq"):
+            assert t[x][:q0].isnan().all() and t[x][q0 + lq:].isnan().all()
+        for x in ("dk", "dv"):
+            assert t[x][:k0].isnan().all() and t[x][k0 + lk:].isnan().all()

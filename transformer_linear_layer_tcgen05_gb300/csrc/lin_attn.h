@@ -29,8 +29,10 @@ struct AttnFwdArgs {
   HeadsPtr o;
   float* lse;   // [heads_q][tokens_q]
   // parts of the keys, and, where there are several, their results in f32:
-  // [part][token][head][dim], [part][head][token]
+  // [part][row][head][dim], [part][head][row], the rows of the sequences one
+  // after another, max_q to each (part_rows in all)
   int32_t parts;
+  int64_t part_rows;
   float *o_part, *lse_part;
   // tiles of a CTA (1 or 2), query heads of a tile (1, or all that share a key
   // head), and its queries: 128 / pack
@@ -46,8 +48,10 @@ struct AttnBwdArgs {
   float* norm;            // [sequences][heads_q >> shift][row tiles]: largest row norm of dO
   HeadsPtr dq, dk, dv;
   // parts of the keys for dQ and of the queries for dK, dV, and, where there
-  // are several, their f32 sums [part][token][head][dim]
+  // are several, their f32 sums [part][row][head][dim], the rows of the
+  // sequences one after another, max_q (max_k) to each
   int32_t q_parts, k_parts;
+  int64_t q_part_rows, k_part_rows;
   // log2 of the query heads that are rows of one tile: 1, or all that share a
   // key head
   int32_t shift;

@@ -114,7 +114,8 @@ lin_status attention(const lin_attention_shape* s, const lin_heads* Q, const lin
   const lin_status st = check_attention(s, v, 4, LSE, true, &c);
   if (st != LIN_SUCCESS) return st;
   if (c.nothing || c.max_q == 0) return LIN_SUCCESS;
-  lin::AttnFwdArgs a{attn_args(s, c), heads_ptr(v[3]), LSE, 1, nullptr, nullptr, 2, 1, 128};
+  lin::AttnFwdArgs a{attn_args(s, c), heads_ptr(v[3]), LSE, 1, s->sequences * c.max_q, nullptr,
+                     nullptr, 2, 1, 128};
   const int sms = sm_count(c.dev);
   auto tiles = [&] {
     return (c.max_q + a.tile_q - 1) / a.tile_q * (s->heads_q / a.pack) * s->sequences;
@@ -136,15 +137,17 @@ lin_status attention(const lin_attention_shape* s, const lin_heads* Q, const lin
   // the products' latency and K, V are read half as often.
   if (tiles() <= sms) a.tiles = 1;
   const int64_t rows = (int64_t)a.tiles * a.tile_q;
-  a.parts = lin::attn_parts((c.max_q + rows - 1) / rows * (s->heads_q / a.pack) * s->sequences,
-                            c.max_k, sms);
+  // (a CTA of two tiles: more than half as many CTAs as SMs, no parts)
+  if (a.tiles == 1)
+    a.parts = lin::attn_parts((c.max_q + rows - 1) / rows * (s->heads_q / a.pack) * s->sequences,
+                              c.max_k, sms);
   lin::AttnFwdMaps maps;
   bool ok = encode_view(&maps.q, v[0], s->dim, a.tile_q, a.pack);
   // without keys the K and V maps are never used
   ok &= encode_view(&maps.k, v[1].extent ? v[1] : v[0], s->dim, 128);
   ok &= encode_view(&maps.v, v[2].extent ? v[2] : v[0], s->dim, 128);
   if (!ok) return cuda_fail(cudaErrorInvalidValue);
-  const uint64_t part_rows = (uint64_t)a.parts * (uint64_t)s->tokens_q * (uint64_t)s->heads_q;
+  const uint64_t part_rows = (uint64_t)a.parts * (uint64_t)a.part_rows * (uint64_t)s->heads_q;
   const size_t bytes = a.parts > 1 ? (size_t)(part_rows * (uint64_t)(s->dim + 1) * 4) : 0;
   if (bytes) {
     a.o_part = static_cast<float*>(take_stream_workspace(c.dev, bytes, stream));
@@ -211,8 +214,10 @@ lin_status attention_backward(const lin_attention_shape* s, const lin_heads* Q, 
   a.k_parts = lin::attn_parts(tk * s->heads_kv * s->sequences, c.max_q * (int64_t)a.s.group, sms);
   // workspace: the parts' sums, delta [heads][tokens], then the largest dO
   // norms of the query tiles
-  const uint64_t dq = a.q_parts > 1 ? (uint64_t)a.q_parts * s->tokens_q * s->heads_q * s->dim : 0;
-  const uint64_t dk = a.k_parts > 1 ? (uint64_t)a.k_parts * s->tokens_k * s->heads_kv * s->dim : 0;
+  a.q_part_rows = s->sequences * c.max_q;
+  a.k_part_rows = s->sequences * c.max_k;
+  const uint64_t dq = a.q_parts > 1 ? (uint64_t)(a.q_parts * a.q_part_rows * s->heads_q * s->dim) : 0;
+  const uint64_t dk = a.k_parts > 1 ? (uint64_t)(a.k_parts * a.k_part_rows * s->heads_kv * s->dim) : 0;
   const uint64_t delta = (uint64_t)s->heads_q * (uint64_t)s->tokens_q;
   const uint64_t norms = (uint64_t)s->sequences * (uint64_t)hq_tiles * (uint64_t)tq;
   const size_t bytes = (size_t)std::max<uint64_t>(16, (dq + 2 * dk + delta + norms) * 4);

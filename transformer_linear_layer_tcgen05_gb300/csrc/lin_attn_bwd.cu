@@ -144,14 +144,16 @@ __device__ __forceinline__ int norm_exponent(float norm) {
 }
 
 // Where a thread's row of a gradient goes: to the 16-bit tensor, or, as one
-// of several parts, in f32 to [part][token][head][dim].
+// of several parts, in f32 to [part][row][head][dim] (`rows` to a part, this
+// one at `row_at`).
 struct HeadGrad {
   uint16_t* row;
   float* part_row;
   __device__ __forceinline__ HeadGrad(const HeadsPtr& t, float* parts_base, int parts, int part,
-                                      int64_t tokens, int heads, int dim, int64_t token, int h)
+                                      int64_t rows, int64_t row_at, int heads, int dim,
+                                      int64_t token, int h)
       : row(t.p + token * t.token_stride + (int64_t)h * t.head_stride),
-        part_row(parts > 1 ? parts_base + ((part * tokens + token) * heads + h) * dim : nullptr) {}
+        part_row(parts > 1 ? parts_base + ((part * rows + row_at) * heads + h) * dim : nullptr) {}
   // N columns from c0 on, times `back` (zeros if there is nothing), those
   // below dim.
   template <bool BF16, int N>
@@ -470,8 +472,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     }
     if (ok) {
       const float back = a.scale * pow2i(-ne);
-      const HeadGrad out(args.dq, args.dq_part, args.q_parts, part, a.tokens_q, a.heads_q, a.dim,
-                         token, h);
+      const HeadGrad out(args.dq, args.dq_part, args.q_parts, part, args.q_part_rows,
+                         (int64_t)b * a.max_q + i, a.heads_q, a.dim, token, h);
 #pragma unroll
       for (int q = 0; q < DP / 32; ++q) {
         const int c0 = half * (DP / 2) + q * 16;
@@ -881,8 +883,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     if (ok) {   // the first half's threads write dV, the others dK
       const float back = half == 0 ? pow2i(-(int)kPShift) : a.scale * pow2i(-ne);
       const HeadGrad out(half == 0 ? args.dv : args.dk, half == 0 ? args.dv_part : args.dk_part,
-                         args.k_parts, part, a.tokens_k, a.heads_q / a.group, a.dim,
-                         (int64_t)sk.start + (live ? key : 0), hk);
+                         args.k_parts, part, args.k_part_rows, (int64_t)b * a.max_k + key,
+                         a.heads_q / a.group, a.dim, (int64_t)sk.start + (live ? key : 0), hk);
 #pragma unroll
       for (int q = 0; q < DP / 32; ++q) {
         uint32_t o[32];
@@ -906,7 +908,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
 
 // ---------------------------------------------------------------- parts
 
-// Gradients from their parts' f32 sums [part][token][head][dim], added in
+// Gradients from their parts' f32 sums [part][row][head][dim], added in
 // order: one, or (dK and dV) two of the same shape in one launch. A CTA per 32
 // rows of a sequence and head, eight entries to a thread.
 struct SumParts {
@@ -920,7 +922,8 @@ __global__ void __launch_bounds__(256)
     lin_attn_sum_parts_kernel(const __grid_constant__ SumParts a) {
   const int h = blockIdx.x, heads = gridDim.x;
   const int which = blockIdx.z >= a.sequences;
-  const SeqRange r = seq_range(a.cu, blockIdx.z - which * a.sequences, a.tokens, a.most);
+  const int b = blockIdx.z - which * a.sequences;
+  const SeqRange r = seq_range(a.cu, b, a.tokens, a.most);
   const HeadsPtr& out = a.out[which];
   const int groups = a.dim / 8;
   pdl_wait();
@@ -928,8 +931,8 @@ __global__ void __launch_bounds__(256)
     const int i = blockIdx.y * 32 + k / groups, col = k % groups * 8;
     if (i >= r.len) continue;
     const int64_t token = (int64_t)r.start + i;
-    const float* p = a.part[which] + (token * heads + h) * a.dim + col;
-    const int64_t step = (int64_t)a.tokens * heads * a.dim;
+    const float* p = a.part[which] + (((int64_t)b * a.most + i) * heads + h) * a.dim + col;
+    const int64_t step = (int64_t)a.sequences * a.most * heads * a.dim;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
 #pragma unroll 4
     for (int q = 0; q < a.parts; ++q, p += step) {

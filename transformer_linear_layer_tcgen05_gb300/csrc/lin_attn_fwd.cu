@@ -105,7 +105,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const AttnArgs& a = args.s;
   const int pack = PACKED ? args.pack : 1, tile_q = PACKED ? args.tile_q : 128;
   const int h0 = (int)blockIdx.x * pack;   // the first head of the CTA
-  const PartOf at = part_of(blockIdx.z, args.parts);
+  // (parts only where every CTA has an SM to itself: one tile to each)
+  const int parts = TILES == 1 ? args.parts : 1;
+  const PartOf at = part_of(blockIdx.z, parts);
   const int b = at.b;
   // longest rows of a causal mask first
   const int i0 = (int)(gridDim.y - 1 - blockIdx.y) * (TILES * tile_q);
@@ -372,9 +374,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // (NaN stays NaN)
       const int64_t token = sq.start + i;
       uint16_t* out = args.o.p + token * args.o.token_stride + (int64_t)h * args.o.head_stride;
-      // [part][token][head][dim] and [part][head][token]
-      float* part_row = args.o_part + (((int64_t)at.part * a.tokens_q + token) * a.heads_q + h) * a.dim;
-      float* lse = args.parts > 1 ? args.lse_part + (int64_t)at.part * a.heads_q * a.tokens_q : args.lse;
+      const int64_t row_at = (int64_t)b * a.max_q + i;   // among the parts' rows
+      float* part_row = args.o_part + ((at.part * args.part_rows + row_at) * a.heads_q + h) * a.dim;
+      float* lse = parts > 1
+                       ? args.lse_part + ((int64_t)at.part * a.heads_q + h) * args.part_rows + row_at
+                       : args.lse + (int64_t)h * a.tokens_q + token;
 #pragma unroll
       for (int q = 0; q < DP / 32; ++q) {
         uint32_t o[32];
@@ -392,7 +396,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             w[e] = nk > 0 ? pack16<BF16>(l == 0.0f ? 0.0f : x * inv, l == 0.0f ? 0.0f : y * inv) : 0u;
           }
           if (!live || col >= a.dim || !dcheck(token < a.tokens_q, a.status, CHK_GLOBAL, token)) continue;
-          if (args.parts > 1) {   // in f32
+          if (parts > 1) {   // in f32
             const float z = nk > 0 ? inv : 0.0f;
             float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
             if (l != 0.0f && nk > 0) {
@@ -409,9 +413,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           }
         }
       }
-      if (live)
-        lse[(int64_t)h * a.tokens_q + token] =
-            l == 0.0f ? -INFINITY : m * a.scale + logf(l);
+      if (live) *lse = l == 0.0f ? -INFINITY : m * a.scale + logf(l);
     }
   }
   __syncwarp();
@@ -438,13 +440,14 @@ __global__ void __launch_bounds__(256)
     const int i = blockIdx.y * 32 + k / groups, col = k % groups * 8;
     if (i >= r.len) continue;
     const int64_t token = (int64_t)r.start + i;
-    const float* ls = args.lse_part + (int64_t)h * a.tokens_q + token;
-    const int64_t ls_step = (int64_t)a.heads_q * a.tokens_q;
+    const int64_t row_at = (int64_t)blockIdx.z * a.max_q + i;
+    const float* ls = args.lse_part + h * args.part_rows + row_at;
+    const int64_t ls_step = a.heads_q * args.part_rows;
     float top = -INFINITY;
     for (int q = 0; q < args.parts; ++q) top = fmaxf(top, ls[q * ls_step]);
     const float shift = top == -INFINITY ? 0.0f : top;   // (a row without a key)
-    const float* p = args.o_part + (token * a.heads_q + h) * a.dim + col;
-    const int64_t step = (int64_t)a.tokens_q * a.heads_q * a.dim;
+    const float* p = args.o_part + (row_at * a.heads_q + h) * a.dim + col;
+    const int64_t step = args.part_rows * a.heads_q * a.dim;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
     float total = 0.0f;
     for (int q = 0; q < args.parts; ++q) {
