@@ -6,8 +6,12 @@ shared library next to this file. Object files go to ``_build/`` at the
 repository root. A rebuild happens only when a source or header is newer than
 the library.
 
-The same call builds ``_lin_calls.so``, the Python extension module of the
-short calls' marshalling (csrc/lin_calls.cpp), with the host compiler.
+``build_calls()`` builds ``_lin_calls``, the Python extension module of the
+short calls' marshalling (csrc/lin_calls.cpp), with the host compiler, for the
+running interpreter and its torch (the file's name carries the interpreter's
+tag). ``build_library()`` builds it beside the library where torch is installed;
+the library itself needs neither torch nor Python's headers, and stands whether
+the module could be built or not.
 
 ``build_library(checked=True)`` builds the same sources with
 ``-DLIN_DEVICE_CHECKS=1`` into ``liblin_checked.so`` (objects in
@@ -17,10 +21,15 @@ memory, TMEM, TMA-coordinate and global indices (include/lin.h).
 
 from __future__ import annotations
 
+import importlib.metadata
+import importlib.util
+import json
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+import warnings
 
 PKG_DIR = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG_DIR)
@@ -29,7 +38,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(PKG_DIR, "liblin.so")
 CHECKED_LIB_PATH = os.path.join(PKG_DIR, "liblin_checked.so")
-CALLS_PATH = os.path.join(PKG_DIR, "_lin_calls.so")
+CALLS_PATH = os.path.join(PKG_DIR, "_lin_calls" + sysconfig.get_config_var("EXT_SUFFIX"))
+CALLS_SOURCE = os.path.join(CSRC, "lin_calls.cpp")
 
 SOURCES = ["lin_api.cu", "lin_kernels_tf32.cu", "lin_kernels_f16.cu",
            "lin_kernels_cluster_swiglu.cu", "lin_kernels_cluster_cvt.cu",
@@ -50,24 +60,47 @@ def _nvcc() -> str:
 
 def _inputs() -> list[str]:
     files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)
-             if f.endswith((".cu", ".cuh", ".h", ".cpp"))]
+             if f.endswith((".cu", ".cuh", ".h"))]
     files.append(os.path.join(INCLUDE, "lin.h"))
     files.append(os.path.abspath(__file__))
     return files
 
 
 def up_to_date(checked: bool = False) -> bool:
-    libs = [CHECKED_LIB_PATH] if checked else [LIB_PATH, CALLS_PATH]
-    if not all(os.path.exists(lib) for lib in libs):
+    lib = CHECKED_LIB_PATH if checked else LIB_PATH
+    if not os.path.exists(lib):
         return False
-    t = min(os.path.getmtime(lib) for lib in libs)
+    t = os.path.getmtime(lib)
     return all(os.path.getmtime(f) <= t for f in _inputs())
+
+
+def _calls_made_for() -> dict:
+    """What the extension module is built for, beside its sources."""
+    try:
+        version = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:   # (a torch without a record of its own)
+        version = "unknown"
+    return {"python": sys.version, "torch": version}
+
+
+def _calls_record() -> str:
+    return os.path.join(BUILD_DIR, os.path.basename(CALLS_PATH) + ".json")
+
+
+def calls_up_to_date() -> bool:
+    try:
+        with open(_calls_record()) as f:
+            if json.load(f) != _calls_made_for():
+                return False
+        t = os.path.getmtime(CALLS_PATH)
+    except (OSError, ValueError):
+        return False
+    return all(os.path.getmtime(f) <= t for f in (
+        CALLS_SOURCE, os.path.join(INCLUDE, "lin.h"), os.path.abspath(__file__)))
 
 
 def _calls_command(out: str, nvcc: str) -> list[str]:
     """The host compiler's command for the extension module."""
-    import sysconfig
-
     import torch
     root = os.path.dirname(torch.__file__)
     inc = os.path.join(root, "include")
@@ -76,15 +109,65 @@ def _calls_command(out: str, nvcc: str) -> list[str]:
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
             "-I", INCLUDE, "-I", sysconfig.get_paths()["include"], "-isystem", inc,
             "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
-            "-isystem", os.path.join(cuda, "include"), os.path.join(CSRC, "lin_calls.cpp"),
+            "-isystem", os.path.join(cuda, "include"), CALLS_SOURCE,
             "-o", out, "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
             "-lc10_cuda"]
+
+
+def _start_calls():
+    """The extension module's compilation, begun; _finish_calls() ends it."""
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    return subprocess.Popen(_calls_command(CALLS_PATH + ".tmp", _nvcc()), stdout=subprocess.PIPE,
+                            stderr=subprocess.STDOUT, text=True)
+
+
+def _finish_calls(proc) -> None:
+    out, _ = proc.communicate()
+    if proc.returncode != 0:
+        raise RuntimeError("compilation failed:\nlin_calls.cpp:\n" + out)
+    os.replace(CALLS_PATH + ".tmp", CALLS_PATH)
+    with open(_calls_record(), "w") as f:
+        json.dump(_calls_made_for(), f)
+
+
+def build_calls(force: bool = False) -> str:
+    """Compile the extension module _lin_calls; return its path. Raises on any
+    failure."""
+    if force or not calls_up_to_date():
+        _finish_calls(_start_calls())
+    return CALLS_PATH
 
 
 def build_library(force: bool = False, verbose: bool = False, extra_flags=(),
                   checked: bool = False) -> str:
     """Compile and link liblin.so (or, ``checked``, liblin_checked.so); return
-    its path. Raises on any failure."""
+    its path. Raises on any failure. The extension module _lin_calls is built
+    beside liblin.so where torch is installed; a failure of that is a warning
+    (the calls that need the module raise)."""
+    calls = problem = None
+    if not checked and importlib.util.find_spec("torch") and (force or not calls_up_to_date()):
+        try:
+            calls = _start_calls()
+        except Exception as e:  # noqa: BLE001  (whatever ails torch or the compiler)
+            problem = e
+    try:
+        path = _build_library(force, verbose, extra_flags, checked)
+    except BaseException:
+        if calls:
+            calls.kill()
+            calls.communicate()
+        raise
+    if calls:
+        try:
+            _finish_calls(calls)
+        except Exception as e:  # noqa: BLE001
+            problem = e
+    if problem:
+        warnings.warn(f"the extension module _lin_calls was not built: {problem}", stacklevel=2)
+    return path
+
+
+def _build_library(force: bool, verbose: bool, extra_flags, checked: bool) -> str:
     lib_path = CHECKED_LIB_PATH if checked else LIB_PATH
     if not force and up_to_date(checked):
         return lib_path
@@ -104,10 +187,6 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags=(),
             print(" ".join(cmd), file=sys.stderr)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE,
                                             stderr=subprocess.STDOUT, text=True)))
-    if not checked:
-        procs.append(("lin_calls.cpp", subprocess.Popen(
-            _calls_command(CALLS_PATH + ".tmp", nvcc), stdout=subprocess.PIPE,
-            stderr=subprocess.STDOUT, text=True)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -125,8 +204,6 @@ def build_library(force: bool = False, verbose: bool = False, extra_flags=(),
     if r.returncode != 0:
         raise RuntimeError("link failed:\n" + r.stdout)
     os.replace(tmp, lib_path)
-    if not checked:
-        os.replace(CALLS_PATH + ".tmp", CALLS_PATH)
     return lib_path
 
 

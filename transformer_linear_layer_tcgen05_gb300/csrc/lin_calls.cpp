@@ -12,6 +12,7 @@
 
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
+#include <torch/version.h>
 
 #include <cmath>
 #include <exception>
@@ -363,4 +364,12 @@ PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_lin_calls", nullptr, -1, kMethod
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__lin_calls() { return PyModule_Create(&kModule); }
+PyMODINIT_FUNC PyInit__lin_calls() {
+  PyObject* m = PyModule_Create(&kModule);
+  // (whose classes and ABI the module was compiled against)
+  if (m && PyModule_AddStringConstant(m, "torch_version", TORCH_VERSION) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

@@ -413,13 +413,16 @@ _calls = None
 def _short_calls():
     global _calls
     if _calls is None:
-        import torch  # noqa: F401  (loads what the module links to)
+        import torch   # (loads what the module links to)
+        how = "; build it with transformer_linear_layer_tcgen05_gb300.build.build_calls()"
         try:
             from . import _lin_calls
         except ImportError as e:
-            raise RuntimeError(
-                "_lin_calls.so is not built for this interpreter; build it with "
-                "transformer_linear_layer_tcgen05_gb300.build.build_library()") from e
+            raise RuntimeError("_lin_calls is not built for this interpreter and torch" + how) from e
+        made_for = getattr(_lin_calls, "torch_version", "an unknown one")
+        if torch.__version__.split("+")[0] != made_for:
+            raise RuntimeError(f"_lin_calls is built for torch {made_for}, not "
+                               f"{torch.__version__}" + how)
         L = lib()
         _lin_calls.bind({name: ctypes.cast(getattr(L, name), _P).value for name in (
             "lin_attention", "lin_attention_backward", "lin_qk_norm_rope",
