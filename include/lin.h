@@ -108,8 +108,11 @@
  * kernels, every shared-memory stage and buffer index, TMEM column range,
  * TMA coordinate alignment, cluster peer rank, and every global index that
  * is not a TMA access (partial tiles, row partials, transform and loss
- * loads, the rows and entries that attention and distillation write) against
- * its buffer. A failed check skips the access and records
+ * loads; rows, heads, parts and row statistics of attention; heads and angles
+ * of the norms and rotation; units and entries of distillation) against its
+ * buffer. Attention's tensor memory columns and copies' innermost coordinates
+ * are constants, checked at compile time or multiples of 64 entries. A failed
+ * check skips the access and records
  * LIN_ERROR_DEVICE_CHECK with the site and the offending value (a skipped
  * load then makes a bounded wait run out: the kernel still exits cleanly);
  * lin_get_device_status() reports it and lin_last_device_check() tells

@@ -205,6 +205,20 @@ __device__ __forceinline__ void load_row_part(uint32_t (&r)[DP / PARTS / 2], con
   }
 }
 
+// Checked build: row `token` (of the keys or the queries) and head h inside
+// their tensor; a place of the ring inside it.
+__device__ __forceinline__ bool q_row_ok(const AttnArgs& a, int64_t token, int h) {
+  return dcheck(token >= 0 && token < a.tokens_q && h >= 0 && h < a.heads_q, a.status, CHK_GLOBAL,
+                token);
+}
+__device__ __forceinline__ bool k_row_ok(const AttnArgs& a, int64_t token, int h) {
+  return dcheck(token >= 0 && token < a.tokens_k && h >= 0 && h < a.heads_q / a.group, a.status,
+                CHK_GLOBAL, token);
+}
+__device__ __forceinline__ bool stage_ok(const AttnArgs& a, int s, int stages) {
+  return dcheck(s >= 0 && s < stages, a.status, CHK_STAGE, s);
+}
+
 // Eight 16-bit entries of a row to global memory.
 __device__ __forceinline__ void store16(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   *reinterpret_cast<uint4*>(p) = make_uint4(a, b, c, d);

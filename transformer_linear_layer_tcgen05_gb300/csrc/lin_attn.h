@@ -46,6 +46,7 @@ struct AttnBwdArgs {
   const float* lse;       // [heads_q][tokens_q]
   float* delta;           // [heads_q][tokens_q]: sum of dO * O of each row
   float* norm;            // [sequences][heads_q >> shift][row tiles]: largest row norm of dO
+  int64_t norms;          // (their number)
   HeadsPtr dq, dk, dv;
   // parts of the keys for dQ and of the queries for dK, dV, and, where there
   // are several, their f32 sums [part][row][head][dim], the rows of the

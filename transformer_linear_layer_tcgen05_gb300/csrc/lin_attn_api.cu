@@ -228,6 +228,7 @@ lin_status attention_backward(const lin_attention_shape* s, const lin_heads* Q, 
   a.dv_part = a.dk_part + dk;
   a.delta = a.dv_part + dk;
   a.norm = a.delta + delta;
+  a.norms = (int64_t)norms;
   int kernels = 0;
   cudaError_t e = lin::launch_attn_bwd(s->dtype == LIN_BFLOAT16, maps, a, (int)s->heads_kv,
                                        (int)s->sequences, &kernels, stream);

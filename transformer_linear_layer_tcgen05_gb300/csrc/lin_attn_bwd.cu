@@ -154,6 +154,10 @@ struct HeadGrad {
                                       int64_t token, int h)
       : row(t.p + token * t.token_stride + (int64_t)h * t.head_stride),
         part_row(parts > 1 ? parts_base + ((part * rows + row_at) * heads + h) * dim : nullptr) {}
+  // Checked build: the row inside its part.
+  __device__ __forceinline__ bool ok(int* status, int64_t rows, int64_t row_at) const {
+    return !part_row || dcheck(row_at >= 0 && row_at < rows, status, CHK_PART, row_at);
+  }
   // N columns from c0 on, times `back` (zeros if there is nothing), those
   // below dim.
   template <bool BF16, int N>
@@ -198,8 +202,11 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   const SeqRange sq = seq_range(a.cu_q, b, a.tokens_q, a.max_q);
   const int rows = sq.len << shift;
   const int64_t norm_at = ((int64_t)b * gridDim.x + blockIdx.x) * gridDim.y + qt;
+  auto norm_ok = [&] {   // (checked build)
+    return dcheck(norm_at >= 0 && norm_at < args.norms, a.status, CHK_STATS, norm_at);
+  };
   if (r0 >= rows) {   // (the whole CTA)
-    if (threadIdx.x == 0 && part == 0) args.norm[norm_at] = 0.0f;
+    if (threadIdx.x == 0 && part == 0 && norm_ok()) args.norm[norm_at] = 0.0f;
     return;
   }
   const SeqRange sk = seq_range(a.cu_k, b, a.tokens_k, a.max_k);
@@ -247,10 +254,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       for (int j = 0; j < n; ++j, ++issued) {
         if (j >= C::N && !attn_wait(bar(C::EMPTY + r.s), r.parity ^ 1, ctl)) break;
         mbar_arrive_expect_tx(bar(C::FULL + r.s), 2 * C::TILE);
-        load_tile<DP, kTurn>(k_tile(r.s), &maps.k, hk, sk.start + (j0 + j) * kTurn,
-                             bar(C::FULL + r.s));
-        load_tile<DP, kTurn>(v_tile(r.s), &maps.v, hk, sk.start + (j0 + j) * kTurn,
-                             bar(C::FULL + r.s));
+        if (stage_ok(a, r.s, C::N) && k_row_ok(a, sk.start + (j0 + j) * kTurn, hk)) {
+          load_tile<DP, kTurn>(k_tile(r.s), &maps.k, hk, sk.start + (j0 + j) * kTurn,
+                               bar(C::FULL + r.s));
+          load_tile<DP, kTurn>(v_tile(r.s), &maps.v, hk, sk.start + (j0 + j) * kTurn,
+                               bar(C::FULL + r.s));
+        }
         r.next();
       }
       if (*abort) {   // no copy may still be in flight when the CTA ends
@@ -262,7 +271,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (n > 0 && k_left < kTurn) {   // cut the last K tile at the sequence's end (dS K runs over it)
       const int s = (n - 1) % C::N;
       if (warp_attn_wait(bar(C::FULL + s), ((n - 1) / C::N) & 1, ctl)) {
-        zero_rows<DP, kTurn>(k_tile(s), k_left, kTurn, lane);
+        if (dcheck(k_left > 0, a.status, CHK_BUFFER, k_left))
+          zero_rows<DP, kTurn>(k_tile(s), k_left, kTurn, lane);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::TAIL));
@@ -279,6 +289,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         if (!attn_wait(bar(C::FULL + next.s), next.parity, ctl) ||
             (++nj == n && k_left < kTurn && !attn_wait(bar(C::TAIL), 0, ctl)))
           return false;
+        if (!stage_ok(a, next.s, C::N)) return false;
         umma_entries_tmem<DP, kTurn, BF16>(C::S_COL + t * kTurn, kQ, k_desc + next.s * STAGE);
         umma_commit(bar(C::S_FULL + t));
         return true;
@@ -318,8 +329,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   } else if (warp < kRowWarps) {
     const int half = warp >> 2, row = tid & 127;
     const int i = (r0 + row) >> shift, h = h0 + (row & ((1 << shift) - 1));
-    const bool live = i < sq.len;
-    const int64_t token = sq.start + (live ? i : 0);
+    const int64_t token = sq.start + (i < sq.len ? i : 0);
+    const bool live = i < sq.len && q_row_ok(a, token, h);
     const float c = a.scale * kLog2E;
     // The row's Q and dO into tensor memory; delta and the norm of dO on the
     // way: each of the row's two threads has half of the entries.
@@ -364,7 +375,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if (lane == 0) red2[warp] = big;
     }
     named_bar_sync(1, 256);
-    if (tid == 0 && part == 0)
+    if (tid == 0 && part == 0 && norm_ok())
       args.norm[norm_at] = fmaxf(fmaxf(red2[0], red2[1]), fmaxf(red2[2], red2[3]));
     const int ne = norm_exponent(norm);
     const float amp = pow2i(ne);
@@ -482,7 +493,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           tmem_ld_32x32b_x16(tmem + lanes + C::OUT_COL + c0, o);
           tmem_wait_ld_x16(o);
         }
-        const bool put = live && dcheck(token < a.tokens_q, a.status, CHK_GLOBAL, token);
+        const bool put = live && out.ok(a.status, args.q_part_rows, (int64_t)b * a.max_q + i);
         out.put<BF16>(o, n > 0, back, c0, put ? a.dim : 0);
       }
     }
@@ -578,7 +589,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     const float* nm = args.norm + ((int64_t)b * gridDim.x + hk) * tiles * passes;
     float big = 0.0f;
     for (int p = 0; p < passes; ++p, nm += tiles)
-      for (int i = t0 * kTurn / 128 + lane; i < tiles; i += 32) big = fmaxf(big, nm[i]);
+      for (int i = t0 * kTurn / 128 + lane; i < tiles; i += 32)
+        if (dcheck(nm + i < args.norm + args.norms, a.status, CHK_STATS, nm + i - args.norm))
+          big = fmaxf(big, nm[i]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, o));
     return norm_exponent(big);
@@ -607,8 +620,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
           const int z = sq.start + ((t0 + tile) * kTurn >> shift);
           if (it >= C::N && !attn_wait(bar(C::EMPTY + r.s), r.parity ^ 1, ctl)) break;
           mbar_arrive_expect_tx(bar(C::FULL + r.s), 2 * C::TILE);
-          load_tile<DP, kTurn>(q_tile(r.s), &maps.q, h, z, bar(C::FULL + r.s));
-          load_tile<DP, kTurn>(do_tile(r.s), &maps.dout, h, z, bar(C::FULL + r.s));
+          if (stage_ok(a, r.s, C::N) && q_row_ok(a, z, h + (1 << shift) - 1)) {
+            load_tile<DP, kTurn>(q_tile(r.s), &maps.q, h, z, bar(C::FULL + r.s));
+            load_tile<DP, kTurn>(do_tile(r.s), &maps.dout, h, z, bar(C::FULL + r.s));
+          }
           r.next();
           if (++tile == per) {
             tile = 0;
@@ -638,10 +653,11 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
 #pragma unroll
       for (int e = 0; e < N; ++e) {
         const int r = (t0 + tile) * kTurn + e * 32 + lane, i = r >> shift;
-        const int64_t at =
-            (int64_t)(h + (r & ((1 << shift) - 1))) * a.tokens_q + sq.start + i;
-        lse[e] = i < sq.len ? args.lse[at] : -INFINITY;
-        delta[e] = i < sq.len ? args.delta[at] : 0.0f;
+        const int hr = h + (r & ((1 << shift) - 1));
+        const int64_t at = (int64_t)hr * a.tokens_q + sq.start + i;
+        const bool in = i < sq.len && q_row_ok(a, sq.start + i, hr);
+        lse[e] = in ? args.lse[at] : -INFINITY;
+        delta[e] = in ? args.delta[at] : 0.0f;
       }
       if (++tile == per) {
         tile = 0;
@@ -678,14 +694,15 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       RingAt<C::N> r;
       for (int it = 0; it < n; ++it) {
         if (!warp_attn_wait(bar(C::FULL + r.s), r.parity, ctl)) break;
-        if (tile == 0 && q_none > 0) {
+        if (tile == 0 && q_none > 0 && stage_ok(a, r.s, C::N) &&
+            dcheck(q_none < kTurn, a.status, CHK_BUFFER, q_none)) {
           zero_rows<DP, kTurn>(q_tile(r.s), 0, q_none, lane);
           zero_rows<DP, kTurn>(do_tile(r.s), 0, q_none, lane);
           fence_proxy_async_smem();
         }
         if (++tile == per) {
           tile = 0;
-          if (q_left < kTurn) {
+          if (q_left < kTurn && dcheck(q_left > 0, a.status, CHK_BUFFER, q_left)) {
             zero_rows<DP, kTurn>(q_tile(r.s), q_left, kTurn, lane);
             zero_rows<DP, kTurn>(do_tile(r.s), q_left, kTurn, lane);
             fence_proxy_async_smem();
@@ -712,6 +729,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       };
       auto scores = [&](int t) -> bool {   // S^T = K Q^T of the next turn
         if (!attn_wait(bar(ready + next.s), next.parity, ctl)) return false;
+        if (!stage_ok(a, next.s, C::N)) return false;
         own(C::S_COL + t * kTurn, kK, k_own, q_desc + next.s * STAGE);
         umma_commit(bar(C::S_FULL + t));
         return true;
@@ -752,7 +770,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   } else if (warp < kRowWarps) {
     const int half = warp >> 2, row = tid & 127;
     const int key = k0 + row;
-    const bool live = key < sk.len;
+    const bool live = key < sk.len && k_row_ok(a, (int64_t)sk.start + key, hk);
     const float c = a.scale * kLog2E;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t s_col = tmem + lanes + C::S_COL + half * kTurn;
@@ -892,7 +910,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
           tmem_ld_32x32b_x32(tmem + lanes + C::OUT_COL + half * DP + q * 32, o);
           tmem_wait_ld_x32(o);
         }
-        const bool put = live && dcheck(sk.start + key < a.tokens_k, a.status, CHK_GLOBAL, sk.start + key);
+        const bool put = live && out.ok(a.status, args.k_part_rows, (int64_t)b * a.max_k + key);
         out.put<BF16>(o, n > 0, back, q * 32, put ? a.dim : 0);
       }
     }
@@ -913,6 +931,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
 // rows of a sequence and head, eight entries to a thread.
 struct SumParts {
   const int32_t* cu;
+  int* status;
   int32_t tokens, most, dim, parts, sequences;
   const float* part[2];
   HeadsPtr out[2];
@@ -931,6 +950,7 @@ __global__ void __launch_bounds__(256)
     const int i = blockIdx.y * 32 + k / groups, col = k % groups * 8;
     if (i >= r.len) continue;
     const int64_t token = (int64_t)r.start + i;
+    if (!dcheck(token < a.tokens && i < a.most, a.status, CHK_GLOBAL, token)) continue;
     const float* p = a.part[which] + (((int64_t)b * a.most + i) * heads + h) * a.dim + col;
     const int64_t step = (int64_t)a.sequences * a.most * heads * a.dim;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
@@ -1020,11 +1040,11 @@ cudaError_t launch_attn_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArg
   };
   cudaError_t e = bf16 ? dims(std::true_type{}) : dims(std::false_type{});
   if (e == cudaSuccess && args.q_parts > 1)
-    e = sum(SumParts{args.s.cu_q, args.s.tokens_q, args.s.max_q, args.s.dim, args.q_parts, sequences,
+    e = sum(SumParts{args.s.cu_q, args.s.status, args.s.tokens_q, args.s.max_q, args.s.dim, args.q_parts, sequences,
                      {args.dq_part, nullptr}, {args.dq, args.dq}},
             hq, 1);
   if (e == cudaSuccess && args.k_parts > 1)
-    e = sum(SumParts{args.s.cu_k, args.s.tokens_k, args.s.max_k, args.s.dim, args.k_parts, sequences,
+    e = sum(SumParts{args.s.cu_k, args.s.status, args.s.tokens_k, args.s.max_k, args.s.dim, args.k_parts, sequences,
                      {args.dk_part, args.dv_part}, {args.dk, args.dv}},
             hk, 2);
   return e;

@@ -80,6 +80,7 @@ struct FwdCfg {
   // tensor memory columns: S (and P over it) of the two tiles, O, P
   static constexpr uint32_t S_COL = 0, O_COL = 256;
   static constexpr uint32_t p_col(int t) { return AHEAD ? 384 + t * 64 : S_COL + t * 128; }
+  static_assert(O_COL >= S_COL + 256 && O_COL + 2 * DP <= (AHEAD ? 384u : 512u), "tensor memory");
 };
 
 // Key tiles that the queries [i0, i0 + n) of a sequence need.
@@ -156,24 +157,28 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         bool second = false;
         if (n0 > 0) {   // (the first rows of a causal mask may see no key at all)
           mbar_arrive_expect_tx(bar(C::Q_FULL), q_bytes);
-          load_tile<DP, 128>(base + C::OFF_Q, &maps.q, h0, z, bar(C::Q_FULL));
+          if (dcheck(q_bytes <= C::TILE, a.status, CHK_BUFFER, q_bytes) && q_row_ok(a, z, h0 + pack - 1))
+            load_tile<DP, 128>(base + C::OFF_Q, &maps.q, h0, z, bar(C::Q_FULL));
         }
         for (int j = 0; j < n; ++j) {
           const int s = j % C::NKV, round = j / C::NKV;
           if (round > 0 && !attn_wait(bar(C::K_EMPTY + s), (round - 1) & 1, ctl)) break;
           mbar_arrive_expect_tx(bar(C::K_FULL + s), C::TILE);
-          load_tile<DP, 128>(base + C::OFF_K + s * C::TILE, &maps.k, hk, sk.start + (j0 + j) * 128,
-                        bar(C::K_FULL + s));
+          if (stage_ok(a, s, C::NKV) && k_row_ok(a, sk.start + (j0 + j) * 128, hk))
+            load_tile<DP, 128>(base + C::OFF_K + s * C::TILE, &maps.k, hk,
+                               sk.start + (j0 + j) * 128, bar(C::K_FULL + s));
           ++k_issued;
           if (j == 0 && n1 > 0) {
             mbar_arrive_expect_tx(bar(C::Q_FULL + 1), q_bytes);
-            load_tile<DP, 128>(base + C::OFF_Q + C::TILE, &maps.q, h0, z + tile_q, bar(C::Q_FULL + 1));
+            if (q_row_ok(a, z + tile_q, h0 + pack - 1))
+              load_tile<DP, 128>(base + C::OFF_Q + C::TILE, &maps.q, h0, z + tile_q, bar(C::Q_FULL + 1));
             second = true;
           }
           if (round > 0 && !attn_wait(bar(C::V_EMPTY + s), (round - 1) & 1, ctl)) break;
           mbar_arrive_expect_tx(bar(C::V_FULL + s), C::TILE);
-          load_tile<DP, 128>(base + C::OFF_V + s * C::TILE, &maps.v, hk, sk.start + (j0 + j) * 128,
-                        bar(C::V_FULL + s));
+          if (stage_ok(a, s, C::NKV))
+            load_tile<DP, 128>(base + C::OFF_V + s * C::TILE, &maps.v, hk,
+                               sk.start + (j0 + j) * 128, bar(C::V_FULL + s));
           ++v_issued;
         }
         // no copy may still be in flight when the CTA ends (after a wait that
@@ -191,7 +196,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (n > 0 && v_left < 128) {   // cut the last V tile at the sequence's end
         const int s = (n - 1) % C::NKV;
         if (warp_wait_phase<kAttnNapNs>(bar(C::V_FULL + s), ((n - 1) / C::NKV) & 1, ctl)) {
-          zero_rows<DP, 128>(base + C::OFF_V + s * C::TILE, v_left, 128, lane);
+          if (dcheck(v_left > 0, a.status, CHK_BUFFER, v_left))
+            zero_rows<DP, 128>(base + C::OFF_V + s * C::TILE, v_left, 128, lane);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(bar(C::TAIL));
@@ -203,6 +209,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const uint64_t k_desc = AttnTile<DP>::k_major(base + C::OFF_K);
         const uint64_t v_desc = AttnTile<DP>::mn_major(base + C::OFF_V);
         auto scores = [&](int t, int s) {   // S_t = Q_t K^T, K in stage s
+          if (!stage_ok(a, s, C::NKV)) return;
           umma_entries<DP, BF16>(C::S_COL + t * 128, q_desc + t * AttnTile<DP>::UNITS,
                                  k_desc + s * AttnTile<DP>::UNITS);
           umma_commit(bar(C::S_FULL + t));
@@ -238,7 +245,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
               ok = ok && attn_wait(bar(C::P_READY + 2 * t + half), j & 1, ctl);
-              if (!ok) break;
+              if (!ok || !stage_ok(a, s, C::NKV)) break;
               tc_fence_after_sync();
               umma_tokens<DP, BF16, 4>(C::O_COL + t * DP, C::p_col(t) + half * 32,
                                        v_desc + s * AttnTile<DP>::UNITS, half * 4,
@@ -395,7 +402,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const float x = __uint_as_float(o[g * 8 + 2 * e]), y = __uint_as_float(o[g * 8 + 2 * e + 1]);
             w[e] = nk > 0 ? pack16<BF16>(l == 0.0f ? 0.0f : x * inv, l == 0.0f ? 0.0f : y * inv) : 0u;
           }
-          if (!live || col >= a.dim || !dcheck(token < a.tokens_q, a.status, CHK_GLOBAL, token)) continue;
+          if (!live || col >= a.dim || !q_row_ok(a, token, h)) continue;
+          if (parts > 1 && !dcheck(row_at < args.part_rows && at.part < parts, a.status, CHK_PART, row_at))
+            continue;
           if (parts > 1) {   // in f32
             const float z = nk > 0 ? inv : 0.0f;
             float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
@@ -413,7 +422,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           }
         }
       }
-      if (live) *lse = l == 0.0f ? -INFINITY : m * a.scale + logf(l);
+      if (live && q_row_ok(a, token, h)) *lse = l == 0.0f ? -INFINITY : m * a.scale + logf(l);
     }
   }
   __syncwarp();
@@ -441,6 +450,7 @@ __global__ void __launch_bounds__(256)
     if (i >= r.len) continue;
     const int64_t token = (int64_t)r.start + i;
     const int64_t row_at = (int64_t)blockIdx.z * a.max_q + i;
+    if (!q_row_ok(a, token, h) || !dcheck(row_at < args.part_rows, a.status, CHK_PART, row_at)) continue;
     const float* ls = args.lse_part + h * args.part_rows + row_at;
     const int64_t ls_step = a.heads_q * args.part_rows;
     float top = -INFINITY;

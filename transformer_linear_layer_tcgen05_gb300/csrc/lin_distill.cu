@@ -92,6 +92,16 @@ __global__ void __launch_bounds__(distill_threads(WARPS), distill_ctas(WARPS))
   __shared__ volatile int abort;
   extern __shared__ float4 ring[];       // slots x tile units, then kEnt x (ids, p, z)[KP]
   const int KP = (a.K + 3) & ~3;         // (whole groups of four, the last one padded with -1)
+#if LIN_DEVICE_CHECKS
+  {   // the slots and the entries inside what the launch gave
+    uint32_t given;
+    asm volatile("mov.u32 %0, %%dynamic_smem_size;" : "=r"(given));
+    const int64_t want = (int64_t)a.slots * a.tile * 16 + (int64_t)kEnt * KP * 12;
+    if (!dcheck(want <= given && a.slots >= 1 && a.slots <= kSlots && a.cluster <= kMaxCluster, a.status,
+                CHK_BUFFER, want))
+      return;   // (every thread of every CTA)
+  }
+#endif
   int* const ids = reinterpret_cast<int*>(ring + a.slots * a.tile);
   float* const ps = reinterpret_cast<float*>(ids + kEnt * KP);
   float* const zs = ps + kEnt * KP;
@@ -243,6 +253,13 @@ __global__ void __launch_bounds__(distill_threads(WARPS), distill_ctas(WARPS))
   int64_t load_row = row0;
   int load_job = 0, loads = 0, load_slot = 0;
   auto unit_begin = [&](int seg) { return (seg * C + rank) * a.tile; };
+  // Checked build: units lo .. hi - 1 inside the row and the part that begins
+  // at u0, the slot inside the ring.
+  auto units_ok = [&](const Row& r, int u0, int lo, int hi, int slot) -> bool {
+    return dcheck(lo >= u0 && hi - u0 <= a.tile && 4 * (int64_t)lo >= r.phase &&
+                      4 * (int64_t)hi - r.phase <= V, a.status, CHK_GLOBAL, lo) &&
+           dcheck(slot >= 0 && slot < a.slots, a.status, CHK_STAGE, slot);
+  };
   auto issue = [&]() {   // (thread 0) the next copy into its slot
     if (load_row >= a.M) return;
     const int seg = load_job < S ? load_job : load_job - S;
@@ -251,7 +268,7 @@ __global__ void __launch_bounds__(distill_threads(WARPS), distill_ctas(WARPS))
     const int lo = max(u0, r.full0), hi = min(min(u0 + a.tile, r.units), r.full1);
     const uint32_t bytes = hi > lo ? (uint32_t)(hi - lo) * 16u : 0u;
     mbar_arrive_expect_tx(full + 8 * load_slot, bytes);
-    if (bytes)
+    if (bytes && units_ok(r, u0, lo, hi, load_slot))
       bulk_load(smem_u32(ring + load_slot * a.tile + (lo - u0)), r.unit0 + (int64_t)lo * 4, bytes,
                 full + 8 * load_slot);
     ++loads;
@@ -308,7 +325,9 @@ __global__ void __launch_bounds__(distill_threads(WARPS), distill_ctas(WARPS))
     for (int seg = 0; seg < S; ++seg) {
       ok = ok && wait_copy(at_sums);
       const int u0 = unit_begin(seg), u1 = min(u0 + a.tile, r.units);
-      const int lo = max(u0, r.full0), hi = ok ? min(u1, r.full1) : 0;
+      const int lo = max(u0, r.full0);
+      int hi = ok ? min(u1, r.full1) : 0;
+      if (hi > lo && !units_ok(r, u0, lo, hi, at_sums.slot)) hi = 0;
       const float4* slot = ring + at_sums.slot * a.tile - u0;
       auto add = [&](const float4* x, int count) {   // (count: a constant)
         float mx = m;
@@ -363,7 +382,7 @@ __global__ void __launch_bounds__(distill_threads(WARPS), distill_ctas(WARPS))
       m = lane < WARPS ? red[it % kRed][lane].x : kLowest;
       s = lane < WARPS ? red[it % kRed][lane].y : 0.0f;
       warp_join(m, s, c);
-      if (lane < C && ok) {
+      if (lane < C && ok && dcheck(rank < kMaxCluster, a.status, CHK_PEER, rank)) {
         const int e = it % kExch;
         const uint32_t to = mapa_shared(smem_u32(&stats[e][rank]), (uint32_t)lane);
         asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(to), "f"(m), "f"(s) : "memory");
@@ -390,7 +409,7 @@ __global__ void __launch_bounds__(distill_threads(WARPS), distill_ctas(WARPS))
     const float ls = log2f(s);   // the row's log-sum-exp less its maximum, base 2
     const float4 tp = teacher[b];
     const bool any = tp.z != 0.0f;
-    if (rank == 0 && tid == 0 && ok)
+    if (rank == 0 && tid == 0 && ok && dcheck(i >= 0 && i < a.M, a.status, CHK_GLOBAL, i))
       a.losses[i] = any ? a.tau * a.tau * kDLn2 * (tp.x - (tp.y + (tp.w - m)) * c + ls) : 0.0f;
     if (a.dlogits) {
       const float* row = a.logits + i * a.ld;
@@ -404,7 +423,9 @@ __global__ void __launch_bounds__(distill_threads(WARPS), distill_ctas(WARPS))
         Cursor& at = twice ? at_sums : at_grad;
         if (twice) ok = ok && wait_copy(at);
         const int u0 = unit_begin(seg), u1 = min(u0 + a.tile, r.units);
-        const int lo = max(u0, r.full0), hi = ok ? min(u1, r.full1) : 0;
+        const int lo = max(u0, r.full0);
+        int hi = ok ? min(u1, r.full1) : 0;
+        if (hi > lo && !units_ok(r, u0, lo, hi, at.slot)) hi = 0;
         const float4* slot = ring + at.slot * a.tile - u0;
         const int ve = ok ? edge_entry(r, u0, u1) : -1;
         const float edge = ve >= 0 ? row[ve] : 0.0f;   // (before it may be overwritten)

@@ -107,6 +107,16 @@ __device__ __forceinline__ int64_t table_row(const RopeArgs& a, int64_t t) {
   return min(max(p, (int64_t)0), (int64_t)a.table_rows - 1);
 }
 
+// Checked build: head `head` of token t inside the tensors; a lane's entries
+// inside the head; four angles inside the tables.
+__device__ __forceinline__ bool head_ok(const RopeArgs& a, int64_t t, int head, const Place& at) {
+  return dcheck(t >= 0 && t < a.tokens && head >= 0 && head < a.hq + 2 * a.hk, a.status, CHK_GLOBAL, t) &&
+         dcheck(at.o0 + 4 <= a.dim && at.o1 + 4 <= a.dim, a.status, CHK_GLOBAL, at.o1);
+}
+__device__ __forceinline__ bool angles_ok(const RopeArgs& a, int64_t row) {
+  return dcheck(row >= 0 && row + 4 <= a.table_rows * (a.rot / 2), a.status, CHK_GLOBAL, row);
+}
+
 // The 16-bit head `head` (of q, k and v in a row) of token t.
 __device__ __forceinline__ uint16_t* head16(const RopeArgs& a, int64_t t, int head) {
   if (head < a.hq) return a.q.p + t * a.q.token_stride + (int64_t)head * a.q.head_stride;
@@ -131,12 +141,16 @@ __global__ void __launch_bounds__(kRopeThreads, kFwdCtas)
   Eight x[kFwdHeads];
 #pragma unroll
   for (int i = 0; i < kFwdHeads; ++i)
-    x[i] = at.on && h0 + i < heads ? load8f(a.x + (t * heads + h0 + i) * a.dim, at) : Eight{};
+    x[i] = at.on && h0 + i < heads && head_ok(a, t, h0 + i, at)
+               ? load8f(a.x + (t * heads + h0 + i) * a.dim, at)
+               : Eight{};
   float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
   if (at.on && at.turned && h0 < heads) {
     const int64_t row = table_row(a, t) * (a.rot / 2) + at.pair;
-    c = *reinterpret_cast<const float4*>(a.cos + row);
-    s = *reinterpret_cast<const float4*>(a.sin + row);
+    if (angles_ok(a, row)) {
+      c = *reinterpret_cast<const float4*>(a.cos + row);
+      s = *reinterpret_cast<const float4*>(a.sin + row);
+    }
   }
   float r[kFwdHeads];
 #pragma unroll
@@ -149,7 +163,7 @@ __global__ void __launch_bounds__(kRopeThreads, kFwdCtas)
 #pragma unroll
   for (int i = 0; i < kFwdHeads; ++i) {
     const int h = h0 + i;
-    if (!at.on || h >= heads) continue;
+    if (!at.on || h >= heads || !head_ok(a, t, h, at)) continue;
     if (h < a.hq + a.hk) {
       const Eight w = load8f(h < a.hq ? a.wq : a.wk, at);
 #pragma unroll
@@ -196,12 +210,13 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdCtas)
 #pragma unroll
     for (int i = 0; i < kBwdHeads; ++i) {
       const int h = h0 + i;
-      x[i] = at.on && h < h_hi && h < a.hq + a.hk ? load8f(xt + i * a.dim, at) : Eight{};
+      x[i] = at.on && h < h_hi && h < a.hq + a.hk && head_ok(a, t, h, at) ? load8f(xt + i * a.dim, at)
+                                                                          : Eight{};
     }
 #pragma unroll
     for (int i = 0; i < kBwdHeads; ++i) {
       g[i] = Eight{};
-      if (!at.on || h0 + i >= h_hi) continue;
+      if (!at.on || h0 + i >= h_hi || !head_ok(a, t, h0 + i, at)) continue;
       const uint16_t* y = head16(a, t, h0 + i);
       const uint2 u0 = *reinterpret_cast<const uint2*>(y + at.o0);
       const uint2 u1 = *reinterpret_cast<const uint2*>(y + at.o1);
@@ -216,8 +231,10 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdCtas)
     float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (at.on && at.turned && h0 < h_hi) {
       const int64_t row = table_row(a, t) * (a.rot / 2) + at.pair;
-      c = *reinterpret_cast<const float4*>(a.cos + row);
-      s = *reinterpret_cast<const float4*>(a.sin + row);
+      if (angles_ok(a, row)) {
+        c = *reinterpret_cast<const float4*>(a.cos + row);
+        s = *reinterpret_cast<const float4*>(a.sin + row);
+      }
     }
     float* out = a.dx + (t * heads + h0) * a.dim;
 #pragma unroll
@@ -234,7 +251,7 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdCtas)
       sg = group_sum<G>(sg);
       const float r = rsqrtf(fmaf(ss, inv_dim, a.eps));
       const float k = sg * r * r * inv_dim;   // mean(g n) / sqrt(...)
-      if (!at.on || h0 + i >= h_hi) continue;
+      if (!at.on || h0 + i >= h_hi || !head_ok(a, t, h0 + i, at)) continue;
       if (normed) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -252,7 +269,7 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdCtas)
       ++t;
     }
   }
-  if (at.on) {
+  if (at.on && dcheck(at.o1 + 4 <= G * 8, a.status, CHK_BUFFER, at.o1)) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       part[group][at.o0 + e] = dw.v[e];

@@ -22,6 +22,7 @@ struct RopeArgs {
   float *dwq, *dwk;       // gradient: [dim]
   float* partial;         // gradient: [CTAs][dim]
   int32_t q_ctas;         // gradient: CTAs that take the query heads (set with their number)
+  int* status;            // device status record (checked build)
 };
 
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, bool inter, bool bf16, cudaStream_t stream);

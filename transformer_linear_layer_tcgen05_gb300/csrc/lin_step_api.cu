@@ -119,6 +119,7 @@ lin_status qk_norm_rope(const lin_qk_norm_rope_shape* s, const float* X, const f
   a.dim = (int32_t)s->dim;
   a.rot = (int32_t)s->rot;
   a.eps = s->eps;
+  a.status = word;
   a.q = heads_ptr(v[0]);
   a.k = heads_ptr(v[1]);
   a.v = heads_ptr(v[2]);
