@@ -30,9 +30,9 @@ struct AttnFwdArgs {
   float* lse;   // [heads_q][tokens_q]
   // parts of the keys, and, where there are several, their results in f32:
   // [part][row][head][dim], [part][head][row], the rows of the sequences one
-  // after another, max_q to each (part_rows in all)
-  int32_t parts;
-  int64_t part_rows;
+  // after another, max_q to each (part_rows in all; with at most half as many
+  // CTAs as SMs, parts hold some million entries: 32-bit indices)
+  int32_t parts, part_rows;
   float *o_part, *lse_part;
   // tiles of a CTA (1 or 2), query heads of a tile (1, or all that share a key
   // head), and its queries: 128 / pack
@@ -52,7 +52,7 @@ struct AttnBwdArgs {
   // are several, their f32 sums [part][row][head][dim], the rows of the
   // sequences one after another, max_q (max_k) to each
   int32_t q_parts, k_parts;
-  int64_t q_part_rows, k_part_rows;
+  int32_t q_part_rows, k_part_rows;
   // log2 of the query heads that are rows of one tile: 1, or all that share a
   // key head
   int32_t shift;

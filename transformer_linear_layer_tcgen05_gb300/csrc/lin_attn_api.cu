@@ -114,7 +114,7 @@ lin_status attention(const lin_attention_shape* s, const lin_heads* Q, const lin
   const lin_status st = check_attention(s, v, 4, LSE, true, &c);
   if (st != LIN_SUCCESS) return st;
   if (c.nothing || c.max_q == 0) return LIN_SUCCESS;
-  lin::AttnFwdArgs a{attn_args(s, c), heads_ptr(v[3]), LSE, 1, s->sequences * c.max_q, nullptr,
+  lin::AttnFwdArgs a{attn_args(s, c), heads_ptr(v[3]), LSE, 1, 0, nullptr,
                      nullptr, 2, 1, 128};
   const int sms = sm_count(c.dev);
   auto tiles = [&] {
@@ -141,6 +141,7 @@ lin_status attention(const lin_attention_shape* s, const lin_heads* Q, const lin
   if (a.tiles == 1)
     a.parts = lin::attn_parts((c.max_q + rows - 1) / rows * (s->heads_q / a.pack) * s->sequences,
                               c.max_k, sms);
+  if (a.parts > 1) a.part_rows = (int32_t)(s->sequences * c.max_q);
   lin::AttnFwdMaps maps;
   bool ok = encode_view(&maps.q, v[0], s->dim, a.tile_q, a.pack);
   // without keys the K and V maps are never used
@@ -214,10 +215,10 @@ lin_status attention_backward(const lin_attention_shape* s, const lin_heads* Q, 
   a.k_parts = lin::attn_parts(tk * s->heads_kv * s->sequences, c.max_q * (int64_t)a.s.group, sms);
   // workspace: the parts' sums, delta [heads][tokens], then the largest dO
   // norms of the query tiles
-  a.q_part_rows = s->sequences * c.max_q;
-  a.k_part_rows = s->sequences * c.max_k;
-  const uint64_t dq = a.q_parts > 1 ? (uint64_t)(a.q_parts * a.q_part_rows * s->heads_q * s->dim) : 0;
-  const uint64_t dk = a.k_parts > 1 ? (uint64_t)(a.k_parts * a.k_part_rows * s->heads_kv * s->dim) : 0;
+  if (a.q_parts > 1) a.q_part_rows = (int32_t)(s->sequences * c.max_q);
+  if (a.k_parts > 1) a.k_part_rows = (int32_t)(s->sequences * c.max_k);
+  const uint64_t dq = (uint64_t)a.q_parts * a.q_part_rows * s->heads_q * s->dim;
+  const uint64_t dk = (uint64_t)a.k_parts * a.k_part_rows * s->heads_kv * s->dim;
   const uint64_t delta = (uint64_t)s->heads_q * (uint64_t)s->tokens_q;
   const uint64_t norms = (uint64_t)s->sequences * (uint64_t)hq_tiles * (uint64_t)tq;
   const size_t bytes = (size_t)std::max<uint64_t>(16, (dq + 2 * dk + delta + norms) * 4);

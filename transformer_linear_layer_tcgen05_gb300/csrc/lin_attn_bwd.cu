@@ -150,12 +150,12 @@ struct HeadGrad {
   uint16_t* row;
   float* part_row;
   __device__ __forceinline__ HeadGrad(const HeadsPtr& t, float* parts_base, int parts, int part,
-                                      int64_t rows, int64_t row_at, int heads, int dim,
+                                      int rows, int row_at, int heads, int dim,
                                       int64_t token, int h)
       : row(t.p + token * t.token_stride + (int64_t)h * t.head_stride),
         part_row(parts > 1 ? parts_base + ((part * rows + row_at) * heads + h) * dim : nullptr) {}
   // Checked build: the row inside its part.
-  __device__ __forceinline__ bool ok(int* status, int64_t rows, int64_t row_at) const {
+  __device__ __forceinline__ bool ok(int* status, int rows, int row_at) const {
     return !part_row || dcheck(row_at >= 0 && row_at < rows, status, CHK_PART, row_at);
   }
   // N columns from c0 on, times `back` (zeros if there is nothing), those
@@ -484,7 +484,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (ok) {
       const float back = a.scale * pow2i(-ne);
       const HeadGrad out(args.dq, args.dq_part, args.q_parts, part, args.q_part_rows,
-                         (int64_t)b * a.max_q + i, a.heads_q, a.dim, token, h);
+                         b * a.max_q + i, a.heads_q, a.dim, token, h);
 #pragma unroll
       for (int q = 0; q < DP / 32; ++q) {
         const int c0 = half * (DP / 2) + q * 16;
@@ -493,7 +493,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           tmem_ld_32x32b_x16(tmem + lanes + C::OUT_COL + c0, o);
           tmem_wait_ld_x16(o);
         }
-        const bool put = live && out.ok(a.status, args.q_part_rows, (int64_t)b * a.max_q + i);
+        const bool put = live && out.ok(a.status, args.q_part_rows, b * a.max_q + i);
         out.put<BF16>(o, n > 0, back, c0, put ? a.dim : 0);
       }
     }
@@ -901,7 +901,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     if (ok) {   // the first half's threads write dV, the others dK
       const float back = half == 0 ? pow2i(-(int)kPShift) : a.scale * pow2i(-ne);
       const HeadGrad out(half == 0 ? args.dv : args.dk, half == 0 ? args.dv_part : args.dk_part,
-                         args.k_parts, part, args.k_part_rows, (int64_t)b * a.max_k + key,
+                         args.k_parts, part, args.k_part_rows, b * a.max_k + key,
                          a.heads_q / a.group, a.dim, (int64_t)sk.start + (live ? key : 0), hk);
 #pragma unroll
       for (int q = 0; q < DP / 32; ++q) {
@@ -910,7 +910,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
           tmem_ld_32x32b_x32(tmem + lanes + C::OUT_COL + half * DP + q * 32, o);
           tmem_wait_ld_x32(o);
         }
-        const bool put = live && out.ok(a.status, args.k_part_rows, (int64_t)b * a.max_k + key);
+        const bool put = live && out.ok(a.status, args.k_part_rows, b * a.max_k + key);
         out.put<BF16>(o, n > 0, back, q * 32, put ? a.dim : 0);
       }
     }
@@ -929,10 +929,11 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
 // Gradients from their parts' f32 sums [part][row][head][dim], added in
 // order: one, or (dK and dV) two of the same shape in one launch. A CTA per 32
 // rows of a sequence and head, eight entries to a thread.
-struct SumParts {
+struct SumParts {   // (step: entries of a part)
   const int32_t* cu;
   int* status;
   int32_t tokens, most, dim, parts, sequences;
+  int64_t step;
   const float* part[2];
   HeadsPtr out[2];
 };
@@ -951,11 +952,10 @@ __global__ void __launch_bounds__(256)
     if (i >= r.len) continue;
     const int64_t token = (int64_t)r.start + i;
     if (!dcheck(token < a.tokens && i < a.most, a.status, CHK_GLOBAL, token)) continue;
-    const float* p = a.part[which] + (((int64_t)b * a.most + i) * heads + h) * a.dim + col;
-    const int64_t step = (int64_t)a.sequences * a.most * heads * a.dim;
+    const float* p = a.part[which] + ((b * a.most + i) * heads + h) * a.dim + col;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
 #pragma unroll 4
-    for (int q = 0; q < a.parts; ++q, p += step) {
+    for (int q = 0; q < a.parts; ++q, p += a.step) {
       const float4 u = __ldcs(reinterpret_cast<const float4*>(p));
       const float4 v = __ldcs(reinterpret_cast<const float4*>(p) + 1);
       x = make_float4(x.x + u.x, x.y + u.y, x.z + u.z, x.w + u.w);
@@ -1041,11 +1041,11 @@ cudaError_t launch_attn_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArg
   cudaError_t e = bf16 ? dims(std::true_type{}) : dims(std::false_type{});
   if (e == cudaSuccess && args.q_parts > 1)
     e = sum(SumParts{args.s.cu_q, args.s.status, args.s.tokens_q, args.s.max_q, args.s.dim, args.q_parts, sequences,
-                     {args.dq_part, nullptr}, {args.dq, args.dq}},
+                     (int64_t)args.q_part_rows * (int)hq * args.s.dim, {args.dq_part, nullptr}, {args.dq, args.dq}},
             hq, 1);
   if (e == cudaSuccess && args.k_parts > 1)
     e = sum(SumParts{args.s.cu_k, args.s.status, args.s.tokens_k, args.s.max_k, args.s.dim, args.k_parts, sequences,
-                     {args.dk_part, args.dv_part}, {args.dk, args.dv}},
+                     (int64_t)args.k_part_rows * (int)hk * args.s.dim, {args.dk_part, args.dv_part}, {args.dk, args.dv}},
             hk, 2);
   return e;
 }
