@@ -34,14 +34,16 @@
 // spares shared memory the reading of them; dK and dV of more than 64 entries
 // leave no room for that.
 //
-// What bounds it. 8192 causal tokens, 16 heads of 128: 633-638 us, 1080 TF/s
-// of the five products that the gradient needs and 1510 of the seven that the
-// two kernels execute, 0.78 of the cuBLAS burst rate under the same power
-// limit as the forward kernel. Adding dQ up over the key tiles in one kernel
-// of five products would want atomics, whose order changes the sums. Heads of
-// 64, same lengths: 467 us, 0.53 of that rate: the element-wise work of a
-// turn and the latencies between the roles. Short calls: 512 tokens, 12 heads
-// 19 us, two kernels of four to eight turns each behind one another.
+// What bounds it. 8192 causal tokens, 16 heads of 128: 618-623 us, 1105 TF/s
+// of the five products that the gradient needs and 1550 of the seven that the
+// two kernels execute, 0.80 of the cuBLAS burst rate under the same power
+// limit as the forward kernel. One kernel of five products would have to add
+// dQ up over the key tiles: with atomics the order of the sums changes, and
+// adds in a fixed order were not tried. Heads of 64, same lengths: 466 us,
+// 0.53 of that rate: the element-wise work of a turn and the latencies between
+// the roles. Short calls: 512 tokens, 12 heads 19 us, two kernels of four to
+// eight turns each behind one another: the second needs no more of the first
+// than delta and the norms of dO, but waits for its end.
 //
 // Where there are fewer tiles than SMs the other side is cut into parts, a
 // CTA each, whose f32 sums a third kernel adds in order.

@@ -23,17 +23,18 @@
 // CTAs than SMs the keys are cut into parts, a CTA each, whose results a
 // second kernel joins by their log-sum-exps.
 //
-// What bounds it. 8192 causal tokens, 32 heads of 128: 333-339 us, 1620-1650
-// TF/s, 0.84-0.85 of the cuBLAS burst rate, with the clock pulled down to
+// What bounds it. 8192 causal tokens, 32 heads of 128: 329-333 us, 1650-1670
+// TF/s, 0.85-0.86 of the cuBLAS burst rate, with the clock pulled down to
 // 1.75-1.87 GHz by the power limit: instructions cost time there even where
 // no unit is full. 2^x by a polynomial in place of every eighth to second one
 // of the special-function unit's: 360-406 us; two threads a row: 388; a
 // thread of its own for each tile's products: 377 (the two tiles' products
-// then alternate, and each waits for both). Heads of 64, 8192 tokens: 139 us,
+// then alternate, and each waits for both). Heads of 64, 8192 tokens: 138 us,
 // 0.51 of that rate: the rows' own work (about 1100 cycles a tile of each
-// warp, half of it the 128 exponentials) comes to twice the products'. Short
-// calls are latency: 512 tokens, 12 heads 8.3 us of which four tiles' turns
-// are some 5.
+// warp, half of it the 128 exponentials) comes to twice the products'; what
+// the power limit rules out at 128 was not measured there. Short calls: 512
+// tokens, 12 heads 8.3-8.5 us of which four tiles' turns are some 5, in which one
+// warpgroup takes all exponentials of a row while the other has no rows.
 #include "lin_attn.cuh"
 
 #include <type_traits>

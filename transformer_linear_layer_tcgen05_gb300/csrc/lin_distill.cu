@@ -10,17 +10,21 @@
 // of exponentials, the CTA's and the cluster's (through distributed shared
 // memory), and for the gradient, written straight out. The gradient comes one
 // row later than the sums, so that the exchange between the CTAs, whose
-// latency is near the time of a whole row, stands in nobody's way. Warps of
-// their own prepare the teacher's entries ahead, since their two dependent
+// latency is near the time of a whole row, stands in nobody's way. A warp of
+// its own prepares the teacher's entries ahead, since their two dependent
 // loads (id, then its logit) would do the same; their places in dz are
 // written again, behind the row, with p taken off.
 //
-// Measured: 4096 rows of 131072 with the gradient 745 us, 5.8 TB/s (floor 641);
-// 512 rows of 16384 16.6 us (10.0); 1000 rows of 50001, the losses alone, 39.3
-// us, 5.1 TB/s (29.9). On the way there: a row by one CTA of 16 warps 3278 us
+// Logits enter as differences, from the row's maximum, the teacher's largest
+// and the largest listed one, before they are multiplied by log2 e / tau.
+//
+// Measured: 4096 rows of 131072 with the gradient 760 us, 5.7 TB/s (floor 641);
+// 512 rows of 16384 17.0 us (10.0); 1000 rows of 50001, the losses alone, 40
+// us, 5.0 TB/s (29.9). On the way there: a row by one CTA of 16 warps 3278 us
 // at 131072 entries (each warp's fixed work for a row), clusters of 16 CTAs
 // with slots of 32 KB 1167 and of 8 with 64 KB 937 (the exchange waited for),
-// the same with the gradient a row behind 745.
+// the same with the gradient a row behind 745, and with every wait's end told
+// from its running out 760.
 //
 // A row is handled in the 16-byte units of memory that it touches, so rows
 // may start anywhere: only the first and the last unit can be partial, and
@@ -75,7 +79,7 @@ __device__ __forceinline__ Row row_units(const float* p, int V) {
 
 }  // namespace
 
-// WARPS warps (and kEnt for the teacher's entries) per CTA; a slot of shared memory holds a
+// WARPS warps (and one for the teacher's entries) per CTA; a slot of shared memory holds a
 // CTA's part of a row of up to distill_units() units. A row of more parts
 // than there are slots is streamed twice, for its sum and for its gradient.
 template <int WARPS>
