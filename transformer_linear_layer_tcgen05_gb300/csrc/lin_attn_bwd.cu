@@ -147,18 +147,18 @@ __device__ __forceinline__ int norm_exponent(float norm) {
 
 // Where a thread's row of a gradient goes: to the 16-bit tensor, or, as one
 // of several parts, in f32 to [part][row][head][dim] (`rows` to a part, this
-// one at `row_at`).
+// one at `row_at`, which without parts may wrap and is not used).
 struct HeadGrad {
   uint16_t* row;
   float* part_row;
   __device__ __forceinline__ HeadGrad(const HeadsPtr& t, float* parts_base, int parts, int part,
-                                      int rows, int row_at, int heads, int dim,
+                                      int rows, uint32_t row_at, int heads, int dim,
                                       int64_t token, int h)
       : row(t.p + token * t.token_stride + (int64_t)h * t.head_stride),
         part_row(parts > 1 ? parts_base + ((part * rows + row_at) * heads + h) * dim : nullptr) {}
   // Checked build: the row inside its part.
-  __device__ __forceinline__ bool ok(int* status, int rows, int row_at) const {
-    return !part_row || dcheck(row_at >= 0 && row_at < rows, status, CHK_PART, row_at);
+  __device__ __forceinline__ bool ok(int* status, int rows, uint32_t row_at) const {
+    return !part_row || dcheck(row_at < (uint32_t)rows, status, CHK_PART, row_at);
   }
   // N columns from c0 on, times `back` (zeros if there is nothing), those
   // below dim.
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     if (ok) {
       const float back = a.scale * pow2i(-ne);
       const HeadGrad out(args.dq, args.dq_part, args.q_parts, part, args.q_part_rows,
-                         b * a.max_q + i, a.heads_q, a.dim, token, h);
+                         (uint32_t)b * a.max_q + i, a.heads_q, a.dim, token, h);
 #pragma unroll
       for (int q = 0; q < DP / 32; ++q) {
         const int c0 = half * (DP / 2) + q * 16;
@@ -495,7 +495,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           tmem_ld_32x32b_x16(tmem + lanes + C::OUT_COL + c0, o);
           tmem_wait_ld_x16(o);
         }
-        const bool put = live && out.ok(a.status, args.q_part_rows, b * a.max_q + i);
+        const bool put = live && out.ok(a.status, args.q_part_rows, (uint32_t)b * a.max_q + i);
         out.put<BF16>(o, n > 0, back, c0, put ? a.dim : 0);
       }
     }
@@ -903,7 +903,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     if (ok) {   // the first half's threads write dV, the others dK
       const float back = half == 0 ? pow2i(-(int)kPShift) : a.scale * pow2i(-ne);
       const HeadGrad out(half == 0 ? args.dv : args.dk, half == 0 ? args.dv_part : args.dk_part,
-                         args.k_parts, part, args.k_part_rows, b * a.max_k + key,
+                         args.k_parts, part, args.k_part_rows, (uint32_t)b * a.max_k + key,
                          a.heads_q / a.group, a.dim, (int64_t)sk.start + (live ? key : 0), hk);
 #pragma unroll
       for (int q = 0; q < DP / 32; ++q) {
@@ -912,7 +912,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
           tmem_ld_32x32b_x32(tmem + lanes + C::OUT_COL + half * DP + q * 32, o);
           tmem_wait_ld_x32(o);
         }
-        const bool put = live && out.ok(a.status, args.k_part_rows, b * a.max_k + key);
+        const bool put = live && out.ok(a.status, args.k_part_rows, (uint32_t)b * a.max_k + key);
         out.put<BF16>(o, n > 0, back, q * 32, put ? a.dim : 0);
       }
     }

@@ -384,7 +384,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const float inv = l > 0.0f ? 1.0f / l : (l == 0.0f ? 0.0f : l);   // (NaN stays NaN)
       const int64_t token = sq.start + i;
       uint16_t* out = args.o.p + token * args.o.token_stride + (int64_t)h * args.o.head_stride;
-      const int row_at = b * a.max_q + i;   // among the parts' rows
+      // among the parts' rows (unsigned: without parts it may wrap, unused)
+      const uint32_t row_at = (uint32_t)b * a.max_q + i;
       float* part_row = args.o_part + ((at.part * args.part_rows + row_at) * a.heads_q + h) * a.dim;
       float* lse = parts > 1
                        ? args.lse_part + (at.part * a.heads_q + h) * args.part_rows + row_at
@@ -406,7 +407,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             w[e] = nk > 0 ? pack16<BF16>(l == 0.0f ? 0.0f : x * inv, l == 0.0f ? 0.0f : y * inv) : 0u;
           }
           if (!live || col >= a.dim || !q_row_ok(a, token, h)) continue;
-          if (parts > 1 && !dcheck(row_at < args.part_rows && at.part < parts, a.status, CHK_PART, row_at))
+          if (parts > 1 && !dcheck(row_at < (uint32_t)args.part_rows && at.part < parts, a.status,
+                                    CHK_PART, row_at))
             continue;
           if (parts > 1) {   // in f32
             const float z = nk > 0 ? inv : 0.0f;
