@@ -391,7 +391,8 @@ lin_status lin_gate_up_w16(const float *X, const uint16_t *WG16, const uint16_t 
  *             heads of a token lie within it; others whose ranges meet count
  *             as sharing one.
  */
-typedef enum lin_dtype { LIN_BINARY16 = 0, LIN_BFLOAT16 = 1 } lin_dtype;
+/* (LIN_BINARY32: where a call says so) */
+typedef enum lin_dtype { LIN_BINARY16 = 0, LIN_BFLOAT16 = 1, LIN_BINARY32 = 2 } lin_dtype;
 
 typedef struct lin_heads {
   void *data;
@@ -459,6 +460,124 @@ lin_status lin_qk_norm_rope_backward(const lin_qk_norm_rope_shape *shape, const 
                                      const lin_heads *DQ, const lin_heads *DK,
                                      const lin_heads *DV, float *DX, float *DWQ, float *DWK,
                                      lin_stream_t stream);
+
+/* The same with several positions to a token (time, height and width of an
+ * image's or a video's patches): positions int32 [axes][tokens], 1 to 4 axes,
+ * and pair_axis int32 [rot/2] (16-byte aligned), the axis whose position is
+ * the table row of pair i (values outside are held to 0 .. axes - 1). The
+ * angle of pair i is entry i of that row: axes whose frequencies begin anew
+ * have their columns of the tables made so. Sections of the pairs, pairs dealt
+ * to the axes in turn, or any other order. All else as above. */
+lin_status lin_qk_norm_rope_axes(const lin_qk_norm_rope_shape *shape, int64_t axes, const float *X,
+                                 const float *WQ, const float *WK, const float *COS,
+                                 const float *SIN, const int32_t *positions,
+                                 const int32_t *pair_axis, const lin_heads *Q, const lin_heads *K,
+                                 const lin_heads *V, lin_stream_t stream);
+lin_status lin_qk_norm_rope_axes_backward(const lin_qk_norm_rope_shape *shape, int64_t axes,
+                                          const float *X, const float *WQ, const float *WK,
+                                          const float *COS, const float *SIN,
+                                          const int32_t *positions, const int32_t *pair_axis,
+                                          const lin_heads *DQ, const lin_heads *DK,
+                                          const lin_heads *DV, float *DX, float *DWQ, float *DWK,
+                                          lin_stream_t stream);
+
+/*
+ * Norms before and after a block
+ * ------------------------------
+ * What stands between two blocks of the residual stream (the pages name
+ * 05_rmsnorm without a description): the norm of a block's output Y, its gate,
+ * the sum with the residual stream X, and the norm that the next block begins
+ * with. Per token, width entries each:
+ *   b = W_POST * Y / sqrt(mean(Y^2) + eps)    (W_POST NULL: b = Y)
+ *   H = residual_scale * X + block_scale * GATE * b
+ *   N = W_PRE * H / sqrt(mean(H^2) + eps)
+ * Y NULL: H = residual_scale * X (a norm alone); N and W_PRE NULL: no norm
+ * behind; H NULL: not written; one of H and N at least. GATE f32 by `gate`:
+ * none (NULL), [width] for each channel, [tokens] for each token, or
+ * [tokens][width]. X, H, DX, DH and the weights: f32; Y, N, DY, DN: `dtype`,
+ * binary16, bfloat16 or binary32. All [tokens][width], dense.
+ * The backward form takes H (the forward call's; X of a call without Y with
+ * residual_scale 1), DH, the gradient that arrives at H itself, and DN, that at
+ * N (either may be NULL, not both; without DN neither H nor W_PRE nor DW_PRE), and gives
+ *   D = DH + the norm's gradient of DN,   DX = residual_scale * D,
+ *   DY from U = block_scale * GATE * D,   DGATE = block_scale * D * b (summed
+ *   over the tokens or the width as GATE's form has it), DW_POST, DW_PRE,
+ * those of them whose tensors the forward call had. DH itself may be DX, and X
+ * of the forward call H (in place); outputs overlap nothing else.
+ * width: a multiple of 4 up to 8192 (0: nothing is done); fewer than 2^40
+ * entries. 16-byte aligned (16-bit tensors: 8; GATE for each token: 4). All arithmetic in float32; sums
+ * over the tokens have a fixed order. Workspace (backward): width floats for
+ * each sum over the tokens and SM.
+ */
+typedef enum lin_gate {
+  LIN_GATE_NONE = 0,
+  LIN_GATE_CHANNEL = 1,
+  LIN_GATE_TOKEN = 2,
+  LIN_GATE_FULL = 3
+} lin_gate;
+
+typedef struct lin_block_norms_shape {
+  int32_t dtype;   /* lin_dtype of Y, N, DY, DN */
+  int32_t gate;    /* lin_gate */
+  int64_t tokens, width;
+  float residual_scale, block_scale, eps;
+} lin_block_norms_shape;
+
+lin_status lin_block_norms(const lin_block_norms_shape *shape, const float *X, const void *Y,
+                           const float *GATE, const float *W_POST, const float *W_PRE, float *H,
+                           void *N, lin_stream_t stream);
+lin_status lin_block_norms_backward(const lin_block_norms_shape *shape, const float *H,
+                                    const void *Y, const float *GATE, const float *W_POST,
+                                    const float *W_PRE, const float *DH, const void *DN, float *DX,
+                                    void *DY, float *DGATE, float *DW_POST, float *DW_PRE,
+                                    lin_stream_t stream);
+
+/*
+ * The AdamW step
+ * --------------
+ * All tensors of a parameter group in one call (a launch for each 384): per
+ * entry, with the gradient x = grad_scale * g,
+ *   m = beta1 m + (1 - beta1) x,   v = beta2 v + (1 - beta2) x^2
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in place (p, m, v; f32), and w16 = binary16(p) where a tensor has such a
+ * copy (what the w16 linear layers read). step counts from 1. state_bits 8: m
+ * and the root of v are held as e4m3 codes (one byte an entry) of entry / scale
+ * in blocks of 256 entries of the tensor, scale = the block's largest
+ * magnitude / 448, f32, ceil(n / 256) of them in m_scale and v_scale. A block
+ * whose largest magnitude is below 2^-100 is held as zeros, a root above zero
+ * as the smallest code at least, and an entry that is no finite number as NaN,
+ * which does not count in its block's scale. Codes and scales of zero are the
+ * states of a new tensor.
+ * lr_device, step_device, grad_scale: device memory, read when the stream
+ * gets there (a captured call then follows a schedule); NULL: lr, step, 1.
+ * With step_device the corrections are computed in float32 (below 1: as 1).
+ * Tensors of any length and alignment (of their entries); those of 32-byte
+ * aligned f32, 8-byte aligned codes and 16-byte aligned w16 are read faster.
+ * What is written overlaps nothing else of the call. 0 <= beta < 1, eps >= 0;
+ * up to 2^20 tensors, each below 2^39 entries; tensors without entries are
+ * passed over.
+ */
+typedef struct lin_adamw_tensor {
+  float *p;
+  const float *g;
+  void *m, *v;               /* f32, or e4m3 codes */
+  float *m_scale, *v_scale;  /* state_bits 8 */
+  uint16_t *w16;             /* NULL: none */
+  int64_t n;
+} lin_adamw_tensor;
+
+typedef struct lin_adamw_step {
+  int32_t state_bits;        /* 32 or 8 */
+  int64_t step;
+  double lr, beta1, beta2, eps, weight_decay;
+  const float *lr_device;    /* NULL: lr */
+  const int32_t *step_device;/* NULL: step */
+  const float *grad_scale;   /* NULL: 1 */
+} lin_adamw_step;
+
+lin_status lin_adamw(const lin_adamw_step *step, const lin_adamw_tensor *tensors, int64_t count,
+                     lin_stream_t stream);
 
 /* Distillation from a teacher's top logits: per row, with z = LOGITS (M rows
  * of V, ld entries apart; what lm_head writes) and the row's K listed

@@ -18,6 +18,7 @@
 #include <exception>
 #include <initializer_list>
 #include <string>
+#include <vector>
 
 #include "lin.h"
 
@@ -25,8 +26,11 @@ namespace {
 
 // Addresses of the library's functions, in the order of kNames.
 const char* const kNames[] = {"lin_attention", "lin_attention_backward", "lin_qk_norm_rope",
-                              "lin_qk_norm_rope_backward", "lin_distill_topk"};
-void* g_address[5];
+                              "lin_qk_norm_rope_backward", "lin_distill_topk",
+                              "lin_qk_norm_rope_axes", "lin_qk_norm_rope_axes_backward",
+                              "lin_block_norms", "lin_block_norms_backward", "lin_adamw"};
+constexpr int kFunctions = sizeof(kNames) / sizeof(kNames[0]);
+void* g_address[kFunctions];
 
 template <typename F>
 F* bound(int i) {
@@ -242,7 +246,8 @@ struct RopeArgs {
   const int32_t* positions = nullptr;
   c10::IntArrayRef x_sizes;
 
-  RopeArgs(PyObject* const* a, const char* const (&names)[3]) {
+  // (`axes`: positions are [axes, tokens])
+  RopeArgs(PyObject* const* a, const char* const (&names)[3], bool axes = false) {
     Heads h;
     const at::Tensor &tq = h.take(a[6], names[0], &q), &tk = h.take(a[7], names[1], &k),
                      &tv = h.take(a[8], names[2], &v);
@@ -274,7 +279,7 @@ struct RopeArgs {
       s.table_rows = tc->size(0);
       s.rot = 2 * tc->size(1);
     }
-    if (a[5] != Py_None) positions = flat<int32_t>(a[5], "positions", at::kInt, {s.tokens});
+    if (a[5] != Py_None && !axes) positions = flat<int32_t>(a[5], "positions", at::kInt, {s.tokens});
     wq = f32(a[1], "wq", {s.dim});
     wk = f32(a[2], "wk", {s.dim});
     s.eps = (float)number(a[9]);
@@ -300,6 +305,222 @@ PyObject* qk_norm_rope_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     float* dwk = f32(a[13], "dwk", {r.s.dim});
     return unlocked(bound<decltype(lin_qk_norm_rope_backward)>(3), &r.s, r.x, r.wq, r.wk, r.cos,
                     r.sin, r.positions, &r.q, &r.k, &r.v, dx, dwq, dwk, stream_of(a[14]));
+  });
+}
+
+// The positions of lin_qk_norm_rope_axes and each pair's axis.
+struct Axes {
+  int64_t count;
+  const int32_t *positions, *pair;
+
+  Axes(PyObject* pos, PyObject* axis, const RopeArgs& r) {
+    const at::Tensor* t = tensor(pos);
+    count = t && t->dim() == 2 ? t->size(0) : 1;
+    positions = flat<int32_t>(pos, "positions", at::kInt, {count, r.s.tokens});
+    pair = flat<int32_t>(axis, "pair_axis", at::kInt, {r.s.rot / 2});
+  }
+};
+
+// RopeArgs', pair_axis, stream
+PyObject* qk_norm_rope_axes(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 13, [&] {
+    const RopeArgs r(a, {"Q", "K", "V"}, true);
+    const Axes x(a[5], a[11], r);
+    return unlocked(bound<decltype(lin_qk_norm_rope_axes)>(5), &r.s, x.count, r.x, r.wq, r.wk, r.cos,
+                    r.sin, x.positions, x.pair, &r.q, &r.k, &r.v, stream_of(a[12]));
+  });
+}
+
+// RopeArgs', pair_axis, dX, dwq, dwk, stream
+PyObject* qk_norm_rope_axes_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 16, [&] {
+    const RopeArgs r(a, {"dQ", "dK", "dV"}, true);
+    const Axes x(a[5], a[11], r);
+    float* dx = f32(a[12], "dX", r.x_sizes);
+    float* dwq = f32(a[13], "dwq", {r.s.dim});
+    float* dwk = f32(a[14], "dwk", {r.s.dim});
+    return unlocked(bound<decltype(lin_qk_norm_rope_axes_backward)>(6), &r.s, x.count, r.x, r.wq,
+                    r.wk, r.cos, r.sin, x.positions, x.pair, &r.q, &r.k, &r.v, dx, dwq, dwk,
+                    stream_of(a[15]));
+  });
+}
+
+// The block's output and what has its type, the gate and the weights: null
+// where they are None.
+struct NormArgs {
+  lin_block_norms_shape s{};
+  c10::IntArrayRef rows;
+
+  // `first`: a tensor [tokens, width] that the call has
+  explicit NormArgs(PyObject* first, const char* name) {
+    const at::Tensor* t = tensor(first);
+    if (!t || t->dim() != 2 || !t->is_cuda())
+      raise(PyExc_TypeError, std::string(name) + " must be a CUDA matrix [tokens, width]");
+    rows = t->sizes();
+    s.tokens = rows[0];
+    s.width = rows[1];
+    s.dtype = LIN_BINARY32;
+  }
+  float* f32_or_none(PyObject* o, const char* name, c10::IntArrayRef shape) {
+    return o == Py_None ? nullptr : f32(o, name, shape);
+  }
+  // Tensors of the block's type (the first one's).
+  void* block(PyObject* o, const char* name) {
+    if (o == Py_None) return nullptr;
+    const at::Tensor* t = tensor(o);
+    const auto type = t ? t->scalar_type() : at::kInt;
+    if (!t || !t->is_cuda() || !t->is_contiguous() || t->sizes() != rows ||
+        (type != at::kHalf && type != at::kBFloat16 && type != at::kFloat) || (typed && type != kind))
+      raise(PyExc_TypeError, std::string(name) + " must be a contiguous float16, bfloat16 or float32 "
+                                 "CUDA tensor " + list_of(rows) + ", of the block's type");
+    typed = true;
+    kind = type;
+    s.dtype = type == at::kHalf ? LIN_BINARY16 : type == at::kBFloat16 ? LIN_BFLOAT16 : LIN_BINARY32;
+    return t->data_ptr();
+  }
+  // The gate, or its gradient: its form is its shape.
+  float* gate(PyObject* o, const char* name) {
+    if (o == Py_None) return nullptr;
+    const at::Tensor* t = tensor(o);
+    const bool channel = t && t->dim() == 1 && t->size(0) == s.width;
+    const bool full = t && t->sizes() == rows && s.width != 1;
+    const bool token = t && t->dim() == 2 && t->size(0) == s.tokens && t->size(1) == 1;
+    if (!channel && !full && !token)
+      raise(PyExc_ValueError, std::string(name) + " must be [width], [tokens, 1] or [tokens, width]");
+    s.gate = channel ? LIN_GATE_CHANNEL : full ? LIN_GATE_FULL : LIN_GATE_TOKEN;
+    return f32(o, name, t->sizes());
+  }
+  void numbers(PyObject* const* a) {
+    s.residual_scale = (float)number(a[0]);
+    s.block_scale = (float)number(a[1]);
+    s.eps = (float)number(a[2]);
+  }
+
+ private:
+  bool typed = false;
+  at::ScalarType kind = at::kFloat;
+};
+
+// X, Y, gate, w_post, w_pre, H, N, residual_scale, block_scale, eps, stream
+PyObject* block_norms(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 11, [&] {
+    NormArgs r(a[0], "X");
+    const float* x = f32(a[0], "X", r.rows);
+    const void* y = r.block(a[1], "Y");
+    const float* g = r.gate(a[2], "gate");
+    const float* post = r.f32_or_none(a[3], "w_post", {r.s.width});
+    const float* pre = r.f32_or_none(a[4], "w_pre", {r.s.width});
+    float* h = r.f32_or_none(a[5], "H", r.rows);
+    void* out = r.block(a[6], "N");
+    r.numbers(a + 7);
+    return unlocked(bound<decltype(lin_block_norms)>(7), &r.s, x, y, g, post, pre, h, out,
+                    stream_of(a[10]));
+  });
+}
+
+// H, Y, gate, w_post, w_pre, DH, DN, DX, DY, dgate, dw_post, dw_pre,
+// residual_scale, block_scale, eps, stream
+PyObject* block_norms_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 16, [&] {
+    NormArgs r(a[7], "DX");
+    const float* h = r.f32_or_none(a[0], "H", r.rows);
+    const void* y = r.block(a[1], "Y");
+    const float* g = r.gate(a[2], "gate");
+    const int32_t form = r.s.gate;
+    const float* post = r.f32_or_none(a[3], "w_post", {r.s.width});
+    const float* pre = r.f32_or_none(a[4], "w_pre", {r.s.width});
+    const float* dh = r.f32_or_none(a[5], "DH", r.rows);
+    const void* dn = r.block(a[6], "DN");
+    float* dx = f32(a[7], "DX", r.rows);
+    void* dy = r.block(a[8], "DY");
+    float* dg = r.gate(a[9], "dgate");
+    if (r.s.gate != form) raise(PyExc_ValueError, "dgate must have the gate's shape");
+    float* dpost = r.f32_or_none(a[10], "dw_post", {r.s.width});
+    float* dpre = r.f32_or_none(a[11], "dw_pre", {r.s.width});
+    r.numbers(a + 12);
+    return unlocked(bound<decltype(lin_block_norms_backward)>(8), &r.s, h, y, g, post, pre, dh, dn,
+                    dx, dy, dg, dpost, dpre, stream_of(a[15]));
+  });
+}
+
+// A list or tuple of n tensors (None: nothing), held while the call reads it.
+struct Tensors {
+  PyObject* items = nullptr;
+
+  Tensors(PyObject* o, const char* name, Py_ssize_t want) {
+    if (o == Py_None) return;
+    items = PySequence_Fast(o, (std::string(name) + " must be a list of tensors").c_str());
+    if (!items) throw Raised();
+    if (want >= 0 && size() != want) {
+      Py_DECREF(items);
+      raise(PyExc_ValueError, std::string(name) + " must have " + std::to_string(want) + " entries");
+    }
+  }
+  ~Tensors() { Py_XDECREF(items); }
+  Tensors(const Tensors&) = delete;
+  Py_ssize_t size() const { return PySequence_Fast_GET_SIZE(items); }
+  PyObject* at(Py_ssize_t i) const { return items ? PySequence_Fast_GET_ITEM(items, i) : Py_None; }
+};
+
+// One tensor of a list: contiguous, of the given type, with n entries.
+void* entry(PyObject* o, const char* name, at::ScalarType type, const char* type_name, int64_t n) {
+  const at::Tensor* t = tensor(o);
+  if (!t || t->scalar_type() != type || !t->is_cuda() || !t->is_contiguous() || t->numel() != n)
+    raise(PyExc_TypeError, std::string(name) + ": contiguous " + type_name + " CUDA tensors of " +
+                               std::to_string(n) + " entries here");
+  return t->data_ptr();
+}
+
+// params, grads, m, v, m_scale, v_scale, w16, step, lr, beta1, beta2, eps,
+// weight_decay, grad_scale, stream
+PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 15, [&] {
+    if (a[0] == Py_None) raise(PyExc_TypeError, "params must be a list of tensors");
+    const Tensors p(a[0], "params", -1);
+    const Py_ssize_t count = p.size();
+    const Tensors g(a[1], "grads", count), m(a[2], "m", count), v(a[3], "v", count),
+        ms(a[4], "m_scale", count), vs(a[5], "v_scale", count), w16(a[6], "w16", count);
+    lin_adamw_step s{};
+    s.state_bits = 32;
+    std::vector<lin_adamw_tensor> list((size_t)count);
+    for (Py_ssize_t i = 0; i < count; ++i) {
+      const at::Tensor* t = tensor(p.at(i));
+      if (!t) raise(PyExc_TypeError, "params must be a list of tensors");
+      lin_adamw_tensor& to = list[(size_t)i];
+      to.n = t->numel();
+      to.p = static_cast<float*>(entry(p.at(i), "params", at::kFloat, "float32", to.n));
+      to.g = static_cast<const float*>(entry(g.at(i), "grads", at::kFloat, "float32", to.n));
+      const at::Tensor* tm = tensor(m.at(i));
+      const bool codes = tm && tm->scalar_type() == at::kFloat8_e4m3fn;
+      if (i == 0) s.state_bits = codes ? 8 : 32;
+      const bool bits8 = s.state_bits == 8;
+      const auto type = bits8 ? at::kFloat8_e4m3fn : at::kFloat;
+      const char* name = bits8 ? "float8_e4m3fn" : "float32";
+      to.m = entry(m.at(i), "m", type, name, to.n);
+      to.v = entry(v.at(i), "v", type, name, to.n);
+      to.m_scale = to.v_scale = nullptr;
+      if (bits8) {
+        to.m_scale = static_cast<float*>(entry(ms.at(i), "m_scale", at::kFloat, "float32", (to.n + 255) / 256));
+        to.v_scale = static_cast<float*>(entry(vs.at(i), "v_scale", at::kFloat, "float32", (to.n + 255) / 256));
+      }
+      to.w16 = w16.at(i) == Py_None
+                   ? nullptr
+                   : static_cast<uint16_t*>(entry(w16.at(i), "w16", at::kHalf, "float16", to.n));
+    }
+    auto device = [&](PyObject* o, const char* name, at::ScalarType type, const char* type_name) -> void* {
+      return tensor(o) ? entry(o, name, type, type_name, 1) : nullptr;
+    };
+    s.step_device = static_cast<const int32_t*>(device(a[7], "step", at::kInt, "int32"));
+    s.step = s.step_device ? 1 : integer(a[7], "step");
+    s.lr_device = static_cast<const float*>(device(a[8], "lr", at::kFloat, "float32"));
+    s.lr = s.lr_device ? 0.0 : number(a[8]);
+    s.beta1 = number(a[9]);
+    s.beta2 = number(a[10]);
+    s.eps = number(a[11]);
+    s.weight_decay = number(a[12]);
+    if (a[13] != Py_None)
+      s.grad_scale = static_cast<const float*>(entry(a[13], "grad_scale", at::kFloat, "float32", 1));
+    return unlocked(bound<decltype(lin_adamw)>(9), &s, list.data(), (int64_t)count, stream_of(a[14]));
   });
 }
 
@@ -330,8 +551,8 @@ PyObject* distill_topk(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 // {name: address} of the library's functions: all of them, or none is taken.
 PyObject* bind(PyObject*, PyObject* addresses) {
-  void* got[5];
-  for (int i = 0; i < 5; ++i) {
+  void* got[kFunctions];
+  for (int i = 0; i < kFunctions; ++i) {
     PyObject* v = PyMapping_GetItemString(addresses, kNames[i]);
     if (!v) return nullptr;
     got[i] = PyLong_AsVoidPtr(v);
@@ -341,7 +562,7 @@ PyObject* bind(PyObject*, PyObject* addresses) {
       return nullptr;
     }
   }
-  for (int i = 0; i < 5; ++i) g_address[i] = got[i];
+  for (int i = 0; i < kFunctions; ++i) g_address[i] = got[i];
   Py_RETURN_NONE;
 }
 
@@ -357,6 +578,11 @@ PyMethodDef kMethods[] = {
     {"qk_norm_rope", as_method(qk_norm_rope), METH_FASTCALL, nullptr},
     {"qk_norm_rope_backward", as_method(qk_norm_rope_backward), METH_FASTCALL, nullptr},
     {"distill_topk", as_method(distill_topk), METH_FASTCALL, nullptr},
+    {"qk_norm_rope_axes", as_method(qk_norm_rope_axes), METH_FASTCALL, nullptr},
+    {"qk_norm_rope_axes_backward", as_method(qk_norm_rope_axes_backward), METH_FASTCALL, nullptr},
+    {"block_norms", as_method(block_norms), METH_FASTCALL, nullptr},
+    {"block_norms_backward", as_method(block_norms_backward), METH_FASTCALL, nullptr},
+    {"adamw", as_method(adamw), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_lin_calls", nullptr, -1, kMethods,

@@ -101,10 +101,13 @@ __device__ __forceinline__ void turn(Eight& x, const float4& c, const float4& s)
   }
 }
 
-// Row of the tables for token t: its position held inside the table.
-__device__ __forceinline__ int64_t table_row(const RopeArgs& a, int64_t t) {
-  const int64_t p = a.pos ? (int64_t)a.pos[t] : t;
+// A position held inside the tables.
+__device__ __forceinline__ int64_t held(const RopeArgs& a, int64_t p) {
   return min(max(p, (int64_t)0), (int64_t)a.table_rows - 1);
+}
+// Row of the tables for token t: its position.
+__device__ __forceinline__ int64_t table_row(const RopeArgs& a, int64_t t) {
+  return held(a, a.pos ? (int64_t)a.pos[t] : t);
 }
 
 // Checked build: head `head` of token t inside the tensors; a lane's entries
@@ -115,6 +118,45 @@ __device__ __forceinline__ bool head_ok(const RopeArgs& a, int64_t t, int head, 
 }
 __device__ __forceinline__ bool angles_ok(const RopeArgs& a, int64_t row) {
   return dcheck(row >= 0 && row + 4 <= a.table_rows * (a.rot / 2), a.status, CHK_GLOBAL, row);
+}
+
+// The angles of token t for a lane's four pairs. AXES: each pair goes by the
+// position of its own axis (all positions of the token are read at once, with
+// the pairs' axes); four pairs of one axis are read together.
+template <bool AXES>
+__device__ __forceinline__ void angles(const RopeArgs& a, int64_t t, int pair, float4& c, float4& s) {
+  const int half = a.rot / 2;
+  if constexpr (!AXES) {
+    const int64_t row = table_row(a, t) * half + pair;
+    if (angles_ok(a, row)) {
+      c = *reinterpret_cast<const float4*>(a.cos + row);
+      s = *reinterpret_cast<const float4*>(a.sin + row);
+    }
+  } else {
+    int32_t p[kMostAxes];
+#pragma unroll
+    for (int k = 0; k < kMostAxes; ++k) p[k] = k < a.axes ? a.pos[k * a.tokens + t] : 0;
+    const int4 q = *reinterpret_cast<const int4*>(a.axis + pair);
+    int ax[4] = {q.x, q.y, q.z, q.w};
+    int64_t row[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      ax[i] = min(max(ax[i], 0), a.axes - 1);
+      int32_t at = p[0];
+#pragma unroll
+      for (int k = 1; k < kMostAxes; ++k) at = ax[i] == k ? p[k] : at;
+      row[i] = held(a, at) * half + pair;
+    }
+    if (!angles_ok(a, row[0]) || !angles_ok(a, row[1]) || !angles_ok(a, row[2]) || !angles_ok(a, row[3]))
+      return;
+    if (ax[0] == ax[1] && ax[0] == ax[2] && ax[0] == ax[3]) {
+      c = *reinterpret_cast<const float4*>(a.cos + row[0]);
+      s = *reinterpret_cast<const float4*>(a.sin + row[0]);
+    } else {
+      c = make_float4(a.cos[row[0]], a.cos[row[1] + 1], a.cos[row[2] + 2], a.cos[row[3] + 3]);
+      s = make_float4(a.sin[row[0]], a.sin[row[1] + 1], a.sin[row[2] + 2], a.sin[row[3] + 3]);
+    }
+  }
 }
 
 // The 16-bit head `head` (of q, k and v in a row) of token t.
@@ -128,7 +170,7 @@ __device__ __forceinline__ uint16_t* head16(const RopeArgs& a, int64_t t, int he
 
 }  // namespace
 
-template <int G, bool INTER, bool BF16>
+template <int G, bool INTER, bool BF16, bool AXES>
 __global__ void __launch_bounds__(kRopeThreads, kFwdCtas)
     lin_qk_norm_rope_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int GROUPS = kRopeThreads / G;
@@ -145,13 +187,7 @@ __global__ void __launch_bounds__(kRopeThreads, kFwdCtas)
                ? load8f(a.x + (t * heads + h0 + i) * a.dim, at)
                : Eight{};
   float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (at.on && at.turned && h0 < heads) {
-    const int64_t row = table_row(a, t) * (a.rot / 2) + at.pair;
-    if (angles_ok(a, row)) {
-      c = *reinterpret_cast<const float4*>(a.cos + row);
-      s = *reinterpret_cast<const float4*>(a.sin + row);
-    }
-  }
+  if (at.on && at.turned && h0 < heads) angles<AXES>(a, t, at.pair, c, s);
   float r[kFwdHeads];
 #pragma unroll
   for (int i = 0; i < kFwdHeads; ++i) {
@@ -182,7 +218,7 @@ __global__ void __launch_bounds__(kRopeThreads, kFwdCtas)
 // group walks over (token, heads) items with a fixed stride; the CTA's groups
 // are added in a fixed order and leave one partial row, and a second kernel
 // adds those.
-template <int G, bool INTER, bool BF16>
+template <int G, bool INTER, bool BF16, bool AXES>
 __global__ void __launch_bounds__(kRopeThreads, kBwdCtas)
     lin_qk_norm_rope_bwd_kernel(const __grid_constant__ RopeArgs a) {
   constexpr int GROUPS = kRopeThreads / G;
@@ -229,13 +265,7 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdCtas)
       }
     }
     float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (at.on && at.turned && h0 < h_hi) {
-      const int64_t row = table_row(a, t) * (a.rot / 2) + at.pair;
-      if (angles_ok(a, row)) {
-        c = *reinterpret_cast<const float4*>(a.cos + row);
-        s = *reinterpret_cast<const float4*>(a.sin + row);
-      }
-    }
+    if (at.on && at.turned && h0 < h_hi) angles<AXES>(a, t, at.pair, c, s);
     float* out = a.dx + (t * heads + h0) * a.dim;
 #pragma unroll
     for (int i = 0; i < kBwdHeads; ++i) {
@@ -314,28 +344,31 @@ namespace {
 
 // Calls f with the kernel's template arguments for the shape.
 template <typename F>
-cudaError_t with_shape(int dim, bool inter, bool bf16, F&& f) {
+cudaError_t with_shape(const RopeArgs& a, bool inter, bool bf16, F&& f) {
+  auto kind = [&](auto g, auto i, auto b) {
+    return a.axis ? f(g, i, b, std::true_type{}) : f(g, i, b, std::false_type{});
+  };
   auto types = [&](auto g) {
     if (inter)
-      return bf16 ? f(g, std::true_type{}, std::true_type{}) : f(g, std::true_type{}, std::false_type{});
-    return bf16 ? f(g, std::false_type{}, std::true_type{})
-                : f(g, std::false_type{}, std::false_type{});
+      return bf16 ? kind(g, std::true_type{}, std::true_type{}) : kind(g, std::true_type{}, std::false_type{});
+    return bf16 ? kind(g, std::false_type{}, std::true_type{})
+                : kind(g, std::false_type{}, std::false_type{});
   };
-  if (dim <= 32) return types(std::integral_constant<int, 4>{});
-  if (dim <= 64) return types(std::integral_constant<int, 8>{});
-  if (dim <= 128) return types(std::integral_constant<int, 16>{});
+  if (a.dim <= 32) return types(std::integral_constant<int, 4>{});
+  if (a.dim <= 64) return types(std::integral_constant<int, 8>{});
+  if (a.dim <= 128) return types(std::integral_constant<int, 16>{});
   return types(std::integral_constant<int, 32>{});
 }
 
 }  // namespace
 
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, bool inter, bool bf16, cudaStream_t stream) {
-  return with_shape(a.dim, inter, bf16, [&](auto g, auto i, auto b) {
+  return with_shape(a, inter, bf16, [&](auto g, auto i, auto b, auto x) {
     constexpr int G = decltype(g)::value;
     constexpr int GROUPS = kRopeThreads / G;
     const int64_t grid = (a.tokens + GROUPS - 1) / GROUPS *
                          ((a.hq + 2 * a.hk + kFwdHeads - 1) / kFwdHeads);
-    lin_qk_norm_rope_kernel<G, decltype(i)::value, decltype(b)::value>
+    lin_qk_norm_rope_kernel<G, decltype(i)::value, decltype(b)::value, decltype(x)::value>
         <<<(unsigned)grid, kRopeThreads, 0, stream>>>(a);
     return cudaGetLastError();
   });
@@ -355,8 +388,9 @@ int qk_norm_rope_bwd_ctas(RopeArgs& a, int sms) {
 
 cudaError_t launch_qk_norm_rope_bwd(const RopeArgs& a, bool inter, bool bf16, int ctas,
                                     cudaStream_t stream) {
-  const cudaError_t e = with_shape(a.dim, inter, bf16, [&](auto g, auto i, auto b) {
-    lin_qk_norm_rope_bwd_kernel<decltype(g)::value, decltype(i)::value, decltype(b)::value>
+  const cudaError_t e = with_shape(a, inter, bf16, [&](auto g, auto i, auto b, auto x) {
+    lin_qk_norm_rope_bwd_kernel<decltype(g)::value, decltype(i)::value, decltype(b)::value,
+                                decltype(x)::value>
         <<<(unsigned)ctas, kRopeThreads, 0, stream>>>(a);
     return cudaGetLastError();
   });

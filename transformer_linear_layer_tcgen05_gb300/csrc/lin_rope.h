@@ -9,11 +9,15 @@
 
 namespace lin {
 
+constexpr int kMostAxes = 4;   // positions of a token
+
 struct RopeArgs {
   const float* x;         // [tokens][(hq + 2 hk) dim]
   const float *wq, *wk;   // [dim]
   const float *cos, *sin; // [table_rows][rot / 2]
-  const int32_t* pos;     // [tokens], null: 0, 1, 2, ...
+  const int32_t* pos;     // [tokens], null: 0, 1, 2, ...; or [axes][tokens]
+  const int32_t* axis;    // [rot / 2]: each pair's axis (null: one position to a token)
+  int32_t axes;
   int64_t tokens, table_rows;
   int32_t hq, hk, dim, rot;
   float eps;

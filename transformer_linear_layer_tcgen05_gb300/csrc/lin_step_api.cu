@@ -1,16 +1,20 @@
-// lin_step_api.cu -- the entry points of include/lin.h around attention and
-// the loss: norms and rotation of the query and key heads, distillation.
+// lin_step_api.cu -- the entry points of include/lin.h around attention, the
+// loss and the weights: norms and rotation of the query and key heads, norms
+// around a block, distillation, the AdamW step.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <cstdlib>
 
 #include "lin.h"
+#include "lin_adamw.h"
 #include "lin_distill.h"
 #include "lin_heads.h"
 #include "lin_internal.h"
+#include "lin_norms.h"
 #include "lin_rope.h"
 
 namespace lin_detail {
@@ -47,13 +51,29 @@ lin_status check_on_device(const Buffer* b, int n, int dev, SeenRange* seen) {
   return LIN_SUCCESS;
 }
 
+// Tensors of one AdamW call, and host memory for what it keeps of them: on the
+// stack for a few, else from the heap (null if there is none).
+constexpr int64_t kMaxTensors = 1 << 20;
+template <typename T>
+struct Scratch {
+  alignas(T) unsigned char few[64 * sizeof(T)];
+  T* p;
+  explicit Scratch(size_t n) : p(reinterpret_cast<T*>(few)) {
+    if (n > 64) p = static_cast<T*>(std::malloc(n * sizeof(T)));
+  }
+  ~Scratch() {
+    if (p != reinterpret_cast<T*>(few)) std::free(p);
+  }
+  Scratch(const Scratch&) = delete;
+};
+
 // Both directions: DX, DWQ and DWK are null in the forward one, where Q, K
-// and V are written.
+// and V are written. axes > 0: positions [axes][tokens] and each pair's axis.
 lin_status qk_norm_rope(const lin_qk_norm_rope_shape* s, const float* X, const float* WQ,
                         const float* WK, const float* COS, const float* SIN,
-                        const int32_t* positions, const lin_heads* Q, const lin_heads* K,
-                        const lin_heads* V, bool backward, float* DX, float* DWQ, float* DWK,
-                        cudaStream_t stream) {
+                        const int32_t* positions, int64_t axes, const int32_t* pair_axis,
+                        const lin_heads* Q, const lin_heads* K, const lin_heads* V, bool backward,
+                        float* DX, float* DWQ, float* DWK, cudaStream_t stream) {
   set_last_launch_info(0, 0);
   if (!s || !Q || !K || !V) return LIN_ERROR_INVALID_VALUE;
   if (s->dtype != LIN_BINARY16 && s->dtype != LIN_BFLOAT16) return LIN_ERROR_INVALID_VALUE;
@@ -77,9 +97,11 @@ lin_status qk_norm_rope(const lin_qk_norm_rope_shape* s, const float* X, const f
   }
   const uint64_t t = (uint64_t)s->tokens, xb = t * heads * s->dim * 4, wb = (uint64_t)s->dim * 4;
   const uint64_t tb = s->rot ? (uint64_t)s->table_rows * s->rot * 2 : 0;
+  const uint64_t pb = axes > 0 ? (s->rot ? (uint64_t)axes * t * 4 : 0) : positions ? t * 4 : 0;
   Buffer b[] = {{X, xb, 16, false},      {WQ, wb, 16, false},
                 {WK, wb, 16, false},     {COS, tb, 16, false},
-                {SIN, tb, 16, false},    {positions, positions ? t * 4 : 0, 4, false},
+                {SIN, tb, 16, false},    {positions, pb, 4, false},
+                {pair_axis, axes > 0 ? (uint64_t)s->rot * 2 : 0, 16, false},
                 {DX, backward ? xb : 0, 16, true}, {DWQ, backward ? wb : 0, 4, true},
                 {DWK, backward ? wb : 0, 4, true}};
   const int nb = (int)(sizeof(b) / sizeof(b[0]));
@@ -112,6 +134,8 @@ lin_status qk_norm_rope(const lin_qk_norm_rope_shape* s, const float* X, const f
   a.cos = COS;
   a.sin = SIN;
   a.pos = positions;
+  a.axis = axes > 0 && s->rot ? pair_axis : nullptr;
+  a.axes = (int32_t)axes;
   a.tokens = s->tokens;
   a.table_rows = s->table_rows;
   a.hq = (int32_t)s->heads_q;
@@ -142,6 +166,265 @@ lin_status qk_norm_rope(const lin_qk_norm_rope_shape* s, const float* X, const f
   if (e == cudaSuccess) e = ef;
   if (e != cudaSuccess) return cuda_fail(e);
   set_last_launch_info(2, bytes);
+  return LIN_SUCCESS;
+}
+
+lin_status check_axes(int64_t axes) {
+  set_last_launch_info(0, 0);
+  return axes < 1 ? LIN_ERROR_INVALID_VALUE
+         : axes > lin::kMostAxes ? LIN_ERROR_UNSUPPORTED_SHAPE : LIN_SUCCESS;
+}
+
+// Both directions: X is the residual stream (forward) or its new value H
+// (gradient).
+lin_status block_norms(const lin_block_norms_shape* s, const float* X, const void* Y,
+                       const float* GATE, const float* W_POST, const float* W_PRE, float* H,
+                       void* N, bool backward, const float* DH, const void* DN, float* DX, void* DY,
+                       float* DGATE, float* DW_POST, float* DW_PRE, cudaStream_t stream) {
+  set_last_launch_info(0, 0);
+  if (!s) return LIN_ERROR_INVALID_VALUE;
+  if (s->dtype != LIN_BINARY16 && s->dtype != LIN_BFLOAT16 && s->dtype != LIN_BINARY32)
+    return LIN_ERROR_INVALID_VALUE;
+  if (s->gate < LIN_GATE_NONE || s->gate > LIN_GATE_FULL || s->tokens < 0 || s->width < 0 ||
+      !std::isfinite(s->residual_scale) || !std::isfinite(s->block_scale) || !(s->eps >= 0.0f) ||
+      std::isinf(s->eps))
+    return LIN_ERROR_INVALID_VALUE;
+  if (s->tokens > kMaxExtent || s->width % 4 != 0 || s->width > lin::kNormMostWidth ||
+      s->tokens * s->width >= (1LL << 40))
+    return LIN_ERROR_UNSUPPORTED_SHAPE;
+  if (s->width == 0 || (s->tokens == 0 && !backward)) return LIN_SUCCESS;
+  int dev = 0;
+  int* word = nullptr;
+  SeenRange seen;
+  lin_status st;
+  if (s->tokens == 0) {
+    // The weights' gradients are sums of nothing (of the tensors of tokens,
+    // which have no entries, nothing is looked at).
+    const uint64_t wb = (uint64_t)s->width * 4;
+    float* const sums[] = {DW_POST, DW_PRE, s->gate == LIN_GATE_CHANNEL ? DGATE : nullptr};
+    Buffer b[3];
+    for (int i = 0; i < 3; ++i) b[i] = Buffer{sums[i], sums[i] ? wb : 0, 16, true};
+    if ((st = check_buffers(b, 3)) != LIN_SUCCESS || (st = current_device(&dev, &word)) != LIN_SUCCESS ||
+        (st = check_on_device(b, 3, dev, &seen)) != LIN_SUCCESS)
+      return st;
+    cudaError_t e = cudaSuccess;
+    for (float* p : sums)
+      if (p && e == cudaSuccess) e = cudaMemsetAsync(p, 0, wb, stream);
+    return e == cudaSuccess ? LIN_SUCCESS : cuda_fail(e);
+  }
+  // What goes together: the block's output with its gate, its norm and their
+  // gradients; the norm behind with its weight's gradient.
+  const bool gated = s->gate != LIN_GATE_NONE, by_channel = s->gate == LIN_GATE_CHANNEL;
+  if (gated != (GATE != nullptr)) return LIN_ERROR_INVALID_VALUE;
+  if (!Y && (gated || W_POST)) return LIN_ERROR_INVALID_VALUE;
+  if (!backward) {
+    if (!X || (!H && !N) || (N != nullptr) != (W_PRE != nullptr)) return LIN_ERROR_INVALID_VALUE;
+  } else {
+    if (!DX || (!DH && !DN) || (DN != nullptr) != (W_PRE != nullptr) ||
+        (DN != nullptr) != (DW_PRE != nullptr) || (W_POST != nullptr) != (DW_POST != nullptr) ||
+        gated != (DGATE != nullptr) || (Y != nullptr) != (DY != nullptr) || (DN && !X))
+      return LIN_ERROR_INVALID_VALUE;
+  }
+  const uint64_t n = (uint64_t)s->tokens * (uint64_t)s->width, wb = (uint64_t)s->width * 4;
+  const uint64_t fb = n * 4, yb = n * (s->dtype == LIN_BINARY32 ? 4 : 2);
+  const uint64_t gb = by_channel ? wb : s->gate == LIN_GATE_TOKEN ? (uint64_t)s->tokens * 4 : fb;
+  const uint32_t ga = s->gate == LIN_GATE_TOKEN ? 4 : 16, ya = s->dtype == LIN_BINARY32 ? 16 : 8;
+  auto has = [](const void* p, uint64_t bytes) { return p ? bytes : 0; };
+  // (in place: H over X, DX over DH)
+  const bool h_in_x = !backward && H == X, dx_in_dh = backward && DX == DH;
+  Buffer b[] = {{X, h_in_x ? 0 : backward && !DN ? 0 : has(X, fb), 16, false},
+                {Y, has(Y, yb), ya, false},
+                {GATE, has(GATE, gb), ga, false},
+                {W_POST, has(W_POST, wb), 16, false},
+                {W_PRE, has(W_PRE, wb), 16, false},
+                {DH, dx_in_dh ? 0 : has(DH, fb), 16, false},
+                {DN, has(DN, yb), ya, false},
+                {H, has(H, fb), 16, true},
+                {N, has(N, yb), ya, true},
+                {DX, has(DX, fb), 16, true},
+                {DY, has(DY, yb), ya, true},
+                {DGATE, has(DGATE, gb), ga, true},
+                {DW_POST, has(DW_POST, wb), 16, true},
+                {DW_PRE, has(DW_PRE, wb), 16, true}};
+  const int nb = (int)(sizeof(b) / sizeof(b[0]));
+  if ((st = check_buffers(b, nb)) != LIN_SUCCESS || (st = current_device(&dev, &word)) != LIN_SUCCESS ||
+      (st = check_on_device(b, nb, dev, &seen)) != LIN_SUCCESS)
+    return st;
+  lin::NormsArgs a{};
+  a.x = X;
+  a.y = Y;
+  a.gate = GATE;
+  a.w_post = W_POST;
+  a.w_pre = W_PRE;
+  a.h = H;
+  a.n = N;
+  a.dh = DH;
+  a.dn = DN;
+  a.dx = DX;
+  a.dy = DY;
+  a.dgate = DGATE;
+  a.dw_post = DW_POST;
+  a.dw_pre = DW_PRE;
+  a.tokens = s->tokens;
+  a.width = (int32_t)s->width;
+  a.form = s->gate;
+  a.dtype = s->dtype;
+  a.residual_scale = s->residual_scale;
+  a.block_scale = s->block_scale;
+  a.eps = s->eps;
+  a.status = word;
+  if (!backward) {
+    const cudaError_t e = lin::launch_block_norms(a, stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+    set_last_launch_info(1, 0);
+    return LIN_SUCCESS;
+  }
+  a.kinds = (DN != nullptr) + (W_POST != nullptr) + by_channel;
+  const int ctas = lin::block_norms_bwd_ctas(a, sm_count(dev));
+  const size_t bytes = (size_t)ctas * (size_t)a.kinds * wb;
+  if (bytes) {
+    a.partial = static_cast<float*>(take_stream_workspace(dev, bytes, stream));
+    if (!a.partial) return LIN_ERROR_CUDA;
+  }
+  cudaError_t e = lin::launch_block_norms_bwd(a, ctas, stream);
+  if (bytes) {
+    const cudaError_t ef = cudaFreeAsync(a.partial, stream);
+    if (e == cudaSuccess) e = ef;
+  }
+  if (e != cudaSuccess) return cuda_fail(e);
+  set_last_launch_info(bytes ? 2 : 1, bytes);
+  return LIN_SUCCESS;
+}
+
+lin_status adamw(const lin_adamw_step* s, const lin_adamw_tensor* tensors, int64_t count,
+                 cudaStream_t stream) {
+  set_last_launch_info(0, 0);
+  if (!s || count < 0 || (count > 0 && !tensors)) return LIN_ERROR_INVALID_VALUE;
+  if (s->state_bits != 32 && s->state_bits != 8) return LIN_ERROR_INVALID_VALUE;
+  auto share = [](double b) { return b >= 0.0 && b < 1.0; };
+  if (!share(s->beta1) || !share(s->beta2) || !(s->eps >= 0.0) || std::isinf(s->eps) ||
+      !std::isfinite(s->weight_decay) || (!s->step_device && s->step < 1) ||
+      (!s->lr_device && !std::isfinite(s->lr)))
+    return LIN_ERROR_INVALID_VALUE;
+  const bool bits8 = s->state_bits == 8;
+  // Each tensor's buffers: presence and alignment, then that no written one
+  // meets another of the call (sorted by address, neighbours are enough).
+  struct Range {
+    uintptr_t at, end;
+    bool out;
+  };
+  auto misaligned = [](const void* p, uintptr_t n) { return reinterpret_cast<uintptr_t>(p) % n != 0; };
+  if (misaligned(s->lr_device, 4) || misaligned(s->step_device, 4) || misaligned(s->grad_scale, 4))
+    return LIN_ERROR_MISALIGNED;
+  if (count > kMaxTensors) return LIN_ERROR_UNSUPPORTED_SHAPE;
+  Scratch<Range> ranges((size_t)count * 7 + 3);
+  Scratch<lin::AdamwTensor> list((size_t)count);
+  Scratch<uint32_t> first((size_t)count);
+  if (!ranges.p || !list.p || !first.p) return LIN_ERROR_CUDA;
+  size_t nr = 0;
+  int64_t used = 0, blocks = 0;
+  auto add = [&](const void* p, uint64_t bytes, bool out) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    if (p && bytes) ranges.p[nr++] = Range{at, at + bytes, out};
+  };
+  add(s->lr_device, 4, false);
+  add(s->step_device, 4, false);
+  add(s->grad_scale, 4, false);
+  const uint64_t state = bits8 ? 1 : 4;
+  for (int64_t i = 0; i < count; ++i) {
+    const lin_adamw_tensor& t = tensors[i];
+    if (t.n < 0) return LIN_ERROR_INVALID_VALUE;
+    if (t.n == 0) continue;
+    if (t.n >= (1LL << 39)) return LIN_ERROR_UNSUPPORTED_SHAPE;
+    if (!t.p || !t.g || !t.m || !t.v || (bits8 && (!t.m_scale || !t.v_scale))) return LIN_ERROR_INVALID_VALUE;
+    const uintptr_t f = 4, c = bits8 ? 1 : 4;
+    if (misaligned(t.p, f) || misaligned(t.g, f) || misaligned(t.m, c) || misaligned(t.v, c) ||
+        (bits8 && (misaligned(t.m_scale, f) || misaligned(t.v_scale, f))) || misaligned(t.w16, 2))
+      return LIN_ERROR_MISALIGNED;
+    const int64_t nb = (t.n + lin::kAdamwBlock - 1) / lin::kAdamwBlock;
+    const uint64_t n = (uint64_t)t.n;
+    add(t.p, n * 4, true);
+    add(t.g, n * 4, false);
+    add(t.m, n * state, true);
+    add(t.v, n * state, true);
+    if (bits8) {
+      add(t.m_scale, (uint64_t)nb * 4, true);
+      add(t.v_scale, (uint64_t)nb * 4, true);
+    }
+    add(t.w16, n * 2, true);
+    const uintptr_t wide = bits8 ? 8 : 32;
+    lin::AdamwTensor& to = list.p[used];
+    to.p = t.p;
+    to.g = t.g;
+    to.m = t.m;
+    to.v = t.v;
+    to.m_scale = t.m_scale;
+    to.v_scale = t.v_scale;
+    to.w16 = t.w16;
+    to.n = t.n;
+    to.wide = !misaligned(t.p, 32) && !misaligned(t.g, 32) && !misaligned(t.m, wide) &&
+              !misaligned(t.v, wide) && !misaligned(t.w16, 16);
+    ++used;
+  }
+  std::sort(ranges.p, ranges.p + nr, [](const Range& a, const Range& b) { return a.at < b.at; });
+  uintptr_t end = 0, written_end = 0;   // behind everything, and what is written, so far
+  for (size_t i = 0; i < nr; ++i) {
+    if (ranges.p[i].at < (ranges.p[i].out ? end : written_end)) return LIN_ERROR_ALIASING;
+    end = std::max(end, ranges.p[i].end);
+    if (ranges.p[i].out) written_end = std::max(written_end, ranges.p[i].end);
+  }
+  if (used == 0) return LIN_SUCCESS;
+  int dev = 0;
+  int* word = nullptr;
+  lin_status st = current_device(&dev, &word);
+  if (st != LIN_SUCCESS) return st;
+  SeenRange seen;   // (by address: neighbours share an allocation)
+  for (size_t i = 0; i < nr; ++i) {
+    const Range& r = ranges.p[i];
+    if ((st = check_buffer(reinterpret_cast<const void*>(r.at), r.end - r.at, dev, &seen)) != LIN_SUCCESS)
+      return st;
+  }
+  lin::AdamwArgs a{};
+  a.beta1 = (float)s->beta1;
+  a.beta1_rest = (float)(1.0 - s->beta1);
+  a.beta2 = (float)s->beta2;
+  a.beta2_rest = (float)(1.0 - s->beta2);
+  a.eps = (float)s->eps;
+  const double t = (double)std::max<int64_t>(s->step, 1);
+  const double c1 = 1.0 / -std::expm1(t * std::log(s->beta1));
+  const double c2 = 1.0 / std::sqrt(-std::expm1(t * std::log(s->beta2)));
+  a.keep = (float)(1.0 - s->lr * s->weight_decay);
+  // (a device learning rate: the kernel multiplies the step's factor by it)
+  a.rate = (float)(s->lr_device || s->step_device ? c1 : s->lr * c1);
+  a.root = (float)c2;
+  a.lr = s->lr_device;
+  a.step = s->step_device;
+  a.lr_value = (float)s->lr;
+  a.decay = (float)s->weight_decay;
+  a.log_beta1 = (float)std::log(s->beta1);
+  a.log_beta2 = (float)std::log(s->beta2);
+  a.grad_scale = s->grad_scale;
+  a.status = word;
+  int kernels = 0;
+  for (int64_t i = 0; i < used;) {
+    // as many tensors as a launch's parameters hold, and fewer than 2^31 blocks
+    int n = 0;
+    blocks = 0;
+    while (i + n < used && n < lin::kAdamwMost) {
+      const int64_t nb = (list.p[i + n].n + lin::kAdamwBlock - 1) / lin::kAdamwBlock;
+      if (blocks + nb >= (1LL << 31) && n > 0) break;
+      first.p[i + n] = (uint32_t)blocks;
+      blocks += nb;
+      ++n;
+    }
+    a.tensors = n;
+    a.blocks = (uint32_t)blocks;
+    const cudaError_t e = lin::launch_adamw(a, list.p + i, first.p + i, bits8, sm_count(dev), stream);
+    if (e != cudaSuccess) return cuda_fail(e);
+    ++kernels;
+    i += n;
+  }
+  set_last_launch_info(kernels, 0);
   return LIN_SUCCESS;
 }
 
@@ -201,8 +484,8 @@ lin_status lin_qk_norm_rope(const lin_qk_norm_rope_shape* shape, const float* X,
                             const float* WK, const float* COS, const float* SIN,
                             const int32_t* positions, const lin_heads* Q, const lin_heads* K,
                             const lin_heads* V, lin_stream_t stream) {
-  return lin_detail::qk_norm_rope(shape, X, WQ, WK, COS, SIN, positions, Q, K, V, false, nullptr,
-                                  nullptr, nullptr, reinterpret_cast<cudaStream_t>(stream));
+  return lin_detail::qk_norm_rope(shape, X, WQ, WK, COS, SIN, positions, 0, nullptr, Q, K, V, false,
+                                  nullptr, nullptr, nullptr, reinterpret_cast<cudaStream_t>(stream));
 }
 
 lin_status lin_qk_norm_rope_backward(const lin_qk_norm_rope_shape* shape, const float* X,
@@ -210,8 +493,56 @@ lin_status lin_qk_norm_rope_backward(const lin_qk_norm_rope_shape* shape, const 
                                      const float* SIN, const int32_t* positions,
                                      const lin_heads* DQ, const lin_heads* DK, const lin_heads* DV,
                                      float* DX, float* DWQ, float* DWK, lin_stream_t stream) {
-  return lin_detail::qk_norm_rope(shape, X, WQ, WK, COS, SIN, positions, DQ, DK, DV, true, DX, DWQ,
-                                  DWK, reinterpret_cast<cudaStream_t>(stream));
+  return lin_detail::qk_norm_rope(shape, X, WQ, WK, COS, SIN, positions, 0, nullptr, DQ, DK, DV,
+                                  true, DX, DWQ, DWK, reinterpret_cast<cudaStream_t>(stream));
+}
+
+lin_status lin_qk_norm_rope_axes(const lin_qk_norm_rope_shape* shape, int64_t axes, const float* X,
+                                 const float* WQ, const float* WK, const float* COS,
+                                 const float* SIN, const int32_t* positions,
+                                 const int32_t* pair_axis, const lin_heads* Q, const lin_heads* K,
+                                 const lin_heads* V, lin_stream_t stream) {
+  const lin_status st = lin_detail::check_axes(axes);
+  if (st != LIN_SUCCESS) return st;
+  return lin_detail::qk_norm_rope(shape, X, WQ, WK, COS, SIN, positions, axes, pair_axis, Q, K, V,
+                                  false, nullptr, nullptr, nullptr,
+                                  reinterpret_cast<cudaStream_t>(stream));
+}
+
+lin_status lin_qk_norm_rope_axes_backward(const lin_qk_norm_rope_shape* shape, int64_t axes,
+                                          const float* X, const float* WQ, const float* WK,
+                                          const float* COS, const float* SIN,
+                                          const int32_t* positions, const int32_t* pair_axis,
+                                          const lin_heads* DQ, const lin_heads* DK,
+                                          const lin_heads* DV, float* DX, float* DWQ, float* DWK,
+                                          lin_stream_t stream) {
+  const lin_status st = lin_detail::check_axes(axes);
+  if (st != LIN_SUCCESS) return st;
+  return lin_detail::qk_norm_rope(shape, X, WQ, WK, COS, SIN, positions, axes, pair_axis, DQ, DK,
+                                  DV, true, DX, DWQ, DWK, reinterpret_cast<cudaStream_t>(stream));
+}
+
+lin_status lin_block_norms(const lin_block_norms_shape* shape, const float* X, const void* Y,
+                           const float* GATE, const float* W_POST, const float* W_PRE, float* H,
+                           void* N, lin_stream_t stream) {
+  return lin_detail::block_norms(shape, X, Y, GATE, W_POST, W_PRE, H, N, false, nullptr, nullptr,
+                                 nullptr, nullptr, nullptr, nullptr, nullptr,
+                                 reinterpret_cast<cudaStream_t>(stream));
+}
+
+lin_status lin_block_norms_backward(const lin_block_norms_shape* shape, const float* H,
+                                    const void* Y, const float* GATE, const float* W_POST,
+                                    const float* W_PRE, const float* DH, const void* DN, float* DX,
+                                    void* DY, float* DGATE, float* DW_POST, float* DW_PRE,
+                                    lin_stream_t stream) {
+  return lin_detail::block_norms(shape, H, Y, GATE, W_POST, W_PRE, nullptr, nullptr, true, DH, DN,
+                                 DX, DY, DGATE, DW_POST, DW_PRE,
+                                 reinterpret_cast<cudaStream_t>(stream));
+}
+
+lin_status lin_adamw(const lin_adamw_step* step, const lin_adamw_tensor* tensors, int64_t count,
+                     lin_stream_t stream) {
+  return lin_detail::adamw(step, tensors, count, reinterpret_cast<cudaStream_t>(stream));
 }
 
 lin_status lin_distill_topk(const float* LOGITS, int64_t ld, const int32_t* ids,

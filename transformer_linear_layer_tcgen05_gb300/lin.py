@@ -15,8 +15,8 @@ Two layers:
   stream (or ``stream=``) and raise ``LinError`` on a non-zero status.
   Binary16 weights may be given as ``torch.float16``, ``torch.int16`` or
   ``torch.uint16`` tensors (only the bit patterns are read). The short calls
-  (attention, norms and rotation, distillation) marshal their tensors in the
-  extension module ``_lin_calls``.
+  (attention, norms and rotation, distillation, the optimizer's step) marshal
+  their tensors in the extension module ``_lin_calls``.
 """
 
 from __future__ import annotations
@@ -90,12 +90,19 @@ SIGNATURES = {
     "lin_attention_backward": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S],
     "lin_qk_norm_rope": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S],
     "lin_qk_norm_rope_backward": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S],
+    "lin_qk_norm_rope_axes": [_P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S],
+    "lin_qk_norm_rope_axes_backward": [_P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                       _S],
+    "lin_block_norms": [_P, _P, _P, _P, _P, _P, _P, _P, _S],
+    "lin_block_norms_backward": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S],
+    "lin_adamw": [_P, _P, _I, _S],
     "lin_distill_topk": [_P, _I, _P, _P, _P, _I, _P, _P, _I, _I, _I, _F, _F, _S],
 }
 
 
 LIN_BINARY16 = 0
 LIN_BFLOAT16 = 1
+LIN_BINARY32 = 2
 
 _lib = None
 
@@ -402,8 +409,8 @@ def lin_gate_up_w16(X, WG16, WU16, GATE, UP, stream=None):
 
 # ------------------------------------------------------------ short calls
 #
-# Attention, norms and rotation, and distillation are short calls of many
-# tensors: their checks and marshalling are the extension module _lin_calls
+# Attention, norms and rotation, distillation and the optimizer's step are short
+# calls of many tensors: their checks and marshalling are the extension module _lin_calls
 # (csrc/lin_calls.cpp, built beside the library), bound once to the library's
 # functions.
 
@@ -426,7 +433,9 @@ def _short_calls():
         L = lib()
         _lin_calls.bind({name: ctypes.cast(getattr(L, name), _P).value for name in (
             "lin_attention", "lin_attention_backward", "lin_qk_norm_rope",
-            "lin_qk_norm_rope_backward", "lin_distill_topk")})
+            "lin_qk_norm_rope_backward", "lin_distill_topk", "lin_qk_norm_rope_axes",
+            "lin_qk_norm_rope_axes_backward", "lin_block_norms", "lin_block_norms_backward",
+            "lin_adamw")})
         _calls = _lin_calls
     return _calls
 
@@ -484,6 +493,70 @@ def lin_qk_norm_rope_backward(X, wq, wk, COS, SIN, positions, DQ, DK, DV, DX, dw
         X, wq, wk, COS, SIN, positions, DQ, DK, DV, eps, interleaved, DX, dwq, dwk,
         _handle(stream)))
     return DX, dwq, dwk
+
+
+def lin_qk_norm_rope_axes(X, wq, wk, COS, SIN, positions, pair_axis, Q, K, V, eps=1e-6,
+                          interleaved=False, stream=None):
+    """lin_qk_norm_rope with several positions to a token: positions int32
+    [axes, tokens] (1 to 4 axes: time, height, width, ...), pair_axis int32
+    [rot / 2], the axis by which each pair turns."""
+    check("lin_qk_norm_rope_axes", (_calls or _short_calls()).qk_norm_rope_axes(
+        X, wq, wk, COS, SIN, positions, Q, K, V, eps, interleaved, pair_axis, _handle(stream)))
+    return Q, K, V
+
+
+def lin_qk_norm_rope_axes_backward(X, wq, wk, COS, SIN, positions, pair_axis, DQ, DK, DV, DX, dwq,
+                                   dwk, eps=1e-6, interleaved=False, stream=None):
+    """dX, dwq, dwk of lin_qk_norm_rope_axes from dQ, dK, dV."""
+    check("lin_qk_norm_rope_axes_backward", (_calls or _short_calls()).qk_norm_rope_axes_backward(
+        X, wq, wk, COS, SIN, positions, DQ, DK, DV, eps, interleaved, pair_axis, DX, dwq, dwk,
+        _handle(stream)))
+    return DX, dwq, dwk
+
+
+def lin_block_norms(X, Y, gate, w_post, w_pre, H, N, residual_scale=1.0, block_scale=1.0, eps=1e-6,
+                    stream=None):
+    """Between two blocks of the residual stream: the block's output Y normed
+    (weight w_post; None: as it is), gated and added to X, and the norm (weight
+    w_pre) that the next block begins with:
+
+        b = w_post Y / rms(Y),  H = residual_scale X + block_scale gate b,
+        N = w_pre H / rms(H)
+
+    X, H [tokens, width] float32 (H may be X); Y, N float16, bfloat16 or
+    float32, both of one type; gate float32 [width], [tokens, 1], [tokens,
+    width] or None. Y None: X's norm alone; N and w_pre None: no norm behind; H
+    None: not written."""
+    check("lin_block_norms", (_calls or _short_calls()).block_norms(
+        X, Y, gate, w_post, w_pre, H, N, residual_scale, block_scale, eps, _handle(stream)))
+    return H, N
+
+
+def lin_block_norms_backward(H, Y, gate, w_post, w_pre, DH, DN, DX, DY, dgate, dw_post, dw_pre,
+                             residual_scale=1.0, block_scale=1.0, eps=1e-6, stream=None):
+    """dX, dY, dgate, dw_post, dw_pre of lin_block_norms from DH and DN (either
+    may be None; DX may be DH) and the forward call's H, Y and weights."""
+    check("lin_block_norms_backward", (_calls or _short_calls()).block_norms_backward(
+        H, Y, gate, w_post, w_pre, DH, DN, DX, DY, dgate, dw_post, dw_pre, residual_scale,
+        block_scale, eps, _handle(stream)))
+    return DX, DY, dgate, dw_post, dw_pre
+
+
+def lin_adamw(params, grads, m, v, m_scale=None, v_scale=None, w16=None, step=1, lr=1e-3,
+              betas=(0.9, 0.999), eps=1e-8, weight_decay=1e-2, grad_scale=None, stream=None):
+    """The AdamW step of all tensors of a parameter group, in place.
+
+    Lists of equal length: params, grads float32; the states m, v float32, or
+    float8_e4m3fn with m_scale, v_scale float32 [ceil(n / 256)] (8-bit states:
+    codes of m and of the root of v by blocks of 256 entries; zeros to begin
+    with); w16 (or None) the tensors' float16 copies to be written, None where
+    a tensor has none. All contiguous. ``step`` counts from 1; ``step``, ``lr``
+    and ``grad_scale`` may be one-entry CUDA tensors (int32, float32, float32),
+    read when the stream gets there."""
+    check("lin_adamw", (_calls or _short_calls()).adamw(
+        params, grads, m, v, m_scale, v_scale, w16, step, lr, betas[0], betas[1], eps,
+        weight_decay, grad_scale, _handle(stream)))
+    return params
 
 
 def lin_distill_topk(LOGITS, ids, teacher, DLOGITS, losses, loss_sum, temperature=1.0,
@@ -641,6 +714,11 @@ OTHER_FUNCS = {
     "qk_norm_rope": lin_qk_norm_rope,
     "qk_norm_rope_backward": lin_qk_norm_rope_backward,
     "distill_topk": lin_distill_topk,
+    "qk_norm_rope_axes": lin_qk_norm_rope_axes,
+    "qk_norm_rope_axes_backward": lin_qk_norm_rope_axes_backward,
+    "block_norms": lin_block_norms,
+    "block_norms_backward": lin_block_norms_backward,
+    "adamw": lin_adamw,
 }
 
 
