@@ -423,6 +423,45 @@ lin_status lin_attention_backward(const lin_attention_shape *shape, const lin_he
                                   const lin_heads *DK, const lin_heads *DV, lin_stream_t stream);
 
 /*
+ * The same with a form of the scores: before the mask and the softmax, with
+ * x = scale q k,
+ *   y = cap tanh(x / cap)              (cap 0: y = x)
+ *   S_ij = y - slopes[h] |i + (keys - queries) - j|      (slopes NULL: y)
+ * the distance counted from the end as the causal mask is; and query i sees of
+ * its sequence's keys those with first_key[i] <= j < end_key[i] (NULL: from the
+ * first, to the last), and of these, with `causal`, those that it leaves. So a
+ * document mask (the keys of the query's own document), a prefix mask (not
+ * causal: end_key = max(place + 1, prefix)), a sliding window, and padding
+ * rows (an empty range) are each a range of keys. slopes: f32 [heads_q], any
+ * sign, constants (they get no gradient); first_key, end_key: int32 [tokens_q],
+ * rows as Q's, keys counted from the sequence's first; held to the sequence. A
+ * form without cap, slopes and ranges (or NULL) is lin_attention itself. LSE,
+ * O and the gradients are those of S; a row whose range is empty is one that
+ * the mask leaves nothing. The backward form's dS has 1 - (y / cap)^2 as a
+ * factor, which is rounded to 11 bits for dQ (dS itself is rounded to 16 bits
+ * for its products). Tiles of keys that no row of a tile of queries sees are
+ * not computed. Workspace (backward, ranges): 8 bytes more for each tile of
+ * 128 queries. cap >= 0 and finite, else LIN_ERROR_INVALID_VALUE; all else as
+ * for lin_attention.
+ */
+typedef struct lin_score_form {
+  float cap;
+  const float *slopes;
+  const int32_t *first_key, *end_key;
+} lin_score_form;
+
+lin_status lin_attention_scores(const lin_attention_shape *shape, const lin_score_form *form,
+                                const lin_heads *Q, const lin_heads *K, const lin_heads *V,
+                                const lin_heads *O, float *LSE, lin_stream_t stream);
+lin_status lin_attention_scores_backward(const lin_attention_shape *shape,
+                                         const lin_score_form *form, const lin_heads *Q,
+                                         const lin_heads *K, const lin_heads *V,
+                                         const lin_heads *O, const float *LSE,
+                                         const lin_heads *DO, const lin_heads *DQ,
+                                         const lin_heads *DK, const lin_heads *DV,
+                                         lin_stream_t stream);
+
+/*
  * Norms and rotation of the query and key heads
  * ---------------------------------------------
  * What stands between the QKV projection and attention (the pages name

@@ -210,3 +210,56 @@ def test_the_module_counts_its_arguments():
                  (calls.block_norms, 11), (calls.block_norms_backward, 16), (calls.adamw, 15)):
         with pytest.raises(TypeError, match=f"{n} arguments, not 1"):
             f(None)
+
+
+# ---------------------------------------------------------------- scores of attention
+
+class Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class Shape(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("causal", ctypes.c_int32)] + \
+        [(k, ctypes.c_int64) for k in ("tokens_q", "tokens_k", "heads_q", "heads_kv", "dim", "sequences",
+                                       "max_q", "max_k")] + \
+        [("cu_q", ctypes.c_void_p), ("cu_k", ctypes.c_void_p), ("scale", ctypes.c_float)]
+
+
+class Form(ctypes.Structure):
+    _fields_ = [("cap", ctypes.c_float), ("slopes", ctypes.c_void_p), ("first_key", ctypes.c_void_p),
+                ("end_key", ctypes.c_void_p)]
+
+
+def _scores(L, backward=False, scale=1.0, **form):
+    s = Shape(0, 1, 16, 16, 2, 1, 64, 1, 16, 16, None, None, scale)
+    t = [Heads(_at(i + 1), 2 * 64, 64) for i in range(8)]
+    f = Form(**form)
+    if backward:
+        args = [*t[:4], _at(30), *t[4:]]
+        return L.lin_attention_scores_backward(
+            ctypes.byref(s), ctypes.byref(f), *(x if isinstance(x, int) else ctypes.byref(x) for x in args), None)
+    return L.lin_attention_scores(ctypes.byref(s), ctypes.byref(f), *(ctypes.byref(x) for x in t[:4]), _at(30),
+                                  None)
+
+
+@pytest.mark.parametrize("backward", [False, True])
+def test_scores_numbers(L, backward):
+    for cap in (-1.0, float("nan"), float("inf"), float("-inf")):
+        assert _scores(L, backward, cap=cap) == INVALID
+    assert _scores(L, backward, scale=0.0, cap=1.0) == INVALID
+    f = L.lin_attention_scores_backward if backward else L.lin_attention_scores
+    assert f(None, None, *[None] * (10 if backward else 6)) == INVALID
+
+
+def test_scores_python():
+    torch = pytest.importorskip("torch")
+    build.build_library()
+    h = torch.zeros(4, 2, 8, dtype=torch.float16)
+    with pytest.raises(TypeError, match="Q must be a CUDA tensor"):
+        lin.lin_attention_scores(h, h, h, h, h, cap=3.0)
+    with pytest.raises(TypeError, match="Q must be a CUDA tensor"):
+        lin.lin_attention_scores_backward(h, h, h, h, h, h, h, h, h, cap=3.0)
+    for f, n in ((lin._short_calls().attention_scores, 16), (lin._short_calls().attention_scores_backward, 20)):
+        with pytest.raises(TypeError, match=f"{n} arguments, not 1"):
+            f(None)

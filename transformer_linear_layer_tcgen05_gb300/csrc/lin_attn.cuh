@@ -11,6 +11,7 @@
 // P^T dO, dS^T Q, dS K).
 #pragma once
 
+#include <climits>
 #include <cuda_bf16.h>
 
 #include "lin_attn.h"
@@ -19,6 +20,7 @@
 namespace lin {
 
 constexpr float kLog2E = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 constexpr int kAttnThreads = 320;   // 8 element-wise warps, 1 copying, 1 issuing products
 constexpr int kAttnCopyWarp = 8;
@@ -218,6 +220,57 @@ __device__ __forceinline__ bool k_row_ok(const AttnArgs& a, int64_t token, int h
 __device__ __forceinline__ bool stage_ok(const AttnArgs& a, int s, int stages) {
   return dcheck(s >= 0 && s < stages, a.status, CHK_STAGE, s);
 }
+
+// ---------------------------------------------------------------- scores
+
+// The keys lo .. hi - 1 of its sequence that a query sees (none: 0, 0).
+struct KeyRange {
+  int lo, hi;
+};
+__device__ __forceinline__ KeyRange key_range(const ScoreForm& f, bool causal, const SeqRange& sq,
+                                              const SeqRange& sk, int i) {
+  int lo = f.first ? max(f.first[sq.start + i], 0) : 0;
+  int hi = f.end ? min(f.end[sq.start + i], sk.len) : sk.len;
+  if (causal) hi = min(hi, i + sk.len - sq.len + 1);
+  return lo < hi ? KeyRange{lo, hi} : KeyRange{0, 0};
+}
+// What the rows of a warp see together (none: INT_MAX, 0), and several warps'.
+__device__ __forceinline__ KeyRange warp_extent(const KeyRange& r) {
+  return KeyRange{__reduce_min_sync(0xffffffffu, r.hi > 0 ? r.lo : INT_MAX),
+                  __reduce_max_sync(0xffffffffu, r.hi)};
+}
+__device__ __forceinline__ KeyRange join_extents(const int* e, int n) {
+  KeyRange r{INT_MAX, 0};
+  for (int w = 0; w < n; ++w) r = KeyRange{min(r.lo, e[2 * w]), max(r.hi, e[2 * w + 1])};
+  return r;
+}
+
+// The scores' form in base-2 units. With u = scale s / cap and r = 1 / (1 +
+// e^2u): tanh u = 1 - 2 r, which neither over- nor underflows to anything but
+// its limits, and its derivative 1 - tanh^2 u = 4 r (1 - r).
+struct ScoreTurn {
+  bool capped, biased, any;
+  float2 arg, top, back, plain;   // 2 log2 e scale / cap; cap log2 e; -2 of it; scale log2 e
+  __device__ __forceinline__ ScoreTurn(const ScoreForm& f, bool on, float scale)
+      : capped(on && f.cap > 0.0f), biased(on && f.slopes != nullptr), any(capped || biased) {
+    const float a = capped ? 2.0f * kLog2E * scale / f.cap : 0.0f, t = f.cap * kLog2E;
+    arg = make_float2(a, a);
+    top = make_float2(t, t);
+    back = make_float2(-2.0f * t, -2.0f * t);
+    plain = make_float2(scale * kLog2E, scale * kLog2E);
+  }
+  // r of two scores
+  __device__ __forceinline__ float2 rest(float2 s) const {
+    const float2 x = mul2(s, arg);
+    const float2 e = add2(make_float2(ex2_approx(x.x), ex2_approx(x.y)), make_float2(1.0f, 1.0f));
+    return make_float2(rcp_approx(e.x), rcp_approx(e.y));
+  }
+  __device__ __forceinline__ float2 value(float2 r) const { return fma2(r, back, top); }
+  static __device__ __forceinline__ float2 slope(float2 r) {
+    const float2 four = mul2(r, make_float2(4.0f, 4.0f));
+    return fma2(make_float2(-four.x, -four.y), r, four);
+  }
+};
 
 // Eight 16-bit entries of a row to global memory.
 __device__ __forceinline__ void store16(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {

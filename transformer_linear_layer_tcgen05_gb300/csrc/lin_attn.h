@@ -24,6 +24,15 @@ struct AttnArgs {
   int* status;
 };
 
+// A form of the scores: z = cap tanh(scale s / cap) - slope |distance| (cap 0:
+// scale s; slopes null: no bias), and the keys first .. end - 1 of a query,
+// counted in its sequence (null: from the first, to the last).
+struct ScoreForm {
+  float cap;
+  const float* slopes;             // [heads_q]
+  const int32_t *first, *end;      // [tokens_q]
+};
+
 struct AttnFwdArgs {
   AttnArgs s;
   HeadsPtr o;
@@ -37,6 +46,7 @@ struct AttnFwdArgs {
   // tiles of a CTA (1 or 2), query heads of a tile (1, or all that share a key
   // head), and its queries: 128 / pack
   int32_t tiles, pack, tile_q;
+  ScoreForm scores;
 };
 
 struct AttnBwdArgs {
@@ -57,6 +67,8 @@ struct AttnBwdArgs {
   // key head
   int32_t shift;
   float *dq_part, *dk_part, *dv_part;
+  ScoreForm scores;
+  int2* extents;          // [sequences][row tiles]: keys that a tile's rows see (ranges of keys)
 };
 
 struct AttnFwdMaps {
@@ -69,14 +81,24 @@ struct AttnBwdMaps {
 // Parts that the other side of a launch of `ctas` CTAs is cut into (`rows`: of
 // the other side that the longest runs over).
 int attn_parts(int64_t ctas, int64_t rows, int sms);
-// One kernel; with several parts another one that joins them.
+// One kernel, without and with a form of the scores; and, with several parts,
+// another one that joins them.
 cudaError_t launch_attn_fwd(bool bf16, const AttnFwdMaps& maps, const AttnFwdArgs& args,
                             int heads_kv, int sequences, cudaStream_t stream);
+cudaError_t launch_attn_scores_fwd(bool bf16, const AttnFwdMaps& maps, const AttnFwdArgs& args,
+                                   int heads_kv, int sequences, cudaStream_t stream);
+cudaError_t launch_attn_join_parts(bool bf16, const AttnFwdArgs& args, int heads, int sequences,
+                                   cudaStream_t stream);
 // Tokens of a box of the backward kernels' maps.
 constexpr int kAttnBwdBox = 64;
-// The dQ kernel (which also leaves delta and norm), the dK, dV kernel, and the
-// sums of their parts; *kernels: how many that were.
+// The dQ kernel (which also leaves delta and norm) and the dK, dV kernel,
+// without and with a form of the scores, and the sums of their parts; *kernels:
+// how many that were.
 cudaError_t launch_attn_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArgs& args,
                             int heads_kv, int sequences, int* kernels, cudaStream_t stream);
+cudaError_t launch_attn_scores_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArgs& args,
+                                   int heads_kv, int sequences, int* kernels, cudaStream_t stream);
+cudaError_t launch_attn_sum_parts(bool bf16, const AttnBwdArgs& args, int heads_kv, int sequences,
+                                  int* kernels, cudaStream_t stream);
 
 }  // namespace lin

@@ -105,17 +105,53 @@ lin::AttnArgs attn_args(const lin_attention_shape* s, const Checked& c) {
   return a;
 }
 
-lin_status attention(const lin_attention_shape* s, const lin_heads* Q, const lin_heads* K,
-                     const lin_heads* V, const lin_heads* O, float* LSE, cudaStream_t stream) {
+// The form's numbers and arrays, after check_attention() has seen the rest.
+lin_status check_form(const lin_score_form* f, const lin_attention_shape* s, const View* views,
+                      int nviews, const float* lse, bool lse_out, const Checked& c) {
+  if (!f) return LIN_SUCCESS;
+  const struct {
+    const void* p;
+    uint64_t bytes;
+  } arrays[] = {{f->slopes, (uint64_t)s->heads_q * 4},
+                {f->first_key, (uint64_t)s->tokens_q * 4},
+                {f->end_key, (uint64_t)s->tokens_q * 4}};
+  SeenRange seen;
+  for (const auto& a : arrays) {
+    if (!a.p || !a.bytes) continue;
+    if ((reinterpret_cast<uintptr_t>(a.p) & 3u) != 0) return LIN_ERROR_MISALIGNED;
+    if (lse_out && overlaps(a.p, a.bytes, lse, (uint64_t)s->heads_q * (uint64_t)s->tokens_q * 4))
+      return LIN_ERROR_ALIASING;
+    for (int i = 0; i < nviews; ++i)
+      if (views[i].out && overlaps(a.p, a.bytes, views[i].t->data, views[i].extent)) return LIN_ERROR_ALIASING;
+    const lin_status st = check_buffer(a.p, a.bytes, c.dev, &seen);
+    if (st != LIN_SUCCESS) return st;
+  }
+  return LIN_SUCCESS;
+}
+// (its numbers are checked before anything touches CUDA)
+bool form_ok(const lin_score_form* f) { return !f || (f->cap >= 0.0f && !std::isinf(f->cap)); }
+// Whether there is a form at all, and the kernels' view of it.
+bool has_form(const lin_score_form* f) {
+  return f && (f->cap > 0.0f || f->slopes || f->first_key || f->end_key);
+}
+lin::ScoreForm score_form(const lin_score_form* f) {
+  return f ? lin::ScoreForm{f->cap, f->slopes, f->first_key, f->end_key} : lin::ScoreForm{};
+}
+
+lin_status attention(const lin_attention_shape* s, const lin_score_form* form, const lin_heads* Q,
+                     const lin_heads* K, const lin_heads* V, const lin_heads* O, float* LSE,
+                     cudaStream_t stream) {
   set_last_launch_info(0, 0);
+  if (!form_ok(form)) return LIN_ERROR_INVALID_VALUE;
   const int64_t hq = s ? s->heads_q : 0, hk = s ? s->heads_kv : 0;
   View v[] = {{Q, 0, hq, false}, {K, -1, hk, false}, {V, -1, hk, false}, {O, 0, hq, true}};
   Checked c;
-  const lin_status st = check_attention(s, v, 4, LSE, true, &c);
+  lin_status st = check_attention(s, v, 4, LSE, true, &c);
+  if (st == LIN_SUCCESS) st = check_form(form, s, v, 4, LSE, true, c);
   if (st != LIN_SUCCESS) return st;
   if (c.nothing || c.max_q == 0) return LIN_SUCCESS;
   lin::AttnFwdArgs a{attn_args(s, c), heads_ptr(v[3]), LSE, 1, 0, nullptr,
-                     nullptr, 2, 1, 128};
+                     nullptr, 2, 1, 128, score_form(form)};
   const int sms = sm_count(c.dev);
   auto tiles = [&] {
     return (c.max_q + a.tile_q - 1) / a.tile_q * (s->heads_q / a.pack) * s->sequences;
@@ -155,8 +191,13 @@ lin_status attention(const lin_attention_shape* s, const lin_heads* Q, const lin
     if (!a.o_part) return LIN_ERROR_CUDA;
     a.lse_part = a.o_part + part_rows * (uint64_t)s->dim;
   }
-  cudaError_t e = lin::launch_attn_fwd(s->dtype == LIN_BFLOAT16, maps, a, (int)s->heads_kv,
-                                       (int)s->sequences, stream);
+  const bool bf16 = s->dtype == LIN_BFLOAT16;
+  cudaError_t e = has_form(form) ? lin::launch_attn_scores_fwd(bf16, maps, a, (int)s->heads_kv,
+                                                               (int)s->sequences, stream)
+                                 : lin::launch_attn_fwd(bf16, maps, a, (int)s->heads_kv,
+                                                        (int)s->sequences, stream);
+  if (e == cudaSuccess && a.parts > 1)
+    e = lin::launch_attn_join_parts(bf16, a, (int)s->heads_q, (int)s->sequences, stream);
   if (bytes) {
     const cudaError_t ef = cudaFreeAsync(a.o_part, stream);
     if (e == cudaSuccess) e = ef;
@@ -166,16 +207,19 @@ lin_status attention(const lin_attention_shape* s, const lin_heads* Q, const lin
   return LIN_SUCCESS;
 }
 
-lin_status attention_backward(const lin_attention_shape* s, const lin_heads* Q, const lin_heads* K,
-                              const lin_heads* V, const lin_heads* O, const float* LSE,
-                              const lin_heads* DO, const lin_heads* DQ, const lin_heads* DK,
-                              const lin_heads* DV, cudaStream_t stream) {
+lin_status attention_backward(const lin_attention_shape* s, const lin_score_form* form,
+                              const lin_heads* Q, const lin_heads* K, const lin_heads* V,
+                              const lin_heads* O, const float* LSE, const lin_heads* DO,
+                              const lin_heads* DQ, const lin_heads* DK, const lin_heads* DV,
+                              cudaStream_t stream) {
   set_last_launch_info(0, 0);
+  if (!form_ok(form)) return LIN_ERROR_INVALID_VALUE;
   const int64_t hq = s ? s->heads_q : 0, hk = s ? s->heads_kv : 0;
   View v[] = {{Q, 0, hq, false},  {K, -1, hk, false}, {V, -1, hk, false}, {O, 0, hq, false},
               {DO, 0, hq, false}, {DQ, 0, hq, true},  {DK, -1, hk, true}, {DV, -1, hk, true}};
   Checked c;
-  const lin_status st = check_attention(s, v, 8, LSE, false, &c);
+  lin_status st = check_attention(s, v, 8, LSE, false, &c);
+  if (st == LIN_SUCCESS) st = check_form(form, s, v, 8, LSE, false, c);
   if (st != LIN_SUCCESS) return st;
   if (c.nothing || (c.max_q == 0 && c.max_k == 0)) return LIN_SUCCESS;
   lin::AttnBwdArgs a{};
@@ -213,15 +257,18 @@ lin_status attention_backward(const lin_attention_shape* s, const lin_heads* Q, 
   const int sms = sm_count(c.dev);
   a.q_parts = lin::attn_parts(tq * hq_tiles * s->sequences, c.max_k, sms);
   a.k_parts = lin::attn_parts(tk * s->heads_kv * s->sequences, c.max_q * (int64_t)a.s.group, sms);
-  // workspace: the parts' sums, delta [heads][tokens], then the largest dO
-  // norms of the query tiles
+  // workspace: the parts' sums, delta [heads][tokens], the largest dO norms of
+  // the query tiles, and (ranges of keys) the keys that each of them sees
   if (a.q_parts > 1) a.q_part_rows = (int32_t)(s->sequences * c.max_q);
   if (a.k_parts > 1) a.k_part_rows = (int32_t)(s->sequences * c.max_k);
   const uint64_t dq = (uint64_t)a.q_parts * a.q_part_rows * s->heads_q * s->dim;
   const uint64_t dk = (uint64_t)a.k_parts * a.k_part_rows * s->heads_kv * s->dim;
   const uint64_t delta = (uint64_t)s->heads_q * (uint64_t)s->tokens_q;
   const uint64_t norms = (uint64_t)s->sequences * (uint64_t)hq_tiles * (uint64_t)tq;
-  const size_t bytes = (size_t)std::max<uint64_t>(16, (dq + 2 * dk + delta + norms) * 4);
+  const bool ranged = form && (form->first_key || form->end_key);
+  const uint64_t before = (dq + 2 * dk + delta + norms + 1) / 2 * 2;   // (8-byte aligned extents)
+  const uint64_t extents = ranged ? 2 * (uint64_t)s->sequences * (uint64_t)tq : 0;
+  const size_t bytes = (size_t)std::max<uint64_t>(16, (before + extents) * 4);
   float* ws = static_cast<float*>(take_stream_workspace(c.dev, bytes, stream));
   if (!ws) return LIN_ERROR_CUDA;
   a.dq_part = ws;
@@ -230,9 +277,14 @@ lin_status attention_backward(const lin_attention_shape* s, const lin_heads* Q, 
   a.delta = a.dv_part + dk;
   a.norm = a.delta + delta;
   a.norms = (int64_t)norms;
+  a.scores = score_form(form);
+  if (ranged) a.extents = reinterpret_cast<int2*>(ws + before);
   int kernels = 0;
-  cudaError_t e = lin::launch_attn_bwd(s->dtype == LIN_BFLOAT16, maps, a, (int)s->heads_kv,
-                                       (int)s->sequences, &kernels, stream);
+  const bool bf16 = s->dtype == LIN_BFLOAT16;
+  const int hkv = (int)s->heads_kv, seqs = (int)s->sequences;
+  cudaError_t e = has_form(form) ? lin::launch_attn_scores_bwd(bf16, maps, a, hkv, seqs, &kernels, stream)
+                                 : lin::launch_attn_bwd(bf16, maps, a, hkv, seqs, &kernels, stream);
+  if (e == cudaSuccess) e = lin::launch_attn_sum_parts(bf16, a, hkv, seqs, &kernels, stream);
   const cudaError_t ef = cudaFreeAsync(ws, stream);
   if (e == cudaSuccess) e = ef;
   if (e != cudaSuccess) return cuda_fail(e);
@@ -248,14 +300,32 @@ extern "C" {
 lin_status lin_attention(const lin_attention_shape* shape, const lin_heads* Q, const lin_heads* K,
                          const lin_heads* V, const lin_heads* O, float* LSE,
                          lin_stream_t stream) {
-  return lin_detail::attention(shape, Q, K, V, O, LSE, reinterpret_cast<cudaStream_t>(stream));
+  return lin_detail::attention(shape, nullptr, Q, K, V, O, LSE,
+                               reinterpret_cast<cudaStream_t>(stream));
 }
 
 lin_status lin_attention_backward(const lin_attention_shape* shape, const lin_heads* Q,
                                   const lin_heads* K, const lin_heads* V, const lin_heads* O,
                                   const float* LSE, const lin_heads* DO, const lin_heads* DQ,
                                   const lin_heads* DK, const lin_heads* DV, lin_stream_t stream) {
-  return lin_detail::attention_backward(shape, Q, K, V, O, LSE, DO, DQ, DK, DV,
+  return lin_detail::attention_backward(shape, nullptr, Q, K, V, O, LSE, DO, DQ, DK, DV,
+                                        reinterpret_cast<cudaStream_t>(stream));
+}
+
+lin_status lin_attention_scores(const lin_attention_shape* shape, const lin_score_form* form,
+                                const lin_heads* Q, const lin_heads* K, const lin_heads* V,
+                                const lin_heads* O, float* LSE, lin_stream_t stream) {
+  return lin_detail::attention(shape, form, Q, K, V, O, LSE, reinterpret_cast<cudaStream_t>(stream));
+}
+
+lin_status lin_attention_scores_backward(const lin_attention_shape* shape,
+                                         const lin_score_form* form, const lin_heads* Q,
+                                         const lin_heads* K, const lin_heads* V,
+                                         const lin_heads* O, const float* LSE,
+                                         const lin_heads* DO, const lin_heads* DQ,
+                                         const lin_heads* DK, const lin_heads* DV,
+                                         lin_stream_t stream) {
+  return lin_detail::attention_backward(shape, form, Q, K, V, O, LSE, DO, DQ, DK, DV,
                                         reinterpret_cast<cudaStream_t>(stream));
 }
 

@@ -28,7 +28,8 @@ namespace {
 const char* const kNames[] = {"lin_attention", "lin_attention_backward", "lin_qk_norm_rope",
                               "lin_qk_norm_rope_backward", "lin_distill_topk",
                               "lin_qk_norm_rope_axes", "lin_qk_norm_rope_axes_backward",
-                              "lin_block_norms", "lin_block_norms_backward", "lin_adamw"};
+                              "lin_block_norms", "lin_block_norms_backward", "lin_adamw",
+                              "lin_attention_scores", "lin_attention_scores_backward"};
 constexpr int kFunctions = sizeof(kNames) / sizeof(kNames[0]);
 void* g_address[kFunctions];
 
@@ -201,6 +202,60 @@ lin_status unlocked(F* f, A... a) {
   st = f(a...);
   Py_END_ALLOW_THREADS
   return st;
+}
+
+// cap, slopes, first_key, end_key
+lin_score_form score_form(PyObject* const* a, const lin_attention_shape& s) {
+  lin_score_form f{};
+  if (a[0] != Py_None) {
+    const double cap = number(a[0]);
+    f.cap = (float)cap;
+    if (!(cap > 0.0) || !(f.cap > 0.0f)) raise(PyExc_ValueError, "cap must be above zero");
+  }
+  if (a[1] != Py_None) f.slopes = f32(a[1], "slopes", {s.heads_q});
+  if (a[2] != Py_None) f.first_key = flat<int32_t>(a[2], "first_key", at::kInt, {s.tokens_q});
+  if (a[3] != Py_None) f.end_key = flat<int32_t>(a[3], "end_key", at::kInt, {s.tokens_q});
+  return f;
+}
+
+// Q, K, V, O, LSE, cu_q, cu_k, max_q, max_k, causal, scale, cap, slopes,
+// first_key, end_key, stream
+PyObject* attention_scores(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 16, [&] {
+    Heads h;
+    lin_heads q, k, v, o;
+    const at::Tensor &tq = h.take(a[0], "Q", &q), &tk = h.take(a[1], "K", &k),
+                     &tv = h.take(a[2], "V", &v), &to = h.take(a[3], "O", &o);
+    const lin_attention_shape s = attention_shape(h, tq, tk, tv, a + 5);
+    same_shape(to, "O", tq);
+    float* lse = f32(a[4], "LSE", {s.heads_q, s.tokens_q});
+    const lin_score_form f = score_form(a + 11, s);
+    return unlocked(bound<decltype(lin_attention_scores)>(10), &s, &f, &q, &k, &v, &o, lse,
+                    stream_of(a[15]));
+  });
+}
+
+// Q, K, V, O, LSE, dO, dQ, dK, dV, cu_q, cu_k, max_q, max_k, causal, scale,
+// cap, slopes, first_key, end_key, stream
+PyObject* attention_scores_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 20, [&] {
+    Heads h;
+    lin_heads q, k, v, o, dout, dq, dk, dv;
+    const at::Tensor &tq = h.take(a[0], "Q", &q), &tk = h.take(a[1], "K", &k),
+                     &tv = h.take(a[2], "V", &v), &to = h.take(a[3], "O", &o),
+                     &tdo = h.take(a[5], "dO", &dout), &tdq = h.take(a[6], "dQ", &dq),
+                     &tdk = h.take(a[7], "dK", &dk), &tdv = h.take(a[8], "dV", &dv);
+    const lin_attention_shape s = attention_shape(h, tq, tk, tv, a + 9);
+    same_shape(to, "O", tq);
+    same_shape(tdo, "dO", tq);
+    same_shape(tdq, "dQ", tq);
+    same_shape(tdk, "dK", tk);
+    same_shape(tdv, "dV", tk);
+    const float* lse = f32(a[4], "LSE", {s.heads_q, s.tokens_q});
+    const lin_score_form f = score_form(a + 15, s);
+    return unlocked(bound<decltype(lin_attention_scores_backward)>(11), &s, &f, &q, &k, &v, &o, lse,
+                    &dout, &dq, &dk, &dv, stream_of(a[19]));
+  });
 }
 
 // Q, K, V, O, LSE, cu_q, cu_k, max_q, max_k, causal, scale, stream
@@ -583,6 +638,8 @@ PyMethodDef kMethods[] = {
     {"block_norms", as_method(block_norms), METH_FASTCALL, nullptr},
     {"block_norms_backward", as_method(block_norms_backward), METH_FASTCALL, nullptr},
     {"adamw", as_method(adamw), METH_FASTCALL, nullptr},
+    {"attention_scores", as_method(attention_scores), METH_FASTCALL, nullptr},
+    {"attention_scores_backward", as_method(attention_scores_backward), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_lin_calls", nullptr, -1, kMethods,

@@ -88,6 +88,8 @@ SIGNATURES = {
     "lin_set_host_block_bytes": [ctypes.c_uint64],
     "lin_attention": [_P, _P, _P, _P, _P, _P, _S],
     "lin_attention_backward": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S],
+    "lin_attention_scores": [_P, _P, _P, _P, _P, _P, _P, _S],
+    "lin_attention_scores_backward": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S],
     "lin_qk_norm_rope": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S],
     "lin_qk_norm_rope_backward": [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S],
     "lin_qk_norm_rope_axes": [_P, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _S],
@@ -435,7 +437,7 @@ def _short_calls():
             "lin_attention", "lin_attention_backward", "lin_qk_norm_rope",
             "lin_qk_norm_rope_backward", "lin_distill_topk", "lin_qk_norm_rope_axes",
             "lin_qk_norm_rope_axes_backward", "lin_block_norms", "lin_block_norms_backward",
-            "lin_adamw")})
+            "lin_adamw", "lin_attention_scores", "lin_attention_scores_backward")})
         _calls = _lin_calls
     return _calls
 
@@ -468,6 +470,35 @@ def lin_attention_backward(Q, K, V, O, LSE, DO, DQ, DK, DV, cu_q=None, cu_k=None
     check("lin_attention_backward", (_calls or _short_calls()).attention_backward(
         Q, K, V, O, LSE, DO, DQ, DK, DV, cu_q, cu_k, max_q, max_k, causal, scale,
         _handle(stream)))
+    return DQ, DK, DV
+
+
+def lin_attention_scores(Q, K, V, O, LSE, cap=None, slopes=None, first_key=None, end_key=None,
+                         cu_q=None, cu_k=None, max_q=None, max_k=None, causal=True, scale=None,
+                         stream=None):
+    """lin_attention with a form of the scores: S = cap tanh(scale Q K^T / cap)
+    - slopes |distance| over each query's own range of keys.
+
+    ``cap`` a number (None: no cap); ``slopes`` float32 [heads], constants;
+    ``first_key``, ``end_key`` int32 [tokens]: the first key that a query sees
+    and the one behind its last, counted in its sequence, held to it, and, with
+    ``causal``, to the causal mask (a document's keys, a prefix, a window; an
+    empty range: O = 0, LSE = -inf). Distances count from the end, as ``causal``
+    does."""
+    check("lin_attention_scores", (_calls or _short_calls()).attention_scores(
+        Q, K, V, O, LSE, cu_q, cu_k, max_q, max_k, causal, scale, cap, slopes, first_key, end_key,
+        _handle(stream)))
+    return O, LSE
+
+
+def lin_attention_scores_backward(Q, K, V, O, LSE, DO, DQ, DK, DV, cap=None, slopes=None,
+                                  first_key=None, end_key=None, cu_q=None, cu_k=None, max_q=None,
+                                  max_k=None, causal=True, scale=None, stream=None):
+    """dQ, dK, dV of lin_attention_scores from dO and that call's inputs and
+    results."""
+    check("lin_attention_scores_backward", (_calls or _short_calls()).attention_scores_backward(
+        Q, K, V, O, LSE, DO, DQ, DK, DV, cu_q, cu_k, max_q, max_k, causal, scale, cap, slopes,
+        first_key, end_key, _handle(stream)))
     return DQ, DK, DV
 
 
@@ -719,6 +750,8 @@ OTHER_FUNCS = {
     "block_norms": lin_block_norms,
     "block_norms_backward": lin_block_norms_backward,
     "adamw": lin_adamw,
+    "attention_scores": lin_attention_scores,
+    "attention_scores_backward": lin_attention_scores_backward,
 }
 
 
