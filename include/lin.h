@@ -438,9 +438,7 @@ lin_status lin_attention_backward(const lin_attention_shape *shape, const lin_he
  * form without cap, slopes and ranges (or NULL) is lin_attention itself. LSE,
  * O and the gradients are those of S; a row whose range is empty is one that
  * the mask leaves nothing. The backward form's dS has 1 - (y / cap)^2 as a
- * factor, which is rounded to 11 bits for dQ (dS itself is rounded to 16 bits
- * for its products). Tiles of keys that no row of a tile of queries sees are
- * not computed. Workspace (backward, ranges): 8 bytes more for each tile of
+ * factor. Tiles of keys that no row of a tile of queries sees are not computed. Workspace (backward, ranges): 8 bytes more for each tile of
  * 128 queries. cap >= 0 and finite, else LIN_ERROR_INVALID_VALUE; all else as
  * for lin_attention.
  */

@@ -45,7 +45,9 @@ SOURCES = ["lin_api.cu", "lin_kernels_tf32.cu", "lin_kernels_f16.cu",
            "lin_kernels_cluster_swiglu.cu", "lin_kernels_cluster_cvt.cu",
            "lin_kernels_cluster_bt.cu", "lin_kernels_cluster_dual.cu", "lin_loss.cu",
            "lin_noalloc.cu", "lin_host.cu", "lin_attn_fwd.cu", "lin_attn_bwd.cu",
-           "lin_attn_scores_fwd.cu", "lin_attn_scores_bwd.cu",
+           "lin_attn_fwd_ranges.cu", "lin_attn_fwd_cap.cu", "lin_attn_fwd_bias.cu",
+           "lin_attn_fwd_cap_bias.cu", "lin_attn_bwd_ranges.cu", "lin_attn_bwd_cap.cu",
+           "lin_attn_bwd_bias.cu", "lin_attn_bwd_cap_bias.cu",
            "lin_attn_api.cu", "lin_rope.cu", "lin_distill.cu", "lin_norms.cu", "lin_adamw.cu",
            "lin_step_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

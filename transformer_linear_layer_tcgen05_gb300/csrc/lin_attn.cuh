@@ -245,30 +245,35 @@ __device__ __forceinline__ KeyRange join_extents(const int* e, int n) {
   return r;
 }
 
-// The scores' form in base-2 units. With u = scale s / cap and r = 1 / (1 +
-// e^2u): tanh u = 1 - 2 r, which neither over- nor underflows to anything but
-// its limits, and its derivative 1 - tanh^2 u = 4 r (1 - r).
+// The scores' form in base-2 units, two scores at a time. With u = scale s /
+// cap and r = 1 / (1 + e^2u): tanh u = 1 - 2 r, which neither over- nor
+// underflows to anything but its limits, and its derivative is 4 r (1 - r). So
+// a capped score is a line in r, and what follows goes by r: the softmax's
+// factor and shift take in the line's. FORM: kCap, kBias, both or none (ranges
+// of keys alone), the compiler's parameter: asked for in the loops, each part
+// of the form cut them into short pieces (16 heads of 128, 8192 tokens, the
+// gradient 1031 us).
 struct ScoreTurn {
-  bool capped, biased, any;
-  float2 arg, top, back, plain;   // 2 log2 e scale / cap; cap log2 e; -2 of it; scale log2 e
-  __device__ __forceinline__ ScoreTurn(const ScoreForm& f, bool on, float scale)
-      : capped(on && f.cap > 0.0f), biased(on && f.slopes != nullptr), any(capped || biased) {
-    const float a = capped ? 2.0f * kLog2E * scale / f.cap : 0.0f, t = f.cap * kLog2E;
+  float2 arg;         // 2 log2 e scale / cap
+  float top, twice;   // cap log2 e, and twice that
+  __device__ __forceinline__ ScoreTurn(const ScoreForm& f, float scale)
+      : top(f.cap * kLog2E), twice(2.0f * top) {
+    const float a = 2.0f * kLog2E * scale / f.cap;
     arg = make_float2(a, a);
-    top = make_float2(t, t);
-    back = make_float2(-2.0f * t, -2.0f * t);
-    plain = make_float2(scale * kLog2E, scale * kLog2E);
   }
-  // r of two scores
+  // r of two scores (SIGN -1: -r); twice * -r + top is the capped score
+  template <int SIGN>
   __device__ __forceinline__ float2 rest(float2 s) const {
+    constexpr float one = (float)SIGN;
     const float2 x = mul2(s, arg);
-    const float2 e = add2(make_float2(ex2_approx(x.x), ex2_approx(x.y)), make_float2(1.0f, 1.0f));
+    float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+    e = SIGN > 0 ? add2(e, make_float2(one, one)) : fma2(e, make_float2(one, one), make_float2(one, one));
     return make_float2(rcp_approx(e.x), rcp_approx(e.y));
   }
-  __device__ __forceinline__ float2 value(float2 r) const { return fma2(r, back, top); }
-  static __device__ __forceinline__ float2 slope(float2 r) {
-    const float2 four = mul2(r, make_float2(4.0f, 4.0f));
-    return fma2(make_float2(-four.x, -four.y), r, four);
+  // p times the cap's derivative, from r
+  static __device__ __forceinline__ float2 times_slope(float2 p, float2 r) {
+    const float2 left = fma2(r, make_float2(-4.0f, -4.0f), make_float2(4.0f, 4.0f));
+    return mul2(mul2(p, r), left);
   }
 };
 

@@ -27,6 +27,7 @@ struct AttnArgs {
 // A form of the scores: z = cap tanh(scale s / cap) - slope |distance| (cap 0:
 // scale s; slopes null: no bias), and the keys first .. end - 1 of a query,
 // counted in its sequence (null: from the first, to the last).
+constexpr int kNoForm = -1, kCap = 1, kBias = 2;   // (forms of ranges alone: 0)
 struct ScoreForm {
   float cap;
   const float* slopes;             // [heads_q]
@@ -81,23 +82,20 @@ struct AttnBwdMaps {
 // Parts that the other side of a launch of `ctas` CTAs is cut into (`rows`: of
 // the other side that the longest runs over).
 int attn_parts(int64_t ctas, int64_t rows, int sms);
-// One kernel, without and with a form of the scores; and, with several parts,
-// another one that joins them.
+// One kernel for a form of the scores (kNoForm, or kCap and kBias, or 0); and,
+// with several parts, another one that joins them.
+template <int FORM>
 cudaError_t launch_attn_fwd(bool bf16, const AttnFwdMaps& maps, const AttnFwdArgs& args,
                             int heads_kv, int sequences, cudaStream_t stream);
-cudaError_t launch_attn_scores_fwd(bool bf16, const AttnFwdMaps& maps, const AttnFwdArgs& args,
-                                   int heads_kv, int sequences, cudaStream_t stream);
 cudaError_t launch_attn_join_parts(bool bf16, const AttnFwdArgs& args, int heads, int sequences,
                                    cudaStream_t stream);
 // Tokens of a box of the backward kernels' maps.
 constexpr int kAttnBwdBox = 64;
-// The dQ kernel (which also leaves delta and norm) and the dK, dV kernel,
-// without and with a form of the scores, and the sums of their parts; *kernels:
-// how many that were.
+// The dQ kernel (which also leaves delta and norm) and the dK, dV kernel for a
+// form of the scores, and the sums of their parts; *kernels: how many that were.
+template <int FORM>
 cudaError_t launch_attn_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArgs& args,
                             int heads_kv, int sequences, int* kernels, cudaStream_t stream);
-cudaError_t launch_attn_scores_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArgs& args,
-                                   int heads_kv, int sequences, int* kernels, cudaStream_t stream);
 cudaError_t launch_attn_sum_parts(bool bf16, const AttnBwdArgs& args, int heads_kv, int sequences,
                                   int* kernels, cudaStream_t stream);
 

@@ -6,6 +6,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "lin.h"
 #include "lin_attn.h"
@@ -130,10 +131,17 @@ lin_status check_form(const lin_score_form* f, const lin_attention_shape* s, con
 }
 // (its numbers are checked before anything touches CUDA)
 bool form_ok(const lin_score_form* f) { return !f || (f->cap >= 0.0f && !std::isinf(f->cap)); }
-// Whether there is a form at all, and the kernels' view of it.
-bool has_form(const lin_score_form* f) {
-  return f && (f->cap > 0.0f || f->slopes || f->first_key || f->end_key);
+// Calls f with the compiler's parameter for the form.
+template <typename F>
+cudaError_t with_form(const lin_score_form* f, F&& go) {
+  if (!f || (!(f->cap > 0.0f) && !f->slopes && !f->first_key && !f->end_key))
+    return go(std::integral_constant<int, lin::kNoForm>{});
+  if (f->cap > 0.0f)
+    return f->slopes ? go(std::integral_constant<int, lin::kCap | lin::kBias>{})
+                     : go(std::integral_constant<int, lin::kCap>{});
+  return f->slopes ? go(std::integral_constant<int, lin::kBias>{}) : go(std::integral_constant<int, 0>{});
 }
+// The kernels' view of it.
 lin::ScoreForm score_form(const lin_score_form* f) {
   return f ? lin::ScoreForm{f->cap, f->slopes, f->first_key, f->end_key} : lin::ScoreForm{};
 }
@@ -192,10 +200,10 @@ lin_status attention(const lin_attention_shape* s, const lin_score_form* form, c
     a.lse_part = a.o_part + part_rows * (uint64_t)s->dim;
   }
   const bool bf16 = s->dtype == LIN_BFLOAT16;
-  cudaError_t e = has_form(form) ? lin::launch_attn_scores_fwd(bf16, maps, a, (int)s->heads_kv,
-                                                               (int)s->sequences, stream)
-                                 : lin::launch_attn_fwd(bf16, maps, a, (int)s->heads_kv,
-                                                        (int)s->sequences, stream);
+  cudaError_t e = with_form(form, [&](auto f) {
+    return lin::launch_attn_fwd<decltype(f)::value>(bf16, maps, a, (int)s->heads_kv, (int)s->sequences,
+                                                    stream);
+  });
   if (e == cudaSuccess && a.parts > 1)
     e = lin::launch_attn_join_parts(bf16, a, (int)s->heads_q, (int)s->sequences, stream);
   if (bytes) {
@@ -282,8 +290,9 @@ lin_status attention_backward(const lin_attention_shape* s, const lin_score_form
   int kernels = 0;
   const bool bf16 = s->dtype == LIN_BFLOAT16;
   const int hkv = (int)s->heads_kv, seqs = (int)s->sequences;
-  cudaError_t e = has_form(form) ? lin::launch_attn_scores_bwd(bf16, maps, a, hkv, seqs, &kernels, stream)
-                                 : lin::launch_attn_bwd(bf16, maps, a, hkv, seqs, &kernels, stream);
+  cudaError_t e = with_form(form, [&](auto f) {
+    return lin::launch_attn_bwd<decltype(f)::value>(bf16, maps, a, hkv, seqs, &kernels, stream);
+  });
   if (e == cudaSuccess) e = lin::launch_attn_sum_parts(bf16, a, hkv, seqs, &kernels, stream);
   const cudaError_t ef = cudaFreeAsync(ws, stream);
   if (e == cudaSuccess) e = ef;

@@ -92,9 +92,7 @@ cudaError_t launch_attn_sum_parts(bool bf16, const AttnBwdArgs& args, int heads_
   return e;
 }
 
-cudaError_t launch_attn_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArgs& args,
-                            int heads_kv, int sequences, int* kernels, cudaStream_t stream) {
-  return launch_attn_bwd_kernels<false>(bf16, maps, args, heads_kv, sequences, kernels, stream);
-}
+template cudaError_t launch_attn_bwd<kNoForm>(bool, const AttnBwdMaps&, const AttnBwdArgs&, int, int, int*,
+                                              cudaStream_t);
 
 }  // namespace lin

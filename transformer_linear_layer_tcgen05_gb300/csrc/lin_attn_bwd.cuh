@@ -199,11 +199,13 @@ struct HeadGrad {
 
 // ---------------------------------------------------------------- dQ
 
-template <int DP, bool BF16, bool SCORES>
+template <int DP, bool BF16, int FORM>
 __global__ void __launch_bounds__(kAttnThreads, 1)
     lin_attn_dq_kernel(const __grid_constant__ AttnBwdMaps maps,
                        const __grid_constant__ AttnBwdArgs args) {
   using C = DqCfg<DP>;
+  constexpr bool SCORES = FORM != kNoForm;
+  constexpr bool CAPPED = SCORES && (FORM & kCap), BIASED = SCORES && (FORM & kBias);
   static_assert(!C::kOwnSmem && C::OFF_OWN == 0, "own operands in tensor memory");
   extern __shared__ uint8_t smem_raw[];
   const AttnArgs& a = args.s;
@@ -430,14 +432,15 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const float amp = pow2i(ne);
     float nd = -delta * amp;
     // a row without a key (L = -inf) has no probabilities
-    const float nl = lse == -INFINITY ? -INFINITY : -lse * kLog2E;
+    float nl = lse == -INFINITY ? -INFINITY : -lse * kLog2E;
     // the last key that this row sees, and the first
     const int lim = SCORES ? mine.hi - 1
                     : live ? (a.causal ? min(sk.len - 1, i + sk.len - sq.len) : sk.len - 1)
                            : -1;
     const int low = SCORES ? mine.lo : 0;
-    const ScoreTurn turned(args.scores, SCORES, a.scale);
-    const float slope = turned.biased ? args.scores.slopes[h] * kLog2E : 0.0f;
+    const ScoreTurn turned(args.scores, a.scale);
+    const float slope = BIASED && live ? args.scores.slopes[h] * kLog2E : 0.0f;
+    if (CAPPED) nl += turned.top;
     const uint32_t s_col = tmem + lanes + C::S_COL + half * kTurn;
     const uint32_t dp_col = tmem + lanes + C::DP_COL + half * kTurn;
     if (few && n == 1 && half == 1) {   // (no tile: nothing to the row's sums below)
@@ -460,31 +463,87 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(C::S_DONE + half));
-      const float2 cc = make_float2(c, c), ll = make_float2(nl, nl);
-      // the cap's derivative (in 11 bits: dS, which it multiplies, is rounded
-      // to as many or fewer for its product)
-      __half2 chain[SCORES ? 32 : 1];
-      if constexpr (SCORES) {
-        const float here = (float)(i + sk.len - sq.len - (j0 + j) * kTurn);
+      const float f = CAPPED ? -turned.twice : c;
+      const float2 cc = make_float2(f, f), ll = make_float2(nl, nl);
+      // P of two scores (capped: of their r)
+      auto probability = [&](float2 x, float2 far) {
+        x = fma2(x, cc, ll);
+        if (BIASED)
+          x = make_float2(fmaf(-slope, fabsf(far.x), x.x), fmaf(-slope, fabsf(far.y), x.y));
+        return make_float2(ex2_approx(x.x), ex2_approx(x.y));
+      };
+      const float here = (float)(i + sk.len - sq.len - (j0 + j) * kTurn);   // (a bias)
+      // All of the row's keys are in the streams' first tiles (few): delta is at
+      // hand as the sum of P dP itself. It replaces the sum of dO O, whose O has
+      // been rounded to 16 bits: with few keys that rounding is no longer small
+      // against dP - delta (at one key the difference is zero).
+      auto sum_delta = [&]() -> bool {
+        float sd = 0.0f, sp = 0.0f;
+        const int lim_h = lim - (SCORES ? j0 + half : half) * kTurn;
+        const int low_h = SCORES ? low - (j0 + half) * kTurn : 0;
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            float2 x = make_float2(__uint_as_float(p[q][e]), __uint_as_float(p[q][e + 1]));
-            if (turned.capped) {
-              x = turned.rest(x);
-              const float2 d = ScoreTurn::slope(x);
-              chain[q * 16 + e / 2] = __floats2half2_rn(d.x, d.y);
-              x = add2(turned.value(x), ll);
-            } else {
-              x = fma2(x, cc, ll);
+          for (int e = 0; e < 32; ++e)
+            if (q * 32 + e <= lim_h && (!SCORES || q * 32 + e >= low_h)) {
+              float x = __uint_as_float(p[q][e]);
+              if (SCORES) x = probability(make_float2(x, x), make_float2(here - (q * 32 + e), 0.0f)).x;
+              sd = fmaf(x, __uint_as_float(d[q][e]), sd);
+              sp += x;
             }
-            if (turned.biased)
-              x = make_float2(fmaf(-slope, fabsf(here - (float)(q * 32 + e)), x.x),
-                              fmaf(-slope, fabsf(here - (float)(q * 32 + e + 1)), x.y));
-            p[q][e] = __float_as_uint(ex2_approx(x.x));
-            p[q][e + 1] = __float_as_uint(ex2_approx(x.y));
+        red[half * 128 + row] = sd;
+        red[256 + half * 128 + row] = sp;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::SUM_READY));
+        if (!warp_attn_wait(bar(C::SUM_READY), 0, ctl)) return false;
+        sp = red[256 + row] + red[384 + row];
+        delta = sp > 0.0f ? (red[row] + red[128 + row]) / sp : 0.0f;
+        nd = -delta * amp;
+        if (half == 0 && live) args.delta[(int64_t)h * a.tokens_q + token] = delta;
+        return true;
+      };
+      auto take_dp = [&]() -> bool {
+        if (!warp_attn_wait(bar(C::DP_FULL + half), u, ctl)) return false;
+        tc_fence_after_sync();
+        tmem_ld_32x32b_x32(dp_col, d[0]);
+        tmem_ld_32x32b_x32(dp_col + 32, d[1]);
+        tmem_wait_ld_x32(d[0]);
+        tmem_wait_ld_x32(d[1]);
+        return true;
+      };
+      if constexpr (SCORES) {
+        if constexpr (CAPPED) {   // r, from which P and the cap's derivative come
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 x =
+                  turned.rest<1>(make_float2(__uint_as_float(p[q][e]), __uint_as_float(p[q][e + 1])));
+              p[q][e] = __float_as_uint(x.x);
+              p[q][e + 1] = __float_as_uint(x.y);
+            }
+        }
+        if (few) {
+          ok = take_dp() && sum_delta();
+          if (!ok) break;
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float2 far = make_float2(here - (float)(q * 32), here - (float)(q * 32 + 1));
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 r = make_float2(__uint_as_float(p[q][e]), __uint_as_float(p[q][e + 1]));
+            float2 x = probability(r, far);
+            far = add2(far, make_float2(-2.0f, -2.0f));
+            if constexpr (CAPPED) x = ScoreTurn::times_slope(x, r);
+            p[q][e] = __float_as_uint(x.x);
+            p[q][e + 1] = __float_as_uint(x.y);
           }
+        }
+        if (!few) {
+          ok = take_dp();
+          if (!ok) break;
+        }
       } else {
 #pragma unroll
         for (int q = 0; q < 2; ++q)
@@ -495,39 +554,10 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             p[q][e + 1] = __float_as_uint(ex2_approx(x.y));
           }
       }
-      ok = warp_attn_wait(bar(C::DP_FULL + half), u, ctl);
-      if (!ok) break;
-      tc_fence_after_sync();
-      tmem_ld_32x32b_x32(dp_col, d[0]);
-      tmem_ld_32x32b_x32(dp_col + 32, d[1]);
-      tmem_wait_ld_x32(d[0]);
-      tmem_wait_ld_x32(d[1]);
-      if (few) {
-        // All of the row's keys are in the streams' first tiles, so delta is
-        // at hand as the sum of P dP itself. It replaces the sum of dO O, whose O has been
-        // rounded to 16 bits: with few keys that rounding is no longer small
-        // against dP - delta (at one key the difference is zero).
-        float sd = 0.0f, sp = 0.0f;
-        const int lim_h = lim - (SCORES ? j0 + half : half) * kTurn;
-        const int low_h = SCORES ? low - (j0 + half) * kTurn : 0;
-#pragma unroll
-        for (int q = 0; q < 2; ++q)
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (q * 32 + e <= lim_h && (!SCORES || q * 32 + e >= low_h)) {
-              sd = fmaf(__uint_as_float(p[q][e]), __uint_as_float(d[q][e]), sd);
-              sp += __uint_as_float(p[q][e]);
-            }
-        red[half * 128 + row] = sd;
-        red[256 + half * 128 + row] = sp;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::SUM_READY));
-        ok = warp_attn_wait(bar(C::SUM_READY), 0, ctl);
+      if constexpr (!SCORES) {
+        ok = take_dp();
+        if (ok && few) ok = sum_delta();
         if (!ok) break;
-        sp = red[256 + row] + red[384 + row];
-        delta = sp > 0.0f ? (red[row] + red[128 + row]) / sp : 0.0f;
-        nd = -delta * amp;
-        if (half == 0 && live) args.delta[(int64_t)h * a.tokens_q + token] = delta;
       }
       const float2 aa = make_float2(amp, amp), dd = make_float2(nd, nd);
 #pragma unroll
@@ -540,15 +570,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
           d[q][e + 1] = __float_as_uint(y.y);
         }
       if constexpr (SCORES) {
-        if (turned.capped) {
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float2 f = __half22float2(chain[e]);
-            uint32_t* x = &d[e >> 4][(2 * e) & 31];
-            x[0] = __float_as_uint(__uint_as_float(x[0]) * f.x);
-            x[1] = __float_as_uint(__uint_as_float(x[1]) * f.y);
-          }
-        }
         const int low_j = low - (j0 + j) * kTurn;
         if (__any_sync(0xffffffffu, low_j > 0)) {
 #pragma unroll
@@ -609,10 +630,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 
 // ---------------------------------------------------------------- dK, dV
 
-template <int DP, bool BF16, bool SCORES>
+template <int DP, bool BF16, int FORM>
 __global__ void __launch_bounds__(kDkvThreads, 1)
     lin_attn_dkv_kernel(const __grid_constant__ AttnBwdMaps maps,
                         const __grid_constant__ AttnBwdArgs args) {
+  constexpr bool SCORES = FORM != kNoForm;
+  constexpr bool CAPPED = SCORES && (FORM & kCap), BIASED = SCORES && (FORM & kBias);
   using C = DkvCfg<DP, SCORES>;
   extern __shared__ uint8_t smem_raw[];
   const AttnArgs& a = args.s;
@@ -778,7 +801,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     float lse[N], delta[N];
     float place[N], slope[N];   // (a form of the scores)
     KeyRange keys[N];
-    const ScoreTurn turned(args.scores, SCORES, a.scale);
+    const ScoreTurn turned(args.scores, a.scale);
     auto load = [&]() {
 #pragma unroll
       for (int e = 0; e < N; ++e) {
@@ -790,7 +813,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         delta[e] = in ? args.delta[at] : 0.0f;
         if constexpr (SCORES) {
           place[e] = (float)(i + off);
-          slope[e] = in && turned.biased ? args.scores.slopes[hr] * kLog2E : 0.0f;
+          slope[e] = in && BIASED ? args.scores.slopes[hr] * kLog2E : 0.0f;
           // (rows behind the end and rows without a key have P = 0 already)
           keys[e] = in ? key_range(args.scores, a.causal, sq, sk, i) : KeyRange{0, 0};
         }
@@ -807,8 +830,10 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       for (int e = 0; e < N; ++e) {
         nl[e] = lse[e] == -INFINITY ? -INFINITY : fmaf(-lse[e], kLog2E, kPShift);
         nd[e] = delta[e] * -damp;
-        // (whatever dO held there)
-        if (SCORES && lse[e] == -INFINITY) nd[e] = 0.0f;
+        if constexpr (SCORES) {
+          if (CAPPED) nl[e] += turned.top;   // (what P's exponent adds to the line in r)
+          if (lse[e] == -INFINITY) nd[e] = 0.0f;    // (whatever dO held there)
+        }
       }
       float at_place[N], at_slope[N];
       KeyRange at_keys[N];
@@ -981,7 +1006,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     }
     const int ne = scale_exponent();
     const float damp = ds_scale(ne);
-    const ScoreTurn turned(args.scores, SCORES, a.scale);
+    const ScoreTurn turned(args.scores, a.scale);
     const float my_key = (float)key;
     constexpr int NQ = kTurn / 32;   // groups of 32 columns of a thread
     bool ok = true;
@@ -1009,7 +1034,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       for (int q = 0; q < NQ; ++q) tmem_ld_32x32b_x32(s_col + q * 32, p[q]);
 #pragma unroll
       for (int q = 0; q < NQ; ++q) tmem_wait_ld_x32(p[q]);
-      const float2 cc = make_float2(c, c), pp = make_float2(damp, damp);
+      const float f = CAPPED ? -turned.twice : c;
+      const float2 cc = make_float2(f, f), pp = make_float2(damp, damp);
       bool cut;
       int first = 0;
       if constexpr (SCORES) {
@@ -1019,51 +1045,49 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         const float4* slope = reinterpret_cast<const float4*>(slope_rows(at_stage));
         const int4* lo = reinterpret_cast<const int4*>(first_rows(at_stage));
         const int4* hi = reinterpret_cast<const int4*>(end_rows(at_stage));
+        auto probabilities = [&](auto masked) {
 #pragma unroll
-        for (int q = 0; q < NQ; ++q)
+          for (int q = 0; q < NQ; ++q)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 r = nl[q * 8 + e];
-            uint32_t* x = &p[q][e * 4];
-            float2 u = make_float2(__uint_as_float(x[0]), __uint_as_float(x[1]));
-            float2 v = make_float2(__uint_as_float(x[2]), __uint_as_float(x[3]));
-            float2 du = make_float2(1.0f, 1.0f), dv = du;   // the cap's derivative
-            if (turned.capped) {
-              u = turned.rest(u);
-              v = turned.rest(v);
-              du = ScoreTurn::slope(u);
-              dv = ScoreTurn::slope(v);
-              u = add2(turned.value(u), make_float2(r.x, r.y));
-              v = add2(turned.value(v), make_float2(r.z, r.w));
-            } else {
-              u = fma2(u, cc, make_float2(r.x, r.y));
-              v = fma2(v, cc, make_float2(r.z, r.w));
+            for (int e = 0; e < 8; ++e) {
+              const float4 l = nl[q * 8 + e];
+              uint32_t* x = &p[q][e * 4];
+              float2 ru = make_float2(__uint_as_float(x[0]), __uint_as_float(x[1]));
+              float2 rv = make_float2(__uint_as_float(x[2]), __uint_as_float(x[3]));
+              if constexpr (CAPPED) {
+                ru = turned.rest<1>(ru);
+                rv = turned.rest<1>(rv);
+              }
+              float2 u = fma2(ru, cc, make_float2(l.x, l.y));
+              float2 v = fma2(rv, cc, make_float2(l.z, l.w));
+              if constexpr (BIASED) {
+                const float4 at = place[q * 8 + e], sl = slope[q * 8 + e];
+                u = make_float2(fmaf(-sl.x, fabsf(at.x - my_key), u.x), fmaf(-sl.y, fabsf(at.y - my_key), u.y));
+                v = make_float2(fmaf(-sl.z, fabsf(at.z - my_key), v.x), fmaf(-sl.w, fabsf(at.w - my_key), v.y));
+              }
+              u = make_float2(ex2_approx(u.x), ex2_approx(u.y));
+              v = make_float2(ex2_approx(v.x), ex2_approx(v.y));
+              if constexpr (decltype(masked)::value) {
+                const int4 first = lo[q * 8 + e], end = hi[q * 8 + e];
+                if (key < first.x || key >= end.x) u.x = 0.0f;
+                if (key < first.y || key >= end.y) u.y = 0.0f;
+                if (key < first.z || key >= end.z) v.x = 0.0f;
+                if (key < first.w || key >= end.w) v.y = 0.0f;
+              }
+              w[q * 16 + e * 2] = pack16<BF16>(u.x, u.y);
+              w[q * 16 + e * 2 + 1] = pack16<BF16>(v.x, v.y);
+              if constexpr (CAPPED) {   // (P itself is not wanted any more)
+                u = ScoreTurn::times_slope(u, ru);
+                v = ScoreTurn::times_slope(v, rv);
+              }
+              x[0] = __float_as_uint(u.x);
+              x[1] = __float_as_uint(u.y);
+              x[2] = __float_as_uint(v.x);
+              x[3] = __float_as_uint(v.y);
             }
-            if (turned.biased) {
-              const float4 at = place[q * 8 + e], sl = slope[q * 8 + e];
-              u = make_float2(fmaf(-sl.x, fabsf(at.x - my_key), u.x), fmaf(-sl.y, fabsf(at.y - my_key), u.y));
-              v = make_float2(fmaf(-sl.z, fabsf(at.z - my_key), v.x), fmaf(-sl.w, fabsf(at.w - my_key), v.y));
-            }
-            u = make_float2(ex2_approx(u.x), ex2_approx(u.y));
-            v = make_float2(ex2_approx(v.x), ex2_approx(v.y));
-            if (cut) {
-              const int4 f = lo[q * 8 + e], l = hi[q * 8 + e];
-              if (key < f.x || key >= l.x) u.x = 0.0f;
-              if (key < f.y || key >= l.y) u.y = 0.0f;
-              if (key < f.z || key >= l.z) v.x = 0.0f;
-              if (key < f.w || key >= l.w) v.y = 0.0f;
-            }
-            w[q * 16 + e * 2] = pack16<BF16>(u.x, u.y);
-            w[q * 16 + e * 2 + 1] = pack16<BF16>(v.x, v.y);
-            if (turned.capped) {   // (P itself is not wanted any more)
-              u = mul2(u, du);
-              v = mul2(v, dv);
-            }
-            x[0] = __float_as_uint(u.x);
-            x[1] = __float_as_uint(u.y);
-            x[2] = __float_as_uint(v.x);
-            x[3] = __float_as_uint(v.y);
-          }
+        };
+        if (cut) probabilities(std::true_type{});
+        else probabilities(std::false_type{});
       } else {
 #pragma unroll
         for (int q = 0; q < NQ; ++q)
@@ -1179,9 +1203,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
 }
 
 // The two kernels of the arguments' head size and type.
-template <bool SCORES>
-cudaError_t launch_attn_bwd_kernels(bool bf16, const AttnBwdMaps& maps, const AttnBwdArgs& args,
-                                    int heads_kv, int sequences, int* kernels, cudaStream_t stream) {
+template <int FORM>
+cudaError_t launch_attn_bwd(bool bf16, const AttnBwdMaps& maps, const AttnBwdArgs& args,
+                            int heads_kv, int sequences, int* kernels, cudaStream_t stream) {
   const unsigned tq = (unsigned)(((args.s.max_q << args.shift) + 127) / 128);
   const unsigned tk = (unsigned)((args.s.max_k + 127) / 128);
   const unsigned hq = (unsigned)(heads_kv * args.s.group), hk = (unsigned)heads_kv;
@@ -1215,8 +1239,8 @@ cudaError_t launch_attn_bwd_kernels(bool bf16, const AttnBwdMaps& maps, const At
     constexpr bool B = decltype(type)::value;
     auto size = [&](auto entries) {
       constexpr int DP = decltype(entries)::value;
-      return both(lin_attn_dq_kernel<DP, B, SCORES>, DqCfg<DP>::SMEM,
-                  lin_attn_dkv_kernel<DP, B, SCORES>, DkvCfg<DP, SCORES>::SMEM);
+      return both(lin_attn_dq_kernel<DP, B, FORM>, DqCfg<DP>::SMEM,
+                  lin_attn_dkv_kernel<DP, B, FORM>, DkvCfg<DP, FORM != kNoForm>::SMEM);
     };
     return args.s.dim <= 64   ? size(std::integral_constant<int, 64>{})
            : args.s.dim <= 96 ? size(std::integral_constant<int, 96>{})

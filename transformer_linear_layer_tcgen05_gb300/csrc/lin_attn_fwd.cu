@@ -61,9 +61,7 @@ cudaError_t launch_attn_join_parts(bool bf16, const AttnFwdArgs& args, int heads
               : cudaLaunchKernelEx(&cfg, lin_attn_join_parts_kernel<false>, args);
 }
 
-cudaError_t launch_attn_fwd(bool bf16, const AttnFwdMaps& maps, const AttnFwdArgs& args,
-                            int heads_kv, int sequences, cudaStream_t stream) {
-  return launch_attn_fwd_kernel<false>(bf16, maps, args, heads_kv, sequences, stream);
-}
+template cudaError_t launch_attn_fwd<kNoForm>(bool, const AttnFwdMaps&, const AttnFwdArgs&, int, int,
+                                              cudaStream_t);
 
 }  // namespace lin

@@ -105,11 +105,13 @@ __device__ __forceinline__ int fwd_key_tiles(int i0, int n, int lq, int lk, int 
 // query heads that share a key head, tile_q queries of them all to a tile.
 // (These are the compiler's parameters: read from the arguments, the rows of
 // a CTA cost the longest problems 2 %, 347 -> 353 us.)
-template <int DP, bool BF16, int TILES, bool PACKED, bool SCORES>
+template <int DP, bool BF16, int TILES, bool PACKED, int FORM>
 __global__ void __launch_bounds__(kFwdThreads, 1)
     lin_attn_fwd_kernel(const __grid_constant__ AttnFwdMaps maps,
                         const __grid_constant__ AttnFwdArgs args) {
   using C = FwdCfg<DP>;
+  constexpr bool SCORES = FORM != kNoForm;
+  constexpr bool CAPPED = SCORES && (FORM & kCap), BIASED = SCORES && (FORM & kBias);
   extern __shared__ uint8_t smem_raw[];
   const AttnArgs& a = args.s;
   const int pack = PACKED ? args.pack : 1, tile_q = PACKED ? args.tile_q : 128;
@@ -325,11 +327,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int i = i0 + t * tile_q + turn;   // query of the sequence
     // (packed: the last rows of a tile may be nobody's)
     const bool live = i < sq.len && t < TILES && (!PACKED || turn < tile_q);
-    // (turned scores are in base-2 units already)
-    const ScoreTurn turned(args.scores, SCORES, a.scale);
-    const float slope = turned.biased ? args.scores.slopes[h] * kLog2E : 0.0f;
-    const float c_plain = a.scale * kLog2E;
-    const float c = SCORES && turned.any ? 1.0f : c_plain;
+    // the factor to base-2 units (biased scores are in them already)
+    const ScoreTurn turned(args.scores, a.scale);
+    const float slope = BIASED && live ? args.scores.slopes[h] * kLog2E : 0.0f;
+    const float c_turned = CAPPED ? turned.twice : a.scale * kLog2E;
+    const float c = BIASED ? 1.0f : c_turned;
     // the last key that this row may see, and the first
     const int lim = SCORES ? mine.hi - 1
                     : live ? (a.causal ? min(sk.len - 1, i + sk.len - sq.len) : sk.len - 1)
@@ -357,26 +359,31 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
       const int lim_j = lim - (j0 + j) * 128;
       if constexpr (SCORES) {
-        if (turned.capped) {
+        if constexpr (CAPPED) {   // -r
 #pragma unroll
           for (int q = 0; q < 4; ++q)
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float2 x = turned.value(
-                  turned.rest(make_float2(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]))));
+              const float2 x = turned.rest<-1>(
+                  make_float2(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])));
               s[q][e] = __float_as_uint(x.x);
               s[q][e + 1] = __float_as_uint(x.y);
             }
         }
-        if (turned.biased) {
+        if constexpr (BIASED) {
           const float here = (float)(i + sk.len - sq.len - (j0 + j) * 128);
-          const float f = turned.capped ? 1.0f : c_plain;
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+          for (int q = 0; q < 4; ++q) {
+            float2 far = make_float2(here - (float)(q * 32), here - (float)(q * 32 + 1));
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              s[q][e] = __float_as_uint(fmaf(-slope, fabsf(here - (float)(q * 32 + e)),
-                                             __uint_as_float(s[q][e]) * f));
+            for (int e = 0; e < 32; e += 2) {
+              const float2 x = mul2(make_float2(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])),
+                                    make_float2(c_turned, c_turned));
+              s[q][e] = __float_as_uint(fmaf(-slope, fabsf(far.x), x.x));
+              s[q][e + 1] = __float_as_uint(fmaf(-slope, fabsf(far.y), x.y));
+              far = add2(far, make_float2(-2.0f, -2.0f));
+            }
+          }
         }
         const int low_j = low - (j0 + j) * 128;
         if (__any_sync(0xffffffffu, lim_j < 127 || low_j > 0)) {
@@ -505,7 +512,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         }
       }
       if (live && q_row_ok(a, token, h)) 
-        *lse = l == 0.0f ? -INFINITY : m * (SCORES && turned.any ? kLn2 : a.scale) + logf(l);
+        *lse = l == 0.0f ? -INFINITY
+               : CAPPED || BIASED ? fmaf(m, c, CAPPED ? turned.top : 0.0f) * kLn2 + logf(l)
+                                      : m * a.scale + logf(l);
     }
   }
   __syncwarp();
@@ -518,9 +527,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 }
 
 // The kernel of the arguments' head size, tiles and type.
-template <bool SCORES>
-cudaError_t launch_attn_fwd_kernel(bool bf16, const AttnFwdMaps& maps, const AttnFwdArgs& args,
-                                   int heads_kv, int sequences, cudaStream_t stream) {
+template <int FORM>
+cudaError_t launch_attn_fwd(bool bf16, const AttnFwdMaps& maps, const AttnFwdArgs& args,
+                            int heads_kv, int sequences, cudaStream_t stream) {
   const unsigned heads = (unsigned)(heads_kv * args.s.group);
   const int rows = args.tiles * args.tile_q;
   const dim3 grid(heads / (unsigned)args.pack, (unsigned)((args.s.max_q + rows - 1) / rows),
@@ -536,13 +545,15 @@ cudaError_t launch_attn_fwd_kernel(bool bf16, const AttnFwdMaps& maps, const Att
     constexpr int DP = decltype(size)::value;
     constexpr uint32_t smem = FwdCfg<DP>::SMEM;
     if (args.tiles == 1)
-      return bf16 ? go(lin_attn_fwd_kernel<DP, true, 1, true, SCORES>, smem)
-                  : go(lin_attn_fwd_kernel<DP, false, 1, true, SCORES>, smem);
-    if (args.pack > 1)
-      return bf16 ? go(lin_attn_fwd_kernel<DP, true, 2, true, SCORES>, smem)
-                  : go(lin_attn_fwd_kernel<DP, false, 2, true, SCORES>, smem);
-    return bf16 ? go(lin_attn_fwd_kernel<DP, true, 2, false, SCORES>, smem)
-                : go(lin_attn_fwd_kernel<DP, false, 2, false, SCORES>, smem);
+      return bf16 ? go(lin_attn_fwd_kernel<DP, true, 1, true, FORM>, smem)
+                  : go(lin_attn_fwd_kernel<DP, false, 1, true, FORM>, smem);
+    if (args.pack > 1 || FORM != kNoForm)
+      return bf16 ? go(lin_attn_fwd_kernel<DP, true, 2, true, FORM>, smem)
+                  : go(lin_attn_fwd_kernel<DP, false, 2, true, FORM>, smem);
+    if constexpr (FORM == kNoForm)   // (a form's rows are dealt out at run time)
+      return bf16 ? go(lin_attn_fwd_kernel<DP, true, 2, false, FORM>, smem)
+                  : go(lin_attn_fwd_kernel<DP, false, 2, false, FORM>, smem);
+    return cudaErrorInvalidValue;
   };
   // (heads of 65 to 96 entries: a quarter less of both products than 128; 4096
   // causal tokens, 16 heads of 96: 52.2 -> 49.1 us)
