@@ -248,11 +248,10 @@ __device__ __forceinline__ KeyRange join_extents(const int* e, int n) {
 // The scores' form in base-2 units, two scores at a time. With u = scale s /
 // cap and r = 1 / (1 + e^2u): tanh u = 1 - 2 r, which neither over- nor
 // underflows to anything but its limits, and its derivative is 4 r (1 - r). So
-// a capped score is a line in r, and what follows goes by r: the softmax's
-// factor and shift take in the line's. FORM: kCap, kBias, both or none (ranges
-// of keys alone), the compiler's parameter: asked for in the loops, each part
-// of the form cut them into short pieces (16 heads of 128, 8192 tokens, the
-// gradient 1031 us).
+// a capped score is a line in r, and the gradient goes by r. FORM: kCap, kBias,
+// both or none (ranges of keys alone), the compiler's parameter: asked for in
+// the loops, each part of the form cut them into short pieces (16 heads of 128,
+// 8192 tokens, the gradient 1031 -> 912 us).
 struct ScoreTurn {
   float2 arg;         // 2 log2 e scale / cap
   float top, twice;   // cap log2 e, and twice that
@@ -261,14 +260,25 @@ struct ScoreTurn {
     const float a = 2.0f * kLog2E * scale / f.cap;
     arg = make_float2(a, a);
   }
-  // r of two scores (SIGN -1: -r); twice * -r + top is the capped score
-  template <int SIGN>
+  // r of two scores
   __device__ __forceinline__ float2 rest(float2 s) const {
-    constexpr float one = (float)SIGN;
     const float2 x = mul2(s, arg);
-    float2 e = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-    e = SIGN > 0 ? add2(e, make_float2(one, one)) : fma2(e, make_float2(one, one), make_float2(one, one));
+    const float2 e = add2(make_float2(ex2_approx(x.x), ex2_approx(x.y)), make_float2(1.0f, 1.0f));
     return make_float2(rcp_approx(e.x), rcp_approx(e.y));
+  }
+  // The capped scores themselves: by r, or, where |u| <= 3/4, as u times a
+  // polynomial of u^2, which spares two of the three turns of the
+  // special-function unit that a score takes (the unit's reciprocals take twice
+  // its exponentials' time).
+  __device__ __forceinline__ float2 by_rest(float2 s) const {
+    return fma2(rest(s), make_float2(-twice, -twice), make_float2(top, top));
+  }
+  static __device__ __forceinline__ float2 by_terms(const ScoreForm& f, float2 s) {
+    const float2 u = mul2(s, f.unit), w = mul2(u, u);
+    float2 p = f.terms[kTanhTerms - 1];
+#pragma unroll
+    for (int k = kTanhTerms - 2; k >= 0; --k) p = fma2(p, w, f.terms[k]);
+    return mul2(u, p);
   }
   // p times the cap's derivative, from r
   static __device__ __forceinline__ float2 times_slope(float2 p, float2 r) {

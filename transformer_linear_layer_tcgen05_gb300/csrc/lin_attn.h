@@ -27,11 +27,15 @@ struct AttnArgs {
 // A form of the scores: z = cap tanh(scale s / cap) - slope |distance| (cap 0:
 // scale s; slopes null: no bias), and the keys first .. end - 1 of a query,
 // counted in its sequence (null: from the first, to the last).
+constexpr int kTanhTerms = 5;
 constexpr int kNoForm = -1, kCap = 1, kBias = 2;   // (forms of ranges alone: 0)
 struct ScoreForm {
   float cap;
   const float* slopes;             // [heads_q]
   const int32_t *first, *end;      // [tokens_q]
+  // (a cap, forward) scale / cap, and cap log2 e times the terms of tanh's
+  // polynomial, twice each, for two scores at a time
+  float2 unit, terms[kTanhTerms];
 };
 
 struct AttnFwdArgs {

@@ -142,8 +142,25 @@ cudaError_t with_form(const lin_score_form* f, F&& go) {
   return f->slopes ? go(std::integral_constant<int, lin::kBias>{}) : go(std::integral_constant<int, 0>{});
 }
 // The kernels' view of it.
-lin::ScoreForm score_form(const lin_score_form* f) {
-  return f ? lin::ScoreForm{f->cap, f->slopes, f->first_key, f->end_key} : lin::ScoreForm{};
+lin::ScoreForm score_form(const lin_score_form* f, float scale) {
+  lin::ScoreForm s{};
+  if (!f) return s;
+  s.cap = f->cap;
+  s.slopes = f->slopes;
+  s.first = f->first_key;
+  s.end = f->end_key;
+  if (!(f->cap > 0.0f)) return s;
+  // tanh(u) / u by u^2 in [0, 9/16]: the polynomial of degree four whose largest
+  // relative error is least (5.7e-7; fitted by reweighted least squares)
+  const double t[lin::kTanhTerms] = {0.999999435, -0.333282516, 0.132589833, -0.0500563041,
+                                     0.0129296326};
+  const float unit = (float)((double)scale / f->cap);
+  s.unit = make_float2(unit, unit);
+  for (int i = 0; i < lin::kTanhTerms; ++i) {
+    const float c = (float)(t[i] * f->cap * 1.4426950408889634);
+    s.terms[i] = make_float2(c, c);
+  }
+  return s;
 }
 
 lin_status attention(const lin_attention_shape* s, const lin_score_form* form, const lin_heads* Q,
@@ -159,7 +176,7 @@ lin_status attention(const lin_attention_shape* s, const lin_score_form* form, c
   if (st != LIN_SUCCESS) return st;
   if (c.nothing || c.max_q == 0) return LIN_SUCCESS;
   lin::AttnFwdArgs a{attn_args(s, c), heads_ptr(v[3]), LSE, 1, 0, nullptr,
-                     nullptr, 2, 1, 128, score_form(form)};
+                     nullptr, 2, 1, 128, score_form(form, s->scale)};
   const int sms = sm_count(c.dev);
   auto tiles = [&] {
     return (c.max_q + a.tile_q - 1) / a.tile_q * (s->heads_q / a.pack) * s->sequences;
@@ -285,7 +302,7 @@ lin_status attention_backward(const lin_attention_shape* s, const lin_score_form
   a.delta = a.dv_part + dk;
   a.norm = a.delta + delta;
   a.norms = (int64_t)norms;
-  a.scores = score_form(form);
+  a.scores = score_form(form, s->scale);
   if (ranged) a.extents = reinterpret_cast<int2*>(ws + before);
   int kernels = 0;
   const bool bf16 = s->dtype == LIN_BFLOAT16;

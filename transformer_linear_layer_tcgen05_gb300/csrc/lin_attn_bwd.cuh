@@ -518,7 +518,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
               const float2 x =
-                  turned.rest<1>(make_float2(__uint_as_float(p[q][e]), __uint_as_float(p[q][e + 1])));
+                  turned.rest(make_float2(__uint_as_float(p[q][e]), __uint_as_float(p[q][e + 1])));
               p[q][e] = __float_as_uint(x.x);
               p[q][e + 1] = __float_as_uint(x.y);
             }
@@ -1055,8 +1055,8 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
               float2 ru = make_float2(__uint_as_float(x[0]), __uint_as_float(x[1]));
               float2 rv = make_float2(__uint_as_float(x[2]), __uint_as_float(x[3]));
               if constexpr (CAPPED) {
-                ru = turned.rest<1>(ru);
-                rv = turned.rest<1>(rv);
+                ru = turned.rest(ru);
+                rv = turned.rest(rv);
               }
               float2 u = fma2(ru, cc, make_float2(l.x, l.y));
               float2 v = fma2(rv, cc, make_float2(l.z, l.w));

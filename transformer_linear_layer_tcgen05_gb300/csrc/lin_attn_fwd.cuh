@@ -128,7 +128,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   if (i0 >= sq.len) return;   // (the whole CTA)
   const SeqRange sk = seq_range(a.cu_k, b, a.tokens_k, a.max_k);
   // key tiles of the two query tiles, and of them those of this part, from j0 on
-  int all0 = 0, all1 = 0, from = 0, j0, n0, n1, n;
+  // (b0, b1: those of them before a tile's own first, a form's ranges)
+  int all0 = 0, all1 = 0, from = 0, j0, n0, n1, n, b0 = 0, b1 = 0;
   auto share = [&] {
     const int all = max(max(all0, all1) - from, 0);
     j0 = from + at.begin(all);
@@ -187,6 +188,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     all0 = (t0.hi + 127) / 128;
     all1 = (t1.hi + 127) / 128;
     share();
+    b0 = max(t0.lo / 128 - j0, 0);
+    b1 = max(t1.lo / 128 - j0, 0);
+    if (b0 >= n0) n0 = b0 = 0;   // (none in this part)
+    if (b1 >= n1) n1 = b1 = 0;
   }
   // (an allocation of all 512 columns begins at column 0)
   constexpr uint32_t tmem = 0;
@@ -261,7 +266,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         };
         bool ok = attn_wait(bar(C::K_FULL), 0, ctl);
         for (int t = 0; t < 2 && ok; ++t) {
-          if ((t ? n1 : n0) == 0) continue;
+          if ((t ? n1 : n0) == 0 || (t ? b1 : b0) > 0) continue;
           ok = attn_wait(bar(C::Q_FULL + t), 0, ctl);
           if (ok) scores(t, 0);
         }
@@ -270,8 +275,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         uint32_t round = 0, round1 = C::NKV == 1;
         for (int j = 0; j < n && ok; ++j) {
           if (j + 1 < n) ok = attn_wait(bar(C::K_FULL + s1), round1 & 1, ctl);
-          if (C::AHEAD && ok && j + 1 < n0) {
-            ok = attn_wait(bar(C::S_TAKEN), j & 1, ctl);
+          if (C::AHEAD && ok && j + 1 < n0 && j + 1 >= b0) {
+            if (j >= b0) ok = attn_wait(bar(C::S_TAKEN), (j - b0) & 1, ctl);
             tc_fence_after_sync();
             if (ok) scores(0, s1);
           }
@@ -279,22 +284,26 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           if (ok && j + 1 == n && v_left < 128) ok = attn_wait(bar(C::TAIL), 0, ctl);
 #pragma unroll 1
           for (int t = 0; t < 2; ++t) {
-            const int nt = t ? n1 : n0;
+            const int nt = t ? n1 : n0, bt = t ? b1 : b0;
             if (j >= nt || !ok) continue;
+            if (j < bt) {   // (its first scores; ahead, the first tile's are out already)
+              if (j + 1 == bt && (!C::AHEAD || t == 1)) scores(t, s1);
+              continue;
+            }
             if (C::AHEAD && t == 1 && j + 1 < nt) {
-              ok = attn_wait(bar(C::S_TAKEN + 1), j & 1, ctl);
+              ok = attn_wait(bar(C::S_TAKEN + 1), (j - bt) & 1, ctl);
               tc_fence_after_sync();
               if (!ok) break;
               scores(1, s1);
             }
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
-              ok = ok && attn_wait(bar(C::P_READY + 2 * t + half), j & 1, ctl);
+              ok = ok && attn_wait(bar(C::P_READY + 2 * t + half), (j - bt) & 1, ctl);
               if (!ok || !stage_ok(a, s, C::NKV)) break;
               tc_fence_after_sync();
               umma_tokens<DP, BF16, 4>(C::O_COL + t * DP, C::p_col(t) + half * 32,
                                        v_desc + s * AttnTile<DP>::UNITS, half * 4,
-                                       j == 0 && half == 0);
+                                       j == bt && half == 0);
             }
             if (!ok) break;
             if (!C::AHEAD && j + 1 < nt)
@@ -321,16 +330,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   } else {
     setmaxnreg_inc<kFwdRegsRow>();
     const int t = warp >> 2, row = tid & 127;
-    const int nk = t ? n1 : n0;
+    const int nk = t ? n1 : n0, bt = t ? b1 : b0;
     const int turn = PACKED ? row / pack : row;
     const int h = PACKED ? h0 + row - turn * pack : h0;
     const int i = i0 + t * tile_q + turn;   // query of the sequence
     // (packed: the last rows of a tile may be nobody's)
     const bool live = i < sq.len && t < TILES && (!PACKED || turn < tile_q);
-    // the factor to base-2 units (biased scores are in them already)
+    // the factor to base-2 units (a form's scores are in them already)
     const ScoreTurn turned(args.scores, a.scale);
     const float slope = BIASED && live ? args.scores.slopes[h] * kLog2E : 0.0f;
-    const float c_turned = CAPPED ? turned.twice : a.scale * kLog2E;
+    const float c_turned = CAPPED ? 1.0f : a.scale * kLog2E;
     const float c = BIASED ? 1.0f : c_turned;
     // the last key that this row may see, and the first
     const int lim = SCORES ? mine.hi - 1
@@ -343,8 +352,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t o_col = tmem + lanes + C::O_COL + t * DP;
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
-    for (int j = 0; j < nk; ++j) {
-      ok = warp_wait_phase<kAttnNapNs>(bar(C::S_FULL + t), j & 1, ctl);
+    for (int j = bt; j < nk; ++j) {
+      ok = warp_wait_phase<kAttnNapNs>(bar(C::S_FULL + t), (j - bt) & 1, ctl);
       if (!ok) break;
       tc_fence_after_sync();
       uint32_t s[4][32];
@@ -359,16 +368,27 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
       const int lim_j = lim - (j0 + j) * 128;
       if constexpr (SCORES) {
-        if constexpr (CAPPED) {   // -r
+        if constexpr (CAPPED) {
+          auto cap = [&](auto small) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const float2 x = make_float2(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
+                const float2 y = decltype(small)::value ? ScoreTurn::by_terms(args.scores, x) : turned.by_rest(x);
+                s[q][e] = __float_as_uint(y.x);
+                s[q][e + 1] = __float_as_uint(y.y);
+              }
+          };
+          float big = 0.0f;
 #pragma unroll
           for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 x = turned.rest<-1>(
-                  make_float2(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])));
-              s[q][e] = __float_as_uint(x.x);
-              s[q][e + 1] = __float_as_uint(x.y);
-            }
+            for (int e = 0; e < 32; e += 2)
+              big = max3(big, fabsf(__uint_as_float(s[q][e])), fabsf(__uint_as_float(s[q][e + 1])));
+          // (NaN is passed over: either way gives NaN)
+          if (__all_sync(0xffffffffu, big * args.scores.unit.x <= 0.75f)) cap(std::true_type{});
+          else cap(std::false_type{});
         }
         if constexpr (BIASED) {
           const float here = (float)(i + sk.len - sq.len - (j0 + j) * 128);
@@ -412,8 +432,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
       // (a row without a key so far has m = -inf: the difference is inf)
       const bool grow = top > m && !((top - m) * c <= 8.0f);
-      if (C::AHEAD && j > 0) {   // P V of the tiles so far: O may change, and P
-        ok = warp_wait_phase<kAttnNapNs>(bar(C::O_FULL + t), (j - 1) & 1, ctl);
+      if (C::AHEAD && j > bt) {   // P V of the tiles so far: O may change, and P
+        ok = warp_wait_phase<kAttnNapNs>(bar(C::O_FULL + t), (j - bt - 1) & 1, ctl);
         if (!ok) break;
         tc_fence_after_sync();
       }
@@ -421,7 +441,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         const float to = fmaxf(m, top);
         const float alpha = to > m ? ex2_approx((m - to) * c) : 1.0f;
         m = to;
-        if (j > 0) {   // P V of the tiles so far is complete (not ahead: S came behind it)
+        if (j > bt) {   // P V of the tiles so far is complete (not ahead: S came behind it)
           l *= alpha;
 #pragma unroll
           for (int q = 0; q < DP / 32; ++q) {
@@ -460,7 +480,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       l += sum[0].x + sum[0].y;
     }
     if (ok && nk > 0) {
-      ok = warp_wait_phase<kAttnNapNs>(bar(C::O_FULL + t), C::AHEAD ? (nk - 1) & 1 : 0, ctl);
+      ok = warp_wait_phase<kAttnNapNs>(bar(C::O_FULL + t), C::AHEAD ? (nk - bt - 1) & 1 : 0, ctl);
       tc_fence_after_sync();
     }
     if (ok) {
@@ -513,7 +533,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
       if (live && q_row_ok(a, token, h)) 
         *lse = l == 0.0f ? -INFINITY
-               : CAPPED || BIASED ? fmaf(m, c, CAPPED ? turned.top : 0.0f) * kLn2 + logf(l)
+               : CAPPED || BIASED ? m * kLn2 + logf(l)
                                       : m * a.scale + logf(l);
     }
   }
