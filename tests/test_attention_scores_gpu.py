@@ -211,6 +211,12 @@ def test_rows_without_keys_give_nothing_whatever_they_hold(d, heads):
     _run(t, lens, True, 0.1, form)
     for k in want:
         assert torch.equal(t[k], want[k]), k
+    # (one entry of the last head alone)
+    t["q"][rows], t["do"][rows] = 0, 0
+    t["do"][rows[7], -1, d - 1] = nan
+    _run(t, lens, True, 0.1, form)
+    for k in want:
+        assert torch.equal(t[k], want[k]), k
 
 
 def test_no_row_sees_anything():

@@ -227,12 +227,22 @@ __device__ __forceinline__ bool stage_ok(const AttnArgs& a, int s, int stages) {
 struct KeyRange {
   int lo, hi;
 };
-__device__ __forceinline__ KeyRange key_range(const ScoreForm& f, bool causal, const SeqRange& sq,
+// (loaded and worked out apart: a load's value used at once would hold up what
+// comes behind it)
+__device__ __forceinline__ KeyRange load_keys(const ScoreForm& f, const SeqRange& sq, const SeqRange& sk,
+                                              int i) {
+  return KeyRange{f.first ? f.first[sq.start + i] : 0, f.end ? f.end[sq.start + i] : sk.len};
+}
+__device__ __forceinline__ KeyRange held_keys(const KeyRange& r, bool causal, const SeqRange& sq,
                                               const SeqRange& sk, int i) {
-  int lo = f.first ? max(f.first[sq.start + i], 0) : 0;
-  int hi = f.end ? min(f.end[sq.start + i], sk.len) : sk.len;
+  const int lo = max(r.lo, 0);
+  int hi = min(r.hi, sk.len);
   if (causal) hi = min(hi, i + sk.len - sq.len + 1);
   return lo < hi ? KeyRange{lo, hi} : KeyRange{0, 0};
+}
+__device__ __forceinline__ KeyRange key_range(const ScoreForm& f, bool causal, const SeqRange& sq,
+                                              const SeqRange& sk, int i) {
+  return held_keys(load_keys(f, sq, sk, i), causal, sq, sk, i);
 }
 // What the rows of a warp see together (none: INT_MAX, 0), and several warps'.
 __device__ __forceinline__ KeyRange warp_extent(const KeyRange& r) {

@@ -73,7 +73,7 @@ struct AttnBwdArgs {
   int32_t shift;
   float *dq_part, *dk_part, *dv_part;
   ScoreForm scores;
-  int2* extents;          // [sequences][row tiles]: keys that a tile's rows see (ranges of keys)
+  int2* extents;          // as norm: the keys that a tile's rows see (ranges of keys; null: none)
 };
 
 struct AttnFwdMaps {

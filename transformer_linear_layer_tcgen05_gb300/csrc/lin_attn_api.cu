@@ -292,7 +292,7 @@ lin_status attention_backward(const lin_attention_shape* s, const lin_score_form
   const uint64_t norms = (uint64_t)s->sequences * (uint64_t)hq_tiles * (uint64_t)tq;
   const bool ranged = form && (form->first_key || form->end_key);
   const uint64_t before = (dq + 2 * dk + delta + norms + 1) / 2 * 2;   // (8-byte aligned extents)
-  const uint64_t extents = ranged ? 2 * (uint64_t)s->sequences * (uint64_t)tq : 0;
+  const uint64_t extents = ranged ? 2 * norms : 0;
   const size_t bytes = (size_t)std::max<uint64_t>(16, (before + extents) * 4);
   float* ws = static_cast<float*>(take_stream_workspace(c.dev, bytes, stream));
   if (!ws) return LIN_ERROR_CUDA;

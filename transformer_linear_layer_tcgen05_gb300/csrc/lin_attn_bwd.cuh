@@ -70,6 +70,9 @@ constexpr int kDkvThreads = 384;
 constexpr int kTailWarp = 10;       // of the dK, dV kernel: zeroes rows that take no part
 constexpr int kStatsWarp = 11;      // of the dK, dV kernel: rows' statistics
 constexpr int kTurn = 64;           // rows of a streamed tile
+// (of a tile's extent, beside the key behind its last) some row without a key
+// holds what is no finite number
+constexpr int kBadFlag = 1 << 30;
 
 // Shared memory and barriers of both kernels. A stage of the ring holds the
 // streamed pair of tiles: A (K in the dQ kernel, Q in the other) and B (V, dO).
@@ -223,10 +226,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   };
   // the keys that the tile's rows see, for the dK, dV kernel
   auto leave_extent = [&](const KeyRange& r) {
-    const int64_t e = (int64_t)b * gridDim.y + qt;
-    if (SCORES && args.extents && threadIdx.x == 0 && part == 0 && blockIdx.x == 0 &&
-        dcheck(e >= 0 && e < args.norms, a.status, CHK_STATS, e))
-      args.extents[e] = make_int2(r.lo, r.hi);
+    if (SCORES && args.extents && threadIdx.x == 0 && part == 0 && norm_ok())
+      args.extents[norm_at] = make_int2(r.lo, r.hi);
   };
   if (r0 >= rows) {   // (the whole CTA)
     if (threadIdx.x == 0 && part == 0 && norm_ok()) args.norm[norm_at] = 0.0f;
@@ -273,6 +274,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   // the keys of this thread's row (row warps), and of all rows
   KeyRange mine{0, 0};
   int* const extents = reinterpret_cast<int*>(ctl_gen + C::OFF_RED) + 8;
+  bool* const bad_rows = reinterpret_cast<bool*>(ctl_gen + C::OFF_RED + 16);   // 8, of the row warps
   if constexpr (SCORES) {
     if (warp < kRowWarps) {
       const int i = (r0 + (tid & 127)) >> shift;
@@ -290,7 +292,6 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
   pdl_launch_dependents();   // (the dK, dV kernel waits for this grid's end before it reads)
   if constexpr (SCORES) {
     const KeyRange all = join_extents(extents, 4);
-    leave_extent(all);
     share(all.lo, all.hi);   // (no key: nothing, whatever lo is)
   }
   // (an allocation of all 512 columns begins at column 0)
@@ -408,6 +409,22 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         dsum = fmaf(u.x, v.x, fmaf(u.y, v.y, dsum));
         nsum = fmaf(v.x, v.x, fmaf(v.y, v.y, nsum));
       }
+      if constexpr (SCORES) {
+        // A row without a key has P = dS = 0, which the second kernel's products
+        // over the queries multiply with its Q and dO: nothing, unless one of
+        // these is no finite number. Such rows, and only such, are zeroed there
+        // (all rows without keys, by a warp between the copies and the products:
+        // nine sequences of up to 997 with one row in twenty 47 -> 72 us).
+        bool bad = false;
+        if (__any_sync(0xffffffffu, live && mine.hi == 0)) {
+          constexpr uint32_t E = BF16 ? 0x7f80u : 0x7c00u;   // the exponent of NaN and infinity
+#pragma unroll
+          for (int e = 0; e < DP / 4; ++e)
+            bad |= (x[e] & E) == E || ((x[e] >> 16) & E) == E || (y[e] & E) == E || ((y[e] >> 16) & E) == E;
+        }
+        bad = __any_sync(0xffffffffu, bad && live && mine.hi == 0);
+        if (lane == 0) bad_rows[warp] = bad;
+      }
     }
     float* red = reinterpret_cast<float*>(smem_raw + C::OFF_ROWS);   // 4 x 128 floats
     red[half * 128 + row] = dsum;
@@ -428,6 +445,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     named_bar_sync(1, 256);
     if (tid == 0 && part == 0 && norm_ok())
       args.norm[norm_at] = fmaxf(fmaxf(red2[0], red2[1]), fmaxf(red2[2], red2[3]));
+    if (SCORES && tid == 0) {
+      bool bad = false;
+      for (int w = 0; w < kRowWarps; ++w) bad |= bad_rows[w];
+      const KeyRange all = join_extents(extents, 4);
+      leave_extent(KeyRange{all.lo, all.hi | (bad ? kBadFlag : 0)});
+    }
     const int ne = norm_exponent(norm);
     const float amp = pow2i(ne);
     float nd = -delta * amp;
@@ -512,35 +535,41 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         return true;
       };
       if constexpr (SCORES) {
-        if constexpr (CAPPED) {   // r, from which P and the cap's derivative come
+        // P times the cap's derivative, from the scores, or (RESTS) from the r
+        // that delta's sum has left in their place
+        auto probabilities = [&](auto rests) {
 #pragma unroll
-          for (int q = 0; q < 2; ++q)
+          for (int q = 0; q < 2; ++q) {
+            float2 far = make_float2(here - (float)(q * 32), here - (float)(q * 32 + 1));
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              const float2 x =
-                  turned.rest(make_float2(__uint_as_float(p[q][e]), __uint_as_float(p[q][e + 1])));
+              float2 r = make_float2(__uint_as_float(p[q][e]), __uint_as_float(p[q][e + 1]));
+              if (CAPPED && !decltype(rests)::value) r = turned.rest(r);
+              float2 x = probability(r, far);
+              if constexpr (BIASED) far = add2(far, make_float2(-2.0f, -2.0f));
+              if constexpr (CAPPED) x = ScoreTurn::times_slope(x, r);
               p[q][e] = __float_as_uint(x.x);
               p[q][e + 1] = __float_as_uint(x.y);
             }
-        }
+          }
+        };
         if (few) {
+          if constexpr (CAPPED) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                const float2 x =
+                    turned.rest(make_float2(__uint_as_float(p[q][e]), __uint_as_float(p[q][e + 1])));
+                p[q][e] = __float_as_uint(x.x);
+                p[q][e + 1] = __float_as_uint(x.y);
+              }
+          }
           ok = take_dp() && sum_delta();
           if (!ok) break;
-        }
-#pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          float2 far = make_float2(here - (float)(q * 32), here - (float)(q * 32 + 1));
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 r = make_float2(__uint_as_float(p[q][e]), __uint_as_float(p[q][e + 1]));
-            float2 x = probability(r, far);
-            far = add2(far, make_float2(-2.0f, -2.0f));
-            if constexpr (CAPPED) x = ScoreTurn::times_slope(x, r);
-            p[q][e] = __float_as_uint(x.x);
-            p[q][e + 1] = __float_as_uint(x.y);
-          }
-        }
-        if (!few) {
+          probabilities(std::true_type{});
+        } else {
+          probabilities(std::false_type{});
           ok = take_dp();
           if (!ok) break;
         }
@@ -661,20 +690,25 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   int t1 = (rows + kTurn - 1) / kTurn;
   int t0 = a.causal ? min((max(k0 - off, 0) << shift) / kTurn, t1) : 0;
   const bool ranged = SCORES && args.extents != nullptr;
+  bool holes = false;   // (in some tile of the sequence) rows to be zeroed: see kBadFlag
   if (ranged) {
     // the first and the last tile of 128 rows that see one of these keys
     pdl_wait();
     const int tiles = ((a.max_q << shift) + 127) / 128;
-    const int2* ext = args.extents + (int64_t)b * tiles;
-    int lo = INT_MAX, hi = -1;
-    for (int i = threadIdx.x & 31; i < tiles; i += 32) {
-      if (!dcheck(ext + i < args.extents + args.norms, a.status, CHK_STATS, i)) continue;
-      const int2 e = ext[i];
-      if (e.x < k0 + 128 && e.y > k0) {
+    const int heads = a.group >> shift;   // (tiles of them)
+    const int2* ext = args.extents + ((int64_t)b * gridDim.x + hk) * tiles * heads;
+    int lo = INT_MAX, hi = -1, bad = 0;
+    for (int k = threadIdx.x & 31; k < tiles * heads; k += 32) {
+      const int i = k % tiles;
+      if (!dcheck(ext + k < args.extents + args.norms, a.status, CHK_STATS, k)) continue;
+      const int2 e = ext[k];
+      bad |= e.y & kBadFlag;
+      if (e.x < k0 + 128 && (e.y & ~kBadFlag) > k0) {
         lo = min(lo, i);
-        hi = i;
+        hi = max(hi, i);
       }
     }
+    holes = __any_sync(0xffffffffu, bad);
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
     t1 = min(t1, 2 * hi + 2);
@@ -688,7 +722,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   const int q_left = rows - (t1 - 1) * kTurn;            // rows of the last tile
   // rows of the first tile that see no key at all (more queries than keys)
   const int q_none = a.causal ? (max(-off, 0) << shift) - t0 * kTurn : 0;
-  const bool cut_rows = ranged || q_left < kTurn || q_none > 0;
+  const bool cut_rows = holes || q_left < kTurn || q_none > 0;
   const int h0 = hk * a.group;
 
   if (!smem_aligned(smem_raw, a.status)) return;
@@ -787,7 +821,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         }
       }
     }
-  } else if (warp == kStatsWarp) {
+  } else if (!SCORES && warp == kStatsWarp) {
     // The rows' statistics of each turn, in the form that the element-wise
     // warps add: rows behind the sequence's end and rows without a key have
     // P = 0. A warp of its own, which has the next turn's on their way while it
@@ -799,9 +833,6 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
     RingAt<C::N> r;
     int h = n > 0 ? h0 + from / per : 0, tile = tile0;
     float lse[N], delta[N];
-    float place[N], slope[N];   // (a form of the scores)
-    KeyRange keys[N];
-    const ScoreTurn turned(args.scores, a.scale);
     auto load = [&]() {
 #pragma unroll
       for (int e = 0; e < N; ++e) {
@@ -811,12 +842,6 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         const bool in = i < sq.len && q_row_ok(a, sq.start + i, hr);
         lse[e] = in ? args.lse[at] : -INFINITY;
         delta[e] = in ? args.delta[at] : 0.0f;
-        if constexpr (SCORES) {
-          place[e] = (float)(i + off);
-          slope[e] = in && BIASED ? args.scores.slopes[hr] * kLog2E : 0.0f;
-          // (rows behind the end and rows without a key have P = 0 already)
-          keys[e] = in ? key_range(args.scores, a.causal, sq, sk, i) : KeyRange{0, 0};
-        }
       }
       if (++tile == per) {
         tile = 0;
@@ -830,20 +855,6 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       for (int e = 0; e < N; ++e) {
         nl[e] = lse[e] == -INFINITY ? -INFINITY : fmaf(-lse[e], kLog2E, kPShift);
         nd[e] = delta[e] * -damp;
-        if constexpr (SCORES) {
-          if (CAPPED) nl[e] += turned.top;   // (what P's exponent adds to the line in r)
-          if (lse[e] == -INFINITY) nd[e] = 0.0f;    // (whatever dO held there)
-        }
-      }
-      float at_place[N], at_slope[N];
-      KeyRange at_keys[N];
-      if constexpr (SCORES) {
-#pragma unroll
-        for (int e = 0; e < N; ++e) {
-          at_place[e] = place[e];
-          at_slope[e] = slope[e];
-          at_keys[e] = keys[e];
-        }
       }
       if (it + 1 < n) load();
       if (it >= C::N && !warp_attn_wait(bar(C::EMPTY + r.s), r.parity ^ 1, ctl)) break;
@@ -852,29 +863,91 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         lse_rows(r.s)[e * 32 + lane] = nl[e];
         delta_rows(r.s)[e * 32 + lane] = nd[e];
       }
-      if constexpr (SCORES) {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(C::FULL + r.s));
+      r.next();
+    }
+  } else if (SCORES && warp == kStatsWarp) {
+    // The same with a form of the scores: each row's place among the keys and
+    // slope, its range of keys, and what all of a tile's rows see.
+    constexpr int N = kTurn / 32;
+    const float damp = ds_scale(scale_exponent());
+    const ScoreTurn turned(args.scores, a.scale);
+    int h = n > 0 ? h0 + from / per : 0, tile = tile0;   // of the next loads
+    struct Rows {
+      float lse[N], delta[N], slope[N];
+      KeyRange keys[N];
+      int i[N];   // (-1: no row)
+    } ahead[2];
+    auto load = [&](Rows& to) {
+#pragma unroll
+      for (int e = 0; e < N; ++e) {
+        const int row = (t0 + tile) * kTurn + e * 32 + lane, i = row >> shift;
+        const int hr = h + (row & ((1 << shift) - 1));
+        const int64_t at = (int64_t)hr * a.tokens_q + sq.start + i;
+        const bool in = i < sq.len && q_row_ok(a, sq.start + i, hr);
+        to.lse[e] = in ? args.lse[at] : -INFINITY;
+        to.delta[e] = in ? args.delta[at] : 0.0f;
+        to.slope[e] = BIASED && in ? args.scores.slopes[hr] : 0.0f;
+        to.keys[e] = in ? load_keys(args.scores, sq, sk, i) : KeyRange{0, 0};
+        to.i[e] = in ? i : -1;
+      }
+      if (++tile == per) {
+        tile = 0;
+        ++h;
+      }
+    };
+    if (n > 0) load(ahead[0]);
+    if (n > 1) load(ahead[1]);
+    RingAt<C::N> r;
+    bool ok = true;
+    for (int it = 0; it < n && ok; it += 2) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        if (it + k >= n || !ok) break;
+        Rows& rows = ahead[k];
+        float nl[N], nd[N];
+        KeyRange keys[N];
         int first = 0, end = INT_MAX;
 #pragma unroll
         for (int e = 0; e < N; ++e) {
-          place_rows(r.s)[e * 32 + lane] = at_place[e];
-          slope_rows(r.s)[e * 32 + lane] = at_slope[e];
-          first_rows(r.s)[e * 32 + lane] = at_keys[e].lo;
-          end_rows(r.s)[e * 32 + lane] = at_keys[e].hi;
-          if (at_keys[e].hi > 0) {
-            first = max(first, at_keys[e].lo);
-            end = min(end, at_keys[e].hi);
+          // (rows behind the end and rows without a key have P = 0 already)
+          keys[e] = rows.i[e] < 0 ? KeyRange{0, 0} : held_keys(rows.keys[e], a.causal, sq, sk, rows.i[e]);
+          // (a capped score is a line in r: its constant with the rest of P's exponent)
+          nl[e] = rows.lse[e] == -INFINITY
+                      ? -INFINITY
+                      : fmaf(-rows.lse[e], kLog2E, CAPPED ? kPShift + turned.top : kPShift);
+          // (a row without a key: whatever its dO held)
+          nd[e] = rows.lse[e] == -INFINITY ? 0.0f : rows.delta[e] * -damp;
+          if (keys[e].hi > 0) {
+            first = max(first, keys[e].lo);
+            end = min(end, keys[e].hi);
           }
         }
         first = __reduce_max_sync(0xffffffffu, first);
         end = __reduce_min_sync(0xffffffffu, end);
+        if (it + k >= C::N) ok = warp_attn_wait(bar(C::EMPTY + r.s), r.parity ^ 1, ctl);
+        if (!ok) break;
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+          lse_rows(r.s)[e * 32 + lane] = nl[e];
+          delta_rows(r.s)[e * 32 + lane] = nd[e];
+          if constexpr (BIASED) {
+            place_rows(r.s)[e * 32 + lane] = (float)(rows.i[e] + off);
+            slope_rows(r.s)[e * 32 + lane] = rows.slope[e] * kLog2E;
+          }
+          first_rows(r.s)[e * 32 + lane] = keys[e].lo;
+          end_rows(r.s)[e * 32 + lane] = keys[e].hi;
+        }
         if (lane == 0) {
           tile_keys(r.s)[0] = first;
           tile_keys(r.s)[1] = end;
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(C::FULL + r.s));
+        r.next();
+        if (it + k + 2 < n) load(rows);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(C::FULL + r.s));
-      r.next();
     }
   } else if (warp == kTailWarp) {
     // Where the last query tile of a head is cut by the sequence's end, or its
@@ -886,17 +959,14 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       int tile = tile0;
       RingAt<C::N> r;
       for (int it = 0; it < n; ++it) {
-        // (ranges of keys: rows without a key anywhere in the tile)
-        uint32_t none[2] = {0u, 0u};
-        if (ranged) {
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int i = ((t0 + tile) * kTurn + e * 32 + lane) >> shift;
-            none[e] = __ballot_sync(0xffffffffu, i < sq.len && q_row_ok(a, sq.start + i, h0) &&
-                                                     key_range(args.scores, a.causal, sq, sk, i).hi == 0);
-          }
-        }
         if (!warp_attn_wait(bar(C::FULL + r.s), r.parity, ctl)) break;
+        // (holes: the rows without a key, by the ranges that came with the stage)
+        uint32_t none[2] = {0u, 0u};
+        if (holes) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            none[e] = __ballot_sync(0xffffffffu, end_rows(r.s)[e * 32 + lane] == 0);
+        }
         if (none[0] | none[1]) {
           constexpr int UNITS = C::Tile::SUB * 8;   // 16-byte units of a row
 #pragma unroll
@@ -1040,54 +1110,65 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
       int first = 0;
       if constexpr (SCORES) {
         const int* bounds = tile_keys(at_stage);
-        cut = bounds[0] > k0 || bounds[1] < k0 + 128;
-        const float4* place = reinterpret_cast<const float4*>(place_rows(at_stage));
-        const float4* slope = reinterpret_cast<const float4*>(slope_rows(at_stage));
-        const int4* lo = reinterpret_cast<const int4*>(first_rows(at_stage));
-        const int4* hi = reinterpret_cast<const int4*>(end_rows(at_stage));
-        auto probabilities = [&](auto masked) {
+        const bool cut_first = bounds[0] > k0, cut_end = bounds[1] < min(k0 + 128, sk.len);
+        cut = cut_first || cut_end;
+        if constexpr (CAPPED) {   // r
+#pragma unroll
+          for (int q = 0; q < NQ; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2) {
+              const float2 x = turned.rest(make_float2(__uint_as_float(p[q][e]), __uint_as_float(p[q][e + 1])));
+              p[q][e] = __float_as_uint(x.x);
+              p[q][e + 1] = __float_as_uint(x.y);
+            }
+        }
+        // what leaves no probability, whatever else is added
+        const uint32_t out = __float_as_uint(CAPPED ? 1e30f : -3e38f);
+        auto leave_out = [&](const int* rows, auto outside) {
+          const int4* at = reinterpret_cast<const int4*>(rows);
 #pragma unroll
           for (int q = 0; q < NQ; ++q)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const float4 l = nl[q * 8 + e];
+              const int4 b = at[q * 8 + e];
               uint32_t* x = &p[q][e * 4];
-              float2 ru = make_float2(__uint_as_float(x[0]), __uint_as_float(x[1]));
-              float2 rv = make_float2(__uint_as_float(x[2]), __uint_as_float(x[3]));
-              if constexpr (CAPPED) {
-                ru = turned.rest(ru);
-                rv = turned.rest(rv);
-              }
-              float2 u = fma2(ru, cc, make_float2(l.x, l.y));
-              float2 v = fma2(rv, cc, make_float2(l.z, l.w));
-              if constexpr (BIASED) {
-                const float4 at = place[q * 8 + e], sl = slope[q * 8 + e];
-                u = make_float2(fmaf(-sl.x, fabsf(at.x - my_key), u.x), fmaf(-sl.y, fabsf(at.y - my_key), u.y));
-                v = make_float2(fmaf(-sl.z, fabsf(at.z - my_key), v.x), fmaf(-sl.w, fabsf(at.w - my_key), v.y));
-              }
-              u = make_float2(ex2_approx(u.x), ex2_approx(u.y));
-              v = make_float2(ex2_approx(v.x), ex2_approx(v.y));
-              if constexpr (decltype(masked)::value) {
-                const int4 first = lo[q * 8 + e], end = hi[q * 8 + e];
-                if (key < first.x || key >= end.x) u.x = 0.0f;
-                if (key < first.y || key >= end.y) u.y = 0.0f;
-                if (key < first.z || key >= end.z) v.x = 0.0f;
-                if (key < first.w || key >= end.w) v.y = 0.0f;
-              }
-              w[q * 16 + e * 2] = pack16<BF16>(u.x, u.y);
-              w[q * 16 + e * 2 + 1] = pack16<BF16>(v.x, v.y);
-              if constexpr (CAPPED) {   // (P itself is not wanted any more)
-                u = ScoreTurn::times_slope(u, ru);
-                v = ScoreTurn::times_slope(v, rv);
-              }
-              x[0] = __float_as_uint(u.x);
-              x[1] = __float_as_uint(u.y);
-              x[2] = __float_as_uint(v.x);
-              x[3] = __float_as_uint(v.y);
+              if (outside(b.x)) x[0] = out;
+              if (outside(b.y)) x[1] = out;
+              if (outside(b.z)) x[2] = out;
+              if (outside(b.w)) x[3] = out;
             }
         };
-        if (cut) probabilities(std::true_type{});
-        else probabilities(std::false_type{});
+        if (cut_first) leave_out(first_rows(at_stage), [&](int b) { return key < b; });
+        if (cut_end) leave_out(end_rows(at_stage), [&](int b) { return key >= b; });
+#pragma unroll
+        for (int q = 0; q < NQ; ++q)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float4 l = nl[q * 8 + e];
+            uint32_t* x = &p[q][e * 4];
+            const float2 ru = make_float2(__uint_as_float(x[0]), __uint_as_float(x[1]));
+            const float2 rv = make_float2(__uint_as_float(x[2]), __uint_as_float(x[3]));
+            float2 u = fma2(ru, cc, make_float2(l.x, l.y));
+            float2 v = fma2(rv, cc, make_float2(l.z, l.w));
+            if constexpr (BIASED) {
+              const float4 at = reinterpret_cast<const float4*>(place_rows(at_stage))[q * 8 + e];
+              const float4 sl = reinterpret_cast<const float4*>(slope_rows(at_stage))[q * 8 + e];
+              u = make_float2(fmaf(-sl.x, fabsf(at.x - my_key), u.x), fmaf(-sl.y, fabsf(at.y - my_key), u.y));
+              v = make_float2(fmaf(-sl.z, fabsf(at.z - my_key), v.x), fmaf(-sl.w, fabsf(at.w - my_key), v.y));
+            }
+            u = make_float2(ex2_approx(u.x), ex2_approx(u.y));
+            v = make_float2(ex2_approx(v.x), ex2_approx(v.y));
+            w[q * 16 + e * 2] = pack16<BF16>(u.x, u.y);
+            w[q * 16 + e * 2 + 1] = pack16<BF16>(v.x, v.y);
+            if constexpr (CAPPED) {   // (P itself is not wanted any more)
+              u = ScoreTurn::times_slope(u, ru);
+              v = ScoreTurn::times_slope(v, rv);
+            }
+            x[0] = __float_as_uint(u.x);
+            x[1] = __float_as_uint(u.y);
+            x[2] = __float_as_uint(v.x);
+            x[3] = __float_as_uint(v.y);
+          }
       } else {
 #pragma unroll
         for (int q = 0; q < NQ; ++q)

@@ -368,6 +368,26 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
       const int lim_j = lim - (j0 + j) * 128;
       if constexpr (SCORES) {
+        // (a row without a key cuts no tile: its sums are dropped at the end)
+        const int low_j = low - (j0 + j) * 128;
+        const bool cut_end = __any_sync(0xffffffffu, lim >= 0 && lim_j < 127);
+        const bool cut_first = __any_sync(0xffffffffu, lim >= 0 && low_j > 0);
+        auto leave_out = [&](uint32_t value) {
+          if (cut_end) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (q * 32 + e > lim_j) s[q][e] = value;
+          }
+          if (cut_first) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (q * 32 + e < low_j) s[q][e] = value;
+          }
+        };
         if constexpr (CAPPED) {
           auto cap = [&](auto small) {
 #pragma unroll
@@ -380,15 +400,21 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 s[q][e + 1] = __float_as_uint(y.y);
               }
           };
-          float big = 0.0f;
+          // By the row's own largest score: what a row's results are does not go
+          // by other rows, nor, where the mask cuts the tile, by what it hides.
+          // (NaN is passed over: either way gives NaN.)
+          float big = INFINITY;
+          if (!cut_end && !cut_first) {
+            big = 0.0f;
 #pragma unroll
-          for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int e = 0; e < 32; e += 2)
-              big = max3(big, fabsf(__uint_as_float(s[q][e])), fabsf(__uint_as_float(s[q][e + 1])));
-          // (NaN is passed over: either way gives NaN)
-          if (__all_sync(0xffffffffu, big * args.scores.unit.x <= 0.75f)) cap(std::true_type{});
+              for (int e = 0; e < 32; e += 2)
+                big = max3(big, fabsf(__uint_as_float(s[q][e])), fabsf(__uint_as_float(s[q][e + 1])));
+          }
+          if (big * args.scores.unit.x <= 0.75f) cap(std::true_type{});
           else cap(std::false_type{});
+          __syncwarp();
         }
         if constexpr (BIASED) {
           const float here = (float)(i + sk.len - sq.len - (j0 + j) * 128);
@@ -405,14 +431,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             }
           }
         }
-        const int low_j = low - (j0 + j) * 128;
-        if (__any_sync(0xffffffffu, lim_j < 127 || low_j > 0)) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (q * 32 + e > lim_j || q * 32 + e < low_j) s[q][e] = 0xff800000u;   // -inf
-        }
+        leave_out(0xff800000u);   // -inf
       } else if (__any_sync(0xffffffffu, lim_j < 127)) {
 #pragma unroll
         for (int q = 0; q < 4; ++q)
@@ -479,6 +498,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       sum[0] = add2(sum[0], sum[1]);
       l += sum[0].x + sum[0].y;
     }
+    if (SCORES && lim < 0) l = 0.0f;   // (a row without a key, whatever it has summed)
     if (ok && nk > 0) {
       ok = warp_wait_phase<kAttnNapNs>(bar(C::O_FULL + t), C::AHEAD ? (nk - bt - 1) & 1 : 0, ctl);
       tc_fence_after_sync();
