@@ -336,11 +336,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int i = i0 + t * tile_q + turn;   // query of the sequence
     // (packed: the last rows of a tile may be nobody's)
     const bool live = i < sq.len && t < TILES && (!PACKED || turn < tile_q);
-    // the factor to base-2 units (a form's scores are in them already)
     const ScoreTurn turned(args.scores, a.scale);
-    const float slope = BIASED && live ? args.scores.slopes[h] * kLog2E : 0.0f;
-    const float c_turned = CAPPED ? 1.0f : a.scale * kLog2E;
-    const float c = BIASED ? 1.0f : c_turned;
+    // the factor to base-2 units (capped scores are in them already), and the
+    // bias of a key's distance, before that factor
+    const float c = CAPPED ? 1.0f : a.scale * kLog2E;
+    const float slope = BIASED && live ? args.scores.slopes[h] * kLog2E / c : 0.0f;
     // the last key that this row may see, and the first
     const int lim = SCORES ? mine.hi - 1
                     : live ? (a.causal ? min(sk.len - 1, i + sk.len - sq.len) : sk.len - 1)
@@ -416,18 +416,27 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           else cap(std::false_type{});
           __syncwarp();
         }
-        if constexpr (BIASED) {
+        if constexpr (BIASED) {   // (in the scores' own units: c comes later)
           const float here = (float)(i + sk.len - sq.len - (j0 + j) * 128);
+          const float2 sl = make_float2(-slope, -slope);
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             float2 far = make_float2(here - (float)(q * 32), here - (float)(q * 32 + 1));
+            if (a.causal) {   // what is not hidden lies behind the query: no sign to drop
 #pragma unroll
-            for (int e = 0; e < 32; e += 2) {
-              const float2 x = mul2(make_float2(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])),
-                                    make_float2(c_turned, c_turned));
-              s[q][e] = __float_as_uint(fmaf(-slope, fabsf(far.x), x.x));
-              s[q][e + 1] = __float_as_uint(fmaf(-slope, fabsf(far.y), x.y));
-              far = add2(far, make_float2(-2.0f, -2.0f));
+              for (int e = 0; e < 32; e += 2) {
+                const float2 x = fma2(far, sl, make_float2(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1])));
+                s[q][e] = __float_as_uint(x.x);
+                s[q][e + 1] = __float_as_uint(x.y);
+                far = add2(far, make_float2(-2.0f, -2.0f));
+              }
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 2) {
+                s[q][e] = __float_as_uint(fmaf(-slope, fabsf(far.x), __uint_as_float(s[q][e])));
+                s[q][e + 1] = __float_as_uint(fmaf(-slope, fabsf(far.y), __uint_as_float(s[q][e + 1])));
+                far = add2(far, make_float2(-2.0f, -2.0f));
+              }
             }
           }
         }
@@ -553,7 +562,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
       if (live && q_row_ok(a, token, h)) 
         *lse = l == 0.0f ? -INFINITY
-               : CAPPED || BIASED ? m * kLn2 + logf(l)
+               : CAPPED ? m * kLn2 + logf(l)
                                       : m * a.scale + logf(l);
     }
   }

@@ -13,7 +13,9 @@
 //
 // Bound by memory: a row's entries stay in registers from its first sum to its
 // results, so each tensor is read or written once. A team of warps has a row,
-// V units of four entries to a thread.
+// V units of four entries to a thread. The gradient's threads copy the units of
+// their next rows into shared memory of their own meanwhile (nobody else's: a
+// copy's end is all that its reader waits for).
 #include "lin_norms.h"
 
 #include "lin_common.cuh"
@@ -160,6 +162,25 @@ __global__ void __launch_bounds__(kNormThreads, 2)
   }
 }
 
+// Bytes of a thread's units of a row in shared memory, and rows on their way.
+template <int T, int V>
+struct NormStage {
+  static constexpr int kUnit = T == LIN_BINARY32 ? 16 : 8;   // of y and dn
+  static constexpr int kThread = V * (32 + 2 * kUnit);
+  static constexpr int kRows = V == 4 ? 1 : V == 2 ? 2 : 4;
+  static constexpr int kBytes = kRows * kThread * kNormThreads;
+  static_assert(kBytes + 4 * kNormMostWidth <= 227 * 1024, "shared memory");
+};
+// A unit's copy; complete after cp_async_wait.
+__device__ __forceinline__ void copy_unit8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // The gradient. A CTA's teams walk over the rows with a fixed stride and keep
 // the sums over the tokens of their columns in registers; the teams' are added
 // in order and leave one partial row of each kind, and a second kernel adds
@@ -167,25 +188,61 @@ __global__ void __launch_bounds__(kNormThreads, 2)
 template <int T, int V>
 __global__ void __launch_bounds__(kNormThreads, 1)
     lin_block_norms_bwd_kernel(const __grid_constant__ NormsArgs a, int warps) {
-  extern __shared__ float4 sums[];   // [units of a row] of a team's sums
+  using Stage = NormStage<T, V>;
+  extern __shared__ float4 shared[];
+  float4* const sums = shared;       // [units of a row] of a team's sums
+  uint8_t* const staged = reinterpret_cast<uint8_t*>(shared) + ((a.width + 3) / 4) * 16;
   __shared__ float4 red[2 * kNormThreads / 32];
   Team team(warps, red);
   const int teams = blockDim.x / team.threads;
+  const int64_t step = (int64_t)gridDim.x * teams;
   const float inv_w = 1.0f / (float)a.width;
+  // Unit i of tensor k (h, dh, y, dn) of the row in place `at`: units of a
+  // tensor side by side over the threads.
+  auto place = [&](int at, int k, int i) {
+    const int before = at * Stage::kThread + V * (k < 2 ? k * 16 : 32 + (k - 2) * Stage::kUnit);
+    const int unit = k < 2 ? 16 : Stage::kUnit;
+    return staged + before * blockDim.x + (i * blockDim.x + threadIdx.x) * unit;
+  };
+  auto copy = [&](int64_t t, int at) {
+    if (t < a.tokens) {
+      const int64_t row = t * a.width;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int col = (i * team.threads + team.thread) * 4;
+        if (col >= a.width || !unit_ok(a, t, col)) continue;
+        if (a.dn) cp_async_16(smem_u32(place(at, 0, i)), a.x + row + col);
+        if (a.dh) cp_async_16(smem_u32(place(at, 1, i)), a.dh + row + col);
+        auto block = [&](const void* from, int k) {
+          if constexpr (T == LIN_BINARY32)
+            cp_async_16(smem_u32(place(at, k, i)), static_cast<const float*>(from) + row + col);
+          else
+            copy_unit8(smem_u32(place(at, k, i)), static_cast<const uint16_t*>(from) + row + col);
+        };
+        if (a.y) block(a.y, 2);
+        if (a.dn) block(a.dn, 3);
+      }
+    }
+    copies_commit();   // (a group for each row, also behind the last one)
+  };
   Four d_pre[V]{}, d_post[V]{}, d_gate[V]{};
-  for (int64_t t = (int64_t)blockIdx.x * teams + team.team; t < a.tokens;
-       t += (int64_t)gridDim.x * teams) {
+  int64_t t = (int64_t)blockIdx.x * teams + team.team;
+#pragma unroll
+  for (int s = 0; s < Stage::kRows; ++s) copy(t + s * step, s);
+  int at = 0;
+  for (; t < a.tokens; t += step) {
     const int64_t row = t * a.width;
     Four h[V], y[V], dn[V], d[V];
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    copies_wait<Stage::kRows - 1>();
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int col = (i * team.threads + team.thread) * 4;
-      const bool in = col < a.width && unit_ok(a, t, col);
-      h[i] = in && a.dn ? load4f(a.x, row + col) : Four{};
-      dn[i] = in && a.dn ? load4<T>(a.dn, row + col) : Four{};
-      y[i] = in && a.y ? load4<T>(a.y, row + col) : Four{};
-      d[i] = in && a.dh ? load4f(a.dh, row + col) : Four{};
+      const bool in = col < a.width;
+      h[i] = in && a.dn ? load4<LIN_BINARY32>(place(at, 0, i), 0) : Four{};
+      d[i] = in && a.dh ? load4<LIN_BINARY32>(place(at, 1, i), 0) : Four{};
+      y[i] = in && a.y ? load4<T>(place(at, 2, i), 0) : Four{};
+      dn[i] = in && a.dn ? load4<T>(place(at, 3, i), 0) : Four{};
     }
     const float gt = a.form == NORM_GATE_TOKEN ? a.gate[t] : 1.0f;
 #pragma unroll
@@ -200,6 +257,9 @@ __global__ void __launch_bounds__(kNormThreads, 1)
       }
     }
     if (a.dn || a.w_post) s = team.sum(s);
+    __syncwarp();   // (what the row's place held has been read: it may change)
+    copy(t + Stage::kRows * step, at);
+    at = at + 1 == Stage::kRows ? 0 : at + 1;
     const float rh = rsqrtf(fmaf(s.x, inv_w, a.eps)), kh = s.y * rh * rh * inv_w;
     const float ry = a.w_post ? rsqrtf(fmaf(s.z, inv_w, a.eps)) : 1.0f;
     s = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -365,8 +425,15 @@ int block_norms_bwd_ctas(const NormsArgs& a, int sms) {
 cudaError_t launch_block_norms_bwd(const NormsArgs& a, int ctas, cudaStream_t stream) {
   const NormShape s = norm_shape(a.width, kNormThreads);
   const cudaError_t e = with_types(a.dtype, s.v, [&](auto t, auto v) {
-    lin_block_norms_bwd_kernel<decltype(t)::value, decltype(v)::value>
-        <<<(unsigned)ctas, s.teams * s.warps * 32, (size_t)a.width * 4, stream>>>(a, s.warps);
+    constexpr int T = decltype(t)::value, V = decltype(v)::value;
+    using Stage = NormStage<T, V>;
+    auto kernel = lin_block_norms_bwd_kernel<T, V>;
+    const int threads = s.teams * s.warps * 32;
+    const size_t smem = (size_t)a.width * 4 + (size_t)Stage::kRows * Stage::kThread * threads;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<(unsigned)ctas, threads, smem, stream>>>(a, s.warps);
     return cudaGetLastError();
   });
   if (e != cudaSuccess || a.kinds == 0) return e;
