@@ -48,7 +48,8 @@ SOURCES = ["lin_api.cu", "lin_kernels_tf32.cu", "lin_kernels_f16.cu",
            "lin_attn_fwd_ranges.cu", "lin_attn_fwd_cap.cu", "lin_attn_fwd_bias.cu",
            "lin_attn_fwd_cap_bias.cu", "lin_attn_bwd_ranges.cu", "lin_attn_bwd_cap.cu",
            "lin_attn_bwd_bias.cu", "lin_attn_bwd_cap_bias.cu",
-           "lin_attn_api.cu", "lin_rope.cu", "lin_distill.cu", "lin_norms.cu", "lin_adamw.cu",
+           "lin_attn_api.cu", "lin_rope.cu", "lin_distill.cu", "lin_norms.cu", "lin_norms_f16.cu",
+           "lin_norms_bf16.cu", "lin_norms_f32.cu", "lin_adamw.cu",
            "lin_step_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CFLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",

@@ -30,10 +30,15 @@ struct NormsArgs {
   int* status;
 };
 
-cudaError_t launch_block_norms(const NormsArgs& a, cudaStream_t stream);
+cudaError_t launch_block_norms(const NormsArgs& a, int sms, cudaStream_t stream);
 // CTAs of the gradient's kernel (rows of its partial sums).
 int block_norms_bwd_ctas(const NormsArgs& a, int sms);
 // The gradient, and, where a.kinds > 0, the sums over its CTAs.
-cudaError_t launch_block_norms_bwd(const NormsArgs& a, int ctas, cudaStream_t stream);
+cudaError_t launch_block_norms_bwd(const NormsArgs& a, int sms, int ctas, cudaStream_t stream);
+// The same for the type T of the block's tensors (its kernels alone).
+template <int T>
+cudaError_t launch_block_norms_of(const NormsArgs& a, int sms, cudaStream_t stream);
+template <int T>
+cudaError_t launch_block_norms_bwd_of(const NormsArgs& a, int sms, int ctas, cudaStream_t stream);
 
 }  // namespace lin

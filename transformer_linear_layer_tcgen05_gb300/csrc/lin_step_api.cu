@@ -274,7 +274,7 @@ lin_status block_norms(const lin_block_norms_shape* s, const float* X, const voi
   a.eps = s->eps;
   a.status = word;
   if (!backward) {
-    const cudaError_t e = lin::launch_block_norms(a, stream);
+    const cudaError_t e = lin::launch_block_norms(a, sm_count(dev), stream);
     if (e != cudaSuccess) return cuda_fail(e);
     set_last_launch_info(1, 0);
     return LIN_SUCCESS;
@@ -286,7 +286,7 @@ lin_status block_norms(const lin_block_norms_shape* s, const float* X, const voi
     a.partial = static_cast<float*>(take_stream_workspace(dev, bytes, stream));
     if (!a.partial) return LIN_ERROR_CUDA;
   }
-  cudaError_t e = lin::launch_block_norms_bwd(a, ctas, stream);
+  cudaError_t e = lin::launch_block_norms_bwd(a, sm_count(dev), ctas, stream);
   if (bytes) {
     const cudaError_t ef = cudaFreeAsync(a.partial, stream);
     if (e == cudaSuccess) e = ef;
