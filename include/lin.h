@@ -504,7 +504,8 @@ lin_status lin_qk_norm_rope_backward(const lin_qk_norm_rope_shape *shape, const 
  * the table row of pair i (values outside are held to 0 .. axes - 1). The
  * angle of pair i is entry i of that row: axes whose frequencies begin anew
  * have their columns of the tables made so. Sections of the pairs, pairs dealt
- * to the axes in turn, or any other order. All else as above. */
+ * to the axes in turn, or any other order. Workspace, of large calls: rot floats
+ * for each token more. All else as above. */
 lin_status lin_qk_norm_rope_axes(const lin_qk_norm_rope_shape *shape, int64_t axes, const float *X,
                                  const float *WQ, const float *WK, const float *COS,
                                  const float *SIN, const int32_t *positions,

@@ -443,7 +443,8 @@ struct NormShape {
   size_t smem;
 };
 template <typename Bytes>
-inline NormShape norm_shape(int64_t tokens, int width, int sms, size_t room, Bytes&& bytes_of_thread) {
+inline NormShape norm_shape(int64_t tokens, int width, int sms, int ctas, size_t room,
+                            Bytes&& bytes_of_thread) {
   const int units = width / 4;
   NormShape s;
   // as many units to a thread as leave every SM's sixteen warps rows of their own
@@ -454,7 +455,7 @@ inline NormShape norm_shape(int64_t tokens, int width, int sms, size_t room, Byt
   s.v = std::max(1, (units + 32 * s.warps - 1) / (32 * s.warps));
   // (a named barrier to each team of several warps; few rows: on many SMs)
   s.teams = std::min(std::max(1, kNormThreads / 32 / s.warps), s.warps > 1 ? 15 : 16);
-  s.teams = (int)std::min<int64_t>(s.teams, std::max<int64_t>(1, (tokens + sms - 1) / sms));
+  s.teams = (int)std::min<int64_t>(s.teams, std::max<int64_t>(1, (tokens + ctas - 1) / ctas));
   const size_t slot = (size_t)s.teams * s.warps * 32 * bytes_of_thread(s.v);
   s.slots = slot * 4 <= room ? 4 : slot * 2 <= room ? 2 : 1;
   s.smem = slot * s.slots;
@@ -462,12 +463,12 @@ inline NormShape norm_shape(int64_t tokens, int width, int sms, size_t room, Byt
 }
 inline NormShape fwd_shape(const NormsArgs& a, int sms) {
   const int b = a.dtype == LIN_BINARY32 ? 16 : 8;
-  return norm_shape(a.tokens, a.width, sms, 112 * 1024,
+  return norm_shape(a.tokens, a.width, sms, 2 * sms, 112 * 1024,
                     [&](int v) { return v * (16 + b); });   // (two CTAs an SM)
 }
 inline NormShape bwd_shape(const NormsArgs& a, int sms) {
   const int b = a.dtype == LIN_BINARY32 ? 16 : 8;
-  return norm_shape(a.tokens, a.width, sms, 226 * 1024 - (size_t)a.width * 12,
+  return norm_shape(a.tokens, a.width, sms, sms, 226 * 1024 - (size_t)a.width * 12,
                     [&](int v) { return v * (32 + 2 * b); });
 }
 

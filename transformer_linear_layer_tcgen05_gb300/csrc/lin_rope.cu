@@ -315,6 +315,21 @@ __global__ void __launch_bounds__(kRopeThreads, kBwdCtas)
   }
 }
 
+// The angles of every token, gathered by its pairs' axes into tables of a row
+// to each token.
+__global__ void __launch_bounds__(kRopeThreads)
+    lin_gather_angles_kernel(const __grid_constant__ RopeArgs a, float* __restrict__ cos_out,
+                             float* __restrict__ sin_out) {
+  const int fours = a.rot / 8;
+  const int64_t k = (int64_t)blockIdx.x * kRopeThreads + threadIdx.x;
+  const int64_t t = k / fours;
+  if (t >= a.tokens) return;
+  float4 c = make_float4(1.f, 1.f, 1.f, 1.f), s = make_float4(0.f, 0.f, 0.f, 0.f);
+  angles<true>(a, t, (int)(k % fours) * 4, c, s);
+  reinterpret_cast<float4*>(cos_out)[k] = c;
+  reinterpret_cast<float4*>(sin_out)[k] = s;
+}
+
 // dwq (y 0) from the first q_rows of the CTAs' partial rows, dwk (y 1) from
 // the others: a CTA per 32 columns, its 32 warps each a share of the rows,
 // then a fixed-order sum over the warps.
@@ -361,6 +376,19 @@ cudaError_t with_shape(const RopeArgs& a, bool inter, bool bf16, F&& f) {
 }
 
 }  // namespace
+
+cudaError_t launch_gather_angles(RopeArgs& a, float* room, cudaStream_t stream) {
+  float* const sines = room + a.tokens * (a.rot / 2);
+  const int64_t threads = a.tokens * (a.rot / 8);
+  lin_gather_angles_kernel<<<(unsigned)((threads + kRopeThreads - 1) / kRopeThreads), kRopeThreads, 0,
+                             stream>>>(a, room, sines);
+  a.cos = room;
+  a.sin = sines;
+  a.pos = nullptr;
+  a.axis = nullptr;
+  a.table_rows = a.tokens;
+  return cudaGetLastError();
+}
 
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, bool inter, bool bf16, cudaStream_t stream) {
   return with_shape(a, inter, bf16, [&](auto g, auto i, auto b, auto x) {

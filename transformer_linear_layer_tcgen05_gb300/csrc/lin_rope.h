@@ -29,6 +29,9 @@ struct RopeArgs {
   int* status;            // device status record (checked build)
 };
 
+// The tokens' angles by their axes as tables in `room` (rot floats to a token),
+// which `a` then has in place of positions and axes.
+cudaError_t launch_gather_angles(RopeArgs& a, float* room, cudaStream_t stream);
 cudaError_t launch_qk_norm_rope(const RopeArgs& a, bool inter, bool bf16, cudaStream_t stream);
 // CTAs of the gradient's kernel (rows of its partial sums); sets a.q_ctas.
 int qk_norm_rope_bwd_ctas(RopeArgs& a, int sms);
