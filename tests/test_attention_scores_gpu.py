@@ -219,6 +219,36 @@ def test_rows_without_keys_give_nothing_whatever_they_hold(d, heads):
         assert torch.equal(t[k], want[k]), k
 
 
+def test_rows_without_keys_that_hold_the_largest_numbers():
+    # (finite ones, whose products are not)
+    import torch
+    lens = [(300, 300)]
+    t = _setup("bfloat16", lens, 2, 1, 64, seed=13)
+    t["k"][:], t["v"][:] = 100 * t["k"], 100 * t["v"]
+    end = np.arange(1, 301).astype(np.int32)
+    none = np.arange(3, 300, 17)
+    end[none] = 0
+    form = dict(end_key=torch.from_numpy(end).cuda())
+    _run(t, lens, True, 0.1, form)
+    want = {k: t[k].clone() for k in ("o", "lse", "dq", "dk", "dv")}
+    assert all(torch.isfinite(t[k]).all() for k in ("o", "dq", "dk", "dv"))
+    rows = torch.from_numpy(none).cuda()
+    for q, do in ((3e38, 1.0), (1.0, -3e38), (1e20, 1e20)):
+        t["q"][rows], t["do"][rows] = q, do
+        _run(t, lens, True, 0.1, form)
+        for k in want:
+            assert torch.equal(t[k], want[k]), (k, q, do)
+
+
+@pytest.mark.parametrize("cap", [1e-3, 300.0, 4096.0])
+def test_small_and_large_caps(cap):
+    lens = [(140, 260)]
+    t = _setup("float16", lens, 2, 2, 64, seed=14, gain=2.0)
+    form = dict(cap=cap)
+    _run(t, lens, True, 0.2, form)
+    _check(t, lens, True, 0.2, form, UNIT["float16"])
+
+
 def test_no_row_sees_anything():
     import torch
     for lens in ([(200, 300)], [(3, 2000)]):

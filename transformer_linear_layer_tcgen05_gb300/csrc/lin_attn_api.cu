@@ -129,8 +129,15 @@ lin_status check_form(const lin_score_form* f, const lin_attention_shape* s, con
   }
   return LIN_SUCCESS;
 }
-// (its numbers are checked before anything touches CUDA)
-bool form_ok(const lin_score_form* f) { return !f || (f->cap >= 0.0f && !std::isinf(f->cap)); }
+// Its numbers, checked before anything touches CUDA. A capped score is off by up
+// to cap 2^-20: beyond caps of 4096 by more than P's rounding to bfloat16.
+lin_status check_cap(const lin_score_form* f, const lin_attention_shape* s) {
+  if (!f) return LIN_SUCCESS;
+  if (!(f->cap >= 0.0f) || std::isinf(f->cap)) return LIN_ERROR_INVALID_VALUE;
+  if (f->cap > 4096.0f) return LIN_ERROR_UNSUPPORTED_SHAPE;
+  if (s && f->cap > 0.0f && !std::isfinite(4.0f * s->scale / f->cap)) return LIN_ERROR_UNSUPPORTED_SHAPE;
+  return LIN_SUCCESS;
+}
 // Calls f with the compiler's parameter for the form.
 template <typename F>
 cudaError_t with_form(const lin_score_form* f, F&& go) {
@@ -167,11 +174,11 @@ lin_status attention(const lin_attention_shape* s, const lin_score_form* form, c
                      const lin_heads* K, const lin_heads* V, const lin_heads* O, float* LSE,
                      cudaStream_t stream) {
   set_last_launch_info(0, 0);
-  if (!form_ok(form)) return LIN_ERROR_INVALID_VALUE;
   const int64_t hq = s ? s->heads_q : 0, hk = s ? s->heads_kv : 0;
   View v[] = {{Q, 0, hq, false}, {K, -1, hk, false}, {V, -1, hk, false}, {O, 0, hq, true}};
   Checked c;
-  lin_status st = check_attention(s, v, 4, LSE, true, &c);
+  lin_status st = check_cap(form, s);
+  if (st == LIN_SUCCESS) st = check_attention(s, v, 4, LSE, true, &c);
   if (st == LIN_SUCCESS) st = check_form(form, s, v, 4, LSE, true, c);
   if (st != LIN_SUCCESS) return st;
   if (c.nothing || c.max_q == 0) return LIN_SUCCESS;
@@ -238,12 +245,12 @@ lin_status attention_backward(const lin_attention_shape* s, const lin_score_form
                               const lin_heads* DQ, const lin_heads* DK, const lin_heads* DV,
                               cudaStream_t stream) {
   set_last_launch_info(0, 0);
-  if (!form_ok(form)) return LIN_ERROR_INVALID_VALUE;
   const int64_t hq = s ? s->heads_q : 0, hk = s ? s->heads_kv : 0;
   View v[] = {{Q, 0, hq, false},  {K, -1, hk, false}, {V, -1, hk, false}, {O, 0, hq, false},
               {DO, 0, hq, false}, {DQ, 0, hq, true},  {DK, -1, hk, true}, {DV, -1, hk, true}};
   Checked c;
-  lin_status st = check_attention(s, v, 8, LSE, false, &c);
+  lin_status st = check_cap(form, s);
+  if (st == LIN_SUCCESS) st = check_attention(s, v, 8, LSE, false, &c);
   if (st == LIN_SUCCESS) st = check_form(form, s, v, 8, LSE, false, c);
   if (st != LIN_SUCCESS) return st;
   if (c.nothing || (c.max_q == 0 && c.max_k == 0)) return LIN_SUCCESS;

@@ -71,7 +71,7 @@ constexpr int kTailWarp = 10;       // of the dK, dV kernel: zeroes rows that ta
 constexpr int kStatsWarp = 11;      // of the dK, dV kernel: rows' statistics
 constexpr int kTurn = 64;           // rows of a streamed tile
 // (of a tile's extent, beside the key behind its last) some row without a key
-// holds what is no finite number
+// holds what a product with zero would not remove
 constexpr int kBadFlag = 1 << 30;
 
 // Shared memory and barriers of both kernels. A stage of the ring holds the
@@ -412,15 +412,18 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
       if constexpr (SCORES) {
         // A row without a key has P = dS = 0, which the second kernel's products
         // over the queries multiply with its Q and dO: nothing, unless one of
-        // these is no finite number. Such rows, and only such, are zeroed there
-        // (all rows without keys, by a warp between the copies and the products:
-        // nine sequences of up to 997 with one row in twenty 47 -> 72 us).
+        // these is no finite number, or so large that S or dP might not be. Such
+        // rows, and only such, are zeroed there (all rows without keys, by a warp
+        // between the copies and the products: nine sequences of up to 997 with
+        // one row in twenty 47 -> 72 us).
         bool bad = false;
         if (__any_sync(0xffffffffu, live && mine.hi == 0)) {
-          constexpr uint32_t E = BF16 ? 0x7f80u : 0x7c00u;   // the exponent of NaN and infinity
+          // (binary16: its largest products are far below float32's end; bfloat16: 2^15)
+          constexpr uint32_t big = BF16 ? 0x4700u : 0x7c00u;
 #pragma unroll
           for (int e = 0; e < DP / 4; ++e)
-            bad |= (x[e] & E) == E || ((x[e] >> 16) & E) == E || (y[e] & E) == E || ((y[e] >> 16) & E) == E;
+            bad |= (x[e] & 0x7fffu) >= big || ((x[e] >> 16) & 0x7fffu) >= big ||
+                   (y[e] & 0x7fffu) >= big || ((y[e] >> 16) & 0x7fffu) >= big;
         }
         bad = __any_sync(0xffffffffu, bad && live && mine.hi == 0);
         if (lane == 0) bad_rows[warp] = bad;
