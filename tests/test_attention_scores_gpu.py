@@ -157,6 +157,17 @@ def test_long_sides_in_parts(kind, dtype):
         _check(t, lens, False, 0.125, form, UNIT[dtype])
 
 
+@pytest.mark.parametrize("kind", ["cap bias docs", "any", "cap window", "bias prefix"])
+@pytest.mark.parametrize("d, heads", [(64, (36, 18)), (128, (33, 11)), (96, (24, 24))])
+def test_many_tiles(kind, d, heads):
+    # more tiles of queries than SMs: two of them to a CTA
+    lens = [(700, 700), (40, 300)]
+    t = _setup("bfloat16", lens, *heads, d, seed=15, gain=2.0)
+    form = _form(kind, lens, heads[0], seed=16)
+    _run(t, lens, "window" in kind, 0.1, form)
+    _check(t, lens, "window" in kind, 0.1, form, UNIT["bfloat16"])
+
+
 @pytest.mark.parametrize("scale", [0.02, 0.5, 8.0])
 def test_scores_far_below_and_above_the_cap(scale):
     lens = [(150, 200)]

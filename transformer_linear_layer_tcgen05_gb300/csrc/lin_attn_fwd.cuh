@@ -76,6 +76,7 @@ struct FwdCfg {
   static constexpr int BARS = DRAIN + 1;
   static constexpr uint32_t OFF_TMEM = BARS * 8, OFF_ABORT = OFF_TMEM + 4;
   static constexpr uint32_t OFF_EXTENTS = 512;   // 16 ints: the warps' keys
+  static constexpr uint32_t OFF_MEET = 640;      // a barrier: two threads to a row
   static_assert(OFF_ABORT + 4 <= OFF_EXTENTS, "barrier region");
   static constexpr uint32_t OFF_Q = 1024;
   static constexpr uint32_t OFF_K = OFF_Q + 2 * TILE;
@@ -112,6 +113,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   using C = FwdCfg<DP>;
   constexpr bool SCORES = FORM != kNoForm;
   constexpr bool CAPPED = SCORES && (FORM & kCap), BIASED = SCORES && (FORM & kBias);
+  // Two threads to a row, one of each warpgroup, where the second one has no
+  // tile: each turns half of the scores, and they meet for the maximum. (Ranges
+  // alone have the sums, bit by bit, of the causal mask that they may be.)
+  constexpr bool SPLIT = TILES == 1 && (CAPPED || BIASED);
+  constexpr int NQ = SPLIT ? 2 : 4;   // groups of 32 columns of a thread
   extern __shared__ uint8_t smem_raw[];
   const AttnArgs& a = args.s;
   const int pack = PACKED ? args.pack : 1, tile_q = PACKED ? args.tile_q : 128;
@@ -158,7 +164,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   }
   if (tid == 0) *abort = 0;
   if (tid < C::BARS) {
-    mbar_init(bar(tid), tid >= C::P_READY && tid < C::O_FULL ? 4 : 1);
+    mbar_init(bar(tid), SPLIT && tid == C::S_TAKEN              ? 8
+                        : tid >= C::P_READY && tid < C::O_FULL ? 4
+                                                               : 1);
+    if (SPLIT && tid == 0) mbar_init(base + C::OFF_MEET, 8);
     fence_barrier_init();
   }
   // the keys of this thread's row, and of each warp's rows
@@ -167,8 +176,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   if constexpr (SCORES) {
     if (warp < 8) {
       const int turn = PACKED ? (tid & 127) / pack : tid & 127;
-      const int i = i0 + (warp >> 2) * tile_q + turn;
-      if (i < sq.len && (warp < 4 || TILES > 1) && (!PACKED || turn < tile_q) &&
+      const int i = i0 + (SPLIT ? 0 : (warp >> 2) * tile_q) + turn;
+      if (i < sq.len && (warp < 4 || TILES > 1 || SPLIT) && (!PACKED || turn < tile_q) &&
           q_row_ok(a, sq.start + i, h0))
         mine = key_range(args.scores, a.causal, sq, sk, i);
       const KeyRange all = warp_extent(mine);
@@ -299,6 +308,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 #pragma unroll 1
             for (int half = 0; half < 2; ++half) {
               ok = ok && attn_wait(bar(C::P_READY + 2 * t + half), (j - bt) & 1, ctl);
+              // (split: both threads of a row may have scaled their half of O)
+              if (SPLIT && half == 0) ok = ok && attn_wait(bar(C::P_READY + 1), (j - bt) & 1, ctl);
               if (!ok || !stage_ok(a, s, C::NKV)) break;
               tc_fence_after_sync();
               umma_tokens<DP, BF16, 4>(C::O_COL + t * DP, C::p_col(t) + half * 32,
@@ -329,7 +340,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     }
   } else {
     setmaxnreg_inc<kFwdRegsRow>();
-    const int t = warp >> 2, row = tid & 127;
+    const int t = SPLIT ? 0 : warp >> 2, row = tid & 127;
+    const int half = SPLIT ? warp >> 2 : 0, col0 = half * 64;   // (split) the thread's columns
     const int nk = t ? n1 : n0, bt = t ? b1 : b0;
     const int turn = PACKED ? row / pack : row;
     const int h = PACKED ? h0 + row - turn * pack : h0;
@@ -347,42 +359,56 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                            : -1;
     const int low = SCORES ? mine.lo : 0;
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // 32 lanes per warp, lane field at bit 16
-    const uint32_t s_col = tmem + lanes + C::S_COL + t * 128;
-    const uint32_t p_col = tmem + lanes + C::p_col(t);
+    const uint32_t s_col = tmem + lanes + C::S_COL + t * 128 + col0;
+    const uint32_t p_col = tmem + lanes + C::p_col(t) + half * 32;
     const uint32_t o_col = tmem + lanes + C::O_COL + t * DP;
     float m = -INFINITY, l = 0.0f;
     bool ok = true;
+    // (split) what the row's two threads tell each other, in two places in turn
+    // (the second tile's queries have none here)
+    volatile float* const told = reinterpret_cast<volatile float*>(gen + C::OFF_Q + C::TILE);
+    auto meet = [&](int at, float mine_is, float* other) -> bool {
+      volatile float* to = told + (at & 1) * 256;
+      to[half * 128 + row] = mine_is;
+      tc_fence_before_sync();   // (either's P may come over what the other has read of S)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(base + C::OFF_MEET);
+      if (!warp_wait_phase<kAttnNapNs>(base + C::OFF_MEET, at & 1, ctl)) return false;
+      tc_fence_after_sync();
+      *other = to[(half ^ 1) * 128 + row];
+      return true;
+    };
     for (int j = bt; j < nk; ++j) {
       ok = warp_wait_phase<kAttnNapNs>(bar(C::S_FULL + t), (j - bt) & 1, ctl);
       if (!ok) break;
       tc_fence_after_sync();
-      uint32_t s[4][32];
+      uint32_t s[NQ][32];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_ld_32x32b_x32(s_col + q * 32, s[q]);
+      for (int q = 0; q < NQ; ++q) tmem_ld_32x32b_x32(s_col + q * 32, s[q]);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) tmem_wait_ld_x32(s[q]);
+      for (int q = 0; q < NQ; ++q) tmem_wait_ld_x32(s[q]);
       if constexpr (C::AHEAD) {
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(C::S_TAKEN + t));
       }
-      const int lim_j = lim - (j0 + j) * 128;
+      const int lim_j = lim - (j0 + j) * 128 - col0;
       if constexpr (SCORES) {
         // (a row without a key cuts no tile: its sums are dropped at the end)
-        const int low_j = low - (j0 + j) * 128;
-        const bool cut_end = __any_sync(0xffffffffu, lim >= 0 && lim_j < 127);
+        const int low_j = low - (j0 + j) * 128 - col0;
+        const bool cut_end = __any_sync(0xffffffffu, lim >= 0 && lim_j < NQ * 32 - 1);
         const bool cut_first = __any_sync(0xffffffffu, lim >= 0 && low_j > 0);
         auto leave_out = [&](uint32_t value) {
           if (cut_end) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < NQ; ++q)
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (q * 32 + e > lim_j) s[q][e] = value;
           }
           if (cut_first) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < NQ; ++q)
 #pragma unroll
               for (int e = 0; e < 32; ++e)
                 if (q * 32 + e < low_j) s[q][e] = value;
@@ -391,7 +417,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if constexpr (CAPPED) {
           auto cap = [&](auto small) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < NQ; ++q)
 #pragma unroll
               for (int e = 0; e < 32; e += 2) {
                 const float2 x = make_float2(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
@@ -407,7 +433,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           if (!cut_end && !cut_first) {
             big = 0.0f;
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
+            for (int q = 0; q < NQ; ++q)
 #pragma unroll
               for (int e = 0; e < 32; e += 2)
                 big = max3(big, fabsf(__uint_as_float(s[q][e])), fabsf(__uint_as_float(s[q][e + 1])));
@@ -417,10 +443,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           __syncwarp();
         }
         if constexpr (BIASED) {   // (in the scores' own units: c comes later)
-          const float here = (float)(i + sk.len - sq.len - (j0 + j) * 128);
+          const float here = (float)(i + sk.len - sq.len - (j0 + j) * 128 - col0);
           const float2 sl = make_float2(-slope, -slope);
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
+          for (int q = 0; q < NQ; ++q) {
             float2 far = make_float2(here - (float)(q * 32), here - (float)(q * 32 + 1));
             if (a.causal) {   // what is not hidden lies behind the query: no sign to drop
 #pragma unroll
@@ -443,21 +469,27 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         leave_out(0xff800000u);   // -inf
       } else if (__any_sync(0xffffffffu, lim_j < 127)) {
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
+        for (int q = 0; q < NQ; ++q)
 #pragma unroll
           for (int e = 0; e < 32; ++e)
             if (q * 32 + e > lim_j) s[q][e] = 0xff800000u;   // -inf
       }
-      float mx[4];
+      float mx[NQ];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < NQ; ++q) {
         mx[q] = __uint_as_float(s[q][0]);
 #pragma unroll
         for (int e = 1; e < 31; e += 2)
           mx[q] = max3(mx[q], __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
         mx[q] = fmaxf(mx[q], __uint_as_float(s[q][31]));
       }
-      const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+      float top = SPLIT ? fmaxf(mx[0], mx[1]) : fmaxf(max3(mx[0], mx[1], mx[NQ - 2]), mx[NQ - 1]);
+      if constexpr (SPLIT) {
+        float other;
+        ok = meet(j - bt, top, &other);
+        if (!ok) break;
+        top = fmaxf(top, other);
+      }
       // (a row without a key so far has m = -inf: the difference is inf)
       const bool grow = top > m && !((top - m) * c <= 8.0f);
       if (C::AHEAD && j > bt) {   // P V of the tiles so far: O may change, and P
@@ -473,6 +505,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           l *= alpha;
 #pragma unroll
           for (int q = 0; q < DP / 32; ++q) {
+            if (SPLIT && (q & 1) != half) continue;
             uint32_t o[32];
             tmem_ld_32x32b_x32(o_col + q * 32, o);
             tmem_wait_ld_x32(o);
@@ -486,7 +519,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const float2 cc = make_float2(c, c), sh = make_float2(shift, shift);
       float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {   // the product may start on the first half
+      for (int q = 0; q < NQ / 2; ++q) {   // the product may start on the first half
         uint32_t p[32];
 #pragma unroll
         for (int e = 0; e < 32; ++e) {
@@ -502,10 +535,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         tmem_wait_st();
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(C::P_READY + 2 * t + q));
+        if (lane == 0) mbar_arrive(bar(C::P_READY + 2 * t + (SPLIT ? half : q)));
       }
       sum[0] = add2(sum[0], sum[1]);
       l += sum[0].x + sum[0].y;
+    }
+    if constexpr (SPLIT) {
+      float other = 0.0f;
+      ok = ok && meet(nk - bt, l, &other);
+      l = half ? other + l : l + other;   // (both threads the same sum)
     }
     if (SCORES && lim < 0) l = 0.0f;   // (a row without a key, whatever it has summed)
     if (ok && nk > 0) {
@@ -525,6 +563,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                        : args.lse + (int64_t)h * a.tokens_q + token;
 #pragma unroll
       for (int q = 0; q < DP / 32; ++q) {
+        if (SPLIT && (q & 1) != half) continue;
         uint32_t o[32];
         if (nk > 0) {   // (uniform over the warp)
           tmem_ld_32x32b_x32(o_col + q * 32, o);
@@ -560,10 +599,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           }
         }
       }
-      if (live && q_row_ok(a, token, h)) 
-        *lse = l == 0.0f ? -INFINITY
-               : CAPPED ? m * kLn2 + logf(l)
-                                      : m * a.scale + logf(l);
+      if (live && half == 0 && q_row_ok(a, token, h))
+        *lse = l == 0.0f ? -INFINITY : m * (CAPPED ? kLn2 : a.scale) + logf(l);
     }
   }
   __syncwarp();
