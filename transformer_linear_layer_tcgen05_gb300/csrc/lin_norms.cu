@@ -6,11 +6,11 @@ namespace lin {
 
 // (lin_norms_f16.cu, lin_norms_bf16.cu, lin_norms_f32.cu)
 extern template cudaError_t launch_block_norms_of<LIN_BINARY16>(const NormsArgs&, int, cudaStream_t);
-extern template cudaError_t launch_block_norms_bwd_of<LIN_BINARY16>(const NormsArgs&, int, int, cudaStream_t);
+extern template cudaError_t launch_block_norms_bwd_of<LIN_BINARY16>(const NormsArgs&, int, cudaStream_t);
 extern template cudaError_t launch_block_norms_of<LIN_BFLOAT16>(const NormsArgs&, int, cudaStream_t);
-extern template cudaError_t launch_block_norms_bwd_of<LIN_BFLOAT16>(const NormsArgs&, int, int, cudaStream_t);
+extern template cudaError_t launch_block_norms_bwd_of<LIN_BFLOAT16>(const NormsArgs&, int, cudaStream_t);
 extern template cudaError_t launch_block_norms_of<LIN_BINARY32>(const NormsArgs&, int, cudaStream_t);
-extern template cudaError_t launch_block_norms_bwd_of<LIN_BINARY32>(const NormsArgs&, int, int, cudaStream_t);
+extern template cudaError_t launch_block_norms_bwd_of<LIN_BINARY32>(const NormsArgs&, int, cudaStream_t);
 
 // The sums over the CTAs' partial rows: a CTA per 32 columns and kind, its 32
 // warps each a share of the rows, then a fixed-order sum over the warps.
@@ -53,14 +53,11 @@ cudaError_t launch_block_norms(const NormsArgs& a, int sms, cudaStream_t stream)
   return with_type(a.dtype, [&](auto t) { return launch_block_norms_of<decltype(t)::value>(a, sms, stream); });
 }
 
-int block_norms_bwd_ctas(const NormsArgs& a, int sms) {
-  const NormShape s = bwd_shape(a, sms);
-  return (int)std::min<int64_t>((a.tokens + s.teams - 1) / s.teams, sms);
-}
+int block_norms_bwd_ctas(const NormsArgs& a, int sms) { return bwd_shape(a, sms).ctas; }
 
 cudaError_t launch_block_norms_bwd(const NormsArgs& a, int sms, int ctas, cudaStream_t stream) {
   const cudaError_t e = with_type(a.dtype, [&](auto t) {
-    return launch_block_norms_bwd_of<decltype(t)::value>(a, sms, ctas, stream);
+    return launch_block_norms_bwd_of<decltype(t)::value>(a, sms, stream);
   });
   if (e != cudaSuccess || a.kinds == 0) return e;
   cudaLaunchAttribute attr[1];

@@ -437,38 +437,39 @@ namespace {
 
 // Units of four entries to a thread and warps of a team (small teams, so that
 // an SM has many rows in hand: what a row takes is the way of its sums), teams of
-// a CTA, and slots of each of them.
+// a CTA, slots of each of them, and CTAs.
 struct NormShape {
-  int v, warps, teams, slots;
+  int v, warps, teams, slots, ctas;
   size_t smem;
 };
 template <typename Bytes>
-inline NormShape norm_shape(int64_t tokens, int width, int sms, int ctas, size_t room,
-                            Bytes&& bytes_of_thread) {
+inline NormShape norm_shape(int64_t tokens, int width, int64_t ctas, size_t room, Bytes&& bytes_of_thread) {
   const int units = width / 4;
   NormShape s;
-  // as many units to a thread as leave every SM's sixteen warps rows of their own
+  // as many units to a thread as let all rows have warps of their own at once
   for (s.v = 1; s.v < 4; ++s.v)
-    if (tokens * ((units + 32 * s.v - 1) / (32 * s.v)) <= 16 * (int64_t)sms) break;
+    if (tokens * ((units + 32 * s.v - 1) / (32 * s.v)) <= kNormThreads / 32 * ctas) break;
   s.warps = (units + 32 * s.v - 1) / (32 * s.v);
   if (s.warps > kNormThreads / 32) s.warps = kNormThreads / 32;
   s.v = std::max(1, (units + 32 * s.warps - 1) / (32 * s.warps));
   // (a named barrier to each team of several warps; few rows: on many SMs)
   s.teams = std::min(std::max(1, kNormThreads / 32 / s.warps), s.warps > 1 ? 15 : 16);
   s.teams = (int)std::min<int64_t>(s.teams, std::max<int64_t>(1, (tokens + ctas - 1) / ctas));
+  s.ctas = (int)std::min<int64_t>((tokens + s.teams - 1) / s.teams, ctas);
+  // slots: four, or what a team has rows and shared memory room for
   const size_t slot = (size_t)s.teams * s.warps * 32 * bytes_of_thread(s.v);
-  s.slots = slot * 4 <= room ? 4 : slot * 2 <= room ? 2 : 1;
+  const int64_t rows = (tokens + (int64_t)s.ctas * s.teams - 1) / ((int64_t)s.ctas * s.teams);
+  s.slots = rows > 2 && slot * 4 <= room ? 4 : rows > 1 && slot * 2 <= room ? 2 : 1;
   s.smem = slot * s.slots;
   return s;
 }
-inline NormShape fwd_shape(const NormsArgs& a, int sms) {
+inline NormShape fwd_shape(const NormsArgs& a, int sms) {   // (two CTAs an SM)
   const int b = a.dtype == LIN_BINARY32 ? 16 : 8;
-  return norm_shape(a.tokens, a.width, sms, 2 * sms, 112 * 1024,
-                    [&](int v) { return v * (16 + b); });   // (two CTAs an SM)
+  return norm_shape(a.tokens, a.width, 2 * (int64_t)sms, 112 * 1024, [&](int v) { return v * (16 + b); });
 }
 inline NormShape bwd_shape(const NormsArgs& a, int sms) {
   const int b = a.dtype == LIN_BINARY32 ? 16 : 8;
-  return norm_shape(a.tokens, a.width, sms, sms, 226 * 1024 - (size_t)a.width * 12,
+  return norm_shape(a.tokens, a.width, sms, 226 * 1024 - (size_t)a.width * 12,
                     [&](int v) { return v * (32 + 2 * b); });
 }
 
@@ -496,32 +497,36 @@ cudaError_t with_norm(int v, int kind, F&& f) {
   }
 }
 
+// Leave for more shared memory than a launch may have without.
+template <typename Kernel>
+cudaError_t more_shared(Kernel kernel, size_t bytes) {
+  if (bytes + 1024 <= 48 * 1024) return cudaSuccess;
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
 template <int T>
 cudaError_t launch_block_norms_of(const NormsArgs& a, int sms, cudaStream_t stream) {
   const NormShape s = fwd_shape(a, sms);
-  const unsigned ctas = (unsigned)std::min<int64_t>((a.tokens + s.teams - 1) / s.teams, 2 * (int64_t)sms);
   const int kind = a.y && a.n && a.h ? (a.w_post ? 4 : 0) + a.form : -1;
   return with_norm<T>(s.v, kind, [&](auto v, auto k) {
     auto kernel = lin_block_norms_kernel<T, decltype(v)::value, decltype(k)::value>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)s.smem);
+    const cudaError_t e = more_shared(kernel, s.smem);
     if (e != cudaSuccess) return e;
-    kernel<<<ctas, s.teams * s.warps * 32, s.smem, stream>>>(a, s.warps, s.slots);
+    kernel<<<s.ctas, s.teams * s.warps * 32, s.smem, stream>>>(a, s.warps, s.slots);
     return cudaGetLastError();
   });
 }
 
 template <int T>
-cudaError_t launch_block_norms_bwd_of(const NormsArgs& a, int sms, int ctas, cudaStream_t stream) {
+cudaError_t launch_block_norms_bwd_of(const NormsArgs& a, int sms, cudaStream_t stream) {
   const NormShape s = bwd_shape(a, sms);
   const int kind = a.y && a.dn && a.dh ? (a.w_post ? 4 : 0) + a.form : -1;
   return with_norm<T>(s.v, kind, [&](auto v, auto k) {
     auto kernel = lin_block_norms_bwd_kernel<T, decltype(v)::value, decltype(k)::value>;
     const size_t smem = (size_t)a.width * 12 + s.smem;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = more_shared(kernel, smem);
     if (e != cudaSuccess) return e;
-    kernel<<<(unsigned)ctas, s.teams * s.warps * 32, smem, stream>>>(a, s.warps, s.slots);
+    kernel<<<s.ctas, s.teams * s.warps * 32, smem, stream>>>(a, s.warps, s.slots);
     return cudaGetLastError();
   });
 }

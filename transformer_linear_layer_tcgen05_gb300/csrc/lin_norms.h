@@ -39,6 +39,6 @@ cudaError_t launch_block_norms_bwd(const NormsArgs& a, int sms, int ctas, cudaSt
 template <int T>
 cudaError_t launch_block_norms_of(const NormsArgs& a, int sms, cudaStream_t stream);
 template <int T>
-cudaError_t launch_block_norms_bwd_of(const NormsArgs& a, int sms, int ctas, cudaStream_t stream);
+cudaError_t launch_block_norms_bwd_of(const NormsArgs& a, int sms, cudaStream_t stream);
 
 }  // namespace lin

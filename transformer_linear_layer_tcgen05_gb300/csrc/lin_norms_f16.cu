@@ -3,5 +3,5 @@
 
 namespace lin {
 template cudaError_t launch_block_norms_of<LIN_BINARY16>(const NormsArgs&, int, cudaStream_t);
-template cudaError_t launch_block_norms_bwd_of<LIN_BINARY16>(const NormsArgs&, int, int, cudaStream_t);
+template cudaError_t launch_block_norms_bwd_of<LIN_BINARY16>(const NormsArgs&, int, cudaStream_t);
 }  // namespace lin
