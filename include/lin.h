@@ -437,11 +437,13 @@ lin_status lin_attention_backward(const lin_attention_shape *shape, const lin_he
  * rows as Q's, keys counted from the sequence's first; held to the sequence. A
  * form without cap, slopes and ranges (or NULL) is lin_attention itself. LSE,
  * O and the gradients are those of S; a row whose range is empty is one that
- * the mask leaves nothing. The backward form's dS has 1 - (y / cap)^2 as a
- * factor. Tiles of keys that no row of a tile of queries sees are not computed. Workspace (backward, ranges): 8 bytes more for each tile of
- * 128 rows of queries. A capped score is off by at most cap 2^-20. cap >= 0 and
- * finite, else LIN_ERROR_INVALID_VALUE; up to 4096, with scale / cap below
- * float32's end, else LIN_ERROR_UNSUPPORTED_SHAPE; all else as for
+ * the mask leaves nothing, and may hold anything in Q and DO; a key that no
+ * query sees takes part (finite K and V). The backward form's dS has
+ * 1 - (y / cap)^2 as a factor. Tiles of keys that no row of a tile of queries
+ * sees are not computed. Workspace (backward, ranges): 8 bytes more for each
+ * tile of 128 rows of queries. A capped score is off by at most cap 2^-20. cap
+ * >= 0 and finite, else LIN_ERROR_INVALID_VALUE; 0 or 2^-20 to 4096, with scale
+ * / cap below float32's end, else LIN_ERROR_UNSUPPORTED_SHAPE; all else as for
  * lin_attention.
  */
 typedef struct lin_score_form {

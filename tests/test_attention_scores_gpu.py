@@ -260,6 +260,36 @@ def test_small_and_large_caps(cap):
     _check(t, lens, True, 0.2, form, UNIT["float16"])
 
 
+@pytest.mark.parametrize("kind", ["cap", "bias", "cap bias", "ranges"])
+def test_pairs_that_the_mask_parts_and_whose_products_are_not_finite(kind):
+    # two documents in a tile: large V and small dO in one, the other way in the
+    # other, so that dO V is infinite between them, and finite in each
+    import torch
+    lens = [(100, 100)]
+    first = torch.tensor([0] * 40 + [40] * 60, dtype=torch.int32, device="cuda")
+    end = torch.tensor([40] * 40 + [100] * 60, dtype=torch.int32, device="cuda")
+    form = dict(_form(kind, lens, 2, seed=17), first_key=first, end_key=end)
+    for causal in (False, True):
+        t = _setup("bfloat16", lens, 2, 1, 64, seed=17)
+        _run(t, lens, causal, 0.2, form)
+        want = {k: t[k].clone() for k in ("o", "dq", "dk", "dv")}
+        t["v"][:40] *= 2.0 ** 75
+        t["do"][:40] *= 2.0 ** -75
+        t["v"][40:] *= 2.0 ** -60
+        t["do"][40:] *= 2.0 ** 60
+        _run(t, lens, causal, 0.2, form)
+        # (powers of two: dO V, dS, dQ and dK of each document are what they were,
+        # but that dK's tile scales by its largest dO, 2^60 of the second document:
+        # in bfloat16, whose exponents are float32's, the first one's dS and sums
+        # of 2^-135 or more of them would have to stay above 2^-126)
+        for k in ("dq", "dk"):
+            assert torch.isfinite(t[k]).all(), k
+            assert torch.equal(t[k][40:], want[k][40:]), k
+        assert torch.equal(t["dq"], want["dq"])
+        assert torch.equal(t["o"][:40] * 2.0 ** -75, want["o"][:40])
+        assert torch.equal(t["dv"][40:] * 2.0 ** -60, want["dv"][40:])
+
+
 def test_no_row_sees_anything():
     import torch
     for lens in ([(200, 300)], [(3, 2000)]):

@@ -247,9 +247,10 @@ def _scores(L, backward=False, scale=1.0, **form):
 def test_scores_numbers(L, backward):
     for cap in (-1.0, float("nan"), float("inf"), float("-inf")):
         assert _scores(L, backward, cap=cap) == INVALID
-    for cap, scale in ((4097.0, 1.0), (1e30, 1.0), (1e-38, 10.0)):
+    for cap, scale in ((4097.0, 1.0), (1e30, 1.0), (1e-38, 10.0), (2.0 ** -21, 1.0), (1e-38, 1e-38)):
         assert _scores(L, backward, scale=scale, cap=cap) == SHAPE
-    assert _scores(L, backward, cap=4096.0) != SHAPE
+    for cap in (2.0 ** -20, 4096.0):
+        assert _scores(L, backward, cap=cap) != SHAPE
     assert _scores(L, backward, scale=0.0, cap=1.0) == INVALID
     f = L.lin_attention_scores_backward if backward else L.lin_attention_scores
     assert f(None, None, *[None] * (10 if backward else 6)) == INVALID

@@ -130,11 +130,13 @@ lin_status check_form(const lin_score_form* f, const lin_attention_shape* s, con
   return LIN_SUCCESS;
 }
 // Its numbers, checked before anything touches CUDA. A capped score is off by up
-// to cap 2^-20: beyond caps of 4096 by more than P's rounding to bfloat16.
+// to cap 2^-20: beyond caps of 4096 by more than P's rounding to bfloat16. Below
+// 2^-20 there is nothing left of a score, and hidden ones could not be told by
+// a value of r.
 lin_status check_cap(const lin_score_form* f, const lin_attention_shape* s) {
   if (!f) return LIN_SUCCESS;
   if (!(f->cap >= 0.0f) || std::isinf(f->cap)) return LIN_ERROR_INVALID_VALUE;
-  if (f->cap > 4096.0f) return LIN_ERROR_UNSUPPORTED_SHAPE;
+  if (f->cap > 4096.0f || (f->cap > 0.0f && f->cap < 0x1p-20f)) return LIN_ERROR_UNSUPPORTED_SHAPE;
   if (s && f->cap > 0.0f && !std::isfinite(4.0f * s->scale / f->cap)) return LIN_ERROR_UNSUPPORTED_SHAPE;
   return LIN_SUCCESS;
 }

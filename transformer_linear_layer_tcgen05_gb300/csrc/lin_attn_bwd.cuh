@@ -1125,8 +1125,9 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
               p[q][e + 1] = __float_as_uint(x.y);
             }
         }
-        // what leaves no probability, whatever else is added
-        const uint32_t out = __float_as_uint(CAPPED ? 1e30f : -3e38f);
+        // what leaves no probability, whatever else is added (of a cap's r: -2^80
+        // at its smallest, times a slope of -0)
+        const uint32_t out = __float_as_uint(CAPPED ? 1e30f : -INFINITY);
         auto leave_out = [&](const int* rows, auto outside) {
           const int4* at = reinterpret_cast<const int4*>(rows);
 #pragma unroll
@@ -1238,7 +1239,7 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
         for (int q = 0; q < NQ; ++q)
 #pragma unroll
           for (int e = 0; e < 32; ++e)
-            if (p[q][e] == 0u) d[q][e] = 0u;
+            if (__uint_as_float(p[q][e]) == 0.0f) d[q][e] = 0u;   // (of either sign: see `out`)
       } else if (cut) {
 #pragma unroll
         for (int q = 0; q < NQ; ++q)

@@ -479,7 +479,7 @@ def lin_attention_scores(Q, K, V, O, LSE, cap=None, slopes=None, first_key=None,
     """lin_attention with a form of the scores: S = cap tanh(scale Q K^T / cap)
     - slopes |distance| over each query's own range of keys.
 
-    ``cap`` a number up to 4096 (None: no cap); ``slopes`` float32 [heads], constants;
+    ``cap`` a number of 2^-20 to 4096 (None: no cap); ``slopes`` float32 [heads], constants;
     ``first_key``, ``end_key`` int32 [tokens]: the first key that a query sees
     and the one behind its last, counted in its sequence, held to it, and, with
     ``causal``, to the causal mask (a document's keys, a prefix, a window; an
