@@ -109,8 +109,8 @@
  * TMA coordinate alignment, cluster peer rank, and every global index that
  * is not a TMA access (partial tiles, row partials, transform and loss
  * loads; rows, heads, parts and row statistics of attention; heads and angles
- * of the norms and rotation; units and entries of distillation) against its
- * buffer. Attention's tensor memory columns and copies' innermost coordinates
+ * of the norms and rotation; units and entries of distillation and of the norms
+ * around a block; blocks of AdamW's tensors) against its buffer. Attention's tensor memory columns and copies' innermost coordinates
  * are constants, checked at compile time or multiples of 64 entries. A failed
  * check skips the access and records
  * LIN_ERROR_DEVICE_CHECK with the site and the offending value (a skipped
@@ -710,9 +710,9 @@ int lin_last_cuda_error(void);
 /* What the last compute call made on the calling thread enqueued: the number
  * of kernels it launched (the GEMM, plus the binary16 pre-pass of X and the
  * split-tail sum where those run, plus the loss kernels of the lm_head form,
- * or the kernels of attention, norms and rotation, and distillation; all
- * blocks' kernels for a host-operand form; 0 if it enqueued none or
- * failed) and the workspace bytes it took from the library's pool. Either
+ * or the kernels of attention, norms and rotation, norms around a block,
+ * distillation and AdamW; all blocks' kernels for a host-operand form; 0 if it
+ * enqueued none or failed) and the workspace bytes it took from the library's pool. Either
  * pointer may be NULL. */
 void lin_last_launch_info(int* kernels, uint64_t* workspace_bytes);
 

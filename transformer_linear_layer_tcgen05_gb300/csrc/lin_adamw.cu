@@ -13,7 +13,10 @@
 // Bound by memory: 28 bytes an entry (f32), 16 (8 bits), 2 more for the copy.
 // A warp takes a block of 256 entries at a time, eight to a lane: the 32-byte
 // accesses of a lane use whole sectors, and the block's largest entries are a
-// shuffle tree, so the codes never leave registers before they are final. The
+// shuffle tree, so the codes never leave registers before they are final. 520
+// million entries, 8 bits and copies, 1495 us, 6.3 TB/s of a copy's 6.8; 12.4
+// million, f32 and copies, 62 us, 6.0 TB/s. Four CTAs an SM: with 3, 5, 6 and 8
+// the first of these takes 1600, 1583, 1743 and 2429 us. The
 // tensors' addresses are parameters of the launch: no table in memory, nothing
 // to copy ahead of it, and a captured launch carries its own.
 //

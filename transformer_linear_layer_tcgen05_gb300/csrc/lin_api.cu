@@ -1185,6 +1185,8 @@ lin_status lin_selftest_wait_timeout(int64_t timeout_us, lin_stream_t stream) {
 }
 
 // 0.3.0: attention, norms and rotation of the heads, distillation
-int lin_version(void) { return 300; }
+// 0.4.0: attention with a form of the scores, norms around a block, rotation by
+// axes, AdamW
+int lin_version(void) { return 400; }
 
 }  // extern "C"

@@ -13,9 +13,13 @@
 //
 // Bound by memory: a row's entries stay in registers from its first sum to its
 // results, so each tensor is read or written once. A team of warps has a row,
-// V units of four entries to a thread. The gradient's threads copy the units of
-// their next rows into shared memory of their own meanwhile (nobody else's: a
-// copy's end is all that its reader waits for).
+// V units of four entries to a thread. The threads copy the units of their next
+// rows into shared memory of their own meanwhile (nobody else's: a copy's end is
+// all that its reader waits for). In TB/s, a copy at 6.8, f32 and bfloat16:
+// 16384 x 2048 forward 5.8 and 5.7, gradient 6.0 and 5.7 (without the copies
+// 4.4); 4096 x 8192 6.2 and 5.1, 4.6 and 4.1 (a row takes a whole CTA, and the
+// gradient's shared memory holds one). Short calls are launches: 512 x 768 in
+// 3.0 us.
 //
 // KIND: what a call has, the compiler's parameter (asked for in the loops, each
 // question ends a run of independent instructions): 4 a norm of the block's
