@@ -290,6 +290,32 @@ def test_pairs_that_the_mask_parts_and_whose_products_are_not_finite(kind):
         assert torch.equal(t["dv"][40:] * 2.0 ** -60, want["dv"][40:])
 
 
+@pytest.mark.parametrize("d, heads", [(64, (2, 1)), (64, (36, 18)), (128, (33, 11))])
+@pytest.mark.parametrize("kind", ["cap", "cap bias", "bias"])
+def test_what_the_mask_hides_does_not_show(kind, d, heads):
+    # one document's queries, keys and values changed: the others' results are
+    # the same bits (scores of a cap are computed four at a time)
+    import torch
+    lens = [(390, 390)]
+    at = torch.arange(390, dtype=torch.int32, device="cuda")
+    cuts = torch.tensor([0, 61, 130, 199, 390], dtype=torch.int32, device="cuda")
+    doc = torch.searchsorted(cuts, at, right=True)
+    form = dict(_form(kind, lens, heads[0], seed=18), first_key=cuts[doc - 1].contiguous(),
+                end_key=cuts[doc].contiguous())
+    t = _setup("float16", lens, *heads, d, seed=18, gain=3.0)
+    rest = torch.cat([at[:130], at[199:]]).long()
+    want = None
+    for gain in (1.0, 7.0, 0.0):
+        for name in ("q", "k", "v"):
+            t[name][130:199] = gain * t[name][130:199].flip(0)
+        _run(t, lens, True, d ** -0.5, form)
+        got = {k: t[k][rest].clone() for k in ("o", "dq", "dk", "dv")}
+        got["lse"] = t["lse"][:, rest].clone()
+        want = want or got
+        for k in want:
+            assert torch.equal(got[k], want[k]), (k, gain)
+
+
 def test_no_row_sees_anything():
     import torch
     for lens in ([(200, 300)], [(3, 2000)]):

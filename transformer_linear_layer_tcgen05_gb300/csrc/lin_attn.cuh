@@ -255,6 +255,12 @@ __device__ __forceinline__ KeyRange join_extents(const int* e, int n) {
   return r;
 }
 
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // The scores' form in base-2 units, two scores at a time. With u = scale s /
 // cap and r = 1 / (1 + e^2u): tanh u = 1 - 2 r, which neither over- nor
 // underflows to anything but its limits, and its derivative is 4 r (1 - r). So
@@ -270,25 +276,47 @@ struct ScoreTurn {
     const float a = 2.0f * kLog2E * scale / f.cap;
     arg = make_float2(a, a);
   }
-  // r of two scores
+  // r of two products q k
   __device__ __forceinline__ float2 rest(float2 s) const {
     const float2 x = mul2(s, arg);
     const float2 e = add2(make_float2(ex2_approx(x.x), ex2_approx(x.y)), make_float2(1.0f, 1.0f));
     return make_float2(rcp_approx(e.x), rcp_approx(e.y));
   }
-  // The capped scores themselves: by r, or, where |u| <= 3/4, as u times a
-  // polynomial of u^2, which spares two of the three turns of the
-  // special-function unit that a score takes (the unit's reciprocals take twice
-  // its exponentials' time).
-  __device__ __forceinline__ float2 by_rest(float2 s) const {
-    return fma2(rest(s), make_float2(-twice, -twice), make_float2(top, top));
+  // r of four products q k by one reciprocal, which takes the special-function
+  // unit twice an exponential's time: that of the product of the four 1 + e^2u,
+  // each held to 2^30 (what is beyond is nothing beside the scores' error; a NaN
+  // stays one, of all four). 8192 tokens, no score below 3/4 of the cap: forward
+  // 748 -> 605 us; the dQ kernel of 16 heads 393 -> 368 (in the other one, where
+  // hidden queries would have to be cleared first, 450 -> 472: it takes two at a
+  // time).
+  __device__ __forceinline__ void rest4(uint32_t* s) const {
+    auto up = [&](int k) {
+      const float2 x = mul2(make_float2(__uint_as_float(s[k]), __uint_as_float(s[k + 1])), arg);
+      return add2(make_float2(ex2_approx(min_nan(x.x, 30.0f)), ex2_approx(min_nan(x.y, 30.0f))),
+                  make_float2(1.0f, 1.0f));
+    };
+    const float2 e = up(0), f = up(2), p = mul2(e, f);
+    const float r = rcp_approx(p.x * p.y);
+    const float2 q = mul2(make_float2(r, r), make_float2(p.y, p.x)), a = mul2(q, f), b = mul2(q, e);
+    s[0] = __float_as_uint(a.x);
+    s[1] = __float_as_uint(a.y);
+    s[2] = __float_as_uint(b.x);
+    s[3] = __float_as_uint(b.y);
   }
-  static __device__ __forceinline__ float2 by_terms(const ScoreForm& f, float2 s) {
-    const float2 u = mul2(s, f.unit), w = mul2(u, u);
-    float2 p = f.terms[kTanhTerms - 1];
+  __device__ __forceinline__ float2 score(float2 r) const {
+    return fma2(r, make_float2(-twice, -twice), make_float2(top, top));
+  }
+  // The capped scores themselves without the special-function unit, where the
+  // products are small beside the cap: s times a polynomial of s^2, of three
+  // terms up to 3/10 of it and of five up to 3/4 (8192 tokens at a cap of 50:
+  // 480 us, five terms alone 585, none 605).
+  template <int N>
+  static __device__ __forceinline__ float2 by_terms(const float2 (&c)[N], float2 s) {
+    const float2 w = mul2(s, s);
+    float2 p = c[N - 1];
 #pragma unroll
-    for (int k = kTanhTerms - 2; k >= 0; --k) p = fma2(p, w, f.terms[k]);
-    return mul2(u, p);
+    for (int k = N - 2; k >= 0; --k) p = fma2(p, w, c[k]);
+    return mul2(s, p);
   }
   // p times the cap's derivative, from r
   static __device__ __forceinline__ float2 times_slope(float2 p, float2 r) {

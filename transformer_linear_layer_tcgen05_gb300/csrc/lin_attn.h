@@ -27,15 +27,17 @@ struct AttnArgs {
 // A form of the scores: z = cap tanh(scale s / cap) - slope |distance| (cap 0:
 // scale s; slopes null: no bias), and the keys first .. end - 1 of a query,
 // counted in its sequence (null: from the first, to the last).
-constexpr int kTanhTerms = 5;
+constexpr int kTanhTerms = 5, kFewTerms = 3;
 constexpr int kNoForm = -1, kCap = 1, kBias = 2;   // (forms of ranges alone: 0)
 struct ScoreForm {
   float cap;
   const float* slopes;             // [heads_q]
   const int32_t *first, *end;      // [tokens_q]
-  // (a cap, forward) scale / cap, and cap log2 e times the terms of tanh's
-  // polynomial, twice each, for two scores at a time
-  float2 unit, terms[kTanhTerms];
+  // (a cap, forward) tanh's polynomials of few and of more terms as those of
+  // products q k in z log2 e, twice each, for two at a time, and how large a
+  // product they take (below zero: none)
+  float few_up_to, up_to;
+  float2 few[kFewTerms], terms[kTanhTerms];
 };
 
 struct AttnFwdArgs {

@@ -159,16 +159,22 @@ lin::ScoreForm score_form(const lin_score_form* f, float scale) {
   s.first = f->first_key;
   s.end = f->end_key;
   if (!(f->cap > 0.0f)) return s;
-  // tanh(u) / u by u^2 in [0, 9/16]: the polynomial of degree four whose largest
-  // relative error is least (5.7e-7; fitted by reweighted least squares)
+  // tanh(u) / u by u^2, up to |u| = 3/10 and 3/4: the polynomials whose largest
+  // relative error is least (1.2e-6 and 5.7e-7, so 2^-21 of the cap; fitted by
+  // reweighted least squares)
+  const double few[lin::kFewTerms] = {0.999998839, -0.333100217, 0.12633946};
   const double t[lin::kTanhTerms] = {0.999999435, -0.333282516, 0.132589833, -0.0500563041,
                                      0.0129296326};
-  const float unit = (float)((double)scale / f->cap);
-  s.unit = make_float2(unit, unit);
-  for (int i = 0; i < lin::kTanhTerms; ++i) {
-    const float c = (float)(t[i] * f->cap * 1.4426950408889634);
+  const double unit = (double)scale / f->cap, full = f->cap * 1.4426950408889634;
+  double power = unit * full;
+  for (int i = 0; i < lin::kTanhTerms; ++i, power *= unit * unit) {
+    const float c = (float)(t[i] * power), d = (float)(i < lin::kFewTerms ? few[i] * power : 0.0);
     s.terms[i] = make_float2(c, c);
+    if (i < lin::kFewTerms) s.few[i] = make_float2(d, d);
   }
+  // (the last terms of the smallest units would leave float32's normal numbers)
+  s.few_up_to = std::fabs(s.few[lin::kFewTerms - 1].x) >= 0x1p-120f ? (float)(0.3 / unit) : -1.0f;
+  s.up_to = std::fabs(s.terms[lin::kTanhTerms - 1].x) >= 0x1p-120f ? (float)(0.75 / unit) : -1.0f;
   return s;
 }
 

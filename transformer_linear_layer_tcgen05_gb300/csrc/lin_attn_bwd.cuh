@@ -478,6 +478,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     bool ok = true;
     for (int j = half; j < n; j += 2) {   // the warpgroup's stream
       const int u = (j >> 1) & 1;
+      // (of the row's keys in this tile; what a branch goes by is at hand when S comes)
+      const int last_j = lim - (j0 + j) * kTurn, first_j = low - (j0 + j) * kTurn;
+      const bool cut = CAPPED && __any_sync(0xffffffffu, last_j < kTurn - 1 || first_j > 0);
       ok = warp_attn_wait(bar(C::S_FULL + half), u, ctl);
       if (!ok) break;
       tc_fence_after_sync();
@@ -538,16 +541,29 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
         return true;
       };
       if constexpr (SCORES) {
-        // P times the cap's derivative, from the scores, or (RESTS) from the r
-        // that delta's sum has left in their place
-        auto probabilities = [&](auto rests) {
+        // r of the scores (hidden ones zeroed: four share a reciprocal, and a row's
+        // results do not go by what its mask hides), and from it P times the
+        // cap's derivative
+        auto rests = [&] {
+          if (cut) {
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int e = 0; e < 32; ++e)
+                if (q * 32 + e > last_j || q * 32 + e < first_j) p[q][e] = 0u;
+          }
+#pragma unroll
+          for (int q = 0; q < 2; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) turned.rest4(&p[q][e]);
+        };
+        auto probabilities = [&] {
 #pragma unroll
           for (int q = 0; q < 2; ++q) {
             float2 far = make_float2(here - (float)(q * 32), here - (float)(q * 32 + 1));
 #pragma unroll
             for (int e = 0; e < 32; e += 2) {
-              float2 r = make_float2(__uint_as_float(p[q][e]), __uint_as_float(p[q][e + 1]));
-              if (CAPPED && !decltype(rests)::value) r = turned.rest(r);
+              const float2 r = make_float2(__uint_as_float(p[q][e]), __uint_as_float(p[q][e + 1]));
               float2 x = probability(r, far);
               if constexpr (BIASED) far = add2(far, make_float2(-2.0f, -2.0f));
               if constexpr (CAPPED) x = ScoreTurn::times_slope(x, r);
@@ -556,23 +572,13 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
           }
         };
+        if constexpr (CAPPED) rests();
         if (few) {
-          if constexpr (CAPPED) {
-#pragma unroll
-            for (int q = 0; q < 2; ++q)
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const float2 x =
-                    turned.rest(make_float2(__uint_as_float(p[q][e]), __uint_as_float(p[q][e + 1])));
-                p[q][e] = __float_as_uint(x.x);
-                p[q][e + 1] = __float_as_uint(x.y);
-              }
-          }
           ok = take_dp() && sum_delta();
           if (!ok) break;
-          probabilities(std::true_type{});
+          probabilities();
         } else {
-          probabilities(std::false_type{});
+          probabilities();
           ok = take_dp();
           if (!ok) break;
         }
