@@ -408,11 +408,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (q * 32 + e > lim_j || q * 32 + e < low_j) s[q][e] = value;
         };
         if constexpr (CAPPED) {
-          // Group by group of 32 keys; those that no row of the warp sees are left as
-          // they are, and hidden ones of the others zeroed. The way goes by the
-          // row's own largest score of the group: what a row's results are does
-          // not go by other rows, nor by what the mask hides. (NaN is passed over:
-          // each way gives NaN.)
+          // Where the mask cuts the tile, by groups of 32 keys: those that no row of
+          // the warp sees are left as they are, and hidden ones of the others
+          // zeroed. The way goes by the row's own largest score of the group or the
+          // tile: a row's results do not go by what other rows hold, nor by what the
+          // mask hides. (NaN is passed over: each way gives NaN.)
           auto two = [&](int q, int e) -> float2 {
             return make_float2(__uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
           };

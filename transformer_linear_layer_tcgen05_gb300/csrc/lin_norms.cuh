@@ -19,7 +19,7 @@
 // 16384 x 2048 forward 5.8 and 5.7, gradient 6.0 and 5.7 (without the copies
 // 4.4); 4096 x 8192 6.2 and 5.1, 4.6 and 4.1 (a row takes a whole CTA, and the
 // gradient's shared memory holds one). Short calls are launches: 512 x 768 in
-// 3.0 us.
+// 3.0-3.3 us.
 //
 // KIND: what a call has, the compiler's parameter (asked for in the loops, each
 // question ends a run of independent instructions): 4 a norm of the block's
