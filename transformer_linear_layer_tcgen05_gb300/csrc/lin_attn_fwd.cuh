@@ -276,21 +276,30 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                                  k_desc + s * AttnTile<DP>::UNITS);
           umma_commit(bar(C::S_FULL + t));
         };
+        // A tile's first scores: its queries' copy is waited for here, once for
+        // each tile that has keys, wherever among the key tiles it begins (copies
+        // complete in no order, so no other wait stands for this one).
+        auto first_scores = [&](int t, int s) -> bool {
+          if (!attn_wait(bar(C::Q_FULL + t), 0, ctl)) return false;
+          scores(t, s);
+          return true;
+        };
         bool ok = attn_wait(bar(C::K_FULL), 0, ctl);
-        for (int t = 0; t < 2 && ok; ++t) {
-          if ((t ? n1 : n0) == 0 || (t ? b1 : b0) > 0) continue;
-          ok = attn_wait(bar(C::Q_FULL + t), 0, ctl);
-          if (ok) scores(t, 0);
-        }
+        for (int t = 0; t < 2 && ok; ++t)
+          if ((t ? n1 : n0) > 0 && (t ? b1 : b0) == 0) ok = first_scores(t, 0);
         if (ok) umma_commit(bar(C::K_EMPTY));
         int s = 0, s1 = 1 % C::NKV;           // stages of tiles j and j + 1
         uint32_t round = 0, round1 = C::NKV == 1;
         for (int j = 0; j < n && ok; ++j) {
           if (j + 1 < n) ok = attn_wait(bar(C::K_FULL + s1), round1 & 1, ctl);
           if (C::AHEAD && ok && j + 1 < n0 && j + 1 >= b0) {
-            if (j >= b0) ok = attn_wait(bar(C::S_TAKEN), (j - b0) & 1, ctl);
-            tc_fence_after_sync();
-            if (ok) scores(0, s1);
+            if (j < b0) {
+              ok = first_scores(0, s1);
+            } else {
+              ok = attn_wait(bar(C::S_TAKEN), (j - b0) & 1, ctl);
+              tc_fence_after_sync();
+              if (ok) scores(0, s1);
+            }
           }
           ok = ok && attn_wait(bar(C::V_FULL + s), round & 1, ctl);
           if (ok && j + 1 == n && v_left < 128) ok = attn_wait(bar(C::TAIL), 0, ctl);
@@ -299,7 +308,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             const int nt = t ? n1 : n0, bt = t ? b1 : b0;
             if (j >= nt || !ok) continue;
             if (j < bt) {   // (its first scores; ahead, the first tile's are out already)
-              if (j + 1 == bt && (!C::AHEAD || t == 1)) scores(t, s1);
+              if (j + 1 == bt && (!C::AHEAD || t == 1)) ok = first_scores(t, s1);
               continue;
             }
             if (C::AHEAD && t == 1 && j + 1 < nt) {
