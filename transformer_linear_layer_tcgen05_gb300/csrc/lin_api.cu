@@ -177,8 +177,12 @@ lin_status check_buffer(const void* p, uint64_t bytes, int dev, SeenRange* seen)
   if (a.device != dev) return LIN_ERROR_INVALID_VALUE;
   CUdeviceptr base = 0;
   size_t size = 0;
-  if (driver().range(&base, &size, reinterpret_cast<CUdeviceptr>(p)) != CUDA_SUCCESS)
-    return LIN_ERROR_INVALID_VALUE;
+  CUresult r = driver().range(&base, &size, reinterpret_cast<CUdeviceptr>(p));
+  // (a host thread whose first CUDA call this is has no context yet, which the
+  // driver's query asks for and the runtime's queries before it do not make)
+  if (r == CUDA_ERROR_INVALID_CONTEXT && cudaSetDevice(dev) == cudaSuccess)
+    r = driver().range(&base, &size, reinterpret_cast<CUdeviceptr>(p));
+  if (r != CUDA_SUCCESS) return LIN_ERROR_INVALID_VALUE;
   const uint64_t off = at - base;
   if (off > size || bytes > size - off) return LIN_ERROR_INVALID_VALUE;
   if (seen) *seen = SeenRange{(uint64_t)base, (uint64_t)base + size};
