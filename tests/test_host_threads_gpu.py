@@ -1,4 +1,5 @@
-"""Calls from several host threads."""
+"""Calls from several host threads: a thread's first call, and one kernel with
+calls of different sizes at once, whose launches want different shared memory."""
 
 import threading
 
@@ -57,3 +58,61 @@ def test_a_threads_first_call(name):
     torch.cuda.synchronize()
     assert not errors
     assert lin.lin_get_device_status() == lin.LIN_SUCCESS
+
+
+def _at_once(calls, times=1500):
+    """Each call `times` times in a host thread of its own; their errors."""
+    import torch
+    errors, start = [], threading.Barrier(len(calls))
+
+    def loop(call):
+        stream = torch.cuda.Stream()
+        start.wait()
+        try:
+            for _ in range(times):
+                call(stream)
+        except Exception as e:   # (told by the thread that joins)
+            errors.append(e)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=loop, args=(c,)) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert lin.lin_get_device_status() == lin.LIN_SUCCESS
+    return errors
+
+
+@pytest.mark.parametrize("gradient", [False, True])
+def test_block_norms(gradient):
+    # (width 2048, bfloat16: 48 and 96 KB forward, 120 and 216 KB of the gradient)
+    import torch
+    width = 2048
+    weights = torch.ones(width, device="cuda"), torch.ones(width, device="cuda")
+    calls, results = [], []
+    for tokens in (600, 1024) if gradient else (1024, 2048):
+        x = torch.randn(tokens, width, device="cuda")
+        y = x.flip(0).bfloat16()
+        h, n = torch.empty_like(x), torch.empty_like(y)
+        out = [torch.empty_like(t) for t in (x, y, weights[0], weights[1])]
+
+        def call(stream, x=x, y=y, h=h, n=n, out=out):
+            if gradient:
+                lin.lin_block_norms_backward(x, y, None, *weights, h, n, out[0], out[1], None,
+                                             out[2], out[3], stream=stream)
+            else:
+                lin.lin_block_norms(x, y, None, *weights, h, n, stream=stream)
+
+        h.copy_(x.flip(1)), n.copy_(y.flip(1))
+        calls.append(call)
+        results.append(out if gradient else [h, n])
+    torch.cuda.synchronize()
+    for c in calls:
+        c(None)
+    torch.cuda.synchronize()
+    want = [[t.clone() for t in r] for r in results]
+    assert not _at_once(calls)
+    for r, w in zip(results, want):
+        assert all(torch.equal(a, b) for a, b in zip(r, w))

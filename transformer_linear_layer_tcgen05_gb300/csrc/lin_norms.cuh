@@ -467,13 +467,15 @@ inline NormShape norm_shape(int64_t tokens, int width, int64_t ctas, size_t room
   s.smem = slot * s.slots;
   return s;
 }
+// Shared memory that a CTA may have of a launch's own.
+constexpr size_t kNormFwdShared = 112 * 1024, kNormBwdShared = 226 * 1024;
 inline NormShape fwd_shape(const NormsArgs& a, int sms) {   // (two CTAs an SM)
   const int b = a.dtype == LIN_BINARY32 ? 16 : 8;
-  return norm_shape(a.tokens, a.width, 2 * (int64_t)sms, 112 * 1024, [&](int v) { return v * (16 + b); });
+  return norm_shape(a.tokens, a.width, 2 * (int64_t)sms, kNormFwdShared, [&](int v) { return v * (16 + b); });
 }
 inline NormShape bwd_shape(const NormsArgs& a, int sms) {
   const int b = a.dtype == LIN_BINARY32 ? 16 : 8;
-  return norm_shape(a.tokens, a.width, sms, 226 * 1024 - (size_t)a.width * 12,
+  return norm_shape(a.tokens, a.width, sms, kNormBwdShared - (size_t)a.width * 12,
                     [&](int v) { return v * (32 + 2 * b); });
 }
 
@@ -501,11 +503,14 @@ cudaError_t with_norm(int v, int kind, F&& f) {
   }
 }
 
-// Leave for more shared memory than a launch may have without.
+// Leave for more shared memory than a launch may have without: always up to
+// `most`, not this call's `bytes`. The leave is the kernel's, in the whole
+// process: set to what a call needs, a smaller call of another host thread could
+// take it back before this one's launch.
 template <typename Kernel>
-cudaError_t more_shared(Kernel kernel, size_t bytes) {
+cudaError_t more_shared(Kernel kernel, size_t bytes, size_t most) {
   if (bytes + 1024 <= 48 * 1024) return cudaSuccess;
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
 }
 
 template <int T>
@@ -514,7 +519,7 @@ cudaError_t launch_block_norms_of(const NormsArgs& a, int sms, cudaStream_t stre
   const int kind = a.y && a.n && a.h ? (a.w_post ? 4 : 0) + a.form : -1;
   return with_norm<T>(s.v, kind, [&](auto v, auto k) {
     auto kernel = lin_block_norms_kernel<T, decltype(v)::value, decltype(k)::value>;
-    const cudaError_t e = more_shared(kernel, s.smem);
+    const cudaError_t e = more_shared(kernel, s.smem, kNormFwdShared);
     if (e != cudaSuccess) return e;
     kernel<<<s.ctas, s.teams * s.warps * 32, s.smem, stream>>>(a, s.warps, s.slots);
     return cudaGetLastError();
@@ -528,7 +533,7 @@ cudaError_t launch_block_norms_bwd_of(const NormsArgs& a, int sms, cudaStream_t 
   return with_norm<T>(s.v, kind, [&](auto v, auto k) {
     auto kernel = lin_block_norms_bwd_kernel<T, decltype(v)::value, decltype(k)::value>;
     const size_t smem = (size_t)a.width * 12 + s.smem;
-    const cudaError_t e = more_shared(kernel, smem);
+    const cudaError_t e = more_shared(kernel, smem, kNormBwdShared);
     if (e != cudaSuccess) return e;
     kernel<<<s.ctas, s.teams * s.warps * 32, smem, stream>>>(a, s.warps, s.slots);
     return cudaGetLastError();
