@@ -116,3 +116,27 @@ def test_block_norms(gradient):
     assert not _at_once(calls)
     for r, w in zip(results, want):
         assert all(torch.equal(a, b) for a, b in zip(r, w))
+
+
+def test_distillation():
+    # (rows of eight warps: 40 and 64 KB to a slot)
+    import torch
+    calls, results = [], []
+    for v in (10000, 16384):
+        m, k = 300, 12
+        z = torch.randn(m, v, device="cuda")
+        ids = torch.arange(k, dtype=torch.int32, device="cuda").repeat(m, 1) * 700
+        teacher = torch.randn(m, k, device="cuda")
+        out = [torch.empty_like(z), torch.empty(m, device="cuda"), torch.empty(1, device="cuda")]
+
+        def call(stream, z=z, ids=ids, teacher=teacher, out=out):
+            lin.lin_distill_topk(z, ids, teacher, *out, stream=stream)
+
+        call(None)
+        calls.append(call)
+        results.append(out)
+    torch.cuda.synchronize()
+    want = [[t.clone() for t in r] for r in results]
+    assert not _at_once(calls)
+    for r, w in zip(results, want):
+        assert all(torch.equal(a, b) for a, b in zip(r, w))

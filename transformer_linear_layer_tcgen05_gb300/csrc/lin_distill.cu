@@ -533,8 +533,10 @@ cudaError_t launch_rows(DistillArgs a, int64_t units, int sms, cudaStream_t stre
   a.slots = d.slots;
   const size_t smem = d.smem;
   auto kernel = lin_distill_kernel<WARPS>;
+  // (the kernel's leave is the whole process's: always the most, so that no call
+  // of another host thread takes back what this one's launch needs)
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)smem);
+                                       (int)(kDistillSmem - kDistillStatic));
   if (e == cudaSuccess && a.cluster > 8)
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e != cudaSuccess) return e;
