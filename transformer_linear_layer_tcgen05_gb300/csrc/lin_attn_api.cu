@@ -172,9 +172,12 @@ lin::ScoreForm score_form(const lin_score_form* f, float scale) {
     s.terms[i] = make_float2(c, c);
     if (i < lin::kFewTerms) s.few[i] = make_float2(d, d);
   }
-  // (the last terms of the smallest units would leave float32's normal numbers)
-  s.few_up_to = std::fabs(s.few[lin::kFewTerms - 1].x) >= 0x1p-120f ? (float)(0.3 / unit) : -1.0f;
-  s.up_to = std::fabs(s.terms[lin::kTanhTerms - 1].x) >= 0x1p-120f ? (float)(0.75 / unit) : -1.0f;
+  // Each is for scores whose terms are normal float32 numbers: the last one, the
+  // farthest from 1, leaves them at the smallest units (it would be zero) and at
+  // the largest (cap unit^9: infinite from 2^128 on, and NaN times a score of 0).
+  auto fits = [](float2 last) { return std::fabs(last.x) >= 0x1p-120f && std::fabs(last.x) <= 0x1p120f; };
+  s.few_up_to = fits(s.few[lin::kFewTerms - 1]) ? (float)(0.3 / unit) : -1.0f;
+  s.up_to = fits(s.terms[lin::kTanhTerms - 1]) ? (float)(0.75 / unit) : -1.0f;
   return s;
 }
 
