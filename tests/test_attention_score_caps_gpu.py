@@ -41,12 +41,12 @@ def _sized(t, cap, scale):
 def _check(t, causal, scale, form, u):
     """test_attention_scores_gpu._check for one sequence, with the steps of dS."""
     q, k, v, do = (_host(t[n]) for n in ("q", "k", "v", "do"))
-    cap, slopes = form["cap"], _host(form.get("slopes"))
+    cap, slopes = form.get("cap"), _host(form.get("slopes"))
     spec = dict(cap=cap, slopes=slopes, first=_host(form.get("first_key")), end=_host(form.get("end_key")))
     o, lse, w = to.attention_scores(q, k, v, causal, scale, **spec)
-    moved = cap * 2.0 ** -20
+    moved = (cap or 0) * 2.0 ** -20
     if slopes is not None:
-        moved += np.minimum(np.abs(slopes).max() * len(k), 40 + 2 * cap) * 2.0 ** -22
+        moved += np.minimum(np.abs(slopes).max() * len(k), 40 + 2 * (cap or 40)) * 2.0 ** -22
     e = 2.0 ** -14 + moved
     got = _host(t["lse"])
     assert np.array_equal(np.isinf(got), np.isinf(lse))

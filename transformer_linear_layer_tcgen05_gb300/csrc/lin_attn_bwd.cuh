@@ -700,26 +700,30 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   int t0 = a.causal ? min((max(k0 - off, 0) << shift) / kTurn, t1) : 0;
   const bool ranged = SCORES && args.extents != nullptr;
   bool holes = false;   // (in some tile of the sequence) rows to be zeroed: see kBadFlag
+  float met = 0.0f;     // (ranges) the largest row norm of dO of the tiles that see one of these keys
   if (ranged) {
     // the first and the last tile of 128 rows that see one of these keys
     pdl_wait();
     const int tiles = ((a.max_q << shift) + 127) / 128;
     const int heads = a.group >> shift;   // (tiles of them)
-    const int2* ext = args.extents + ((int64_t)b * gridDim.x + hk) * tiles * heads;
-    int lo = INT_MAX, hi = -1, bad = 0;
+    const int64_t ext = ((int64_t)b * gridDim.x + hk) * tiles * heads;
+    int lo = INT_MAX, hi = -1, bad = 0, big = 0;
     for (int k = threadIdx.x & 31; k < tiles * heads; k += 32) {
       const int i = k % tiles;
-      if (!dcheck(ext + k < args.extents + args.norms, a.status, CHK_STATS, k)) continue;
-      const int2 e = ext[k];
+      if (!dcheck(ext + k < args.norms, a.status, CHK_STATS, k)) continue;
+      const int2 e = args.extents[ext + k];
+      const int norm = __float_as_int(args.norm[ext + k]);   // (not negative: ordered as it is)
       bad |= e.y & kBadFlag;
       if (e.x < k0 + 128 && (e.y & ~kBadFlag) > k0) {
         lo = min(lo, i);
         hi = max(hi, i);
+        big = max(big, norm);
       }
     }
     holes = __any_sync(0xffffffffu, bad);
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
+    met = __int_as_float(__reduce_max_sync(0xffffffffu, big));
     t1 = min(t1, 2 * hi + 2);
     t0 = min(max(t0, lo < INT_MAX ? 2 * lo : 0), t1);
   }
@@ -773,10 +777,12 @@ __global__ void __launch_bounds__(kDkvThreads, 1)
   // The exponent of dS's scale, from the largest row norm of dO that this tile
   // of keys meets, in tiles of 128 rows: behind a causal mask from the one of
   // its first turn on (the rows before it may be larger by more than binary16
-  // spans). By each warp that wants it, once the dQ kernel, which leaves the
-  // norms and delta, is done; the copies and the first products do not wait for
-  // that.
+  // spans), with ranges of keys of the tiles that see one of its keys (other
+  // documents' may be as much larger). By each warp that wants it, once the dQ
+  // kernel, which leaves the norms and delta, is done; the copies and the first
+  // products do not wait for that.
   auto scale_exponent = [&]() -> int {
+    if (ranged) return norm_exponent(met);
     pdl_wait();
     const int tiles = ((a.max_q << shift) + 127) / 128;
     const float* nm = args.norm + ((int64_t)b * gridDim.x + hk) * tiles * passes;
