@@ -374,7 +374,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const uint32_t s_col = tmem + lanes + C::S_COL + t * 128 + col0;
     const uint32_t p_col = tmem + lanes + C::p_col(t) + half * 32;
     const uint32_t o_col = tmem + lanes + C::O_COL + t * DP;
-    float m = -INFINITY, l = 0.0f;
+    // (A row that sees no key at all, which with ranges keeps its scores, has a
+    // maximum that nothing exceeds: it never asks for a new one. What is in its
+    // place may be nobody's, and whatever was in memory.)
+    float m = SCORES && lim < 0 ? INFINITY : -INFINITY, l = 0.0f;
     bool ok = true;
     // (split) what the row's two threads tell each other, in two places in turn
     // (the second tile's queries have none here)
@@ -545,8 +548,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         tc_fence_after_sync();
       }
       if (__any_sync(0xffffffffu, grow)) {
-        const float to = fmaxf(m, top);
-        const float alpha = to > m ? ex2_approx((m - to) * c) : 1.0f;
+        // (capped and biased scores: only rows that ask for it take it, so that a
+        // row's results do not go by what other rows of its warp hold)
+        const float to = CAPPED || BIASED ? (grow ? top : m) : fmaxf(m, top);
+        const float alpha = (CAPPED || BIASED ? grow : to > m) ? ex2_approx((m - to) * c) : 1.0f;
         m = to;
         if (j > bt) {   // P V of the tiles so far is complete (not ahead: S came behind it)
           l *= alpha;
