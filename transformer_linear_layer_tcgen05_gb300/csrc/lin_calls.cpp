@@ -517,13 +517,51 @@ struct Tensors {
   PyObject* at(Py_ssize_t i) const { return items ? PySequence_Fast_GET_ITEM(items, i) : Py_None; }
 };
 
-// One tensor of a list: contiguous, of the given type, with n entries.
-void* entry(PyObject* o, const char* name, at::ScalarType type, const char* type_name, int64_t n) {
+// One tensor of a list: contiguous, of the given type, with n entries. (A list has
+// hundreds: what is raised stands out of line.)
+[[noreturn]] __attribute__((noinline)) void no_entry(const char* name, const char* type_name, int64_t n) {
+  raise(PyExc_TypeError, std::string(name) + ": contiguous " + type_name + " CUDA tensors of " +
+                             std::to_string(n) + " entries here");
+}
+inline void* entry(PyObject* o, const char* name, at::ScalarType type, const char* type_name, int64_t n) {
   const at::Tensor* t = tensor(o);
   if (!t || t->scalar_type() != type || !t->is_cuda() || !t->is_contiguous() || t->numel() != n)
-    raise(PyExc_TypeError, std::string(name) + ": contiguous " + type_name + " CUDA tensors of " +
-                               std::to_string(n) + " entries here");
+    no_entry(name, type_name, n);
   return t->data_ptr();
+}
+
+// Whether two contiguous tensors of as many entries have them in the same order:
+// their shapes are alike but for ones in them, or one is flat.
+bool same_order(c10::IntArrayRef a, c10::IntArrayRef b) {
+  int long_a = 0, long_b = 0;   // sizes that are no ones
+  for (const int64_t n : a) long_a += n != 1;
+  for (const int64_t n : b) long_b += n != 1;
+  if (long_a <= 1 || long_b <= 1) return true;
+  if (long_a != long_b) return false;
+  size_t k = 0;
+  for (const int64_t n : a) {
+    if (n == 1) continue;
+    while (b[k] == 1) ++k;
+    if (n != b[k++]) return false;
+  }
+  return true;
+}
+
+[[noreturn]] __attribute__((noinline)) void no_order(const char* name, const at::Tensor& t,
+                                                     const at::Tensor& weight) {
+  raise(PyExc_ValueError, std::string(name) + list_of(t.sizes()) + " for a weight " +
+                              list_of(weight.sizes()) + ": the weight's shape, or flat");
+}
+// An entry of a list that lies as the weight does: as `entry`, and in its order
+// (beside a flat weight any has it).
+inline void* beside(PyObject* o, const char* name, at::ScalarType type, const char* type_name,
+                    const at::Tensor& weight, int64_t n) {
+  void* p = entry(o, name, type, type_name, n);
+  if (weight.dim() > 1) {
+    const at::Tensor& t = *tensor(o);
+    if (t.sizes() != weight.sizes() && !same_order(t.sizes(), weight.sizes())) no_order(name, t, weight);
+  }
+  return p;
 }
 
 // params, grads, m, v, m_scale, v_scale, w16, step, lr, beta1, beta2, eps,
@@ -544,15 +582,14 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
       lin_adamw_tensor& to = list[(size_t)i];
       to.n = t->numel();
       to.p = static_cast<float*>(entry(p.at(i), "params", at::kFloat, "float32", to.n));
-      to.g = static_cast<const float*>(entry(g.at(i), "grads", at::kFloat, "float32", to.n));
+      to.g = static_cast<const float*>(beside(g.at(i), "grads", at::kFloat, "float32", *t, to.n));
       const at::Tensor* tm = tensor(m.at(i));
-      const bool codes = tm && tm->scalar_type() == at::kFloat8_e4m3fn;
-      if (i == 0) s.state_bits = codes ? 8 : 32;
+      if (i == 0) s.state_bits = tm && tm->scalar_type() == at::kFloat8_e4m3fn ? 8 : 32;
       const bool bits8 = s.state_bits == 8;
       const auto type = bits8 ? at::kFloat8_e4m3fn : at::kFloat;
       const char* name = bits8 ? "float8_e4m3fn" : "float32";
-      to.m = entry(m.at(i), "m", type, name, to.n);
-      to.v = entry(v.at(i), "v", type, name, to.n);
+      to.m = beside(m.at(i), "m", type, name, *t, to.n);
+      to.v = beside(v.at(i), "v", type, name, *t, to.n);
       to.m_scale = to.v_scale = nullptr;
       if (bits8) {
         to.m_scale = static_cast<float*>(entry(ms.at(i), "m_scale", at::kFloat, "float32", (to.n + 255) / 256));
@@ -560,7 +597,7 @@ PyObject* adamw(PyObject*, PyObject* const* a, Py_ssize_t n) {
       }
       to.w16 = w16.at(i) == Py_None
                    ? nullptr
-                   : static_cast<uint16_t*>(entry(w16.at(i), "w16", at::kHalf, "float16", to.n));
+                   : static_cast<uint16_t*>(beside(w16.at(i), "w16", at::kHalf, "float16", *t, to.n));
     }
     auto device = [&](PyObject* o, const char* name, at::ScalarType type, const char* type_name) -> void* {
       return tensor(o) ? entry(o, name, type, type_name, 1) : nullptr;

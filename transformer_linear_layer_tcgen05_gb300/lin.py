@@ -581,7 +581,8 @@ def lin_adamw(params, grads, m, v, m_scale=None, v_scale=None, w16=None, step=1,
     float8_e4m3fn with m_scale, v_scale float32 [ceil(n / 256)] (8-bit states:
     codes of m and of the root of v by blocks of 256 entries; zeros to begin
     with); w16 (or None) the tensors' float16 copies to be written, None where
-    a tensor has none. All contiguous. ``step`` counts from 1; ``step``, ``lr``
+    a tensor has none. All contiguous, and grads, m, v and w16 of the weight's
+    shape (or flat: its entries in its order). ``step`` counts from 1; ``step``, ``lr``
     and ``grad_scale`` may be one-entry CUDA tensors (int32, float32, float32),
     read when the stream gets there."""
     check("lin_adamw", (_calls or _short_calls()).adamw(
