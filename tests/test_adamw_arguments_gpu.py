@@ -1,4 +1,5 @@
-"""lin_adamw's arguments: tensors that are laid out like the weights."""
+"""lin_adamw's arguments: tensors that are laid out like the weights, and the
+smallest eps."""
 
 import pytest
 
@@ -62,3 +63,19 @@ def test_flat_tensors_and_ones_in_a_shape(bits):
     got = {k: t.clone() for k, t in st.items()}
     _step(dict(got, p=got["p"].view(-1)), bits)
     assert torch.equal(got["p"], want["p"])
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("eps", [1e-300, 1e-46, 1e-42, 2e-39, 1e-38, 1e-20])
+@pytest.mark.parametrize("on_device", [False, True])
+def test_eps_below_what_float32_holds(bits, eps, on_device):
+    # entries that have had no gradient yet: 0 / eps
+    import torch
+    st = _group((700,), bits)
+    st["g"][::3] = 0
+    want = st["p"][::3] * (1 - 0.01 * 0.1)
+    step = torch.ones(1, dtype=torch.int32, device="cuda") if on_device else 1
+    _step(st, bits, step=step, lr=0.01, eps=eps, weight_decay=0.1)
+    # (the factor rounded to float32, and the product)
+    assert (st["p"][::3] - want).abs().le(2.0 ** -22 * want.abs()).all()
+    assert torch.isfinite(st["p"]).all()

@@ -432,7 +432,11 @@ lin_status adamw(const lin_adamw_step* s, const lin_adamw_tensor* tensors, int64
   a.beta1_rest = (float)(1.0 - s->beta1);
   a.beta2 = (float)s->beta2;
   a.beta2_rest = (float)(1.0 - s->beta2);
-  a.eps = (float)s->eps;
+  // (Above zero it stays so, and of float32's normal numbers: where there has been
+  // no gradient the kernel's 0 / eps would be 0 / 0, or 0 times an infinite
+  // reciprocal. The root of a v above zero is 2^-75 or more, beside which this is
+  // nothing.)
+  a.eps = s->eps > 0.0 ? std::max((float)s->eps, 0x1p-126f) : 0.0f;
   const double t = (double)std::max<int64_t>(s->step, 1);
   const double c1 = 1.0 / -std::expm1(t * std::log(s->beta1));
   const double c2 = 1.0 / std::sqrt(-std::expm1(t * std::log(s->beta2)));
