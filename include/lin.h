@@ -118,7 +118,8 @@
  * lin_get_device_status() reports it and lin_last_device_check() tells
  * which. In liblin.so the checks compile away.
  *
- * Thread safety: every entry point may be called from several host threads.
+ * Thread safety: every entry point may be called from several host threads,
+ * and as a thread's first use of CUDA.
  */
 #ifndef LIN_H
 #define LIN_H
@@ -439,12 +440,17 @@ lin_status lin_attention_backward(const lin_attention_shape *shape, const lin_he
  * O and the gradients are those of S; a row whose range is empty is one that
  * the mask leaves nothing, and may hold anything in Q and DO; a key that no
  * query sees takes part (finite K and V). The backward form's dS has
- * 1 - (y / cap)^2 as a factor. Tiles of keys that no row of a tile of queries
- * sees are not computed. Workspace (backward, ranges): 8 bytes more for each
- * tile of 128 rows of queries. A capped score is off by at most cap 2^-20. cap
- * >= 0 and finite, else LIN_ERROR_INVALID_VALUE; 0 or 2^-20 to 4096, with scale
- * / cap below float32's end, else LIN_ERROR_UNSUPPORTED_SHAPE; all else as for
- * lin_attention.
+ * 1 - (y / cap)^2 as a factor. Tiles of queries run over the tiles of keys from
+ * the first to the last that one of their rows sees. The same call gives the same
+ * bits, and with a cap or slopes a row's O, LSE and DQ do not go by what other
+ * rows hold. In binary16 dS, of which dK is made, is off by up to 2^-29 of the
+ * largest row norm of DO in the tiles of 128 rows that see the tile of 128 keys
+ * (documents that share no tile do not count with each other's). Workspace
+ * (backward, ranges): 8 bytes more for each tile of 128 rows of queries. A capped
+ * score is off by at most cap 2^-20. cap >= 0 and finite, else
+ * LIN_ERROR_INVALID_VALUE; 0 or 2^-20 to 4096, with scale / cap below float32's
+ * end, else LIN_ERROR_UNSUPPORTED_SHAPE. Without a cap, slopes times distances /
+ * scale stay below float32's end too. All else as for lin_attention.
  */
 typedef struct lin_score_form {
   float cap;
@@ -596,7 +602,8 @@ lin_status lin_block_norms_backward(const lin_block_norms_shape *shape, const fl
  * With step_device the corrections are computed in float32 (below 1: as 1).
  * Tensors of any length and alignment (of their entries); those of 32-byte
  * aligned f32, 8-byte aligned codes and 16-byte aligned w16 are read faster.
- * What is written overlaps nothing else of the call. 0 <= beta < 1, eps >= 0;
+ * What is written overlaps nothing else of the call. 0 <= beta < 1, eps >= 0
+ * (above zero: 2^-126 at least);
  * up to 2^20 tensors, each below 2^39 entries; tensors without entries are
  * passed over.
  */

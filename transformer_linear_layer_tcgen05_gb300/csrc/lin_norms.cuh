@@ -16,7 +16,7 @@
 // V units of four entries to a thread. The threads copy the units of their next
 // rows into shared memory of their own meanwhile (nobody else's: a copy's end is
 // all that its reader waits for). In TB/s, a copy at 6.8, f32 and bfloat16:
-// 16384 x 2048 forward 5.8 and 5.7, gradient 6.0 and 5.7 (without the copies
+// 16384 x 2048 forward 5.8 and 5.7, gradient 5.9 and 5.7 (without the copies
 // 4.4); 4096 x 8192 6.2 and 5.1, 4.6 and 4.1 (a row takes a whole CTA, and the
 // gradient's shared memory holds one). Short calls are launches: 512 x 768 in
 // 3.0-3.3 us.
