@@ -28,7 +28,10 @@ def _calls():
     z, dz, loss = rnd(8, 400), rnd(8, 400), torch.empty(9, device="cuda")
     ids = torch.arange(8, dtype=torch.int32, device="cuda").repeat(8, 1)
     teacher = rnd(8, 8)
+    xh, wh, yh = x.cpu(), w.cpu(), torch.empty(64, 64)
     return {
+        "matmul_host": lambda s: lin.lin_matmul_host(xh, wh, yh, stream=s),
+        "status": lambda s: lin.check("status", lin.lin_get_device_status()),
         "matmul": lambda s: lin.lin_matmul(x, w, y, stream=s),
         "attention": lambda s: lin.lin_attention(q, k, v, o, lse, stream=s),
         "block_norms": lambda s: lin.lin_block_norms(x, None, None, None, ones, h, n, stream=s),
@@ -37,7 +40,7 @@ def _calls():
     }
 
 
-@pytest.mark.parametrize("name", ["matmul", "attention", "block_norms", "adamw", "distill_topk"])
+@pytest.mark.parametrize("name", ["matmul_host", "status", "matmul", "attention", "block_norms", "adamw", "distill_topk"])
 def test_a_threads_first_call(name):
     # (a thread that has made no CUDA call of its own yet)
     import torch
